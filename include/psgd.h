@@ -424,6 +424,137 @@ psgd_status_t psgd_subspace_overlap(psgd_plan_t plan, const float* q_a, const fl
                                     double* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Element types of the tensors that the operators below take and give.
+ */
+#define PSGD_DTYPE_F32 0
+#define PSGD_DTYPE_BF16 1
+#define PSGD_DTYPE_F16 2
+
+/*
+ * Global gradient norm and clipping over a list of tensors.
+ *
+ *   n_t = ||scale * g_t||, N = sqrt(sum_t n_t^2), c = min(1, max_norm / (N + 1e-6)),
+ *   out_t = scale * c * g_t
+ *
+ * `scale` is what the gradients are to be multiplied by first (1 over a loss
+ * scale or over a number of accumulated batches; 1 for none).  An output may
+ * be its own gradient (in place) or any other memory, for example the tensor's
+ * place in the flat buffer that psgd_compress reads, with conversion to the
+ * output's type (one rounding, nearest even).  Squares are summed in fp64 in
+ * a fixed order: repeated calls agree bit for bit.
+ *
+ * stats receives 2 + ntensors floats on the device: N, c, then every n_t.  A
+ * NaN in a gradient makes N, c and every output NaN; an infinity makes N
+ * infinite and c zero (finite values become zero, infinite ones NaN): the
+ * caller that skips such a step looks at N.
+ *
+ * psgd_clip_create       host only.  ntensors >= 0 tensors of numel[t] >= 0
+ *                        elements (0: an empty tensor, norm 0), of type
+ *                        in_dtypes[t], outputs of type out_dtypes[t].
+ *                        Errors: PSGD_ERR_INVALID_ARG.
+ * psgd_clip_workspace    bytes of device workspace the calls below need, 256-
+ *                        byte aligned, owned by the caller.
+ * psgd_clip_workspace_init  writes the list's tables into the workspace; once
+ *                        per (clip, workspace) pair, not for graph capture
+ *                        (it copies from the host).
+ * psgd_clip_bind         writes the tensors' addresses into the workspace:
+ *                        ntensors gradient pointers and as many output
+ *                        pointers (out NULL: norms only), host arrays that
+ *                        are read before the call returns.  Any alignment
+ *                        to the element type is accepted (16-byte alignment
+ *                        is fastest).  Again whenever an address changes.
+ *                        Errors: PSGD_ERR_INVALID_ARG for a NULL or misaligned
+ *                        pointer of a tensor that is not empty, for outputs
+ *                        that overlap each other or a gradient (other than
+ *                        the gradient of the same tensor in place, with
+ *                        types of the same size).
+ * psgd_clip_norm         stats only: reads the gradients once.
+ * psgd_clip_apply        stats and outputs.  The outputs must have been bound.
+ *
+ * Errors of the last two: PSGD_ERR_INVALID_ARG for a NULL or misaligned stats,
+ * a negative or NaN max_norm (an infinite one clips nothing), a scale that is
+ * not finite; PSGD_ERR_WORKSPACE; PSGD_ERR_HIP.  Calls that share a workspace
+ * must be ordered by their stream.
+ */
+typedef struct psgd_clip* psgd_clip_t;
+psgd_status_t psgd_clip_create(int32_t ntensors, const int64_t* numel, const int32_t* in_dtypes,
+                               const int32_t* out_dtypes, psgd_clip_t* out);
+void psgd_clip_destroy(psgd_clip_t clip);
+psgd_status_t psgd_clip_workspace(psgd_clip_t clip, size_t* bytes);
+psgd_status_t psgd_clip_workspace_init(psgd_clip_t clip, void* workspace, size_t workspace_bytes, hipStream_t stream);
+psgd_status_t psgd_clip_bind(psgd_clip_t clip, const void* const* in, void* const* out, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+psgd_status_t psgd_clip_norm(psgd_clip_t clip, float max_norm, float scale, float* stats, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+psgd_status_t psgd_clip_apply(psgd_clip_t clip, float max_norm, float scale, float* stats, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Microscaled 4-bit operands (MXFP4): OCP E2M1 values (0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and their negatives) in blocks of 32 along a row, each block with one
+ * E8M0 scale 2^(byte - 127) ("OCP Microscaling Formats (MX) Specification"
+ * v1.0; byte 255 is NaN and makes the whole block NaN).  As with the 8-bit
+ * factor payload, the scale of a block is 2^k with k the smallest integer
+ * >= -127 for which the block's largest magnitude is at most 6 * 2^k, so that
+ * no value saturates; a block that holds an infinity or a NaN becomes NaN.
+ *
+ * An operand of rows x cols values is two device buffers, 16-byte aligned,
+ * whose sizes psgd_mx_sizes gives:
+ *   codes   16 bytes per block, ceil(cols / 32) blocks per row, row after row;
+ *           element 2 j of a block in the low nibble of byte j, element 2 j + 1
+ *           in the high one; code = index of the magnitude in the list above,
+ *           plus 8 if negative; the last block is padded with zero codes;
+ *   scales  tiles of 32 rows x 256 columns, 256 bytes each, the tiles of one
+ *           row of tiles after each other: the scale of row i, block b is byte
+ *           ((i / 32) * ceil(cols / 256) + b / 8) * 256 + (b % 8 / 4) * 128
+ *           + (i % 32) * 4 + b % 4.  Bytes of blocks past the last column are
+ *           zero; bytes of rows past the last row are not read for results.
+ *
+ * psgd_mx_quantize -- x: rows x cols values of type `dtype`, row stride ld
+ * elements.  rand: NULL rounds to nearest, ties to the even code; else rows x
+ * cols random bytes r (contiguous), and a value goes to its upper neighbour
+ * (in magnitude) where the fraction between its neighbours, times 256, is
+ * above r + 0.5, else to the lower one.  Each of the three outputs may be left
+ * out (NULL): row_codes / row_scales, the operand of x (blocks along its
+ * rows); col_codes / col_scales, the operand of x^T (cols x rows, blocks along
+ * x's columns: what a product that sums over x's rows needs); values, rows x
+ * cols of x's type with row stride ldv, the values that the row operand stands
+ * for (may be x itself, in place; a value beyond fp16's range becomes
+ * infinite).  The result does not depend on the launch: equal inputs give
+ * equal bytes.
+ *
+ * psgd_mx_dequantize -- the values of an operand, in the given type.
+ *
+ * psgd_mx_product -- C = A B^T (accumulate: C += A B^T) for A m x k and B n x k
+ * operands: summed over k in fp32 (E2M1 products are exact) in an order that
+ * depends on the sizes alone, rounded once to C's type.  k = 0 gives zeros.
+ * workspace: psgd_mx_product_workspace bytes (may be 0, then NULL is allowed),
+ * 256-byte aligned, scratch.
+ *
+ * psgd_mx_linear -- y = Q(x) W^T: psgd_mx_quantize (nearest) of x's rows into
+ * the workspace, then the product with the n x k operand W.  For a layer whose
+ * weights were quantised once: serving, also of single tokens (m = 1).
+ *
+ * Sizes are 0 .. INT32_MAX.  Errors: PSGD_ERR_INVALID_ARG (sizes, strides, an
+ * unknown type, NULL or misaligned buffers, overlapping buffers);
+ * PSGD_ERR_WORKSPACE; PSGD_ERR_HIP.  All calls only enqueue kernels.
+ */
+psgd_status_t psgd_mx_sizes(int64_t rows, int64_t cols, size_t* code_bytes, size_t* scale_bytes);
+psgd_status_t psgd_mx_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                               const uint8_t* rand, uint8_t* row_codes, uint8_t* row_scales, uint8_t* col_codes,
+                               uint8_t* col_scales, void* values, int64_t ldv, hipStream_t stream);
+psgd_status_t psgd_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
+                                 int32_t dtype, int64_t ld, hipStream_t stream);
+psgd_status_t psgd_mx_product_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
+psgd_status_t psgd_mx_product(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes, const uint8_t* a_scales,
+                              const uint8_t* b_codes, const uint8_t* b_scales, void* c, int32_t dtype, int64_t ldc,
+                              int32_t accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
+psgd_status_t psgd_mx_linear_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
+psgd_status_t psgd_mx_linear(int64_t m, int64_t n, int64_t k, const void* x, int32_t x_dtype, int64_t ldx,
+                             const uint8_t* w_codes, const uint8_t* w_scales, void* y, int32_t y_dtype, int64_t ldy,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Per-stage timing with HIP events recorded on the call's stream.  While
  * enabled, every compress / decompress / refresh call records one event pair
  * per stage it runs (psgd_refresh records its products under EF_P, MTP and

@@ -45,6 +45,10 @@ PSGD_STAGE_RESIDUAL = 4
 PSGD_STAGE_PASSTHRU = 5
 PSGD_STAGE_REFRESH = 6
 PSGD_NSTAGES = 7
+PSGD_DTYPE_F32 = 0
+PSGD_DTYPE_BF16 = 1
+PSGD_DTYPE_F16 = 2
+
 STAGE_NAMES = ["ef_p", "gs", "mtp", "qreduce", "residual", "passthru", "refresh"]
 
 # Every symbol include/psgd.h declares.
@@ -52,6 +56,10 @@ EXPORTED = [
     "psgd_plan_create", "psgd_plan_destroy", "psgd_plan_get_info", "psgd_plan_tensor",
     "psgd_workspace_init", "psgd_compress", "psgd_compress_noalloc", "psgd_decompress", "psgd_refresh", "psgd_init_q",
     "psgd_step_stats", "psgd_subspace_overlap",
+    "psgd_clip_create", "psgd_clip_destroy", "psgd_clip_workspace", "psgd_clip_workspace_init", "psgd_clip_bind",
+    "psgd_clip_norm", "psgd_clip_apply",
+    "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize", "psgd_mx_product_workspace", "psgd_mx_product",
+    "psgd_mx_linear_workspace", "psgd_mx_linear",
     "psgd_timing_enable", "psgd_timing_stages", "psgd_timing_read", "psgd_stream_probe", "psgd_stream_copy", "psgd_last_error",
     "psgd_version",
 ]
@@ -142,13 +150,32 @@ lib.psgd_timing_stages.argtypes = [_vp, ctypes.c_uint32]
 lib.psgd_timing_read.argtypes = [_vp, ctypes.POINTER(ctypes.c_double), _i64p]
 lib.psgd_stream_copy.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
 lib.psgd_stream_probe.argtypes = [_vp, ctypes.c_int32, _vp, ctypes.c_int32, ctypes.c_size_t, _vp, _vp]
+_sz, _i64, _i32, _szp = ctypes.c_size_t, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)
+lib.psgd_clip_create.argtypes = [_i32, _i64p, _i32p, _i32p, ctypes.POINTER(_vp)]
+lib.psgd_clip_destroy.argtypes = [_vp]
+lib.psgd_clip_destroy.restype = None
+lib.psgd_clip_workspace.argtypes = [_vp, _szp]
+lib.psgd_clip_workspace_init.argtypes = [_vp, _vp, _sz, _vp]
+lib.psgd_clip_bind.argtypes = [_vp, _vp, _vp, _vp, _sz, _vp]
+lib.psgd_clip_norm.argtypes = [_vp, ctypes.c_float, ctypes.c_float, _vp, _vp, _sz, _vp]
+lib.psgd_clip_apply.argtypes = lib.psgd_clip_norm.argtypes
+lib.psgd_mx_sizes.argtypes = [_i64, _i64, _szp, _szp]
+lib.psgd_mx_quantize.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
+lib.psgd_mx_dequantize.argtypes = [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]
+lib.psgd_mx_product_workspace.argtypes = [_i64, _i64, _i64, _szp]
+lib.psgd_mx_product.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _vp, _sz, _vp]
+lib.psgd_mx_linear_workspace.argtypes = [_i64, _i64, _i64, _szp]
+lib.psgd_mx_linear.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _i64, _vp, _sz, _vp]
 lib.psgd_last_error.restype = ctypes.c_char_p
 lib.psgd_version.restype = ctypes.c_char_p
 for _f in ["psgd_plan_create", "psgd_plan_get_info", "psgd_plan_tensor", "psgd_workspace_init", "psgd_compress",
            "psgd_compress_noalloc",
            "psgd_decompress", "psgd_refresh", "psgd_init_q", "psgd_timing_enable", "psgd_timing_stages", "psgd_timing_read",
            "psgd_stream_copy",
-           "psgd_stream_probe", "psgd_step_stats", "psgd_subspace_overlap"]:
+           "psgd_stream_probe", "psgd_step_stats", "psgd_subspace_overlap",
+           "psgd_clip_create", "psgd_clip_workspace", "psgd_clip_workspace_init", "psgd_clip_bind", "psgd_clip_norm",
+           "psgd_clip_apply", "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize", "psgd_mx_product_workspace",
+           "psgd_mx_product", "psgd_mx_linear_workspace", "psgd_mx_linear"]:
     getattr(lib, _f).restype = ctypes.c_int
 
 
@@ -250,6 +277,99 @@ def psgd_subspace_overlap(plan: int, q_a: int, q_b: int, scratch: int, out: int,
                           workspace_bytes: int, stream: int = 0) -> None:
     _check("psgd_subspace_overlap", lib.psgd_subspace_overlap(plan, q_a or None, q_b or None, scratch or None,
                                                               out or None, workspace, workspace_bytes, stream))
+
+
+def psgd_clip_create(numel: Sequence[int], in_dtypes: Sequence[int], out_dtypes: Sequence[int]) -> int:
+    if len(numel) != len(in_dtypes) or len(numel) != len(out_dtypes):
+        raise ValueError("numel, in_dtypes and out_dtypes must have the same length")
+    n = len(numel)
+    out = _vp()
+    _check("psgd_clip_create", lib.psgd_clip_create(n, _arr64(numel), (_i32 * n)(*in_dtypes), (_i32 * n)(*out_dtypes),
+                                                    ctypes.byref(out)))
+    return out.value
+
+
+def psgd_clip_destroy(clip: int) -> None:
+    lib.psgd_clip_destroy(clip)
+
+
+def psgd_clip_workspace(clip: int) -> int:
+    b = _sz()
+    _check("psgd_clip_workspace", lib.psgd_clip_workspace(clip, ctypes.byref(b)))
+    return b.value
+
+
+def psgd_clip_workspace_init(clip: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check("psgd_clip_workspace_init", lib.psgd_clip_workspace_init(clip, workspace or None, workspace_bytes, stream))
+
+
+def psgd_clip_bind(clip: int, ins: Sequence[int], outs: Optional[Sequence[int]], workspace: int, workspace_bytes: int,
+                   stream: int = 0) -> None:
+    """ins / outs: device pointers (ints), one per tensor; outs None: norms only."""
+    n = len(ins)
+    if outs is not None and len(outs) != n:
+        raise ValueError("ins and outs must have the same length")
+    a_in = (_vp * max(1, n))(*ins)
+    a_out = (_vp * max(1, n))(*outs) if outs is not None else None
+    _check("psgd_clip_bind", lib.psgd_clip_bind(clip, a_in, a_out, workspace or None, workspace_bytes, stream))
+
+
+def psgd_clip_norm(clip: int, max_norm: float, scale: float, stats: int, workspace: int, workspace_bytes: int,
+                   stream: int = 0) -> None:
+    _check("psgd_clip_norm", lib.psgd_clip_norm(clip, max_norm, scale, stats or None, workspace or None,
+                                                workspace_bytes, stream))
+
+
+def psgd_clip_apply(clip: int, max_norm: float, scale: float, stats: int, workspace: int, workspace_bytes: int,
+                    stream: int = 0) -> None:
+    _check("psgd_clip_apply", lib.psgd_clip_apply(clip, max_norm, scale, stats or None, workspace or None,
+                                                  workspace_bytes, stream))
+
+
+def psgd_mx_sizes(rows: int, cols: int):
+    """(bytes of the codes, bytes of the scales) of a rows x cols operand."""
+    c, s = _sz(), _sz()
+    _check("psgd_mx_sizes", lib.psgd_mx_sizes(rows, cols, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def psgd_mx_quantize(x: int, dtype: int, rows: int, cols: int, ld: int, rand: int, row_codes: int, row_scales: int,
+                     col_codes: int, col_scales: int, values: int, ldv: int, stream: int = 0) -> None:
+    _check("psgd_mx_quantize", lib.psgd_mx_quantize(x or None, dtype, rows, cols, ld, rand or None, row_codes or None,
+                                                    row_scales or None, col_codes or None, col_scales or None,
+                                                    values or None, ldv, stream))
+
+
+def psgd_mx_dequantize(codes: int, scales: int, rows: int, cols: int, out: int, dtype: int, ld: int,
+                       stream: int = 0) -> None:
+    _check("psgd_mx_dequantize", lib.psgd_mx_dequantize(codes or None, scales or None, rows, cols, out or None, dtype,
+                                                        ld, stream))
+
+
+def psgd_mx_product_workspace(m: int, n: int, k: int) -> int:
+    b = _sz()
+    _check("psgd_mx_product_workspace", lib.psgd_mx_product_workspace(m, n, k, ctypes.byref(b)))
+    return b.value
+
+
+def psgd_mx_product(m: int, n: int, k: int, a_codes: int, a_scales: int, b_codes: int, b_scales: int, c: int,
+                    dtype: int, ldc: int, accumulate: bool, workspace: int, workspace_bytes: int,
+                    stream: int = 0) -> None:
+    _check("psgd_mx_product", lib.psgd_mx_product(m, n, k, a_codes or None, a_scales or None, b_codes or None,
+                                                  b_scales or None, c or None, dtype, ldc, 1 if accumulate else 0,
+                                                  workspace or None, workspace_bytes, stream))
+
+
+def psgd_mx_linear_workspace(m: int, n: int, k: int) -> int:
+    b = _sz()
+    _check("psgd_mx_linear_workspace", lib.psgd_mx_linear_workspace(m, n, k, ctypes.byref(b)))
+    return b.value
+
+
+def psgd_mx_linear(m: int, n: int, k: int, x: int, x_dtype: int, ldx: int, w_codes: int, w_scales: int, y: int,
+                   y_dtype: int, ldy: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check("psgd_mx_linear", lib.psgd_mx_linear(m, n, k, x or None, x_dtype, ldx, w_codes or None, w_scales or None,
+                                                y or None, y_dtype, ldy, workspace or None, workspace_bytes, stream))
 
 
 def psgd_timing_enable(plan: int, enable: bool) -> None:

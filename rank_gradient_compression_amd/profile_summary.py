@@ -57,6 +57,12 @@ def source_file(kernel: str) -> str:
         return "kernels_diag.hip"
     if k.startswith("k_round_fp8"):
         return "kernels_payload.hip"
+    if k.startswith("k_clip"):
+        return "kernels_clip.hip"
+    if k.startswith(("k_mx_quant", "k_mx_dequant")):
+        return "kernels_mxquant.hip"
+    if k.startswith("k_mx"):
+        return "kernels_mxprod.hip"
     return "kernels_valu.hip"
 
 

@@ -183,3 +183,9 @@ class PowerSGD:
             self.close()
         except Exception:
             pass
+
+
+# The operators beside the compression: the global norm and clipping of the
+# gradients it reads, and the microscaled 4-bit operands and products.
+from .torch_ops import (GradientClip, MxTensor, mx_dequantize, mx_linear, mx_linear_backward,  # noqa: E402,F401
+                        mx_linear_forward, mx_linear_train, mx_product, mx_quantize, mx_quantize_both, mx_quantize_t)

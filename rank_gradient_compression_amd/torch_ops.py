@@ -1,0 +1,300 @@
+"""The gradient clip and the microscaled 4-bit operands over PyTorch tensors.
+
+Like the PowerSGD class it allocates buffers and marshals pointers; the
+computation runs in libpsgd.so, on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+from typing import Optional, Sequence, Tuple
+
+import torch
+
+from . import binding as B
+
+_DTYPES = {torch.float32: B.PSGD_DTYPE_F32, torch.bfloat16: B.PSGD_DTYPE_BF16, torch.float16: B.PSGD_DTYPE_F16}
+
+
+def _dtype(t: torch.Tensor) -> int:
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"expected float32, bfloat16 or float16, got {t.dtype}") from None
+
+
+def _stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _matrix(x: torch.Tensor, name: str) -> int:
+    """The row stride of a row-major matrix (unit column stride)."""
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {x.dim()} dimensions")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return x.stride(0) if rows > 1 else max(1, cols)
+
+
+# ------------------------------------------------------------------- the clip
+class GradientClip:
+    """Global norm of a list of gradients, and the clipped gradients.
+
+    grads  contiguous tensors (float32, bfloat16 or float16, any mixture)
+    outs   where the clipped gradients go: one contiguous tensor per gradient
+           and of its size, of any of the three types -- for example the
+           tensor's view of PowerSGD.grads, so that clipping also packs the
+           gradients for the compression; None clips in place
+
+    The handle keeps the addresses; bind() replaces them when the tensors move.
+    """
+
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
+        self.handle = 0
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        self._check(grads, outs)
+        self.device = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+        self._numel = [g.numel() for g in grads]
+        self._in, self._out = [_dtype(g) for g in grads], [_dtype(o) for o in outs]
+        self.handle = B.psgd_clip_create(self._numel, self._in, self._out)
+        self.ws_bytes = B.psgd_clip_workspace(self.handle)
+        with torch.cuda.device(self.device):
+            self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            B.psgd_clip_workspace_init(self.handle, self.workspace.data_ptr(), self.ws_bytes, _stream(self.device))
+            self._bind(grads, outs)
+
+    @staticmethod
+    def _check(grads, outs) -> None:
+        if len(grads) != len(outs):
+            raise ValueError(f"{len(grads)} gradients but {len(outs)} outputs")
+        for t in (*grads, *outs):
+            if not t.is_cuda or not t.is_contiguous() or t.device != grads[0].device:
+                raise ValueError("gradients and outputs must be contiguous tensors on one GPU")
+        for g, o in zip(grads, outs):
+            if g.numel() != o.numel():
+                raise ValueError(f"an output of {o.numel()} elements for a gradient of {g.numel()}")
+
+    def _bind(self, grads, outs) -> None:
+        self.grads, self.outs = grads, outs  # kept alive: the workspace holds their addresses
+        B.psgd_clip_bind(self.handle, [g.data_ptr() for g in grads], [o.data_ptr() for o in outs],
+                         self.workspace.data_ptr(), self.ws_bytes, _stream(self.device))
+
+    def bind(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None) -> None:
+        """New tensors of the same sizes and types (psgd_clip_bind)."""
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        self._check(grads, outs)
+        if ([g.numel() for g in grads] != self._numel or [_dtype(g) for g in grads] != self._in
+                or [_dtype(o) for o in outs] != self._out):
+            raise ValueError("the tensors differ in size or type from the handle's")
+        if grads and grads[0].device != self.device:
+            raise ValueError("the tensors are on another GPU than the handle's workspace")
+        with torch.cuda.device(self.device):
+            self._bind(grads, outs)
+
+    def _call(self, fn, max_norm: float, scale: float) -> torch.Tensor:
+        stats = torch.empty(2 + len(self._numel), dtype=torch.float32, device=self.device)
+        with torch.cuda.device(self.device):
+            fn(self.handle, float(max_norm), float(scale), stats.data_ptr(), self.workspace.data_ptr(), self.ws_bytes,
+               _stream(self.device))
+        return stats
+
+    def norm(self, max_norm: float = float("inf"), scale: float = 1.0) -> torch.Tensor:
+        """float32 (2 + n) on the device: the global norm of scale * grads, the
+        coefficient that max_norm asks for, then every tensor's norm."""
+        return self._call(B.psgd_clip_norm, max_norm, scale)
+
+    def clip(self, max_norm: float, scale: float = 1.0) -> torch.Tensor:
+        """The same, and outs = scale * coefficient * grads."""
+        return self._call(B.psgd_clip_apply, max_norm, scale)
+
+    def close(self) -> None:
+        if self.handle:
+            B.psgd_clip_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ------------------------------------------------ microscaled 4-bit operands
+class MxTensor:
+    """A rows x cols operand: codes and scales as psgd.h lays them out."""
+
+    __slots__ = ("rows", "cols", "codes", "scales")
+
+    def __init__(self, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor):
+        self.rows, self.cols, self.codes, self.scales = rows, cols, codes, scales
+
+    @staticmethod
+    def empty(rows: int, cols: int, device) -> "MxTensor":
+        nblk, nch = (cols + 31) // 32, (cols + 255) // 256
+        code_bytes, scale_bytes = rows * nblk * 16, (rows + 31) // 32 * nch * 256
+        # one allocation; the scales start at a multiple of 256 bytes
+        off = (code_bytes + 255) & ~255
+        buf = torch.empty(off + scale_bytes, dtype=torch.uint8, device=device)
+        return MxTensor(rows, cols, buf[:code_bytes], buf[off:])
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    @property
+    def shape(self) -> Tuple[int, int]:
+        return self.rows, self.cols
+
+
+def _rand(rand: Optional[torch.Tensor], x: torch.Tensor) -> int:
+    if rand is None:
+        return 0
+    if rand.dtype != torch.uint8 or rand.shape != x.shape or not rand.is_contiguous() or rand.device != x.device:
+        raise ValueError("rand must be a contiguous uint8 matrix of x's shape on x's device")
+    return rand.data_ptr()
+
+
+def _quantize(x, rand, row: Optional[MxTensor], col: Optional[MxTensor], values) -> None:
+    ld = _matrix(x, "x")
+    ldv = 0
+    if values is not None:
+        if values.shape != x.shape or values.dtype != x.dtype or values.device != x.device:
+            raise ValueError("values must have x's shape, type and device")
+        ldv = _matrix(values, "values")
+    with torch.cuda.device(x.device):
+        B.psgd_mx_quantize(x.data_ptr(), _dtype(x), x.shape[0], x.shape[1], ld, _rand(rand, x),
+                           row.codes.data_ptr() if row else 0, row.scales.data_ptr() if row else 0,
+                           col.codes.data_ptr() if col else 0, col.scales.data_ptr() if col else 0,
+                           values.data_ptr() if values is not None else 0, ldv, _stream(x.device))
+
+
+def mx_quantize(x: torch.Tensor, rand: Optional[torch.Tensor] = None,
+                values: Optional[torch.Tensor] = None) -> MxTensor:
+    """The operand of x: blocks of 32 along its rows.  rand: uint8 of x's shape
+    for stochastic rounding (None: nearest).  values: receives the values that
+    the codes stand for (x's shape and type; may be x itself)."""
+    q = MxTensor.empty(x.shape[0], x.shape[-1], x.device)
+    _quantize(x, rand, q, None, values)
+    return q
+
+
+def mx_quantize_both(x: torch.Tensor, rand: Optional[torch.Tensor] = None) -> Tuple[MxTensor, MxTensor]:
+    """The operands of x and of x^T (blocks along x's rows and along its
+    columns), from one reading of x."""
+    q, t = MxTensor.empty(x.shape[0], x.shape[-1], x.device), MxTensor.empty(x.shape[-1], x.shape[0], x.device)
+    _quantize(x, rand, q, t, None)
+    return q, t
+
+
+def mx_quantize_t(x: torch.Tensor, rand: Optional[torch.Tensor] = None) -> MxTensor:
+    """The operand of x^T: blocks of 32 along x's columns."""
+    t = MxTensor.empty(x.shape[-1], x.shape[0], x.device)
+    _quantize(x, rand, None, t, None)
+    return t
+
+
+def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of an operand."""
+    if out is None:
+        out = torch.empty(q.rows, q.cols, dtype=dtype, device=q.device)
+    elif out.shape != q.shape or out.device != q.device:
+        raise ValueError("out must have the operand's shape and device")
+    ld = _matrix(out, "out")
+    with torch.cuda.device(q.device):
+        B.psgd_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, out.data_ptr(), _dtype(out), ld,
+                             _stream(q.device))
+    return out
+
+
+def _result(out, m: int, n: int, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(m, n, dtype=dtype, device=device)
+    if out.shape != (m, n) or out.device != device:
+        raise ValueError(f"out must be a {m} x {n} matrix on {device}")
+    return out
+
+
+def mx_product(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
+               accumulate: bool = False) -> torch.Tensor:
+    """a b^T (accumulate: added to out), summed in fp32 and rounded once."""
+    if a.cols != b.cols or a.device != b.device:
+        raise ValueError(f"operands of {a.cols} and {b.cols} columns, on {a.device} and {b.device}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    m, n, k = a.rows, b.rows, a.cols
+    c = _result(out, m, n, dtype, a.device)
+    ldc = _matrix(c, "out")
+    need = B.psgd_mx_product_workspace(m, n, k)
+    ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
+    with torch.cuda.device(a.device):
+        B.psgd_mx_product(m, n, k, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
+                          c.data_ptr(), _dtype(c), ldc, accumulate, ws.data_ptr() if need else 0, need,
+                          _stream(a.device))
+    return c
+
+
+def mx_linear(x: torch.Tensor, w: MxTensor, out: Optional[torch.Tensor] = None,
+              dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """y = Q(x) w^T for weights that were quantised once (psgd_mx_linear); y
+    has x's type unless dtype or out says otherwise."""
+    ldx = _matrix(x, "x")
+    m, k = x.shape
+    if k != w.cols or x.device != w.device:
+        raise ValueError(f"x has {k} columns on {x.device}, the weights {w.cols} on {w.device}")
+    y = _result(out, m, w.rows, dtype or x.dtype, x.device)
+    need = B.psgd_mx_linear_workspace(m, w.rows, k)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    with torch.cuda.device(x.device):
+        B.psgd_mx_linear(m, w.rows, k, x.data_ptr(), _dtype(x), ldx, w.codes.data_ptr(), w.scales.data_ptr(),
+                         y.data_ptr(), _dtype(y), _matrix(y, "out"), ws.data_ptr(), need, _stream(x.device))
+    return y
+
+
+def mx_linear_forward(x: torch.Tensor, w: torch.Tensor):
+    """y = Q(x) Q(w)^T for full-precision weights, and what the backward pass
+    needs: the operands of x^T and w^T, whose blocks run along the axes that
+    its products sum over."""
+    xr, xt = mx_quantize_both(x)
+    wr, wt = mx_quantize_both(w)
+    return mx_product(xr, wr, dtype=x.dtype), (xt, wt)
+
+
+def mx_linear_backward(dy: torch.Tensor, saved, rand: Optional[torch.Tensor] = None,
+                       dw: Optional[torch.Tensor] = None, accumulate: bool = False):
+    """Gradients of the layer with the quantisers taken as the identity:
+    dx = Q(dy) Q(w^T)^T in dy's type and dw = Q(dy^T) Q(x^T)^T in fp32, each
+    quantised along the axis it sums over; rand rounds dy stochastically.  dw:
+    the matrix to write (accumulate: to add to), for example a view of
+    PowerSGD.grads."""
+    xt, wt = saved
+    dyr, dyt = mx_quantize_both(dy, rand)
+    dx = mx_product(dyr, wt, dtype=dy.dtype)
+    return dx, mx_product(dyt, xt, out=dw, accumulate=accumulate)
+
+
+class _MxLinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, stochastic, generator):
+        flat = x.reshape(-1, x.shape[-1])
+        y, ctx.saved = mx_linear_forward(flat, w)
+        ctx.x_shape, ctx.w_dtype, ctx.stochastic, ctx.generator = x.shape, w.dtype, stochastic, generator
+        return y.view(*x.shape[:-1], w.shape[0])
+
+    @staticmethod
+    def backward(ctx, dy):
+        flat = dy.reshape(-1, dy.shape[-1]).contiguous()
+        rand = None
+        if ctx.stochastic:
+            rand = torch.randint(0, 256, flat.shape, dtype=torch.uint8, device=flat.device, generator=ctx.generator)
+        dx, dw = mx_linear_backward(flat, ctx.saved, rand)
+        return dx.view(ctx.x_shape), dw.to(ctx.w_dtype), None, None
+
+
+def mx_linear_train(x: torch.Tensor, w: torch.Tensor, stochastic: bool = True, generator=None) -> torch.Tensor:
+    """The layer under autograd: x of any leading shape, w out x in.  With
+    `stochastic` the incoming gradient is rounded with random bytes of
+    `generator` (None: the device's default one)."""
+    return _MxLinearFunction.apply(x, w, stochastic, generator)
