@@ -26,12 +26,18 @@ struct Elem<kBF16> {
     const __hip_bfloat16 b = __float2bfloat16(v);
     return __builtin_bit_cast(uint16_t, b);
   }
+  static __device__ __forceinline__ uint32_t down2(float v, float w) {  // v in the low half
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{v, w}), v2b));
+  }
 };
 template <>
 struct Elem<kF16> {
   using type = uint16_t;
   static __device__ __forceinline__ float up(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
   static __device__ __forceinline__ uint16_t down(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+  static __device__ __forceinline__ uint32_t down2(float v, float w) { return down(v) | (uint32_t)down(w) << 16; }
 };
 
 // Scale byte of a block whose largest magnitude has the bit pattern `amax`
