@@ -365,7 +365,7 @@ extern "C" psgd_status_t psgd_mx_linear_workspace(int64_t m, int64_t n, int64_t 
   clear_error();
   if (bad_dim(m) || bad_dim(n) || bad_dim(k) || !bytes)
     return invalid("psgd_mx_linear_workspace", "a size is negative or above INT32_MAX, or bytes is NULL");
-  *bytes = linear_operand_bytes(m, k) + mx_product_workspace(m, n, k);
+  *bytes = mx_linear_fuses(m, k) ? 0 : linear_operand_bytes(m, k) + mx_product_workspace(m, n, k);
   return PSGD_OK;
 }
 
@@ -378,6 +378,11 @@ extern "C" psgd_status_t psgd_mx_linear(int64_t m, int64_t n, int64_t k, const v
   if (psgd_status_t s = check_strided(fn, x, x_dtype, m, k, ldx)) return s;
   if (overlap(x, strided_bytes(m, k, ldx, x_dtype), y, strided_bytes(m, n, ldy, y_dtype)))
     return invalid(fn, "y overlaps x");
+  if (mx_linear_fuses(m, k)) {
+    if (m == 0 || n == 0) return PSGD_OK;
+    const MxProductArgs p{m, n, k, {nullptr, nullptr}, {w_codes, w_scales}, y, y_dtype, m > 1 ? ldy : n, false};
+    return launch_status(launch_mx_linear_fused(p, x, x_dtype, m > 1 ? ldx : k, stream), fn);
+  }
   const size_t op = linear_operand_bytes(m, k);
   if (psgd_status_t s = check_product_ws(fn, op + mx_product_workspace(m, n, k), ws, bytes)) return s;
   if (m == 0 || n == 0) return PSGD_OK;

@@ -11,6 +11,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "psgd_mx_device.h"
 
 namespace psgd {
@@ -100,12 +102,12 @@ __device__ __forceinline__ void tile_of_block(int b, int ntm, int ntn, int* tm, 
   *tn = in / rows;
 }
 
-template <int ROWS>
+template <int ROWS, int WAVES>
 __device__ __forceinline__ void fetch_chunk(__amdgpu_buffer_rsrc_t rs, uint8_t* lds, uint32_t lane_off, uint32_t lane_off1, uint32_t pitch,
                                             uint32_t chunk_off, int wave) {
 #pragma unroll
-  for (int j = 0; j < ROWS / 32; ++j) {
-    const int row = wave * (ROWS / 4) + j * 8;
+  for (int j = 0; j < ROWS / 8 / WAVES; ++j) {
+    const int row = wave * (ROWS / WAVES) + j * 8;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         rs, (__attribute__((address_space(3))) void*)(lds + row * kChunkBytes), 16,
         (int)((j & 1 ? lane_off1 : lane_off) + (uint32_t)row * pitch + chunk_off), 0, 0, 0);
@@ -181,7 +183,7 @@ __device__ __forceinline__ void add16(float* v, v4u q) {
 // costs.  The row pitch of 8 floats beyond a multiple of 16 puts the two rows
 // that a write covers into opposite banks.  Rows past the end of C lie outside
 // the buffer descriptor, columns past it get an offset outside it.
-template <int DT, int TM, int TN, bool ACC>
+template <int DT, int RE, int TM, int TN, bool ACC>
 __device__ __forceinline__ void mx_store(const MxProductArgs& p, float* lds, int64_t row0, int64_t col0, int lane,
                                          const v16f (&acc)[TM][TN]) {
   using T = typename Elem<DT>::type;
@@ -199,17 +201,19 @@ __device__ __forceinline__ void mx_store(const MxProductArgs& p, float* lds, int
   const float* rd = lds + (lane / LPR) * PITCH + c;
   const uint32_t off = c < cols ? (lane / LPR) * ldb + c * (uint32_t)sizeof(T) : 0x80000000u;
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
+  for (int i = 0; i < TM * (32 / RE); ++i) {  // RE rows: registers e0 .. e0 + RE / 2 of row tile i * RE / 32
+    const int e0 = i * (RE / 2) % 16;
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) wr[((e >> 2) * 8 + (e & 3)) * PITCH + j * 32] = acc[i][j][e];
+      for (int e = 0; e < RE / 2; ++e)
+        wr[((e >> 2) * 8 + (e & 3)) * PITCH + j * 32] = acc[i * RE / 32][j][e0 + e];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     if (wide) {
 #pragma unroll
-      for (int k = 0; k < 32; k += RPI) {
-        const uint32_t o = off + (uint32_t)(i * 32 + k) * ldb;
+      for (int k = 0; k < RE; k += RPI) {
+        const uint32_t o = off + (uint32_t)(i * RE + k) * ldb;
         float v[E];
         __builtin_memcpy(v, __builtin_assume_aligned(rd + k * PITCH, 16), sizeof v);
         if constexpr (ACC) add16<DT>(v, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)o, 0, 0));
@@ -217,10 +221,10 @@ __device__ __forceinline__ void mx_store(const MxProductArgs& p, float* lds, int
       }
     } else {
 #pragma unroll 1
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < RE; ++k) {
 #pragma unroll
         for (uint32_t x = lane; x < COLS; x += 64) {
-          const uint32_t o = x < cols ? (uint32_t)(i * 32 + k) * ldb + x * (uint32_t)sizeof(T) : 0x80000000u;
+          const uint32_t o = x < cols ? (uint32_t)(i * RE + k) * ldb + x * (uint32_t)sizeof(T) : 0x80000000u;
           float v = lds[k * PITCH + x];
           if constexpr (sizeof(T) == 4) {
             if constexpr (ACC) v += __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rc, (int)o, 0, 0));
@@ -237,13 +241,31 @@ __device__ __forceinline__ void mx_store(const MxProductArgs& p, float* lds, int
   }
 }
 
-template <int DT, int TM, int TN, int OCC>
-__global__ __launch_bounds__(256, OCC) void k_mx_prod_lds(MxProductArgs p, int ntm, int ntn) {
-  constexpr int BM = 64 * TM, BN = 64 * TN;
+// Rows of results that a wavefront passes through LDS at a time: 32, or 16
+// where the stages have no room for 32 of each wavefront (rows of TN * 32 + 8
+// floats, as many wavefronts to a stage array as fit).
+template <int WAVES, int TN, int SA, int SB>
+constexpr int mx_epilogue_rows() {
+  constexpr int need = 32 * (TN * 32 + 8) * 4;
+  return 2 * (SA / need + SB / need) >= WAVES ? 32 : 16;
+}
+template <int WAVES, int TN, int SA, int SB>
+__device__ __forceinline__ float* mx_epilogue_lds(int wave, uint8_t* a0, uint8_t* b0, uint8_t* a1, uint8_t* b1) {
+  constexpr int NEED = mx_epilogue_rows<WAVES, TN, SA, SB>() * (TN * 32 + 8) * 4, NA = SA / NEED, NB = SB / NEED;
+  static_assert(2 * (NA + NB) >= WAVES, "stages too small for the results");
+  if (wave < NA) return reinterpret_cast<float*>(a0 + wave * NEED);
+  if (wave < NA + NB) return reinterpret_cast<float*>(b0 + (wave - NA) * NEED);
+  if (wave < 2 * NA + NB) return reinterpret_cast<float*>(a1 + (wave - NA - NB) * NEED);
+  return reinterpret_cast<float*>(b1 + (wave - 2 * NA - NB) * NEED);
+}
+
+template <int DT, int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p, int ntm, int ntn) {
+  constexpr int WAVES = WM * WN, BM = WM * 32 * TM, BN = WN * 32 * TN;
   __shared__ __align__(16) uint8_t a0[BM * kChunkBytes], b0[BN * kChunkBytes], a1[BM * kChunkBytes],
       b1[BN * kChunkBytes];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
   int tm, tn;
   tile_of_block(blockIdx.x, ntm, ntn, &tm, &tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
@@ -262,9 +284,9 @@ __global__ __launch_bounds__(256, OCC) void k_mx_prod_lds(MxProductArgs p, int n
   // a wavefront's scale tiles; past the last tile of rows the last one again
   const uint32_t rtm = (uint32_t)((p.m + 31) / 32 - 1 - m0 / 32), rtn = (uint32_t)((p.n + 31) / 32 - 1 - n0 / 32);
   const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(p.a.scales + m0 / 32 * nch * 256), 0, (int)((min(rtm, 2u * TM - 1) + 1) * nch * 256), 0x00020000);
+      const_cast<uint8_t*>(p.a.scales + m0 / 32 * nch * 256), 0, (int)((min(rtm, (uint32_t)(WM * TM - 1)) + 1) * nch * 256), 0x00020000);
   const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(p.b.scales + n0 / 32 * nch * 256), 0, (int)((min(rtn, 2u * TN - 1) + 1) * nch * 256), 0x00020000);
+      const_cast<uint8_t*>(p.b.scales + n0 / 32 * nch * 256), 0, (int)((min(rtn, (uint32_t)(WN * TN - 1)) + 1) * nch * 256), 0x00020000);
   uint32_t as[TM], bs[TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i) as[i] = min((uint32_t)(wm * TM + i), rtm) * nch * 256;
@@ -311,8 +333,8 @@ __global__ __launch_bounds__(256, OCC) void k_mx_prod_lds(MxProductArgs p, int n
   auto fetch = [&](uint32_t ch, uint8_t* da, uint8_t* db) {
     // no chunk past the last: an offset beyond the descriptor reads nothing
     const uint32_t o = ch < nch ? ch * kChunkBytes : 0x80000000u;
-    fetch_chunk<BM>(ra, da, lane_off, lane_off1, pitch, o, wave);
-    fetch_chunk<BN>(rb, db, lane_off, lane_off1, pitch, o, wave);
+    fetch_chunk<BM, WAVES>(ra, da, lane_off, lane_off1, pitch, o, wave);
+    fetch_chunk<BN, WAVES>(rb, db, lane_off, lane_off1, pitch, o, wave);
   };
   fetch(0, a0, b0);
   __syncthreads();
@@ -327,11 +349,204 @@ __global__ __launch_bounds__(256, OCC) void k_mx_prod_lds(MxProductArgs p, int n
     chunk(a1, b1, a0, b0, ta, tb);
   }
   // (every wavefront is behind its last barrier: the stages are free)
-  float* ep = reinterpret_cast<float*>(wave == 0 ? a0 : wave == 1 ? b0 : wave == 2 ? a1 : b1);
+  constexpr int RE = mx_epilogue_rows<WAVES, TN, sizeof a0, sizeof b0>();
+  float* ep = mx_epilogue_lds<WAVES, TN, sizeof a0, sizeof b0>(wave, a0, b0, a1, b1);
   if (p.accumulate)
-    mx_store<DT, TM, TN, true>(p, ep, m0 + wm * TM * 32, n0 + wn * TN * 32, lane, acc);
+    mx_store<DT, RE, TM, TN, true>(p, ep, m0 + wm * TM * 32, n0 + wn * TN * 32, lane, acc);
   else
-    mx_store<DT, TM, TN, false>(p, ep, m0 + wm * TM * 32, n0 + wn * TN * 32, lane, acc);
+    mx_store<DT, RE, TM, TN, false>(p, ep, m0 + wm * TM * 32, n0 + wn * TN * 32, lane, acc);
+}
+
+// Few rows on one side (up to 128): the product is a stream of the other
+// operand, "wide" here, and this kernel keeps its loads in flight.  One
+// workgroup = 32 rows of the wide operand, its wavefronts take the summed
+// axis' chunks in turn (neighbouring wavefronts read neighbouring 128 bytes of
+// a row) and their partial tiles are added through LDS in wavefront order.
+// The narrow operand comes from memory (XDT < 0), or, for a few thousand
+// values, straight from the activations of type XDT, which every workgroup
+// quantises into LDS by itself: one launch instead of two, and the first
+// loads of the wide operand are already on their way meanwhile.
+struct MxSkinnyArgs {
+  int64_t narrow, wide, k;  // rows of the two operands, summed axis
+  MxOperand x, w;           // narrow (XDT < 0) and wide operand
+  const void* act;          // narrow x k activations, row stride ld (XDT >= 0)
+  int64_t ld;
+  void* c;
+  int64_t sx, sw;           // strides of C along the narrow and the wide operand's rows
+  int dtype;
+  bool accumulate;
+};
+
+// 64 bytes of codes and four scales of one lane's row in one chunk.
+struct MxLane {
+  uint4 q[4];
+  uint32_t s;
+  __device__ __forceinline__ void load(const uint8_t* row, const uint32_t* sc, int64_t ch, int g, int64_t nblk) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q[i] = *reinterpret_cast<const uint4*>(row + min(ch * 8 + 4 * g + i, nblk - 1) * 16);
+    s = sc[ch * 64];
+  }
+};
+__device__ __forceinline__ v16f mx_chunk4(const MxLane& a, const MxLane& b, v16f c) {
+  c = mx_mfma<0>(a.q[0], b.q[0], c, a.s, b.s);
+  c = mx_mfma<1>(a.q[1], b.q[1], c, a.s, b.s);
+  c = mx_mfma<2>(a.q[2], b.q[2], c, a.s, b.s);
+  return mx_mfma<3>(a.q[3], b.q[3], c, a.s, b.s);
+}
+
+// One block of 32 activations (n of them valid) to codes and scale byte.
+template <int DT>
+__device__ __forceinline__ uint32_t mx_quant_block(const typename Elem<DT>::type* p, int n, uint4* q) {
+  using T = typename Elem<DT>::type;
+  T v[32];
+  if (n >= 32 && ((uintptr_t)p & 15) == 0) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 16 / (int)sizeof(T))
+      __builtin_memcpy(&v[i], __builtin_assume_aligned(p + i, 16), 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = i < n ? p[i] : (T)0;
+  }
+  float f[32];
+  uint32_t am = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    f[i] = Elem<DT>::up(v[i]);
+    am = max(am, __float_as_uint(f[i]) & 0x7fffffffu);
+  }
+  const uint32_t sb = mx_scale_byte(am);
+  const float inv = sb == 255u ? 0.f : mx_inv_scale(sb);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = sb == 255u ? 0.f : f[i] * inv;
+  q->x = mx_encode8(f);
+  q->y = mx_encode8(f + 8);
+  q->z = mx_encode8(f + 16);
+  q->w = mx_encode8(f + 24);
+  return sb;
+}
+
+// Activations that a workgroup quantises by itself: at most this many blocks,
+// two for each thread of a workgroup of 512.  (Every workgroup repeats the
+// work; from here on a launch of its own is cheaper.)
+constexpr int kFusedBlocks = 1024;
+
+template <int MT, int XDT>
+__global__ __launch_bounds__(1024 / MT) void k_mx_prod_skinny(MxSkinnyArgs p) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int waves = blockDim.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, g = lane >> 5;
+  const int64_t w0 = (int64_t)blockIdx.x * 32;
+  const int64_t nch = mx_chunks(p.k), nblk = mx_blocks(p.k), pitch = nblk * 16;
+  const uint8_t* wrow = p.w.codes + min(w0 + r, p.wide - 1) * pitch;
+  const uint32_t* wsc = reinterpret_cast<const uint32_t*>(p.w.scales) + blockIdx.x * nch * 64 + lane;
+  MxLane w;
+  int64_t ch = wave;
+  if (ch < nch) w.load(wrow, wsc, ch, g, nblk);
+  uint8_t* xs = lds + kFusedBlocks * 16;  // scales: chunk-wise dwords per row, as in an operand's tiles
+  if constexpr (XDT >= 0) {
+    using T = typename Elem < XDT < 0 ? 0 : XDT > ::type;
+    const T* act = static_cast<const T*>(p.act);
+    const int total = (int)(p.narrow * nch * 8);  // (blocks past the last get scale 0)
+    for (int i = threadIdx.x; i < total; i += blockDim.x) {
+      const int row = i / (int)(nch * 8), b = i % (int)(nch * 8);
+      uint32_t sb = 0;
+      if (b < nblk)
+        sb = mx_quant_block < XDT < 0 ? 0 : XDT > (act + row * p.ld + b * 32, (int)min((int64_t)32, p.k - b * 32),
+                                                  reinterpret_cast<uint4*>(lds) + row * nblk + b);
+      xs[((b >> 2) * (int)p.narrow + row) * 4 + (b & 3)] = (uint8_t)sb;
+    }
+    __syncthreads();
+  }
+  const uint8_t* xrow[MT];
+  const uint32_t* xsc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    xrow[t] = p.x.codes + min((int64_t)t * 32 + r, p.narrow - 1) * pitch;
+    xsc[t] = reinterpret_cast<const uint32_t*>(p.x.scales) + min((int64_t)t, (p.narrow - 1) / 32) * nch * 64 + lane;
+  }
+  v16f acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[t][e] = 0.f;
+  for (; ch < nch; ch += waves) {
+    const MxLane cur = w;
+    if (ch + waves < nch) w.load(wrow, wsc, ch + waves, g, nblk);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      MxLane x;
+      if constexpr (XDT >= 0) {
+        const int row = min(r, (int)p.narrow - 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x.q[i] = reinterpret_cast<const uint4*>(lds)[row * nblk + min(ch * 8 + 4 * g + i, nblk - 1)];
+        x.s = reinterpret_cast<const uint32_t*>(xs)[(ch * 2 + g) * p.narrow + row];
+      } else {
+        x.load(xrow[t], xsc[t], ch, g, nblk);
+      }
+      acc[t] = mx_chunk4(x, cur, acc[t]);
+    }
+  }
+  if constexpr (XDT >= 0) __syncthreads();  // (the quantised activations' LDS is reused)
+  float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) red[((wave * MT + t) * 16 + e) * 64 + lane] = acc[t][e];
+  __syncthreads();
+  // tile element (narrow row i, wide row j) = lane (i / 4 % 2) * 32 + j, register i / 8 * 4 + i % 4
+  for (int o = threadIdx.x; o < MT * 1024; o += blockDim.x) {
+    const int i = p.sw == 1 ? o / 32 % 32 : o % 32, j = p.sw == 1 ? o % 32 : o / 32 % 32, t = o / 1024;
+    const int64_t row = t * 32 + i, col = w0 + j;
+    if (row >= p.narrow || col >= p.wide) continue;
+    const int at = (t * 16 + i / 8 * 4 + i % 4) * 64 + (i / 4 % 2) * 32 + j;
+    float v = 0.f;
+    for (int k = 0; k < waves; ++k) v += red[k * MT * 1024 + at];
+    const int64_t ci = row * p.sx + col * p.sw;
+    if (p.dtype == kF32)
+      store_c<kF32>(p.c, ci, v, p.accumulate);
+    else if (p.dtype == kBF16)
+      store_c<kBF16>(p.c, ci, v, p.accumulate);
+    else
+      store_c<kF16>(p.c, ci, v, p.accumulate);
+  }
+}
+
+// Wavefronts per workgroup: enough in all to keep some 2048 of them loading
+// (a wavefront has 4 KB in flight), at most 16, and no more than LDS has room
+// for MT partial tiles of each, nor than there are chunks.
+template <int MT, int XDT>
+static void skinny(const MxSkinnyArgs& p, hipStream_t s) {
+  const int64_t tiles = (p.wide + 31) / 32, nch = mx_chunks(p.k);
+  int waves = 4;
+  while (waves < 16 / MT && waves * tiles < 2048 && waves < nch) waves *= 2;
+  size_t lds = (size_t)waves * MT * 4096;
+  if (XDT >= 0) lds = std::max<size_t>(lds, kFusedBlocks * 17 + 1024 * 4);
+  hipLaunchKernelGGL((k_mx_prod_skinny<MT, XDT>), dim3((unsigned)tiles), dim3(64 * waves), lds, s, p);
+}
+
+static void product_skinny(const MxSkinnyArgs& p, hipStream_t s) {
+  if (p.narrow <= 32)
+    skinny<1, -1>(p, s);
+  else if (p.narrow <= 64)
+    skinny<2, -1>(p, s);
+  else
+    skinny<4, -1>(p, s);
+}
+
+bool mx_linear_fuses(int64_t m, int64_t k) { return m <= 32 && k > 0 && m * mx_chunks(k) * 8 <= kFusedBlocks; }
+
+hipError_t launch_mx_linear_fused(const MxProductArgs& p, const void* x, int x_dtype, int64_t ldx, hipStream_t s) {
+  MxSkinnyArgs a{p.m, p.n, p.k, {nullptr, nullptr}, p.b, x, ldx, p.c, p.ldc, 1, p.dtype, false};
+  if (x_dtype == kF32)
+    skinny<1, kF32>(a, s);
+  else if (x_dtype == kBF16)
+    skinny<1, kBF16>(a, s);
+  else
+    skinny<1, kF16>(a, s);
+  return hipGetLastError();
 }
 
 // An empty sum: C = 0, or C unchanged.
@@ -343,6 +558,14 @@ __global__ __launch_bounds__(256) void k_mx_prod_zero(MxProductArgs p) {
 
 size_t mx_product_workspace(int64_t, int64_t, int64_t) { return 0; }
 
+template <int DT, int WM, int WN, int TM, int TN>
+static void product_lds(const MxProductArgs& p, hipStream_t s) {
+  constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
+  const int ntm = (int)((p.m + BM - 1) / BM), ntn = (int)((p.n + BN - 1) / BN);
+  hipLaunchKernelGGL((k_mx_prod_lds<DT, WM, WN, TM, TN>), dim3((unsigned)(ntm * ntn)), dim3(64 * WM * WN), 0, s, p, ntm,
+                     ntn);
+}
+
 template <int DT>
 static void product_dt(const MxProductArgs& p, hipStream_t s) {
   if (p.k == 0) {
@@ -350,9 +573,25 @@ static void product_dt(const MxProductArgs& p, hipStream_t s) {
       hipLaunchKernelGGL((k_mx_prod_zero<DT>), dim3((unsigned)((p.m * p.n + 255) / 256)), dim3(256), 0, s, p);
     return;
   }
-  if (p.m >= 256 && p.n >= 256 && mx_pitch(p.k) * 256 <= INT32_MAX && p.ldc * 4 * 128 <= INT32_MAX) {
-    const int ntm = (int)((p.m + 255) / 256), nt = (int)((p.n + 255) / 256);
-    hipLaunchKernelGGL((k_mx_prod_lds<DT, 4, 4, 1>), dim3((unsigned)(ntm * nt)), dim3(256), 0, s, p, ntm, nt);
+  if (p.m <= 128 || p.n <= 128) {
+    // the side with fewer rows is the narrow one; C's strides follow it
+    if (p.m <= p.n)
+      product_skinny(MxSkinnyArgs{p.m, p.n, p.k, p.a, p.b, nullptr, 0, p.c, p.ldc, 1, p.dtype, p.accumulate}, s);
+    else
+      product_skinny(MxSkinnyArgs{p.n, p.m, p.k, p.b, p.a, nullptr, 0, p.c, 1, p.ldc, p.dtype, p.accumulate}, s);
+    return;
+  }
+  if (mx_pitch(p.k) * 256 <= INT32_MAX && p.ldc * 4 * 128 <= INT32_MAX) {
+    // 256 x 256 tiles where they occupy more than half of the 256 compute
+    // units; fewer are halved (2048 x 4096 x 11008: 128 tiles 70 us, 256
+    // halves 62 us; 2048 x 11008 x 4096: 344 tiles 64 us, 688 halves 72 us).
+    const int64_t nt = ((p.m + 255) / 256) * ((p.n + 255) / 256);
+    if (nt > 128)
+      product_lds<DT, 2, 4, 4, 2>(p, s);
+    else if (nt > 32)
+      product_lds<DT, 2, 2, 2, 4>(p, s);
+    else
+      product_lds<DT, 2, 2, 2, 2>(p, s);
     return;
   }
   const int ntn = (int)((p.n + 63) / 64);

@@ -60,6 +60,10 @@ struct MxProductArgs {
   bool accumulate;
 };
 hipError_t launch_mx_product(const MxProductArgs& p, void* ws, hipStream_t s);
+// y = Q(x) B^T in one launch, for so few activations that every workgroup
+// quantises them by itself (mx_linear_fuses); p.a is not read.
+bool mx_linear_fuses(int64_t m, int64_t k);
+hipError_t launch_mx_linear_fused(const MxProductArgs& p, const void* x, int x_dtype, int64_t ldx, hipStream_t s);
 size_t mx_product_workspace(int64_t m, int64_t n, int64_t k);
 
 }  // namespace psgd

@@ -5,6 +5,7 @@ computation runs in libpsgd.so, on the current stream of the tensors' device.
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -23,6 +24,38 @@ def _dtype(t: torch.Tensor) -> int:
 
 def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+# The raw handle without building a Stream object, where this PyTorch has it:
+# small calls are bound by the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(device: torch.device, fn, *args) -> None:
+    """fn(*args, stream) with `device` current, on its current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            fn(*args, _stream(device))
+    else:
+        fn(*args, _raw_stream(device.index) if _raw_stream is not None else _stream(device))
+
+
+@functools.lru_cache(maxsize=4096)
+def _product_workspace(m: int, n: int, k: int) -> int:
+    return B.psgd_mx_product_workspace(m, n, k)
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_workspace(m: int, n: int, k: int) -> int:
+    return B.psgd_mx_linear_workspace(m, n, k)
+
+
+def _scratch(nbytes: int, device: torch.device):
+    """(tensor, address) of nbytes of scratch; (None, 0) for none."""
+    if nbytes == 0:
+        return None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr()
 
 
 def _matrix(x: torch.Tensor, name: str) -> int:
@@ -94,21 +127,20 @@ class GradientClip:
         with torch.cuda.device(self.device):
             self._bind(grads, outs)
 
-    def _call(self, fn, max_norm: float, scale: float) -> torch.Tensor:
+    def _run(self, fn, max_norm: float, scale: float) -> torch.Tensor:
         stats = torch.empty(2 + len(self._numel), dtype=torch.float32, device=self.device)
-        with torch.cuda.device(self.device):
-            fn(self.handle, float(max_norm), float(scale), stats.data_ptr(), self.workspace.data_ptr(), self.ws_bytes,
-               _stream(self.device))
+        _call(self.device, fn, self.handle, max_norm, scale, stats.data_ptr(), self.workspace.data_ptr(),
+              self.ws_bytes)
         return stats
 
     def norm(self, max_norm: float = float("inf"), scale: float = 1.0) -> torch.Tensor:
         """float32 (2 + n) on the device: the global norm of scale * grads, the
         coefficient that max_norm asks for, then every tensor's norm."""
-        return self._call(B.psgd_clip_norm, max_norm, scale)
+        return self._run(B.psgd_clip_norm, max_norm, scale)
 
     def clip(self, max_norm: float, scale: float = 1.0) -> torch.Tensor:
         """The same, and outs = scale * coefficient * grads."""
-        return self._call(B.psgd_clip_apply, max_norm, scale)
+        return self._run(B.psgd_clip_apply, max_norm, scale)
 
     def close(self) -> None:
         if self.handle:
@@ -126,27 +158,36 @@ class GradientClip:
 class MxTensor:
     """A rows x cols operand: codes and scales as psgd.h lays them out."""
 
-    __slots__ = ("rows", "cols", "codes", "scales")
+    __slots__ = ("rows", "cols", "buf", "device", "codes_ptr", "scales_ptr")
 
-    def __init__(self, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor):
-        self.rows, self.cols, self.codes, self.scales = rows, cols, codes, scales
+    def __init__(self, rows: int, cols: int, device):
+        """Uninitialised operand: one allocation, the scales behind the codes
+        at a multiple of 256 bytes."""
+        off = self._scales_at(rows, cols)
+        self.rows, self.cols = rows, cols
+        self.buf = torch.empty(off + (rows + 31) // 32 * ((cols + 255) // 256) * 256, dtype=torch.uint8, device=device)
+        self.device = self.buf.device
+        self.codes_ptr = self.buf.data_ptr()
+        self.scales_ptr = self.codes_ptr + off
 
     @staticmethod
-    def empty(rows: int, cols: int, device) -> "MxTensor":
-        nblk, nch = (cols + 31) // 32, (cols + 255) // 256
-        code_bytes, scale_bytes = rows * nblk * 16, (rows + 31) // 32 * nch * 256
-        # one allocation; the scales start at a multiple of 256 bytes
-        off = (code_bytes + 255) & ~255
-        buf = torch.empty(off + scale_bytes, dtype=torch.uint8, device=device)
-        return MxTensor(rows, cols, buf[:code_bytes], buf[off:])
-
-    @property
-    def device(self) -> torch.device:
-        return self.codes.device
+    def _scales_at(rows: int, cols: int) -> int:
+        return (rows * ((cols + 31) // 32) * 16 + 255) & ~255
 
     @property
     def shape(self) -> Tuple[int, int]:
         return self.rows, self.cols
+
+    @property
+    def codes(self) -> torch.Tensor:
+        """The codes' bytes, rows x (16 per block)."""
+        n = (self.cols + 31) // 32 * 16
+        return self.buf[:self.rows * n].view(self.rows, n)
+
+    @property
+    def scales(self) -> torch.Tensor:
+        """The scales' bytes, in the tiles of psgd.h."""
+        return self.buf[self._scales_at(self.rows, self.cols):]
 
 
 def _rand(rand: Optional[torch.Tensor], x: torch.Tensor) -> int:
@@ -164,11 +205,10 @@ def _quantize(x, rand, row: Optional[MxTensor], col: Optional[MxTensor], values)
         if values.shape != x.shape or values.dtype != x.dtype or values.device != x.device:
             raise ValueError("values must have x's shape, type and device")
         ldv = _matrix(values, "values")
-    with torch.cuda.device(x.device):
-        B.psgd_mx_quantize(x.data_ptr(), _dtype(x), x.shape[0], x.shape[1], ld, _rand(rand, x),
-                           row.codes.data_ptr() if row else 0, row.scales.data_ptr() if row else 0,
-                           col.codes.data_ptr() if col else 0, col.scales.data_ptr() if col else 0,
-                           values.data_ptr() if values is not None else 0, ldv, _stream(x.device))
+    rows, cols = x.shape
+    _call(x.device, B.psgd_mx_quantize, x.data_ptr(), _dtype(x), rows, cols, ld, _rand(rand, x),
+          row.codes_ptr if row else 0, row.scales_ptr if row else 0, col.codes_ptr if col else 0,
+          col.scales_ptr if col else 0, values.data_ptr() if values is not None else 0, ldv)
 
 
 def mx_quantize(x: torch.Tensor, rand: Optional[torch.Tensor] = None,
@@ -176,7 +216,7 @@ def mx_quantize(x: torch.Tensor, rand: Optional[torch.Tensor] = None,
     """The operand of x: blocks of 32 along its rows.  rand: uint8 of x's shape
     for stochastic rounding (None: nearest).  values: receives the values that
     the codes stand for (x's shape and type; may be x itself)."""
-    q = MxTensor.empty(x.shape[0], x.shape[-1], x.device)
+    q = MxTensor(x.shape[0], x.shape[-1], x.device)
     _quantize(x, rand, q, None, values)
     return q
 
@@ -184,14 +224,14 @@ def mx_quantize(x: torch.Tensor, rand: Optional[torch.Tensor] = None,
 def mx_quantize_both(x: torch.Tensor, rand: Optional[torch.Tensor] = None) -> Tuple[MxTensor, MxTensor]:
     """The operands of x and of x^T (blocks along x's rows and along its
     columns), from one reading of x."""
-    q, t = MxTensor.empty(x.shape[0], x.shape[-1], x.device), MxTensor.empty(x.shape[-1], x.shape[0], x.device)
+    q, t = MxTensor(x.shape[0], x.shape[-1], x.device), MxTensor(x.shape[-1], x.shape[0], x.device)
     _quantize(x, rand, q, t, None)
     return q, t
 
 
 def mx_quantize_t(x: torch.Tensor, rand: Optional[torch.Tensor] = None) -> MxTensor:
     """The operand of x^T: blocks of 32 along x's columns."""
-    t = MxTensor.empty(x.shape[-1], x.shape[0], x.device)
+    t = MxTensor(x.shape[-1], x.shape[0], x.device)
     _quantize(x, rand, None, t, None)
     return t
 
@@ -203,9 +243,7 @@ def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.float32, out: Optional
     elif out.shape != q.shape or out.device != q.device:
         raise ValueError("out must have the operand's shape and device")
     ld = _matrix(out, "out")
-    with torch.cuda.device(q.device):
-        B.psgd_mx_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, out.data_ptr(), _dtype(out), ld,
-                             _stream(q.device))
+    _call(q.device, B.psgd_mx_dequantize, q.codes_ptr, q.scales_ptr, q.rows, q.cols, out.data_ptr(), _dtype(out), ld)
     return out
 
 
@@ -227,12 +265,10 @@ def mx_product(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dty
     m, n, k = a.rows, b.rows, a.cols
     c = _result(out, m, n, dtype, a.device)
     ldc = _matrix(c, "out")
-    need = B.psgd_mx_product_workspace(m, n, k)
-    ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
-    with torch.cuda.device(a.device):
-        B.psgd_mx_product(m, n, k, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
-                          c.data_ptr(), _dtype(c), ldc, accumulate, ws.data_ptr() if need else 0, need,
-                          _stream(a.device))
+    need = _product_workspace(m, n, k)
+    ws, ws_ptr = _scratch(need, a.device)
+    _call(a.device, B.psgd_mx_product, m, n, k, a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, c.data_ptr(),
+          _dtype(c), ldc, accumulate, ws_ptr, need)
     return c
 
 
@@ -245,11 +281,10 @@ def mx_linear(x: torch.Tensor, w: MxTensor, out: Optional[torch.Tensor] = None,
     if k != w.cols or x.device != w.device:
         raise ValueError(f"x has {k} columns on {x.device}, the weights {w.cols} on {w.device}")
     y = _result(out, m, w.rows, dtype or x.dtype, x.device)
-    need = B.psgd_mx_linear_workspace(m, w.rows, k)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    with torch.cuda.device(x.device):
-        B.psgd_mx_linear(m, w.rows, k, x.data_ptr(), _dtype(x), ldx, w.codes.data_ptr(), w.scales.data_ptr(),
-                         y.data_ptr(), _dtype(y), _matrix(y, "out"), ws.data_ptr(), need, _stream(x.device))
+    need = _linear_workspace(m, w.rows, k)
+    ws, ws_ptr = _scratch(need, x.device)
+    _call(x.device, B.psgd_mx_linear, m, w.rows, k, x.data_ptr(), _dtype(x), ldx, w.codes_ptr, w.scales_ptr,
+          y.data_ptr(), _dtype(y), _matrix(y, "out"), ws_ptr, need)
     return y
 
 
