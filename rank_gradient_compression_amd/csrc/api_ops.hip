@@ -12,6 +12,7 @@
 
 #include "psgd_clip.h"
 #include "psgd_internal.h"
+#include "psgd_kernels.h"
 #include "psgd_mx.h"
 
 namespace psgd {
@@ -89,32 +90,38 @@ extern "C" psgd_status_t psgd_clip_create(int32_t ntensors, const int64_t* numel
   psgd_clip* c = nullptr;
   try {
     c = new psgd_clip;
-    // Tiles of a power of two of elements, at least 8192 (eight 16-byte loads
-    // of fp32 per thread) and so many that a large set has at most about 4096
-    // tiles: the one workgroup that joins their sums stays short.
-    int64_t tile = 8192;
-    while (tile < (int64_t(1) << 30) && total / tile > 4096) tile *= 2;
-    c->tile = (int32_t)tile;
     c->tensors.resize((size_t)ntensors);
-    int64_t ntiles = 0;
+    int64_t nsums = 0, nchunks = 0, bytes = 0;
     for (int32_t t = 0; t < ntensors; ++t) {
-      ClipTensor& d = c->tensors[(size_t)t];
-      const int64_t n = (numel[t] + tile - 1) / tile;
-      d = ClipTensor{nullptr, nullptr, numel[t], in_dtypes[t], out_dtypes[t], (int32_t)ntiles, (int32_t)n};
-      ntiles += n;
-      if (ntiles > kMaxGrid / 2) {
+      const int64_t n = numel[t], chunks = (n + kClipChunk - 1) / kClipChunk;
+      // its share of the norm's workgroups, by size
+      const int64_t share = n == 0 ? 0 : (int64_t)((double)n / (double)total * kClipSumGroups) + 1;
+      const int64_t groups = std::min(chunks, share);
+      if (nchunks + chunks > kMaxGrid) {
         delete c;
         return invalid(fn, "the set is too large");
       }
-      c->map.insert(c->map.end(), (size_t)n, t);
+      c->tensors[(size_t)t] = ClipTensor{nullptr,          nullptr,         n, in_dtypes[t], out_dtypes[t],
+                                         (int32_t)nsums, (int32_t)groups, (int32_t)nchunks, 0};
+      c->sum_map.insert(c->sum_map.end(), (size_t)groups, t);
+      c->chunk_map.insert(c->chunk_map.end(), (size_t)chunks, t);
+      nsums += groups;
+      nchunks += chunks;
+      bytes += n * dtype_bytes(in_dtypes[t]);
     }
+    c->stream = bytes > kStreamHintBytes;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
-    c->lay.map_off = up(c->tensors.size() * sizeof(ClipTensor));
-    c->lay.sums_off = c->lay.map_off + up(c->map.size() * sizeof(int32_t));
-    c->lay.bytes = std::max<size_t>(256, c->lay.sums_off + up(c->map.size() * sizeof(double)));
+    c->lay.sum_map_off = up(c->tensors.size() * sizeof(ClipTensor));
+    c->lay.chunk_map_off = c->lay.sum_map_off + up(c->sum_map.size() * sizeof(int32_t));
+    c->lay.sums_off = c->lay.chunk_map_off + up(c->chunk_map.size() * sizeof(int32_t));
+    c->lay.bytes = std::max<size_t>(256, c->lay.sums_off + up(c->sum_map.size() * sizeof(double)));
     c->tables.assign(c->lay.sums_off, 0);
-    if (!c->tensors.empty()) memcpy(c->tables.data(), c->tensors.data(), c->tensors.size() * sizeof(ClipTensor));
-    if (!c->map.empty()) memcpy(c->tables.data() + c->lay.map_off, c->map.data(), c->map.size() * sizeof(int32_t));
+    auto put = [&](size_t off, const void* p, size_t n) {
+      if (n) memcpy(c->tables.data() + off, p, n);
+    };
+    put(0, c->tensors.data(), c->tensors.size() * sizeof(ClipTensor));
+    put(c->lay.sum_map_off, c->sum_map.data(), c->sum_map.size() * sizeof(int32_t));
+    put(c->lay.chunk_map_off, c->chunk_map.data(), c->chunk_map.size() * sizeof(int32_t));
   } catch (const std::bad_alloc&) {
     delete c;
     return invalid(fn, "out of host memory");
@@ -206,11 +213,13 @@ static ClipArgs clip_args(const psgd_clip* c, void* ws, float scale, float max_n
   char* b = static_cast<char*>(ws);
   ClipArgs a{};
   a.tensors = reinterpret_cast<const ClipTensor*>(b);
-  a.map = reinterpret_cast<const int32_t*>(b + c->lay.map_off);
+  a.sum_map = reinterpret_cast<const int32_t*>(b + c->lay.sum_map_off);
+  a.chunk_map = reinterpret_cast<const int32_t*>(b + c->lay.chunk_map_off);
   a.sums = reinterpret_cast<double*>(b + c->lay.sums_off);
   a.ntensors = (int32_t)c->tensors.size();
-  a.ntiles = (int32_t)c->map.size();
-  a.tile = c->tile;
+  a.nsums = (int32_t)c->sum_map.size();
+  a.nchunks = (int32_t)c->chunk_map.size();
+  a.stream = c->stream;
   a.scale = scale;
   a.max_norm = max_norm;
   a.stats = stats;

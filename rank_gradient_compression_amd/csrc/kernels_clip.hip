@@ -3,12 +3,12 @@
 //   n_t = || scale * g_t ||,  N = sqrt(sum n_t^2),  c = min(1, max_norm / (N + 1e-6)),
 //   out_t = scale * c * g_t
 //
-// Three launches: sums of squares per tile, their fixed-order sum (one
-// workgroup), the scaled write.  Squares are summed in fp64: an fp32 square
-// overflows from 1.8e19 on, and the one conversion per element is hidden
-// behind the reads.  Bound: HBM, the gradients read twice (once if the last
-// level of cache holds them) and written once.  Sums are made in a fixed
-// order without atomics, so a repeated call agrees bit for bit.
+// Three launches: sums of squares, their fixed-order sum (one workgroup), the
+// scaled write.  Squares are summed in fp64: an fp32 square overflows from
+// 1.8e19 on, and the one conversion per element is hidden behind the reads.
+// Bound: HBM, the gradients read twice (the second reading from the last level
+// of cache as far as it holds them) and written once.  Sums are made in a
+// fixed order without atomics, so a repeated call agrees bit for bit.
 
 #include <hip/hip_runtime.h>
 
@@ -24,73 +24,107 @@ __global__ __launch_bounds__(256) void k_clip_bind(ClipTensor* tensors, ClipPoin
   tensors[first + i].out = p.out[i];
 }
 
-// Calls f(i, values, valid) for every group of E consecutive elements of the
-// tile [e0, e1) that this thread takes; 16-byte loads where the address allows.
-template <int DT, int E, int UNROLL, typename F>
+// E consecutive elements from p, as one access.
+template <int DT, int E, bool NT>
+__device__ __forceinline__ void load_group(const typename Elem<DT>::type* p, typename Elem<DT>::type (&v)[E]) {
+  using T = typename Elem<DT>::type;
+  typedef uint32_t vec __attribute__((ext_vector_type(E * sizeof(T) / 4)));
+  const vec* q = reinterpret_cast<const vec*>(p);
+  const vec x = NT ? __builtin_nontemporal_load(q) : *q;
+  __builtin_memcpy(v, &x, sizeof x);
+}
+
+// Calls f(i, values, valid) for the groups of E consecutive elements that this
+// thread takes of the elements [e0, e1), e1 - e0 <= kClipChunk: all loads
+// first.  Groups that do not start on E elements' bytes are read one element
+// at a time.
+template <int DT, int E, bool NT, typename F>
 __device__ __forceinline__ void walk(const void* base, int64_t e0, int64_t e1, F f) {
   using T = typename Elem<DT>::type;
-  const T* g = static_cast<const T*>(base);
-  const bool wide = ((uintptr_t)(g + e0) & (E * sizeof(T) - 1)) == 0;
-  for (int64_t i0 = e0; i0 < e1; i0 += 256 * E * UNROLL) {
+  constexpr int UNROLL = kClipChunk / 256 / E;
+  const T* g = static_cast<const T*>(base) + e0;
+  const int n = (int)(e1 - e0);
+  if (((uintptr_t)g & (E * sizeof(T) - 1)) == 0 && n == kClipChunk) {
     T v[UNROLL][E];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int64_t i = i0 + (u * 256 + (int)threadIdx.x) * E;
-      if (wide && i + E <= e1) {
-        __builtin_memcpy(v[u], __builtin_assume_aligned(g + i, E * sizeof(T)), E * sizeof(T));
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j) v[u][j] = i + j < e1 ? g[i + j] : (T)0;
-      }
-    }
+    for (int u = 0; u < UNROLL; ++u) load_group<DT, E, NT>(g + (u * 256 + (int)threadIdx.x) * E, v[u]);
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      const int64_t i = i0 + (u * 256 + (int)threadIdx.x) * E;
       float x[E];
 #pragma unroll
       for (int j = 0; j < E; ++j) x[j] = Elem<DT>::up(v[u][j]);
-      if (i < e1) f(i, x, (int)min((int64_t)E, e1 - i));
+      f(e0 + (u * 256 + (int)threadIdx.x) * E, x, E);
+    }
+  } else {
+    for (int i = (int)threadIdx.x * E; i < n; i += 256 * E) {
+      float x[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] = i + j < n ? Elem<DT>::up(g[i + j]) : 0.f;
+      f(e0 + i, x, min(E, n - i));
     }
   }
 }
 
-__device__ __forceinline__ double block_sum(double s) {
+template <int DT, bool NT>
+__device__ __forceinline__ double chunk_squares(const ClipTensor& t, int first) {
+  constexpr int E = 16 / dtype_bytes(DT);
+  double s0 = 0, s1 = 0;
+  for (int64_t e0 = (int64_t)first * kClipChunk; e0 < t.numel; e0 += (int64_t)t.nsums * kClipChunk)
+    walk<DT, E, NT>(t.in, e0, min(t.numel, e0 + kClipChunk), [&](int64_t, const float(&x)[E], int) {
+#pragma unroll
+      for (int j = 0; j < E; j += 2) {
+        s0 = fma((double)x[j], (double)x[j], s0);
+        s1 = fma((double)x[j + 1], (double)x[j + 1], s1);
+      }
+    });
+  return s0 + s1;
+}
+
+// Workgroup i of a tensor takes the chunks i, i + nsums, ...: the workgroups
+// that run together read one moving front of the tensor.
+template <bool NT>
+__global__ __launch_bounds__(256) void k_clip_sums(ClipArgs a) {
+  const ClipTensor t = a.tensors[a.sum_map[blockIdx.x]];
+  const int first = (int)blockIdx.x - t.first_sum;
+  double s = t.in_dtype == kF32    ? chunk_squares<kF32, NT>(t, first)
+             : t.in_dtype == kBF16 ? chunk_squares<kBF16, NT>(t, first)
+                                   : chunk_squares<kF16, NT>(t, first);
   __shared__ double w[4];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
   if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = s;
   __syncthreads();
-  return (w[0] + w[1]) + (w[2] + w[3]);
+  if (threadIdx.x == 0) a.sums[blockIdx.x] = (w[0] + w[1]) + (w[2] + w[3]);
 }
 
-__global__ __launch_bounds__(256) void k_clip_sums(ClipArgs a) {
-  const int tile = blockIdx.x;
-  const ClipTensor t = a.tensors[a.map[tile]];
-  const int64_t e0 = (int64_t)(tile - t.first_tile) * a.tile, e1 = min(t.numel, e0 + a.tile);
-  double s = 0;
-  auto add = [&](int64_t, auto& x, int) {
-    for (float v : x) s = fma((double)v, (double)v, s);
-  };
-  if (t.in_dtype == kF32)
-    walk<kF32, 4, 4>(t.in, e0, e1, add);
-  else if (t.in_dtype == kBF16)
-    walk<kBF16, 8, 4>(t.in, e0, e1, add);
-  else
-    walk<kF16, 8, 4>(t.in, e0, e1, add);
-  s = block_sum(s);
-  if (threadIdx.x == 0) a.sums[tile] = s;
-}
-
-// One workgroup: wavefront w sums the tiles of tensors w, w + 16, ... and
-// the tensors' sums are added in order.
+// One workgroup: all sums into LDS at once (in one wait for memory), then
+// wavefront w adds those of tensors w, w + 16, ... and the tensors' sums are
+// added in order.  Sums beyond LDS (lists of thousands of tensors) are read
+// where they are.
 __global__ __launch_bounds__(1024) void k_clip_final(ClipArgs a) {
   __shared__ double part[16];
+  __shared__ double lds[kClipSumGroups + 1024];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  constexpr int N = (kClipSumGroups + 1024) / 1024;
+  double v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int at = i * 1024 + (int)threadIdx.x;
+    v[i] = at < a.nsums ? a.sums[at] : 0.0;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) lds[i * 1024 + threadIdx.x] = v[i];
+  __syncthreads();
   double tot = 0;
   for (int t = w; t < a.ntensors; t += 16) {
-    const int f = a.tensors[t].first_tile, n = a.tensors[t].ntiles;
+    const int f = a.tensors[t].first_sum, n = a.tensors[t].nsums;
     double s = 0;
-    for (int i = lane; i < n; i += 64) s += a.sums[f + i];
+    if (f + n <= N * 1024) {
+#pragma unroll 8
+      for (int i = lane; i < n; i += 64) s += lds[f + i];
+    } else {
+      for (int i = lane; i < n; i += 64) s += a.sums[f + i];
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
     tot += s;
@@ -108,41 +142,52 @@ __global__ __launch_bounds__(1024) void k_clip_final(ClipArgs a) {
   }
 }
 
-template <int DT, int E>
-__device__ __forceinline__ void store_group(void* base, int64_t i, const float (&x)[E], float c, int n) {
-  using T = typename Elem<DT>::type;
-  T* o = static_cast<T*>(base) + i;
-  T v[E];
+// One chunk, from type IN to type OUT, in groups of 16 bytes of the wider
+// one, so that the loads and the stores of a wavefront are contiguous.
+template <int IN, int OUT, bool NT>
+__device__ __forceinline__ void scale_chunk(const ClipTensor& t, int64_t e0, float c) {
+  constexpr int E = 16 / (dtype_bytes(IN) > dtype_bytes(OUT) ? dtype_bytes(IN) : dtype_bytes(OUT));
+  using T = typename Elem<OUT>::type;
+  typedef uint32_t vec __attribute__((ext_vector_type(E * sizeof(T) / 4)));
+  walk<IN, E, NT>(t.in, e0, min(t.numel, e0 + kClipChunk), [&](int64_t i, const float(&x)[E], int n) {
+    T* o = static_cast<T*>(t.out) + i;
+    T v[E];
 #pragma unroll
-  for (int j = 0; j < E; ++j) v[j] = Elem<DT>::down(x[j] * c);
-  if (n == E && ((uintptr_t)o & (E * sizeof(T) - 1)) == 0) {
-    __builtin_memcpy(__builtin_assume_aligned(o, E * sizeof(T)), v, E * sizeof(T));
-  } else {
+    for (int j = 0; j < E; ++j) v[j] = Elem<OUT>::down(x[j] * c);
+    if (n == E && ((uintptr_t)o & (sizeof(vec) - 1)) == 0) {
+      vec q;
+      __builtin_memcpy(&q, v, sizeof q);
+      if (NT)
+        __builtin_nontemporal_store(q, reinterpret_cast<vec*>(o));
+      else
+        *reinterpret_cast<vec*>(o) = q;
+    } else {
 #pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (j < n) o[j] = v[j];
-  }
+      for (int j = 0; j < E; ++j)
+        if (j < n) o[j] = v[j];
+    }
+  });
 }
 
+// Workgroups run through the chunks from the last to the first: the norm's
+// pass has read the last ones last, and the cache still holds them.
+template <bool NT>
 __global__ __launch_bounds__(256) void k_clip_apply(ClipArgs a) {
-  const int tile = blockIdx.x;
-  const ClipTensor t = a.tensors[a.map[tile]];
-  const int64_t e0 = (int64_t)(tile - t.first_tile) * a.tile, e1 = min(t.numel, e0 + a.tile);
+  const int chunk = a.nchunks - 1 - (int)blockIdx.x;
+  const ClipTensor t = a.tensors[a.chunk_map[chunk]];
+  const int64_t e0 = (int64_t)(chunk - t.first_chunk) * kClipChunk;
   const float c = a.stats[1] * a.scale;
-  auto put = [&](int64_t i, auto& x, int n) {
-    if (t.out_dtype == kF32)
-      store_group<kF32>(t.out, i, x, c, n);
-    else if (t.out_dtype == kBF16)
-      store_group<kBF16>(t.out, i, x, c, n);
-    else
-      store_group<kF16>(t.out, i, x, c, n);
-  };
-  if (t.in_dtype == kF32)
-    walk<kF32, 4, 4>(t.in, e0, e1, put);
-  else if (t.in_dtype == kBF16)
-    walk<kBF16, 8, 4>(t.in, e0, e1, put);
-  else
-    walk<kF16, 8, 4>(t.in, e0, e1, put);
+  switch (t.in_dtype * 3 + t.out_dtype) {
+    case kF32 * 3 + kF32: return scale_chunk<kF32, kF32, NT>(t, e0, c);
+    case kF32 * 3 + kBF16: return scale_chunk<kF32, kBF16, NT>(t, e0, c);
+    case kF32 * 3 + kF16: return scale_chunk<kF32, kF16, NT>(t, e0, c);
+    case kBF16 * 3 + kF32: return scale_chunk<kBF16, kF32, NT>(t, e0, c);
+    case kBF16 * 3 + kBF16: return scale_chunk<kBF16, kBF16, NT>(t, e0, c);
+    case kBF16 * 3 + kF16: return scale_chunk<kBF16, kF16, NT>(t, e0, c);
+    case kF16 * 3 + kF32: return scale_chunk<kF16, kF32, NT>(t, e0, c);
+    case kF16 * 3 + kBF16: return scale_chunk<kF16, kBF16, NT>(t, e0, c);
+    default: return scale_chunk<kF16, kF16, NT>(t, e0, c);
+  }
 }
 
 hipError_t launch_clip_bind(ClipTensor* tensors, const ClipPointers& p, int first, int n, hipStream_t s) {
@@ -151,8 +196,11 @@ hipError_t launch_clip_bind(ClipTensor* tensors, const ClipPointers& p, int firs
 }
 
 hipError_t launch_clip_norm(const ClipArgs& a, hipStream_t s) {
-  if (a.ntiles > 0) {
-    hipLaunchKernelGGL(k_clip_sums, dim3((unsigned)a.ntiles), dim3(256), 0, s, a);
+  if (a.nsums > 0) {
+    if (a.stream)
+      hipLaunchKernelGGL(k_clip_sums<true>, dim3((unsigned)a.nsums), dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL(k_clip_sums<false>, dim3((unsigned)a.nsums), dim3(256), 0, s, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(k_clip_final, dim3(1), dim3(1024), 0, s, a);
@@ -160,8 +208,11 @@ hipError_t launch_clip_norm(const ClipArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_clip_apply(const ClipArgs& a, hipStream_t s) {
-  if (a.ntiles == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_clip_apply, dim3((unsigned)a.ntiles), dim3(256), 0, s, a);
+  if (a.nchunks == 0) return hipSuccess;
+  if (a.stream)
+    hipLaunchKernelGGL(k_clip_apply<true>, dim3((unsigned)a.nchunks), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(k_clip_apply<false>, dim3((unsigned)a.nchunks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

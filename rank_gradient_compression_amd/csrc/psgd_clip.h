@@ -11,17 +11,25 @@
 
 namespace psgd {
 
+// Elements that a workgroup handles at a time: 32 of each of its 256 threads.
+constexpr int kClipChunk = 8192;
+// Workgroups of the norm's pass over the whole list (and one more per tensor
+// at most): eight on each compute unit, twice.
+constexpr int kClipSumGroups = 4096;
+
 struct ClipTensor {
   const void* in;
   void* out;
   int64_t numel;
   int32_t in_dtype, out_dtype;
-  int32_t first_tile, ntiles;
+  int32_t first_sum, nsums;  // its workgroups of the norm's pass (each takes every nsums-th chunk)
+  int32_t first_chunk;       // its workgroups of the writing pass, one per chunk
+  int32_t pad;
 };
 
-// Workspace: [tensors][tile map][tile sums of squares, fp64].
+// Workspace: [tensors][norm workgroup -> tensor][writing workgroup -> tensor][sums of squares, fp64].
 struct ClipLayout {
-  size_t map_off, sums_off, bytes;
+  size_t sum_map_off, chunk_map_off, sums_off, bytes;
 };
 
 constexpr int kClipBindPairs = 240;  // pointer pairs one launch carries in its arguments
@@ -32,10 +40,10 @@ struct ClipPointers {
 
 struct ClipArgs {
   const ClipTensor* tensors;
-  const int32_t* map;  // tile -> tensor
+  const int32_t *sum_map, *chunk_map;
   double* sums;
-  int32_t ntensors, ntiles;
-  int32_t tile;  // elements of a tile
+  int32_t ntensors, nsums, nchunks;
+  bool stream;  // more bytes than the caches keep: streaming accesses
   float scale, max_norm;
   float* stats;
 };
@@ -48,8 +56,8 @@ hipError_t launch_clip_apply(const ClipArgs& a, hipStream_t s);
 
 struct psgd_clip {
   std::vector<psgd::ClipTensor> tensors;
-  std::vector<int32_t> map;
-  std::vector<uint8_t> tables;  // tensors + map, as uploaded
+  std::vector<int32_t> sum_map, chunk_map;
+  std::vector<uint8_t> tables;  // tensors and maps, as uploaded
   psgd::ClipLayout lay{};
-  int32_t tile = 0;
+  bool stream = false;
 };
