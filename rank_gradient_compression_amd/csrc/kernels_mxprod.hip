@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "psgd_mx_device.h"
 
@@ -358,42 +359,68 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
 }
 
 // Few rows on one side (up to 128): the product is a stream of the other
-// operand, "wide" here, and this kernel keeps its loads in flight.  One
-// workgroup = 32 rows of the wide operand, its wavefronts take the summed
-// axis' chunks in turn (neighbouring wavefronts read neighbouring 128 bytes of
-// a row) and their partial tiles are added through LDS in wavefront order.
+// operand, "wide" here, and what counts is how many of its bytes are under
+// way.  One workgroup = MT * 32 rows of the narrow operand (all of them) times
+// NT * 32 rows of the wide one; its wavefronts take the summed axis' chunks in
+// turn (neighbouring wavefronts read neighbouring 128 bytes of a row) and their
+// partial tiles are added through LDS in wavefront order.  Each wavefront
+// stages its chunks in LDS of its own, two ahead, straight from memory in
+// whole 128-byte rows: reading the matrix cores' layout (16 bytes of each of
+// 32 rows per access) from memory instead kept the cache's address lookup
+// busy and took 12 us where this takes 8 (24 x 4096 x 11008).
 // The narrow operand comes from memory (XDT < 0), or, for a few thousand
 // values, straight from the activations of type XDT, which every workgroup
 // quantises into LDS by itself: one launch instead of two, and the first
 // loads of the wide operand are already on their way meanwhile.
+// With MT = NT = 2 the same kernel serves small products of any shape.
 struct MxSkinnyArgs {
   int64_t narrow, wide, k;  // rows of the two operands, summed axis
   MxOperand x, w;           // narrow (XDT < 0) and wide operand
   const void* act;          // narrow x k activations, row stride ld (XDT >= 0)
   int64_t ld;
   void* c;
-  int64_t sx, sw;           // strides of C along the narrow and the wide operand's rows
+  int64_t ldc;
   int dtype;
   bool accumulate;
 };
 
-// 64 bytes of codes and four scales of one lane's row in one chunk.
-struct MxLane {
-  uint4 q[4];
-  uint32_t s;
-  __device__ __forceinline__ void load(const uint8_t* row, const uint32_t* sc, int64_t ch, int g, int64_t nblk) {
+// Waits until at most N of this wavefront's memory accesses are under way.
+template <int N>
+__device__ __forceinline__ void wait_memory() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x0f70 | (N >> 4) << 14);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// One operand's part of a wavefront's chunk: T tiles of 32 rows.
+template <int T>
+struct MxTiles {
+  __amdgpu_buffer_rsrc_t codes, scales;
+  uint32_t pitch, nch, so[T];
+  __device__ __forceinline__ MxTiles(const MxOperand& o, int64_t t0, int64_t rows, int64_t k) {
+    pitch = (uint32_t)mx_pitch(k);
+    nch = (uint32_t)mx_chunks(k);
+    const uint32_t left = (uint32_t)min((int64_t)(T * 32), rows - t0 * 32), tiles = (left + 31) / 32;
+    codes = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.codes + t0 * 32 * pitch), 0, (int)(left * pitch),
+                                              0x00020000);
+    scales = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.scales + t0 * nch * 256), 0,
+                                               (int)(tiles * nch * 256), 0x00020000);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      q[i] = *reinterpret_cast<const uint4*>(row + min(ch * 8 + 4 * g + i, nblk - 1) * 16);
-    s = sc[ch * 64];
+    for (int t = 0; t < T; ++t) so[t] = min((uint32_t)t, tiles - 1) * nch * 256;
+  }
+  // Chunk ch to LDS (T * 4 KB) and its scales to s; past the last chunk,
+  // nothing (zero codes).
+  __device__ __forceinline__ void fetch(uint32_t ch, uint8_t* lds, uint32_t (&s)[T], uint32_t off0, uint32_t off1,
+                                        int lane) const {
+    const uint32_t o = ch < nch ? ch * kChunkBytes : 0x80000000u, sc = min(ch, nch - 1) * 256;
+#pragma unroll
+    for (int t = 0; t < T; ++t) s[t] = __builtin_amdgcn_raw_buffer_load_b32(scales, lane * 4, (int)(so[t] + sc), 0);
+#pragma unroll
+    for (int j = 0; j < T * 4; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(codes, (__attribute__((address_space(3))) void*)(lds + j * 1024), 16,
+                                               (int)((j & 1 ? off1 : off0) + j * 8 * pitch + o), 0, 0, 0);
   }
 };
-__device__ __forceinline__ v16f mx_chunk4(const MxLane& a, const MxLane& b, v16f c) {
-  c = mx_mfma<0>(a.q[0], b.q[0], c, a.s, b.s);
-  c = mx_mfma<1>(a.q[1], b.q[1], c, a.s, b.s);
-  c = mx_mfma<2>(a.q[2], b.q[2], c, a.s, b.s);
-  return mx_mfma<3>(a.q[3], b.q[3], c, a.s, b.s);
-}
 
 // One block of 32 activations (n of them valid) to codes and scale byte.
 template <int DT>
@@ -427,84 +454,134 @@ __device__ __forceinline__ uint32_t mx_quant_block(const typename Elem<DT>::type
 }
 
 // Activations that a workgroup quantises by itself: at most this many blocks,
-// two for each thread of a workgroup of 512.  (Every workgroup repeats the
+// four for each thread of a workgroup of 256.  (Every workgroup repeats the
 // work; from here on a launch of its own is cheaper.)
 constexpr int kFusedBlocks = 1024;
 
-template <int MT, int XDT>
-__global__ __launch_bounds__(1024 / MT) void k_mx_prod_skinny(MxSkinnyArgs p) {
-  extern __shared__ __align__(16) uint8_t lds[];
-  const int waves = blockDim.x >> 6, lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+template <int WAVES, int MT, int NT, bool SWAP, int XDT>
+__global__ __launch_bounds__(WAVES * 64, 1) void k_mx_prod_skinny(MxSkinnyArgs p, int nwt) {
+  constexpr int XT = XDT >= 0 ? 0 : MT, XT1 = XT > 0 ? XT : 1;  // tiles of the narrow operand that are staged
+  constexpr int STAGE = (XT + NT) * 4096, LOADS = 5 * (XT + NT);
+  constexpr int RED = WAVES * MT * NT * 4096;
+  static_assert(RED <= 2 * WAVES * STAGE, "no room for the partial tiles");
+  __shared__ __align__(16) uint8_t st0[WAVES * STAGE], st1[WAVES * STAGE];
+  __shared__ __align__(16) uint8_t xc[XDT >= 0 ? kFusedBlocks * 16 : 16], xs[XDT >= 0 ? kFusedBlocks : 16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, g = lane >> 5;
-  const int64_t w0 = (int64_t)blockIdx.x * 32;
-  const int64_t nch = mx_chunks(p.k), nblk = mx_blocks(p.k), pitch = nblk * 16;
-  const uint8_t* wrow = p.w.codes + min(w0 + r, p.wide - 1) * pitch;
-  const uint32_t* wsc = reinterpret_cast<const uint32_t*>(p.w.scales) + blockIdx.x * nch * 64 + lane;
-  MxLane w;
-  int64_t ch = wave;
-  if (ch < nch) w.load(wrow, wsc, ch, g, nblk);
-  uint8_t* xs = lds + kFusedBlocks * 16;  // scales: chunk-wise dwords per row, as in an operand's tiles
+  const int64_t x0 = (int64_t)(blockIdx.x / nwt) * MT, w0 = (int64_t)(blockIdx.x % nwt) * NT;  // first tiles of 32
+  const MxTiles<NT> w(p.w, w0, p.wide, p.k);
+  const MxTiles<XT1> x(XT > 0 ? p.x : p.w, XT > 0 ? x0 : w0, XT > 0 ? p.narrow : p.wide, p.k);
+  const uint32_t nch = w.nch, pitch = w.pitch;
+  // (the slots of the large products' tiles)
+  const uint32_t off0 = (lane >> 3) * pitch + (((lane & 7) ^ (lane >> 4)) << 4);
+  const uint32_t off1 = (lane >> 3) * pitch + (((lane & 7) ^ (4 + (lane >> 4))) << 4);
+  uint32_t off[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) off[s] = r * kChunkBytes + (((4 * g + s) ^ ((r >> 1) & 7)) << 4);
+  uint8_t *const m0 = st0 + wave * STAGE, *const m1 = st1 + wave * STAGE;
+  uint32_t sw0[NT], sw1[NT], sx0[XT1], sx1[XT1];
+  auto fetch = [&](uint32_t ch, uint8_t* m, uint32_t(&sw)[NT], uint32_t(&sx)[XT1]) {
+    w.fetch(ch, m, sw, off0, off1, lane);
+    if constexpr (XT > 0) x.fetch(ch, m + NT * 4096, sx, off0, off1, lane);
+  };
+  uint32_t ch = wave;
+  // (the order of the loads is what wait_memory counts on)
+  fetch(ch, m0, sw0, sx0);
+  __builtin_amdgcn_sched_barrier(0);
+  fetch(ch + WAVES, m1, sw1, sx1);
+  __builtin_amdgcn_sched_barrier(0);
   if constexpr (XDT >= 0) {
-    using T = typename Elem < XDT < 0 ? 0 : XDT > ::type;
-    const T* act = static_cast<const T*>(p.act);
-    const int total = (int)(p.narrow * nch * 8);  // (blocks past the last get scale 0)
-    for (int i = threadIdx.x; i < total; i += blockDim.x) {
-      const int row = i / (int)(nch * 8), b = i % (int)(nch * 8);
+    constexpr int XD = XDT < 0 ? 0 : XDT;
+    const auto* act = static_cast<const typename Elem<XD>::type*>(p.act);
+    const int rows = (int)p.narrow, nblk = (int)mx_blocks(p.k), per = (int)nch * 8;
+    // (blocks past the last get zero codes and scale 0; scales as in an operand's tiles: chunk, half, row, byte)
+    for (int i = threadIdx.x; i < rows * per; i += WAVES * 64) {
+      const int row = i / per, b = i % per;
+      uint4 q = make_uint4(0, 0, 0, 0);
       uint32_t sb = 0;
-      if (b < nblk)
-        sb = mx_quant_block < XDT < 0 ? 0 : XDT > (act + row * p.ld + b * 32, (int)min((int64_t)32, p.k - b * 32),
-                                                  reinterpret_cast<uint4*>(lds) + row * nblk + b);
-      xs[((b >> 2) * (int)p.narrow + row) * 4 + (b & 3)] = (uint8_t)sb;
+      if (b < nblk) sb = mx_quant_block<XD>(act + row * p.ld + b * 32, (int)min((int64_t)32, p.k - b * 32), &q);
+      reinterpret_cast<uint4*>(xc)[i] = q;
+      xs[((b >> 2) * rows + row) * 4 + (b & 3)] = (uint8_t)sb;
     }
-    __syncthreads();
+    // (a barrier that waits for LDS alone: the stages stay under way)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
   }
-  const uint8_t* xrow[MT];
-  const uint32_t* xsc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    xrow[t] = p.x.codes + min((int64_t)t * 32 + r, p.narrow - 1) * pitch;
-    xsc[t] = reinterpret_cast<const uint32_t*>(p.x.scales) + min((int64_t)t, (p.narrow - 1) / 32) * nch * 64 + lane;
-  }
-  v16f acc[MT];
+  v16f acc[MT][NT];
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[t][e] = 0.f;
-  for (; ch < nch; ch += waves) {
-    const MxLane cur = w;
-    if (ch + waves < nch) w.load(wrow, wsc, ch + waves, g, nblk);
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      MxLane x;
-      if constexpr (XDT >= 0) {
-        const int row = min(r, (int)p.narrow - 1);
+      for (int e = 0; e < 16; ++e) acc[t][u][e] = 0.f;
+  auto chunk = [&](uint32_t at, const uint8_t* m, const uint32_t(&sw)[NT], const uint32_t(&sx)[XT1]) {
+    const int xrow = XDT >= 0 ? min(r, (int)p.narrow - 1) : 0;
+    uint32_t fx = 0;
+    if constexpr (XDT >= 0) fx = reinterpret_cast<const uint32_t*>(xs)[(min(at, nch - 1) * 2 + g) * (int)p.narrow + xrow];
+    auto step = [&](auto S) {
+      constexpr int s = decltype(S)::value;
+      uint4 a[MT], b[NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x.q[i] = reinterpret_cast<const uint4*>(lds)[row * nblk + min(ch * 8 + 4 * g + i, nblk - 1)];
-        x.s = reinterpret_cast<const uint32_t*>(xs)[(ch * 2 + g) * p.narrow + row];
-      } else {
-        x.load(xrow[t], xsc[t], ch, g, nblk);
+      for (int t = 0; t < MT; ++t) {
+        if constexpr (XDT >= 0)
+          a[t] = reinterpret_cast<const uint4*>(xc)[xrow * (int)nch * 8 + min(at, nch - 1) * 8 + 4 * g + s];
+        else
+          a[t] = *reinterpret_cast<const uint4*>(m + (NT + t) * 4096 + off[s]);
       }
-      acc[t] = mx_chunk4(x, cur, acc[t]);
-    }
-  }
-  if constexpr (XDT >= 0) __syncthreads();  // (the quantised activations' LDS is reused)
-  float* red = reinterpret_cast<float*>(lds);
+#pragma unroll
+      for (int u = 0; u < NT; ++u) b[u] = *reinterpret_cast<const uint4*>(m + u * 4096 + off[s]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          const uint32_t ss = XDT >= 0 ? fx : sx[XDT >= 0 ? 0 : t];
+          acc[t][u] = SWAP ? mx_mfma<s>(b[u], a[t], acc[t][u], sw[u], ss) : mx_mfma<s>(a[t], b[u], acc[t][u], ss, sw[u]);
+        }
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  };
+  // (a wavefront without a chunk adds one of zero codes)
+  do {
+    wait_memory<LOADS>();
+    chunk(ch, m0, sw0, sx0);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(ch + 2 * WAVES, m0, sw0, sx0);
+    wait_memory<LOADS>();
+    chunk(ch + WAVES, m1, sw1, sx1);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(ch + 3 * WAVES, m1, sw1, sx1);
+    ch += 2 * WAVES;
+  } while (ch < nch);
+  __syncthreads();  // (waits for the last fetches, of nothing, as well)
+  // the partial tiles: the first WAVES * STAGE bytes in st0, the rest in st1
+  constexpr int UNITS = MT * NT * 16;  // 256-byte registers of a wavefront
+  constexpr int SPLIT = WAVES * STAGE / 256;
+  auto at = [&](int i) { return reinterpret_cast<float*>(i < SPLIT ? st0 + i * 256 : st1 + (i - SPLIT) * 256) + lane; };
 #pragma unroll
   for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) red[((wave * MT + t) * 16 + e) * 64 + lane] = acc[t][e];
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) *at(wave * UNITS + (t * NT + u) * 16 + e) = acc[t][u][e];
   __syncthreads();
-  // tile element (narrow row i, wide row j) = lane (i / 4 % 2) * 32 + j, register i / 8 * 4 + i % 4
-  for (int o = threadIdx.x; o < MT * 1024; o += blockDim.x) {
-    const int i = p.sw == 1 ? o / 32 % 32 : o % 32, j = p.sw == 1 ? o % 32 : o / 32 % 32, t = o / 1024;
-    const int64_t row = t * 32 + i, col = w0 + j;
-    if (row >= p.narrow || col >= p.wide) continue;
-    const int at = (t * 16 + i / 8 * 4 + i % 4) * 64 + (i / 4 % 2) * 32 + j;
+  // Register e of tile (t, u): lane % 32 is the column of C, 4 * (lane / 32) +
+  // e / 4 * 8 + e % 4 its row; the wavefronts share the registers.
+  const int64_t rows = SWAP ? p.wide : p.narrow, cols = SWAP ? p.narrow : p.wide;
+  for (int o = wave; o < UNITS; o += WAVES) {
+    const int e = o % 16, u = o / 16 % NT, t = o / 16 / NT;
+    const int64_t tx = (x0 + t) * 32, tw = (w0 + u) * 32;
+    const int64_t row0 = (SWAP ? tw : tx) + (e >> 2) * 8 + (e & 3), col = (SWAP ? tx : tw) + r;
+    if (row0 >= rows) continue;
     float v = 0.f;
-    for (int k = 0; k < waves; ++k) v += red[k * MT * 1024 + at];
-    const int64_t ci = row * p.sx + col * p.sw;
+#pragma unroll
+    for (int k = 0; k < WAVES; ++k) v += *at(k * UNITS + o);
+    const int64_t row = row0 + g * 4;
+    if (row >= rows || col >= cols) continue;
+    const int64_t ci = row * p.ldc + col;
     if (p.dtype == kF32)
       store_c<kF32>(p.c, ci, v, p.accumulate);
     else if (p.dtype == kBF16)
@@ -514,38 +591,42 @@ __global__ __launch_bounds__(1024 / MT) void k_mx_prod_skinny(MxSkinnyArgs p) {
   }
 }
 
-// Wavefronts per workgroup: enough in all to keep some 2048 of them loading
-// (a wavefront has 4 KB in flight), at most 16, and no more than LDS has room
-// for MT partial tiles of each, nor than there are chunks.
-template <int MT, int XDT>
+// Eight wavefronts to a workgroup where all tiles fit on the compute units
+// together (their stages take 128 KB of LDS), four (two workgroups to a
+// compute unit) where they do not, or where there is nothing to share.
+template <int MT, int NT, bool SWAP, int XDT>
 static void skinny(const MxSkinnyArgs& p, hipStream_t s) {
-  const int64_t tiles = (p.wide + 31) / 32, nch = mx_chunks(p.k);
-  int waves = 4;
-  while (waves < 16 / MT && waves * tiles < 2048 && waves < nch) waves *= 2;
-  size_t lds = (size_t)waves * MT * 4096;
-  if (XDT >= 0) lds = std::max<size_t>(lds, kFusedBlocks * 17 + 1024 * 4);
-  hipLaunchKernelGGL((k_mx_prod_skinny<MT, XDT>), dim3((unsigned)tiles), dim3(64 * waves), lds, s, p);
+  const int64_t nwt = (p.wide + NT * 32 - 1) / (NT * 32), tiles = nwt * ((p.narrow + MT * 32 - 1) / (MT * 32));
+  if constexpr (MT == 1 && NT == 1) {
+    if (tiles <= 256 && mx_chunks(p.k) > 4) {
+      hipLaunchKernelGGL((k_mx_prod_skinny<8, MT, NT, SWAP, XDT>), dim3((unsigned)tiles), dim3(512), 0, s, p, (int)nwt);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((k_mx_prod_skinny<4, MT, NT, SWAP, XDT>), dim3((unsigned)tiles), dim3(256), 0, s, p, (int)nwt);
 }
 
+// SWAP: the narrow side is C's columns.
+template <bool SWAP>
 static void product_skinny(const MxSkinnyArgs& p, hipStream_t s) {
   if (p.narrow <= 32)
-    skinny<1, -1>(p, s);
+    skinny<1, 1, SWAP, -1>(p, s);
   else if (p.narrow <= 64)
-    skinny<2, -1>(p, s);
+    skinny<2, 1, SWAP, -1>(p, s);
   else
-    skinny<4, -1>(p, s);
+    skinny<4, 1, SWAP, -1>(p, s);
 }
 
 bool mx_linear_fuses(int64_t m, int64_t k) { return m <= 32 && k > 0 && m * mx_chunks(k) * 8 <= kFusedBlocks; }
 
 hipError_t launch_mx_linear_fused(const MxProductArgs& p, const void* x, int x_dtype, int64_t ldx, hipStream_t s) {
-  MxSkinnyArgs a{p.m, p.n, p.k, {nullptr, nullptr}, p.b, x, ldx, p.c, p.ldc, 1, p.dtype, false};
+  MxSkinnyArgs a{p.m, p.n, p.k, {nullptr, nullptr}, p.b, x, ldx, p.c, p.ldc, p.dtype, false};
   if (x_dtype == kF32)
-    skinny<1, kF32>(a, s);
+    skinny<1, 1, false, kF32>(a, s);
   else if (x_dtype == kBF16)
-    skinny<1, kBF16>(a, s);
+    skinny<1, 1, false, kBF16>(a, s);
   else
-    skinny<1, kF16>(a, s);
+    skinny<1, 1, false, kF16>(a, s);
   return hipGetLastError();
 }
 
@@ -573,25 +654,32 @@ static void product_dt(const MxProductArgs& p, hipStream_t s) {
       hipLaunchKernelGGL((k_mx_prod_zero<DT>), dim3((unsigned)((p.m * p.n + 255) / 256)), dim3(256), 0, s, p);
     return;
   }
-  if (p.m <= 128 || p.n <= 128) {
-    // the side with fewer rows is the narrow one; C's strides follow it
+  const MxSkinnyArgs ab{p.m, p.n, p.k, p.a, p.b, nullptr, 0, p.c, p.ldc, p.dtype, p.accumulate};
+  const MxSkinnyArgs ba{p.n, p.m, p.k, p.b, p.a, nullptr, 0, p.c, p.ldc, p.dtype, p.accumulate};
+  const bool fits = mx_pitch(p.k) * 256 <= INT32_MAX && p.ldc * 4 * 128 <= INT32_MAX;  // 32-bit offsets in a tile
+  if (fits && (p.m <= 128 || p.n <= 128)) {
     if (p.m <= p.n)
-      product_skinny(MxSkinnyArgs{p.m, p.n, p.k, p.a, p.b, nullptr, 0, p.c, p.ldc, 1, p.dtype, p.accumulate}, s);
+      product_skinny<false>(ab, s);
     else
-      product_skinny(MxSkinnyArgs{p.n, p.m, p.k, p.b, p.a, nullptr, 0, p.c, 1, p.ldc, p.dtype, p.accumulate}, s);
+      product_skinny<true>(ba, s);
     return;
   }
-  if (mx_pitch(p.k) * 256 <= INT32_MAX && p.ldc * 4 * 128 <= INT32_MAX) {
-    // 256 x 256 tiles where they occupy more than half of the 256 compute
-    // units; fewer are halved (2048 x 4096 x 11008: 128 tiles 70 us, 256
-    // halves 62 us; 2048 x 11008 x 4096: 344 tiles 64 us, 688 halves 72 us).
-    const int64_t nt = ((p.m + 255) / 256) * ((p.n + 255) / 256);
-    if (nt > 128)
-      product_lds<DT, 2, 4, 4, 2>(p, s);
-    else if (nt > 32)
+  // Tiles as large as still give each of the 256 compute units one: a larger
+  // tile reads its operands fewer times, but an idle compute unit costs more
+  // (2048 x 4096 x 11008: 128 tiles of 256 x 256 70 us, 256 of 128 x 256 54;
+  // 2048 x 11008 x 4096: 344 of 256 x 256 58 us, 688 of 128 x 256 72).  A
+  // single chunk is a write of C and hardly a product: small workgroups that
+  // store from the accumulators (11008 x 4096 x 64: 33 us against 41).
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((p.m + bm - 1) / bm) * ((p.n + bn - 1) / bn); };
+  if (fits && p.k > 256) {
+    if (tiles(64, 64) <= 256)
+      skinny<2, 2, false, -1>(ab, s);
+    else if (tiles(128, 128) <= 256)
+      product_lds<DT, 2, 2, 2, 2>(p, s);
+    else if (tiles(128, 256) <= 256)
       product_lds<DT, 2, 2, 2, 4>(p, s);
     else
-      product_lds<DT, 2, 2, 2, 2>(p, s);
+      product_lds<DT, 2, 4, 4, 2>(p, s);
     return;
   }
   const int ntn = (int)((p.n + 63) / 64);
