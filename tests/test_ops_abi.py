@@ -1,0 +1,160 @@
+"""Host-side refusals and sizes of the clip and of the microscaled operands:
+every error returns before any device call, so these run without a GPU."""
+import ctypes
+
+import pytest
+
+R = pytest.importorskip("rank_gradient_compression_amd")
+B = R.binding
+
+P = 4096  # a 16-byte aligned address that nothing dereferences
+F32, BF16, F16 = B.PSGD_DTYPE_F32, B.PSGD_DTYPE_BF16, B.PSGD_DTYPE_F16
+BIG = 1 << 31
+
+
+def refused(fn, *args, status=B.PSGD_ERR_INVALID_ARG, match=None):
+    with pytest.raises(B.PsgdError, match=match) as e:
+        fn(*args)
+    assert e.value.status == status
+    assert fn.__name__ in str(e.value)
+
+
+@pytest.mark.parametrize("rows,cols,codes,scales", [(0, 5, 0, 0), (5, 0, 0, 0), (1, 1, 16, 256), (32, 256, 32 * 128, 256),
+                                                    (33, 257, 33 * 9 * 16, 2 * 2 * 256), (4, 11008, 4 * 344 * 16, 43 * 256)])
+def test_sizes(rows, cols, codes, scales):
+    assert B.psgd_mx_sizes(rows, cols) == (codes, scales)
+
+
+def test_sizes_refused():
+    refused(B.psgd_mx_sizes, -1, 4)
+    refused(B.psgd_mx_sizes, 4, BIG)
+    assert B.lib.psgd_mx_sizes(1, 1, None, None) == B.PSGD_ERR_INVALID_ARG
+    for fn in (B.psgd_mx_product_workspace, B.psgd_mx_linear_workspace):
+        refused(fn, -1, 4, 4)
+        refused(fn, 4, 4, BIG)
+
+
+def quant(x=P, dtype=F32, rows=4, cols=64, ld=64, rand=0, rc=1 << 20, rs=2 << 20, cc=0, cs=0, values=0, ldv=0):
+    B.psgd_mx_quantize(x, dtype, rows, cols, ld, rand, rc, rs, cc, cs, values, ldv)
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(dtype=3), "type"), (dict(dtype=-1), "type"), (dict(rows=-1), "negative"), (dict(cols=BIG), "INT32_MAX"),
+    (dict(ld=63), "stride"), (dict(ld=BIG), "stride"), (dict(x=0), "NULL"), (dict(x=P + 2), "aligned"),
+    (dict(rc=0), "together"), (dict(rs=0), "together"), (dict(cc=1 << 22), "together"),
+    (dict(rc=0, rs=0), "no output"), (dict(rc=(1 << 20) + 8), "16-byte"), (dict(rs=(2 << 20) + 4), "16-byte"),
+    (dict(rc=P, rs=2 << 20), "overlap"), (dict(rc=1 << 20, rs=1 << 20), "overlap"),
+    (dict(values=P + 64, ldv=64), "overlaps x"), (dict(values=P, ldv=80), "overlaps x"),
+    (dict(values=1 << 22, ldv=63), "stride"), (dict(values=(1 << 22) + 1, ldv=64), "aligned"),
+    (dict(values=1 << 20, ldv=64), "overlap"), (dict(rand=1 << 20), "overlap"),
+    (dict(cc=1 << 20, cs=4 << 20), "overlap"),
+    (dict(rows=(1 << 31) - 1, cols=(1 << 31) - 1, ld=(1 << 31) - 1, x=1 << 62, rc=0, rs=0, values=1 << 62,
+          ldv=(1 << 31) - 1), "too large"),
+])
+def test_quantize_refused(kw, match):
+    with pytest.raises(B.PsgdError, match=match) as e:
+        quant(**kw)
+    assert e.value.status == B.PSGD_ERR_INVALID_ARG
+
+
+def test_empty_matrices_are_accepted_without_a_device():
+    quant(rows=0)
+    quant(cols=0, ld=0)
+    B.psgd_mx_dequantize(0, 0, 0, 7, 0, F32, 7)
+    B.psgd_mx_product(0, 5, 7, 0, 0, P, P, 0, F32, 5, False, 0, 0)
+    B.psgd_mx_linear(0, 5, 7, 0, F32, 7, P, P, 0, F32, 5, 0, 0)
+
+
+def test_dequantize_refused():
+    ok = [1 << 20, 2 << 20, 4, 64, P, F32, 64]
+    for at, bad, match in [(0, 0, "NULL"), (1, 0, "NULL"), (0, (1 << 20) + 8, "16-byte"), (2, -1, "negative"),
+                           (3, BIG, "INT32_MAX"), (4, 0, "NULL"), (4, P + 1, "aligned"), (5, 9, "type"),
+                           (6, 63, "stride"), (4, 1 << 20, "overlaps"), (4, 2 << 20, "overlaps")]:
+        args = list(ok)
+        args[at] = bad
+        refused(B.psgd_mx_dequantize, *args, match=match)
+
+
+def test_product_refused():
+    ok = [8, 8, 64, 1 << 20, 2 << 20, 3 << 20, 4 << 20, P, F32, 8, False, 0, 0]
+    for at, bad, match in [(0, -1, "negative"), (1, BIG, "INT32_MAX"), (2, -3, "negative"), (3, 0, "NULL"),
+                           (4, 0, "NULL"), (5, 0, "NULL"), (6, (4 << 20) + 1, "16-byte"), (7, 0, "NULL"),
+                           (7, P + 2, "aligned"), (8, 5, "type"), (9, 7, "stride"), (7, 1 << 20, "overlaps"),
+                           (7, 4 << 20, "overlaps")]:
+        args = list(ok)
+        args[at] = bad
+        refused(B.psgd_mx_product, *args, match=match)
+
+
+def test_linear_refused():
+    m, n, k = 64, 96, 512  # too many activations for one launch: a workspace is needed
+    need = B.psgd_mx_linear_workspace(m, n, k)
+    assert need >= sum(B.psgd_mx_sizes(m, k))
+    ok = [m, n, k, 1 << 24, BF16, k, 1 << 20, 2 << 20, 1 << 25, BF16, n, 1 << 26, need]
+    for at, bad, match in [(3, 0, "NULL"), (4, 4, "type"), (5, k - 1, "stride"), (6, 0, "NULL"), (8, 0, "NULL"),
+                           (9, 7, "type"), (10, n - 1, "stride"), (8, 1 << 24, "overlaps")]:
+        args = list(ok)
+        args[at] = bad
+        refused(B.psgd_mx_linear, *args, match=match)
+    for at, bad in [(11, 0), (11, (1 << 26) + 128), (12, need - 1)]:
+        args = list(ok)
+        args[at] = bad
+        refused(B.psgd_mx_linear, *args, status=B.PSGD_ERR_WORKSPACE)
+
+
+def test_clip_create_refused():
+    refused(B.psgd_clip_create, [-1], [F32], [F32])
+    refused(B.psgd_clip_create, [1 << 50], [F32], [F32])
+    refused(B.psgd_clip_create, [1 << 46, 1 << 46], [F32] * 2, [F32] * 2)
+    refused(B.psgd_clip_create, [1 << 45], [F32], [F32])
+    refused(B.psgd_clip_create, [4], [3], [F32])
+    refused(B.psgd_clip_create, [4], [F32], [-1])
+    out = ctypes.c_void_p(7)
+    assert B.lib.psgd_clip_create(-1, None, None, None, ctypes.byref(out)) == B.PSGD_ERR_INVALID_ARG
+    assert out.value is None
+    assert B.lib.psgd_clip_create(1, None, None, None, ctypes.byref(out)) == B.PSGD_ERR_INVALID_ARG
+    assert B.lib.psgd_clip_create(0, None, None, None, None) == B.PSGD_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        B.psgd_clip_create([1, 2], [F32], [F32, F32])
+
+
+def test_clip_calls_refused():
+    c = B.psgd_clip_create([100, 0, 50], [F32, BF16, BF16], [F32, F32, BF16])
+    try:
+        need = B.psgd_clip_workspace(c)
+        ws = 1 << 26
+        for bad in ((0, need), (ws + 16, need), (ws, need - 1)):
+            refused(B.psgd_clip_workspace_init, c, *bad, status=B.PSGD_ERR_WORKSPACE)
+            refused(B.psgd_clip_bind, c, [P, 0, 2 * P], [P, 0, 2 * P], *bad, status=B.PSGD_ERR_WORKSPACE)
+            refused(B.psgd_clip_norm, c, 1.0, 1.0, P, *bad, status=B.PSGD_ERR_WORKSPACE)
+            refused(B.psgd_clip_apply, c, 1.0, 1.0, P, *bad, status=B.PSGD_ERR_WORKSPACE)
+        for ins, outs, match in [([0, 0, 2 * P], None, "NULL"), ([P + 2, 0, 2 * P], None, "aligned"),
+                                 ([P, 0, 2 * P + 1], None, "aligned"), ([P, 0, 2 * P], [0, 0, 2 * P], "NULL"),
+                                 ([P, 0, 2 * P], [P, 0, P + 64], "two outputs"),
+                                 ([P, 0, 2 * P], [P + 64, 0, 4 * P], "overlaps a gradient"),
+                                 ([P, 0, 2 * P], [2 * P, 0, 4 * P], "overlaps a gradient")]:
+            refused(B.psgd_clip_bind, c, ins, outs, ws, need, match=match)
+        assert B.lib.psgd_clip_bind(c, None, None, ws, need, None) == B.PSGD_ERR_INVALID_ARG
+        for fn in (B.psgd_clip_norm, B.psgd_clip_apply):
+            refused(fn, c, 1.0, 1.0, 0, ws, need, match="stats")
+            refused(fn, c, 1.0, 1.0, P + 2, ws, need, match="stats")
+            refused(fn, c, -1.0, 1.0, P, ws, need, match="max_norm")
+            refused(fn, c, float("nan"), 1.0, P, ws, need, match="max_norm")
+            refused(fn, c, 1.0, float("inf"), P, ws, need, match="scale")
+            refused(fn, c, 1.0, float("nan"), P, ws, need, match="scale")
+    finally:
+        B.psgd_clip_destroy(c)
+
+
+def test_clip_in_place_with_another_element_size_is_refused():
+    c = B.psgd_clip_create([100], [BF16], [F32])
+    try:
+        refused(B.psgd_clip_bind, c, [P], [P], 1 << 26, B.psgd_clip_workspace(c), match="overlaps a gradient")
+    finally:
+        B.psgd_clip_destroy(c)
+
+
+def test_null_handles():
+    assert B.lib.psgd_clip_workspace(None, None) == B.PSGD_ERR_INVALID_ARG
+    refused(B.psgd_clip_norm, None, 1.0, 1.0, P, 1 << 26, 1 << 20)
+    B.psgd_clip_destroy(None)
