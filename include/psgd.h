@@ -506,8 +506,8 @@ psgd_status_t psgd_clip_apply(psgd_clip_t clip, float max_norm, float scale, flo
  *           plus 8 if negative; the last block is padded with zero codes;
  *   scales  tiles of 32 rows x 256 columns, 256 bytes each, the tiles of one
  *           row of tiles after each other: the scale of row i, block b is byte
- *           ((i / 32) * ceil(cols / 256) + b / 8) * 256 + (b % 8 / 4) * 128
- *           + (i % 32) * 4 + b % 4.  Bytes of blocks past the last column are
+ *           ((i / 32) * ceil(cols / 256) + b / 8) * 256 + (b % 8 / 2) * 64
+ *           + (i % 16) * 4 + (i % 32 / 16) * 2 + b % 2.  Bytes of blocks past the last column are
  *           zero; bytes of rows past the last row are not read for results.
  *
  * psgd_mx_quantize -- x: rows x cols values of type `dtype`, row stride ld

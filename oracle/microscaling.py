@@ -83,7 +83,7 @@ def pack_codes(codes: np.ndarray) -> np.ndarray:
 def scale_index(i: int, b: int, cols: int) -> int:
     """Byte of row i, block b among an operand's scale tiles."""
     chunks = -(-cols // 256)
-    return ((i // 32) * chunks + b // 8) * 256 + (b % 8) // 4 * 128 + (i % 32) * 4 + b % 4
+    return ((i // 32) * chunks + b // 8) * 256 + b % 8 // 2 * 64 + i % 16 * 4 + i % 32 // 16 * 2 + b % 2
 
 
 def pack_scales(scales: np.ndarray, cols: int) -> Tuple[np.ndarray, np.ndarray]:

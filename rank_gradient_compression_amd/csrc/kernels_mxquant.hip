@@ -119,7 +119,7 @@ __device__ __forceinline__ void quant_rows_tile(const MxQuantArgs& a, int nch, u
     else
       code = mx_encode4(f);
     const int blk = col >> 5;
-    if ((threadIdx.x % L) == 0) tb[((blk & 7) >> 2) * 128 + r * 4 + (blk & 3)] = (uint8_t)sb;
+    if ((threadIdx.x % L) == 0) tb[mx_scale_in_tile(r, blk & 7)] = (uint8_t)sb;
     if (live && (FULL || blk < nblk)) {
       if (a.row_codes) {
         uint8_t* cp = a.row_codes + row * (nblk * 16) + (col >> 1);
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantArgs a, int nct) {
   constexpr int P = kColPitch<DT>, SKEW = kColSkew<DT>, RP = kColRandPitch;
   __shared__ __align__(16) T tile[128 * P + 4 * SKEW];
   __shared__ __align__(16) uint8_t rtile[RAND ? 128 * RP : 16];
-  __shared__ uint32_t stile[ROWS ? 128 : 1];
+  __shared__ uint32_t stile[ROWS ? 128 : 1], ctile[128];  // four tiles' half chunks
   const int rt = blockIdx.x / nct, ct = blockIdx.x % nct;
   const int64_t row0 = (int64_t)rt * 128, col0 = (int64_t)ct * 128;
   const int64_t nblk_r = mx_blocks(a.cols), nblk_c = mx_blocks(a.rows);
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantArgs a, int nct) {
       }
       const uint32_t sb = mx_scale_byte(am);
       const uint4 q = encode_block<RAND>(f, sb, [&](int k) { return rtile[r * RP + b * 32 + k]; });
-      reinterpret_cast<uint8_t*>(stile)[r * 4 + b] = (uint8_t)sb;
+      reinterpret_cast<uint8_t*>(stile)[r / 32 * 128 + mx_scale_in_tile(r % 32, b)] = (uint8_t)sb;
       if (row0 + r < a.rows && ct * 4 + b < nblk_r)
         *reinterpret_cast<uint4*>(a.row_codes + ((row0 + r) * nblk_r + ct * 4 + b) * 16) = q;
     }
@@ -284,26 +284,21 @@ __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantArgs a, int nct) {
     }
     const uint32_t sb = mx_scale_byte(am);
     const uint4 q = encode_block<RAND>(f, sb, [&](int k) { return rtile[(b * 32 + k) * RP + c]; });
-    uint32_t s4 = sb << (8 * b);  // the four scales of a column, from its four lanes
-    s4 |= (uint32_t)__shfl_xor((int)s4, 1);
-    s4 |= (uint32_t)__shfl_xor((int)s4, 2);
-    const int64_t cc = col0 + c;
-    if (cc < a.cols) {
-      if (rt * 4 + b < nblk_c) *reinterpret_cast<uint4*>(a.col_codes + (cc * nblk_c + rt * 4 + b) * 16) = q;
-      if (b == 0)
-        reinterpret_cast<uint32_t*>(a.col_scales)[((cc / 32) * mx_chunks(a.rows) + rt / 2) * 64 + (rt & 1) * 32 +
-                                                  cc % 32] = s4;
-    }
+    reinterpret_cast<uint8_t*>(ctile)[c / 32 * 128 + mx_scale_in_tile(c % 32, b)] = (uint8_t)sb;
+    if (col0 + c < a.cols && rt * 4 + b < nblk_c)
+      *reinterpret_cast<uint4*>(a.col_codes + ((col0 + c) * nblk_c + rt * 4 + b) * 16) = q;
   }
-  if constexpr (ROWS) {
-    // rows row0 .. row0 + 127 are four row tiles; these columns are half a chunk
-    __syncthreads();
-    if (threadIdx.x < 128) {
-      const int64_t tr = row0 / 32 + threadIdx.x / 32;
-      if (tr < (a.rows + 31) / 32)
-        reinterpret_cast<uint32_t*>(a.row_scales)[(tr * mx_chunks(a.cols) + ct / 2) * 64 + (ct & 1) * 32 +
-                                                  threadIdx.x % 32] = stile[threadIdx.x];
-    }
+  __syncthreads();
+  // 128 rows (columns) are four tiles of scales, 128 columns (rows) half a chunk
+  const int t = threadIdx.x % 128 / 32, at = threadIdx.x % 32;
+  if (threadIdx.x < 128) {
+    if (col0 / 32 + t < (a.cols + 31) / 32)
+      reinterpret_cast<uint32_t*>(a.col_scales)[((col0 / 32 + t) * mx_chunks(a.rows) + rt / 2) * 64 + (rt & 1) * 32 + at] =
+          ctile[threadIdx.x];
+  } else if constexpr (ROWS) {
+    if (row0 / 32 + t < (a.rows + 31) / 32)
+      reinterpret_cast<uint32_t*>(a.row_scales)[((row0 / 32 + t) * mx_chunks(a.cols) + ct / 2) * 64 + (ct & 1) * 32 + at] =
+          stile[threadIdx.x - 128];
   }
 }
 
@@ -327,7 +322,7 @@ __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ 
     if (r >= nrows) break;
     const uint32_t q = *reinterpret_cast<const uint32_t*>(codes + (row0 + r) * (nblk * 16) + (col >> 1));
     const int b = c >> 5;
-    const uint32_t sb = scales[((int64_t)rt * nch + ch) * 256 + (b >> 2) * 128 + r * 4 + (b & 3)];
+    const uint32_t sb = scales[((int64_t)rt * nch + ch) * 256 + mx_scale_in_tile(r, b)];
     const int k = (int)sb - 127;
     const float2 d[4] = {mx_decode2<0>(q, k), mx_decode2<1>(q, k), mx_decode2<2>(q, k), mx_decode2<3>(q, k)};
     T o[8];

@@ -16,13 +16,16 @@ __host__ __device__ constexpr int dtype_bytes(int d) { return d == kF32 ? 4 : 2;
 //         codes); element 2j in the low nibble of byte j.
 // scales: tiles of 32 rows x 256 columns, 256 bytes each, row tile by row
 //         tile: the byte of row i, block b is at
-//         ((i/32) * nch + b/8) * 256 + ((b%8)/4) * 128 + (i%32) * 4 + b%4,
-//         so that lane (i%32) + 32 * ((b%8)/4) of a wavefront finds the four
-//         scales of its four matrix-core steps in one dword and a wavefront
-//         loads a tile with one 256-byte access.  Blocks past the last column
-//         have scale 0 (2^-127): the product of two such blocks is below
-//         2^-248 and vanishes in fp32, whatever their codes.
+//         ((i/32) * nch + b/8) * 256 + mx_scale_in_tile(i%32, b%8), so that
+//         lane (i%16) + 16 * ((b%8)/2) of a wavefront finds the scales of its
+//         two matrix-core steps for rows i%16 and 16 + i%16 in one dword and
+//         a wavefront loads a tile with one 256-byte access.  Blocks past the
+//         last column have scale 0 (2^-127): the product of two such blocks
+//         is below 2^-248 and vanishes in fp32, whatever their codes.
 constexpr int kMxBlock = 32;
+__host__ __device__ constexpr int mx_scale_in_tile(int row, int blk) {
+  return (blk >> 1) * 64 + (row & 15) * 4 + (row >> 4) * 2 + (blk & 1);
+}
 __host__ __device__ inline int64_t mx_blocks(int64_t cols) { return (cols + 31) >> 5; }
 __host__ __device__ inline int64_t mx_pitch(int64_t cols) { return mx_blocks(cols) * 16; }
 __host__ __device__ inline int64_t mx_chunks(int64_t cols) { return (cols + 255) >> 8; }

@@ -68,10 +68,10 @@ def test_scale_tiles_are_a_bijection():
     nb = -(-cols // 32)
     seen = {MX.scale_index(i, b, cols) for i in range(rows) for b in range(nb)}
     assert len(seen) == rows * nb and max(seen) < 3 * 3 * 256
-    # a lane's four scales of one chunk are one aligned dword
-    for i in (0, 33, 69):
-        for b in (0, 4, 8, 12):
-            j = [MX.scale_index(i, b + s, cols) for s in range(4)]
+    # rows i and i + 16 and two neighbouring blocks make one aligned dword
+    for i in (0, 9, 47):
+        for b in (0, 2, 4, 14):
+            j = [MX.scale_index(i + h, b + s, cols) for h in (0, 16) for s in (0, 1)]
             assert j[0] % 4 == 0 and j == list(range(j[0], j[0] + 4))
 
 
