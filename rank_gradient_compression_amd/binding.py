@@ -335,9 +335,11 @@ def psgd_mx_sizes(rows: int, cols: int):
 
 def psgd_mx_quantize(x: int, dtype: int, rows: int, cols: int, ld: int, rand: int, row_codes: int, row_scales: int,
                      col_codes: int, col_scales: int, values: int, ldv: int, stream: int = 0) -> None:
-    _check("psgd_mx_quantize", lib.psgd_mx_quantize(x or None, dtype, rows, cols, ld, rand or None, row_codes or None,
-                                                    row_scales or None, col_codes or None, col_scales or None,
-                                                    values or None, ldv, stream))
+    # (ctypes passes an address of 0 as NULL)
+    st = lib.psgd_mx_quantize(x, dtype, rows, cols, ld, rand, row_codes, row_scales, col_codes, col_scales, values, ldv,
+                              stream)
+    if st:
+        _check("psgd_mx_quantize", st)
 
 
 def psgd_mx_dequantize(codes: int, scales: int, rows: int, cols: int, out: int, dtype: int, ld: int,
@@ -355,9 +357,10 @@ def psgd_mx_product_workspace(m: int, n: int, k: int) -> int:
 def psgd_mx_product(m: int, n: int, k: int, a_codes: int, a_scales: int, b_codes: int, b_scales: int, c: int,
                     dtype: int, ldc: int, accumulate: bool, workspace: int, workspace_bytes: int,
                     stream: int = 0) -> None:
-    _check("psgd_mx_product", lib.psgd_mx_product(m, n, k, a_codes or None, a_scales or None, b_codes or None,
-                                                  b_scales or None, c or None, dtype, ldc, 1 if accumulate else 0,
-                                                  workspace or None, workspace_bytes, stream))
+    st = lib.psgd_mx_product(m, n, k, a_codes, a_scales, b_codes, b_scales, c, dtype, ldc, 1 if accumulate else 0,
+                             workspace, workspace_bytes, stream)
+    if st:
+        _check("psgd_mx_product", st)
 
 
 def psgd_mx_linear_workspace(m: int, n: int, k: int) -> int:
@@ -368,8 +371,10 @@ def psgd_mx_linear_workspace(m: int, n: int, k: int) -> int:
 
 def psgd_mx_linear(m: int, n: int, k: int, x: int, x_dtype: int, ldx: int, w_codes: int, w_scales: int, y: int,
                    y_dtype: int, ldy: int, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
-    _check("psgd_mx_linear", lib.psgd_mx_linear(m, n, k, x or None, x_dtype, ldx, w_codes or None, w_scales or None,
-                                                y or None, y_dtype, ldy, workspace or None, workspace_bytes, stream))
+    st = lib.psgd_mx_linear(m, n, k, x, x_dtype, ldx, w_codes, w_scales, y, y_dtype, ldy, workspace, workspace_bytes,
+                            stream)
+    if st:
+        _check("psgd_mx_linear", st)
 
 
 def psgd_timing_enable(plan: int, enable: bool) -> None:

@@ -16,28 +16,31 @@ _DTYPES = {torch.float32: B.PSGD_DTYPE_F32, torch.bfloat16: B.PSGD_DTYPE_BF16, t
 
 
 def _dtype(t: torch.Tensor) -> int:
-    try:
-        return _DTYPES[t.dtype]
-    except KeyError:
-        raise ValueError(f"expected float32, bfloat16 or float16, got {t.dtype}") from None
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"expected float32, bfloat16 or float16, got {t.dtype}")
+    return d
 
 
 def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-# The raw handle without building a Stream object, where this PyTorch has it:
-# small calls are bound by the host.
+# Small calls are bound by the host, so the common path (the tensors' device is
+# the current one) asks PyTorch's C layer for the device and the raw stream
+# where it offers them, instead of building Stream objects and contexts.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(device: torch.device, fn, *args) -> None:
     """fn(*args, stream) with `device` current, on its current stream."""
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if _raw_stream is not None and index == _current_device():
+        fn(*args, _raw_stream(index))
+    else:
         with torch.cuda.device(device):
             fn(*args, _stream(device))
-    else:
-        fn(*args, _raw_stream(device.index) if _raw_stream is not None else _stream(device))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -58,16 +61,17 @@ def _scratch(nbytes: int, device: torch.device):
     return ws, ws.data_ptr()
 
 
-def _matrix(x: torch.Tensor, name: str) -> int:
-    """The row stride of a row-major matrix (unit column stride)."""
-    if x.dim() != 2:
-        raise ValueError(f"{name} must be a matrix, got {x.dim()} dimensions")
+def _matrix(x: torch.Tensor, name: str):
+    """(rows, columns, row stride) of a row-major matrix on the GPU."""
+    st = x.stride()
+    if len(st) != 2:
+        raise ValueError(f"{name} must be a matrix, got {len(st)} dimensions")
     if not x.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
     rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    if st[1] != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return x.stride(0) if rows > 1 else max(1, cols)
+    return rows, cols, (st[0] if rows > 1 else max(1, cols))
 
 
 # ------------------------------------------------------------------- the clip
@@ -163,12 +167,13 @@ class MxTensor:
     def __init__(self, rows: int, cols: int, device):
         """Uninitialised operand: one allocation, the scales behind the codes
         at a multiple of 256 bytes."""
-        off = self._scales_at(rows, cols)
+        off = (rows * ((cols + 31) >> 5) * 16 + 255) & ~255
         self.rows, self.cols = rows, cols
-        self.buf = torch.empty(off + (rows + 31) // 32 * ((cols + 255) // 256) * 256, dtype=torch.uint8, device=device)
-        self.device = self.buf.device
-        self.codes_ptr = self.buf.data_ptr()
-        self.scales_ptr = self.codes_ptr + off
+        self.buf = buf = torch.empty(off + ((rows + 31) >> 5) * ((cols + 255) >> 8) * 256, dtype=torch.uint8,
+                                     device=device)
+        self.device = buf.device
+        self.codes_ptr = ptr = buf.data_ptr()
+        self.scales_ptr = ptr + off
 
     @staticmethod
     def _scales_at(rows: int, cols: int) -> int:
@@ -190,25 +195,32 @@ class MxTensor:
         return self.buf[self._scales_at(self.rows, self.cols):]
 
 
-def _rand(rand: Optional[torch.Tensor], x: torch.Tensor) -> int:
-    if rand is None:
-        return 0
+def _rand(rand: torch.Tensor, x: torch.Tensor) -> int:
     if rand.dtype != torch.uint8 or rand.shape != x.shape or not rand.is_contiguous() or rand.device != x.device:
         raise ValueError("rand must be a contiguous uint8 matrix of x's shape on x's device")
     return rand.data_ptr()
 
 
-def _quantize(x, rand, row: Optional[MxTensor], col: Optional[MxTensor], values) -> None:
-    ld = _matrix(x, "x")
-    ldv = 0
+def _quantize(x, rand, want_row: bool, want_col: bool, values):
+    rows, cols, ld = _matrix(x, "x")
+    dtype, device = _dtype(x), x.device
+    ptr, ldv = 0, 0
     if values is not None:
-        if values.shape != x.shape or values.dtype != x.dtype or values.device != x.device:
+        vr, vc, ldv = _matrix(values, "values")
+        if vr != rows or vc != cols or values.dtype != x.dtype or values.device != device:
             raise ValueError("values must have x's shape, type and device")
-        ldv = _matrix(values, "values")
-    rows, cols = x.shape
-    _call(x.device, B.psgd_mx_quantize, x.data_ptr(), _dtype(x), rows, cols, ld, _rand(rand, x),
-          row.codes_ptr if row else 0, row.scales_ptr if row else 0, col.codes_ptr if col else 0,
-          col.scales_ptr if col else 0, values.data_ptr() if values is not None else 0, ldv)
+        ptr = values.data_ptr()
+    r = 0 if rand is None else _rand(rand, x)
+    q = t = None
+    rc = rs = cc = cs = 0
+    if want_row:
+        q = MxTensor(rows, cols, device)
+        rc, rs = q.codes_ptr, q.scales_ptr
+    if want_col:
+        t = MxTensor(cols, rows, device)
+        cc, cs = t.codes_ptr, t.scales_ptr
+    _call(device, B.psgd_mx_quantize, x.data_ptr(), dtype, rows, cols, ld, r, rc, rs, cc, cs, ptr, ldv)
+    return q, t
 
 
 def mx_quantize(x: torch.Tensor, rand: Optional[torch.Tensor] = None,
@@ -216,24 +228,18 @@ def mx_quantize(x: torch.Tensor, rand: Optional[torch.Tensor] = None,
     """The operand of x: blocks of 32 along its rows.  rand: uint8 of x's shape
     for stochastic rounding (None: nearest).  values: receives the values that
     the codes stand for (x's shape and type; may be x itself)."""
-    q = MxTensor(x.shape[0], x.shape[-1], x.device)
-    _quantize(x, rand, q, None, values)
-    return q
+    return _quantize(x, rand, True, False, values)[0]
 
 
 def mx_quantize_both(x: torch.Tensor, rand: Optional[torch.Tensor] = None) -> Tuple[MxTensor, MxTensor]:
     """The operands of x and of x^T (blocks along x's rows and along its
     columns), from one reading of x."""
-    q, t = MxTensor(x.shape[0], x.shape[-1], x.device), MxTensor(x.shape[-1], x.shape[0], x.device)
-    _quantize(x, rand, q, t, None)
-    return q, t
+    return _quantize(x, rand, True, True, None)
 
 
 def mx_quantize_t(x: torch.Tensor, rand: Optional[torch.Tensor] = None) -> MxTensor:
     """The operand of x^T: blocks of 32 along x's columns."""
-    t = MxTensor(x.shape[-1], x.shape[0], x.device)
-    _quantize(x, rand, None, t, None)
-    return t
+    return _quantize(x, rand, False, True, None)[1]
 
 
 def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -242,32 +248,33 @@ def mx_dequantize(q: MxTensor, dtype: torch.dtype = torch.float32, out: Optional
         out = torch.empty(q.rows, q.cols, dtype=dtype, device=q.device)
     elif out.shape != q.shape or out.device != q.device:
         raise ValueError("out must have the operand's shape and device")
-    ld = _matrix(out, "out")
+    _, _, ld = _matrix(out, "out")
     _call(q.device, B.psgd_mx_dequantize, q.codes_ptr, q.scales_ptr, q.rows, q.cols, out.data_ptr(), _dtype(out), ld)
     return out
 
 
-def _result(out, m: int, n: int, dtype, device) -> torch.Tensor:
+def _result(out, m: int, n: int, dtype, device):
+    """(the result's matrix, its row stride)."""
     if out is None:
-        return torch.empty(m, n, dtype=dtype, device=device)
-    if out.shape != (m, n) or out.device != device:
+        return torch.empty(m, n, dtype=dtype, device=device), max(1, n)
+    rows, cols, ld = _matrix(out, "out")
+    if rows != m or cols != n or out.device != device:
         raise ValueError(f"out must be a {m} x {n} matrix on {device}")
-    return out
+    return out, ld
 
 
 def mx_product(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
                accumulate: bool = False) -> torch.Tensor:
     """a b^T (accumulate: added to out), summed in fp32 and rounded once."""
-    if a.cols != b.cols or a.device != b.device:
-        raise ValueError(f"operands of {a.cols} and {b.cols} columns, on {a.device} and {b.device}")
+    m, n, k, device = a.rows, b.rows, a.cols, a.device
+    if k != b.cols or device != b.device:
+        raise ValueError(f"operands of {k} and {b.cols} columns, on {device} and {b.device}")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    m, n, k = a.rows, b.rows, a.cols
-    c = _result(out, m, n, dtype, a.device)
-    ldc = _matrix(c, "out")
+    c, ldc = _result(out, m, n, dtype, device)
     need = _product_workspace(m, n, k)
-    ws, ws_ptr = _scratch(need, a.device)
-    _call(a.device, B.psgd_mx_product, m, n, k, a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, c.data_ptr(),
+    ws, ws_ptr = _scratch(need, device)
+    _call(device, B.psgd_mx_product, m, n, k, a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, c.data_ptr(),
           _dtype(c), ldc, accumulate, ws_ptr, need)
     return c
 
@@ -276,15 +283,15 @@ def mx_linear(x: torch.Tensor, w: MxTensor, out: Optional[torch.Tensor] = None,
               dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """y = Q(x) w^T for weights that were quantised once (psgd_mx_linear); y
     has x's type unless dtype or out says otherwise."""
-    ldx = _matrix(x, "x")
-    m, k = x.shape
-    if k != w.cols or x.device != w.device:
-        raise ValueError(f"x has {k} columns on {x.device}, the weights {w.cols} on {w.device}")
-    y = _result(out, m, w.rows, dtype or x.dtype, x.device)
-    need = _linear_workspace(m, w.rows, k)
-    ws, ws_ptr = _scratch(need, x.device)
-    _call(x.device, B.psgd_mx_linear, m, w.rows, k, x.data_ptr(), _dtype(x), ldx, w.codes_ptr, w.scales_ptr,
-          y.data_ptr(), _dtype(y), _matrix(y, "out"), ws_ptr, need)
+    m, k, ldx = _matrix(x, "x")
+    n, device = w.rows, x.device
+    if k != w.cols or device != w.device:
+        raise ValueError(f"x has {k} columns on {device}, the weights {w.cols} on {w.device}")
+    y, ldy = _result(out, m, n, dtype or x.dtype, device)
+    need = _linear_workspace(m, n, k)
+    ws, ws_ptr = _scratch(need, device)
+    _call(device, B.psgd_mx_linear, m, n, k, x.data_ptr(), _dtype(x), ldx, w.codes_ptr, w.scales_ptr, y.data_ptr(),
+          _dtype(y), ldy, ws_ptr, need)
     return y
 
 
