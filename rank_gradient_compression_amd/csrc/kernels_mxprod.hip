@@ -148,18 +148,6 @@ __device__ __forceinline__ void tile_of_block(int b, int ntm, int ntn, int* tm, 
   *tn = in / rows;
 }
 
-template <int ROWS, int WAVES>
-__device__ __forceinline__ void fetch_chunk(__amdgpu_buffer_rsrc_t rs, uint8_t* lds, uint32_t lane_off, uint32_t lane_off1,
-                                            uint32_t pitch, uint32_t chunk_off, int wave) {
-#pragma unroll
-  for (int j = 0; j < ROWS / 8 / WAVES; ++j) {
-    const int row = wave * (ROWS / WAVES) + j * 8;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rs, (__attribute__((address_space(3))) void*)(lds + row * kChunkBytes), 16,
-        (int)((j & 1 ? lane_off1 : lane_off) + (uint32_t)row * pitch + chunk_off), 0, 0, 0);
-  }
-}
-
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 // E values as one 16-byte vector of the result's type.
@@ -314,20 +302,26 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
 #pragma unroll
     for (int j = 0; j < HB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   uint32_t sa[TM], sb[TN], ta[TM], tb[TN];
-  auto scales = [&](uint32_t ch, uint32_t(&xa)[TM], uint32_t(&xb)[TN]) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-      xa[i] = __builtin_amdgcn_raw_buffer_load_b32(rsa, lane * 4, (int)(as[i] + ch * 256), 0);
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-      xb[j] = __builtin_amdgcn_raw_buffer_load_b32(rsb, lane * 4, (int)(bs[j] + ch * 256), 0);
-  };
   const int la = wm * TM * 32 * kChunkBytes, lb = wn * TN * 32 * kChunkBytes;
-  auto fetch = [&](uint32_t ch, uint8_t* da, uint8_t* db) {
-    // no chunk past the last: an offset beyond the descriptor reads nothing
+  // One of the PA + PB loads (8 rows each) of a wavefront's share of a chunk,
+  // and one of its TM + TN scale tiles.  No chunk past the last: an offset
+  // beyond the descriptor reads nothing.
+  constexpr int PA = BM / 8 / WAVES, PB = BN / 8 / WAVES;
+  auto load_rows = [&](int j, uint32_t ch, uint8_t* da, uint8_t* db) {
+    const bool isa = j < PA;
+    const int i = isa ? j : j - PA, row = wave * (isa ? BM / WAVES : BN / WAVES) + i * 8;
     const uint32_t o = ch < nch ? ch * kChunkBytes : 0x80000000u;
-    fetch_chunk<BM, WAVES>(ra, da, lane_off, lane_off1, pitch, o, wave);
-    fetch_chunk<BN, WAVES>(rb, db, lane_off, lane_off1, pitch, o, wave);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        isa ? ra : rb, (__attribute__((address_space(3))) void*)((isa ? da : db) + row * kChunkBytes), 16,
+        (int)((i & 1 ? lane_off1 : lane_off) + (uint32_t)row * pitch + o), 0, 0, 0);
+  };
+  auto load_scale = [&](int j, uint32_t ch, uint32_t(&xa)[TM], uint32_t(&xb)[TN]) {
+    const uint32_t o = min(ch, nch - 1) * 256;
+    if (j < TM)
+      xa[j < TM ? j : 0] = __builtin_amdgcn_raw_buffer_load_b32(rsa, lane * 4, (int)(as[j < TM ? j : 0] + o), 0);
+    else
+      xb[j < TM ? 0 : j - TM] =
+          __builtin_amdgcn_raw_buffer_load_b32(rsb, lane * 4, (int)(bs[j < TM ? 0 : j - TM] + o), 0);
   };
   auto read_a = [&](const uint8_t* m, int q) {  // group q of a chunk
     return *reinterpret_cast<const uint4*>(m + la + off[q / HA] + q % HA * 16 * kChunkBytes);
@@ -339,8 +333,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
   // The barrier stands DEPTH groups before the chunk's end: their operands are
   // in registers, so their products cover it and the first reads of the next
   // chunk, and behind it every wavefront is done with this chunk's stage.
-  auto chunk = [&](const uint8_t* ca, const uint8_t* cb, const uint8_t* na, const uint8_t* nb,
-                   const uint32_t(&xa)[TM], const uint32_t(&xb)[TN]) {
+  // The next chunk's loads are issued two to a group of a 128 x 128 tile, one
+  // to a group of a 256 x 256 tile: all at once they hold up the products
+  // behind them (8192^3: 288 us against 281).
+  constexpr int PER_GROUP = (PA + PB) * 2 / GROUPS;
+  static_assert((PA + PB) <= PER_GROUP * (GROUPS - DEPTH) && TM + TN <= GROUPS - DEPTH, "loads behind the barrier");
+  auto chunk = [&](uint32_t next, const uint8_t* ca, const uint8_t* cb, uint8_t* na, uint8_t* nb,
+                   const uint32_t(&xa)[TM], const uint32_t(&xb)[TN], uint32_t(&ya)[TM], uint32_t(&yb)[TN]) {
     uint4 a[GROUPS + DEPTH], b[3][HB];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) a[d] = qa[d];
@@ -354,6 +353,10 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int j = 0; j < PER_GROUP; ++j)
+        if (q * PER_GROUP + j < PA + PB) load_rows(q * PER_GROUP + j, next, na, nb);
+      if (q < TM + TN) load_scale(q, next, ya, yb);
       // B's next operands first: the first groups of step 0 read step 1's, the
       // first groups behind the barrier the next chunk's
 #pragma unroll
@@ -378,8 +381,10 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
 #pragma unroll
     for (int j = 0; j < HB; ++j) qb[j] = b[2][j];
   };
-  scales(0, sa, sb);
-  fetch(0, a0, b0);
+#pragma unroll
+  for (int j = 0; j < TM + TN; ++j) load_scale(j, 0, sa, sb);
+#pragma unroll
+  for (int j = 0; j < PA + PB; ++j) load_rows(j, 0, a0, b0);
   __syncthreads();
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) qa[d] = read_a(a0, d);
@@ -387,12 +392,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
   for (int j = 0; j < HB; ++j) qb[j] = read_b(b0, 0, j);
   // (an odd last chunk is paired with one of zero codes)
   for (uint32_t ch = 0; ch < nch; ch += 2) {
-    scales(min(ch + 1, nch - 1), ta, tb);
-    fetch(ch + 1, a1, b1);
-    chunk(a0, b0, a1, b1, sa, sb);
-    scales(min(ch + 2, nch - 1), sa, sb);
-    fetch(ch + 2, a0, b0);
-    chunk(a1, b1, a0, b0, ta, tb);
+    chunk(ch + 1, a0, b0, a1, b1, sa, sb, ta, tb);
+    chunk(ch + 2, a1, b1, a0, b0, ta, tb, sa, sb);
   }
   // (every wavefront is behind its last barrier: the stages are free)
   constexpr int RE = mx_epilogue_rows<WAVES, TN, sizeof a0, sizeof b0>();
@@ -716,20 +717,19 @@ static void product_dt(const MxProductArgs& p, hipStream_t s) {
       product_skinny<true>(ba, s);
     return;
   }
-  // Tiles as large as still give each of the 256 compute units one: a larger
-  // tile reads its operands fewer times, but an idle compute unit costs more
-  // (2048 x 4096 x 11008: 128 tiles of 256 x 256 70 us, 256 of 128 x 256 54;
-  // 2048 x 11008 x 4096: 344 of 256 x 256 58 us, 688 of 128 x 256 72).  A
-  // single chunk is a write of C and hardly a product: small workgroups that
-  // store from the accumulators (11008 x 4096 x 64: 33 us against 41).
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((p.m + bm - 1) / bm) * ((p.n + bn - 1) / bn); };
+  // Tiles as large as still occupy more than half of the 256 compute units: a
+  // larger tile reads its operands fewer times, but idle compute units cost
+  // more (2048 x 4096 x 11008: 128 tiles of 256 x 256 70 us, 512 of 128 x 128,
+  // two workgroups to a compute unit, 60; 2048 x 11008 x 4096: 344 of 256 x
+  // 256 64 us, 1376 of 128 x 128 67).  Below, 64 x 64 tiles whose wavefronts
+  // share the summed axis.  A single chunk is a write of C and hardly a
+  // product: small workgroups.
+  auto tiles = [&](int64_t b) { return ((p.m + b - 1) / b) * ((p.n + b - 1) / b); };
   if (fits && p.k > 256) {
-    if (tiles(64, 64) <= 256)
+    if (tiles(64) <= 256)
       skinny<4, 2, false, -1>(ab, s);
-    else if (tiles(128, 128) <= 256)
+    else if (tiles(256) <= 128)
       product_lds<DT, 2, 2, 2, 2>(p, s);
-    else if (tiles(128, 256) <= 256)
-      product_lds<DT, 2, 2, 2, 4>(p, s);
     else
       product_lds<DT, 2, 4, 4, 2>(p, s);
     return;
