@@ -70,13 +70,43 @@ __device__ __forceinline__ void store4(void* c, int64_t i, v4f v, int64_t n, boo
   }
 }
 
-// Any sizes: one wavefront = one 32 x 32 tile of C, operands straight from
-// memory.  Row and block indexes past the end are clamped into the operand:
-// such rows are not stored, and such blocks have scale 0 in both operands.
+// Workgroup b of `total` to a position in the walk over C's tiles: consecutive
+// workgroups go to the eight XCDs in turn, each with an L2 of its own, so XCD x
+// takes the x-th eighth of the walk.
+__device__ __forceinline__ int xcd_position(int b, int total) {
+  const int q = total / 8, rem = total % 8, x = b % 8;
+  return x * q + min(x, rem) + b / 8;
+}
+
+// The walk of the large products: groups of 8 tile rows, so that the 32 tiles
+// that an XCD's compute units work on at a time form an 8 x 4 block that
+// shares its operands in L2.
+__device__ __forceinline__ void tile_of_block(int b, int ntm, int ntn, int* tm, int* tn) {
+  const int t = xcd_position(b, ntm * ntn);
+  const int first = t / (8 * ntn) * 8, rows = min(8, ntm - first), in = t % (8 * ntn);
+  *tm = first + in % rows;
+  *tn = in / rows;
+}
+
+template <int DT>
+__device__ __forceinline__ void store1(void* c, int64_t i, float v, bool acc) {
+  auto* p = static_cast<typename Elem<DT>::type*>(c) + i;
+  *p = Elem<DT>::down(acc ? v + Elem<DT>::up(*p) : v);
+}
+
+// Any sizes, and the choice for sums of one chunk, which are a write of C and
+// hardly a product: one wavefront = one 32 x 32 tile of C, operands straight
+// from memory.  Row and block indexes past the end are clamped into the
+// operand: such rows are not stored, and such blocks have scale 0 in both
+// operands.  Here A's rows are the first operand, so that a register is 16
+// columns of four rows; two neighbouring tiles exchange quarters of the
+// lanes, and every store is 128 bytes of fp32 in two rows (11008 x 4096 x 64:
+// 33 us; with 64 bytes in 16 rows, from the other operand order, 56).
 template <int DT>
 __global__ __launch_bounds__(256) void k_mx_prod_tile(MxProductArgs p, int ntn) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t tm = (int64_t)(blockIdx.x / ntn) * 2 + (wave >> 1), tn = (int64_t)(blockIdx.x % ntn) * 2 + (wave & 1);
+  const int t = xcd_position(blockIdx.x, gridDim.x);  // (lines that two neighbouring tiles write meet in one L2)
+  const int64_t tm = (int64_t)(t / ntn) * 2 + (wave >> 1), tn = (int64_t)(t % ntn) * 2 + (wave & 1);
   if (tm * 32 >= p.m || tn * 32 >= p.n) return;
   const int64_t nch = mx_chunks(p.k), nblk = mx_blocks(p.k), pitch = nblk * 16;
   const int r = lane & 15, g = lane >> 4;
@@ -108,18 +138,21 @@ __global__ __launch_bounds__(256) void k_mx_prod_tile(MxProductArgs p, int ntn) 
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mx_mfma_at(s, j, i, b[s][j], a[s][i], acc[i][j], sb, sa);
+        for (int j = 0; j < 2; ++j) acc[i][j] = mx_mfma_at(s, i, j, a[s][i], b[s][j], acc[i][j], sa, sb);
   }
+  const int64_t row0 = tm * 32 + 8 * (g >> 1), col = tn * 32 + 16 * (g & 1) + r;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t row = tm * 32 + 16 * i + r;
-    if (row >= p.m) continue;
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t col = tn * 32 + 16 * j + 4 * g;
-      if (col < p.n) store4<DT>(p.c, row * p.ldc + col, acc[i][j], p.n - col, p.accumulate);
+    for (int e = 0; e < 4; ++e) {
+      const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][0][e]), __float_as_uint(acc[i][1][e]),
+                                                      false, false);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t row = row0 + 16 * i + 4 * h + e;
+        if (row < p.m && col < p.n) store1<DT>(p.c, row * p.ldc + col, __uint_as_float(x[h]), p.accumulate);
+      }
     }
-  }
 }
 
 // Large products: a workgroup computes a BM x BN tile of C with WM x WN
@@ -135,18 +168,6 @@ __global__ __launch_bounds__(256) void k_mx_prod_tile(MxProductArgs p, int ntn) 
 // descriptors end with the tile's last row: rows past it read as zero, without
 // a fault.
 constexpr int kChunkBytes = 128;
-
-// Workgroup to tile: consecutive workgroups go to the eight XCDs in turn, each
-// with an L2 of its own, so XCD x gets the x-th eighth of the tiles, and these
-// are walked in groups of 8 tile rows: the 32 tiles that an XCD's compute
-// units work on at a time form an 8 x 4 block that shares its operands in L2.
-__device__ __forceinline__ void tile_of_block(int b, int ntm, int ntn, int* tm, int* tn) {
-  const int total = ntm * ntn, q = total / 8, rem = total % 8, x = b % 8;
-  const int t = x * q + min(x, rem) + b / 8;
-  const int first = t / (8 * ntn) * 8, rows = min(8, ntm - first), in = t % (8 * ntn);
-  *tm = first + in % rows;
-  *tn = in / rows;
-}
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
