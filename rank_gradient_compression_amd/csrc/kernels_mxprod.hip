@@ -494,30 +494,21 @@ struct MxRows {
 template <int DT>
 __device__ __forceinline__ uint32_t mx_quant_block(const typename Elem<DT>::type* p, int n, uint4* q) {
   using T = typename Elem<DT>::type;
-  T v[32];
-  if (n >= 32 && ((uintptr_t)p & 15) == 0) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 16 / (int)sizeof(T))
-      __builtin_memcpy(&v[i], __builtin_assume_aligned(p + i, 16), 16);
+  constexpr int W = 32 / kPerWord<DT>;
+  uint32_t w[W], am = 0;
+  if (n >= 32) {
+    __builtin_memcpy(w, p, sizeof w);
   } else {
+    T v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = i < n ? p[i] : (T)0;
+    __builtin_memcpy(w, v, sizeof w);
   }
-  float f[32];
-  uint32_t am = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    f[i] = Elem<DT>::up(v[i]);
-    am = max(am, __float_as_uint(f[i]) & 0x7fffffffu);
-  }
-  const uint32_t sb = mx_scale_byte(am);
-  const float inv = sb == 255u ? 0.f : mx_inv_scale(sb);
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = sb == 255u ? 0.f : f[i] * inv;
-  q->x = mx_encode8(f);
-  q->y = mx_encode8(f + 8);
-  q->z = mx_encode8(f + 16);
-  q->w = mx_encode8(f + 24);
+  for (int i = 0; i < W; ++i) am = mx_max_words<DT>(am, w[i]);
+  const uint32_t sb = mx_scale_byte(mx_max_bits<DT>(am));
+  *q = make_uint4(mx_nearest8<DT>(w, sb), mx_nearest8<DT>(w + W / 4, sb), mx_nearest8<DT>(w + W / 2, sb),
+                  mx_nearest8<DT>(w + 3 * W / 4, sb));
   return sb;
 }
 

@@ -14,23 +14,25 @@
 
 namespace psgd {
 
-// N consecutive elements of a row from column `col` on; zero past `cols`.  FULL:
-// all N are inside the row (whatever its alignment: the hardware takes 16-byte
-// accesses at any element's address, and on rows of 650 floats they beat pairs
-// of 8-byte ones).  Else every element is read at a column clamped into the
-// row and masked afterwards: a branch around a load would make the compiler
-// wait for it before it issues the next.
+// N consecutive elements of a row from column `col` on, as words; zero past
+// `cols`.  FULL: all N are inside the row (whatever its alignment: the hardware
+// takes 16-byte accesses at any element's address, and on rows of 650 floats
+// they beat pairs of 8-byte ones).  Else every element is read at a column
+// clamped into the row and masked afterwards: a branch around a load would
+// make the compiler wait for it before it issues the next.
 template <int DT, bool FULL, int N>
 __device__ __forceinline__ void load_elems(const typename Elem<DT>::type* row, int64_t col, int64_t cols,
-                                           typename Elem<DT>::type (&v)[N]) {
+                                           uint32_t (&w)[N]) {
   using T = typename Elem<DT>::type;
   if (FULL) {
-    __builtin_memcpy(v, row + col, sizeof v);
+    __builtin_memcpy(w, row + col, sizeof w);
   } else {
+    T v[N * kPerWord<DT>];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = row[min(col + i, cols - 1)];
+    for (int i = 0; i < N * kPerWord<DT>; ++i) v[i] = row[min(col + i, cols - 1)];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = col + i < cols ? v[i] : (T)0;
+    for (int i = 0; i < N * kPerWord<DT>; ++i) v[i] = col + i < cols ? v[i] : (T)0;
+    __builtin_memcpy(w, v, sizeof w);
   }
 }
 
@@ -45,105 +47,73 @@ __device__ __forceinline__ void store_elems(typename Elem<DT>::type* p, int n, c
   }
 }
 
+// N words of random bytes of a row, clamped into it as above.
 template <bool FULL, int N>
-__device__ __forceinline__ void load_bytes(const uint8_t* row, int64_t col, int64_t cols, uint8_t (&v)[N]) {
+__device__ __forceinline__ void load_bytes(const uint8_t* row, int64_t col, int64_t cols, uint32_t (&w)[N]) {
   if (FULL) {
-    __builtin_memcpy(v, row + col, N);
+    __builtin_memcpy(w, row + col, sizeof w);
   } else {
+    uint8_t v[4 * N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = row[min(col + i, cols - 1)];
+    for (int i = 0; i < 4 * N; ++i) v[i] = row[min(col + i, cols - 1)];
+    __builtin_memcpy(w, v, sizeof w);
   }
 }
 
-// Largest magnitude (bit pattern) over groups of L consecutive lanes.
+// Largest of a value over groups of L consecutive lanes, by lane exchanges of
+// the vector unit: within pairs, within quads, quads of eight mirrored.
 template <int L>
 __device__ __forceinline__ uint32_t group_max(uint32_t a) {
-#pragma unroll
-  for (int o = 1; o < L; o <<= 1) a = max(a, (uint32_t)__shfl_xor((int)a, o));
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xf, 0xf, true));
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x4E, 0xf, 0xf, true));
+  if (L == 8) a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x141, 0xf, 0xf, true));
   return a;
 }
 
 // Row operand.  One workgroup = 32 rows x 256 columns (one tile of scales);
-// every thread takes 16 bytes of a row at a time, so 4 (16-bit types) or 8
-// (fp32) neighbouring lanes share a block and agree on its exponent by lane
-// exchanges; scales are gathered in LDS and leave as one 256-byte tile.
+// every thread takes 8 values of a row at a time, so 4 neighbouring lanes share
+// a block and agree on its exponent by lane exchanges; scales are gathered in
+// LDS and leave as one 256-byte tile.
 template <int DT, bool RAND, bool VALUES, bool FULL>
 __device__ __forceinline__ void quant_rows_tile(const MxQuantArgs& a, int nch, uint32_t (&tile)[64]) {
   using T = typename Elem<DT>::type;
-  constexpr int E = 16 / (int)sizeof(T);   // elements per thread and row
-  constexpr int L = kMxBlock / E;          // lanes per block
-  constexpr int TPR = 256 / E;             // threads per row of the tile
-  constexpr int RPP = 256 / TPR;           // rows per sweep of the workgroup
-  constexpr int SWEEPS = 32 / RPP;
+  constexpr int W = 8 / kPerWord<DT>;  // words of 8 values
   const int rt = blockIdx.x / nch, ch = blockIdx.x % nch;
   const int64_t row0 = (int64_t)rt * 32;
-  const int col = ch * 256 + (int)(threadIdx.x % TPR) * E;
-  const int nvalid = (int)min((int64_t)E, max((int64_t)0, a.cols - col));
+  const int64_t col = (int64_t)ch * 256 + (int)(threadIdx.x % 32) * 8;
+  const int nvalid = (int)min((int64_t)8, max((int64_t)0, a.cols - col));
   const int nrows = (int)min((int64_t)32, a.rows - row0);
   const int64_t nblk = mx_blocks(a.cols);
   const T* x = static_cast<const T*>(a.x);
-  T v[SWEEPS][E];
-  uint8_t rnd[SWEEPS][E];
+  uint32_t v[4][W], rnd[4][2];
 #pragma unroll
-  for (int s = 0; s < SWEEPS; ++s) {
-    const int r = s * RPP + (int)threadIdx.x / TPR;
-    load_elems<DT, FULL>(x + (row0 + min(r, nrows - 1)) * a.ld, col, a.cols, v[s]);
-    if constexpr (RAND) load_bytes<FULL>(a.rand + (row0 + min(r, nrows - 1)) * a.cols, col, a.cols, rnd[s]);
+  for (int s = 0; s < 4; ++s) {
+    const int64_t row = row0 + min(s * 8 + (int)threadIdx.x / 32, nrows - 1);
+    load_elems<DT, FULL>(x + row * a.ld, col, a.cols, v[s]);
+    if constexpr (RAND) load_bytes<FULL>(a.rand + row * a.cols, col, a.cols, rnd[s]);
   }
   uint8_t* tb = reinterpret_cast<uint8_t*>(tile);
 #pragma unroll
-  for (int s = 0; s < SWEEPS; ++s) {
-    const int r = s * RPP + (int)threadIdx.x / TPR;
-    const int64_t row = row0 + r;
-    const bool live = r < nrows;
-    float f[E];
+  for (int s = 0; s < 4; ++s) {
+    const int r = s * 8 + (int)threadIdx.x / 32;
     uint32_t am = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      f[i] = Elem<DT>::up(v[s][i]);
-      am = max(am, __float_as_uint(f[i]) & 0x7fffffffu);
-    }
-    am = group_max<L>(am);
-    const uint32_t sb = mx_scale_byte(am);
-    const float inv = sb == 255u ? 0.f : mx_inv_scale(sb);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      float t = f[i] * inv;
-      if (sb == 255u) t = 0.f;  // 0 * NaN
-      if constexpr (RAND) t = mx_stochastic(t, rnd[s][i]);
-      f[i] = t;
-    }
-    uint32_t code;
-    if constexpr (E == 8)
-      code = mx_encode8(f);
-    else
-      code = mx_encode4(f);
-    const int blk = col >> 5;
-    if ((threadIdx.x % L) == 0) tb[mx_scale_in_tile(r, blk & 7)] = (uint8_t)sb;
-    if (live && (FULL || blk < nblk)) {
-      if (a.row_codes) {
-        uint8_t* cp = a.row_codes + row * (nblk * 16) + (col >> 1);
-        if constexpr (E == 8)
-          *reinterpret_cast<uint32_t*>(cp) = code;
-        else
-          *reinterpret_cast<uint16_t*>(cp) = (uint16_t)code;
-      }
+    for (int i = 0; i < W; ++i) am = mx_max_words<DT>(am, v[s][i]);
+    const uint32_t sb = mx_scale_byte(group_max<4>(mx_max_bits<DT>(am)));
+    const uint32_t code = mx_encode8<DT, RAND>(v[s], sb, rnd[s]);
+    const int blk = (int)(col >> 5);
+    if ((threadIdx.x & 3) == 0) tb[mx_scale_in_tile(r, blk & 7)] = (uint8_t)sb;
+    if (r < nrows && (FULL || blk < nblk)) {
+      if (a.row_codes) *reinterpret_cast<uint32_t*>(a.row_codes + (row0 + r) * (nblk * 16) + (col >> 1)) = code;
       if constexpr (VALUES) {
         const int k = (int)sb - 127;
-        T o[E];
-        float2 d[E / 2];
-        d[0] = mx_decode2<0>(code, k);
-        d[1] = mx_decode2<1>(code, k);
-        if constexpr (E == 8) {
-          d[2] = mx_decode2<2>(code, k);
-          d[3] = mx_decode2<3>(code, k);
-        }
+        const float2 d[4] = {mx_decode2<0>(code, k), mx_decode2<1>(code, k), mx_decode2<2>(code, k),
+                             mx_decode2<3>(code, k)};
+        T o[8];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float q = sb == 255u ? __uint_as_float(0x7fc00000u) : (i & 1) ? d[i / 2].y : d[i / 2].x;
-          o[i] = Elem<DT>::down(q);
-        }
-        store_elems<DT, FULL>(static_cast<T*>(a.values) + row * a.ldv + col, nvalid, o);
+        for (int i = 0; i < 8; ++i)
+          o[i] = Elem<DT>::down(sb == 255u ? __uint_as_float(0x7fc00000u) : (i & 1) ? d[i / 2].y : d[i / 2].x);
+        store_elems<DT, FULL>(static_cast<T*>(a.values) + (row0 + r) * a.ldv + col, nvalid, o);
       }
     }
   }
@@ -166,127 +136,114 @@ __global__ __launch_bounds__(256) void k_mx_quant_rows(MxQuantArgs a, int nch) {
 // operand of the same reading of x where it is wanted.  One workgroup = 128 x
 // 128 values held in LDS: four blocks per column give 64 contiguous bytes of
 // codes per column and per row.  In LDS each group of 32 rows is shifted by
-// 64 bytes against the one above (16 columns of two 2-byte values), so that
-// the four blocks of a column that neighbouring lanes read fall into distinct
-// banks.
+// 64 bytes against the one above, so that the four blocks of a column, which
+// neighbouring lanes read, fall into distinct banks.
 template <int DT>
 constexpr int kColPitch = 128 + 16 / dtype_bytes(DT);  // row pitch in LDS, elements
 template <int DT>
-constexpr int kColSkew = 64 * (DT == kF32 ? 2 : 1) / dtype_bytes(DT);  // shift per 32 rows
+constexpr int kColSkew = 64 / dtype_bytes(DT);  // shift per 32 rows, elements
 constexpr int kColRandPitch = 132;
 
 // The tile into LDS, and its random bytes.
 template <int DT, bool RAND, bool FULL>
-__device__ __forceinline__ void cols_tile_load(const MxQuantArgs& a, int64_t row0, int64_t col,
+__device__ __forceinline__ void cols_tile_load(const MxQuantArgs& a, int64_t row0, int64_t col0,
                                                typename Elem<DT>::type* tile, uint8_t* rtile) {
   using T = typename Elem<DT>::type;
-  constexpr int E = 16 / (int)sizeof(T), TPR = 128 / E, RPP = 256 / TPR, SWEEPS = 128 / RPP;
+  constexpr int E = 4 * kPerWord<DT>, TPR = 128 / E, RPP = 256 / TPR, SWEEPS = 128 / RPP;  // 16 bytes per thread and row
   const T* x = static_cast<const T*>(a.x);
   const int c = (int)(threadIdx.x % TPR) * E, r0 = (int)threadIdx.x / TPR;
-  T v[SWEEPS][E];
-  uint8_t rnd[SWEEPS][E];
+  uint32_t v[SWEEPS][4], rnd[SWEEPS][E / 4];
 #pragma unroll
   for (int s = 0; s < SWEEPS; ++s) {
     const int64_t row = min(row0 + s * RPP + r0, a.rows - 1);
-    load_elems<DT, FULL>(x + row * a.ld, col, a.cols, v[s]);
-    if constexpr (RAND) load_bytes<FULL>(a.rand + row * a.cols, col, a.cols, rnd[s]);
+    load_elems<DT, FULL>(x + row * a.ld, col0 + c, a.cols, v[s]);
+    if constexpr (RAND) load_bytes<FULL>(a.rand + row * a.cols, col0 + c, a.cols, rnd[s]);
   }
 #pragma unroll
   for (int s = 0; s < SWEEPS; ++s) {
     const int r = s * RPP + r0;
-    if (row0 + r >= a.rows)
-#pragma unroll
-      for (int i = 0; i < E; ++i) v[s][i] = (T)0;
-    __builtin_memcpy(__builtin_assume_aligned(&tile[r * kColPitch<DT> + (r >> 5) * kColSkew<DT> + c], 16), v[s], 16);
+    uint4 q = make_uint4(v[s][0], v[s][1], v[s][2], v[s][3]);
+    if (row0 + r >= a.rows) q = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(&tile[r * kColPitch<DT> + (r >> 5) * kColSkew<DT> + c]) = q;
     if constexpr (RAND) __builtin_memcpy(__builtin_assume_aligned(&rtile[r * kColRandPitch + c], 4), rnd[s], E);
   }
 }
 
-// 32 values of a block that a thread holds, to 16 bytes of codes.
-template <bool RAND, typename R>
-__device__ __forceinline__ uint4 encode_block(float (&f)[32], uint32_t sb, R rnd) {
-  const float inv = sb == 255u ? 0.f : mx_inv_scale(sb);
-  uint4 q;
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-#pragma unroll
-    for (int i = 8 * h; i < 8 * h + 8; ++i) {
-      float t = sb == 255u ? 0.f : f[i] * inv;
-      if constexpr (RAND) t = mx_stochastic(t, rnd(i));
-      f[i] = t;
-    }
-    (&q.x)[h] = mx_encode8(&f[8 * h]);
-  }
-  return q;
+// A block of 32 values to 16 bytes of codes.
+template <int DT, bool RAND>
+__device__ __forceinline__ uint4 encode_block(const uint32_t (&w)[32 / kPerWord<DT>], uint32_t sb,
+                                              const uint32_t (&rnd)[8]) {
+  constexpr int W = 8 / kPerWord<DT>;
+  return make_uint4(mx_encode8<DT, RAND>(w, sb, rnd), mx_encode8<DT, RAND>(w + W, sb, rnd + 2),
+                    mx_encode8<DT, RAND>(w + 2 * W, sb, rnd + 4), mx_encode8<DT, RAND>(w + 3 * W, sb, rnd + 6));
 }
 
 // (The instructions of a small call come from memory too: the parts are
-// loops, and the three kinds of tiles share all but their loads.)
+// loops, and the kinds of tiles share all but their loads.)
 template <int DT, bool RAND, bool ROWS>
 __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantArgs a, int nct) {
   using T = typename Elem<DT>::type;
-  constexpr int P = kColPitch<DT>, SKEW = kColSkew<DT>, RP = kColRandPitch;
+  constexpr int P = kColPitch<DT>, SKEW = kColSkew<DT>, RP = kColRandPitch, PW = kPerWord<DT>;
   __shared__ __align__(16) T tile[128 * P + 4 * SKEW];
   __shared__ __align__(16) uint8_t rtile[RAND ? 128 * RP : 16];
   __shared__ uint32_t stile[ROWS ? 128 : 1], ctile[128];  // four tiles' half chunks
   const int rt = blockIdx.x / nct, ct = blockIdx.x % nct;
   const int64_t row0 = (int64_t)rt * 128, col0 = (int64_t)ct * 128;
   const int64_t nblk_r = mx_blocks(a.cols), nblk_c = mx_blocks(a.rows);
-  {
-    constexpr int E = 16 / (int)sizeof(T);
-    const int64_t col = col0 + (int)(threadIdx.x % (128 / E)) * E;
-    if (col0 + 128 <= a.cols)
-      cols_tile_load<DT, RAND, true>(a, row0, col, tile, rtile);
-    else
-      cols_tile_load<DT, RAND, false>(a, row0, col, tile, rtile);
-  }
+  if (col0 + 128 <= a.cols)
+    cols_tile_load<DT, RAND, true>(a, row0, col0, tile, rtile);
+  else
+    cols_tile_load<DT, RAND, false>(a, row0, col0, tile, rtile);
   __syncthreads();
   if constexpr (ROWS) {
     // A thread takes blocks of 32 columns of a row: 512 blocks in the tile.
-    // (A row's four blocks go to four wavefront quarters, so that the reads of
-    // 16 lanes fall into 16 rows.)
 #pragma unroll 1
     for (int i = threadIdx.x; i < 512; i += 256) {
       const int r = i % 128, b = i / 128;
       const T* src = &tile[r * P + (r >> 5) * SKEW + b * 32];
-      float f[32];
-      uint32_t am = 0;
-      constexpr int E = 16 / (int)sizeof(T);
+      uint32_t w[32 / PW], rnd[8], am = 0;
+      __builtin_memcpy(w, __builtin_assume_aligned(src, 16), sizeof w);
+      if constexpr (RAND) __builtin_memcpy(rnd, __builtin_assume_aligned(&rtile[r * RP + b * 32], 4), 32);
 #pragma unroll
-      for (int j = 0; j < 32; j += E) {
-        T v[E];
-        __builtin_memcpy(v, __builtin_assume_aligned(src + j, 16), 16);
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-          f[j + k] = Elem<DT>::up(v[k]);
-          am = max(am, __float_as_uint(f[j + k]) & 0x7fffffffu);
-        }
-      }
-      const uint32_t sb = mx_scale_byte(am);
-      const uint4 q = encode_block<RAND>(f, sb, [&](int k) { return rtile[r * RP + b * 32 + k]; });
+      for (int j = 0; j < 32 / PW; ++j) am = mx_max_words<DT>(am, w[j]);
+      const uint32_t sb = mx_scale_byte(mx_max_bits<DT>(am));
+      const uint4 q = encode_block<DT, RAND>(w, sb, rnd);
       reinterpret_cast<uint8_t*>(stile)[r / 32 * 128 + mx_scale_in_tile(r % 32, b)] = (uint8_t)sb;
       if (row0 + r < a.rows && ct * 4 + b < nblk_r)
         *reinterpret_cast<uint4*>(a.row_codes + ((row0 + r) * nblk_r + ct * 4 + b) * 16) = q;
     }
   }
-  // A thread takes blocks of 32 rows of a column; the four blocks of a column
-  // sit in neighbouring lanes.
+  // A thread takes blocks of 32 rows of a column, or of a pair of columns of a
+  // 16-bit type (one word of each row); the four blocks of a column sit in
+  // neighbouring lanes.
 #pragma unroll 1
-  for (int i = threadIdx.x; i < 512; i += 256) {
-    const int b = i & 3, c = i >> 2;
+  for (int i = threadIdx.x; i < 512 / PW; i += 256) {
+    const int b = i & 3, c = (i >> 2) * PW;
     const T* src = &tile[b * (32 * P + SKEW) + c];
-    float f[32];
-    uint32_t am = 0;
+    uint32_t w[32], am = 0;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      f[j] = Elem<DT>::up(src[j * P]);
-      am = max(am, __float_as_uint(f[j]) & 0x7fffffffu);
+      __builtin_memcpy(&w[j], __builtin_assume_aligned(src + j * P, 4), 4);
+      am = mx_max_words<DT>(am, w[j]);
     }
-    const uint32_t sb = mx_scale_byte(am);
-    const uint4 q = encode_block<RAND>(f, sb, [&](int k) { return rtile[(b * 32 + k) * RP + c]; });
-    reinterpret_cast<uint8_t*>(ctile)[c / 32 * 128 + mx_scale_in_tile(c % 32, b)] = (uint8_t)sb;
-    if (col0 + c < a.cols && rt * 4 + b < nblk_c)
-      *reinterpret_cast<uint4*>(a.col_codes + ((col0 + c) * nblk_c + rt * 4 + b) * 16) = q;
+#pragma unroll
+    for (int h = 0; h < PW; ++h) {  // column c + h
+      uint32_t u[32 / PW], rnd[8];
+#pragma unroll
+      for (int j = 0; j < 32 / PW; ++j)
+        u[j] = PW == 1 ? w[j] : __builtin_amdgcn_perm(w[PW * j + PW - 1], w[PW * j], h ? 0x07060302u : 0x05040100u);
+      if constexpr (RAND) {
+        uint8_t y[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = rtile[(b * 32 + j) * RP + c + h];
+        __builtin_memcpy(rnd, y, 32);
+      }
+      const uint32_t sb = mx_scale_byte(PW == 1 ? am : mx_half_max_bits<DT>(h ? am >> 16 : am & 0xffffu));
+      const uint4 q = encode_block<DT, RAND>(u, sb, rnd);
+      reinterpret_cast<uint8_t*>(ctile)[c / 32 * 128 + mx_scale_in_tile(c % 32 + h, b)] = (uint8_t)sb;
+      if (col0 + c + h < a.cols && rt * 4 + b < nblk_c)
+        *reinterpret_cast<uint4*>(a.col_codes + ((col0 + c + h) * nblk_c + rt * 4 + b) * 16) = q;
+    }
   }
   __syncthreads();
   // 128 rows (columns) are four tiles of scales, 128 columns (rows) half a chunk

@@ -55,35 +55,95 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax) {
 // 253 (the largest that a finite block gets).
 __device__ __forceinline__ float mx_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// Eight fp32 values, already times 2^-k (magnitudes at most 6), to eight
-// codes, nearest with ties to the even code: the hardware's conversion.
-__device__ __forceinline__ uint32_t mx_encode8(const float* v) {
-  uint32_t r = 0;
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], 1.0f, 0);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], 1.0f, 1);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[4], v[5], 1.0f, 2);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[6], v[7], 1.0f, 3);
-  return r;
+// Runs of values are handled as the words they are loaded in: one fp32 value
+// or two 16-bit ones to a word.
+template <int DT>
+constexpr int kPerWord = 4 / dtype_bytes(DT);
+
+// Largest magnitude of N words, as the bits of an fp32 value (sign clear).
+// The bit patterns of every type order like the magnitudes, infinities and
+// NaN above all finite values.
+__device__ __forceinline__ uint32_t mx_pk_max(uint32_t a, uint32_t b) {
+  typedef uint16_t v2s __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(v2s, a), __builtin_bit_cast(v2s, b)));
 }
-__device__ __forceinline__ uint32_t mx_encode4(const float* v) {
-  uint32_t r = 0;
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[0], v[1], 1.0f, 0);
-  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, v[2], v[3], 1.0f, 1);
-  return r & 0xffffu;
+template <int DT>
+__device__ __forceinline__ uint32_t mx_max_words(uint32_t m, uint32_t w) {
+  return DT == kF32 ? max(m, w & 0x7fffffffu) : mx_pk_max(m, w & 0x7fff7fffu);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t mx_half_max_bits(uint32_t h) {  // of a 16-bit pattern
+  return DT == kBF16 ? h << 16 : __float_as_uint(Elem<kF16>::up((uint16_t)h));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t mx_max_bits(uint32_t m) {
+  return DT == kF32 ? m : mx_half_max_bits<DT>(max(m & 0xffffu, m >> 16));
 }
 
-// Stochastic rounding of a value already times 2^-k to the format's grid with
-// one random byte: up when the fraction between the two neighbours, times
-// 256, is above r + 0.5.  Every step is exact in fp32 (the grid's steps are
-// powers of two), so the result depends on x and r alone.
-__device__ __forceinline__ float mx_stochastic(float x, uint32_t r) {
-  const float a = fabsf(x);
-  const float step = a < 2.f ? 0.5f : a < 4.f ? 1.f : 2.f;
-  const float inv = a < 2.f ? 2.f : a < 4.f ? 1.f : 0.5f;
-  const float t = a * inv;
-  const float low = floorf(t);
-  const float up = (t - low) * 256.f > (float)r + 0.5f ? 1.f : 0.f;
-  return copysignf((low + up) * step, x);
+// Eight values to eight codes of x * 2^-k, nearest with ties to the even code:
+// the hardware's conversion, which takes 2^k and the values as they are.
+// (Every step is exact but the one rounding; byte 255 gives zero codes.)
+template <int DT>
+__device__ __forceinline__ uint32_t mx_nearest8(const uint32_t* w, uint32_t byte) {
+  typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+  typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+  const float scale = __uint_as_float(byte << 23);
+  uint32_t r = 0;
+  if constexpr (DT == kF32) {
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[0]), __uint_as_float(w[1]), scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[2]), __uint_as_float(w[3]), scale, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[4]), __uint_as_float(w[5]), scale, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(w[6]), __uint_as_float(w[7]), scale, 3);
+  } else if constexpr (DT == kBF16) {
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(v2b, w[0]), scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(v2b, w[1]), scale, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(v2b, w[2]), scale, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(v2b, w[3]), scale, 3);
+  } else {
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(v2h, w[0]), scale, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(v2h, w[1]), scale, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(v2h, w[2]), scale, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(v2h, w[3]), scale, 3);
+  }
+  return byte == 255u ? 0u : r;
+}
+
+// Stochastic rounding of one value to its code with one random byte r: up when
+// the fraction between the two neighbours, times 256, is above r + 0.5.  From
+// magnitude 1 on the code's spacing is bit 22 of an fp32 number (one fraction
+// bit), below it is 1/2: in either case the magnitude, as an integer whose
+// bit 22 counts codes, plus 2^22 - 1 - (r + 0.5) 2^14 carries into bit 22
+// exactly when the fraction is above the threshold.  Below 1 the integer is
+// a * 2^23: exact for 16-bit types (a value above the smallest threshold, 2^13,
+// has its 11 bits or fewer above 1), rounded up for fp32, which keeps "above
+// the threshold".  (All values are doubled here, to shift the sign out.)
+template <int DT>
+__device__ __forceinline__ uint32_t mx_stochastic_code(float x, float inv, uint32_t r) {
+  const float t = x * inv, a = fabsf(t);
+  const uint32_t big = (__float_as_uint(t) << 1) - (0xFCu << 23);
+  const uint32_t small = DT == kF32 ? (uint32_t)ceilf(a * 0x1p23f) << 1 : (uint32_t)(a * 0x1p24f);
+  const uint32_t m = (a < 1.f ? small : big) + (2u * (0x3fffffu - 0x2000u) - (r << 15));
+  return (m >> 23) | (__float_as_uint(x) >> 28 & 8u);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t mx_stochastic8(const uint32_t* w, uint32_t byte, const uint32_t* rnd) {
+  const float inv = byte == 255u ? 0.f : mx_inv_scale(byte);
+  uint32_t q = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = DT == kF32 ? __uint_as_float(w[i]) : Elem<DT>::up((uint16_t)(w[i / 2] >> (i & 1) * 16));
+    q |= mx_stochastic_code<DT>(x, inv, rnd[i / 4] >> (i & 3) * 8 & 255u) << 4 * i;
+  }
+  return byte == 255u ? 0u : q;
+}
+
+// Eight values of DT's words to codes; rnd: their eight random bytes.
+template <int DT, bool RAND>
+__device__ __forceinline__ uint32_t mx_encode8(const uint32_t* w, uint32_t byte, const uint32_t* rnd) {
+  if constexpr (RAND)
+    return mx_stochastic8<DT>(w, byte, rnd);
+  else
+    return mx_nearest8<DT>(w, byte);
 }
 
 // Two values of byte `SEL` of a code word, times 2^(byte - 127).
