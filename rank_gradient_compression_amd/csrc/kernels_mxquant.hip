@@ -144,28 +144,35 @@ template <int DT>
 constexpr int kColSkew = 64 / dtype_bytes(DT);  // shift per 32 rows, elements
 constexpr int kColRandPitch = 132;
 
-// The tile into LDS, and its random bytes.
+// The tile into LDS, and its random bytes: all of a thread's 16-byte loads
+// under way at once, or half of them where a tile on the last columns is read
+// element by element (the addresses would take the registers that keep further
+// workgroups resident).
 template <int DT, bool RAND, bool FULL>
 __device__ __forceinline__ void cols_tile_load(const MxQuantArgs& a, int64_t row0, int64_t col0,
                                                typename Elem<DT>::type* tile, uint8_t* rtile) {
   using T = typename Elem<DT>::type;
   constexpr int E = 4 * kPerWord<DT>, TPR = 128 / E, RPP = 256 / TPR, SWEEPS = 128 / RPP;  // 16 bytes per thread and row
+  constexpr int GROUP = FULL ? SWEEPS : SWEEPS / 2;
   const T* x = static_cast<const T*>(a.x);
   const int c = (int)(threadIdx.x % TPR) * E, r0 = (int)threadIdx.x / TPR;
-  uint32_t v[SWEEPS][4], rnd[SWEEPS][E / 4];
+#pragma unroll 1
+  for (int s0 = 0; s0 < SWEEPS; s0 += GROUP) {
+    uint32_t v[GROUP][4], rnd[GROUP][E / 4];
 #pragma unroll
-  for (int s = 0; s < SWEEPS; ++s) {
-    const int64_t row = min(row0 + s * RPP + r0, a.rows - 1);
-    load_elems<DT, FULL>(x + row * a.ld, col0 + c, a.cols, v[s]);
-    if constexpr (RAND) load_bytes<FULL>(a.rand + row * a.cols, col0 + c, a.cols, rnd[s]);
-  }
+    for (int s = 0; s < GROUP; ++s) {
+      const int64_t row = min(row0 + (s0 + s) * RPP + r0, a.rows - 1);
+      load_elems<DT, FULL>(x + row * a.ld, col0 + c, a.cols, v[s]);
+      if constexpr (RAND) load_bytes<FULL>(a.rand + row * a.cols, col0 + c, a.cols, rnd[s]);
+    }
 #pragma unroll
-  for (int s = 0; s < SWEEPS; ++s) {
-    const int r = s * RPP + r0;
-    uint4 q = make_uint4(v[s][0], v[s][1], v[s][2], v[s][3]);
-    if (row0 + r >= a.rows) q = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(&tile[r * kColPitch<DT> + (r >> 5) * kColSkew<DT> + c]) = q;
-    if constexpr (RAND) __builtin_memcpy(__builtin_assume_aligned(&rtile[r * kColRandPitch + c], 4), rnd[s], E);
+    for (int s = 0; s < GROUP; ++s) {
+      const int r = (s0 + s) * RPP + r0;
+      uint4 q = make_uint4(v[s][0], v[s][1], v[s][2], v[s][3]);
+      if (row0 + r >= a.rows) q = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(&tile[r * kColPitch<DT> + (r >> 5) * kColSkew<DT> + c]) = q;
+      if constexpr (RAND) __builtin_memcpy(__builtin_assume_aligned(&rtile[r * kColRandPitch + c], 4), rnd[s], E);
+    }
   }
 }
 
@@ -187,7 +194,8 @@ __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantArgs a, int nct) {
   __shared__ __align__(16) T tile[128 * P + 4 * SKEW];
   __shared__ __align__(16) uint8_t rtile[RAND ? 128 * RP : 16];
   __shared__ uint32_t stile[ROWS ? 128 : 1], ctile[128];  // four tiles' half chunks
-  const int rt = blockIdx.x / nct, ct = blockIdx.x % nct;
+  // (a tile writes half lines of codes; neighbouring tiles on one XCD fill them up in its L2)
+  const int t0 = xcd_position(blockIdx.x, gridDim.x), rt = t0 / nct, ct = t0 % nct;
   const int64_t row0 = (int64_t)rt * 128, col0 = (int64_t)ct * 128;
   const int64_t nblk_r = mx_blocks(a.cols), nblk_c = mx_blocks(a.rows);
   if (col0 + 128 <= a.cols)
@@ -196,10 +204,11 @@ __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantArgs a, int nct) {
     cols_tile_load<DT, RAND, false>(a, row0, col0, tile, rtile);
   __syncthreads();
   if constexpr (ROWS) {
-    // A thread takes blocks of 32 columns of a row: 512 blocks in the tile.
+    // A thread takes blocks of 32 columns of a row: 512 blocks in the tile, the
+    // four of a row in neighbouring lanes (64 contiguous bytes of codes).
 #pragma unroll 1
     for (int i = threadIdx.x; i < 512; i += 256) {
-      const int r = i % 128, b = i / 128;
+      const int r = i >> 2, b = i & 3;
       const T* src = &tile[r * P + (r >> 5) * SKEW + b * 32];
       uint32_t w[32 / PW], rnd[8], am = 0;
       __builtin_memcpy(w, __builtin_assume_aligned(src, 16), sizeof w);
@@ -221,25 +230,35 @@ __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantArgs a, int nct) {
     const int b = i & 3, c = (i >> 2) * PW;
     const T* src = &tile[b * (32 * P + SKEW) + c];
     uint32_t w[32], am = 0;
+    uint16_t rnd[RAND ? 32 : 1];  // PW random bytes of each row
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       __builtin_memcpy(&w[j], __builtin_assume_aligned(src + j * P, 4), 4);
+      if constexpr (RAND && PW == 1) rnd[j] = rtile[(b * 32 + j) * RP + c];
+      if constexpr (RAND && PW == 2) __builtin_memcpy(&rnd[j], __builtin_assume_aligned(&rtile[(b * 32 + j) * RP + c], 2), 2);
       am = mx_max_words<DT>(am, w[j]);
     }
 #pragma unroll
     for (int h = 0; h < PW; ++h) {  // column c + h
-      uint32_t u[32 / PW], rnd[8];
-#pragma unroll
-      for (int j = 0; j < 32 / PW; ++j)
-        u[j] = PW == 1 ? w[j] : __builtin_amdgcn_perm(w[PW * j + PW - 1], w[PW * j], h ? 0x07060302u : 0x05040100u);
-      if constexpr (RAND) {
-        uint8_t y[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] = rtile[(b * 32 + j) * RP + c + h];
-        __builtin_memcpy(rnd, y, 32);
-      }
       const uint32_t sb = mx_scale_byte(PW == 1 ? am : mx_half_max_bits<DT>(h ? am >> 16 : am & 0xffffu));
-      const uint4 q = encode_block<DT, RAND>(u, sb, rnd);
+      uint4 q;
+      if constexpr (RAND) {
+        const float inv = sb == 255u ? 0.f : mx_inv_scale(sb);
+        uint32_t code[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float v = PW == 1 ? __uint_as_float(w[j]) : Elem<DT>::up((uint16_t)(w[j] >> 16 * h));
+          code[j / 8] |= mx_stochastic_code<DT>(v, inv, (uint32_t)rnd[j] >> 8 * h & 255u) << 4 * (j & 7);
+        }
+        q = sb == 255u ? make_uint4(0, 0, 0, 0) : make_uint4(code[0], code[1], code[2], code[3]);
+      } else {
+        uint32_t u[32 / PW];
+#pragma unroll
+        for (int j = 0; j < 32 / PW; ++j)
+          u[j] = PW == 1 ? w[j] : __builtin_amdgcn_perm(w[PW * j + PW - 1], w[PW * j], h ? 0x07060302u : 0x05040100u);
+        q = make_uint4(mx_nearest8<DT>(u, sb), mx_nearest8<DT>(u + 8 / PW, sb), mx_nearest8<DT>(u + 16 / PW, sb),
+                       mx_nearest8<DT>(u + 24 / PW, sb));
+      }
       reinterpret_cast<uint8_t*>(ctile)[c / 32 * 128 + mx_scale_in_tile(c % 32 + h, b)] = (uint8_t)sb;
       if (col0 + c + h < a.cols && rt * 4 + b < nblk_c)
         *reinterpret_cast<uint4*>(a.col_codes + ((col0 + c + h) * nblk_c + rt * 4 + b) * 16) = q;

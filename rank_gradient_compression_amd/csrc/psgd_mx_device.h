@@ -146,6 +146,14 @@ __device__ __forceinline__ uint32_t mx_encode8(const uint32_t* w, uint32_t byte,
     return mx_nearest8<DT>(w, byte);
 }
 
+// Workgroup b of `total` to a position in the walk over a matrix's tiles:
+// consecutive workgroups go to the eight XCDs in turn, each with an L2 of its
+// own, so XCD x takes the x-th eighth of the walk.
+__device__ __forceinline__ int xcd_position(int b, int total) {
+  const int q = total / 8, rem = total % 8, x = b % 8;
+  return x * q + min(x, rem) + b / 8;
+}
+
 // Two values of byte `SEL` of a code word, times 2^(byte - 127).
 template <int SEL>
 __device__ __forceinline__ float2 mx_decode2(uint32_t codes, int k) {
