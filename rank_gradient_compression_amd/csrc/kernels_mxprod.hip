@@ -70,10 +70,11 @@ __device__ __forceinline__ void store4(void* c, int64_t i, v4f v, int64_t n, boo
   }
 }
 
-// Position t of the walk over the 256 x 256 tiles of large products: groups of
-// 8 tile rows, so that the 32 tiles that an XCD's compute units work on at a
-// time form an 8 x 4 block that shares its operands in L2.
-__device__ __forceinline__ void tile_at(int t, int ntm, int ntn, int* tm, int* tn) {
+// The walk of the large products: groups of 8 tile rows, so that the 32 tiles
+// that an XCD's compute units work on at a time form an 8 x 4 block that
+// shares its operands in L2.
+__device__ __forceinline__ void tile_of_block(int b, int ntm, int ntn, int* tm, int* tn) {
+  const int t = xcd_position(b, ntm * ntn);
   const int first = t / (8 * ntn) * 8, rows = min(8, ntm - first), in = t % (8 * ntn);
   *tm = first + in % rows;
   *tn = in / rows;
@@ -270,7 +271,7 @@ __device__ __forceinline__ float* mx_epilogue_lds(int wave, uint8_t* a0, uint8_t
 }
 
 template <int DT, int WM, int WN, int TM, int TN>
-__global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p, int ntm, int ntn, int first) {
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p, int ntm, int ntn) {
   constexpr int WAVES = WM * WN, BM = WM * 32 * TM, BN = WN * 32 * TN;
   // Groups of products: one tile of 16 rows of A times all of the wavefront's
   // B; a chunk is two steps of HA groups.  A's operands are read DEPTH groups
@@ -280,13 +281,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
       b1[BN * kChunkBytes];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN;
-  // a 256 x 256 tile of the walk from position `first` on, or a part of it
-  constexpr int SM = 256 / BM, SN = 256 / BN;
-  const int at = xcd_position(blockIdx.x, gridDim.x);
   int tm, tn;
-  tile_at(first + at / (SM * SN), ntm, ntn, &tm, &tn);
-  const int64_t m0 = (int64_t)tm * 256 + at % SM * BM, n0 = (int64_t)tn * 256 + at / SM % SN * BN;
-  if (m0 >= p.m || n0 >= p.n) return;
+  tile_of_block(blockIdx.x, ntm, ntn, &tm, &tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const uint32_t nch = (uint32_t)mx_chunks(p.k), pitch = (uint32_t)mx_pitch(p.k);
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(p.a.codes + m0 * pitch), 0, (int)((uint32_t)min((int64_t)BM, p.m - m0) * pitch), 0x00020000);
@@ -699,15 +696,12 @@ __global__ __launch_bounds__(256) void k_mx_prod_zero(MxProductArgs p) {
 
 size_t mx_product_workspace(int64_t, int64_t, int64_t) { return 0; }
 
-// `count` of the 256 x 256 tiles, from position `first` of their walk on, by
-// tiles of WM * TM * 32 x WN * TN * 32.
 template <int DT, int WM, int WN, int TM, int TN>
-static void product_lds(const MxProductArgs& p, int first, int count, hipStream_t s) {
-  constexpr int PARTS = (256 / (WM * TM * 32)) * (256 / (WN * TN * 32));
-  if (count == 0) return;
-  const int ntm = (int)((p.m + 255) / 256), ntn = (int)((p.n + 255) / 256);
-  hipLaunchKernelGGL((k_mx_prod_lds<DT, WM, WN, TM, TN>), dim3((unsigned)(count * PARTS)), dim3(64 * WM * WN), 0, s, p,
-                     ntm, ntn, first);
+static void product_lds(const MxProductArgs& p, hipStream_t s) {
+  constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
+  const int ntm = (int)((p.m + BM - 1) / BM), ntn = (int)((p.n + BN - 1) / BN);
+  hipLaunchKernelGGL((k_mx_prod_lds<DT, WM, WN, TM, TN>), dim3((unsigned)(ntm * ntn)), dim3(64 * WM * WN), 0, s, p, ntm,
+                     ntn);
 }
 
 template <int DT>
@@ -727,22 +721,21 @@ static void product_dt(const MxProductArgs& p, hipStream_t s) {
       product_skinny<true>(ba, s);
     return;
   }
-  // Tiles of 256 x 256, one to each of the 256 compute units at a time: a
-  // larger tile reads its operands fewer times.  A last round that would leave
-  // half of the compute units idle is cut into quarters, two workgroups to a
-  // compute unit (2048 x 11008 x 4096: 344 tiles 64 us, 256 and 88 in quarters
-  // 47; 2048 x 4096 x 11008: 128 tiles 70 us, in quarters 60).  Where even
-  // 64 x 64 tiles are few, such tiles whose wavefronts share the summed axis.
-  // A single chunk is a write of C and hardly a product: small workgroups.
+  // Tiles as large as still occupy more than half of the 256 compute units: a
+  // larger tile reads its operands fewer times, but idle compute units cost
+  // more (2048 x 4096 x 11008: 128 tiles of 256 x 256 70 us, 512 of 128 x 128,
+  // two workgroups to a compute unit, 60; 2048 x 11008 x 4096: 344 of 256 x
+  // 256 64 us, 1376 of 128 x 128 67).  Below, 64 x 64 tiles whose wavefronts
+  // share the summed axis.  A single chunk is a write of C and hardly a
+  // product: small workgroups.
   auto tiles = [&](int64_t b) { return ((p.m + b - 1) / b) * ((p.n + b - 1) / b); };
   if (fits && p.k > 256) {
-    if (tiles(64) <= 256) {
+    if (tiles(64) <= 256)
       skinny<4, 2, false, -1>(ab, s);
-    } else {
-      const int total = (int)tiles(256), rest = total % 256 <= 128 ? total % 256 : 0;
-      product_lds<DT, 2, 4, 4, 2>(p, 0, total - rest, s);
-      product_lds<DT, 2, 2, 2, 2>(p, total - rest, rest, s);
-    }
+    else if (tiles(256) <= 128)
+      product_lds<DT, 2, 2, 2, 2>(p, s);
+    else
+      product_lds<DT, 2, 4, 4, 2>(p, s);
     return;
   }
   const int ntn = (int)((p.n + 63) / 64);
