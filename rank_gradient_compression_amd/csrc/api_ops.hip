@@ -91,7 +91,7 @@ extern "C" psgd_status_t psgd_clip_create(int32_t ntensors, const int64_t* numel
   try {
     c = new psgd_clip;
     c->tensors.resize((size_t)ntensors);
-    int64_t nsums = 0, nchunks = 0, bytes = 0;
+    int64_t nsums = 0, nchunks = 0, bytes_in = 0, bytes_out = 0;
     for (int32_t t = 0; t < ntensors; ++t) {
       const int64_t n = numel[t], chunks = (n + kClipChunk - 1) / kClipChunk;
       // its share of the norm's workgroups, by size
@@ -107,9 +107,11 @@ extern "C" psgd_status_t psgd_clip_create(int32_t ntensors, const int64_t* numel
       c->chunk_map.insert(c->chunk_map.end(), (size_t)chunks, t);
       nsums += groups;
       nchunks += chunks;
-      bytes += n * dtype_bytes(in_dtypes[t]);
+      bytes_in += n * dtype_bytes(in_dtypes[t]);
+      bytes_out += n * dtype_bytes(out_dtypes[t]);
     }
-    c->stream = bytes > kStreamHintBytes;
+    c->stream_in = bytes_in > kStreamHintBytes;
+    c->stream_out = bytes_in + bytes_out > kClipCacheBytes;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     c->lay.sum_map_off = up(c->tensors.size() * sizeof(ClipTensor));
     c->lay.chunk_map_off = c->lay.sum_map_off + up(c->sum_map.size() * sizeof(int32_t));
@@ -219,7 +221,8 @@ static ClipArgs clip_args(const psgd_clip* c, void* ws, float scale, float max_n
   a.ntensors = (int32_t)c->tensors.size();
   a.nsums = (int32_t)c->sum_map.size();
   a.nchunks = (int32_t)c->chunk_map.size();
-  a.stream = c->stream;
+  a.stream_in = c->stream_in;
+  a.stream_out = c->stream_out;
   a.scale = scale;
   a.max_norm = max_norm;
   a.stats = stats;

@@ -143,13 +143,19 @@ __global__ __launch_bounds__(1024) void k_clip_final(ClipArgs a) {
 }
 
 // One chunk, from type IN to type OUT, in groups of 16 bytes of the wider
-// one, so that the loads and the stores of a wavefront are contiguous.
-template <int IN, int OUT, bool NT>
+// one, so that the loads and the stores of a wavefront are contiguous.  Stores
+// are nontemporal where in and out together would not stay in the last level
+// of cache: they leave the gradients there from the norm's pass to this one,
+// and no dirty lines for the next call's norm to push out (fp32, 64 Mi values:
+// 155 -> 128 us, with a reader of the outputs behind it 228 -> 216; 32 Mi: 80
+// -> 68, 110 -> 113; 8 Mi: 21.3 and 21.4, 31.5 and 34, stored as usual).
+// Loads are nontemporal beyond a gibibyte of gradients (300 Mi: 638 -> 600 us).
+template <int IN, int OUT, bool NTL, bool NTS>
 __device__ __forceinline__ void scale_chunk(const ClipTensor& t, int64_t e0, float c) {
   constexpr int E = 16 / (dtype_bytes(IN) > dtype_bytes(OUT) ? dtype_bytes(IN) : dtype_bytes(OUT));
   using T = typename Elem<OUT>::type;
   typedef uint32_t vec __attribute__((ext_vector_type(E * sizeof(T) / 4)));
-  walk<IN, E, NT>(t.in, e0, min(t.numel, e0 + kClipChunk), [&](int64_t i, const float(&x)[E], int n) {
+  walk<IN, E, NTL>(t.in, e0, min(t.numel, e0 + kClipChunk), [&](int64_t i, const float(&x)[E], int n) {
     T* o = static_cast<T*>(t.out) + i;
     T v[E];
 #pragma unroll
@@ -157,7 +163,7 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, int64_t e0, flo
     if (n == E && ((uintptr_t)o & (sizeof(vec) - 1)) == 0) {
       vec q;
       __builtin_memcpy(&q, v, sizeof q);
-      if (NT)
+      if (NTS)
         __builtin_nontemporal_store(q, reinterpret_cast<vec*>(o));
       else
         *reinterpret_cast<vec*>(o) = q;
@@ -171,22 +177,22 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, int64_t e0, flo
 
 // Workgroups run through the chunks from the last to the first: the norm's
 // pass has read the last ones last, and the cache still holds them.
-template <bool NT>
+template <bool NTL, bool NTS>
 __global__ __launch_bounds__(256) void k_clip_apply(ClipArgs a) {
   const int chunk = a.nchunks - 1 - (int)blockIdx.x;
   const ClipTensor t = a.tensors[a.chunk_map[chunk]];
   const int64_t e0 = (int64_t)(chunk - t.first_chunk) * kClipChunk;
   const float c = a.stats[1] * a.scale;
   switch (t.in_dtype * 3 + t.out_dtype) {
-    case kF32 * 3 + kF32: return scale_chunk<kF32, kF32, NT>(t, e0, c);
-    case kF32 * 3 + kBF16: return scale_chunk<kF32, kBF16, NT>(t, e0, c);
-    case kF32 * 3 + kF16: return scale_chunk<kF32, kF16, NT>(t, e0, c);
-    case kBF16 * 3 + kF32: return scale_chunk<kBF16, kF32, NT>(t, e0, c);
-    case kBF16 * 3 + kBF16: return scale_chunk<kBF16, kBF16, NT>(t, e0, c);
-    case kBF16 * 3 + kF16: return scale_chunk<kBF16, kF16, NT>(t, e0, c);
-    case kF16 * 3 + kF32: return scale_chunk<kF16, kF32, NT>(t, e0, c);
-    case kF16 * 3 + kBF16: return scale_chunk<kF16, kBF16, NT>(t, e0, c);
-    default: return scale_chunk<kF16, kF16, NT>(t, e0, c);
+    case kF32 * 3 + kF32: return scale_chunk<kF32, kF32, NTL, NTS>(t, e0, c);
+    case kF32 * 3 + kBF16: return scale_chunk<kF32, kBF16, NTL, NTS>(t, e0, c);
+    case kF32 * 3 + kF16: return scale_chunk<kF32, kF16, NTL, NTS>(t, e0, c);
+    case kBF16 * 3 + kF32: return scale_chunk<kBF16, kF32, NTL, NTS>(t, e0, c);
+    case kBF16 * 3 + kBF16: return scale_chunk<kBF16, kBF16, NTL, NTS>(t, e0, c);
+    case kBF16 * 3 + kF16: return scale_chunk<kBF16, kF16, NTL, NTS>(t, e0, c);
+    case kF16 * 3 + kF32: return scale_chunk<kF16, kF32, NTL, NTS>(t, e0, c);
+    case kF16 * 3 + kBF16: return scale_chunk<kF16, kBF16, NTL, NTS>(t, e0, c);
+    default: return scale_chunk<kF16, kF16, NTL, NTS>(t, e0, c);
   }
 }
 
@@ -197,7 +203,7 @@ hipError_t launch_clip_bind(ClipTensor* tensors, const ClipPointers& p, int firs
 
 hipError_t launch_clip_norm(const ClipArgs& a, hipStream_t s) {
   if (a.nsums > 0) {
-    if (a.stream)
+    if (a.stream_in)
       hipLaunchKernelGGL(k_clip_sums<true>, dim3((unsigned)a.nsums), dim3(256), 0, s, a);
     else
       hipLaunchKernelGGL(k_clip_sums<false>, dim3((unsigned)a.nsums), dim3(256), 0, s, a);
@@ -209,10 +215,13 @@ hipError_t launch_clip_norm(const ClipArgs& a, hipStream_t s) {
 
 hipError_t launch_clip_apply(const ClipArgs& a, hipStream_t s) {
   if (a.nchunks == 0) return hipSuccess;
-  if (a.stream)
-    hipLaunchKernelGGL(k_clip_apply<true>, dim3((unsigned)a.nchunks), dim3(256), 0, s, a);
+  const dim3 g((unsigned)a.nchunks), b(256);
+  if (a.stream_in)
+    hipLaunchKernelGGL((k_clip_apply<true, true>), g, b, 0, s, a);
+  else if (a.stream_out)
+    hipLaunchKernelGGL((k_clip_apply<false, true>), g, b, 0, s, a);
   else
-    hipLaunchKernelGGL(k_clip_apply<false>, dim3((unsigned)a.nchunks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_clip_apply<false, false>), g, b, 0, s, a);
   return hipGetLastError();
 }
 

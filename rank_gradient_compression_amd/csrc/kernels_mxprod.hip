@@ -289,9 +289,14 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
       const_cast<uint8_t*>(p.a.codes + m0 * pitch), 0, (int)((uint32_t)min((int64_t)BM, p.m - m0) * pitch), 0x00020000);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(p.b.codes + n0 * pitch), 0, (int)((uint32_t)min((int64_t)BN, p.n - n0) * pitch), 0x00020000);
-  // (r / 2) % 8 of this lane's row in an even and in an odd group of 8 rows
-  const uint32_t lane_off = (lane >> 3) * pitch + (((lane & 7) ^ (lane >> 4)) << 4);
-  const uint32_t lane_off1 = (lane >> 3) * pitch + (((lane & 7) ^ (4 + (lane >> 4))) << 4);
+  // One of the PA + PB loads of 8 rows of a wavefront's share of a chunk: the
+  // slot of a block is its number ^ (r / 2) % 8, so it depends on whether the
+  // group of 8 rows is an even or an odd one of the tile.
+  constexpr int PA = BM / 8 / WAVES, PB = BN / 8 / WAVES;
+  const int swap_a = PA & wave & 1, swap_b = PB & wave & 1;  // the wavefront's first group is an odd one
+  auto lane_off = [&](int odd) { return (lane >> 3) * pitch + (((lane & 7) ^ (4 * odd + (lane >> 4))) << 4); };
+  const uint32_t lane_a[2] = {lane_off(swap_a), lane_off(1 - swap_a)};
+  const uint32_t lane_b[2] = {lane_off(swap_b), lane_off(1 - swap_b)};
   const int r = lane & 15, g = lane >> 4;
   uint32_t off[2];
 #pragma unroll
@@ -316,17 +321,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
     for (int j = 0; j < HB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   uint32_t sa[TM], sb[TN], ta[TM], tb[TN];
   const int la = wm * TM * 32 * kChunkBytes, lb = wn * TN * 32 * kChunkBytes;
-  // One of the PA + PB loads (8 rows each) of a wavefront's share of a chunk,
-  // and one of its TM + TN scale tiles.  No chunk past the last: an offset
-  // beyond the descriptor reads nothing.
-  constexpr int PA = BM / 8 / WAVES, PB = BN / 8 / WAVES;
+  // One of those loads, and one of the wavefront's TM + TN scale tiles.  No
+  // chunk past the last: an offset beyond the descriptor reads nothing.
   auto load_rows = [&](int j, uint32_t ch, uint8_t* da, uint8_t* db) {
     const bool isa = j < PA;
     const int i = isa ? j : j - PA, row = wave * (isa ? BM / WAVES : BN / WAVES) + i * 8;
     const uint32_t o = ch < nch ? ch * kChunkBytes : 0x80000000u;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         isa ? ra : rb, (__attribute__((address_space(3))) void*)((isa ? da : db) + row * kChunkBytes), 16,
-        (int)((i & 1 ? lane_off1 : lane_off) + (uint32_t)row * pitch + o), 0, 0, 0);
+        (int)((isa ? lane_a : lane_b)[i & 1] + (uint32_t)row * pitch + o), 0, 0, 0);
   };
   auto load_scale = [&](int j, uint32_t ch, uint32_t(&xa)[TM], uint32_t(&xb)[TN]) {
     const uint32_t o = min(ch, nch - 1) * 256;
@@ -734,6 +737,8 @@ static void product_dt(const MxProductArgs& p, hipStream_t s) {
       skinny<4, 2, false, -1>(ab, s);
     else if (tiles(256) <= 128)
       product_lds<DT, 2, 2, 2, 2>(p, s);
+    else if (3 * ((((p.m + 191) / 192) * ((p.n + 255) / 256) + 255) / 256) < 4 * ((tiles(256) + 255) / 256))
+      product_lds<DT, 2, 4, 3, 2>(p, s);
     else
       product_lds<DT, 2, 4, 4, 2>(p, s);
     return;

@@ -14,31 +14,63 @@
 
 namespace psgd {
 
-// N consecutive elements of a row from column `col` on, as words; zero past
-// `cols`.  FULL: all N are inside the row (whatever its alignment: the hardware
-// takes 16-byte accesses at any element's address, and on rows of 650 floats
-// they beat pairs of 8-byte ones).  Else every element is read at a column
-// clamped into the row and masked afterwards: a branch around a load would
-// make the compiler wait for it before it issues the next.
-template <int DT, bool FULL, int N>
+// How a run of elements that may cross the row's end is read.  FULL: all of it
+// is inside the row.  EDGE: the row is at least as long as the run, which is
+// read from an earlier column if need be, inside the row, and shifted down.
+// NARROW: element by element, at columns clamped into the row (a branch around
+// a load would make the compiler wait for it before it issues the next).
+// Whatever the row's alignment: the hardware takes 16-byte accesses at any
+// element's address, and on rows of 650 floats they beat pairs of 8-byte ones.
+enum Reach { FULL, EDGE, NARROW };
+
+// w shifted down by `bytes` (any number up from 0; zeros come in).
+template <int N>
+__device__ __forceinline__ void shift_down(uint32_t (&w)[N], uint32_t bytes) {
+  const uint32_t words = bytes / 4;
+#pragma unroll
+  for (int h = N / 2; h > 0; h /= 2) {
+    const uint32_t on = words & h ? ~0u : 0u;  // (a mask: the choice of an array's element would put it into memory)
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = (i + h < N ? w[i + h < N ? i + h : 0] & on : 0u) | (w[i] & ~on);
+  }
+  const uint32_t any = bytes < 4 * N ? ~0u : 0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    w[i] = __builtin_amdgcn_alignbyte(i + 1 < N ? w[i + 1 < N ? i + 1 : 0] : 0u, w[i], bytes & 3) & any;
+}
+
+// N words of consecutive elements of a row from column `col` on; zero past
+// `cols`.
+template <int DT, Reach R, int N>
 __device__ __forceinline__ void load_elems(const typename Elem<DT>::type* row, int64_t col, int64_t cols,
                                            uint32_t (&w)[N]) {
   using T = typename Elem<DT>::type;
-  if (FULL) {
+  constexpr int E = N * kPerWord<DT>;
+  if (R == FULL) {
     __builtin_memcpy(w, row + col, sizeof w);
+  } else if (R == EDGE) {
+    __builtin_memcpy(w, row + min(col, cols - E), sizeof w);
   } else {
-    T v[N * kPerWord<DT>];
+    T v[E];
 #pragma unroll
-    for (int i = 0; i < N * kPerWord<DT>; ++i) v[i] = row[min(col + i, cols - 1)];
+    for (int i = 0; i < E; ++i) v[i] = row[min(col + i, cols - 1)];
 #pragma unroll
-    for (int i = 0; i < N * kPerWord<DT>; ++i) v[i] = col + i < cols ? v[i] : (T)0;
+    for (int i = 0; i < E; ++i) v[i] = col + i < cols ? v[i] : (T)0;
     __builtin_memcpy(w, v, sizeof w);
   }
 }
 
-template <int DT, bool FULL, int N>
+// What is left to do once the words are there (apart from the loads, so that
+// all loads of a thread are issued first).
+template <int BYTES, Reach R, int N>
+__device__ __forceinline__ void settle(int64_t col, int64_t cols, uint32_t (&w)[N]) {
+  constexpr int E = N * 4 / BYTES;
+  if (R == EDGE) shift_down(w, (uint32_t)max((int64_t)0, col - (cols - E)) * BYTES);
+}
+
+template <int DT, bool WHOLE, int N>
 __device__ __forceinline__ void store_elems(typename Elem<DT>::type* p, int n, const typename Elem<DT>::type (&v)[N]) {
-  if (FULL || n >= N) {
+  if (WHOLE || n >= N) {
     __builtin_memcpy(p, v, sizeof v);
   } else {
 #pragma unroll
@@ -48,10 +80,12 @@ __device__ __forceinline__ void store_elems(typename Elem<DT>::type* p, int n, c
 }
 
 // N words of random bytes of a row, clamped into it as above.
-template <bool FULL, int N>
+template <Reach R, int N>
 __device__ __forceinline__ void load_bytes(const uint8_t* row, int64_t col, int64_t cols, uint32_t (&w)[N]) {
-  if (FULL) {
+  if (R == FULL) {
     __builtin_memcpy(w, row + col, sizeof w);
+  } else if (R == EDGE) {
+    __builtin_memcpy(w, row + min(col, cols - 4 * N), sizeof w);
   } else {
     uint8_t v[4 * N];
 #pragma unroll
@@ -74,7 +108,7 @@ __device__ __forceinline__ uint32_t group_max(uint32_t a) {
 // every thread takes 8 values of a row at a time, so 4 neighbouring lanes share
 // a block and agree on its exponent by lane exchanges; scales are gathered in
 // LDS and leave as one 256-byte tile.
-template <int DT, bool RAND, bool VALUES, bool FULL>
+template <int DT, bool RAND, bool VALUES, Reach R>
 __device__ __forceinline__ void quant_rows_tile(const MxQuantArgs& a, int nch, uint32_t (&tile)[64]) {
   using T = typename Elem<DT>::type;
   constexpr int W = 8 / kPerWord<DT>;  // words of 8 values
@@ -85,25 +119,24 @@ __device__ __forceinline__ void quant_rows_tile(const MxQuantArgs& a, int nch, u
   const int nrows = (int)min((int64_t)32, a.rows - row0);
   const int64_t nblk = mx_blocks(a.cols);
   const T* x = static_cast<const T*>(a.x);
-  uint32_t v[4][W], rnd[4][2];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int64_t row = row0 + min(s * 8 + (int)threadIdx.x / 32, nrows - 1);
-    load_elems<DT, FULL>(x + row * a.ld, col, a.cols, v[s]);
-    if constexpr (RAND) load_bytes<FULL>(a.rand + row * a.cols, col, a.cols, rnd[s]);
-  }
   uint8_t* tb = reinterpret_cast<uint8_t*>(tile);
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
+  auto load = [&](int s, uint32_t(&v)[W], uint32_t(&rnd)[2]) {
+    const int64_t row = row0 + min(s * 8 + (int)threadIdx.x / 32, nrows - 1);
+    load_elems<DT, R>(x + row * a.ld, col, a.cols, v);
+    if constexpr (RAND) load_bytes<R>(a.rand + row * a.cols, col, a.cols, rnd);
+  };
+  auto quantise = [&](int s, uint32_t(&v)[W], uint32_t(&rnd)[2]) {
     const int r = s * 8 + (int)threadIdx.x / 32;
+    settle<sizeof(T), R>(col, a.cols, v);
+    if constexpr (RAND) settle<1, R>(col, a.cols, rnd);
     uint32_t am = 0;
 #pragma unroll
-    for (int i = 0; i < W; ++i) am = mx_max_words<DT>(am, v[s][i]);
+    for (int i = 0; i < W; ++i) am = mx_max_words<DT>(am, v[i]);
     const uint32_t sb = mx_scale_byte(group_max<4>(mx_max_bits<DT>(am)));
-    const uint32_t code = mx_encode8<DT, RAND>(v[s], sb, rnd[s]);
+    const uint32_t code = mx_encode8<DT, RAND>(v, sb, rnd);
     const int blk = (int)(col >> 5);
     if ((threadIdx.x & 3) == 0) tb[mx_scale_in_tile(r, blk & 7)] = (uint8_t)sb;
-    if (r < nrows && (FULL || blk < nblk)) {
+    if (r < nrows && (R == FULL || blk < nblk)) {
       if (a.row_codes) *reinterpret_cast<uint32_t*>(a.row_codes + (row0 + r) * (nblk * 16) + (col >> 1)) = code;
       if constexpr (VALUES) {
         const int k = (int)sb - 127;
@@ -113,9 +146,23 @@ __device__ __forceinline__ void quant_rows_tile(const MxQuantArgs& a, int nch, u
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           o[i] = Elem<DT>::down(sb == 255u ? __uint_as_float(0x7fc00000u) : (i & 1) ? d[i / 2].y : d[i / 2].x);
-        store_elems<DT, FULL>(static_cast<T*>(a.values) + (row0 + r) * a.ldv + col, nvalid, o);
+        store_elems<DT, R == FULL>(static_cast<T*>(a.values) + (row0 + r) * a.ldv + col, nvalid, o);
       }
     }
+  };
+  if constexpr (R == NARROW) {  // (one row at a time: the addresses of all would take the other tiles' registers)
+#pragma unroll 1
+    for (int s = 0; s < 4; ++s) {
+      uint32_t v[W], rnd[2];
+      load(s, v, rnd);
+      quantise(s, v, rnd);
+    }
+  } else {
+    uint32_t v[4][W], rnd[4][2];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) load(s, v[s], rnd[s]);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) quantise(s, v[s], rnd[s]);
   }
   if (!a.row_scales) return;
   __syncthreads();
@@ -127,9 +174,11 @@ template <int DT, bool RAND, bool VALUES>
 __global__ __launch_bounds__(256) void k_mx_quant_rows(MxQuantArgs a, int nch) {
   __shared__ uint32_t tile[64];
   if ((int64_t)(blockIdx.x % nch) * 256 + 256 <= a.cols)
-    quant_rows_tile<DT, RAND, VALUES, true>(a, nch, tile);
+    quant_rows_tile<DT, RAND, VALUES, FULL>(a, nch, tile);
+  else if (a.cols >= 8)
+    quant_rows_tile<DT, RAND, VALUES, EDGE>(a, nch, tile);
   else
-    quant_rows_tile<DT, RAND, VALUES, false>(a, nch, tile);
+    quant_rows_tile<DT, RAND, VALUES, NARROW>(a, nch, tile);
 }
 
 // Column operand (the operand of x^T, blocks along x's rows), with the row
@@ -145,15 +194,15 @@ constexpr int kColSkew = 64 / dtype_bytes(DT);  // shift per 32 rows, elements
 constexpr int kColRandPitch = 132;
 
 // The tile into LDS, and its random bytes: all of a thread's 16-byte loads
-// under way at once, or half of them where a tile on the last columns is read
-// element by element (the addresses would take the registers that keep further
-// workgroups resident).
-template <int DT, bool RAND, bool FULL>
+// under way at once, or a quarter of them where a narrow matrix is read element by
+// element (the addresses would take the registers that keep further workgroups
+// resident).
+template <int DT, bool RAND, Reach R>
 __device__ __forceinline__ void cols_tile_load(const MxQuantArgs& a, int64_t row0, int64_t col0,
                                                typename Elem<DT>::type* tile, uint8_t* rtile) {
   using T = typename Elem<DT>::type;
   constexpr int E = 4 * kPerWord<DT>, TPR = 128 / E, RPP = 256 / TPR, SWEEPS = 128 / RPP;  // 16 bytes per thread and row
-  constexpr int GROUP = FULL ? SWEEPS : SWEEPS / 2;
+  constexpr int GROUP = R == NARROW ? SWEEPS / 4 : SWEEPS;
   const T* x = static_cast<const T*>(a.x);
   const int c = (int)(threadIdx.x % TPR) * E, r0 = (int)threadIdx.x / TPR;
 #pragma unroll 1
@@ -162,12 +211,14 @@ __device__ __forceinline__ void cols_tile_load(const MxQuantArgs& a, int64_t row
 #pragma unroll
     for (int s = 0; s < GROUP; ++s) {
       const int64_t row = min(row0 + (s0 + s) * RPP + r0, a.rows - 1);
-      load_elems<DT, FULL>(x + row * a.ld, col0 + c, a.cols, v[s]);
-      if constexpr (RAND) load_bytes<FULL>(a.rand + row * a.cols, col0 + c, a.cols, rnd[s]);
+      load_elems<DT, R>(x + row * a.ld, col0 + c, a.cols, v[s]);
+      if constexpr (RAND) load_bytes<R>(a.rand + row * a.cols, col0 + c, a.cols, rnd[s]);
     }
 #pragma unroll
     for (int s = 0; s < GROUP; ++s) {
       const int r = (s0 + s) * RPP + r0;
+      settle<sizeof(T), R>(col0 + c, a.cols, v[s]);
+      if constexpr (RAND) settle<1, R>(col0 + c, a.cols, rnd[s]);
       uint4 q = make_uint4(v[s][0], v[s][1], v[s][2], v[s][3]);
       if (row0 + r >= a.rows) q = make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4*>(&tile[r * kColPitch<DT> + (r >> 5) * kColSkew<DT> + c]) = q;
@@ -199,9 +250,11 @@ __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantArgs a, int nct) {
   const int64_t row0 = (int64_t)rt * 128, col0 = (int64_t)ct * 128;
   const int64_t nblk_r = mx_blocks(a.cols), nblk_c = mx_blocks(a.rows);
   if (col0 + 128 <= a.cols)
-    cols_tile_load<DT, RAND, true>(a, row0, col0, tile, rtile);
+    cols_tile_load<DT, RAND, FULL>(a, row0, col0, tile, rtile);
+  else if (a.cols >= 8)
+    cols_tile_load<DT, RAND, EDGE>(a, row0, col0, tile, rtile);
   else
-    cols_tile_load<DT, RAND, false>(a, row0, col0, tile, rtile);
+    cols_tile_load<DT, RAND, NARROW>(a, row0, col0, tile, rtile);
   __syncthreads();
   if constexpr (ROWS) {
     // A thread takes blocks of 32 columns of a row: 512 blocks in the tile, the

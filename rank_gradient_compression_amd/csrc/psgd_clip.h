@@ -17,6 +17,10 @@ constexpr int kClipChunk = 8192;
 // at most): eight on each compute unit, twice.
 constexpr int kClipSumGroups = 4096;
 
+// Gradients and outputs of more bytes than this do not stay side by side in the
+// 256 MB last level of cache.
+constexpr int64_t kClipCacheBytes = int64_t(192) << 20;
+
 struct ClipTensor {
   const void* in;
   void* out;
@@ -43,7 +47,7 @@ struct ClipArgs {
   const int32_t *sum_map, *chunk_map;
   double* sums;
   int32_t ntensors, nsums, nchunks;
-  bool stream;  // more bytes than the caches keep: streaming accesses
+  bool stream_in, stream_out;  // more bytes than the caches keep: streaming loads, streaming stores
   float scale, max_norm;
   float* stats;
 };
@@ -59,5 +63,5 @@ struct psgd_clip {
   std::vector<int32_t> sum_map, chunk_map;
   std::vector<uint8_t> tables;  // tensors and maps, as uploaded
   psgd::ClipLayout lay{};
-  bool stream = false;
+  bool stream_in = false, stream_out = false;  // stream_in implies stream_out
 };
