@@ -349,12 +349,14 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
   // The barrier stands DEPTH groups before the chunk's end: their operands are
   // in registers, so their products cover it and the first reads of the next
   // chunk, and behind it every wavefront is done with this chunk's stage.
-  // The next chunk's loads are issued two to a group of a 128 x 128 tile, one
-  // to a group of a 256 x 256 tile: all at once they hold up the products
-  // behind them (8192^3: 288 us against 281).
+  // From there on the loads of the chunk after the next go into that stage,
+  // two to a group of a 128 x 128 tile, one to a group of the larger ones, so
+  // that the last of them has three quarters of a chunk to arrive (2048 x 4096
+  // x 11008: 55 us with the loads in the next chunk's first groups, 52 so);
+  // all at once they hold up the products behind them.
   constexpr int PER_GROUP = (PA + PB) * 2 / GROUPS;
-  static_assert((PA + PB) <= PER_GROUP * (GROUPS - DEPTH) && TM + TN <= GROUPS - DEPTH, "loads behind the barrier");
-  auto chunk = [&](uint32_t next, const uint8_t* ca, const uint8_t* cb, uint8_t* na, uint8_t* nb,
+  static_assert(PA + PB <= PER_GROUP * GROUPS && TM + TN <= GROUPS - DEPTH, "loads between two barriers");
+  auto chunk = [&](uint32_t next, uint8_t* ca, uint8_t* cb, uint8_t* na, uint8_t* nb,
                    const uint32_t(&xa)[TM], const uint32_t(&xb)[TN], uint32_t(&ya)[TM], uint32_t(&yb)[TN]) {
     uint4 a[GROUPS + DEPTH], b[3][HB];
 #pragma unroll
@@ -369,9 +371,11 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
       }
+      const bool behind = q >= GROUPS - DEPTH;
+      const int load = (behind ? q - (GROUPS - DEPTH) : q + DEPTH) * PER_GROUP;
 #pragma unroll
-      for (int j = 0; j < PER_GROUP; ++j)
-        if (q * PER_GROUP + j < PA + PB) load_rows(q * PER_GROUP + j, next, na, nb);
+      for (int j = load; j < load + PER_GROUP; ++j)
+        if (j < PA + PB) load_rows(j, behind ? next + 1 : next, behind ? ca : na, behind ? cb : nb);
       if (q < TM + TN) load_scale(q, next, ya, yb);
       // B's next operands first: the first groups of step 0 read step 1's, the
       // first groups behind the barrier the next chunk's
@@ -403,6 +407,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
   for (int j = 0; j < PA + PB; ++j) load_rows(j, 0, a0, b0);
   __syncthreads();
 #pragma unroll
+  for (int j = 0; j < min(PA + PB, DEPTH * PER_GROUP); ++j) load_rows(j, 1, a1, b1);
+#pragma unroll
   for (int d = 0; d < DEPTH; ++d) qa[d] = read_a(a0, d);
 #pragma unroll
   for (int j = 0; j < HB; ++j) qb[j] = read_b(b0, 0, j);
@@ -411,7 +417,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
     chunk(ch + 1, a0, b0, a1, b1, sa, sb, ta, tb);
     chunk(ch + 2, a1, b1, a0, b0, ta, tb, sa, sb);
   }
-  // (every wavefront is behind its last barrier: the stages are free)
+  __syncthreads();  // (the last loads, of no chunk, write zeros into a stage)
   constexpr int RE = mx_epilogue_rows<WAVES, TN, sizeof a0, sizeof b0>();
   float* ep = mx_epilogue_lds<WAVES, TN, sizeof a0, sizeof b0>(wave, a0, b0, a1, b1);
   if (p.accumulate)
