@@ -528,12 +528,22 @@ psgd_status_t psgd_clip_apply(psgd_clip_t clip, float max_norm, float scale, flo
  * psgd_mx_product -- C = A B^T (accumulate: C += A B^T) for A m x k and B n x k
  * operands: summed over k in fp32 (E2M1 products are exact) in an order that
  * depends on the sizes alone, rounded once to C's type.  k = 0 gives zeros.
- * workspace: psgd_mx_product_workspace bytes (may be 0, then NULL is allowed),
- * 256-byte aligned, scratch.
  *
  * psgd_mx_linear -- y = Q(x) W^T: psgd_mx_quantize (nearest) of x's rows into
  * the workspace, then the product with the n x k operand W.  For a layer whose
  * weights were quantised once: serving, also of single tokens (m = 1).
+ * workspace: psgd_mx_linear_workspace bytes (0 for few activations; then NULL
+ * is allowed), 256-byte aligned, scratch.
+ *
+ * psgd_mx_train_forward / psgd_mx_train_backward -- a layer whose weights are
+ * quantised in every step: y = Q(x) Q(w)^T for x m x k and w n x k, which also
+ * writes the operands of x^T (k x m) and w^T (k x n) that the backward pass
+ * takes; then dx = Q(dy) Q(w^T)^T (m x k) and dw = Q(dy^T) Q(x^T)^T (n x k;
+ * accumulate: added to dw), each with dy quantised along the axis it sums
+ * over, from one reading of dy; rand as above, for dy.  dx or dw may be NULL
+ * where that gradient is not wanted.  The same bytes as the single calls in
+ * turn, with fewer launches.  workspace: psgd_mx_train_workspace bytes for
+ * either call, 256-byte aligned, scratch.
  *
  * Sizes are 0 .. INT32_MAX.  Errors: PSGD_ERR_INVALID_ARG (sizes, strides, an
  * unknown type, NULL or misaligned buffers, overlapping buffers);
@@ -545,14 +555,23 @@ psgd_status_t psgd_mx_quantize(const void* x, int32_t dtype, int64_t rows, int64
                                uint8_t* col_scales, void* values, int64_t ldv, hipStream_t stream);
 psgd_status_t psgd_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
                                  int32_t dtype, int64_t ld, hipStream_t stream);
-psgd_status_t psgd_mx_product_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
 psgd_status_t psgd_mx_product(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes, const uint8_t* a_scales,
                               const uint8_t* b_codes, const uint8_t* b_scales, void* c, int32_t dtype, int64_t ldc,
-                              int32_t accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
+                              int32_t accumulate, hipStream_t stream);
 psgd_status_t psgd_mx_linear_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
 psgd_status_t psgd_mx_linear(int64_t m, int64_t n, int64_t k, const void* x, int32_t x_dtype, int64_t ldx,
                              const uint8_t* w_codes, const uint8_t* w_scales, void* y, int32_t y_dtype, int64_t ldy,
                              void* workspace, size_t workspace_bytes, hipStream_t stream);
+psgd_status_t psgd_mx_train_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
+psgd_status_t psgd_mx_train_forward(int64_t m, int64_t n, int64_t k, const void* x, int32_t x_dtype, int64_t ldx,
+                                    const void* w, int32_t w_dtype, int64_t ldw, uint8_t* xt_codes, uint8_t* xt_scales,
+                                    uint8_t* wt_codes, uint8_t* wt_scales, void* y, int32_t y_dtype, int64_t ldy,
+                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void* dy, int32_t dy_dtype, int64_t lddy,
+                                     const uint8_t* rand, const uint8_t* xt_codes, const uint8_t* xt_scales,
+                                     const uint8_t* wt_codes, const uint8_t* wt_scales, void* dx, int32_t dx_dtype,
+                                     int64_t lddx, void* dw, int32_t dw_dtype, int64_t lddw, int32_t accumulate,
+                                     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
  * Per-stage timing with HIP events recorded on the call's stream.  While

@@ -13,8 +13,8 @@ from .binding import (PSGD_FLAG_GRADS_BF16, PSGD_FLAG_MOMENTUM, PSGD_KIND_COMPRE
                       psgd_plan_destroy, psgd_plan_get_info, psgd_plan_tensor, psgd_refresh, psgd_stream_copy,
                       psgd_clip_apply, psgd_clip_bind, psgd_clip_create, psgd_clip_destroy, psgd_clip_norm,
                       psgd_clip_workspace, psgd_clip_workspace_init, psgd_mx_dequantize, psgd_mx_linear,
-                      psgd_mx_linear_workspace, psgd_mx_product, psgd_mx_product_workspace, psgd_mx_quantize,
-                      psgd_mx_sizes, PSGD_DTYPE_BF16, PSGD_DTYPE_F16, PSGD_DTYPE_F32,
+                      psgd_mx_linear_workspace, psgd_mx_product, psgd_mx_quantize, psgd_mx_sizes,
+                      psgd_mx_train_backward, psgd_mx_train_forward, psgd_mx_train_workspace, PSGD_DTYPE_BF16, PSGD_DTYPE_F16, PSGD_DTYPE_F32,
                       psgd_step_stats, psgd_stream_probe, psgd_subspace_overlap,
                       psgd_timing_enable, psgd_timing_read, psgd_timing_stages, psgd_version, psgd_workspace_init,
                       step_opts)

@@ -58,8 +58,8 @@ EXPORTED = [
     "psgd_step_stats", "psgd_subspace_overlap",
     "psgd_clip_create", "psgd_clip_destroy", "psgd_clip_workspace", "psgd_clip_workspace_init", "psgd_clip_bind",
     "psgd_clip_norm", "psgd_clip_apply",
-    "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize", "psgd_mx_product_workspace", "psgd_mx_product",
-    "psgd_mx_linear_workspace", "psgd_mx_linear",
+    "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize", "psgd_mx_product", "psgd_mx_linear_workspace",
+    "psgd_mx_linear", "psgd_mx_train_workspace", "psgd_mx_train_forward", "psgd_mx_train_backward",
     "psgd_timing_enable", "psgd_timing_stages", "psgd_timing_read", "psgd_stream_probe", "psgd_stream_copy", "psgd_last_error",
     "psgd_version",
 ]
@@ -162,10 +162,14 @@ lib.psgd_clip_apply.argtypes = lib.psgd_clip_norm.argtypes
 lib.psgd_mx_sizes.argtypes = [_i64, _i64, _szp, _szp]
 lib.psgd_mx_quantize.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
 lib.psgd_mx_dequantize.argtypes = [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]
-lib.psgd_mx_product_workspace.argtypes = [_i64, _i64, _i64, _szp]
-lib.psgd_mx_product.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _vp, _sz, _vp]
+lib.psgd_mx_product.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _vp]
 lib.psgd_mx_linear_workspace.argtypes = [_i64, _i64, _i64, _szp]
 lib.psgd_mx_linear.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _i64, _vp, _sz, _vp]
+lib.psgd_mx_train_workspace.argtypes = [_i64, _i64, _i64, _szp]
+lib.psgd_mx_train_forward.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i32,
+                                      _i64, _vp, _sz, _vp]
+lib.psgd_mx_train_backward.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp,
+                                       _i32, _i64, _i32, _vp, _sz, _vp]
 lib.psgd_last_error.restype = ctypes.c_char_p
 lib.psgd_version.restype = ctypes.c_char_p
 for _f in ["psgd_plan_create", "psgd_plan_get_info", "psgd_plan_tensor", "psgd_workspace_init", "psgd_compress",
@@ -174,8 +178,9 @@ for _f in ["psgd_plan_create", "psgd_plan_get_info", "psgd_plan_tensor", "psgd_w
            "psgd_stream_copy",
            "psgd_stream_probe", "psgd_step_stats", "psgd_subspace_overlap",
            "psgd_clip_create", "psgd_clip_workspace", "psgd_clip_workspace_init", "psgd_clip_bind", "psgd_clip_norm",
-           "psgd_clip_apply", "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize", "psgd_mx_product_workspace",
-           "psgd_mx_product", "psgd_mx_linear_workspace", "psgd_mx_linear"]:
+           "psgd_clip_apply", "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize",
+           "psgd_mx_product", "psgd_mx_linear_workspace", "psgd_mx_linear", "psgd_mx_train_workspace",
+           "psgd_mx_train_forward", "psgd_mx_train_backward"]:
     getattr(lib, _f).restype = ctypes.c_int
 
 
@@ -348,17 +353,10 @@ def psgd_mx_dequantize(codes: int, scales: int, rows: int, cols: int, out: int, 
                                                         ld, stream))
 
 
-def psgd_mx_product_workspace(m: int, n: int, k: int) -> int:
-    b = _sz()
-    _check("psgd_mx_product_workspace", lib.psgd_mx_product_workspace(m, n, k, ctypes.byref(b)))
-    return b.value
-
-
 def psgd_mx_product(m: int, n: int, k: int, a_codes: int, a_scales: int, b_codes: int, b_scales: int, c: int,
-                    dtype: int, ldc: int, accumulate: bool, workspace: int, workspace_bytes: int,
-                    stream: int = 0) -> None:
+                    dtype: int, ldc: int, accumulate: bool, stream: int = 0) -> None:
     st = lib.psgd_mx_product(m, n, k, a_codes, a_scales, b_codes, b_scales, c, dtype, ldc, 1 if accumulate else 0,
-                             workspace, workspace_bytes, stream)
+                             stream)
     if st:
         _check("psgd_mx_product", st)
 
@@ -375,6 +373,33 @@ def psgd_mx_linear(m: int, n: int, k: int, x: int, x_dtype: int, ldx: int, w_cod
                             stream)
     if st:
         _check("psgd_mx_linear", st)
+
+
+def psgd_mx_train_workspace(m: int, n: int, k: int) -> int:
+    b = _sz()
+    _check("psgd_mx_train_workspace", lib.psgd_mx_train_workspace(m, n, k, ctypes.byref(b)))
+    return b.value
+
+
+def psgd_mx_train_forward(m: int, n: int, k: int, x: int, x_dtype: int, ldx: int, w: int, w_dtype: int, ldw: int,
+                          xt_codes: int, xt_scales: int, wt_codes: int, wt_scales: int, y: int, y_dtype: int, ldy: int,
+                          workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    st = lib.psgd_mx_train_forward(m, n, k, x, x_dtype, ldx, w, w_dtype, ldw, xt_codes, xt_scales, wt_codes, wt_scales,
+                                   y, y_dtype, ldy, workspace, workspace_bytes, stream)
+    if st:
+        _check("psgd_mx_train_forward", st)
+
+
+def psgd_mx_train_backward(m: int, n: int, k: int, dy: int, dy_dtype: int, lddy: int, rand: int, xt_codes: int,
+                           xt_scales: int, wt_codes: int, wt_scales: int, dx: int, dx_dtype: int, lddx: int, dw: int,
+                           dw_dtype: int, lddw: int, accumulate: bool, workspace: int, workspace_bytes: int,
+                           stream: int = 0) -> None:
+    """dx or dw 0: not wanted."""
+    st = lib.psgd_mx_train_backward(m, n, k, dy, dy_dtype, lddy, rand, xt_codes, xt_scales, wt_codes, wt_scales, dx,
+                                    dx_dtype, lddx, dw, dw_dtype, lddw, 1 if accumulate else 0, workspace,
+                                    workspace_bytes, stream)
+    if st:
+        _check("psgd_mx_train_backward", st)
 
 
 def psgd_timing_enable(plan: int, enable: bool) -> None:

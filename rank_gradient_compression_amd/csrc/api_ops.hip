@@ -333,7 +333,7 @@ static psgd_status_t check_product(const char* fn, int64_t m, int64_t n, int64_t
   return PSGD_OK;
 }
 
-static psgd_status_t check_product_ws(const char* fn, size_t need, const void* ws, size_t bytes) {
+static psgd_status_t check_workspace(const char* fn, size_t need, const void* ws, size_t bytes) {
   if (need == 0) return PSGD_OK;
   if (!ws || misaligned(ws, 256) || bytes < need) {
     set_error("%s: the workspace must be %zu bytes, 256-byte aligned", fn, need);
@@ -342,18 +342,10 @@ static psgd_status_t check_product_ws(const char* fn, size_t need, const void* w
   return PSGD_OK;
 }
 
-extern "C" psgd_status_t psgd_mx_product_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes) {
-  clear_error();
-  if (bad_dim(m) || bad_dim(n) || bad_dim(k) || !bytes)
-    return invalid("psgd_mx_product_workspace", "a size is negative or above INT32_MAX, or bytes is NULL");
-  *bytes = mx_product_workspace(m, n, k);
-  return PSGD_OK;
-}
-
 extern "C" psgd_status_t psgd_mx_product(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes,
                                          const uint8_t* a_scales, const uint8_t* b_codes, const uint8_t* b_scales,
-                                         void* c, int32_t dtype, int64_t ldc, int32_t accumulate, void* ws,
-                                         size_t bytes, hipStream_t stream) {
+                                         void* c, int32_t dtype, int64_t ldc, int32_t accumulate,
+                                         hipStream_t stream) {
   clear_error();
   const char* fn = "psgd_mx_product";
   if (psgd_status_t s = check_product(fn, m, n, k, b_codes, b_scales, c, dtype, ldc)) return s;
@@ -362,22 +354,38 @@ extern "C" psgd_status_t psgd_mx_product(int64_t m, int64_t n, int64_t k, const 
   const size_t cb = strided_bytes(m, n, ldc, dtype);
   if (overlap(c, cb, a_codes, (size_t)(m * mx_pitch(k))) || overlap(c, cb, a_scales, (size_t)mx_scale_bytes(m, k)))
     return invalid(fn, "the result overlaps an operand");
-  if (psgd_status_t s = check_product_ws(fn, mx_product_workspace(m, n, k), ws, bytes)) return s;
   const MxProductArgs p{m, n, k, {a_codes, a_scales}, {b_codes, b_scales}, c, dtype, m > 1 ? ldc : n, accumulate != 0};
-  return launch_status(launch_mx_product(p, ws, stream), fn);
+  return launch_status(launch_mx_product(p, stream), fn);
 }
 
-// Workspace of the linear layer: the activations' operand, then the product's.
+// Operands in a workspace: codes, then scales, each from a multiple of 256 bytes on.
 static size_t up256(size_t b) { return (b + 255) / 256 * 256; }
-static size_t linear_operand_bytes(int64_t m, int64_t k) {
-  return up256((size_t)(m * mx_pitch(k))) + up256((size_t)mx_scale_bytes(m, k));
+static size_t operand_bytes(int64_t rows, int64_t cols) {
+  return up256((size_t)(rows * mx_pitch(cols))) + up256((size_t)mx_scale_bytes(rows, cols));
+}
+struct WsOperand {
+  uint8_t *codes, *scales;
+};
+static WsOperand ws_operand(void* ws, size_t off, int64_t rows, int64_t cols) {
+  uint8_t* codes = static_cast<uint8_t*>(ws) + off;
+  return {codes, codes + up256((size_t)(rows * mx_pitch(cols)))};
+}
+
+static MxQuantArgs quant_args(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld) {
+  MxQuantArgs a{};
+  a.x = x;
+  a.dtype = dtype;
+  a.rows = rows;
+  a.cols = cols;
+  a.ld = rows > 1 ? ld : cols;
+  return a;
 }
 
 extern "C" psgd_status_t psgd_mx_linear_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   clear_error();
   if (bad_dim(m) || bad_dim(n) || bad_dim(k) || !bytes)
     return invalid("psgd_mx_linear_workspace", "a size is negative or above INT32_MAX, or bytes is NULL");
-  *bytes = mx_linear_fuses(m, k) ? 0 : linear_operand_bytes(m, k) + mx_product_workspace(m, n, k);
+  *bytes = mx_linear_fuses(m, k) ? 0 : operand_bytes(m, k);
   return PSGD_OK;
 }
 
@@ -390,25 +398,128 @@ extern "C" psgd_status_t psgd_mx_linear(int64_t m, int64_t n, int64_t k, const v
   if (psgd_status_t s = check_strided(fn, x, x_dtype, m, k, ldx)) return s;
   if (overlap(x, strided_bytes(m, k, ldx, x_dtype), y, strided_bytes(m, n, ldy, y_dtype)))
     return invalid(fn, "y overlaps x");
+  MxProductArgs p{m, n, k, {nullptr, nullptr}, {w_codes, w_scales}, y, y_dtype, m > 1 ? ldy : n, false};
   if (mx_linear_fuses(m, k)) {
     if (m == 0 || n == 0) return PSGD_OK;
-    const MxProductArgs p{m, n, k, {nullptr, nullptr}, {w_codes, w_scales}, y, y_dtype, m > 1 ? ldy : n, false};
     return launch_status(launch_mx_linear_fused(p, x, x_dtype, m > 1 ? ldx : k, stream), fn);
   }
-  const size_t op = linear_operand_bytes(m, k);
-  if (psgd_status_t s = check_product_ws(fn, op + mx_product_workspace(m, n, k), ws, bytes)) return s;
+  if (psgd_status_t s = check_workspace(fn, operand_bytes(m, k), ws, bytes)) return s;
   if (m == 0 || n == 0) return PSGD_OK;
-  uint8_t* codes = static_cast<uint8_t*>(ws);
-  uint8_t* scales = codes + up256((size_t)(m * mx_pitch(k)));
-  MxQuantArgs a{};
-  a.x = x;
-  a.dtype = x_dtype;
-  a.rows = m;
-  a.cols = k;
-  a.ld = m > 1 ? ldx : k;
-  a.row_codes = codes;
-  a.row_scales = scales;
+  const WsOperand q = ws_operand(ws, 0, m, k);
+  MxQuantArgs a = quant_args(x, x_dtype, m, k, ldx);
+  a.row_codes = q.codes;
+  a.row_scales = q.scales;
   if (psgd_status_t s = launch_status(launch_mx_quantize(a, stream), fn)) return s;
-  const MxProductArgs p{m, n, k, {codes, scales}, {w_codes, w_scales}, y, y_dtype, m > 1 ? ldy : n, false};
-  return launch_status(launch_mx_product(p, codes ? codes + op : nullptr, stream), fn);
+  p.a = {q.codes, q.scales};
+  return launch_status(launch_mx_product(p, stream), fn);
+}
+
+// -------------------------------------------------- the layer's training pass
+extern "C" psgd_status_t psgd_mx_train_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+  clear_error();
+  if (bad_dim(m) || bad_dim(n) || bad_dim(k) || !bytes)
+    return invalid("psgd_mx_train_workspace", "a size is negative or above INT32_MAX, or bytes is NULL");
+  *bytes = std::max(operand_bytes(m, k) + operand_bytes(n, k), operand_bytes(m, n) + operand_bytes(n, m));
+  return PSGD_OK;
+}
+
+namespace {
+struct Range {
+  const void* p;
+  size_t n;
+};
+Range codes_of(const uint8_t* codes, int64_t rows, int64_t cols) { return {codes, (size_t)(rows * mx_pitch(cols))}; }
+Range scales_of(const uint8_t* scales, int64_t rows, int64_t cols) {
+  return {scales, (size_t)mx_scale_bytes(rows, cols)};
+}
+// One of the first `nout` ranges shares a byte with another range.
+template <int N>
+bool outputs_overlap(const Range (&r)[N], int nout) {
+  for (int i = 0; i < nout; ++i)
+    for (int j = 0; j < N; ++j)
+      if (i != j && r[i].p && r[j].p && overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
+  return false;
+}
+}  // namespace
+
+// Sizes whose tiles a launch can count, whichever of the three axes it spans.
+static psgd_status_t check_train(const char* fn, int64_t m, int64_t n, int64_t k, const uint8_t* xt_codes,
+                                 const uint8_t* xt_scales, const uint8_t* wt_codes, const uint8_t* wt_scales,
+                                 const void* ws, size_t bytes) {
+  if (bad_dim(m) || bad_dim(n) || bad_dim(k)) return invalid(fn, "a size is negative or above INT32_MAX");
+  const int64_t sizes[3][2] = {{m, k}, {n, k}, {m, n}};
+  for (const auto& s : sizes)
+    if (((s[0] + 127) / 32) * ((s[1] + 127) / 32) > kMaxGrid / 4 || s[0] * s[1] / 256 > kMaxGrid / 2)
+      return invalid(fn, "the layer is too large");
+  if (m && k)
+    if (psgd_status_t s = check_operand(fn, xt_codes, xt_scales, k, m)) return s;
+  if (n && k)
+    if (psgd_status_t s = check_operand(fn, wt_codes, wt_scales, k, n)) return s;
+  size_t need;
+  psgd_mx_train_workspace(m, n, k, &need);
+  return check_workspace(fn, need, ws, bytes);
+}
+
+extern "C" psgd_status_t psgd_mx_train_forward(int64_t m, int64_t n, int64_t k, const void* x, int32_t x_dtype,
+                                               int64_t ldx, const void* w, int32_t w_dtype, int64_t ldw,
+                                               uint8_t* xt_codes, uint8_t* xt_scales, uint8_t* wt_codes,
+                                               uint8_t* wt_scales, void* y, int32_t y_dtype, int64_t ldy, void* ws,
+                                               size_t bytes, hipStream_t stream) {
+  clear_error();
+  const char* fn = "psgd_mx_train_forward";
+  if (psgd_status_t s = check_train(fn, m, n, k, xt_codes, xt_scales, wt_codes, wt_scales, ws, bytes)) return s;
+  if (psgd_status_t s = check_strided(fn, x, x_dtype, m, k, ldx)) return s;
+  if (psgd_status_t s = check_strided(fn, w, w_dtype, n, k, ldw)) return s;
+  if (psgd_status_t s = check_strided(fn, y, y_dtype, m, n, ldy)) return s;
+  const Range r[] = {{y, strided_bytes(m, n, ldy, y_dtype)}, codes_of(xt_codes, k, m), scales_of(xt_scales, k, m),
+                     codes_of(wt_codes, k, n),               scales_of(wt_scales, k, n), {ws, bytes},
+                     {x, strided_bytes(m, k, ldx, x_dtype)}, {w, strided_bytes(n, k, ldw, w_dtype)}};
+  if (outputs_overlap(r, 6)) return invalid(fn, "an output or the workspace overlaps another buffer");
+  const WsOperand xr = ws_operand(ws, 0, m, k), wr = ws_operand(ws, operand_bytes(m, k), n, k);
+  MxQuantArgs a = quant_args(x, x_dtype, m, k, ldx), b = quant_args(w, w_dtype, n, k, ldw);
+  a.row_codes = xr.codes, a.row_scales = xr.scales, a.col_codes = xt_codes, a.col_scales = xt_scales;
+  b.row_codes = wr.codes, b.row_scales = wr.scales, b.col_codes = wt_codes, b.col_scales = wt_scales;
+  if (psgd_status_t s = launch_status(launch_mx_quantize_pair(a, b, stream), fn)) return s;
+  const MxProductArgs p{m, n, k, {xr.codes, xr.scales}, {wr.codes, wr.scales}, y, y_dtype, m > 1 ? ldy : n, false};
+  return launch_status(launch_mx_product(p, stream), fn);
+}
+
+extern "C" psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void* dy, int32_t dy_dtype,
+                                                int64_t lddy, const uint8_t* rand, const uint8_t* xt_codes,
+                                                const uint8_t* xt_scales, const uint8_t* wt_codes,
+                                                const uint8_t* wt_scales, void* dx, int32_t dx_dtype, int64_t lddx,
+                                                void* dw, int32_t dw_dtype, int64_t lddw, int32_t accumulate, void* ws,
+                                                size_t bytes, hipStream_t stream) {
+  clear_error();
+  const char* fn = "psgd_mx_train_backward";
+  if (psgd_status_t s = check_train(fn, m, n, k, xt_codes, xt_scales, wt_codes, wt_scales, ws, bytes)) return s;
+  if (psgd_status_t s = check_strided(fn, dy, dy_dtype, m, n, lddy)) return s;
+  if (dx)
+    if (psgd_status_t s = check_strided(fn, dx, dx_dtype, m, k, lddx)) return s;
+  if (dw)
+    if (psgd_status_t s = check_strided(fn, dw, dw_dtype, n, k, lddw)) return s;
+  const Range r[] = {{dx, strided_bytes(m, k, lddx, dx_dtype)},
+                     {dw, strided_bytes(n, k, lddw, dw_dtype)},
+                     {ws, bytes},
+                     {dy, strided_bytes(m, n, lddy, dy_dtype)},
+                     {rand, (size_t)(m * n)},
+                     codes_of(xt_codes, k, m),
+                     scales_of(xt_scales, k, m),
+                     codes_of(wt_codes, k, n),
+                     scales_of(wt_scales, k, n)};
+  if (outputs_overlap(r, 3)) return invalid(fn, "an output or the workspace overlaps another buffer");
+  if (!dx && !dw) return PSGD_OK;
+  const WsOperand dr = ws_operand(ws, 0, m, n), dt = ws_operand(ws, operand_bytes(m, n), n, m);
+  MxQuantArgs a = quant_args(dy, dy_dtype, m, n, lddy);
+  a.rand = rand;
+  if (dx) a.row_codes = dr.codes, a.row_scales = dr.scales;
+  if (dw) a.col_codes = dt.codes, a.col_scales = dt.scales;
+  if (psgd_status_t s = launch_status(launch_mx_quantize(a, stream), fn)) return s;
+  if (dx) {
+    const MxProductArgs p{m, k, n, {dr.codes, dr.scales}, {wt_codes, wt_scales}, dx, dx_dtype, m > 1 ? lddx : k, false};
+    if (psgd_status_t s = launch_status(launch_mx_product(p, stream), fn)) return s;
+  }
+  if (!dw) return PSGD_OK;
+  const MxProductArgs p{n, k, m, {dt.codes, dt.scales}, {xt_codes, xt_scales}, dw, dw_dtype, n > 1 ? lddw : k, accumulate != 0};
+  return launch_status(launch_mx_product(p, stream), fn);
 }

@@ -703,7 +703,6 @@ __global__ __launch_bounds__(256) void k_mx_prod_zero(MxProductArgs p) {
   if (i < p.m * p.n) static_cast<typename Elem<DT>::type*>(p.c)[i / p.n * p.ldc + i % p.n] = Elem<DT>::down(0.f);
 }
 
-size_t mx_product_workspace(int64_t, int64_t, int64_t) { return 0; }
 
 template <int DT, int WM, int WN, int TM, int TN>
 static void product_lds(const MxProductArgs& p, hipStream_t s) {
@@ -753,7 +752,7 @@ static void product_dt(const MxProductArgs& p, hipStream_t s) {
   hipLaunchKernelGGL((k_mx_prod_tile<DT>), dim3((unsigned)(((p.m + 63) / 64) * ntn)), dim3(256), 0, s, p, ntn);
 }
 
-hipError_t launch_mx_product(const MxProductArgs& p, void*, hipStream_t s) {
+hipError_t launch_mx_product(const MxProductArgs& p, hipStream_t s) {
   if (p.m == 0 || p.n == 0) return hipSuccess;
   if (p.dtype == kF32)
     product_dt<kF32>(p, s);

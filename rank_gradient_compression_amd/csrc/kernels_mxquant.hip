@@ -236,17 +236,27 @@ __device__ __forceinline__ uint4 encode_block(const uint32_t (&w)[32 / kPerWord<
                     mx_encode8<DT, RAND>(w + 2 * W, sb, rnd + 4), mx_encode8<DT, RAND>(w + 3 * W, sb, rnd + 6));
 }
 
+// Up to two matrices of one launch: a small layer's training pass is bound by
+// its launches (700 x 650 and 2600 x 650 together instead of one by one).
+struct MxQuantJobs {
+  MxQuantArgs job[2];
+  int tiles[2], nct[2];  // tiles of 128 x 128, and how many of them side by side
+};
+
 // (The instructions of a small call come from memory too: the parts are
 // loops, and the kinds of tiles share all but their loads.)
 template <int DT, bool RAND, bool ROWS>
-__global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantArgs a, int nct) {
+__global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantJobs jobs) {
+  const int which = (int)blockIdx.x >= jobs.tiles[0];
+  const MxQuantArgs& a = jobs.job[which];
+  const int nct = jobs.nct[which];
   using T = typename Elem<DT>::type;
   constexpr int P = kColPitch<DT>, SKEW = kColSkew<DT>, RP = kColRandPitch, PW = kPerWord<DT>;
   __shared__ __align__(16) T tile[128 * P + 4 * SKEW];
   __shared__ __align__(16) uint8_t rtile[RAND ? 128 * RP : 16];
   __shared__ uint32_t stile[ROWS ? 128 : 1], ctile[128];  // four tiles' half chunks
   // (a tile writes half lines of codes; neighbouring tiles on one XCD fill them up in its L2)
-  const int t0 = xcd_position(blockIdx.x, gridDim.x), rt = t0 / nct, ct = t0 % nct;
+  const int t0 = xcd_position(blockIdx.x - which * jobs.tiles[0], jobs.tiles[which]), rt = t0 / nct, ct = t0 % nct;
   const int64_t row0 = (int64_t)rt * 128, col0 = (int64_t)ct * 128;
   const int64_t nblk_r = mx_blocks(a.cols), nblk_c = mx_blocks(a.rows);
   if (col0 + 128 <= a.cols)
@@ -376,20 +386,25 @@ static void quant_rows(const MxQuantArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_mx_quant_rows<DT, false, false>), g, b, 0, s, a, nch);
 }
 
+// b: a second matrix that wants the same operands with the same rounding.
 template <int DT>
-static void quant_cols(const MxQuantArgs& a, hipStream_t s) {
-  // whole chunks of 256 both ways, so that the scales past the end are written
-  const int nct = 2 * (int)mx_chunks(a.cols);
-  const dim3 g((unsigned)(2 * mx_chunks(a.rows) * nct)), b(256);
+static void quant_cols(const MxQuantArgs& a, const MxQuantArgs* b, hipStream_t s) {
+  MxQuantJobs j{{a, b ? *b : MxQuantArgs{}}, {0, 0}, {0, 0}};
+  for (int i = 0; i < (b ? 2 : 1); ++i) {
+    // whole chunks of 256 both ways, so that the scales past the end are written
+    j.nct[i] = 2 * (int)mx_chunks(j.job[i].cols);
+    j.tiles[i] = (int)(2 * mx_chunks(j.job[i].rows)) * j.nct[i];
+  }
+  const dim3 g((unsigned)(j.tiles[0] + j.tiles[1])), blk(256);
   const bool rows = a.row_codes != nullptr;
   if (a.rand && rows)
-    hipLaunchKernelGGL((k_mx_quant_cols<DT, true, true>), g, b, 0, s, a, nct);
+    hipLaunchKernelGGL((k_mx_quant_cols<DT, true, true>), g, blk, 0, s, j);
   else if (a.rand)
-    hipLaunchKernelGGL((k_mx_quant_cols<DT, true, false>), g, b, 0, s, a, nct);
+    hipLaunchKernelGGL((k_mx_quant_cols<DT, true, false>), g, blk, 0, s, j);
   else if (rows)
-    hipLaunchKernelGGL((k_mx_quant_cols<DT, false, true>), g, b, 0, s, a, nct);
+    hipLaunchKernelGGL((k_mx_quant_cols<DT, false, true>), g, blk, 0, s, j);
   else
-    hipLaunchKernelGGL((k_mx_quant_cols<DT, false, false>), g, b, 0, s, a, nct);
+    hipLaunchKernelGGL((k_mx_quant_cols<DT, false, false>), g, blk, 0, s, j);
 }
 
 template <int DT>
@@ -397,7 +412,7 @@ static void quantize(const MxQuantArgs& a, hipStream_t s) {
   if (a.col_codes) {
     MxQuantArgs c = a;
     if (a.values) c.row_codes = c.row_scales = nullptr;  // the row operand comes with its values below
-    quant_cols<DT>(c, s);
+    quant_cols<DT>(c, nullptr, s);
     if (!a.values) return;
   }
   quant_rows<DT>(a, s);
@@ -412,6 +427,23 @@ hipError_t launch_mx_quantize(const MxQuantArgs& a, hipStream_t s) {
   else
     quantize<kF16>(a, s);
   return hipGetLastError();
+}
+
+hipError_t launch_mx_quantize_pair(const MxQuantArgs& a, const MxQuantArgs& b, hipStream_t s) {
+  auto both = [](const MxQuantArgs& q) {
+    return q.rows && q.cols && q.row_codes && q.col_codes && !q.rand && !q.values;
+  };
+  if (a.dtype == b.dtype && both(a) && both(b)) {
+    if (a.dtype == kF32)
+      quant_cols<kF32>(a, &b, s);
+    else if (a.dtype == kBF16)
+      quant_cols<kBF16>(a, &b, s);
+    else
+      quant_cols<kF16>(a, &b, s);
+    return hipGetLastError();
+  }
+  if (hipError_t e = launch_mx_quantize(a, s); e != hipSuccess) return e;
+  return launch_mx_quantize(b, s);
 }
 
 template <int DT>

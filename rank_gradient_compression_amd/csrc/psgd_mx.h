@@ -51,6 +51,8 @@ struct MxQuantArgs {
   int64_t ldv;
 };
 hipError_t launch_mx_quantize(const MxQuantArgs& a, hipStream_t s);
+// Two matrices, in one launch where both want both operands in the same way.
+hipError_t launch_mx_quantize_pair(const MxQuantArgs& a, const MxQuantArgs& b, hipStream_t s);
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
                                 int dtype, int64_t ld, hipStream_t s);
 
@@ -62,11 +64,10 @@ struct MxProductArgs {
   int64_t ldc;
   bool accumulate;
 };
-hipError_t launch_mx_product(const MxProductArgs& p, void* ws, hipStream_t s);
+hipError_t launch_mx_product(const MxProductArgs& p, hipStream_t s);
 // y = Q(x) B^T in one launch, for so few activations that every workgroup
 // quantises them by itself (mx_linear_fuses); p.a is not read.
 bool mx_linear_fuses(int64_t m, int64_t k);
 hipError_t launch_mx_linear_fused(const MxProductArgs& p, const void* x, int x_dtype, int64_t ldx, hipStream_t s);
-size_t mx_product_workspace(int64_t m, int64_t n, int64_t k);
 
 }  // namespace psgd

@@ -44,13 +44,13 @@ def _call(device: torch.device, fn, *args) -> None:
 
 
 @functools.lru_cache(maxsize=4096)
-def _product_workspace(m: int, n: int, k: int) -> int:
-    return B.psgd_mx_product_workspace(m, n, k)
+def _linear_workspace(m: int, n: int, k: int) -> int:
+    return B.psgd_mx_linear_workspace(m, n, k)
 
 
 @functools.lru_cache(maxsize=4096)
-def _linear_workspace(m: int, n: int, k: int) -> int:
-    return B.psgd_mx_linear_workspace(m, n, k)
+def _train_workspace(m: int, n: int, k: int) -> int:
+    return B.psgd_mx_train_workspace(m, n, k)
 
 
 def _scratch(nbytes: int, device: torch.device):
@@ -272,10 +272,8 @@ def mx_product(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dty
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     c, ldc = _result(out, m, n, dtype, device)
-    need = _product_workspace(m, n, k)
-    ws, ws_ptr = _scratch(need, device)
     _call(device, B.psgd_mx_product, m, n, k, a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, c.data_ptr(),
-          _dtype(c), ldc, accumulate, ws_ptr, need)
+          _dtype(c), ldc, accumulate)
     return c
 
 
@@ -296,25 +294,56 @@ def mx_linear(x: torch.Tensor, w: MxTensor, out: Optional[torch.Tensor] = None,
 
 
 def mx_linear_forward(x: torch.Tensor, w: torch.Tensor):
-    """y = Q(x) Q(w)^T for full-precision weights, and what the backward pass
-    needs: the operands of x^T and w^T, whose blocks run along the axes that
-    its products sum over."""
-    xr, xt = mx_quantize_both(x)
-    wr, wt = mx_quantize_both(w)
-    return mx_product(xr, wr, dtype=x.dtype), (xt, wt)
+    """y = Q(x) Q(w)^T for full-precision weights (psgd_mx_train_forward), and
+    what the backward pass needs: the operands of x^T and w^T, whose blocks run
+    along the axes that its products sum over."""
+    m, k, ldx = _matrix(x, "x")
+    n, kw, ldw = _matrix(w, "w")
+    device = x.device
+    if k != kw or device != w.device:
+        raise ValueError(f"x has {k} columns on {device}, the weights {kw} on {w.device}")
+    dtype, w_dtype = _dtype(x), _dtype(w)
+    xt, wt = MxTensor(k, m, device), MxTensor(k, n, device)
+    y = torch.empty(m, n, dtype=x.dtype, device=device)
+    need = _train_workspace(m, n, k)
+    ws, ws_ptr = _scratch(need, device)
+    _call(device, B.psgd_mx_train_forward, m, n, k, x.data_ptr(), dtype, ldx, w.data_ptr(), w_dtype, ldw, xt.codes_ptr,
+          xt.scales_ptr, wt.codes_ptr, wt.scales_ptr, y.data_ptr(), dtype, max(1, n), ws_ptr, need)
+    return y, (xt, wt)
 
 
 def mx_linear_backward(dy: torch.Tensor, saved, rand: Optional[torch.Tensor] = None,
-                       dw: Optional[torch.Tensor] = None, accumulate: bool = False):
-    """Gradients of the layer with the quantisers taken as the identity:
-    dx = Q(dy) Q(w^T)^T in dy's type and dw = Q(dy^T) Q(x^T)^T in fp32, each
-    quantised along the axis it sums over; rand rounds dy stochastically.  dw:
-    the matrix to write (accumulate: to add to), for example a view of
-    PowerSGD.grads."""
+                       dw: Optional[torch.Tensor] = None, accumulate: bool = False, need_dx: bool = True,
+                       need_dw: bool = True):
+    """Gradients of the layer with the quantisers taken as the identity
+    (psgd_mx_train_backward): dx = Q(dy) Q(w^T)^T in dy's type and dw =
+    Q(dy^T) Q(x^T)^T in fp32, each quantised along the axis it sums over; rand
+    rounds dy stochastically.  dw: the matrix to write (accumulate: to add to),
+    for example a view of PowerSGD.grads.  A gradient that is not needed is
+    None and costs nothing."""
     xt, wt = saved
-    dyr, dyt = mx_quantize_both(dy, rand)
-    dx = mx_product(dyr, wt, dtype=dy.dtype)
-    return dx, mx_product(dyt, xt, out=dw, accumulate=accumulate)
+    m, n, lddy = _matrix(dy, "dy")
+    k, device = xt.rows, dy.device
+    if m != xt.cols or n != wt.cols or device != xt.device:
+        raise ValueError(f"dy is {m} x {n} on {device}, the forward pass was {xt.cols} x {wt.cols} on {xt.device}")
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs dw")
+    dtype = _dtype(dy)
+    r = 0 if rand is None else _rand(rand, dy)
+    dx, dx_ptr, dw_ptr, dw_dtype, lddw = None, 0, 0, dtype, k
+    if need_dx:
+        dx = torch.empty(m, k, dtype=dy.dtype, device=device)
+        dx_ptr = dx.data_ptr()
+    if need_dw:
+        dw, lddw = _result(dw, n, k, torch.float32, device)
+        dw_ptr, dw_dtype = dw.data_ptr(), _dtype(dw)
+    else:
+        dw = None
+    need = _train_workspace(m, n, k)
+    ws, ws_ptr = _scratch(need, device)
+    _call(device, B.psgd_mx_train_backward, m, n, k, dy.data_ptr(), dtype, lddy, r, xt.codes_ptr, xt.scales_ptr,
+          wt.codes_ptr, wt.scales_ptr, dx_ptr, dtype, max(1, k), dw_ptr, dw_dtype, lddw, accumulate, ws_ptr, need)
+    return dx, dw
 
 
 class _MxLinearFunction(torch.autograd.Function):
@@ -331,8 +360,9 @@ class _MxLinearFunction(torch.autograd.Function):
         rand = None
         if ctx.stochastic:
             rand = torch.randint(0, 256, flat.shape, dtype=torch.uint8, device=flat.device, generator=ctx.generator)
-        dx, dw = mx_linear_backward(flat, ctx.saved, rand)
-        return dx.view(ctx.x_shape), dw.to(ctx.w_dtype), None, None
+        need_dx, need_dw = ctx.needs_input_grad[:2]
+        dx, dw = mx_linear_backward(flat, ctx.saved, rand, need_dx=need_dx, need_dw=need_dw)
+        return dx.view(ctx.x_shape) if need_dx else None, dw.to(ctx.w_dtype) if need_dw else None, None, None
 
 
 def mx_linear_train(x: torch.Tensor, w: torch.Tensor, stochastic: bool = True, generator=None) -> torch.Tensor:

@@ -293,6 +293,69 @@ def test_linear_under_autograd():
     assert torch.equal(x.grad.reshape(42, 96), dx) and torch.equal(w.grad, dw.to(BF16))
 
 
+@pytest.mark.parametrize("m,k,n,xd,wd", [(1, 33, 5, F32, F32), (130, 70, 300, BF16, BF16), (70, 257, 129, BF16, F32),
+                                         (300, 650, 260, F16, F16)])
+@pytest.mark.parametrize("stochastic", [False, True])
+def test_training_pass_is_the_single_calls(m, k, n, xd, wd, stochastic):
+    """One launch for two matrices, gradients left out, rows with a stride: the
+    same bytes as the quantiser and the product called one by one."""
+    say(f"[mx] training pass {m}x{k}x{n} {xd} {wd} {stochastic}")
+    x, w, dy = matrix(m, k + 3, xd, 1)[:, :k], matrix(n, k, wd, 2), matrix(m, n + 5, xd, 3)[:, 2: n + 2]
+    rand = rand_bytes(m, n) if stochastic else None
+    y, (xt, wt) = T.mx_linear_forward(x, w)
+    dx, dw = T.mx_linear_backward(dy, (xt, wt), rand=rand)
+    xr, xt1 = T.mx_quantize_both(x)
+    wr, wt1 = T.mx_quantize_both(w)
+    dyr, dyt = T.mx_quantize_both(dy, rand)
+    for got, want in ((xt, xt1), (wt, wt1)):
+        assert torch.equal(T.mx_dequantize(got), T.mx_dequantize(want)) and torch.equal(got.codes, want.codes)
+    assert torch.equal(y, T.mx_product(xr, wr, dtype=xd))
+    assert torch.equal(dx, T.mx_product(dyr, wt1, dtype=xd))
+    assert torch.equal(dw, T.mx_product(dyt, xt1))
+    only_x, none = T.mx_linear_backward(dy, (xt, wt), rand=rand, need_dw=False)
+    assert none is None and torch.equal(only_x, dx)
+    none, only_w = T.mx_linear_backward(dy, (xt, wt), rand=rand, need_dx=False)
+    assert none is None and torch.equal(only_w, dw)
+    assert T.mx_linear_backward(dy, (xt, wt), need_dx=False, need_dw=False) == (None, None)
+
+
+@pytest.mark.parametrize("m,k,n", [(0, 5, 7), (5, 0, 7), (5, 7, 0), (0, 0, 0)])
+def test_training_pass_of_nothing(m, k, n):
+    z = lambda r, c: torch.zeros(r, c, device=DEV)  # noqa: E731
+    y, saved = T.mx_linear_forward(z(m, k), z(n, k))
+    dx, dw = T.mx_linear_backward(z(m, n), saved, dw=torch.ones(n, k, device=DEV))
+    for got, shape in ((y, (m, n)), (dx, (m, k)), (dw, (n, k))):
+        assert got.shape == shape and not bool(got.any())
+
+
+def test_frozen_weights_under_autograd():
+    x = matrix(40, 96, BF16, 1).requires_grad_(True)
+    w = matrix(50, 96, BF16, 2)
+    T.mx_linear_train(x, w, stochastic=False).sum().backward()
+    assert w.grad is None and x.grad.shape == x.shape
+    x, w = x.detach(), w.requires_grad_(True)
+    T.mx_linear_train(x, w, stochastic=False).sum().backward()
+    assert x.grad is None and w.grad.shape == w.shape
+
+
+def test_training_pass_refuses():
+    x, w = torch.zeros(4, 64, device=DEV), torch.zeros(8, 64, device=DEV)
+    _, saved = T.mx_linear_forward(x, w)
+    for bad in (torch.zeros(8, 63, device=DEV), torch.zeros(8, 64), torch.zeros(64, 8, device=DEV).t(), w.double()):
+        with pytest.raises(ValueError):
+            T.mx_linear_forward(x, bad)
+    dy = torch.zeros(4, 8, device=DEV)
+    for bad in (dy[:3], torch.zeros(4, 9, device=DEV), dy.cpu(), dy.double()):
+        with pytest.raises(ValueError):
+            T.mx_linear_backward(bad, saved)
+    with pytest.raises(ValueError):
+        T.mx_linear_backward(dy, saved, accumulate=True)
+    with pytest.raises(ValueError):
+        T.mx_linear_backward(dy, saved, dw=torch.zeros(8, 63, device=DEV))
+    with pytest.raises(ValueError):
+        T.mx_linear_backward(dy, saved, rand=torch.zeros(4, 9, dtype=torch.uint8, device=DEV))
+
+
 def test_torch_layer_refuses():
     x = torch.zeros(4, 64, device=DEV)
     q = T.mx_quantize(x)

@@ -29,7 +29,7 @@ def test_sizes_refused():
     refused(B.psgd_mx_sizes, -1, 4)
     refused(B.psgd_mx_sizes, 4, BIG)
     assert B.lib.psgd_mx_sizes(1, 1, None, None) == B.PSGD_ERR_INVALID_ARG
-    for fn in (B.psgd_mx_product_workspace, B.psgd_mx_linear_workspace):
+    for fn in (B.psgd_mx_linear_workspace, B.psgd_mx_train_workspace):
         refused(fn, -1, 4, 4)
         refused(fn, 4, 4, BIG)
 
@@ -61,7 +61,7 @@ def test_empty_matrices_are_accepted_without_a_device():
     quant(rows=0)
     quant(cols=0, ld=0)
     B.psgd_mx_dequantize(0, 0, 0, 7, 0, F32, 7)
-    B.psgd_mx_product(0, 5, 7, 0, 0, P, P, 0, F32, 5, False, 0, 0)
+    B.psgd_mx_product(0, 5, 7, 0, 0, P, P, 0, F32, 5, False)
     B.psgd_mx_linear(0, 5, 7, 0, F32, 7, P, P, 0, F32, 5, 0, 0)
 
 
@@ -76,7 +76,7 @@ def test_dequantize_refused():
 
 
 def test_product_refused():
-    ok = [8, 8, 64, 1 << 20, 2 << 20, 3 << 20, 4 << 20, P, F32, 8, False, 0, 0]
+    ok = [8, 8, 64, 1 << 20, 2 << 20, 3 << 20, 4 << 20, P, F32, 8, False]
     for at, bad, match in [(0, -1, "negative"), (1, BIG, "INT32_MAX"), (2, -3, "negative"), (3, 0, "NULL"),
                            (4, 0, "NULL"), (5, 0, "NULL"), (6, (4 << 20) + 1, "16-byte"), (7, 0, "NULL"),
                            (7, P + 2, "aligned"), (8, 5, "type"), (9, 7, "stride"), (7, 1 << 20, "overlaps"),
@@ -100,6 +100,44 @@ def test_linear_refused():
         args = list(ok)
         args[at] = bad
         refused(B.psgd_mx_linear, *args, status=B.PSGD_ERR_WORKSPACE)
+
+
+def train_args(m=40, n=96, k=70):
+    need = B.psgd_mx_train_workspace(m, n, k)
+    assert need >= sum(B.psgd_mx_sizes(m, k)) + sum(B.psgd_mx_sizes(n, k))
+    assert need >= sum(B.psgd_mx_sizes(m, n)) + sum(B.psgd_mx_sizes(n, m))
+    forward = [m, n, k, 1 << 24, BF16, k, 2 << 24, F32, k, 3 << 24, 4 << 24, 5 << 24, 6 << 24, 7 << 24, BF16, n,
+               8 << 24, need]
+    backward = [m, n, k, 1 << 24, BF16, n, 2 << 24, 3 << 24, 4 << 24, 5 << 24, 6 << 24, 7 << 24, BF16, k, 8 << 24, F32,
+                k, False, 9 << 24, need]
+    return forward, backward
+
+
+def test_training_pass_refused():
+    forward, backward = train_args()
+    for at, bad, match in [(0, -1, "negative"), (2, BIG, "INT32_MAX"), (3, 0, "NULL"), (4, 3, "type"), (5, 69, "stride"),
+                           (6, (2 << 24) + 2, "aligned"), (7, 4, "type"), (8, 69, "stride"), (9, 0, "NULL"),
+                           (10, (4 << 24) + 1, "16-byte"), (11, 0, "NULL"), (13, 0, "NULL"), (15, 95, "stride"),
+                           (13, 1 << 24, "overlaps"), (9, 2 << 24, "overlaps"), (11, 3 << 24, "overlaps"),
+                           (16, 7 << 24, "overlaps")]:
+        args = list(forward)
+        args[at] = bad
+        refused(B.psgd_mx_train_forward, *args, match=match)
+    for at, bad, match in [(1, -1, "negative"), (0, BIG, "INT32_MAX"), (3, 0, "NULL"), (4, 3, "type"), (5, 95, "stride"),
+                           (7, 0, "NULL"), (10, (6 << 24) + 4, "16-byte"), (11, (7 << 24) + 1, "aligned"),
+                           (13, 69, "stride"), (15, -1, "type"), (16, 69, "stride"), (11, 8 << 24, "overlaps"),
+                           (14, 1 << 24, "overlaps"), (14, 2 << 24, "overlaps"), (11, 3 << 24, "overlaps"),
+                           (18, 8 << 24, "overlaps")]:
+        args = list(backward)
+        args[at] = bad
+        refused(B.psgd_mx_train_backward, *args, match=match)
+    for fn, ok, ws in ((B.psgd_mx_train_forward, forward, 16), (B.psgd_mx_train_backward, backward, 18)):
+        for at, bad in [(ws, 0), (ws, (9 << 24) + 128), (ws + 1, ok[ws + 1] - 1)]:
+            args = list(ok)
+            args[at] = bad
+            refused(fn, *args, status=B.PSGD_ERR_WORKSPACE)
+    big = (1 << 31) - 1
+    refused(B.psgd_mx_train_forward, big, big, 1, *forward[3:], match="too large")
 
 
 def test_clip_create_refused():
