@@ -16,7 +16,8 @@ namespace psgd {
 
 // How a run of elements that may cross the row's end is read.  FULL: all of it
 // is inside the row.  EDGE: the row is at least as long as the run, which is
-// read from an earlier column if need be, inside the row, and shifted down.
+// read from an earlier column if need be, inside the row, and shifted down
+// (what is shifted out may be another tile's, which writes it in place).
 // NARROW: element by element, at columns clamped into the row (a branch around
 // a load would make the compiler wait for it before it issues the next).
 // Whatever the row's alignment: the hardware takes 16-byte accesses at any
@@ -237,7 +238,8 @@ __device__ __forceinline__ uint4 encode_block(const uint32_t (&w)[32 / kPerWord<
 }
 
 // Up to two matrices of one launch: a small layer's training pass is bound by
-// its launches (700 x 650 and 2600 x 650 together instead of one by one).
+// its launches (700 x 650 and 2600 x 650 in fp32: 8.3 us together, 5.6 and 6.7
+// one by one, and 2.6 us of the host for each launch).
 struct MxQuantJobs {
   MxQuantArgs job[2];
   int tiles[2], nct[2];  // tiles of 128 x 128, and how many of them side by side

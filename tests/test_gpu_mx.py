@@ -79,6 +79,18 @@ def test_quantize_bit_for_bit(dtype, stochastic):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_every_width_of_a_last_tile(dtype):
+    for cols in [*range(1, 40), *range(250, 272)]:
+        x, r = matrix(3, cols, dtype, seed=21), rand_bytes(3, cols)
+        rn = r.cpu().numpy()
+        say(f"[mx] width {cols} {dtype}")
+        v = x.clone()
+        check_operand(T.mx_quantize(v, rand=r, values=v), f64(x), rn, "rows, in place")
+        assert np.array_equal(f64(v), MX.round_values(f64(x), rn)), "values differ"
+        check_operand(T.mx_quantize_t(x, rand=r), f64(x).T, rn.T, "columns")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_strided_and_unaligned_rows(dtype):
     for off, ld in [(0, 700), (1, 701), (3, 650 + 3), (2, 652)]:
         rows, cols = 37, 649
