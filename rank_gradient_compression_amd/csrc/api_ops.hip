@@ -252,7 +252,6 @@ extern "C" psgd_status_t psgd_clip_apply(psgd_clip_t c, float max_norm, float sc
   const char* fn = "psgd_clip_apply";
   if (psgd_status_t s = check_clip_call(fn, c, max_norm, scale, stats, ws, bytes)) return s;
   const ClipArgs a = clip_args(c, ws, scale, max_norm, stats);
-  if (psgd_status_t s = launch_status(launch_clip_norm(a, stream), fn)) return s;
   return launch_status(launch_clip_apply(a, stream), fn);
 }
 

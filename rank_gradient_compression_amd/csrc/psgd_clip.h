@@ -21,6 +21,10 @@ constexpr int kClipSumGroups = 4096;
 // 256 MB last level of cache.
 constexpr int64_t kClipCacheBytes = int64_t(192) << 20;
 
+// Up to this many sums of squares the writing pass adds them by itself.
+constexpr int kClipInlineSums = 1024;
+constexpr int kClipStatsTensors = 8;  // tensors whose norms one of its workgroups then writes
+
 struct ClipTensor {
   const void* in;
   void* out;
@@ -54,6 +58,7 @@ struct ClipArgs {
 
 hipError_t launch_clip_bind(ClipTensor* tensors, const ClipPointers& p, int first, int n, hipStream_t s);
 hipError_t launch_clip_norm(const ClipArgs& a, hipStream_t s);
+// The norm, and the clipped gradients.
 hipError_t launch_clip_apply(const ClipArgs& a, hipStream_t s);
 
 }  // namespace psgd
