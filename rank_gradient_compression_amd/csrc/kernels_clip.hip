@@ -4,8 +4,9 @@
 //   out_t = scale * c * g_t
 //
 // Sums of squares, their fixed-order sum (one workgroup; for short lists every
-// workgroup of the next launch by itself), the scaled write.  Squares are summed in fp64: an fp32 square overflows from
-// 1.8e19 on, and the one conversion per element is hidden behind the reads.
+// workgroup of the next launch by itself), the scaled write.  Squares are
+// summed in fp64: an fp32 square overflows from 1.8e19 on, and the one
+// conversion per element is hidden behind the reads.
 // Bound: HBM, the gradients read twice (the second reading from the last level
 // of cache as far as it holds them) and written once.  Sums are made in a
 // fixed order without atomics, so a repeated call agrees bit for bit.
@@ -205,8 +206,8 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, int64_t e0, flo
 // pass has read the last ones last, and the cache still holds them.
 // INLINE: every workgroup adds the few sums of a short list by itself and
 // further ones write the norms, kClipStatsTensors tensors each, which saves a
-// launch (4 tensors, 1 Mi values: 11.5 -> 7.8 us, 8 Mi: 21.1 -> 19.1; 1536 sums
-// of 12 Mi values, 28.3 with the launch, would read as much again as the norm).
+// launch (4 tensors, 1 Mi values: 11.5 -> 7.8 us, 8 Mi: 21.1 -> 19.1; every
+// workgroup reads all sums, so the gain is used up as the list grows).
 template <bool NTL, bool NTS, bool INLINE>
 __global__ __launch_bounds__(256) void k_clip_apply(ClipArgs a) {
   float coefficient;

@@ -153,13 +153,18 @@ __global__ __launch_bounds__(256) void k_mx_prod_tile(MxProductArgs p, int ntn) 
 // straight into LDS (16 bytes per lane, no registers), two stages, so the next
 // chunk arrives while the matrix cores work on this one.  The hardware writes
 // LDS in lane order; each lane therefore *fetches* the block that belongs
-// there: block b of row r sits at slot b ^ (r / 2 % 8), which spreads the
-// 16-byte reads of 16 neighbouring rows over all 64 banks (counted: no
-// conflicts; b ^ (r % 8) had one for every read).  Scales come from memory
-// into registers a chunk ahead, 256 contiguous bytes per 32 rows.  Buffer
-// descriptors end with the tile's last row: rows past it read as zero, without
-// a fault.
+// there: block b of row r sits at slot b ^ mx_slot_key(r).  Scales come from
+// memory into registers a chunk ahead, 256 contiguous bytes per 32 rows.
+// Buffer descriptors end with the tile's last row: rows past it read as zero,
+// without a fault.
 constexpr int kChunkBytes = 128;
+
+// Two rows of 128 bytes cover the 64 banks.  A 16-byte read goes through them
+// in groups of lanes that take rows 0-3 and 12-15 of one block and rows 4-11
+// of the block two further: with key (r / 2) % 8 both halves meet (counted:
+// 3.7 conflict cycles a read), (r / 2 + 6) % 8 keeps them apart (0.1), and
+// eight neighbouring rows stay apart too.
+__device__ __forceinline__ int mx_slot_key(int row) { return ((row >> 1) + 6) & 7; }
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
@@ -290,17 +295,17 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(p.b.codes + n0 * pitch), 0, (int)((uint32_t)min((int64_t)BN, p.n - n0) * pitch), 0x00020000);
   // One of the PA + PB loads of 8 rows of a wavefront's share of a chunk: the
-  // slot of a block is its number ^ (r / 2) % 8, so it depends on whether the
-  // group of 8 rows is an even or an odd one of the tile.
+  // slots of its blocks depend on whether the group of 8 rows is an even or an
+  // odd one of the tile.
   constexpr int PA = BM / 8 / WAVES, PB = BN / 8 / WAVES;
   const int swap_a = PA & wave & 1, swap_b = PB & wave & 1;  // the wavefront's first group is an odd one
-  auto lane_off = [&](int odd) { return (lane >> 3) * pitch + (((lane & 7) ^ (4 * odd + (lane >> 4))) << 4); };
+  auto lane_off = [&](int odd) { return (lane >> 3) * pitch + (((lane & 7) ^ mx_slot_key(8 * odd + (lane >> 3))) << 4); };
   const uint32_t lane_a[2] = {lane_off(swap_a), lane_off(1 - swap_a)};
   const uint32_t lane_b[2] = {lane_off(swap_b), lane_off(1 - swap_b)};
   const int r = lane & 15, g = lane >> 4;
   uint32_t off[2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) off[s] = r * kChunkBytes + (((2 * g + s) ^ ((r >> 1) & 7)) << 4);
+  for (int s = 0; s < 2; ++s) off[s] = r * kChunkBytes + (((2 * g + s) ^ mx_slot_key(r)) << 4);
   // a wavefront's scale tiles; past the last tile of rows the last one again
   const uint32_t rtm = (uint32_t)((p.m + 31) / 32 - 1 - m0 / 32), rtn = (uint32_t)((p.n + 31) / 32 - 1 - n0 / 32);
   const __amdgpu_buffer_rsrc_t rsa =
@@ -535,11 +540,11 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_mx_prod_skinny(MxSkinnyArgs p
   const XR x(STAGED ? p.x : p.w, STAGED ? x0 : w0, STAGED ? p.narrow : p.wide, p.k);
   const uint32_t nch = w.nch, pitch = w.pitch;
   // (the slots of the large products' tiles)
-  const uint32_t off0 = (lane >> 3) * pitch + (((lane & 7) ^ (lane >> 4)) << 4);
-  const uint32_t off1 = (lane >> 3) * pitch + (((lane & 7) ^ (4 + (lane >> 4))) << 4);
+  const uint32_t off0 = (lane >> 3) * pitch + (((lane & 7) ^ mx_slot_key(lane >> 3)) << 4);
+  const uint32_t off1 = (lane >> 3) * pitch + (((lane & 7) ^ mx_slot_key(8 + (lane >> 3))) << 4);
   uint32_t off[2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) off[s] = r * kChunkBytes + (((2 * g + s) ^ ((r >> 1) & 7)) << 4);
+  for (int s = 0; s < 2; ++s) off[s] = r * kChunkBytes + (((2 * g + s) ^ mx_slot_key(r)) << 4);
   uint8_t *const m0 = st0 + wave * STAGE, *const m1 = st1 + wave * STAGE;
   uint32_t sw0[WR::T], sw1[WR::T], sx0[XR::T], sx1[XR::T];
   auto fetch = [&](uint32_t ch, uint8_t* m, uint32_t(&sw)[WR::T], uint32_t(&sx)[XR::T]) {
