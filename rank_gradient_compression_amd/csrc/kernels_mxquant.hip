@@ -129,7 +129,10 @@ __device__ __forceinline__ void quant_rows_tile(const MxQuantArgs& a, int nch, u
   auto quantise = [&](int s, uint32_t(&v)[W], uint32_t(&rnd)[2]) {
     const int r = s * 8 + (int)threadIdx.x / 32;
     settle<sizeof(T), R>(col, a.cols, v);
-    if constexpr (RAND) settle<1, R>(col, a.cols, rnd);
+    if constexpr (RAND) {
+      settle<1, R>(col, a.cols, rnd);
+      rnd[0] = ~rnd[0], rnd[1] = ~rnd[1];
+    }
     uint32_t am = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) am = mx_max_words<DT>(am, v[i]);
@@ -194,10 +197,10 @@ template <int DT>
 constexpr int kColSkew = 64 / dtype_bytes(DT);  // shift per 32 rows, elements
 constexpr int kColRandPitch = 132;
 
-// The tile into LDS, and its random bytes: all of a thread's 16-byte loads
-// under way at once, or a quarter of them where a narrow matrix is read element by
-// element (the addresses would take the registers that keep further workgroups
-// resident).
+// The tile into LDS, and its random bytes' complements: all of a thread's
+// 16-byte loads under way at once, or a quarter of them where a narrow matrix
+// is read element by element (the addresses would take the registers that keep
+// further workgroups resident).
 template <int DT, bool RAND, Reach R>
 __device__ __forceinline__ void cols_tile_load(const MxQuantArgs& a, int64_t row0, int64_t col0,
                                                typename Elem<DT>::type* tile, uint8_t* rtile) {
@@ -219,7 +222,11 @@ __device__ __forceinline__ void cols_tile_load(const MxQuantArgs& a, int64_t row
     for (int s = 0; s < GROUP; ++s) {
       const int r = (s0 + s) * RPP + r0;
       settle<sizeof(T), R>(col0 + c, a.cols, v[s]);
-      if constexpr (RAND) settle<1, R>(col0 + c, a.cols, rnd[s]);
+      if constexpr (RAND) {
+        settle<1, R>(col0 + c, a.cols, rnd[s]);
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) rnd[s][i] = ~rnd[s][i];
+      }
       uint4 q = make_uint4(v[s][0], v[s][1], v[s][2], v[s][3]);
       if (row0 + r >= a.rows) q = make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4*>(&tile[r * kColPitch<DT> + (r >> 5) * kColSkew<DT> + c]) = q;
@@ -308,14 +315,12 @@ __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantJobs jobs) {
       const uint32_t sb = mx_scale_byte(PW == 1 ? am : mx_half_max_bits<DT>(h ? am >> 16 : am & 0xffffu));
       uint4 q;
       if constexpr (RAND) {
-        const float inv = sb == 255u ? 0.f : mx_inv_scale(sb);
-        uint32_t code[4] = {0, 0, 0, 0};
+        uint32_t code[4];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float v = PW == 1 ? __uint_as_float(w[j]) : Elem<DT>::up((uint16_t)(w[j] >> 16 * h));
-          code[j / 8] |= mx_stochastic_code<DT>(v, inv, (uint32_t)rnd[j] >> 8 * h & 255u) << 4 * (j & 7);
-        }
-        q = sb == 255u ? make_uint4(0, 0, 0, 0) : make_uint4(code[0], code[1], code[2], code[3]);
+        for (int j = 0; j < 4; ++j)
+          code[j] = h ? mx_stochastic8_column<DT, 1>(w + 8 * j, sb, rnd + 8 * j)
+                      : mx_stochastic8_column<DT, 0>(w + 8 * j, sb, rnd + 8 * j);
+        q = make_uint4(code[0], code[1], code[2], code[3]);
       } else {
         uint32_t u[32 / PW];
 #pragma unroll

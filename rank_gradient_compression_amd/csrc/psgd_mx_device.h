@@ -108,40 +108,93 @@ __device__ __forceinline__ uint32_t mx_nearest8(const uint32_t* w, uint32_t byte
   return byte == 255u ? 0u : r;
 }
 
-// Stochastic rounding of one value to its code with one random byte r: up when
-// the fraction between the two neighbours, times 256, is above r + 0.5.  From
-// magnitude 1 on the code's spacing is bit 22 of an fp32 number (one fraction
-// bit), below it is 1/2: in either case the magnitude, as an integer whose
-// bit 22 counts codes, plus 2^22 - 1 - (r + 0.5) 2^14 carries into bit 22
-// exactly when the fraction is above the threshold.  Below 1 the integer is
-// a * 2^23: exact for 16-bit types (a value above the smallest threshold, 2^13,
-// has its 11 bits or fewer above 1), rounded up for fp32, which keeps "above
-// the threshold".  (All values are doubled here, to shift the sign out.)
-template <int DT>
-__device__ __forceinline__ uint32_t mx_stochastic_code(float x, float inv, uint32_t r) {
-  const float t = x * inv, a = fabsf(t);
-  const uint32_t big = (__float_as_uint(t) << 1) - (0xFCu << 23);
-  const uint32_t small = DT == kF32 ? (uint32_t)ceilf(a * 0x1p23f) << 1 : (uint32_t)(a * 0x1p24f);
-  const uint32_t m = (a < 1.f ? small : big) + (2u * (0x3fffffu - 0x2000u) - (r << 15));
-  return (m >> 23) | (__float_as_uint(x) >> 28 & 8u);
+// Stochastic rounding of one value x to its code with one random byte r: up
+// when the fraction between the two neighbours, times 256, is above r + 0.5.
+// From magnitude 1 on, the codes follow the upper bits of an fp32 number: bit
+// 22 counts them.  Below 1 they are 1/2 apart; (a + 1) / 2 lies in [1/2, 1),
+// where bit 22 counts halves of a, and is above a exactly there, so the larger
+// of the two continues the count downwards (code 0 at 1/2).  The magnitude's
+// bits plus 2^22 - 1 - (r + 0.5) 2^14 carry into bit 22 exactly when the
+// fraction is above the threshold.  (a + 1) / 2 is exact for 16-bit types
+// wherever a is above the smallest threshold, 2^-10; for fp32 a is rounded up
+// to a multiple of 2^-23 instead, which keeps "above the threshold".
+//
+// Everything is shifted up by two bits, so that the code is the top byte and
+// the random byte a byte too: mx_threshold puts ~r (byte i of rn), the constant
+// and minus 1/2's code together in one permutation (10 instructions a value in
+// all, 16 without these two steps: both operands of 2048 x 11008 bf16 43 -> 33
+// us).
+__device__ __forceinline__ uint32_t mx_threshold(uint32_t rn, int i) {
+  return __builtin_amdgcn_perm(rn, 0x04007ffcu, 0x03040100u + ((uint32_t)i << 16));
 }
 template <int DT>
-__device__ __forceinline__ uint32_t mx_stochastic8(const uint32_t* w, uint32_t byte, const uint32_t* rnd) {
+__device__ __forceinline__ uint32_t mx_stochastic(float x, float inv, uint32_t threshold) {
+  const float a = fabsf(x) * inv;
+  uint32_t bits;
+  if (DT == kF32)
+    bits = a < 1.f ? 0x3f000000u + (uint32_t)ceilf(a * 0x1p23f) : __float_as_uint(a);
+  else
+    bits = __float_as_uint(fmaxf(a, fmaf(a, 0.5f, 0.5f)));
+  return (bits << 2) + threshold;
+}
+
+// Byte B of four words.
+template <int B>
+__device__ __forceinline__ uint32_t gather_bytes(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+  return __builtin_amdgcn_perm(w1, w0, 0x0c0c0400u + B * 0x101u) |
+         __builtin_amdgcn_perm(w3, w2, 0x04000c0cu + B * 0x01010000u);
+}
+
+// Eight codes (the top bytes of m) and signs (bit 7 of byte E of the words e
+// and of byte O of the words o, for the even and the odd values) to a word.
+template <int E, int O>
+__device__ __forceinline__ uint32_t mx_pack8(const uint32_t (&m)[8], uint32_t e0, uint32_t e1, uint32_t e2, uint32_t e3,
+                                             uint32_t o0, uint32_t o1, uint32_t o2, uint32_t o3) {
+  const uint32_t even = gather_bytes<3>(m[0], m[2], m[4], m[6]), odd = gather_bytes<3>(m[1], m[3], m[5], m[7]);
+  const uint32_t se = gather_bytes<E>(e0, e1, e2, e3) & 0x80808080u;
+  const uint32_t so = gather_bytes<O>(o0, o1, o2, o3) & 0x80808080u;
+  return even | odd << 4 | se >> 4 | so;
+}
+
+// rn: the complements of the eight random bytes.
+template <int DT>
+__device__ __forceinline__ uint32_t mx_stochastic8(const uint32_t* w, uint32_t byte, const uint32_t* rn) {
   const float inv = byte == 255u ? 0.f : mx_inv_scale(byte);
-  uint32_t q = 0;
+  uint32_t m[8], q;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float x = DT == kF32 ? __uint_as_float(w[i]) : Elem<DT>::up((uint16_t)(w[i / 2] >> (i & 1) * 16));
-    q |= mx_stochastic_code<DT>(x, inv, rnd[i / 4] >> (i & 3) * 8 & 255u) << 4 * i;
+    m[i] = mx_stochastic<DT>(x, inv, mx_threshold(rn[i / 4], i & 3));
   }
+  if constexpr (DT == kF32)
+    q = mx_pack8<3, 3>(m, w[0], w[2], w[4], w[6], w[1], w[3], w[5], w[7]);
+  else
+    q = mx_pack8<1, 3>(m, w[0], w[1], w[2], w[3], w[0], w[1], w[2], w[3]);
   return byte == 255u ? 0u : q;
 }
 
-// Eight values of DT's words to codes; rnd: their eight random bytes.
+// The same for eight words that hold one value each, the half H of a 16-bit
+// type's, with a random byte's complement in byte H of rn.
+template <int DT, int H>
+__device__ __forceinline__ uint32_t mx_stochastic8_column(const uint32_t* w, uint32_t byte, const uint16_t* rn) {
+  const float inv = byte == 255u ? 0.f : mx_inv_scale(byte);
+  uint32_t m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = DT == kF32 ? __uint_as_float(w[i]) : Elem<DT>::up((uint16_t)(w[i] >> 16 * H));
+    m[i] = mx_stochastic<DT>(x, inv, mx_threshold(rn[i], H));
+  }
+  constexpr int B = DT == kF32 || H ? 3 : 1;
+  const uint32_t q = mx_pack8<B, B>(m, w[0], w[2], w[4], w[6], w[1], w[3], w[5], w[7]);
+  return byte == 255u ? 0u : q;
+}
+
+// Eight values of DT's words to codes; rn: the complements of their eight
+// random bytes.
 template <int DT, bool RAND>
-__device__ __forceinline__ uint32_t mx_encode8(const uint32_t* w, uint32_t byte, const uint32_t* rnd) {
+__device__ __forceinline__ uint32_t mx_encode8(const uint32_t* w, uint32_t byte, const uint32_t* rn) {
   if constexpr (RAND)
-    return mx_stochastic8<DT>(w, byte, rnd);
+    return mx_stochastic8<DT>(w, byte, rn);
   else
     return mx_nearest8<DT>(w, byte);
 }
