@@ -734,20 +734,24 @@ static void product_dt(const MxProductArgs& p, hipStream_t s) {
       product_skinny<true>(ba, s);
     return;
   }
-  // Tiles as large as still occupy more than half of the 256 compute units: a
-  // larger tile reads its operands fewer times, but idle compute units cost
-  // more (2048 x 4096 x 11008: 128 tiles of 256 x 256 70 us, 512 of 128 x 128,
-  // two workgroups to a compute unit, 60; 2048 x 11008 x 4096: 344 of 256 x
-  // 256 64 us, 1376 of 128 x 128 67).  Below, 64 x 64 tiles whose wavefronts
-  // share the summed axis.  A single chunk is a write of C and hardly a
-  // product: small workgroups.
-  auto tiles = [&](int64_t b) { return ((p.m + b - 1) / b) * ((p.n + b - 1) / b); };
+  // Large tiles read their operands fewer times, but 256 compute units work on
+  // one each at a time, so what counts is the rounds.  192 rows instead of 256
+  // where their rounds, 3/4 as long, end sooner (2048 x 11008 x 4096,
+  // bf16: 344 tiles of 256 x 256, two rounds, 65 us; 473 of 192 x 256, two
+  // shorter ones, 54; 1376 of 128 x 128 59).  Where large tiles occupy at most
+  // half of the compute units, 128 x 128, two to a compute unit (2048 x 4096 x
+  // 11008: 128 tiles of 256 x 256 70 us, 176 of 192 x 256 61, 512 of 128 x 128
+  // 52); where even 64 x 64 tiles are few, such tiles whose wavefronts share
+  // the summed axis.  A single chunk is a write of C and hardly a product:
+  // small workgroups.
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((p.m + bm - 1) / bm) * ((p.n + bn - 1) / bn); };
+  auto rounds = [&](int64_t bm) { return (tiles(bm, 256) + 255) / 256; };
   if (fits && p.k > 256) {
-    if (tiles(64) <= 256)
+    if (tiles(64, 64) <= 256)
       skinny<4, 2, false, -1>(ab, s);
-    else if (tiles(256) <= 128)
+    else if (tiles(256, 256) <= 128)
       product_lds<DT, 2, 2, 2, 2>(p, s);
-    else if (3 * ((((p.m + 191) / 192) * ((p.n + 255) / 256) + 255) / 256) < 4 * ((tiles(256) + 255) / 256))
+    else if (3 * rounds(192) < 4 * rounds(256))
       product_lds<DT, 2, 4, 3, 2>(p, s);
     else
       product_lds<DT, 2, 4, 4, 2>(p, s);
