@@ -469,7 +469,9 @@ psgd_status_t psgd_subspace_overlap(psgd_plan_t plan, const float* q_a, const fl
  *                        the gradient of the same tensor in place, with
  *                        types of the same size).
  * psgd_clip_norm         stats only: reads the gradients once.
- * psgd_clip_apply        stats and outputs.  The outputs must have been bound.
+ * psgd_clip_apply        stats and outputs.  Without bound outputs it writes
+ *                        the stats alone; without bound gradients the norms
+ *                        are NaN.
  *
  * Errors of the last two: PSGD_ERR_INVALID_ARG for a NULL or misaligned stats,
  * a negative or NaN max_norm (an infinite one clips nothing), a scale that is

@@ -87,7 +87,8 @@ template <bool NT>
 __global__ __launch_bounds__(256) void k_clip_sums(ClipArgs a) {
   const ClipTensor t = a.tensors[a.sum_map[blockIdx.x]];
   const int first = (int)blockIdx.x - t.first_sum;
-  double s = t.in_dtype == kF32    ? chunk_squares<kF32, NT>(t, first)
+  double s = !t.in                 ? __longlong_as_double(0x7ff8000000000000)  // never bound
+             : t.in_dtype == kF32  ? chunk_squares<kF32, NT>(t, first)
              : t.in_dtype == kBF16 ? chunk_squares<kBF16, NT>(t, first)
                                    : chunk_squares<kF16, NT>(t, first);
   __shared__ double w[4];
@@ -234,6 +235,7 @@ __global__ __launch_bounds__(256) void k_clip_apply(ClipArgs a) {
   }
   const int chunk = a.nchunks - 1 - (int)blockIdx.x;
   const ClipTensor t = a.tensors[a.chunk_map[chunk]];
+  if (!t.in || !t.out) return;  // bound without outputs, or never
   const int64_t e0 = (int64_t)(chunk - t.first_chunk) * kClipChunk;
   const float c = coefficient * a.scale;
   switch (t.in_dtype * 3 + t.out_dtype) {

@@ -355,6 +355,7 @@ class _MxLinearFunction(torch.autograd.Function):
         return y.view(*x.shape[:-1], w.shape[0])
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         flat = dy.reshape(-1, dy.shape[-1]).contiguous()
         rand = None

@@ -16,6 +16,7 @@ if not torch.cuda.is_available():
 import workloads as W  # noqa: E402
 from gpu_util import say  # noqa: E402
 from oracle import microscaling as MX  # noqa: E402
+from rank_gradient_compression_amd import binding as B  # noqa: E402
 from rank_gradient_compression_amd import torch_api as T  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -160,6 +161,28 @@ def test_more_than_2_to_the_31_elements():
     s = f64(c.clip(norm / 2))
     assert s[0] == pytest.approx(norm, rel=2.0 ** -23) and s[1] == pytest.approx(0.5, rel=1e-6)
     assert float(g[-1]) == 1.5 and float(g[-2]) == 2.0 ** -11 and float(g[0]) == 2.0 ** -11
+
+
+def test_calls_before_and_without_bound_outputs():
+    for n in (5000, 12_000_000):  # both ways of adding the sums
+        g = [torch.full((n // 20,), 0.5, device=DEV) for _ in range(20 if n > 5000 else 1)]
+        o = [torch.full_like(t, 7.0) for t in g]
+        h = B.psgd_clip_create([t.numel() for t in g], [B.PSGD_DTYPE_F32] * len(g), [B.PSGD_DTYPE_F32] * len(g))
+        nbytes = B.psgd_clip_workspace(h)
+        ws, stats = torch.empty(nbytes, dtype=torch.uint8, device=DEV), torch.zeros(2 + len(g), device=DEV)
+        s = torch.cuda.current_stream().cuda_stream
+        B.psgd_clip_workspace_init(h, ws.data_ptr(), nbytes, s)
+        B.psgd_clip_apply(h, 1.0, 1.0, stats.data_ptr(), ws.data_ptr(), nbytes, s)
+        assert bool(torch.isnan(stats).all()), "never bound"
+        B.psgd_clip_bind(h, [t.data_ptr() for t in g], None, ws.data_ptr(), nbytes, s)
+        B.psgd_clip_apply(h, 1.0, 1.0, stats.data_ptr(), ws.data_ptr(), nbytes, s)
+        norm = 0.5 * sum(t.numel() for t in g) ** 0.5
+        assert abs(float(stats[0]) - norm) <= 2.0 ** -23 * norm and all(bool((t == 7.0).all()) for t in o)
+        B.psgd_clip_bind(h, [t.data_ptr() for t in g], [t.data_ptr() for t in o], ws.data_ptr(), nbytes, s)
+        B.psgd_clip_apply(h, 1.0, 1.0, stats.data_ptr(), ws.data_ptr(), nbytes, s)
+        assert all(bool((t == t[0]).all()) and 0 < float(t[0]) < 0.5 for t in o)
+        torch.cuda.synchronize()
+        B.psgd_clip_destroy(h)
 
 
 def test_refusals():
