@@ -3,10 +3,10 @@
 //   n_t = || scale * g_t ||,  N = sqrt(sum n_t^2),  c = min(1, max_norm / (N + 1e-6)),
 //   out_t = scale * c * g_t
 //
-// Sums of squares, their fixed-order sum (one workgroup; for short lists every
-// workgroup of the next launch by itself), the scaled write.  Squares are
-// summed in fp64: an fp32 square overflows from 1.8e19 on, and the one
-// conversion per element is hidden behind the reads.
+// Sums of squares; their sum in one fixed order, by a workgroup of its own or,
+// for short lists, by every workgroup of the next launch; the scaled write.
+// Squares are summed in fp64: an fp32 square overflows from 1.8e19 on, and the
+// one conversion per element is hidden behind the reads.
 // Bound: HBM, the gradients read twice (the second reading from the last level
 // of cache as far as it holds them) and written once.  Sums are made in a
 // fixed order without atomics, so a repeated call agrees bit for bit.
@@ -139,12 +139,12 @@ __device__ __forceinline__ void tensor_norms(const ClipArgs& a, int first, int s
 }
 
 // One workgroup: all sums into LDS at once (in one wait for memory), then four
-// wavefronts add them all, and all add each tensor's.  Sums beyond LDS
-// (lists of thousands of tensors) are read where they are.
+// wavefronts add them all, and all add each tensor's.  Sums beyond LDS (lists
+// of more than a thousand tensors) are read where they are.
 __global__ __launch_bounds__(1024) void k_clip_final(ClipArgs a) {
   __shared__ double part[4];
-  __shared__ double lds[kClipSumGroups + 1024];
-  constexpr int N = (kClipSumGroups + 1024) / 1024;
+  constexpr int N = 2;
+  __shared__ double lds[N * 1024];
   double v[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -205,10 +205,10 @@ __device__ __forceinline__ void scale_chunk(const ClipTensor& t, int64_t e0, flo
 
 // Workgroups run through the chunks from the last to the first: the norm's
 // pass has read the last ones last, and the cache still holds them.
-// INLINE: every workgroup adds the few sums of a short list by itself and
-// further ones write the norms, kClipStatsTensors tensors each, which saves a
-// launch (4 tensors, 1 Mi values: 11.5 -> 7.8 us, 8 Mi: 21.1 -> 19.1; every
-// workgroup reads all sums, so the gain is used up as the list grows).
+// INLINE: every workgroup adds the sums by itself, and further ones write the
+// norms, kClipStatsTensors tensors each, instead of a launch in between (fp32,
+// two lists in turn: 2 Mi values 13.5 against 15.8 us, 32 Mi 69.4 and 71.5, 64
+// Mi 130 and 132; but 667e6 bf16 values, 81 thousand workgroups, 905 and 876).
 template <bool NTL, bool NTS, bool INLINE>
 __global__ __launch_bounds__(256) void k_clip_apply(ClipArgs a) {
   float coefficient;
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(256) void k_clip_apply(ClipArgs a) {
       const int first = extra * kClipStatsTensors;
       tensor_norms(a, first + __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64), 4,
                    min(a.ntensors, first + kClipStatsTensors), load);
-      if (blockIdx.x + 1 == gridDim.x && threadIdx.x == 0) {
+      if (extra == 0 && threadIdx.x == 0) {
         a.stats[0] = r.x;
         a.stats[1] = r.y;
       }
@@ -272,15 +272,19 @@ hipError_t launch_clip_norm(const ClipArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_clip_apply(const ClipArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)a.nchunks), b(256);
-  if (a.nchunks > 0 && a.nsums <= kClipInlineSums) {  // (far below the streaming sizes)
+  if (a.nchunks == 0) return launch_clip_norm(a, s);
+  const dim3 b(256);
+  if (a.nsums <= kClipInlineSums && a.nchunks <= kClipInlineChunks) {  // (far below the streaming loads' size)
     if (hipError_t e = launch_clip_sums(a, s); e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_clip_apply<false, false, true>), dim3(g.x + (a.ntensors - 1) / kClipStatsTensors + 1), b, 0,
-                       s, a);
+    const dim3 g((unsigned)(a.nchunks + (a.ntensors - 1) / kClipStatsTensors + 1));
+    if (a.stream_out)
+      hipLaunchKernelGGL((k_clip_apply<false, true, true>), g, b, 0, s, a);
+    else
+      hipLaunchKernelGGL((k_clip_apply<false, false, true>), g, b, 0, s, a);
     return hipGetLastError();
   }
   if (hipError_t e = launch_clip_norm(a, s); e != hipSuccess) return e;
-  if (a.nchunks == 0) return hipSuccess;
+  const dim3 g((unsigned)a.nchunks);
   if (a.stream_in)
     hipLaunchKernelGGL((k_clip_apply<true, true, false>), g, b, 0, s, a);
   else if (a.stream_out)

@@ -14,15 +14,19 @@ namespace psgd {
 // Elements that a workgroup handles at a time: 32 of each of its 256 threads.
 constexpr int kClipChunk = 8192;
 // Workgroups of the norm's pass over the whole list (and one more per tensor
-// at most): eight on each compute unit, twice.
-constexpr int kClipSumGroups = 4096;
+// at most): nearly four on each compute unit, each with 32 KB under way, are
+// enough for the memory, and their sums few (667e6 bf16 values: 876 us with the
+// writing pass, 885 with 4096 workgroups).
+constexpr int kClipSumGroups = 960;
 
 // Gradients and outputs of more bytes than this do not stay side by side in the
 // 256 MB last level of cache.
 constexpr int64_t kClipCacheBytes = int64_t(192) << 20;
 
-// Up to this many sums of squares the writing pass adds them by itself.
-constexpr int kClipInlineSums = 1024;
+// Up to this many sums of squares, and workgroups that read them all, the
+// writing pass adds them by itself.
+constexpr int kClipInlineSums = 2048;
+constexpr int kClipInlineChunks = 8192;
 constexpr int kClipStatsTensors = 8;  // tensors whose norms one of its workgroups then writes
 
 struct ClipTensor {

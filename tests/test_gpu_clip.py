@@ -164,8 +164,9 @@ def test_more_than_2_to_the_31_elements():
 
 
 def test_calls_before_and_without_bound_outputs():
-    for n in (5000, 12_000_000):  # both ways of adding the sums
-        g = [torch.full((n // 20,), 0.5, device=DEV) for _ in range(20 if n > 5000 else 1)]
+    # few sums, which the writing pass adds, and more than it (and LDS) takes
+    for count, size in ((1, 5000), (20, 600_000), (2100, 70)):
+        g = [torch.full((size,), 0.5, device=DEV) for _ in range(count)]
         o = [torch.full_like(t, 7.0) for t in g]
         h = B.psgd_clip_create([t.numel() for t in g], [B.PSGD_DTYPE_F32] * len(g), [B.PSGD_DTYPE_F32] * len(g))
         nbytes = B.psgd_clip_workspace(h)
