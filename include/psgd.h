@@ -560,7 +560,7 @@ psgd_status_t psgd_mx_dequantize(const uint8_t* codes, const uint8_t* scales, in
 psgd_status_t psgd_mx_product(int64_t m, int64_t n, int64_t k, const uint8_t* a_codes, const uint8_t* a_scales,
                               const uint8_t* b_codes, const uint8_t* b_scales, void* c, int32_t dtype, int64_t ldc,
                               int32_t accumulate, hipStream_t stream);
-psgd_status_t psgd_mx_linear_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
+psgd_status_t psgd_mx_linear_workspace(int64_t m, int64_t n, int64_t k, int32_t x_dtype, size_t* bytes);
 psgd_status_t psgd_mx_linear(int64_t m, int64_t n, int64_t k, const void* x, int32_t x_dtype, int64_t ldx,
                              const uint8_t* w_codes, const uint8_t* w_scales, void* y, int32_t y_dtype, int64_t ldy,
                              void* workspace, size_t workspace_bytes, hipStream_t stream);

@@ -163,7 +163,7 @@ lib.psgd_mx_sizes.argtypes = [_i64, _i64, _szp, _szp]
 lib.psgd_mx_quantize.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
 lib.psgd_mx_dequantize.argtypes = [_vp, _vp, _i64, _i64, _vp, _i32, _i64, _vp]
 lib.psgd_mx_product.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _vp]
-lib.psgd_mx_linear_workspace.argtypes = [_i64, _i64, _i64, _szp]
+lib.psgd_mx_linear_workspace.argtypes = [_i64, _i64, _i64, _i32, _szp]
 lib.psgd_mx_linear.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _i64, _vp, _sz, _vp]
 lib.psgd_mx_train_workspace.argtypes = [_i64, _i64, _i64, _szp]
 lib.psgd_mx_train_forward.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i32,
@@ -361,9 +361,9 @@ def psgd_mx_product(m: int, n: int, k: int, a_codes: int, a_scales: int, b_codes
         _check("psgd_mx_product", st)
 
 
-def psgd_mx_linear_workspace(m: int, n: int, k: int) -> int:
+def psgd_mx_linear_workspace(m: int, n: int, k: int, x_dtype: int) -> int:
     b = _sz()
-    _check("psgd_mx_linear_workspace", lib.psgd_mx_linear_workspace(m, n, k, ctypes.byref(b)))
+    _check("psgd_mx_linear_workspace", lib.psgd_mx_linear_workspace(m, n, k, x_dtype, ctypes.byref(b)))
     return b.value
 
 

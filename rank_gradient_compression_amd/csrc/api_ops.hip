@@ -380,11 +380,12 @@ static MxQuantArgs quant_args(const void* x, int32_t dtype, int64_t rows, int64_
   return a;
 }
 
-extern "C" psgd_status_t psgd_mx_linear_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+extern "C" psgd_status_t psgd_mx_linear_workspace(int64_t m, int64_t n, int64_t k, int32_t x_dtype, size_t* bytes) {
   clear_error();
+  if (!known_dtype(x_dtype)) return invalid("psgd_mx_linear_workspace", "unknown element type");
   if (bad_dim(m) || bad_dim(n) || bad_dim(k) || !bytes)
     return invalid("psgd_mx_linear_workspace", "a size is negative or above INT32_MAX, or bytes is NULL");
-  *bytes = mx_linear_fuses(m, k) ? 0 : operand_bytes(m, k);
+  *bytes = mx_linear_fuses(m, n, k, x_dtype) ? 0 : operand_bytes(m, k);
   return PSGD_OK;
 }
 
@@ -398,7 +399,7 @@ extern "C" psgd_status_t psgd_mx_linear(int64_t m, int64_t n, int64_t k, const v
   if (overlap(x, strided_bytes(m, k, ldx, x_dtype), y, strided_bytes(m, n, ldy, y_dtype)))
     return invalid(fn, "y overlaps x");
   MxProductArgs p{m, n, k, {nullptr, nullptr}, {w_codes, w_scales}, y, y_dtype, m > 1 ? ldy : n, false};
-  if (mx_linear_fuses(m, k)) {
+  if (mx_linear_fuses(m, n, k, x_dtype)) {
     if (m == 0 || n == 0) return PSGD_OK;
     return launch_status(launch_mx_linear_fused(p, x, x_dtype, m > 1 ? ldx : k, stream), fn);
   }

@@ -448,8 +448,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
 // whole 128-byte rows: reading the matrix cores' layout (16 bytes of each of
 // many rows per access) from memory instead kept the cache's address lookup
 // busy and took 12 us where this takes 7.5 (24 x 4096 x 11008).
-// The narrow operand comes from memory (XDT < 0), or, for a few thousand
-// values, straight from the activations of type XDT, which every workgroup
+// The narrow operand comes from memory (XDT < 0), or, where it is small enough,
+// straight from the activations of type XDT, which every workgroup
 // quantises into LDS by itself: one launch instead of two, and the first
 // loads of the wide operand are already on their way meanwhile.
 // With 64 x 64 tiles the same kernel serves small products of any shape.
@@ -525,10 +525,9 @@ __device__ __forceinline__ uint32_t mx_quant_block(const typename Elem<DT>::type
   return sb;
 }
 
-// Activations that a workgroup quantises by itself: at most this many blocks,
-// four for each thread of a workgroup of 256.  (Every workgroup repeats the
-// work; from here on a launch of its own is cheaper.)
-constexpr int kFusedBlocks = 1024;
+// The operand of the activations that a workgroup quantises by itself: codes
+// and scales, in dynamic LDS (18 bytes per block).
+extern __shared__ __align__(16) uint8_t psgd_mx_act[];
 
 template <int WAVES, int MT, int NT, bool SWAP, int XDT>
 __global__ __launch_bounds__(WAVES * 64, 1) void k_mx_prod_skinny(MxSkinnyArgs p, int nwt) {
@@ -539,7 +538,6 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_mx_prod_skinny(MxSkinnyArgs p
   constexpr int TILES = MT * 2 * NT;  // 16 x 16 tiles of a wavefront, 1 KB each
   static_assert(TILES * 1024 <= 2 * STAGE, "no room for the partial tiles");
   __shared__ __align__(16) uint8_t st0[WAVES * STAGE], st1[WAVES * STAGE];
-  __shared__ __align__(16) uint8_t xc[STAGED ? 16 : kFusedBlocks * 16], xs[STAGED ? 16 : kFusedBlocks * 2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int64_t x0 = (int64_t)(blockIdx.x / nwt) * (MT * 16), w0 = (int64_t)(blockIdx.x % nwt) * (NT * 32);  // first rows
@@ -565,6 +563,7 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_mx_prod_skinny(MxSkinnyArgs p
   fetch(ch + WAVES, m1, sw1, sx1);
   __builtin_amdgcn_sched_barrier(0);
   const int xrows = STAGED ? 0 : (int)p.narrow, xr16 = min(xrows, 16), xper = (int)nch * 8;
+  uint8_t *const xc = psgd_mx_act, *const xs = xc + xrows * xper * 16;
   if constexpr (!STAGED) {
     constexpr int XD = XDT < 0 ? 0 : XDT;
     const auto* act = static_cast<const typename Elem<XD>::type*>(p.act);
@@ -665,13 +664,15 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_mx_prod_skinny(MxSkinnyArgs p
 template <int MT, int NT, bool SWAP, int XDT>
 static void skinny(const MxSkinnyArgs& p, hipStream_t s) {
   const int64_t nwt = (p.wide + NT * 32 - 1) / (NT * 32), tiles = nwt * ((p.narrow + MT * 16 - 1) / (MT * 16));
+  const uint32_t lds = XDT < 0 ? 0 : (uint32_t)(p.narrow * mx_chunks(p.k) * 8 * 18);
   if constexpr (MT <= 2 && NT == 1) {
     if (tiles <= 256 && mx_chunks(p.k) > 4) {
-      hipLaunchKernelGGL((k_mx_prod_skinny<8, MT, NT, SWAP, XDT>), dim3((unsigned)tiles), dim3(512), 0, s, p, (int)nwt);
+      hipLaunchKernelGGL((k_mx_prod_skinny<8, MT, NT, SWAP, XDT>), dim3((unsigned)tiles), dim3(512), lds, s, p,
+                         (int)nwt);
       return;
     }
   }
-  hipLaunchKernelGGL((k_mx_prod_skinny<4, MT, NT, SWAP, XDT>), dim3((unsigned)tiles), dim3(256), 0, s, p, (int)nwt);
+  hipLaunchKernelGGL((k_mx_prod_skinny<4, MT, NT, SWAP, XDT>), dim3((unsigned)tiles), dim3(256), lds, s, p, (int)nwt);
 }
 
 // SWAP: the narrow side is C's columns.
@@ -687,7 +688,17 @@ static void product_skinny(const MxSkinnyArgs& p, hipStream_t s) {
     skinny<8, 1, SWAP, -1>(p, s);
 }
 
-bool mx_linear_fuses(int64_t m, int64_t k) { return m <= 32 && k > 0 && m * mx_chunks(k) * 8 <= kFusedBlocks; }
+// Every workgroup (32 rows of the weights) repeats the activations' work, and
+// those of one compute unit share it.  What that may cost is what a launch of
+// its own takes, about 4 us; an fp32 block costs three of 16 bits, and more than
+// 3584 blocks would not leave LDS for the stages (two launches take 10.1 us.
+// 4096 rows of weights, bf16: 16 x 4096 6.6, 24 x 4096 7.9, 8 x 11008 10.1;
+// fp32: 8 x 4096 7.8, 12 x 4096 9.6, 4 x 11008 11.8.  11008 rows, bf16: 8 x 4096
+// 8.3, 12 x 4096 9.6, 16 x 4096 10.5; fp32: 4 x 4096 9.1, 8 x 4096 12.4).
+bool mx_linear_fuses(int64_t m, int64_t n, int64_t k, int x_dtype) {
+  const int64_t blocks = m * mx_chunks(k) * 8, per_cu = (n + 32 * 256 - 1) / (32 * 256);
+  return m <= 32 && k > 0 && blocks * (x_dtype == kF32 ? 3 : 1) * per_cu <= 3584;
+}
 
 template <int MT>
 static void linear_fused(const MxSkinnyArgs& a, int x_dtype, hipStream_t s) {

@@ -67,7 +67,7 @@ struct MxProductArgs {
 hipError_t launch_mx_product(const MxProductArgs& p, hipStream_t s);
 // y = Q(x) B^T in one launch, for so few activations that every workgroup
 // quantises them by itself (mx_linear_fuses); p.a is not read.
-bool mx_linear_fuses(int64_t m, int64_t k);
+bool mx_linear_fuses(int64_t m, int64_t n, int64_t k, int x_dtype);
 hipError_t launch_mx_linear_fused(const MxProductArgs& p, const void* x, int x_dtype, int64_t ldx, hipStream_t s);
 
 }  // namespace psgd

@@ -44,8 +44,8 @@ def _call(device: torch.device, fn, *args) -> None:
 
 
 @functools.lru_cache(maxsize=4096)
-def _linear_workspace(m: int, n: int, k: int) -> int:
-    return B.psgd_mx_linear_workspace(m, n, k)
+def _linear_workspace(m: int, n: int, k: int, x_dtype: int) -> int:
+    return B.psgd_mx_linear_workspace(m, n, k, x_dtype)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -285,10 +285,11 @@ def mx_linear(x: torch.Tensor, w: MxTensor, out: Optional[torch.Tensor] = None,
     n, device = w.rows, x.device
     if k != w.cols or device != w.device:
         raise ValueError(f"x has {k} columns on {device}, the weights {w.cols} on {w.device}")
+    x_dtype = _dtype(x)
     y, ldy = _result(out, m, n, dtype or x.dtype, device)
-    need = _linear_workspace(m, n, k)
+    need = _linear_workspace(m, n, k, x_dtype)
     ws, ws_ptr = _scratch(need, device)
-    _call(device, B.psgd_mx_linear, m, n, k, x.data_ptr(), _dtype(x), ldx, w.codes_ptr, w.scales_ptr, y.data_ptr(),
+    _call(device, B.psgd_mx_linear, m, n, k, x.data_ptr(), x_dtype, ldx, w.codes_ptr, w.scales_ptr, y.data_ptr(),
           _dtype(y), ldy, ws_ptr, need)
     return y
 

@@ -239,7 +239,7 @@ def test_padding_is_never_read_as_data():
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 500, 4096), (3, 77, 650), (4, 100, 8000), (16, 64, 300), (24, 96, 1100), (40, 64, 333),
-                                   (300, 200, 650), (7, 1, 32)])
+                                   (300, 200, 650), (7, 1, 32), (32, 40, 2500), (28, 33, 4000), (9, 8300, 2600)])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
 def test_linear(m, n, k, dtype):
     x, w = matrix(m, k, dtype, seed=8), matrix(n, k, dtype, seed=9)

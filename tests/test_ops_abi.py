@@ -29,9 +29,10 @@ def test_sizes_refused():
     refused(B.psgd_mx_sizes, -1, 4)
     refused(B.psgd_mx_sizes, 4, BIG)
     assert B.lib.psgd_mx_sizes(1, 1, None, None) == B.PSGD_ERR_INVALID_ARG
-    for fn in (B.psgd_mx_linear_workspace, B.psgd_mx_train_workspace):
-        refused(fn, -1, 4, 4)
-        refused(fn, 4, 4, BIG)
+    for fn, more in ((B.psgd_mx_linear_workspace, (F32,)), (B.psgd_mx_train_workspace, ())):
+        refused(fn, -1, 4, 4, *more)
+        refused(fn, 4, 4, BIG, *more)
+    refused(B.psgd_mx_linear_workspace, 4, 4, 4, 3, match="type")
 
 
 def quant(x=P, dtype=F32, rows=4, cols=64, ld=64, rand=0, rc=1 << 20, rs=2 << 20, cc=0, cs=0, values=0, ldv=0):
@@ -88,7 +89,7 @@ def test_product_refused():
 
 def test_linear_refused():
     m, n, k = 64, 96, 512  # too many activations for one launch: a workspace is needed
-    need = B.psgd_mx_linear_workspace(m, n, k)
+    need = B.psgd_mx_linear_workspace(m, n, k, BF16)
     assert need >= sum(B.psgd_mx_sizes(m, k))
     ok = [m, n, k, 1 << 24, BF16, k, 1 << 20, 2 << 20, 1 << 25, BF16, n, 1 << 26, need]
     for at, bad, match in [(3, 0, "NULL"), (4, 4, "type"), (5, k - 1, "stride"), (6, 0, "NULL"), (8, 0, "NULL"),
