@@ -114,12 +114,15 @@ class GradientClip:
                 raise ValueError(f"an output of {o.numel()} elements for a gradient of {g.numel()}")
 
     def _bind(self, grads, outs) -> None:
-        self.grads, self.outs = grads, outs  # kept alive: the workspace holds their addresses
         B.psgd_clip_bind(self.handle, [g.data_ptr() for g in grads], [o.data_ptr() for o in outs],
                          self.workspace.data_ptr(), self.ws_bytes, _stream(self.device))
+        # Kept alive: the workspace holds their addresses.  After the call, since
+        # a refused one leaves the old addresses there.
+        self.grads, self.outs = grads, outs
 
     def bind(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None) -> None:
-        """New tensors of the same sizes and types (psgd_clip_bind)."""
+        """New tensors of the same sizes and types (psgd_clip_bind).  Where it
+        raises, the handle keeps the tensors that it had."""
         grads = list(grads)
         outs = grads if outs is None else list(outs)
         self._check(grads, outs)

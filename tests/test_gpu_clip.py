@@ -6,6 +6,9 @@ the coefficient's rounding, the product's and the output type's own: 2^-22 in
 fp32, 2^-8 + 2^-22 in bfloat16, 2^-11 + 2^-22 in float16, of its own size, or
 half the type's smallest step.
 """
+import gc
+import weakref
+
 import numpy as np
 import pytest
 
@@ -226,3 +229,19 @@ def test_another_stream_and_graph_replays():
         replayed = [o.clone() for o in outs] + [stats.clone()]
         eager = c.clip(0.2)
         assert all(torch.equal(a, b) for a, b in zip(replayed, outs + [eager]))
+
+
+def test_refused_bind_keeps_the_binding():
+    sizes = [3000, 500]
+    gs = grads(sizes, [F32, F32])
+    outs = [torch.empty_like(g) for g in gs]
+    before, refs = [f64(g) for g in gs], [weakref.ref(t) for t in (*gs, *outs)]
+    c = T.GradientClip(gs, outs)
+    others = grads(sizes, [F32, F32], seed=8)
+    for bad in ([others[0], others[0][:500]], [others[1].new_empty(3000), others[0][:500]]):
+        with pytest.raises(B.PsgdError, match="overlap"):
+            c.bind(others, bad)
+    del gs, outs
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    check(None, c.clip(0.1), [r() for r in refs[2:]], 0.1, before=before)

@@ -197,3 +197,22 @@ def test_null_handles():
     assert B.lib.psgd_clip_workspace(None, None) == B.PSGD_ERR_INVALID_ARG
     refused(B.psgd_clip_norm, None, 1.0, 1.0, P, 1 << 26, 1 << 20)
     B.psgd_clip_destroy(None)
+
+
+def test_refused_bind_keeps_the_old_tensors_alive(monkeypatch):
+    """The device table keeps the old addresses when psgd_clip_bind refuses, so
+    the handle has to keep the tensors behind them."""
+    torch = pytest.importorskip("torch")
+    ops = pytest.importorskip("rank_gradient_compression_amd.torch_ops")
+    monkeypatch.setattr(ops, "_stream", lambda device: 0)
+    c = ops.GradientClip.__new__(ops.GradientClip)  # no device: the refusal comes before any device call
+    c.handle = B.psgd_clip_create([8, 8], [F32, F32], [F32, F32])
+    c.device, c.ws_bytes = torch.device("cuda", 0), B.psgd_clip_workspace(c.handle)
+    buf = torch.empty(c.ws_bytes + 256, dtype=torch.uint8)
+    c.workspace = buf[-buf.data_ptr() % 256:]
+    old = c.grads = c.outs = [torch.zeros(8), torch.zeros(8)]
+    new, out = [torch.zeros(8), torch.zeros(8)], torch.zeros(8)
+    with pytest.raises(B.PsgdError, match="two outputs overlap"):
+        c._bind(new, [out, out])
+    assert c.grads is old and c.outs is old
+    c.close()
