@@ -445,8 +445,9 @@ psgd_status_t psgd_subspace_overlap(psgd_plan_t plan, const float* q_a, const fl
  *
  * stats receives 2 + ntensors floats on the device: N, c, then every n_t.  A
  * NaN in a gradient makes N, c and every output NaN; an infinity makes N
- * infinite and c zero (finite values become zero, infinite ones NaN): the
- * caller that skips such a step looks at N.
+ * infinite and c zero (finite values become zero, infinite ones NaN), or 1
+ * where max_norm is infinite too (nothing is clipped): the caller that skips
+ * such a step looks at N.
  *
  * psgd_clip_create       host only.  ntensors >= 0 tensors of numel[t] >= 0
  *                        elements (0: an empty tensor, norm 0), of type

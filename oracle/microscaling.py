@@ -108,6 +108,6 @@ def clip(grads, max_norm: float, scale: float = 1.0):
         sq = [float(np.sum((np.asarray(g, np.float64) * scale) ** 2)) for g in grads]
         norm = math.sqrt(sum(sq)) if not any(math.isnan(s) for s in sq) else math.nan
         c = max_norm / (norm + 1e-6)
-        coef = c if (math.isnan(c) or c < 1.0) else 1.0
+        coef = math.nan if math.isnan(norm) else (c if c < 1.0 else 1.0)  # 1 for inf / inf: nothing is clipped
         outs = [np.asarray(g, np.float64) * scale * coef for g in grads]
     return norm, coef, [math.sqrt(s) for s in sq], outs

@@ -115,7 +115,8 @@ __device__ __forceinline__ void total_of_sums(int n, Load load, double (&w)[4]) 
 __device__ __forceinline__ float2 norm_and_coefficient(const ClipArgs& a, const double (&w)[4]) {
   const double norm = sqrt((w[0] + w[1]) + (w[2] + w[3])) * fabs((double)a.scale);
   const double c = (double)a.max_norm / (norm + 1e-6);
-  return make_float2((float)norm, c < 1.0 || c != c ? (float)c : 1.f);  // NaN stays NaN
+  // (an infinite max_norm clips nothing, an infinite norm included: the quotient is NaN there)
+  return make_float2((float)norm, norm != norm ? (float)norm : c < 1.0 ? (float)c : 1.f);
 }
 
 // The norms of tensors first, first + step, ... below end, by one wavefront:

@@ -245,3 +245,20 @@ def test_refused_bind_keeps_the_binding():
     gc.collect()
     assert all(r() is not None for r in refs)
     check(None, c.clip(0.1), [r() for r in refs[2:]], 0.1, before=before)
+
+
+@pytest.mark.parametrize("count", [1, 2100])  # sums added by the writing pass, and by a launch of their own
+def test_infinite_limit_clips_nothing(count):
+    gs = grads([700] * count, [F32] * count)
+    gs[-1][5], gs[0][6] = float("inf"), float("-inf")
+    outs = [torch.empty_like(g) for g in gs]
+    c = T.GradientClip(gs, outs)
+    for stats in (c.clip(float("inf")), c.norm()):
+        s = f64(stats)
+        assert np.isinf(s[0]) and s[1] == 1.0 and np.isinf(s[[2, -1]]).all() and np.isfinite(s[3:-1]).all()
+    assert all(torch.equal(o, g) for o, g in zip(outs, gs))
+    gs[0][7] = float("nan")
+    for stats in (c.clip(float("inf")), c.norm()):
+        s = f64(stats)
+        assert np.isnan(s[:3]).all()
+    assert all(bool(o.isnan().all()) for o in outs)

@@ -103,3 +103,10 @@ def test_planted_mistakes_fail_a_pin():
     # swapped nibbles
     c, _ = MX.quantize(x)
     assert not np.array_equal((c[:, 1::2] | (c[:, 0::2] << 4)), MX.pack_codes(c))
+
+
+def test_infinite_limit_clips_nothing():
+    norm, c, _, outs = MX.clip([np.array([np.inf, 2.0])], math.inf)
+    assert norm == math.inf and c == 1.0 and outs[0].tolist() == [math.inf, 2.0]
+    assert MX.clip([np.array([3.0])], math.inf)[1] == 1.0
+    assert math.isnan(MX.clip([np.array([np.nan, np.inf])], math.inf)[1])
