@@ -403,7 +403,11 @@ extern "C" psgd_status_t psgd_mx_linear(int64_t m, int64_t n, int64_t k, const v
     if (m == 0 || n == 0) return PSGD_OK;
     return launch_status(launch_mx_linear_fused(p, x, x_dtype, m > 1 ? ldx : k, stream), fn);
   }
-  if (psgd_status_t s = check_workspace(fn, operand_bytes(m, k), ws, bytes)) return s;
+  const size_t need = operand_bytes(m, k);
+  if (psgd_status_t s = check_workspace(fn, need, ws, bytes)) return s;
+  if (overlap(ws, need, x, strided_bytes(m, k, ldx, x_dtype)) || overlap(ws, need, y, strided_bytes(m, n, ldy, y_dtype)) ||
+      overlap(ws, need, w_codes, (size_t)(n * mx_pitch(k))) || overlap(ws, need, w_scales, (size_t)mx_scale_bytes(n, k)))
+    return invalid(fn, "the workspace overlaps another buffer");
   if (m == 0 || n == 0) return PSGD_OK;
   const WsOperand q = ws_operand(ws, 0, m, k);
   MxQuantArgs a = quant_args(x, x_dtype, m, k, ldx);

@@ -216,3 +216,17 @@ def test_refused_bind_keeps_the_old_tensors_alive(monkeypatch):
         c._bind(new, [out, out])
     assert c.grads is old and c.outs is old
     c.close()
+
+
+def test_linear_workspace_over_a_buffer_is_refused():
+    m, n, k = 64, 96, 512
+    need = B.psgd_mx_linear_workspace(m, n, k, BF16)
+    x, codes, scales, y, ws = 1 << 24, 1 << 20, 2 << 20, 1 << 25, 1 << 26
+    args = lambda w, f=need: (m, n, k, x, BF16, k, codes, scales, y, BF16, n, w, f)  # noqa: E731
+    for other, size in ((x, 2 * m * k), (y, 2 * m * n), (codes, n * k // 2), (scales, n * k // 32)):
+        assert size % 256 == 0
+        for at in (other, other + size - 256, other - need + 256):
+            refused(B.psgd_mx_linear, *args(at), match="workspace overlaps")
+    # few activations need none: what is passed is not looked at
+    assert B.psgd_mx_linear_workspace(0, n, k, BF16) == 0
+    B.psgd_mx_linear(0, n, k, 0, BF16, k, codes, scales, 0, BF16, n, codes, need)
