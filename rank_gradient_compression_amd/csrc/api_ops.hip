@@ -287,6 +287,8 @@ extern "C" psgd_status_t psgd_mx_quantize(const void* x, int32_t dtype, int64_t 
     const bool in_place = values == x && (ldv == ld || rows == 1);
     if (!in_place && overlap(x, xb, values, strided_bytes(rows, cols, ldv, dtype)))
       return invalid(fn, "values overlaps x without being x in place");
+    if (rand && overlap(rand, (size_t)(rows * cols), values, strided_bytes(rows, cols, ldv, dtype)))
+      return invalid(fn, "values overlaps rand");
   }
   const void* outs[] = {row_codes, row_scales, col_codes, col_scales};
   const size_t sizes[] = {(size_t)(rows * mx_pitch(cols)), (size_t)mx_scale_bytes(rows, cols),

@@ -230,3 +230,10 @@ def test_linear_workspace_over_a_buffer_is_refused():
     # few activations need none: what is passed is not looked at
     assert B.psgd_mx_linear_workspace(0, n, k, BF16) == 0
     B.psgd_mx_linear(0, n, k, 0, BF16, k, codes, scales, 0, BF16, n, codes, need)
+
+
+@pytest.mark.parametrize("at", [0, 4 * 64 - 1, 4 - 4 * 4 * 64])
+def test_quantize_values_over_the_random_bytes_are_refused(at):
+    with pytest.raises(B.PsgdError, match="values overlaps rand") as e:
+        quant(rand=1 << 22, values=((1 << 22) + at) // 4 * 4, ldv=64)
+    assert e.value.status == B.PSGD_ERR_INVALID_ARG
