@@ -510,8 +510,9 @@ psgd_status_t psgd_clip_apply(psgd_clip_t clip, float max_norm, float scale, flo
  *   scales  tiles of 32 rows x 256 columns, 256 bytes each, the tiles of one
  *           row of tiles after each other: the scale of row i, block b is byte
  *           ((i / 32) * ceil(cols / 256) + b / 8) * 256 + (b % 8 / 2) * 64
- *           + (i % 16) * 4 + (i % 32 / 16) * 2 + b % 2.  Bytes of blocks past the last column are
- *           zero; bytes of rows past the last row are not read for results.
+ *           + (i % 16) * 4 + (i % 32 / 16) * 2 + b % 2.  Bytes of blocks past
+ *           the last column and of rows past the last row are written as
+ *           zero; the latter are not read for results.
  *
  * psgd_mx_quantize -- x: rows x cols values of type `dtype`, row stride ld
  * elements.  rand: NULL rounds to nearest, ties to the even code; else rows x

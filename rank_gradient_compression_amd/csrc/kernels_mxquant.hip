@@ -139,7 +139,8 @@ __device__ __forceinline__ void quant_rows_tile(const MxQuantArgs& a, int nch, u
     const uint32_t sb = mx_scale_byte(group_max<4>(mx_max_bits<DT>(am)));
     const uint32_t code = mx_encode8<DT, RAND>(v, sb, rnd);
     const int blk = (int)(col >> 5);
-    if ((threadIdx.x & 3) == 0) tb[mx_scale_in_tile(r, blk & 7)] = (uint8_t)sb;
+    // (a row past the last holds the last one's values, which in place another wavefront may have rounded already)
+    if ((threadIdx.x & 3) == 0) tb[mx_scale_in_tile(r, blk & 7)] = r < nrows ? (uint8_t)sb : 0;
     if (r < nrows && (R == FULL || blk < nblk)) {
       if (a.row_codes) *reinterpret_cast<uint32_t*>(a.row_codes + (row0 + r) * (nblk * 16) + (col >> 1)) = code;
       if constexpr (VALUES) {

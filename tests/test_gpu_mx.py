@@ -444,3 +444,23 @@ def test_offsets_beyond_32_bits():
     c = T.mx_product(a, b)
     last = T.mx_product(T.mx_quantize(xa[-50:].contiguous()), b)
     assert torch.equal(c[-50:], last)
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 300), (33, 257), (70, 5), (9, 650)])
+def test_equal_inputs_give_equal_bytes_in_place(rows, cols):
+    """The whole operand, the scale bytes of rows past the last included."""
+    say(f"[mx] bytes in place {rows}x{cols}")
+    past = np.ones(-(-rows // 32) * -(-cols // 256) * 256, bool)
+    for i in range(rows):
+        for b in range(-(-cols // 32)):
+            past[MX.scale_index(i, b, cols)] = False
+    for dtype in (F32, BF16, F16):
+        x = matrix(rows, cols, dtype, seed=31)
+        r = rand_bytes(rows, cols)
+        want = T.mx_quantize(x, rand=r)
+        both, _ = T.mx_quantize_both(x, rand=r)
+        v = x.clone()
+        got = T.mx_quantize(v, rand=r, values=v)
+        for q in (want, both, got):
+            assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
+            assert not q.scales.cpu().numpy()[past].any(), "scale bytes of rows past the last"
