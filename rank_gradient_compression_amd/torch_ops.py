@@ -6,6 +6,7 @@ computation runs in libpsgd.so, on the current stream of the tensors' device.
 from __future__ import annotations
 
 import functools
+import math
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -350,18 +351,27 @@ def mx_linear_backward(dy: torch.Tensor, saved, rand: Optional[torch.Tensor] = N
     return dx, dw
 
 
+def _as_matrix(x: torch.Tensor) -> torch.Tensor:
+    """x as a matrix with x's last axis as rows that the library reads: as it is
+    where rows are contiguous and apart, else copied (transposed, every other
+    column, expanded)."""
+    m = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])  # (no -1: an axis may be empty)
+    rows, cols = m.shape
+    apart = rows <= 1 or m.stride(0) >= cols
+    return m if apart and (cols <= 1 or m.stride(1) == 1) else m.contiguous()
+
+
 class _MxLinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, stochastic, generator):
-        flat = x.reshape(-1, x.shape[-1])
-        y, ctx.saved = mx_linear_forward(flat, w)
+        y, ctx.saved = mx_linear_forward(_as_matrix(x), _as_matrix(w))
         ctx.x_shape, ctx.w_dtype, ctx.stochastic, ctx.generator = x.shape, w.dtype, stochastic, generator
         return y.view(*x.shape[:-1], w.shape[0])
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        flat = dy.reshape(-1, dy.shape[-1]).contiguous()
+        flat = _as_matrix(dy).contiguous()
         rand = None
         if ctx.stochastic:
             rand = torch.randint(0, 256, flat.shape, dtype=torch.uint8, device=flat.device, generator=ctx.generator)
@@ -371,7 +381,7 @@ class _MxLinearFunction(torch.autograd.Function):
 
 
 def mx_linear_train(x: torch.Tensor, w: torch.Tensor, stochastic: bool = True, generator=None) -> torch.Tensor:
-    """The layer under autograd: x of any leading shape, w out x in.  With
-    `stochastic` the incoming gradient is rounded with random bytes of
+    """The layer under autograd: x of any leading shape, w out x in, any strides
+    (copied where their rows are not contiguous).  With `stochastic` the incoming gradient is rounded with random bytes of
     `generator` (None: the device's default one)."""
     return _MxLinearFunction.apply(x, w, stochastic, generator)

@@ -464,3 +464,27 @@ def test_equal_inputs_give_equal_bytes_in_place(rows, cols):
         for q in (want, both, got):
             assert torch.equal(q.codes, want.codes) and torch.equal(q.scales, want.scales)
             assert not q.scales.cpu().numpy()[past].any(), "scale bytes of rows past the last"
+
+
+def test_autograd_layer_of_strided_activations_and_weights():
+    m, k, n = 40, 96, 50
+    base, wb = matrix(m, k, BF16, 1), matrix(n, k, BF16, 2)
+    wide, tall = torch.zeros(m, 2 * k, dtype=BF16, device=DEV), torch.zeros(n, 2 * k, dtype=BF16, device=DEV)
+    wide[:, ::2], tall[:, ::2] = base, wb
+    one = base[:1]
+    dy = matrix(n, m, BF16, 3).t()
+    for x, w in ((base.t().contiguous().t(), wb), (base, wb.t().contiguous().t()), (wide[:, ::2], tall[:, ::2]),
+                 (one.expand(m, k), wb)):
+        plain, wp = x.clone(memory_format=torch.contiguous_format), w.clone(memory_format=torch.contiguous_format)
+        x, w = x.detach().requires_grad_(True), w.detach().requires_grad_(True)
+        y = T.mx_linear_train(x, w, stochastic=False)
+        dx, dw = torch.autograd.grad(y, (x, w), dy)
+        want, saved = T.mx_linear_forward(plain, wp)
+        dx1, dw1 = T.mx_linear_backward(dy.contiguous(), saved)
+        assert torch.equal(y.detach(), want) and torch.equal(dx, dx1) and torch.equal(dw, dw1.to(BF16))
+    for shape, wshape in (((3, 0, 64), (50, 64)), ((3, 2, 0), (50, 0)), ((3, 2, 64), (0, 64))):
+        x, w = torch.ones(shape, device=DEV, requires_grad=True), torch.ones(wshape, device=DEV, requires_grad=True)
+        y = T.mx_linear_train(x, w, stochastic=False)
+        assert y.shape == (*shape[:-1], wshape[0]) and not bool(y.any())
+        y.sum().backward()
+        assert x.grad.shape == shape and w.grad.shape == wshape and not bool(x.grad.any()) and not bool(w.grad.any())

@@ -237,3 +237,42 @@ def test_quantize_values_over_the_random_bytes_are_refused(at):
     with pytest.raises(B.PsgdError, match="values overlaps rand") as e:
         quant(rand=1 << 22, values=((1 << 22) + at) // 4 * 4, ldv=64)
     assert e.value.status == B.PSGD_ERR_INVALID_ARG
+
+
+def strided_layers(torch):
+    """(x, w): activations and weights whose rows are not contiguous, or empty."""
+    g = torch.Generator().manual_seed(3)
+    z = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    yield z(64, 40).t(), z(50, 64)
+    yield z(40, 64), z(64, 50).t()
+    yield z(40, 128)[:, ::2], z(50, 128)[:, ::2]
+    yield z(1, 64).expand(40, 64), z(64).expand(50, 64)
+    yield z(6, 64, 7).transpose(1, 2), z(50, 64)
+    yield z(64), z(50, 64)
+    yield z(3, 0, 64), z(50, 64)
+    yield z(3, 2, 0), z(50, 0)
+    yield z(3, 2, 64), z(0, 64)
+
+
+def test_autograd_layer_takes_any_strides(monkeypatch):
+    """What reaches the library are matrices with contiguous, separate rows
+    (the calls themselves stood in for by fp32 products)."""
+    torch = pytest.importorskip("torch")
+    ops = pytest.importorskip("rank_gradient_compression_amd.torch_ops")
+
+    def readable(m):
+        rows, cols = m.shape
+        assert (cols <= 1 or m.stride(1) == 1) and (rows <= 1 or m.stride(0) >= cols)
+        return m
+
+    monkeypatch.setattr(ops, "mx_linear_forward", lambda x, w: (readable(x) @ readable(w).t(), (x, w)))
+    monkeypatch.setattr(ops, "mx_linear_backward", lambda dy, saved, rand=None, need_dx=True, need_dw=True: (
+        readable(dy) @ saved[1], dy.t() @ saved[0]))
+    for x, w in strided_layers(torch):
+        x, w = x.requires_grad_(True), w.requires_grad_(True)
+        y = ops.mx_linear_train(x, w, stochastic=False)
+        want = x.detach() @ w.detach().t()
+        assert y.shape == want.shape and torch.allclose(y, want, atol=1e-5)
+        got = torch.autograd.grad(y.sum() * 2, (x, w))
+        assert got[0].shape == x.shape and got[1].shape == w.shape
+        assert torch.allclose(got[0], 2 * w.detach().sum(0).expand(x.shape), atol=1e-4)
