@@ -168,13 +168,15 @@ class MxTensor:
 
     __slots__ = ("rows", "cols", "buf", "device", "codes_ptr", "scales_ptr")
 
-    def __init__(self, rows: int, cols: int, device):
+    def __init__(self, rows: int, cols: int, device, buf: Optional[torch.Tensor] = None):
         """Uninitialised operand: one allocation, the scales behind the codes
-        at a multiple of 256 bytes."""
+        at a multiple of 256 bytes.  buf: the buffer of an operand of this size
+        instead."""
         off = (rows * ((cols + 31) >> 5) * 16 + 255) & ~255
         self.rows, self.cols = rows, cols
-        self.buf = buf = torch.empty(off + ((rows + 31) >> 5) * ((cols + 255) >> 8) * 256, dtype=torch.uint8,
-                                     device=device)
+        if buf is None:
+            buf = torch.empty(off + ((rows + 31) >> 5) * ((cols + 255) >> 8) * 256, dtype=torch.uint8, device=device)
+        self.buf = buf
         self.device = buf.device
         self.codes_ptr = ptr = buf.data_ptr()
         self.scales_ptr = ptr + off
@@ -364,7 +366,9 @@ def _as_matrix(x: torch.Tensor) -> torch.Tensor:
 class _MxLinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, stochastic, generator):
-        y, ctx.saved = mx_linear_forward(_as_matrix(x), _as_matrix(w))
+        y, (xt, wt) = mx_linear_forward(_as_matrix(x), _as_matrix(w))
+        ctx.save_for_backward(xt.buf, wt.buf)  # (as tensors, which autograd lets go of behind the backward pass)
+        ctx.sizes = (xt.shape, wt.shape)
         ctx.x_shape, ctx.w_dtype, ctx.stochastic, ctx.generator = x.shape, w.dtype, stochastic, generator
         return y.view(*x.shape[:-1], w.shape[0])
 
@@ -376,7 +380,8 @@ class _MxLinearFunction(torch.autograd.Function):
         if ctx.stochastic:
             rand = torch.randint(0, 256, flat.shape, dtype=torch.uint8, device=flat.device, generator=ctx.generator)
         need_dx, need_dw = ctx.needs_input_grad[:2]
-        dx, dw = mx_linear_backward(flat, ctx.saved, rand, need_dx=need_dx, need_dw=need_dw)
+        saved = tuple(MxTensor(*size, buf.device, buf) for size, buf in zip(ctx.sizes, ctx.saved_tensors))
+        dx, dw = mx_linear_backward(flat, saved, rand, need_dx=need_dx, need_dw=need_dw)
         return dx.view(ctx.x_shape) if need_dx else None, dw.to(ctx.w_dtype) if need_dw else None, None, None
 
 

@@ -488,3 +488,23 @@ def test_autograd_layer_of_strided_activations_and_weights():
         assert y.shape == (*shape[:-1], wshape[0]) and not bool(y.any())
         y.sum().backward()
         assert x.grad.shape == shape and w.grad.shape == wshape and not bool(x.grad.any()) and not bool(w.grad.any())
+
+
+def test_autograd_layer_lets_go_of_its_operands():
+    x, w = matrix(2048, 1024, BF16, 1).requires_grad_(True), matrix(512, 1024, BF16, 2).requires_grad_(True)
+    dy = matrix(2048, 512, BF16, 3)
+    T.mx_linear_train(x, w, stochastic=False).backward(dy)
+    dx, dw = x.grad.clone(), w.grad.clone()
+    x.grad = w.grad = None
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    y = T.mx_linear_train(x, w, stochastic=False)
+    operands = sum(B.psgd_mx_sizes(1024, 2048)) + sum(B.psgd_mx_sizes(1024, 512))
+    assert torch.cuda.memory_allocated() - before >= operands + y.numel() * 2
+    y.backward(dy)
+    x_dx, w_dw, x.grad, w.grad = x.grad, w.grad, None, None
+    assert torch.equal(x_dx, dx) and torch.equal(w_dw, dw)
+    del x_dx, w_dw
+    assert torch.cuda.memory_allocated() - before <= y.numel() * 2 + 4096
+    with pytest.raises(RuntimeError, match="second time"):
+        y.backward(dy)

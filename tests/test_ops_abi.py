@@ -1,6 +1,9 @@
 """Host-side refusals and sizes of the clip and of the microscaled operands:
 every error returns before any device call, so these run without a GPU."""
 import ctypes
+import gc
+import weakref
+from types import SimpleNamespace
 
 import pytest
 
@@ -265,9 +268,10 @@ def test_autograd_layer_takes_any_strides(monkeypatch):
         assert (cols <= 1 or m.stride(1) == 1) and (rows <= 1 or m.stride(0) >= cols)
         return m
 
-    monkeypatch.setattr(ops, "mx_linear_forward", lambda x, w: (readable(x) @ readable(w).t(), (x, w)))
+    operand = lambda x: SimpleNamespace(buf=readable(x).clone(), shape=tuple(x.shape))  # noqa: E731
+    monkeypatch.setattr(ops, "mx_linear_forward", lambda x, w: (x @ w.t(), (operand(x), operand(w))))
     monkeypatch.setattr(ops, "mx_linear_backward", lambda dy, saved, rand=None, need_dx=True, need_dw=True: (
-        readable(dy) @ saved[1], dy.t() @ saved[0]))
+        readable(dy) @ saved[1].buf, dy.t() @ saved[0].buf))
     for x, w in strided_layers(torch):
         x, w = x.requires_grad_(True), w.requires_grad_(True)
         y = ops.mx_linear_train(x, w, stochastic=False)
@@ -276,3 +280,28 @@ def test_autograd_layer_takes_any_strides(monkeypatch):
         got = torch.autograd.grad(y.sum() * 2, (x, w))
         assert got[0].shape == x.shape and got[1].shape == w.shape
         assert torch.allclose(got[0], 2 * w.detach().sum(0).expand(x.shape), atol=1e-4)
+
+
+def test_autograd_layer_lets_go_of_its_operands(monkeypatch):
+    """Behind the backward pass, while the result is still held, and not before."""
+    torch = pytest.importorskip("torch")
+    ops = pytest.importorskip("rank_gradient_compression_amd.torch_ops")
+    kept = []
+
+    def forward(x, w):
+        saved = [SimpleNamespace(buf=t.clone(), shape=tuple(t.shape)) for t in (x, w)]
+        kept.extend(weakref.ref(s.buf) for s in saved)
+        return x @ w.t(), tuple(saved)
+
+    monkeypatch.setattr(ops, "mx_linear_forward", forward)
+    monkeypatch.setattr(ops, "mx_linear_backward", lambda dy, saved, rand=None, need_dx=True, need_dw=True: (
+        dy @ saved[1].buf, dy.t() @ saved[0].buf))
+    x, w = torch.randn(4, 64, requires_grad=True), torch.randn(8, 64, requires_grad=True)
+    y = ops.mx_linear_train(x, w, stochastic=False)
+    y.sum().backward(retain_graph=True)
+    gc.collect()
+    assert all(r() is not None for r in kept)
+    y.sum().backward()
+    gc.collect()
+    assert all(r() is None for r in kept)
+    assert torch.equal(x.grad, 2 * w.detach().sum(0).expand(4, 64))
