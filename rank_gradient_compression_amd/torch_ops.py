@@ -86,6 +86,12 @@ class GradientClip:
            gradients for the compression; None clips in place
 
     The handle keeps the addresses; bind() replaces them when the tensors move.
+
+    A handle's calls share its workspace and take effect in the order in which
+    they are made: a call on another stream than the one before it waits for
+    that stream.  (Not while a graph is captured: there the caller orders the
+    replays.)  The gradients themselves are read and the outputs written on the
+    current stream, like any tensors.
     """
 
     def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
@@ -98,6 +104,7 @@ class GradientClip:
         self._in, self._out = [_dtype(g) for g in grads], [_dtype(o) for o in outs]
         self.handle = B.psgd_clip_create(self._numel, self._in, self._out)
         self.ws_bytes = B.psgd_clip_workspace(self.handle)
+        self._last = torch.cuda.current_stream(self.device)  # the stream of the last call
         with torch.cuda.device(self.device):
             self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
             B.psgd_clip_workspace_init(self.handle, self.workspace.data_ptr(), self.ws_bytes, _stream(self.device))
@@ -114,7 +121,23 @@ class GradientClip:
             if g.numel() != o.numel():
                 raise ValueError(f"an output of {o.numel()} elements for a gradient of {g.numel()}")
 
+    def _order(self) -> None:
+        """What follows on the current stream comes after the handle's last call."""
+        index = self.device.index
+        if _raw_stream is not None and _raw_stream(index) == self._last.cuda_stream:
+            return
+        stream = torch.cuda.current_stream(self.device)
+        if stream == self._last:
+            return
+        with torch.cuda.device(self.device):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        stream.wait_stream(self._last)
+        self.workspace.record_stream(stream)
+        self._last = stream
+
     def _bind(self, grads, outs) -> None:
+        self._order()
         B.psgd_clip_bind(self.handle, [g.data_ptr() for g in grads], [o.data_ptr() for o in outs],
                          self.workspace.data_ptr(), self.ws_bytes, _stream(self.device))
         # Kept alive: the workspace holds their addresses.  After the call, since
@@ -137,6 +160,7 @@ class GradientClip:
 
     def _run(self, fn, max_norm: float, scale: float) -> torch.Tensor:
         stats = torch.empty(2 + len(self._numel), dtype=torch.float32, device=self.device)
+        self._order()
         _call(self.device, fn, self.handle, max_norm, scale, stats.data_ptr(), self.workspace.data_ptr(),
               self.ws_bytes)
         return stats

@@ -262,3 +262,31 @@ def test_infinite_limit_clips_nothing(count):
         s = f64(stats)
         assert np.isnan(s[:3]).all()
     assert all(bool(o.isnan().all()) for o in outs)
+
+
+def test_calls_of_one_handle_on_several_streams():
+    """Construction, binding and clips in turn on two streams, the first of
+    them behind work that takes a while, without a host synchronisation."""
+    sizes = [30000, 7]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    sets = [grads(sizes, [F32, BF16], seed=i) for i in range(4)]
+    outs = [[torch.empty(n, device=DEV) for n in sizes] for _ in sets]
+    busy = torch.ones(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    stats = []
+    with torch.cuda.stream(a):
+        for _ in range(20):
+            torch.mm(busy, busy)
+        c = T.GradientClip(sets[0], outs[0])
+    with torch.cuda.stream(b):
+        stats.append(c.clip(0.1))
+    for i, s in ((1, a), (2, b), (3, a)):
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                torch.mm(busy, busy)
+            c.bind(sets[i], outs[i])
+        with torch.cuda.stream(b if s is a else a):
+            stats.append(c.clip(0.1))
+    torch.cuda.synchronize()
+    for g, o, s in zip(sets, outs, stats):
+        check(g, s, o, 0.1)

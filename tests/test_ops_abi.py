@@ -208,6 +208,7 @@ def test_refused_bind_keeps_the_old_tensors_alive(monkeypatch):
     torch = pytest.importorskip("torch")
     ops = pytest.importorskip("rank_gradient_compression_amd.torch_ops")
     monkeypatch.setattr(ops, "_stream", lambda device: 0)
+    monkeypatch.setattr(ops.GradientClip, "_order", lambda self: None, raising=False)
     c = ops.GradientClip.__new__(ops.GradientClip)  # no device: the refusal comes before any device call
     c.handle = B.psgd_clip_create([8, 8], [F32, F32], [F32, F32])
     c.device, c.ws_bytes = torch.device("cuda", 0), B.psgd_clip_workspace(c.handle)
@@ -305,3 +306,50 @@ def test_autograd_layer_lets_go_of_its_operands(monkeypatch):
     gc.collect()
     assert all(r() is None for r in kept)
     assert torch.equal(x.grad, 2 * w.detach().sum(0).expand(4, 64))
+
+
+def test_clip_calls_wait_for_the_stream_of_the_call_before(monkeypatch):
+    """On stand-ins for the streams: the waits that the calls of one handle ask
+    for, whose workspace one call writes and the next one reads."""
+    torch = pytest.importorskip("torch")
+    ops = pytest.importorskip("rank_gradient_compression_amd.torch_ops")
+    log, now, capturing = [], [None], [False]
+
+    class Stream:
+        def __init__(self, raw):
+            self.cuda_stream = raw
+
+        def wait_stream(self, other):
+            log.append(("wait", self.cuda_stream, other.cuda_stream))
+
+    class Device:
+        def __init__(self, device):
+            pass
+
+        __enter__ = __exit__ = lambda *a: None
+
+    workspace = SimpleNamespace(data_ptr=lambda: 256, record_stream=lambda s: log.append(("record", s.cuda_stream)))
+    c = ops.GradientClip.__new__(ops.GradientClip)
+    a, b = Stream(1), Stream(2)
+    now[0] = a
+    c.handle, c.device, c.workspace, c.ws_bytes, c._last = 0, torch.device("cuda", 0), workspace, 256, a
+    c._numel, c._in, c._out = [], [], []
+    monkeypatch.setattr(ops, "_raw_stream", lambda index: now[0].cuda_stream)
+    monkeypatch.setattr(ops.torch.cuda, "current_stream", lambda device=None: now[0])
+    monkeypatch.setattr(ops.torch.cuda, "device", Device)
+    monkeypatch.setattr(ops.torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    monkeypatch.setattr(ops.torch, "empty", lambda *n, **kw: SimpleNamespace(data_ptr=lambda: 4))
+    monkeypatch.setattr(ops, "_call", lambda device, fn, *args: log.append(("call", now[0].cuda_stream)))
+    monkeypatch.setattr(ops.B, "psgd_clip_bind", lambda *args: log.append(("bind", args[-1])))
+    c.clip(1.0)
+    now[0] = b
+    c.norm()
+    c.clip(1.0)
+    now[0] = a
+    c.bind([], [])
+    now[0], capturing[0] = b, True
+    c.clip(1.0)
+    capturing[0] = False
+    c.clip(1.0)
+    to_b, to_a = [("wait", 2, 1), ("record", 2)], [("wait", 1, 2), ("record", 1)]
+    assert log == [("call", 1), *to_b, ("call", 2), ("call", 2), *to_a, ("bind", 1), ("call", 2), *to_b, ("call", 2)]
