@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import functools
 import math
+import warnings
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -310,7 +311,12 @@ def mx_product(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dty
 def mx_linear(x: torch.Tensor, w: MxTensor, out: Optional[torch.Tensor] = None,
               dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """y = Q(x) w^T for weights that were quantised once (psgd_mx_linear); y
-    has x's type unless dtype or out says otherwise."""
+    has x's type unless dtype or out says otherwise.  For serving: no gradient
+    flows through it (mx_linear_train has one), and an x that asks for one
+    draws a warning."""
+    if x.requires_grad and torch.is_grad_enabled():
+        warnings.warn("mx_linear gives x no gradient: use mx_linear_train, or torch.no_grad() if none is wanted",
+                      stacklevel=2)
     m, k, ldx = _matrix(x, "x")
     n, device = w.rows, x.device
     if k != w.cols or device != w.device:

@@ -8,6 +8,8 @@ fp32, at most 64 to a matrix-core step, so an entry's error is at most
 rounding: 2^-8 (bfloat16) or 2^-11 (float16) of the entry, at least the type's
 smallest step.
 """
+import warnings
+
 import numpy as np
 import pytest
 
@@ -508,3 +510,16 @@ def test_autograd_layer_lets_go_of_its_operands():
     assert torch.cuda.memory_allocated() - before <= y.numel() * 2 + 4096
     with pytest.raises(RuntimeError, match="second time"):
         y.backward(dy)
+
+
+def test_linear_warns_where_a_gradient_would_be_lost():
+    x, w = matrix(4, 64, BF16, 1), T.mx_quantize(matrix(8, 64, BF16, 2))
+    want = T.mx_linear(x, w)
+    with pytest.warns(UserWarning, match="mx_linear_train"):
+        y = T.mx_linear(x.requires_grad_(True), w)
+    assert torch.equal(y, want) and not y.requires_grad
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with torch.no_grad():
+            T.mx_linear(x, w)
+        T.mx_linear(x.detach(), w)

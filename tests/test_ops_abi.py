@@ -353,3 +353,10 @@ def test_clip_calls_wait_for_the_stream_of_the_call_before(monkeypatch):
     c.clip(1.0)
     to_b, to_a = [("wait", 2, 1), ("record", 2)], [("wait", 1, 2), ("record", 1)]
     assert log == [("call", 1), *to_b, ("call", 2), ("call", 2), *to_a, ("bind", 1), ("call", 2), *to_b, ("call", 2)]
+
+
+def test_linear_warns_where_a_gradient_would_be_lost():
+    torch = pytest.importorskip("torch")
+    ops = pytest.importorskip("rank_gradient_compression_amd.torch_ops")
+    with pytest.warns(UserWarning, match="mx_linear_train"), pytest.raises(ValueError, match="on the GPU"):
+        ops.mx_linear(torch.zeros(4, 64, requires_grad=True), SimpleNamespace())
