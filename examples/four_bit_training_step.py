@@ -8,9 +8,9 @@ their global norm and compressed with PowerSGD:
   clip                 GradientClip: the norm over all gradients, and the
                        clipped gradients written into the flat buffer
   compress             PowerSGD.compress at rank 4, error feedback, SGD with
-                       momentum fused into the residual pass; the factors are
-                       sent as 4-bit codes: the hook rounds P and Q in place
-                       (values of the codes) before an all-reduce would sum them
+                       momentum fused into the residual pass; the hook rounds
+                       every column of P and Q to 4-bit codes' values before
+                       an all-reduce would sum them
 
 Run on the GPU:  python examples/four_bit_training_step.py [--steps N]
 """
@@ -26,6 +26,24 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from rank_gradient_compression_amd import binding as B  # noqa: E402
 from rank_gradient_compression_amd import torch_api as T  # noqa: E402
+
+
+def four_bit_hook(ps):
+    """Aggregation hook that rounds each column of each factor, in place, to the
+    values of 4-bit codes with blocks of 32 along the column; a multi-worker
+    hook would exchange the codes and average.  Whatever error this makes stays
+    in the error memory.  The pass-through values behind P's factors have none,
+    so they are left as they are."""
+
+    def hook(buf: int, count: int, stream: int) -> int:
+        is_p = buf == ps.p.data_ptr()
+        for i in ps.compressed():
+            _, _, p_off, q_off = ps.tensors[i]
+            at, n = buf + 4 * (p_off if is_p else q_off), ps.views[i][0 if is_p else 1]
+            B.psgd_mx_quantize(at, B.PSGD_DTYPE_F32, ps.rank, n, n, 0, 0, 0, 0, 0, at, n, stream)
+        return 0
+
+    return hook
 
 
 def train(steps: int = 60, tokens: int = 700, d_in: int = 650, hidden: int = 512, d_out: int = 64, rank: int = 4,
@@ -47,14 +65,7 @@ def train(steps: int = 60, tokens: int = 700, d_in: int = 650, hidden: int = 512
     flat = [ps.view(ps.grads, i).view(-1) for i in range(4)]
     clip = None
 
-    def send_as_four_bits(buf: int, count: int, stream: int) -> int:
-        """Aggregation hook: the buffer as rows of 32-value blocks, rounded in
-        place; a multi-worker hook would exchange the codes and average."""
-        whole = count // 32 * 32
-        B.psgd_mx_quantize(buf, B.PSGD_DTYPE_F32, 1, whole, whole, 0, 0, 0, 0, 0, buf, whole, stream)
-        return 0
-
-    hook = B.make_hook(send_as_four_bits)
+    hook = B.make_hook(four_bit_hook(ps))
     losses = []
     for _ in range(steps):
         for p in leaves:
