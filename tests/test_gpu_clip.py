@@ -290,3 +290,35 @@ def test_calls_of_one_handle_on_several_streams():
     torch.cuda.synchronize()
     for g, o, s in zip(sets, outs, stats):
         check(g, s, o, 0.1)
+
+
+# bytes beyond which the outputs are stored past the cache, sums and chunks of
+# 8192 values up to which the writing pass adds the sums (the library's limits)
+STREAM_BYTES, INLINE_CHUNKS = 192 << 20, 8192
+
+
+@pytest.mark.parametrize("dtype,out,sizes,inline", [
+    (F32, F32, [30_000_001, 1_000_000], True), (BF16, F32, [40_000_003], True),
+    (F32, F32, [70_000_001, 13], False), (F32, BF16, [20_000_000, 49_999_999], False)])
+def test_lists_larger_than_the_cache(dtype, out, sizes, inline):
+    """Streaming stores, with the sums added by the writing pass and by a launch
+    of their own; the outputs in float64 on the device."""
+    size = lambda d: torch.empty(0, dtype=d).element_size()  # noqa: E731
+    total, chunks = sum(sizes), sum(-(-n // 8192) for n in sizes)
+    assert total * (size(dtype) + size(out)) > STREAM_BYTES and total * size(dtype) < 1 << 30
+    assert (chunks <= INLINE_CHUNKS) == inline
+    g = torch.Generator(device=DEV)
+    g.manual_seed(total)
+    gs = [(1e-3 * torch.randn(n, generator=g, device=DEV)).to(dtype) for n in sizes]
+    outs = [torch.full((n,), 9.0, dtype=out, device=DEV) for n in sizes]
+    say(f"[clip] {sizes} {dtype} -> {out}")
+    per = [float((t.double() ** 2).sum()) ** 0.5 for t in gs]
+    norm = sum(p * p for p in per) ** 0.5
+    limit = 0.4 * norm
+    s = f64(T.GradientClip(gs, outs).clip(limit))
+    coef = limit / (norm + 1e-6)
+    # (the norms of the reference are float64 sums in another order: 2^-40 is far above their error)
+    assert np.allclose(s, [norm, coef, *per], rtol=2.0 ** -23 + 2.0 ** -40, atol=0)
+    for t, o in zip(gs, outs):
+        want = t.double() * coef
+        assert bool(((o.double() - want).abs() <= REL[out] * want.abs() + STEP[out]).all())

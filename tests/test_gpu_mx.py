@@ -523,3 +523,81 @@ def test_linear_warns_where_a_gradient_would_be_lost():
         with torch.no_grad():
             T.mx_linear(x, w)
         T.mx_linear(x.detach(), w)
+
+
+def large_tile(m, n, k):
+    """Rows and columns of the tile that a product of more than 128 rows on both
+    sides and several chunks takes (the library's rule, evaluated here so that
+    the shapes below are seen to reach every one of them)."""
+    tiles = lambda bm, bn: -(-m // bm) * -(-n // bn)  # noqa: E731
+    rounds = lambda bm: -(-tiles(bm, 256) // 256)  # noqa: E731
+    assert m > 128 and n > 128 and k > 256
+    if tiles(64, 64) <= 256:
+        return 64, 64
+    if tiles(256, 256) <= 128:
+        return 128, 128
+    return (192, 256) if 3 * rounds(192) < 4 * rounds(256) else (256, 256)
+
+
+# both sides off the tile's multiples, a last block that is not full, an odd and
+# an even number of chunks of 256
+@pytest.mark.parametrize("m,n,k,tile", [(700, 650, 2600, (64, 64)), (1500, 2030, 290, (128, 128)), (4100, 2050, 770, (192, 256)),
+                                        (4000, 10900, 290, (256, 256)), (4010, 10999, 570, (256, 256))])
+def test_every_large_tile(m, n, k, tile):
+    """Sampled rows, and all of the last tile's, against float64; the bytes around the result stay."""
+    assert large_tile(m, n, k) == tile
+    x, w = matrix(m, k, F32, seed=41), matrix(n, k, F32, seed=42)
+    a, b = T.mx_quantize(x), T.mx_quantize(w)
+    rows = sorted({0, 15, 16, 63, tile[0] - 1, tile[0], m // 2, *range(m - 1 - (m - 1) % tile[0], m)})
+    a64, b64 = f64(T.mx_dequantize(a))[rows], f64(T.mx_dequantize(b))
+    for dtype in (F32, BF16, F16):
+        say(f"[mx] tile {tile} {m}x{n}x{k} {dtype}")
+        want, tol = product_bound(a64, b64, dtype)
+        off, ld = 3, n + 5
+        buf = torch.full((off + m * ld + 8,), 0.5, dtype=dtype, device=DEV)
+        out = buf[off:off + m * ld].view(m, ld)
+        T.mx_product(a, b, out=out[:, :n], accumulate=True)
+        got = f64(out[rows, :n])
+        assert within(got, want + 0.5, tol + HALF_STEP[dtype] * (np.abs(want) + 0.5) + 2.0 ** -24, dtype)
+        c = T.mx_product(a, b, dtype=dtype)
+        assert within(f64(c[rows]), want, tol, dtype)
+        T.mx_product(a, b, out=out[:, :n])
+        assert torch.equal(out[:, :n], c), "a strided result differs"
+        d = torch.full((m, n), 0.5, dtype=dtype, device=DEV)
+        T.mx_product(a, b, out=d, accumulate=True)
+        assert within(f64(d[rows]), want + 0.5, tol + HALF_STEP[dtype] * (np.abs(want) + 0.5) + 2.0 ** -24, dtype)
+        assert bool((out[:, n:] == 0.5).all()) and bool((buf[:off] == 0.5).all()) and bool((buf[off + m * ld:] == 0.5).all())
+
+
+def test_stochastic_layer_under_autograd():
+    """The default: the incoming gradient's random bytes come from the generator."""
+    x, w = matrix(70, 96, BF16, 1), matrix(50, 96, BF16, 2)
+    dy = matrix(70, 50, BF16, 3)
+    y, saved = T.mx_linear_forward(x, w)
+    seeds = []
+    for seed in (5, 6):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        rand = torch.randint(0, 256, dy.shape, dtype=torch.uint8, device=DEV, generator=g)
+        dx, dw = T.mx_linear_backward(dy, saved, rand=rand)
+        # (that pass against the oracle, with the same bytes)
+        rn = rand.cpu().numpy()
+        for got, a64, b64 in ((dx, MX.round_values(f64(dy), rn), MX.round_values(f64(w).T)),
+                              (dw, MX.round_values(f64(dy).T, rn.T), MX.round_values(f64(x).T))):
+            want, tol = product_bound(a64, b64, got.dtype)
+            assert within(f64(got), want, tol, got.dtype)
+        g.manual_seed(seed)
+        xl, wl = x.clone().requires_grad_(True), w.clone().requires_grad_(True)
+        out = T.mx_linear_train(xl, wl, generator=g)
+        assert torch.equal(out.detach(), y)
+        out.backward(dy)
+        assert torch.equal(xl.grad, dx) and torch.equal(wl.grad, dw.to(BF16))
+        seeds.append(dx)
+    assert not torch.equal(*seeds)
+    torch.manual_seed(9)
+    rand = torch.randint(0, 256, dy.shape, dtype=torch.uint8, device=DEV)
+    dx, _ = T.mx_linear_backward(dy, saved, rand=rand)
+    torch.manual_seed(9)
+    xl = x.clone().requires_grad_(True)
+    T.mx_linear_train(xl, w).backward(dy)
+    assert torch.equal(xl.grad, dx)
