@@ -450,8 +450,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_mx_prod_lds(MxProductArgs p
 // busy and took 12 us where this takes 7.5 (24 x 4096 x 11008).
 // The narrow operand comes from memory (XDT < 0), or, where it is small enough,
 // straight from the activations of type XDT, which every workgroup
-// quantises into LDS by itself: one launch instead of two, and the first
-// loads of the wide operand are already on their way meanwhile.
+// quantises into LDS by itself: one launch instead of two, with the first
+// loads of the wide operand asked for before those of the activations.
 // With 64 x 64 tiles the same kernel serves small products of any shape.
 struct MxSkinnyArgs {
   int64_t narrow, wide, k;  // rows of the two operands, summed axis
@@ -578,7 +578,8 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_mx_prod_skinny(MxSkinnyArgs p
       reinterpret_cast<uint4*>(xc)[i] = q;
       xs[((b >> 1) * xr16 + (row & 15)) * 4 + (row >> 4) * 2 + (b & 1)] = (uint8_t)sb;
     }
-    // (a barrier that waits for LDS alone: the stages stay under way)
+    // (A barrier for LDS alone.  The stages were asked for first and loads come
+    // back in order, so a wavefront that has its activations has its stages too.)
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
@@ -690,8 +691,9 @@ static void product_skinny(const MxSkinnyArgs& p, hipStream_t s) {
 
 // Every workgroup (32 rows of the weights) repeats the activations' work, and
 // those of one compute unit share it.  What that may cost is what a launch of
-// its own takes, about 4 us; an fp32 block costs three of 16 bits, and more than
-// 3584 blocks would not leave LDS for the stages (two launches take 10.1 us.
+// its own takes, about 4 us, and an fp32 block costs three of 16 bits: 3584
+// blocks is where that is reached (LDS would take more: beside the stages' 64 KB
+// there is room for 5461 blocks of 18 bytes.  Two launches take 10.1 us.
 // 4096 rows of weights, bf16: 16 x 4096 6.6, 24 x 4096 7.9, 8 x 11008 10.1;
 // fp32: 8 x 4096 7.8, 12 x 4096 9.6, 4 x 11008 11.8.  11008 rows, bf16: 8 x 4096
 // 8.3, 12 x 4096 9.6, 16 x 4096 10.5; fp32: 4 x 4096 9.1, 8 x 4096 12.4).

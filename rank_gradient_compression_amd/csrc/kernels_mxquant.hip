@@ -190,8 +190,12 @@ __global__ __launch_bounds__(256) void k_mx_quant_rows(MxQuantArgs a, int nch) {
 // operand of the same reading of x where it is wanted.  One workgroup = 128 x
 // 128 values held in LDS: four blocks per column give 64 contiguous bytes of
 // codes per column and per row.  In LDS each group of 32 rows is shifted by
-// 64 bytes against the one above, so that the four blocks of a column, which
-// neighbouring lanes read, fall into distinct banks.
+// 64 bytes against the one above, so that reading the values down the columns,
+// where neighbouring lanes take the four blocks of a column, the 64 lanes'
+// words fall into 64 banks.  The other accesses do meet: the random bytes, whose
+// tile has no such shift (blocks two apart share banks), 16-byte stores and the
+// reads along the rows; over all LDS instructions 2.4 conflict cycles each are
+// counted, 3.0 with random bytes.
 template <int DT>
 constexpr int kColPitch = 128 + 16 / dtype_bytes(DT);  // row pitch in LDS, elements
 template <int DT>
@@ -349,7 +353,8 @@ __global__ __launch_bounds__(256) void k_mx_quant_cols(MxQuantJobs jobs) {
   }
 }
 
-// Codes back to values: one thread = 8 codes (4 bytes) of a row.
+// Codes back to values: one thread = 8 codes (4 bytes) of a row.  The bytes
+// would take 60 us for 32000 x 4096 to bf16; it takes 128 (2.6 TB/s).
 template <int DT>
 __global__ __launch_bounds__(256) void k_mx_dequant(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                     int64_t rows, int64_t cols, typename Elem<DT>::type* __restrict__ out,

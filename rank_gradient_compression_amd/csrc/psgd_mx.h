@@ -21,7 +21,8 @@ __host__ __device__ constexpr int dtype_bytes(int d) { return d == kF32 ? 4 : 2;
 //         two matrix-core steps for rows i%16 and 16 + i%16 in one dword and
 //         a wavefront loads a tile with one 256-byte access.  Blocks past the
 //         last column have scale 0 (2^-127): the product of two such blocks
-//         is below 2^-248 and vanishes in fp32, whatever their codes.
+//         is at most 32 * 36 * 2^-254, below 2^-243, and vanishes in fp32,
+//         whatever their codes.
 constexpr int kMxBlock = 32;
 __host__ __device__ constexpr int mx_scale_in_tile(int row, int blk) {
   return (blk >> 1) * 64 + (row & 15) * 4 + (row >> 4) * 2 + (blk & 1);
