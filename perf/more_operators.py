@@ -225,19 +225,16 @@ def _plain_xent(s, grads):
     return out if b is None else out + [e.sum(dim=0).to(x.dtype)]
 
 
-def _plain_steps(u, dtype):
-    """Newton-Schulz; in 64 bits where fp32 results are asked for: directions of
-    small singular values grow by 3.4 a step, and what rounding adds to them
-    with them."""
+def _plain_steps(u):
     a, b, c = _ABC
-    x = u.double() if dtype == torch.float32 else u.float()
-    x = x / (x.double().square().sum().sqrt().to(x.dtype) + 1e-7)
+    x = u.float()
+    x = x / (x.square().sum().sqrt() + 1e-7)
     tall = x.shape[0] > x.shape[1]
     x = x.t() if tall else x
     for _ in range(_STEPS):
         g = torch.matmul(x, x.t())
         x = a * x + torch.matmul(b * g + c * torch.matmul(g, g), x)
-    return (x.t() if tall else x).float()
+    return x.t() if tall else x
 
 
 def _run_plain(s):
@@ -245,11 +242,11 @@ def _run_plain(s):
     if op in ("xent", "xent_train"):
         return _plain_xent(s, op == "xent_train")
     if op == "ortho":
-        return _plain_steps(s["x"], s["x"].dtype).to(s["x"].dtype)
+        return _plain_steps(s["x"]).to(s["x"].dtype)
     for g, m, p in zip(s["grads"], s["momentum"], s["params"]):
         gf = g.float()
         m.mul_(_MU).add_(gf)
-        o = _plain_steps(gf + _MU * m, p.dtype)
+        o = _plain_steps(gf + _MU * m)
         scale = math.sqrt(max(1.0, p.shape[0] / p.shape[1]))
         p.copy_(p.float() * (1.0 - _LR * _WD) - _LR * scale * o)
     return s["params"] + s["momentum"]
