@@ -578,6 +578,80 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Softmax cross entropy over a large vocabulary, from hidden states and output
+ * weights, without keeping the logits.
+ *
+ *   l_tv = x_t . w_v + b_v,  lse_t = log sum_v exp l_tv,  loss_t = lse_t - l_{t,y_t}
+ *   G_tv = u_t (exp(l_tv - lse_t) - [v = y_t])
+ *   dx = s G w,  dw = s G^T x,  db = s sum_t G_t
+ *
+ * x: tokens x dim (row stride ldx elements), w: vocab x dim (row stride ldw),
+ * bias: vocab values or NULL, all of type `dtype`.  targets: tokens words y_t.
+ * A token whose target is negative or `ignore_index` is ignored: its loss and
+ * its G are zero and its row of x is not looked at for dw (its lse is still
+ * written).  A target of `vocab` or more is an error in the data: its loss is
+ * NaN and its G zero.  weights: u_t, one float per token (not looked at for
+ * ignored tokens), or NULL for ones.  s is `scale`, divided by the number of
+ * tokens that are not ignored (by 1 if there is none) where `mean` is set.
+ * A bias of -infinity takes a word out of the vocabulary.
+ *
+ * psgd_xent_forward   loss and lse, tokens floats each: scoring, evaluation.
+ * psgd_xent_train     the same, and the gradients that are wanted (not NULL):
+ *                     dx, tokens x dim of type `dtype` (row stride lddx);
+ *                     dw, vocab x dim of type dw_dtype (row stride lddw);
+ *                     dbias, vocab values of type `dtype`.  With `accumulate`
+ *                     dw and dbias are added to what is there.
+ *
+ * Precision: products are summed in fp32.  16-bit tensors: probabilities and G
+ * have one rounding each to 16 bits (fp16, then `dtype`) before the gradients'
+ * products.  fp32 tensors are taken as sums of two fp16 values (22 bits;
+ * values below 2^-39 of a tensor's largest vanish).  Sums run in an order that
+ * depends on the sizes alone: equal calls give equal bits.
+ *
+ * workspace: psgd_xent_workspace bytes for the same arguments (`train`: for
+ * psgd_xent_train), 256-byte aligned, scratch.  It holds at most 1 GiB of
+ * probabilities (or those of 256 tokens) whatever the number of tokens, and
+ * copies of operands that the kernels cannot read in place: fp32 ones, and
+ * 16-bit ones whose address is no multiple of 16 bytes or whose dim or row
+ * stride is no multiple of 8.
+ *
+ * Sizes: 0 <= tokens <= INT32_MAX, 1 <= vocab, dim <= PSGD_XENT_MAX_DIM, row
+ * strides up to INT32_MAX (up to PSGD_XENT_MAX_DIM where the operand is read in
+ * place).  Errors: PSGD_ERR_INVALID_ARG (sizes, strides, an unknown type, NULL
+ * or misaligned buffers, outputs or a workspace that overlap another buffer, a
+ * scale that is not finite); PSGD_ERR_WORKSPACE; PSGD_ERR_HIP.  All calls only
+ * enqueue kernels.
+ */
+#define PSGD_XENT_MAX_DIM 4000000
+typedef struct psgd_xent {
+  int64_t tokens, vocab, dim;
+  const void* x;
+  int64_t ldx;
+  const void* w;
+  int64_t ldw;
+  const void* bias;
+  const int64_t* targets;
+  int64_t ignore_index;
+  const float* weights;
+  float* loss;
+  float* lse;
+  void* dx;
+  int64_t lddx;
+  void* dw;
+  int64_t lddw;
+  void* dbias;
+  float scale;
+  int32_t mean;
+  int32_t dtype;
+  int32_t dw_dtype;
+  int32_t accumulate;
+  int32_t reserved; /* 0 */
+} psgd_xent_t;
+psgd_status_t psgd_xent_workspace(const psgd_xent_t* args, int32_t train, size_t* bytes);
+psgd_status_t psgd_xent_forward(const psgd_xent_t* args, void* workspace, size_t workspace_bytes, hipStream_t stream);
+psgd_status_t psgd_xent_train(const psgd_xent_t* args, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Per-stage timing with HIP events recorded on the call's stream.  While
  * enabled, every compress / decompress / refresh call records one event pair
  * per stage it runs (psgd_refresh records its products under EF_P, MTP and

@@ -60,6 +60,7 @@ EXPORTED = [
     "psgd_clip_norm", "psgd_clip_apply",
     "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize", "psgd_mx_product", "psgd_mx_linear_workspace",
     "psgd_mx_linear", "psgd_mx_train_workspace", "psgd_mx_train_forward", "psgd_mx_train_backward",
+    "psgd_xent_workspace", "psgd_xent_forward", "psgd_xent_train",
     "psgd_timing_enable", "psgd_timing_stages", "psgd_timing_read", "psgd_stream_probe", "psgd_stream_copy", "psgd_last_error",
     "psgd_version",
 ]
@@ -95,6 +96,19 @@ def step_opts(power_iters: int = 0, refresh_iters: int = 0, flags: int = 0, sgd_
               sgd_momentum: float = 0.0, params: int = 0, sgd_buf: int = 0, zero_cols: int = 0) -> psgd_step_opts_t:
     return psgd_step_opts_t(power_iters, refresh_iters, flags, sgd_lr, sgd_momentum, params or None, sgd_buf or None,
                             zero_cols or None)
+
+
+class psgd_xent_t(ctypes.Structure):
+    """One cross-entropy call: addresses as ints (0 or None: NULL)."""
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64), ("x", ctypes.c_void_p),
+        ("ldx", ctypes.c_int64), ("w", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("bias", ctypes.c_void_p),
+        ("targets", ctypes.c_void_p), ("ignore_index", ctypes.c_int64), ("weights", ctypes.c_void_p),
+        ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+        ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64), ("dbias", ctypes.c_void_p), ("scale", ctypes.c_float),
+        ("mean", ctypes.c_int32), ("dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
 
 
 psgd_reduce_fn = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p)
@@ -170,6 +184,9 @@ lib.psgd_mx_train_forward.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _i
                                       _i64, _vp, _sz, _vp]
 lib.psgd_mx_train_backward.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp,
                                        _i32, _i64, _i32, _vp, _sz, _vp]
+lib.psgd_xent_workspace.argtypes = [ctypes.POINTER(psgd_xent_t), _i32, _szp]
+lib.psgd_xent_forward.argtypes = [ctypes.POINTER(psgd_xent_t), _vp, _sz, _vp]
+lib.psgd_xent_train.argtypes = lib.psgd_xent_forward.argtypes
 lib.psgd_last_error.restype = ctypes.c_char_p
 lib.psgd_version.restype = ctypes.c_char_p
 for _f in ["psgd_plan_create", "psgd_plan_get_info", "psgd_plan_tensor", "psgd_workspace_init", "psgd_compress",
@@ -180,7 +197,8 @@ for _f in ["psgd_plan_create", "psgd_plan_get_info", "psgd_plan_tensor", "psgd_w
            "psgd_clip_create", "psgd_clip_workspace", "psgd_clip_workspace_init", "psgd_clip_bind", "psgd_clip_norm",
            "psgd_clip_apply", "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize",
            "psgd_mx_product", "psgd_mx_linear_workspace", "psgd_mx_linear", "psgd_mx_train_workspace",
-           "psgd_mx_train_forward", "psgd_mx_train_backward"]:
+           "psgd_mx_train_forward", "psgd_mx_train_backward", "psgd_xent_workspace", "psgd_xent_forward",
+           "psgd_xent_train"]:
     getattr(lib, _f).restype = ctypes.c_int
 
 
@@ -400,6 +418,20 @@ def psgd_mx_train_backward(m: int, n: int, k: int, dy: int, dy_dtype: int, lddy:
                                     workspace_bytes, stream)
     if st:
         _check("psgd_mx_train_backward", st)
+
+
+def psgd_xent_workspace(args: psgd_xent_t, train: bool) -> int:
+    b = _sz()
+    _check("psgd_xent_workspace", lib.psgd_xent_workspace(ctypes.byref(args), 1 if train else 0, ctypes.byref(b)))
+    return b.value
+
+
+def psgd_xent_forward(args: psgd_xent_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check("psgd_xent_forward", lib.psgd_xent_forward(ctypes.byref(args), workspace, workspace_bytes, stream))
+
+
+def psgd_xent_train(args: psgd_xent_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check("psgd_xent_train", lib.psgd_xent_train(ctypes.byref(args), workspace, workspace_bytes, stream))
 
 
 def psgd_timing_enable(plan: int, enable: bool) -> None:

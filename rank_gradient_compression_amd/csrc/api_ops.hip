@@ -14,6 +14,7 @@
 #include "psgd_internal.h"
 #include "psgd_kernels.h"
 #include "psgd_mx.h"
+#include "psgd_xent.h"
 
 namespace psgd {
 
@@ -528,4 +529,92 @@ extern "C" psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k,
   if (!dw) return PSGD_OK;
   const MxProductArgs p{n, k, m, {dt.codes, dt.scales}, {xt_codes, xt_scales}, dw, dw_dtype, n > 1 ? lddw : k, accumulate != 0};
   return launch_status(launch_mx_product(p, stream), fn);
+}
+
+// ------------------------------------------------- vocabulary cross entropy
+static psgd_status_t check_xent(const char* fn, const psgd_xent_t* p, bool train, XentArgs* a) {
+  if (!p) return invalid(fn, "args is NULL");
+  if (p->reserved != 0) return invalid(fn, "reserved must be 0");
+  if (!known_dtype(p->dtype) || (train && p->dw && !known_dtype(p->dw_dtype)))
+    return invalid(fn, "unknown element type");
+  if (bad_dim(p->tokens)) return invalid(fn, "the number of tokens is negative or above INT32_MAX");
+  if (p->vocab < 1 || p->vocab > PSGD_XENT_MAX_DIM || p->dim < 1 || p->dim > PSGD_XENT_MAX_DIM)
+    return invalid(fn, "vocab or dim is below 1 or above PSGD_XENT_MAX_DIM");
+  const int64_t t = p->tokens, v = p->vocab, d = p->dim;
+  if (psgd_status_t s = check_strided(fn, p->x, p->dtype, t, d, p->ldx)) return s;
+  if (psgd_status_t s = check_strided(fn, p->w, p->dtype, v, d, p->ldw)) return s;
+  if (misaligned(p->bias, dtype_bytes(p->dtype)) || misaligned(p->targets, 8) || misaligned(p->weights, 4) ||
+      misaligned(p->loss, 4) || misaligned(p->lse, 4))
+    return invalid(fn, "a buffer is not aligned to its element type");
+  if (t && (!p->targets || !p->loss || !p->lse)) return invalid(fn, "a required buffer is NULL");
+  if (!(p->scale - p->scale == 0.f)) return invalid(fn, "scale is not finite");
+  if (v * ((d + 63) / 64) / 32 > kMaxGrid || t * ((d + 63) / 64) / 32 > kMaxGrid || v * d / 256 >= kMaxGrid ||
+      t * d / 256 >= kMaxGrid)
+    return invalid(fn, "the layer is too large");
+  *a = XentArgs{t,        v,          d,       p->dtype, p->x,         t > 1 ? p->ldx : d, p->w,      v > 1 ? p->ldw : d,
+                p->bias,  p->targets, p->ignore_index,  p->weights,    p->scale,           p->mean != 0,
+                p->loss,  p->lse,     nullptr, 0,        nullptr,      kF32,               0,         nullptr, false};
+  if (train) {
+    if (p->dx)
+      if (psgd_status_t s = check_strided(fn, p->dx, p->dtype, t, d, p->lddx)) return s;
+    if (p->dw)
+      if (psgd_status_t s = check_strided(fn, p->dw, p->dw_dtype, v, d, p->lddw)) return s;
+    if (misaligned(p->dbias, dtype_bytes(p->dtype))) return invalid(fn, "a buffer is not aligned to its element type");
+    a->dx = t ? p->dx : nullptr;
+    a->lddx = t > 1 ? p->lddx : d;
+    a->dw = p->dw;
+    a->dw_dtype = p->dw_dtype;
+    a->lddw = v > 1 ? p->lddw : d;
+    a->dbias = p->dbias;
+    a->accumulate = p->accumulate != 0;
+  }
+  return PSGD_OK;
+}
+
+static psgd_status_t check_xent_layout(const char* fn, const XentArgs& a, const XentLayout& l) {
+  if ((!l.pack_x && a.ldx > PSGD_XENT_MAX_DIM) || (!l.pack_w && a.ldw > PSGD_XENT_MAX_DIM))
+    return invalid(fn, "the row stride of an operand that is read in place is above PSGD_XENT_MAX_DIM");
+  return PSGD_OK;
+}
+
+extern "C" psgd_status_t psgd_xent_workspace(const psgd_xent_t* args, int32_t train, size_t* bytes) {
+  clear_error();
+  const char* fn = "psgd_xent_workspace";
+  XentArgs a;
+  if (psgd_status_t s = check_xent(fn, args, train != 0, &a)) return s;
+  if (!bytes) return invalid(fn, "bytes is NULL");
+  *bytes = xent_layout(a, train != 0).bytes;
+  return PSGD_OK;
+}
+
+static psgd_status_t run_xent(const char* fn, const psgd_xent_t* args, bool train, void* ws, size_t bytes,
+                              hipStream_t stream) {
+  clear_error();
+  XentArgs a;
+  if (psgd_status_t s = check_xent(fn, args, train, &a)) return s;
+  const XentLayout l = xent_layout(a, train);
+  if (psgd_status_t s = check_xent_layout(fn, a, l)) return s;
+  if (psgd_status_t s = check_workspace(fn, l.bytes, ws, bytes)) return s;
+  const size_t e = (size_t)dtype_bytes(a.dtype), tf = (size_t)a.t * sizeof(float);
+  const Range r[] = {{a.loss, tf},
+                     {a.lse, tf},
+                     {a.dx, strided_bytes(a.t, a.d, a.lddx, a.dtype)},
+                     {a.dw, strided_bytes(a.v, a.d, a.lddw, a.dw_dtype)},
+                     {a.dbias, (size_t)a.v * e},
+                     {ws, l.bytes},
+                     {a.x, strided_bytes(a.t, a.d, a.ldx, a.dtype)},
+                     {a.w, strided_bytes(a.v, a.d, a.ldw, a.dtype)},
+                     {a.bias, (size_t)a.v * e},
+                     {a.targets, (size_t)a.t * sizeof(int64_t)},
+                     {a.weights, tf}};
+  if (outputs_overlap(r, 6)) return invalid(fn, "an output or the workspace overlaps another buffer");
+  return launch_status(launch_xent(a, l, train, ws, stream), fn);
+}
+
+extern "C" psgd_status_t psgd_xent_forward(const psgd_xent_t* args, void* ws, size_t bytes, hipStream_t stream) {
+  return run_xent("psgd_xent_forward", args, false, ws, bytes, stream);
+}
+
+extern "C" psgd_status_t psgd_xent_train(const psgd_xent_t* args, void* ws, size_t bytes, hipStream_t stream) {
+  return run_xent("psgd_xent_train", args, true, ws, bytes, stream);
 }

@@ -1,0 +1,747 @@
+// Softmax cross entropy over a large vocabulary from hidden states and output
+// weights, without keeping the logits, and its gradients (gfx950).
+//
+//   l = x w^T + b,  lse_t = log sum_v exp l_tv,  loss_t = lse_t - l_{t, y_t}
+//   G_tv = u_t (exp(l_tv - lse_t) - [v = y_t])
+//   dx = s G w,  dw = s G^T x,  db = s sum_t G_t
+//
+// The vocabulary is taken in pieces: a tile of the product x w^T ends with its
+// rows' maximum m and sum of exp(l - m) over each segment of columns, and the
+// logits are gone.  Training keeps E = exp(l - m), at most 1, in 16 bits (fp32
+// tensors: 32) for a block of tokens whatever the batch, from which one
+// pass over the block makes G once the rows' sums are known.  That is three
+// products of T x V x D in all; forming the logits again for the gradients
+// instead of keeping E would be a fourth (a third more of the time), the pass
+// over E and G is 4 bytes a value (3% of it at D = 4096).
+// E in fp16 carries a relative error of 2^-12, G is rounded once to the type
+// that the products take; the target's entry, which would cancel, is formed
+// from the loss, exp(-loss) - 1, instead.  Sums, maxima and products are fp32.
+//
+// fp32 tensors are split into two fp16 planes (psgd_mma_device.h) under one
+// power of two that brings the largest finite value to 2^13 .. 2^14.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "psgd_mma_device.h"
+#include "psgd_xent.h"
+
+namespace psgd {
+
+// scalars that the device works out for itself
+enum { kSx, kSw, kInvSx, kInvSw, kGs, kAlphaX, kAlphaW, kAlphaB, kScalars };
+
+constexpr int kMaxGroups = 512;     // workgroups that look for a tensor's largest value
+constexpr int64_t kBlockBytes = int64_t(1) << 30;  // of E (and G) at a time
+constexpr int kGradRows = 16;       // tokens of a workgroup of the pass over E
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float load_any(const void* p, int dtype, int64_t i) {
+  if (dtype == kF32) return static_cast<const float*>(p)[i];
+  if (dtype == kBF16) return Elem<kBF16>::up(static_cast<const uint16_t*>(p)[i]);
+  return Elem<kF16>::up(static_cast<const uint16_t*>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void* p, int dtype, int64_t i, float v) {
+  if (dtype == kF32)
+    static_cast<float*>(p)[i] = v;
+  else if (dtype == kBF16)
+    static_cast<uint16_t*>(p)[i] = Elem<kBF16>::down(v);
+  else
+    static_cast<uint16_t*>(p)[i] = Elem<kF16>::down(v);
+}
+__device__ __forceinline__ bool ignored(int64_t y, int64_t ignore) { return y < 0 || y == ignore; }
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// ------------------------------------------------------------ preparations
+// Largest finite magnitude of two fp32 matrices, one partial maximum per
+// workgroup: the first `kMaxGroups` take x, the others w.
+__global__ __launch_bounds__(256) void k_xent_max(XentArgs a, float* out) {
+  const bool second = blockIdx.x >= kMaxGroups;
+  const float* p = static_cast<const float*>(second ? a.w : a.x);
+  const int64_t rows = second ? a.v : a.t, ld = second ? a.ldw : a.ldx, d = a.d;
+  const int b = blockIdx.x % kMaxGroups;
+  float m = 0.f;
+  for (int64_t row = b; row < rows; row += kMaxGroups) {
+    const float* q = p + row * ld;
+    for (int64_t i = threadIdx.x; i < d; i += 256) {
+      const float v = fabsf(q[i]);
+      m = v < __builtin_inff() ? fmaxf(m, v) : m;
+    }
+  }
+  m = wave_max(m);
+  __shared__ float part[4];
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) out[blockIdx.x] = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+}
+
+// 2^e that brings m to 2^13 .. 2^14, e within what fp32 can hold and invert.
+__device__ __forceinline__ int fit_exponent(float m) {
+  if (!(m > 0.f)) return 0;
+  int e;
+  (void)frexpf(m, &e);  // m = f 2^e, f in [1/2, 1)
+  return min(max(14 - e, -126), 126);
+}
+
+// The scalars, by one workgroup.
+__global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool split, const float* partmax, float* sc) {
+  float u = 0.f, mx = 0.f, mw = 0.f;
+  double n = 0.0;
+  if (train)
+    for (int64_t t = threadIdx.x; t < a.t; t += 256) {
+      if (ignored(a.targets[t], a.ignore)) continue;
+      n += 1.0;
+      const float v = a.weights ? fabsf(a.weights[t]) : 1.f;
+      u = v < __builtin_inff() ? fmaxf(u, v) : u;
+    }
+  if (split)
+    for (int i = threadIdx.x; i < kMaxGroups; i += 256) {
+      mx = fmaxf(mx, partmax[i]);
+      mw = fmaxf(mw, partmax[kMaxGroups + i]);
+    }
+  u = wave_max(u), mx = wave_max(mx), mw = wave_max(mw);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o);
+  __shared__ float pu[4], px[4], pw[4];
+  __shared__ double pn[4];
+  if ((threadIdx.x & 63) == 0) {
+    const int w = threadIdx.x >> 6;
+    pu[w] = u, px[w] = mx, pw[w] = mw, pn[w] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 4; ++w) u = fmaxf(u, pu[w]), mx = fmaxf(mx, px[w]), mw = fmaxf(mw, pw[w]), n += pn[w];
+  const int ex = split ? fit_exponent(mx) : 0, ew = split ? fit_exponent(mw) : 0, eg = fit_exponent(u);
+  const double s = a.mean ? (double)a.scale / fmax(n, 1.0) : (double)a.scale;
+  sc[kSx] = ldexpf(1.f, ex);
+  sc[kSw] = ldexpf(1.f, ew);
+  sc[kInvSx] = ldexpf(1.f, -ex);
+  sc[kInvSw] = ldexpf(1.f, -ew);
+  sc[kGs] = ldexpf(1.f, eg);
+  sc[kAlphaX] = (float)ldexp(s, -eg - ew);
+  sc[kAlphaW] = (float)ldexp(s, -eg - ex);
+  sc[kAlphaB] = (float)ldexp(s, -eg);
+}
+
+// Rows to operands: `parts` planes of 16 bits, zeros behind the row's end.  One
+// thread = 8 values.  clean: rows of ignored tokens become zero in a second
+// copy, the one that dw's product takes: their G is zero, and zero times what
+// such a row may hold need not be.
+template <int DT>
+__global__ __launch_bounds__(256) void k_xent_pack(const void* x, int64_t ld, int64_t rows, int64_t d, int64_t dp,
+                                                   const float* scale, uint16_t* out, uint16_t* clean,
+                                                   const int64_t* targets, int64_t ignore) {
+  using T = typename Elem<DT>::type;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = dp / 8;
+  if (i >= rows * per) return;
+  const int64_t row = i / per, c = i % per * 8;
+  const T* p = static_cast<const T*>(x) + row * ld + c;
+  T v[8];
+  if (c + 8 <= d) {
+    __builtin_memcpy(v, p, sizeof v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < d ? p[e] : (T)0;
+  }
+  uint16_t hi[8], lo[8];
+  if constexpr (DT == kF32) {
+    const float s = *scale;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float z = v[e] * s;
+      const _Float16 h = (_Float16)z;
+      hi[e] = __builtin_bit_cast(uint16_t, h);
+      const float r = z - (float)h;
+      lo[e] = Elem<kF16>::down(r == r ? r : 0.f);  // (infinite and NaN values stay so in hi)
+    }
+  } else {
+    __builtin_memcpy(hi, v, sizeof hi);
+  }
+  const int64_t at = row * dp + c, plane = rows * dp;
+  if (out) {
+    __builtin_memcpy(out + at, hi, sizeof hi);
+    if constexpr (DT == kF32) __builtin_memcpy(out + plane + at, lo, sizeof lo);
+  }
+  if (clean) {
+    if (ignored(targets[row], ignore)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) hi[e] = lo[e] = 0;
+    }
+    __builtin_memcpy(clean + at, hi, sizeof hi);
+    if constexpr (DT == kF32) __builtin_memcpy(clean + plane + at, lo, sizeof lo);
+  }
+}
+
+// ------------------------------------------------------------------ logits
+struct XentTile {
+  MmaSide x, w;
+  int64_t t, v, d;  // tokens of the block
+  int terms;
+  const float* sc;
+  const void* bias;
+  int bias_dtype;
+  const int64_t* targets;
+  float2* stats;  // t x nseg: maximum and sum
+  int64_t nseg;
+  float* target;  // t: the target's logit
+  void* e;        // t x vp
+  int64_t vp;
+};
+
+// A row's logits of one segment: lane group g has columns col0 + 16 j + 4 g + e.
+// KEEP: 0 keeps no E, 1 fp16, 2 fp32.
+template <int HB, int KEEP>
+__device__ __forceinline__ void xent_row(const XentTile& p, int64_t row, int64_t col0, int g, const v4f (&acc)[HB],
+                                         const v4f (&bias)[HB], float is, float iw, int64_t y) {
+  float l[HB * 4], m = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < HB * 4; ++i) {
+    const int64_t col = col0 + i / 4 * 16 + 4 * g + i % 4;
+    l[i] = acc[i / 4][i % 4] * is * iw + bias[i / 4][i % 4];
+    l[i] = col < p.v ? l[i] : -__builtin_inff();
+    m = fmaxf(m, l[i]);
+  }
+  m = fmaxf(m, __shfl_xor(m, 16));
+  m = fmaxf(m, __shfl_xor(m, 32));
+  const float ref = m == -__builtin_inff() ? 0.f : m;  // (a segment of masked words: sums of zero)
+  float ex[HB * 4], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < HB * 4; ++i) {
+    ex[i] = __builtin_amdgcn_exp2f((l[i] - ref) * kLog2e);
+    sum += ex[i];
+  }
+  sum += __shfl_xor(sum, 16);
+  sum += __shfl_xor(sum, 32);
+  if (row >= p.t) return;
+  if (g == 0) p.stats[row * p.nseg + col0 / (HB * 16)] = make_float2(m, sum);
+  const int64_t at = y - col0 - 4 * g;  // the target among this lane's columns
+  if (at >= 0 && at < HB * 16 && at % 16 < 4 && y < p.v) {
+#pragma unroll
+    for (int i = 0; i < HB * 4; ++i)
+      if (at == i / 4 * 16 + i % 4) p.target[row] = l[i];
+  }
+  if constexpr (KEEP == 1) {
+    uint16_t* e = static_cast<uint16_t*>(p.e) + row * p.vp + col0 + 4 * g;
+#pragma unroll
+    for (int j = 0; j < HB; ++j)
+      *reinterpret_cast<uint2*>(e + j * 16) = make_uint2(Elem<kF16>::down2(ex[j * 4], ex[j * 4 + 1]),
+                                                         Elem<kF16>::down2(ex[j * 4 + 2], ex[j * 4 + 3]));
+  } else if constexpr (KEEP == 2) {
+    float* e = static_cast<float*>(p.e) + row * p.vp + col0 + 4 * g;
+#pragma unroll
+    for (int j = 0; j < HB; ++j)
+      *reinterpret_cast<float4*>(e + j * 16) = make_float4(ex[j * 4], ex[j * 4 + 1], ex[j * 4 + 2], ex[j * 4 + 3]);
+  }
+}
+
+template <int HB>
+__device__ __forceinline__ void xent_bias(const XentTile& p, int64_t col0, int g, v4f (&bias)[HB]) {
+#pragma unroll
+  for (int i = 0; i < HB * 4; ++i) {
+    const int64_t col = col0 + i / 4 * 16 + 4 * g + i % 4;
+    bias[i / 4][i % 4] = p.bias && col < p.v ? load_any(p.bias, p.bias_dtype, col) : 0.f;
+  }
+}
+
+template <int DT, int KEEP, int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_logits(XentTile p, int ntm, int ntn) {
+  using Tile = MmaTile<DT, true, true, WM, WN, TM, TN>;
+  __shared__ __align__(16) uint8_t a0[Tile::BM * kMmaBytes], b0[Tile::BN * kMmaBytes], a1[Tile::BM * kMmaBytes],
+      b1[Tile::BN * kMmaBytes];
+  int tm, tn;
+  mma_tile_of_block(blockIdx.x, ntm, ntn, &tm, &tn);
+  const uint32_t nch = (uint32_t)((p.d + kMmaK - 1) / kMmaK);
+  typename Tile::Acc acc;
+  Tile::run(p.x, p.w, p.d, 0, nch * p.terms, (int64_t)tm * Tile::BM, (int64_t)tn * Tile::BN, a0, b0, a1, b1, acc);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int64_t row0 = (int64_t)tm * Tile::BM + wave / WN * TM * 32 + r;
+  const int64_t col0 = (int64_t)tn * Tile::BN + wave % WN * TN * 32;
+  if (col0 >= p.v) return;
+  v4f bias[Tile::HB];
+  xent_bias<Tile::HB>(p, col0, g, bias);
+  const float is = p.terms > 1 ? p.sc[kInvSx] : 1.f, iw = p.terms > 1 ? p.sc[kInvSw] : 1.f;
+#pragma unroll
+  for (int i = 0; i < Tile::HA; ++i) {
+    const int64_t row = row0 + i * 16;
+    if (row - r >= p.t) break;
+    xent_row<Tile::HB, KEEP>(p, row, col0, g, acc[i], bias, is, iw, row < p.t ? p.targets[row] : -1);
+  }
+}
+
+// Few tokens: a stream of the weights, and what counts is how many of its bytes
+// are under way.  A workgroup takes all tokens (MT * 16) and 32 words; its eight
+// wavefronts take the chunks in turn, each staging its own in LDS, two ahead,
+// in whole 128-byte rows, and their partial tiles are added in wavefront order.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x0f70 | (N >> 4) << 14);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int DT, int KEEP, int MT>
+__global__ __launch_bounds__(512, 1) void k_xent_logits_few(XentTile p) {
+  constexpr int WAVES = 8, HB = 2;
+  using LX = MmaLoad<true, MT * 16, 1>;
+  using LW = MmaLoad<true, 32, 1>;
+  constexpr int STAGE = LX::kBytes + LW::kBytes, LOADS = LX::kLoads + LW::kLoads, TILES = MT * HB;
+  static_assert(TILES * 1024 <= 2 * STAGE, "no room for the partial tiles");
+  __shared__ __align__(16) uint8_t st0[WAVES * STAGE], st1[WAVES * STAGE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t col0 = (int64_t)xcd_position(blockIdx.x, gridDim.x) * 32;
+  LX lx(p.x, 0, 0, lane);
+  LW lw(p.w, col0, 0, lane);
+  const MmaRead<true, MT * 16> rx(0, lane);
+  const MmaRead<true, 32> rw(0, lane);
+  const uint32_t nch = (uint32_t)((p.d + kMmaK - 1) / kMmaK), total = nch * p.terms;
+  uint8_t *const m0 = st0 + wave * STAGE, *const m1 = st1 + wave * STAGE;
+  auto fetch = [&](uint32_t c, uint8_t* m) {
+    const uint32_t term = c / nch, kc = c % nch, left = c < total ? (uint32_t)p.d - kc * kMmaK : 0;
+    lx.seek(term >> 1, kc, left);
+    lw.seek(term & 1, kc, left);
+#pragma unroll
+    for (int j = 0; j < LW::kLoads; ++j) lw.load(j, m + LX::kBytes, 0);
+#pragma unroll
+    for (int j = 0; j < LX::kLoads; ++j) lx.load(j, m, 0);
+  };
+  v4f acc[MT][HB];
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) acc[i / HB][i % HB] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto chunk = [&](const uint8_t* m) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint4 b[HB];
+#pragma unroll
+      for (int j = 0; j < HB; ++j) b[j] = rw(m + LX::kBytes, s, j);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const uint4 a = rx(m, s, i);
+#pragma unroll
+        for (int j = 0; j < HB; ++j) acc[i][j] = mma16<DT>(b[j], a, acc[i][j]);
+      }
+    }
+  };
+  uint32_t c = wave;
+  fetch(c, m0);
+  __builtin_amdgcn_sched_barrier(0);
+  fetch(c + WAVES, m1);
+  // (a wavefront without a chunk adds one of zeros)
+  do {
+    wait_loads<LOADS>();
+    chunk(m0);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(c + 2 * WAVES, m0);
+    wait_loads<LOADS>();
+    chunk(m1);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(c + 3 * WAVES, m1);
+    c += 2 * WAVES;
+  } while (c < total);
+  __syncthreads();  // (waits for the last fetches, of nothing, as well)
+  constexpr int SPLIT = WAVES * STAGE / 1024;  // partial tiles in st0, the rest in st1
+  auto at = [&](int i) {
+    return reinterpret_cast<v4f*>(i < SPLIT ? st0 + i * 1024 : st1 + (i - SPLIT) * 1024) + lane;
+  };
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) *at(wave * TILES + i) = acc[i / HB][i % HB];
+  __syncthreads();
+  const float is = p.terms > 1 ? p.sc[kInvSx] : 1.f, iw = p.terms > 1 ? p.sc[kInvSw] : 1.f;
+  for (int i = wave; i < MT; i += WAVES) {
+    if (i * 16 >= p.t) break;
+    v4f v[HB], bias[HB];
+#pragma unroll
+    for (int j = 0; j < HB; ++j) {
+      v[j] = *at(i * HB + j);
+#pragma unroll
+      for (int k = 1; k < WAVES; ++k) v[j] += *at(k * TILES + i * HB + j);
+    }
+    xent_bias<HB>(p, col0, g, bias);
+    const int64_t row = i * 16 + r;
+    xent_row<HB, KEEP>(p, row, col0, g, v, bias, is, iw, row < p.t ? p.targets[row] : -1);
+  }
+}
+
+// One wavefront per token: the sum over the segments, in a fixed order.
+__global__ __launch_bounds__(256) void k_xent_lse(const float2* stats, int64_t t, int64_t nseg, int64_t v,
+                                                  const int64_t* targets, int64_t ignore, const float* target,
+                                                  float* loss, float* lse) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= t) return;
+  const float2* s = stats + row * nseg;
+  float m = -__builtin_inff(), sum = 0.f;
+  for (int64_t i = lane; i < nseg; i += 64) {
+    const float2 x = s[i];
+    const float n = fmaxf(m, x.x), ref = n == -__builtin_inff() ? 0.f : n;
+    sum = sum * __builtin_amdgcn_exp2f((m - ref) * kLog2e) + x.y * __builtin_amdgcn_exp2f((x.x - ref) * kLog2e);
+    m = n;
+  }
+  const float top = wave_max(m), ref = top == -__builtin_inff() ? 0.f : top;
+  sum = wave_sum(sum * __builtin_amdgcn_exp2f((m - ref) * kLog2e));
+  if (lane != 0) return;
+  const float l = ref + logf(sum);
+  lse[row] = l;
+  const int64_t y = targets[row];
+  loss[row] = ignored(y, ignore) ? 0.f : y < v ? l - target[row] : __builtin_nanf("");
+}
+
+// ------------------------------------------------------------- the gradient
+struct XentGrad {
+  int64_t t, v, vp, nseg;
+  int seg_shift;
+  const float2* stats;
+  const float *lse, *loss, *weights, *sc;
+  const int64_t* targets;
+  int64_t ignore;
+  void* e;       // fp16 (G in its place) or fp32
+  uint16_t* g;   // G, or its two planes
+  float* db;     // partial sums, or null
+};
+
+// E to G, eight columns a thread, kGradRows tokens a workgroup one after the
+// other: two readings of a line's worth are under way while one is worked on.
+// A workgroup's columns' sums go to its row of db.
+template <int DT>  // of G: kF16 and kBF16 in E's place, kF32 as two planes
+__global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, t0 = (int64_t)blockIdx.y * kGradRows;
+  if (c >= p.vp) return;
+  const float gs = p.sc[kGs];
+  const int64_t seg = min(c >> p.seg_shift, p.nseg - 1);
+  const int n = (int)min((int64_t)kGradRows, p.t - t0);
+  float sums[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const int64_t row = t0 + i, at = row * p.vp + c, y = p.targets[row];
+    const bool off = ignored(y, p.ignore) || y >= p.v;
+    float v[8];
+    if constexpr (DT == kF32) {
+      __builtin_memcpy(v, static_cast<const float*>(p.e) + at, sizeof v);
+    } else {
+      uint16_t h[8];
+      __builtin_memcpy(h, static_cast<const uint16_t*>(p.e) + at, sizeof h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = Elem<kF16>::up(h[e]);
+    }
+    const float u = (p.weights ? p.weights[row] : 1.f) * gs;
+    const float f = u * __builtin_amdgcn_exp2f((p.stats[row * p.nseg + seg].x - p.lse[row]) * kLog2e);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = off || c + e >= p.v ? 0.f : v[e] * f;
+    if (!off && y >= c && y < c + 8) {
+      const float z = u * expm1f(-p.loss[row]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (y == c + e) v[e] = z;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[e] += v[e];
+    uint16_t h[8];
+    if constexpr (DT == kF32) {
+      uint16_t lo[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[e] = Elem<kF16>::down(v[e]);
+        const float r = v[e] - Elem<kF16>::up(h[e]);
+        lo[e] = Elem<kF16>::down(r == r ? r : 0.f);
+      }
+      __builtin_memcpy(p.g + p.t * p.vp + at, lo, sizeof lo);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = Elem<DT>::down(v[e]);
+    }
+    __builtin_memcpy(p.g + at, h, sizeof h);
+  }
+  if (p.db) {
+    float* d = p.db + (int64_t)blockIdx.y * p.vp + c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] = sums[e];
+  }
+}
+
+// db = (add +) alpha * the partial sums in order.
+__global__ __launch_bounds__(256) void k_xent_db(const float* part, int64_t rows, int64_t vp, int64_t v, const float* sc,
+                                                 void* db, int dtype, bool add) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c >= v) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int64_t i = 0; i < rows; ++i) s += part[i * vp + c];
+  s *= sc[kAlphaB];
+  if (add) s += load_any(db, dtype, c);
+  store_any(db, dtype, c, s);
+}
+
+struct XentProduct {
+  MmaSide a, b;
+  int64_t k;
+  int terms;
+  const float* alpha;  // or null: 1
+  MmaOut out;
+  int64_t split_stride;  // elements between the results of two pieces of the summed axis (gridDim.y of them)
+};
+
+template <int DT, int ODT, bool AKC, int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p, int ntm, int ntn) {
+  using Tile = MmaTile<DT, AKC, false, WM, WN, TM, TN>;
+  __shared__ __align__(16) uint8_t a0[Tile::BM * kMmaBytes], b0[Tile::BN * kMmaBytes], a1[Tile::BM * kMmaBytes],
+      b1[Tile::BN * kMmaBytes];
+  int tm, tn;
+  mma_tile_of_block(blockIdx.x, ntm, ntn, &tm, &tn);
+  const int64_t m0 = (int64_t)tm * Tile::BM, n0 = (int64_t)tn * Tile::BN;
+  const uint32_t total = (uint32_t)((p.k + kMmaK - 1) / kMmaK) * p.terms;
+  const uint32_t c0 = (uint32_t)((uint64_t)total * blockIdx.y / gridDim.y);
+  const uint32_t c1 = (uint32_t)((uint64_t)total * (blockIdx.y + 1) / gridDim.y);
+  typename Tile::Acc acc;
+  Tile::run(p.a, p.b, p.k, c0, c1, m0, n0, a0, b0, a1, b1, acc);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float* lds = mma_epilogue_lds<Tile>(wave, a0, b0, a1, b1);
+  p.out.c = static_cast<typename Elem<ODT>::type*>(p.out.c) + blockIdx.y * p.split_stride;
+  mma_store<ODT>(p.out, p.alpha ? *p.alpha : 1.f, lds, m0 + wave / WN * TM * 32, n0 + wave % WN * TN * 32, acc);
+}
+
+// dx = alpha * the pieces' sums in order.
+__global__ __launch_bounds__(256) void k_xent_dx(const float* part, int64_t pieces, int64_t t, int64_t d,
+                                                 const float* alpha, void* dx, int dtype, int64_t lddx) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= t * d) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int64_t k = 0; k < pieces; ++k) s += part[k * t * d + i];
+  store_any(dx, dtype, i / d * lddx + i % d, s * *alpha);
+}
+
+// Gradients of a loss over no word or no token.
+__global__ __launch_bounds__(256) void k_xent_zero(void* p, int dtype, int64_t rows, int64_t cols, int64_t ld) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < rows * cols) store_any(p, dtype, i / cols * ld + i % cols, 0.f);
+}
+
+// ---------------------------------------------------------------- the host
+static int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+static int64_t cdiv(int64_t v, int64_t by) { return (v + by - 1) / by; }
+static unsigned grid(int64_t n) { return (unsigned)cdiv(n, 256); }
+
+// An operand that the tile loop can read where it is.
+static bool readable(const void* p, int64_t ld, int64_t d, int dtype) {
+  return dtype != kF32 && ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && d % 8 == 0;
+}
+
+constexpr int64_t kFewTokens = 32;
+
+XentLayout xent_layout(const XentArgs& a, bool train) {
+  XentLayout l{};
+  const bool f32 = a.dtype == kF32;
+  l.parts = f32 ? 2 : 1;
+  l.pack_x = !readable(a.x, a.ldx, a.d, a.dtype);
+  l.pack_w = !readable(a.w, a.ldw, a.d, a.dtype);
+  l.dp = up(a.d, 64);
+  l.vp = up(a.v, 64);
+  // (a block's rows are a multiple of the tiles', and few tokens are one block)
+  l.block = std::max<int64_t>(1, a.t);
+  if (train) l.block = std::min(l.block, std::max<int64_t>(256, kBlockBytes / (l.vp * (f32 ? 8 : 2)) / 256 * 256));
+  l.seg_shift = a.t <= kFewTokens ? 5 : 6;
+  l.nseg = cdiv(a.v, int64_t(1) << l.seg_shift);
+  const int64_t tiles = cdiv(l.block, 128) * cdiv(a.d, 128), chunks = cdiv(a.v, kMmaK) * (f32 ? 3 : 1);
+  l.dx_splits = std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, tiles), chunks / 8, 128}));
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t was = at;
+    at += (bytes + 255) / 256 * 256;
+    return was;
+  };
+  l.scalars = take(kScalars * sizeof(float));
+  l.partmax = take(f32 ? 2 * kMaxGroups * sizeof(float) : 0);
+  // x as the logits' operand, then (training) with ignored tokens' rows zero
+  l.x = take((size_t)((l.pack_x ? 1 : 0) + (train ? 1 : 0)) * l.parts * a.t * l.dp * 2);
+  l.w = take(l.pack_w ? (size_t)l.parts * a.v * l.dp * 2 : 0);
+  l.stats = take((size_t)l.block * l.nseg * sizeof(float2));
+  l.target = take((size_t)l.block * sizeof(float));
+  if (train) {
+    l.e = take((size_t)l.block * l.vp * (f32 ? 4 : 2));
+    l.g = f32 ? take((size_t)l.block * l.vp * 4) : l.e;
+    l.db = take(a.dbias ? (size_t)cdiv(l.block, kGradRows) * l.vp * sizeof(float) : 0);
+    l.dxp = take(a.dx && l.dx_splits > 1 ? (size_t)l.dx_splits * l.block * a.d * sizeof(float) : 0);
+    l.dwp = take(a.dw && a.dw_dtype != kF32 && l.block < a.t ? (size_t)a.v * a.d * sizeof(float) : 0);
+  }
+  l.bytes = std::max<size_t>(at, 256);
+  return l;
+}
+
+template <int DT>
+static void pack(const void* x, int64_t ld, int64_t rows, int64_t d, int64_t dp, const float* scale, uint16_t* out,
+                 uint16_t* clean, const XentArgs& a, hipStream_t s) {
+  if (rows == 0 || d == 0) return;
+  hipLaunchKernelGGL((k_xent_pack<DT>), dim3(grid(rows * dp / 8)), dim3(256), 0, s, x, ld, rows, d, dp, scale, out,
+                     clean, a.targets, a.ignore);
+}
+static void pack_any(const void* x, int64_t ld, int64_t rows, int64_t dp, const float* scale, uint16_t* out,
+                     uint16_t* clean, const XentArgs& a, hipStream_t s) {
+  if (a.dtype == kF32)
+    pack<kF32>(x, ld, rows, a.d, dp, scale, out, clean, a, s);
+  else if (a.dtype == kBF16)
+    pack<kBF16>(x, ld, rows, a.d, dp, scale, out, clean, a, s);
+  else
+    pack<kF16>(x, ld, rows, a.d, dp, scale, out, clean, a, s);
+}
+
+template <int DT, int KEEP>
+static void logits(const XentTile& p, int64_t tokens, hipStream_t s) {
+  if (tokens <= kFewTokens) {
+    const dim3 g((unsigned)cdiv(p.v, 32)), b(512);
+    if (p.t <= 16)
+      hipLaunchKernelGGL((k_xent_logits_few<DT, KEEP, 1>), g, b, 0, s, p);
+    else
+      hipLaunchKernelGGL((k_xent_logits_few<DT, KEEP, 2>), g, b, 0, s, p);
+    return;
+  }
+  if (cdiv(p.t, 256) * cdiv(p.v, 256) >= 256) {
+    const int ntm = (int)cdiv(p.t, 256), ntn = (int)cdiv(p.v, 256);
+    hipLaunchKernelGGL((k_xent_logits<DT, KEEP, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
+  } else {
+    const int ntm = (int)cdiv(p.t, 128), ntn = (int)cdiv(p.v, 128);
+    hipLaunchKernelGGL((k_xent_logits<DT, KEEP, 2, 2, 2, 2>), dim3(ntm * ntn), dim3(256), 0, s, p, ntm, ntn);
+  }
+}
+
+template <int DT, int ODT, bool AKC>
+static void product_to(const XentProduct& p, int64_t pieces, hipStream_t s) {
+  if (pieces == 1 && cdiv(p.out.m, 256) * cdiv(p.out.n, 256) >= 192) {
+    const int ntm = (int)cdiv(p.out.m, 256), ntn = (int)cdiv(p.out.n, 256);
+    hipLaunchKernelGGL((k_xent_product<DT, ODT, AKC, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
+  } else {
+    const int ntm = (int)cdiv(p.out.m, 128), ntn = (int)cdiv(p.out.n, 128);
+    hipLaunchKernelGGL((k_xent_product<DT, ODT, AKC, 2, 2, 2, 2>), dim3(ntm * ntn, (unsigned)pieces), dim3(256), 0, s,
+                       p, ntm, ntn);
+  }
+}
+template <int DT, bool AKC>
+static void product(const XentProduct& p, int odt, int64_t pieces, hipStream_t s) {
+  if (odt == kF32)
+    product_to<DT, kF32, AKC>(p, pieces, s);
+  else if (odt == kBF16)
+    product_to<DT, kBF16, AKC>(p, pieces, s);
+  else
+    product_to<DT, kF16, AKC>(p, pieces, s);
+}
+
+// DT: what the products take; KEEP: how E is kept.
+template <int DT, int KEEP>
+static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* ws, int64_t t0, hipStream_t s) {
+  const int64_t n = std::min(l.block, a.t - t0), plane_x = a.t * l.dp;
+  const float* sc = reinterpret_cast<const float*>(ws + l.scalars);
+  uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
+  float2* const stats = reinterpret_cast<float2*>(ws + l.stats);
+  float* const target = reinterpret_cast<float*>(ws + l.target);
+  const int terms = l.parts == 2 ? 3 : 1;
+  XentTile p{};
+  p.x = l.pack_x ? MmaSide{px + t0 * l.dp, plane_x, l.dp, n}
+                 : MmaSide{static_cast<const uint16_t*>(a.x) + t0 * a.ldx, 0, a.ldx, n};
+  p.w = l.pack_w ? MmaSide{reinterpret_cast<uint16_t*>(ws + l.w), a.v * l.dp, l.dp, a.v}
+                 : MmaSide{static_cast<const uint16_t*>(a.w), 0, a.ldw, a.v};
+  p.t = n, p.v = a.v, p.d = a.d, p.terms = terms, p.sc = sc, p.bias = a.bias, p.bias_dtype = a.dtype;
+  p.targets = a.targets + t0, p.stats = stats, p.nseg = l.nseg, p.target = target, p.e = ws + l.e, p.vp = l.vp;
+  if (train)
+    logits<DT, KEEP>(p, a.t, s);
+  else
+    logits<DT, 0>(p, a.t, s);
+  hipLaunchKernelGGL(k_xent_lse, dim3((unsigned)cdiv(n, 4)), dim3(256), 0, s, stats, n, l.nseg, a.v, a.targets + t0,
+                     a.ignore, target, a.loss + t0, a.lse + t0);
+  if (!train || !(a.dx || a.dw || a.dbias)) return;
+  uint16_t* const g = reinterpret_cast<uint16_t*>(ws + l.g);
+  float* const db = reinterpret_cast<float*>(ws + l.db);
+  const int64_t parts = cdiv(n, kGradRows);
+  const XentGrad q{n,     a.v, l.vp, l.nseg, l.seg_shift, stats, a.lse + t0, a.loss + t0, a.weights ? a.weights + t0 : nullptr,
+                   sc, a.targets + t0, a.ignore, ws + l.e, g, a.dbias ? db : nullptr};
+  hipLaunchKernelGGL((k_xent_grad<KEEP == 2 ? kF32 : DT>), dim3((unsigned)cdiv(l.vp, 2048), (unsigned)parts), dim3(256),
+                     0, s, q);
+  if (a.dbias)
+    hipLaunchKernelGGL(k_xent_db, dim3(grid(a.v)), dim3(256), 0, s, db, parts, l.vp, a.v, sc, a.dbias, a.dtype,
+                       a.accumulate || t0 > 0);
+  if (a.dx) {
+    XentProduct d{};
+    d.a = MmaSide{g, n * l.vp, l.vp, n};
+    d.b = p.w;
+    d.b.len = a.d;
+    d.k = a.v, d.terms = terms;
+    const int eb = dtype_bytes(a.dtype);
+    uint8_t* const dx = static_cast<uint8_t*>(a.dx) + t0 * a.lddx * eb;
+    if (l.dx_splits > 1) {
+      float* const part = reinterpret_cast<float*>(ws + l.dxp);
+      d.out = MmaOut{part, a.d, n, a.d, nullptr, false};
+      d.split_stride = n * a.d;
+      product<DT, true>(d, kF32, l.dx_splits, s);
+      hipLaunchKernelGGL(k_xent_dx, dim3(grid(n * a.d)), dim3(256), 0, s, part, l.dx_splits, n, a.d, sc + kAlphaX, dx,
+                         a.dtype, a.lddx);
+    } else {
+      d.alpha = sc + kAlphaX;
+      d.out = MmaOut{dx, a.lddx, n, a.d, nullptr, false};
+      product<DT, true>(d, a.dtype, 1, s);
+    }
+  }
+  if (a.dw) {
+    XentProduct d{};
+    d.a = MmaSide{g, n * l.vp, l.vp, a.v};
+    d.b = MmaSide{px + (l.pack_x ? l.parts * plane_x : 0) + t0 * l.dp, plane_x, l.dp, a.d};
+    d.k = n, d.terms = terms, d.alpha = sc + kAlphaW;
+    // Blocks before the last add up in fp32: in dw itself, or in memory of
+    // their own where dw has fewer bits.
+    const bool last = t0 + n == a.t, wide = a.dw_dtype == kF32;
+    float* const sum = reinterpret_cast<float*>(ws + l.dwp);
+    if (wide)
+      d.out = MmaOut{a.dw, a.lddw, a.v, a.d, nullptr, a.accumulate || t0 > 0};
+    else if (!last)
+      d.out = MmaOut{sum, a.d, a.v, a.d, nullptr, t0 > 0};
+    else
+      d.out = MmaOut{a.dw, a.lddw, a.v, a.d, t0 > 0 ? sum : nullptr, a.accumulate};
+    product<DT, false>(d, wide || !last ? kF32 : a.dw_dtype, 1, s);
+  }
+}
+
+hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void* workspace, hipStream_t s) {
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  float* const sc = reinterpret_cast<float*>(ws + l.scalars);
+  float* const partmax = reinterpret_cast<float*>(ws + l.partmax);
+  const bool f32 = a.dtype == kF32;
+  if (a.t == 0) {
+    if (train && !a.accumulate) {
+      if (a.dw && a.v && a.d)
+        hipLaunchKernelGGL(k_xent_zero, dim3(grid(a.v * a.d)), dim3(256), 0, s, a.dw, a.dw_dtype, a.v, a.d, a.lddw);
+      if (a.dbias)
+        hipLaunchKernelGGL(k_xent_zero, dim3(grid(a.v)), dim3(256), 0, s, a.dbias, a.dtype, int64_t(1), a.v, a.v);
+    }
+    return hipGetLastError();
+  }
+  if (f32) hipLaunchKernelGGL(k_xent_max, dim3(2 * kMaxGroups), dim3(256), 0, s, a, partmax);
+  if (f32 || train) hipLaunchKernelGGL(k_xent_prep, dim3(1), dim3(256), 0, s, a, train, f32, partmax, sc);
+  if (l.pack_w)
+    pack_any(a.w, a.ldw, a.v, l.dp, sc + kSw, reinterpret_cast<uint16_t*>(ws + l.w), nullptr, a, s);
+  if (l.pack_x || train) {
+    uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
+    pack_any(a.x, a.ldx, a.t, l.dp, sc + kSx, l.pack_x ? px : nullptr,
+             train ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr, a, s);
+  }
+  for (int64_t t0 = 0; t0 < a.t; t0 += l.block) {
+    if (a.dtype == kBF16)
+      block<kBF16, 1>(a, l, train, ws, t0, s);
+    else if (a.dtype == kF16)
+      block<kF16, 1>(a, l, train, ws, t0, s);
+    else
+      block<kF16, 2>(a, l, train, ws, t0, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace psgd
