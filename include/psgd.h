@@ -652,6 +652,69 @@ psgd_status_t psgd_xent_forward(const psgd_xent_t* args, void* workspace, size_t
 psgd_status_t psgd_xent_train(const psgd_xent_t* args, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Orthogonalised updates of a list of matrices, and the optimiser step around
+ * them (Muon): what may follow the decompression instead of momentum SGD.
+ *
+ *   m <- mu m + g,  u = g + mu m (nesterov) or m;  u = g without m
+ *   X = u / (||u||_F + eps);  steps times, with A = X X^T (X^T X where rows >
+ *   cols):  X <- a X + (b A + c A^2) X  (X on the left there)
+ *   update = X;  param <- (1 - lr weight_decay) param - lr lr_scale X
+ *
+ * The usual coefficients, 3.4445, -4.7750, 2.0315, bring every singular value
+ * that is not tiny against the norm to 0.7 .. 1.2 in five steps.
+ *
+ * psgd_muon_step   one step over ntensors matrices (the array is read before
+ *                  the call returns).  grad: rows x cols, row stride ldg.
+ *                  momentum: rows x cols floats, contiguous, read and written,
+ *                  or NULL.  param (read and written, row stride ldp) and
+ *                  update (written, row stride ldu; may be grad itself, with
+ *                  its type and stride): either may be NULL, not both.  Rows or
+ *                  cols 0: an empty matrix, left alone.  A zero gradient gives
+ *                  a zero X; an infinite or NaN one makes its matrix's update
+ *                  and param NaN.
+ *
+ * Precision (opts.pieces): 1 takes the products on one fp16 value per entry of
+ * X, A and B, with a X from two (about 2e-3 of the update, relative norm, what
+ * bfloat16 has to give), 2 on two (about 1e-6; three products for one), 0
+ * chooses per matrix: 1 where what is written is bfloat16, else 2.  Sums of
+ * squares are fp64, products are summed in fp32, in orders that depend on the
+ * list's sizes alone: equal calls give equal bits.
+ *
+ * workspace: psgd_muon_workspace bytes for the same list (pointers are not
+ * looked at but for being NULL), 256-byte aligned, scratch; a long list is
+ * worked off in groups that share it.
+ *
+ * Errors: PSGD_ERR_INVALID_ARG (sizes beyond PSGD_MUON_MAX_DIM, strides, unknown
+ * types, NULL or misaligned buffers, buffers that overlap, options that are not
+ * finite, steps outside 1 .. 100, coefficients under which singular values grow
+ * beyond 16); PSGD_ERR_WORKSPACE; PSGD_ERR_HIP.  Only enqueues kernels.
+ */
+#define PSGD_MUON_MAX_DIM 1000000
+typedef struct psgd_muon_tensor {
+  const void* grad;
+  int64_t ldg;
+  float* momentum;
+  void* param;
+  int64_t ldp;
+  void* update;
+  int64_t ldu;
+  int64_t rows, cols;
+  float lr_scale;
+  int32_t grad_dtype, param_dtype, update_dtype;
+} psgd_muon_tensor_t;
+typedef struct psgd_muon_opts {
+  float lr, momentum, weight_decay;
+  float a, b, c, eps;
+  int32_t steps;
+  int32_t nesterov;
+  int32_t pieces; /* 0, 1 or 2 */
+} psgd_muon_opts_t;
+psgd_status_t psgd_muon_workspace(int32_t ntensors, const psgd_muon_tensor_t* tensors, const psgd_muon_opts_t* opts,
+                                  size_t* bytes);
+psgd_status_t psgd_muon_step(int32_t ntensors, const psgd_muon_tensor_t* tensors, const psgd_muon_opts_t* opts,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Per-stage timing with HIP events recorded on the call's stream.  While
  * enabled, every compress / decompress / refresh call records one event pair
  * per stage it runs (psgd_refresh records its products under EF_P, MTP and

@@ -60,7 +60,7 @@ EXPORTED = [
     "psgd_clip_norm", "psgd_clip_apply",
     "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize", "psgd_mx_product", "psgd_mx_linear_workspace",
     "psgd_mx_linear", "psgd_mx_train_workspace", "psgd_mx_train_forward", "psgd_mx_train_backward",
-    "psgd_xent_workspace", "psgd_xent_forward", "psgd_xent_train",
+    "psgd_xent_workspace", "psgd_xent_forward", "psgd_xent_train", "psgd_muon_workspace", "psgd_muon_step",
     "psgd_timing_enable", "psgd_timing_stages", "psgd_timing_read", "psgd_stream_probe", "psgd_stream_copy", "psgd_last_error",
     "psgd_version",
 ]
@@ -108,6 +108,24 @@ class psgd_xent_t(ctypes.Structure):
         ("dw", ctypes.c_void_p), ("lddw", ctypes.c_int64), ("dbias", ctypes.c_void_p), ("scale", ctypes.c_float),
         ("mean", ctypes.c_int32), ("dtype", ctypes.c_int32), ("dw_dtype", ctypes.c_int32),
         ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class psgd_muon_tensor_t(ctypes.Structure):
+    """One matrix of an orthogonalised step: addresses as ints (0 or None: NULL)."""
+    _fields_ = [
+        ("grad", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("momentum", ctypes.c_void_p), ("param", ctypes.c_void_p),
+        ("ldp", ctypes.c_int64), ("update", ctypes.c_void_p), ("ldu", ctypes.c_int64), ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64), ("lr_scale", ctypes.c_float), ("grad_dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32), ("update_dtype", ctypes.c_int32),
+    ]
+
+
+class psgd_muon_opts_t(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float), ("a", ctypes.c_float),
+        ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float), ("steps", ctypes.c_int32),
+        ("nesterov", ctypes.c_int32), ("pieces", ctypes.c_int32),
     ]
 
 
@@ -187,6 +205,8 @@ lib.psgd_mx_train_backward.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _
 lib.psgd_xent_workspace.argtypes = [ctypes.POINTER(psgd_xent_t), _i32, _szp]
 lib.psgd_xent_forward.argtypes = [ctypes.POINTER(psgd_xent_t), _vp, _sz, _vp]
 lib.psgd_xent_train.argtypes = lib.psgd_xent_forward.argtypes
+lib.psgd_muon_workspace.argtypes = [_i32, ctypes.POINTER(psgd_muon_tensor_t), ctypes.POINTER(psgd_muon_opts_t), _szp]
+lib.psgd_muon_step.argtypes = [_i32, ctypes.POINTER(psgd_muon_tensor_t), ctypes.POINTER(psgd_muon_opts_t), _vp, _sz, _vp]
 lib.psgd_last_error.restype = ctypes.c_char_p
 lib.psgd_version.restype = ctypes.c_char_p
 for _f in ["psgd_plan_create", "psgd_plan_get_info", "psgd_plan_tensor", "psgd_workspace_init", "psgd_compress",
@@ -198,7 +218,7 @@ for _f in ["psgd_plan_create", "psgd_plan_get_info", "psgd_plan_tensor", "psgd_w
            "psgd_clip_apply", "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize",
            "psgd_mx_product", "psgd_mx_linear_workspace", "psgd_mx_linear", "psgd_mx_train_workspace",
            "psgd_mx_train_forward", "psgd_mx_train_backward", "psgd_xent_workspace", "psgd_xent_forward",
-           "psgd_xent_train"]:
+           "psgd_xent_train", "psgd_muon_workspace", "psgd_muon_step"]:
     getattr(lib, _f).restype = ctypes.c_int
 
 
@@ -432,6 +452,18 @@ def psgd_xent_forward(args: psgd_xent_t, workspace: int, workspace_bytes: int, s
 
 def psgd_xent_train(args: psgd_xent_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
     _check("psgd_xent_train", lib.psgd_xent_train(ctypes.byref(args), workspace, workspace_bytes, stream))
+
+
+def psgd_muon_workspace(tensors, opts: psgd_muon_opts_t) -> int:
+    """tensors: a ctypes array of psgd_muon_tensor_t."""
+    b = _sz()
+    _check("psgd_muon_workspace", lib.psgd_muon_workspace(len(tensors), tensors, ctypes.byref(opts), ctypes.byref(b)))
+    return b.value
+
+
+def psgd_muon_step(tensors, opts: psgd_muon_opts_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check("psgd_muon_step", lib.psgd_muon_step(len(tensors), tensors, ctypes.byref(opts), workspace, workspace_bytes,
+                                                stream))
 
 
 def psgd_timing_enable(plan: int, enable: bool) -> None:

@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libpsgd.so")
 
 SOURCES = ["plan.cpp", "api.hip", "kernels_valu.hip", "kernels_mfma.hip", "kernels_rng.hip", "kernels_probe.hip",
            "kernels_diag.hip", "kernels_payload.hip", "api_ops.hip", "kernels_clip.hip", "kernels_mxquant.hip",
-           "kernels_mxprod.hip", "kernels_xent.hip"]
+           "kernels_mxprod.hip", "kernels_xent.hip", "kernels_muon.hip"]
 
 # Packed fp32 instructions are disabled for all device code.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

@@ -13,6 +13,7 @@
 #include "psgd_clip.h"
 #include "psgd_internal.h"
 #include "psgd_kernels.h"
+#include "psgd_muon.h"
 #include "psgd_mx.h"
 #include "psgd_xent.h"
 
@@ -617,4 +618,104 @@ extern "C" psgd_status_t psgd_xent_forward(const psgd_xent_t* args, void* ws, si
 
 extern "C" psgd_status_t psgd_xent_train(const psgd_xent_t* args, void* ws, size_t bytes, hipStream_t stream) {
   return run_xent("psgd_xent_train", args, true, ws, bytes, stream);
+}
+
+// ------------------------------------------------------ orthogonalised step
+static bool finite(float v) { return v - v == 0.f; }
+
+// The list without its empty matrices.
+static psgd_status_t check_muon(const char* fn, int32_t n, const psgd_muon_tensor_t* t, const psgd_muon_opts_t* o,
+                                std::vector<MuonTensor>* out, MuonOpts* opts) {
+  if (n < 0 || (n > 0 && !t)) return invalid(fn, "negative tensor count or a NULL list");
+  if (!o) return invalid(fn, "opts is NULL");
+  for (float v : {o->lr, o->momentum, o->weight_decay, o->a, o->b, o->c, o->eps})
+    if (!finite(v)) return invalid(fn, "an option is not finite");
+  if (o->eps < 0.f) return invalid(fn, "eps is negative");
+  if (o->steps < 1 || o->steps > 100) return invalid(fn, "steps is outside 1 .. 100");
+  if (o->pieces < 0 || o->pieces > 2) return invalid(fn, "pieces must be 0, 1 or 2");
+  *opts = MuonOpts{o->momentum, 1.f - o->lr * o->weight_decay, o->a, o->b, o->c, o->eps, o->steps, o->nesterov != 0};
+  float sx, sa, sb;
+  if (!muon_scales(*opts, &sx, &sa, &sb)) return invalid(fn, "the coefficients let singular values grow beyond 16");
+  for (int32_t i = 0; i < n; ++i) {
+    const psgd_muon_tensor_t& x = t[i];
+    if (x.rows < 0 || x.cols < 0 || x.rows > PSGD_MUON_MAX_DIM || x.cols > PSGD_MUON_MAX_DIM)
+      return invalid(fn, "a size is negative or above PSGD_MUON_MAX_DIM");
+    if (psgd_status_t s = check_strided(fn, x.grad, x.grad_dtype, x.rows, x.cols, x.ldg)) return s;
+    if (x.param)
+      if (psgd_status_t s = check_strided(fn, x.param, x.param_dtype, x.rows, x.cols, x.ldp)) return s;
+    if (x.update)
+      if (psgd_status_t s = check_strided(fn, x.update, x.update_dtype, x.rows, x.cols, x.ldu)) return s;
+    if (misaligned(x.momentum, 4)) return invalid(fn, "a buffer is not aligned to its element type");
+    if (!finite(x.lr_scale) || !finite(o->lr * x.lr_scale)) return invalid(fn, "lr_scale is not finite");
+    if (x.rows == 0 || x.cols == 0) continue;
+    if (!x.param && !x.update) return invalid(fn, "a matrix has neither param nor update");
+    if (((x.rows + 127) / 128) * ((x.cols + 127) / 128) > (1 << 24) || std::min(x.rows, x.cols) > 300000)
+      return invalid(fn, "a matrix is too large");
+    const bool one = (!x.param || x.param_dtype == kBF16) && (!x.update || x.update_dtype == kBF16);
+    const int pieces = o->pieces ? o->pieces : one ? 1 : 2;
+    out->push_back(MuonTensor{x.grad, x.momentum, x.param, x.update, x.rows > 1 ? x.ldg : x.cols,
+                              x.rows > 1 ? x.ldp : x.cols, x.rows > 1 ? x.ldu : x.cols, x.rows, x.cols,
+                              o->lr * x.lr_scale, x.grad_dtype, x.param ? x.param_dtype : kF32,
+                              x.update ? x.update_dtype : kF32, pieces});
+  }
+  return PSGD_OK;
+}
+
+extern "C" psgd_status_t psgd_muon_workspace(int32_t n, const psgd_muon_tensor_t* tensors, const psgd_muon_opts_t* opts,
+                                             size_t* bytes) {
+  clear_error();
+  const char* fn = "psgd_muon_workspace";
+  try {
+    std::vector<MuonTensor> t;
+    MuonOpts o;
+    if (psgd_status_t s = check_muon(fn, n, tensors, opts, &t, &o)) return s;
+    if (!bytes) return invalid(fn, "bytes is NULL");
+    *bytes = muon_workspace(t);
+  } catch (const std::bad_alloc&) {
+    return invalid(fn, "out of host memory");
+  }
+  return PSGD_OK;
+}
+
+extern "C" psgd_status_t psgd_muon_step(int32_t n, const psgd_muon_tensor_t* tensors, const psgd_muon_opts_t* opts,
+                                        void* ws, size_t bytes, hipStream_t stream) {
+  clear_error();
+  const char* fn = "psgd_muon_step";
+  try {
+    std::vector<MuonTensor> t;
+    MuonOpts o;
+    if (psgd_status_t s = check_muon(fn, n, tensors, opts, &t, &o)) return s;
+    const size_t need = muon_workspace(t);
+    if (psgd_status_t s = check_workspace(fn, need, ws, bytes)) return s;
+    // what is written, each range with the gradient that it may replace
+    struct Out {
+      uintptr_t b, e;
+      const MuonTensor* in_place;
+    };
+    std::vector<Out> outs;
+    auto put = [&](const void* p, size_t len, const MuonTensor* in_place) {
+      if (p && len) outs.push_back({(uintptr_t)p, (uintptr_t)p + len, in_place});
+    };
+    put(ws, need, nullptr);
+    for (const MuonTensor& x : t) {
+      put(x.mom, (size_t)(x.r * x.c) * 4, nullptr);
+      put(x.param, strided_bytes(x.r, x.c, x.ldp, x.pdt), nullptr);
+      put(x.upd, strided_bytes(x.r, x.c, x.ldu, x.udt),
+          x.upd == x.grad && x.udt == x.gdt && x.ldu == x.ldg ? &x : nullptr);
+    }
+    std::sort(outs.begin(), outs.end(), [](const Out& x, const Out& y) { return x.b < y.b; });
+    for (size_t i = 1; i < outs.size(); ++i)
+      if (outs[i].b < outs[i - 1].e) return invalid(fn, "an output or the workspace overlaps another output");
+    for (const MuonTensor& x : t) {
+      const uintptr_t b = (uintptr_t)x.grad, e = b + strided_bytes(x.r, x.c, x.ldg, x.gdt);
+      auto it = std::upper_bound(outs.begin(), outs.end(), b, [](uintptr_t v, const Out& r) { return v < r.e; });
+      for (; it != outs.end() && it->b < e; ++it)
+        if (it->in_place != &x)
+          return invalid(fn, "an output overlaps a gradient other than being its own update in place");
+    }
+    if (t.empty()) return PSGD_OK;
+    return launch_status(launch_muon(t, o, ws, stream), fn);
+  } catch (const std::bad_alloc&) {
+    return invalid(fn, "out of host memory");
+  }
 }

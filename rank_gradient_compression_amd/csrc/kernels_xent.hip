@@ -263,7 +263,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_logits(XentTile p, int
   mma_tile_of_block(blockIdx.x, ntm, ntn, &tm, &tn);
   const uint32_t nch = (uint32_t)((p.d + kMmaK - 1) / kMmaK);
   typename Tile::Acc acc;
-  Tile::run(p.x, p.w, p.d, 0, nch * p.terms, (int64_t)tm * Tile::BM, (int64_t)tn * Tile::BN, a0, b0, a1, b1, acc);
+  Tile::run(p.x, p.w, p.d, p.terms, 0, nch * p.terms, (int64_t)tm * Tile::BM, (int64_t)tn * Tile::BN, a0, b0, a1, b1, acc);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int64_t row0 = (int64_t)tm * Tile::BM + wave / WN * TM * 32 + r;
   const int64_t col0 = (int64_t)tn * Tile::BN + wave % WN * TN * 32;
@@ -308,9 +308,9 @@ __global__ __launch_bounds__(512, 1) void k_xent_logits_few(XentTile p) {
   const uint32_t nch = (uint32_t)((p.d + kMmaK - 1) / kMmaK), total = nch * p.terms;
   uint8_t *const m0 = st0 + wave * STAGE, *const m1 = st1 + wave * STAGE;
   auto fetch = [&](uint32_t c, uint8_t* m) {
-    const uint32_t term = c / nch, kc = c % nch, left = c < total ? (uint32_t)p.d - kc * kMmaK : 0;
-    lx.seek(term >> 1, kc, left);
-    lw.seek(term & 1, kc, left);
+    const uint32_t term = c / nch + 3 - p.terms, kc = c % nch, left = c < total ? (uint32_t)p.d - kc * kMmaK : 0;
+    lx.seek(term == 1, kc, left);
+    lw.seek(term == 0, kc, left);
 #pragma unroll
     for (int j = 0; j < LW::kLoads; ++j) lw.load(j, m + LX::kBytes, 0);
 #pragma unroll
@@ -505,7 +505,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p,
   const uint32_t c0 = (uint32_t)((uint64_t)total * blockIdx.y / gridDim.y);
   const uint32_t c1 = (uint32_t)((uint64_t)total * (blockIdx.y + 1) / gridDim.y);
   typename Tile::Acc acc;
-  Tile::run(p.a, p.b, p.k, c0, c1, m0, n0, a0, b0, a1, b1, acc);
+  Tile::run(p.a, p.b, p.k, p.terms, c0, c1, m0, n0, a0, b0, a1, b1, acc);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* lds = mma_epilogue_lds<Tile>(wave, a0, b0, a1, b1);
   p.out.c = static_cast<typename Elem<ODT>::type*>(p.out.c) + blockIdx.y * p.split_stride;

@@ -162,7 +162,8 @@ __device__ __forceinline__ void sched_lds_reads() {
 }
 
 // The loop: accumulators of chunks c0 .. c1 - 1 of the terms' chunks (term t's
-// are t * nch .. + nch - 1).  Terms: planes (0, 0), (0, 1), (1, 0).
+// are t * nch .. + nch - 1).  Terms: one, planes (0, 0); or three, (0, 1),
+// (1, 0) and then (0, 0), so that the small ones are rounded at their own size.
 //
 // Groups of products: one tile of 16 rows of A times all of the wavefront's B;
 // a chunk is two steps of HA groups.  A's operands are read DEPTH groups
@@ -182,8 +183,8 @@ struct MmaTile {
   static_assert(PA + PB <= PER_GROUP * GROUPS, "loads between two barriers");
   typedef v4f Acc[HA][HB];
 
-  static __device__ __forceinline__ void run(const MmaSide& sa, const MmaSide& sb, int64_t k, uint32_t c0, uint32_t c1,
-                                             int64_t m0, int64_t n0, uint8_t* a0, uint8_t* b0, uint8_t* a1,
+  static __device__ __forceinline__ void run(const MmaSide& sa, const MmaSide& sb, int64_t k, uint32_t terms,
+                                             uint32_t c0, uint32_t c1, int64_t m0, int64_t n0, uint8_t* a0, uint8_t* b0, uint8_t* a1,
                                              uint8_t* b1, Acc& acc) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     LA la(sa, m0, wave, lane);
@@ -191,11 +192,11 @@ struct MmaTile {
     const MmaRead<AKC, BM> ra(wave / WN * HA, lane);
     const MmaRead<BKC, BN> rb(wave % WN * HB, lane);
     const uint32_t nch = (uint32_t)((k + kMmaK - 1) / kMmaK);
-    uint32_t term = c0 / nch, kc = c0 % nch, chunks = c1 - c0;  // of the next chunk to load; chunks left
+    uint32_t term = c0 / nch + 3 - terms, kc = c0 % nch, chunks = c1 - c0;  // of the next chunk to load; chunks left
     auto seek = [&] {
       const uint32_t left = ((uint32_t)k - kc * kMmaK) * min(chunks, 1u);
-      la.seek(term >> 1, kc, left);
-      lb.seek(term & 1, kc, left);
+      la.seek(term == 1, kc, left);
+      lb.seek(term == 0, kc, left);
     };
     auto step = [&] {
       chunks -= min(chunks, 1u);

@@ -189,5 +189,7 @@ class PowerSGD:
 # gradients it reads, and the microscaled 4-bit operands and products.
 from .torch_ops import (GradientClip, MxTensor, mx_dequantize, mx_linear, mx_linear_backward,  # noqa: E402,F401
                         mx_linear_forward, mx_linear_train, mx_product, mx_quantize, mx_quantize_both, mx_quantize_t)
-# The two ends of the step: the loss over a vocabulary.
+# The two ends of the step: the loss over a vocabulary, and the orthogonalised
+# update of the weights.
+from .torch_muon import Muon, orthogonalize  # noqa: E402,F401
 from .torch_xent import cross_entropy, cross_entropy_train, linear_cross_entropy  # noqa: E402,F401
