@@ -622,7 +622,7 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
  * scale that is not finite); PSGD_ERR_WORKSPACE; PSGD_ERR_HIP.  All calls only
  * enqueue kernels.
  */
-#define PSGD_XENT_MAX_DIM 4000000
+#define PSGD_XENT_MAX_DIM 2000000
 typedef struct psgd_xent {
   int64_t tokens, vocab, dim;
   const void* x;

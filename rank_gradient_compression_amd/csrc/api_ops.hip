@@ -649,7 +649,8 @@ static psgd_status_t check_muon(const char* fn, int32_t n, const psgd_muon_tenso
     if (!finite(x.lr_scale) || !finite(o->lr * x.lr_scale)) return invalid(fn, "lr_scale is not finite");
     if (x.rows == 0 || x.cols == 0) continue;
     if (!x.param && !x.update) return invalid(fn, "a matrix has neither param nor update");
-    if (((x.rows + 127) / 128) * ((x.cols + 127) / 128) > (1 << 24) || std::min(x.rows, x.cols) > 300000)
+    // (the products' chunks are counted in 32 bits)
+    if ((x.rows / 128 + 1) * (x.cols / 128 + 1) * (std::max(x.rows, x.cols) / 64 + 1) * 3 > INT32_MAX)
       return invalid(fn, "a matrix is too large");
     const bool one = (!x.param || x.param_dtype == kBF16) && (!x.update || x.update_dtype == kBF16);
     const int pieces = o->pieces ? o->pieces : one ? 1 : 2;
@@ -658,6 +659,8 @@ static psgd_status_t check_muon(const char* fn, int32_t n, const psgd_muon_tenso
                               o->lr * x.lr_scale, x.grad_dtype, x.param ? x.param_dtype : kF32,
                               x.update ? x.update_dtype : kF32, pieces});
   }
+  // (a group of matrices has as many pieces throughout)
+  std::stable_sort(out->begin(), out->end(), [](const MuonTensor& x, const MuonTensor& y) { return x.pieces < y.pieces; });
   return PSGD_OK;
 }
 

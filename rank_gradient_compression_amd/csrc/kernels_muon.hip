@@ -32,7 +32,7 @@
 
 namespace psgd {
 
-constexpr int kSumGroups = 256;   // workgroups of one matrix's norm, at most
+constexpr int kSumGroups = 1024;  // workgroups of one matrix's norm, at most
 constexpr int kSumChunk = 8192;   // values of a workgroup at a time
 
 __host__ __device__ inline int64_t muon_ld(int64_t c) { return (c + 63) / 64 * 64; }
@@ -59,16 +59,37 @@ __device__ __forceinline__ float4 muon_load4(const void* p, int dtype, int64_t i
     return make_float4(Elem<kBF16>::up(h[0]), Elem<kBF16>::up(h[1]), Elem<kBF16>::up(h[2]), Elem<kBF16>::up(h[3]));
   return make_float4(Elem<kF16>::up(h[0]), Elem<kF16>::up(h[1]), Elem<kF16>::up(h[2]), Elem<kF16>::up(h[3]));
 }
+__device__ __forceinline__ float2 muon_load2(const void* p, int dtype, int64_t i) {
+  if (dtype == kF32) return *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i);
+  if (dtype == kBF16) return make_float2(Elem<kBF16>::up((uint16_t)w), Elem<kBF16>::up((uint16_t)(w >> 16)));
+  return make_float2(Elem<kF16>::up((uint16_t)w), Elem<kF16>::up((uint16_t)(w >> 16)));
+}
+__device__ __forceinline__ bool aligned2(const void* p, int dtype) {
+  return ((uintptr_t)p & (dtype == kF32 ? 7 : 3)) == 0;
+}
 __device__ __forceinline__ bool aligned4(const void* p, int dtype) {
   return ((uintptr_t)p & (dtype == kF32 ? 15 : 7)) == 0;
 }
 
-// The matrix whose range, from first(mat) on, holds workgroup or tile t.
-template <typename F>
-__device__ __forceinline__ int muon_find(const MuonArgs& p, int t, F first) {
-  int i = 0;
-  while (i + 1 < p.n && t >= first(p.mat[i + 1])) ++i;
-  return i;
+// The tables, from the arguments of one launch.
+__global__ __launch_bounds__(256) void k_muon_table(MuonTable p, MuonTable* t) {
+  const uint32_t* from = reinterpret_cast<const uint32_t*>(&p);
+  uint32_t* to = reinterpret_cast<uint32_t*>(t);
+  for (int i = threadIdx.x; i < (int)(sizeof p / 4); i += 256) to[i] = from[i];
+}
+
+__device__ __forceinline__ uint16_t* muon_at(const MuonArgs& p, uint32_t place) {
+  return reinterpret_cast<uint16_t*>(p.ws + (size_t)place * 256);
+}
+__device__ __forceinline__ uint16_t* muon_x(const MuonArgs& p, const MuonMat& t, bool next) {
+  return muon_at(p, p.odd != next ? t.x1 : t.x0);
+}
+
+// The last matrix whose range starts at t or before: every lane looks at one.
+__device__ __forceinline__ int muon_find(const int32_t (&starts)[kMuonGroup], int t) {
+  const int lane = threadIdx.x & 63;
+  return __popcll(__ballot(starts[min(lane, kMuonGroup - 1)] <= t && lane < kMuonGroup)) - 1;
 }
 
 __device__ __forceinline__ float muon_momentum(float mu, float m, float g) { return fmaf(mu, m, g); }
@@ -78,13 +99,14 @@ __device__ __forceinline__ float muon_update(const MuonArgs& p, bool has, float 
 
 // New momentum and the sum of squares of u, in fp64 and a fixed order.
 __global__ __launch_bounds__(256) void k_muon_norm(MuonArgs p) {
-  const int i = muon_find(p, blockIdx.x, [](const MuonMat& m) { return m.sum0; });
-  const MuonMat& t = p.mat[i];
+  const int i = muon_find(p.table->first[kNorm], blockIdx.x);
+  const int sum0 = p.table->first[kNorm][i], nsums = p.table->chunks[kNorm][i];
+  const MuonMat t = p.table->mat[i];
   const int64_t n = (int64_t)t.r * t.c;
   const bool has = t.mom != nullptr;
   const bool wide = (t.ldg == t.c || t.r == 1) && aligned4(t.grad, t.gdt) && (!has || aligned4(t.mom, kF32));
   double s = 0.0;
-  for (int64_t e0 = (int64_t)(blockIdx.x - t.sum0) * kSumChunk; e0 < n; e0 += (int64_t)t.nsums * kSumChunk) {
+  for (int64_t e0 = (int64_t)(blockIdx.x - sum0) * kSumChunk; e0 < n; e0 += (int64_t)nsums * kSumChunk) {
     if (wide && e0 + kSumChunk <= n) {
       float4 g[8], m[8];
 #pragma unroll
@@ -135,21 +157,16 @@ __device__ __forceinline__ void muon_pieces(const float (&v)[8], uint4* hi, uint
   __builtin_memcpy(hi, h, sizeof h);
   __builtin_memcpy(lo, l, sizeof l);
 }
-__device__ __forceinline__ void muon_add(float (&v)[8], float f, const uint16_t* p) {  // v += f * p[0..7]
-  uint16_t h[8];
-  __builtin_memcpy(h, __builtin_assume_aligned(p, 16), sizeof h);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = fmaf(f, Elem<kF16>::up(h[e]), v[e]);
-}
 
 // The first X, zeros behind a row's end: eight values a thread.
 __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
-  const int i = muon_find(p, blockIdx.x, [](const MuonMat& m) { return m.start0; });
-  const MuonMat& t = p.mat[i];
+  const int i = muon_find(p.table->first[kStart], blockIdx.x);
+  const int sum0 = p.table->first[kNorm][i], nsums = p.table->chunks[kNorm][i];
+  const MuonMat t = p.table->mat[i];
   __shared__ double part[4];
   {
     double s = 0.0;
-    for (int k = threadIdx.x; k < t.nsums; k += 256) s += p.sums[t.sum0 + k];
+    for (int k = threadIdx.x; k < nsums; k += 256) s += p.sums[sum0 + k];
 #pragma unroll
     for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
@@ -158,7 +175,7 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   const double norm = sqrt(part[0] + part[1] + part[2] + part[3]);
   // (a double: 1 over the norm of tiny gradients is no fp32 number)
   const double inv = (double)p.sx / (norm + (double)p.eps);
-  const int64_t ld = muon_ld(t.c), per = ld / 8, at = (int64_t)(blockIdx.x - t.start0) * 256 + threadIdx.x;
+  const int64_t ld = muon_ld(t.c), per = ld / 8, at = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * 256 + threadIdx.x;
   if (at >= t.r * per) return;
   const int64_t row = at / per, col = at % per * 8;
   const bool has = t.mom != nullptr;
@@ -166,6 +183,8 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   const int64_t ge = row * t.ldg + col, me = row * t.c + col;
   const bool wide = col + 8 <= t.c && t.c % 4 == 0 && t.ldg % 4 == 0 && aligned4(t.grad, t.gdt) &&
                     (!has || aligned4(t.mom, kF32));
+  const bool pairs = col + 8 <= t.c && t.c % 2 == 0 && t.ldg % 2 == 0 && aligned2(t.grad, t.gdt) &&
+                     (!has || aligned2(t.mom, kF32));
   if (wide) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -174,6 +193,16 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
       v[4 * h] = muon_update(p, has, g.x, m.x), v[4 * h + 1] = muon_update(p, has, g.y, m.y);
       v[4 * h + 2] = muon_update(p, has, g.z, m.z), v[4 * h + 3] = muon_update(p, has, g.w, m.w);
     }
+  } else if (pairs) {
+    float2 g[4], m[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      g[h] = muon_load2(t.grad, t.gdt, ge + 2 * h);
+      m[h] = has ? *reinterpret_cast<const float2*>(t.mom + me + 2 * h) : make_float2(0.f, 0.f);
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      v[2 * h] = muon_update(p, has, g[h].x, m[h].x), v[2 * h + 1] = muon_update(p, has, g[h].y, m[h].y);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -183,180 +212,317 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   for (int e = 0; e < 8; ++e) v[e] = col + e < t.c ? (float)((double)v[e] * inv) : 0.f;
   uint4 hi, lo;
   muon_pieces(v, &hi, &lo);
-  *reinterpret_cast<uint4*>(t.x0 + row * ld + col) = hi;
-  *reinterpret_cast<uint4*>(t.x0 + t.r * ld + row * ld + col) = lo;
+  uint16_t* const x = muon_at(p, t.x0) + row * 2 * ld + col;
+  *reinterpret_cast<uint4*>(x) = hi;
+  *reinterpret_cast<uint4*>(x + ld) = lo;
 }
 
 // ---------------------------------------------------------------- products
-enum { kGram, kPoly, kUpdate };
-
-// Tile number t of the upper triangle of nt x nt tiles, row by row.
-__device__ __forceinline__ void muon_sym_tile(int t, int nt, int* tm, int* tn) {
-  int m = 0;
-  while (t >= nt - m) t -= nt - m, ++m;
-  *tm = m;
-  *tn = m + t;
+// Tile t of those on and above the diagonal of ntm x ntn, RB times as high as
+// wide: groups of 8 tile rows, column by column, so that neighbours share their
+// operands in L2.
+template <int RB>
+__device__ __forceinline__ void muon_sym_tile(int t, int ntm, int ntn, int* tm, int* tn) {
+  for (int g = 0;; g += 8) {
+    const int h = min(8, ntm - g), cols = ntn - RB * g, edge = min(RB * h, cols);  // columns that the diagonal crosses
+    int c = 0;
+    for (; c < edge && t >= c / RB + 1; ++c) t -= c / RB + 1;
+    if (c < edge) {
+      *tm = g + t;
+      *tn = RB * g + c;
+      return;
+    }
+    if (t < h * (cols - edge)) {
+      *tm = g + t % h;
+      *tn = RB * g + edge + t / h;
+      return;
+    }
+    t -= h * (cols - edge);
+  }
 }
 
-// Eight finished values of row `row` from column `col` on.  acc: the product's.
-template <int OP>
-__device__ __forceinline__ void muon_finish(const MuonArgs& p, const MuonMat& t, int64_t row, int64_t col,
-                                            float (&v)[8]) {
-  const int64_t k = min(t.r, t.c), ldk = muon_ld(k), ld = muon_ld(t.c);
-  if constexpr (OP == kGram) {
+__device__ __forceinline__ void muon_add(float (&v)[8], float f, uint4 q) {  // v += f * eight halves
+  uint16_t h[8];
+  __builtin_memcpy(h, &q, sizeof h);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= p.sa / (p.sx * p.sx);
-  } else if constexpr (OP == kPoly) {
+  for (int e = 0; e < 8; ++e) v[e] = fmaf(f, Elem<kF16>::up(h[e]), v[e]);
+}
+
+// Eight neighbouring values of the caller's, n of them there.
+__device__ __forceinline__ void muon_save8(void* p, int dtype, int64_t i, const float (&v)[8], int n) {
+  uint8_t* at = static_cast<uint8_t*>(p) + i * dtype_bytes(dtype);
+  if (n >= 8 && ((uintptr_t)at & 15) == 0) {
+    if (dtype == kF32) {
+      __builtin_memcpy(__builtin_assume_aligned(at, 16), v, sizeof v);
+    } else {
+      uint16_t h[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= p.c * (p.sb / (p.sa * p.sa));
-    const float f = p.b * (p.sb / p.sa);
-    muon_add(v, f, t.a + row * ldk + col);
-    if (t.pieces == 2) muon_add(v, f, t.a + k * ldk + row * ldk + col);
+      for (int e = 0; e < 8; ++e) h[e] = dtype == kBF16 ? Elem<kBF16>::down(v[e]) : Elem<kF16>::down(v[e]);
+      __builtin_memcpy(__builtin_assume_aligned(at, 16), h, sizeof h);
+    }
   } else {
-    const float s = p.last ? 1.f / p.sx : 1.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= s / p.sb;
-    muon_add(v, p.a * s, t.x0 + row * ld + col);
-    muon_add(v, p.a * s, t.x0 + t.r * ld + row * ld + col);
+    for (int e = 0; e < 8; ++e)
+      if (e < n) muon_save(p, dtype, i + e, v[e]);
   }
-  if (OP == kUpdate && p.last) {
-    for (int e = 0; e < 8; ++e) {
-      if (col + e >= t.c) break;
-      if (t.upd) muon_save(t.upd, t.udt, row * t.ldu + col + e, v[e]);
-      if (t.param) {
-        const int64_t i = row * t.ldp + col + e;
-        muon_save(t.param, t.pdt, i, fmaf(p.decay, muon_load(t.param, t.pdt, i), -t.step * v[e]));
+}
+__device__ __forceinline__ void muon_load8(const void* p, int dtype, int64_t i, float (&v)[8], int n) {
+  const uint8_t* at = static_cast<const uint8_t*>(p) + i * dtype_bytes(dtype);
+  if (n >= 8 && ((uintptr_t)at & 15) == 0) {
+    if (dtype == kF32) {
+      __builtin_memcpy(v, __builtin_assume_aligned(at, 16), sizeof v);
+    } else {
+      uint16_t h[8];
+      __builtin_memcpy(h, __builtin_assume_aligned(at, 16), sizeof h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = dtype == kBF16 ? Elem<kBF16>::up(h[e]) : Elem<kF16>::up(h[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? muon_load(p, dtype, i + e) : 0.f;
+  }
+}
+
+// Results of 32 rows of one wavefront's columns from their sums, through LDS of
+// its own: eight neighbouring columns a lane, and, across the diagonal, 32
+// neighbouring rows.  What they are added to (A, or X) is asked for a piece
+// ahead.
+template <int OP, bool PAIR, int HB>
+struct MuonResults {
+  static constexpr int COLS = HB * 16, PITCH = COLS + 4, LPR = COLS / 8, RPI = 64 / LPR, Q = 32 / RPI;
+  static constexpr bool SYM = OP == kGram || OP == kPoly;
+  static_assert(COLS == 64, "a column a lane");
+  const MuonArgs& p;
+  const MuonMat& t;
+  int lane;
+  bool mirror;
+  int64_t k, rows, ld, pitch;  // (zeros behind a row's end as well; pieces side by side)
+  static constexpr bool TWO = !SYM || PAIR;
+  struct Old {
+    uint4 hi[Q], lo[Q];
+  };
+
+  __device__ __forceinline__ MuonResults(const MuonArgs& args, const MuonMat& mat, bool across)
+      : p(args), t(mat), lane(threadIdx.x & 63), mirror(SYM && across), k(min(mat.r, mat.c)) {
+    rows = SYM ? k : mat.r;
+    ld = muon_ld(SYM ? k : mat.c);
+    pitch = TWO ? 2 * ld : ld;
+  }
+  __device__ __forceinline__ void ask(int64_t row0, int64_t col0, Old& o) const {
+    if constexpr (OP != kGram) {
+      const uint16_t* at = (OP == kPoly ? muon_at(p, t.a) : muon_x(p, t, false)) + min(col0 + lane % LPR * 8, ld - 8);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const uint16_t* x = at + min(row0 + q * RPI + lane / LPR, rows - 1) * pitch;
+        o.hi[q] = *reinterpret_cast<const uint4*>(x);
+        if (TWO) o.lo[q] = *reinterpret_cast<const uint4*>(x + ld);
       }
     }
-    return;
   }
-  uint16_t* out = OP == kGram ? t.a + row * ldk + col : OP == kPoly ? t.b + row * ldk + col : t.x1 + row * ld + col;
-  uint4 hi, lo;
-  muon_pieces(v, &hi, &lo);
-  *reinterpret_cast<uint4*>(out) = hi;
-  if (OP == kUpdate)
-    *reinterpret_cast<uint4*>(out + t.r * ld) = lo;
-  else if (t.pieces == 2)
-    *reinterpret_cast<uint4*>(out + k * ldk) = lo;
-}
-
-// 32 values of column `row` of the tile, that is of row `row` across the
-// diagonal, from its column `col` on.
-template <int OP>
-__device__ __forceinline__ void muon_mirror(const MuonMat& t, int64_t row, int64_t col, const float (&v)[32]) {
-  const int64_t k = min(t.r, t.c), ldk = muon_ld(k);
-  uint16_t* out = (OP == kGram ? t.a : t.b) + row * ldk + col;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = v[q * 8 + e];
-    uint4 hi, lo;
-    muon_pieces(x, &hi, &lo);
-    *reinterpret_cast<uint4*>(out + q * 8) = hi;
-    if (t.pieces == 2) *reinterpret_cast<uint4*>(out + k * ldk + q * 8) = lo;
+  __device__ __forceinline__ static void meet() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
-}
-
-// A launch's tiles (blockIdx.x) times the pieces of the summed axis
-// (blockIdx.y).  PHASE 0: sums and results; 1: sums of one piece to memory, in
-// the lanes' own order; 2: those added in order, and results.
-template <int OP, int PHASE, int WM, int WN, int TM, int TN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_muon_product(MuonArgs p) {
-  using Wide = MmaTile<kF16, true, OP != kUpdate, WM, WN, TM, TN>;
-  using Tall = MmaTile<kF16, OP != kGram, OP != kGram, WM, WN, TM, TN>;
-  constexpr int HA = Wide::HA, HB = Wide::HB, BM = Wide::BM, BN = Wide::BN;
-  __shared__ __align__(16) uint8_t a0[BM * kMmaBytes], b0[BN * kMmaBytes], a1[BM * kMmaBytes], b1[BN * kMmaBytes];
-  const int tile = xcd_position(blockIdx.x, gridDim.x);
-  const int i = muon_find(p, tile, [](const MuonMat& m) { return OP == kUpdate ? m.full0 : m.sym0; });
-  const MuonMat& t = p.mat[i];
-  const int64_t k = min(t.r, t.c), ldk = muon_ld(k), ld = muon_ld(t.c);
-  const bool tall = t.r > t.c;
-  int tm, tn;
-  if constexpr (OP == kUpdate) {
-    const int ntm = (t.r + BM - 1) / BM, ntn = (t.c + BN - 1) / BN, at = tile - t.full0;
-    const int first = at / (8 * ntn) * 8, rows = min(8, ntm - first), in = at % (8 * ntn);
-    tm = first + in % rows;
-    tn = in / rows;
-  } else {
-    muon_sym_tile(tile - t.sym0, (int)((k + BM - 1) / BM), &tm, &tn);
-  }
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  typename Wide::Acc acc;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  v4f* const part = reinterpret_cast<v4f*>(p.partial) + (int64_t)tile * (BM * BN / 4) + wave * (HA * HB * 64) + lane;
-  const int64_t piece = (int64_t)p.tiles * (BM * BN / 4);
-  if constexpr (PHASE < 2) {
-    const MmaSide x{t.x0, t.r * ld, ld, OP == kGram ? k : tall ? t.r : t.c};
-    const MmaSide s{OP == kPoly ? t.a : t.b, k * ldk, ldk, k};
-    const int64_t sum = OP == kGram ? max(t.r, t.c) : k;
-    const uint32_t terms = t.pieces == 2 ? 3 : 1, total = (uint32_t)((sum + kMmaK - 1) / kMmaK) * terms;
-    const uint32_t c0 = (uint32_t)((uint64_t)total * blockIdx.y / gridDim.y);
-    const uint32_t c1 = (uint32_t)((uint64_t)total * (blockIdx.y + 1) / gridDim.y);
-    if constexpr (OP == kPoly) {
-      Wide::run(s, s, sum, terms, c0, c1, m0, n0, a0, b0, a1, b1, acc);
-    } else {
-      if (tall)
-        Tall::run(x, OP == kGram ? x : s, sum, terms, c0, c1, m0, n0, a0, b0, a1, b1, acc);
-      else
-        Wide::run(OP == kGram ? x : s, x, sum, terms, c0, c1, m0, n0, a0, b0, a1, b1, acc);
-    }
-  }
-  if constexpr (PHASE == 1) {
-#pragma unroll
-    for (int h = 0; h < HA * HB; ++h) part[blockIdx.y * piece + h * 64] = acc[h / HB][h % HB];
-    return;
-  }
-  if constexpr (PHASE == 2) {
-#pragma unroll
-    for (int h = 0; h < HA * HB; ++h) {
-      v4f v = part[h * 64];
-      for (int q = 1; q < p.splits; ++q) v += part[q * piece + h * 64];
-      acc[h / HB][h % HB] = v;
-    }
-  }
-  // Results, 32 rows of the wavefront's at a time, through LDS of its own: eight
-  // neighbouring columns a lane, and, across the diagonal, 32 neighbouring rows.
-  constexpr int COLS = HB * 16, PITCH = COLS + 4;
-  float* const lds = mma_epilogue_lds<Wide>(wave, a0, b0, a1, b1);
-  float* const wr = lds + (lane & 15) * PITCH + (lane >> 4) * 4;
-  const int64_t row0 = m0 + wave / WN * TM * 32, col0 = n0 + wave % WN * TN * 32;
-  const int64_t rows = OP == kUpdate ? t.r : k, cols = OP == kUpdate ? ld : ldk;  // (zeros behind the row's end as well)
-  const bool mirror = OP != kUpdate && tm != tn;
-#pragma unroll
-  for (int h = 0; h < HA / 2; ++h) {
+  __device__ __forceinline__ void put(float* lds, int64_t row0, int64_t col0, const v4f (&acc)[2][HB],
+                                      const Old& o) const {
+    if (row0 >= rows || col0 >= ld) return;
+    const int64_t col = col0 + lane % LPR * 8;
+    float* const wr = lds + (lane & 15) * PITCH + (lane >> 4) * 4;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int j = 0; j < HB; ++j) *reinterpret_cast<v4f*>(wr + q * 16 * PITCH + j * 16) = acc[h * 2 + q][j];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    constexpr int LPR = COLS / 8, RPI = 64 / LPR;
-#pragma unroll 1
-    for (int q = 0; q < 32 / RPI; ++q) {
+      for (int j = 0; j < HB; ++j) *reinterpret_cast<v4f*>(wr + q * 16 * PITCH + j * 16) = acc[q][j];
+    meet();
+    const float f = OP == kGram ? p.sa / (p.sx * p.sx) : OP == kPoly ? p.c * (p.sb / (p.sa * p.sa))
+                                                       : OP == kUpdate ? 1.f / p.sb : 1.f / (p.sb * p.sx);
+    const float g = OP == kPoly ? p.b * (p.sb / p.sa) : OP == kUpdate ? p.a : p.a / p.sx;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
       const int in = q * RPI + lane / LPR;
-      const int64_t row = row0 + h * 32 + in, col = col0 + lane % LPR * 8;
-      if (row >= rows || col >= cols) continue;
+      const int64_t row = row0 + in;
       float* const at = lds + in * PITCH + lane % LPR * 8;
       float v[8];
       __builtin_memcpy(v, __builtin_assume_aligned(at, 16), sizeof v);
-      muon_finish<OP>(p, t, row, col, v);
-      if (mirror) __builtin_memcpy(__builtin_assume_aligned(at, 16), v, sizeof v);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (mirror) {
-      const int64_t row = col0 + lane, col = row0 + h * 32;
-      if (row < k && col < ldk) {
-        float v[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = row0 + h * 32 + e < k ? lds[e * PITCH + lane] : 0.f;
-        muon_mirror<OP>(t, row, col, v);
+      for (int e = 0; e < 8; ++e) v[e] *= f;
+      if constexpr (OP != kGram) {
+        muon_add(v, g, o.hi[q]);
+        if (TWO) muon_add(v, g, o.lo[q]);
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      if (OP == kLast || mirror) __builtin_memcpy(__builtin_assume_aligned(at, 16), v, sizeof v);
+      if constexpr (OP != kLast) {
+        if (row < rows && col < ld) {
+          uint16_t* out = (OP == kUpdate ? muon_x(p, t, true) : muon_at(p, OP == kGram ? t.a : t.b)) + row * pitch + col;
+          uint4 h, l;
+          muon_pieces(v, &h, &l);
+          *reinterpret_cast<uint4*>(out) = h;
+          if (TWO) *reinterpret_cast<uint4*>(out + ld) = l;
+        }
+      }
+    }
+    meet();
+    if constexpr (OP == kLast) {
+      // (of any type and alignment: code too long to be there for each piece's rows)
+      const int n = (int)min((int64_t)8, t.c - col);
+#pragma unroll 1
+      for (int q = 0; q < Q; ++q) {
+        const int64_t row = row0 + q * RPI + lane / LPR;
+        if (row >= rows || n <= 0) continue;
+        float v[8], w[8];
+        __builtin_memcpy(v, __builtin_assume_aligned(lds + (q * RPI + lane / LPR) * PITCH + lane % LPR * 8, 16), sizeof v);
+        if (t.upd) muon_save8(t.upd, t.udt, row * t.ldu + col, v, n);
+        if (t.param) {
+          muon_load8(t.param, t.pdt, row * t.ldp + col, w, n);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = fmaf(p.decay, w[e], -t.step * v[e]);
+          muon_save8(t.param, t.pdt, row * t.ldp + col, w, n);
+        }
+      }
+      meet();
+    }
+    if (mirror) {
+      const int64_t mrow = col0 + lane;
+      if (mrow < k) {
+        uint16_t* const out = muon_at(p, OP == kGram ? t.a : t.b) + mrow * pitch + row0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = row0 + q * 8 + e < k ? lds[(q * 8 + e) * PITCH + lane] : 0.f;
+          uint4 h, l;
+          muon_pieces(v, &h, &l);
+          *reinterpret_cast<uint4*>(out + q * 8) = h;
+          if (TWO) *reinterpret_cast<uint4*>(out + ld + q * 8) = l;
+        }
+      }
+      meet();
     }
   }
+};
+
+struct MuonTile {
+  int tm, tn;
+};
+template <int OP, int BM, int BN>
+__device__ __forceinline__ MuonTile muon_tile(const MuonMat& t, int at) {  // tile `at` of the matrix
+  MuonTile r;
+  if constexpr (OP == kUpdate || OP == kLast) {
+    const int ntm = (t.r + BM - 1) / BM, ntn = (t.c + BN - 1) / BN;
+    const int first = at / (8 * ntn) * 8, rows = min(8, ntm - first), in = at % (8 * ntn);
+    r.tm = first + in % rows;
+    r.tn = in / rows;
+  } else {
+    muon_sym_tile<BM / BN>(at, (min(t.r, t.c) + BM - 1) / BM, (min(t.r, t.c) + BN - 1) / BN, &r.tm, &r.tn);
+  }
+  return r;
+}
+
+// First chunk of a share.
+__device__ __forceinline__ int muon_share(const MuonShares& s, int w) {
+  return s.chunk0 + (int)((int64_t)s.chunks * w / s.shares);
+}
+
+template <int OP, bool PAIR, int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_muon_product(MuonArgs p) {
+  using Wide = MmaTile<kF16, PAIR, true, OP == kGram || OP == kPoly, WM, WN, TM, TN>;
+  using Tall = MmaTile<kF16, PAIR, OP != kGram, OP != kGram, WM, WN, TM, TN>;
+  constexpr int HA = Wide::HA, HB = Wide::HB, BM = Wide::BM, BN = Wide::BN;
+  __shared__ __align__(16) uint8_t a0[BM * kMmaBytes], b0[BN * kMmaBytes], a1[BM * kMmaBytes], b1[BN * kMmaBytes];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  constexpr int KIND = OP == kLast ? kUpdate : OP;
+  const MuonTable& tab = *p.table;
+  // Whole tiles in blocks of 32 to an XCD (workgroups go to the eight XCDs in
+  // turn), shares in eighths; a share's chunks are those of tiles in a row.
+  int b = blockIdx.x, c, end;
+  const bool share = b >= p.sh.whole;
+  if (!share) {
+    const int x = b % 8, j = b / 8;
+    if (b < p.sh.whole / 256 * 256) b = (j / 32 * 8 + x) * 32 + j % 32;
+    const int i = muon_find(tab.first[KIND], b), n = tab.chunks[KIND][i];
+    c = tab.chunk0[KIND][i] + (b - tab.first[KIND][i]) * n;
+    end = c + n;
+  } else {
+    b = xcd_position(b - p.sh.whole, p.sh.shares);
+    c = muon_share(p.sh, b);
+    end = muon_share(p.sh, b + 1);
+  }
+  for (int slot = 0; c < end; slot = 1) {
+    const int i = muon_find(tab.chunk0[KIND], c), chunk0 = tab.chunk0[KIND][i], chunks = tab.chunks[KIND][i];
+    const MuonMat t = tab.mat[i];
+    const int c0 = (c - chunk0) % chunks, c1 = min(chunks, c0 + end - c);
+    const MuonTile at = muon_tile<OP, BM, BN>(t, (c - chunk0) / chunks);
+    const int64_t m0 = (int64_t)at.tm * BM, n0 = (int64_t)at.tn * BN;
+    const int64_t k = min(t.r, t.c), ldk = muon_ld(k), ld = muon_ld(t.c);
+    const bool tall = t.r > t.c;
+    const MmaSide x{muon_x(p, t, false), ld, 2 * ld, OP == kGram ? k : tall ? t.r : t.c};
+    const MmaSide s{muon_at(p, OP == kPoly ? t.a : t.b), ldk, PAIR ? 2 * ldk : ldk, k};
+    const int64_t sum = OP == kGram ? max(t.r, t.c) : k;
+    typename Wide::Acc acc;
+    if constexpr (OP == kPoly) {
+      Wide::run(s, s, sum, c0, c1, m0, n0, a0, b0, a1, b1, acc);
+    } else {
+      if (tall)
+        Tall::run(x, OP == kGram ? x : s, sum, c0, c1, m0, n0, a0, b0, a1, b1, acc);
+      else
+        Wide::run(OP == kGram ? x : s, x, sum, c0, c1, m0, n0, a0, b0, a1, b1, acc);
+    }
+    if (c1 - c0 == chunks) {
+      float* const lds = mma_epilogue_lds<Wide>(wave, a0, b0, a1, b1);
+      const MuonResults<OP, PAIR, HB> res(p, t, at.tn / (BM / BN) != at.tm);
+      const int64_t row0 = m0 + wave / WN * TM * 32, col0 = n0 + wave % WN * TN * 32;
+      typename MuonResults<OP, PAIR, HB>::Old old[2];
+      res.ask(row0, col0, old[0]);
+#pragma unroll
+      for (int h = 0; h < HA / 2; ++h) {
+        v4f piece[2][HB];
+#pragma unroll
+        for (int j = 0; j < HB; ++j) piece[0][j] = acc[2 * h][j], piece[1][j] = acc[2 * h + 1][j];
+        if (h + 1 < HA / 2) res.ask(row0 + (h + 1) * 32, col0, old[(h + 1) & 1]);
+        res.put(lds, row0 + h * 32, col0, piece, old[h & 1]);
+      }
+    } else {
+      v4f* const part = reinterpret_cast<v4f*>(p.parts) + (int64_t)(2 * b + slot) * (BM * BN / 4) +
+                        wave * (HA * HB * 64) + lane;
+#pragma unroll
+      for (int h = 0; h < HA * HB; ++h) part[h * 64] = acc[h / HB][h % HB];
+    }
+    c += c1 - c0;
+    if (share) __syncthreads();  // (the next tile's loads go where results passed)
+  }
+}
+
+// Tiles of several shares: their sums added in order.  One wavefront takes 32
+// rows of what one wavefront of the product had.
+template <int OP, bool PAIR, int WM, int WN, int TM, int TN>
+__global__ __launch_bounds__(64) void k_muon_join(MuonArgs p) {
+  constexpr int HB = 2 * TN, HA = 2 * TM, BM = WM * TM * 32, BN = WN * TN * 32, PIECES = WM * WN * TM;
+  __shared__ __align__(16) float lds[32 * (HB * 16 + 4)];
+  constexpr int KIND = OP == kLast ? kUpdate : OP;
+  const MuonTable& tab = *p.table;
+  const int tile = p.sh.whole + blockIdx.x / PIECES, wave = blockIdx.x % PIECES / TM, h = blockIdx.x % TM;
+  const int mat = muon_find(tab.first[KIND], tile), in = tile - tab.first[KIND][mat], chunks = tab.chunks[KIND][mat];
+  const MuonMat t = tab.mat[mat];
+  const MuonTile at = muon_tile<OP, BM, BN>(t, in);
+  const int c0 = tab.chunk0[KIND][mat] + in * chunks, c1 = c0 + chunks;
+  int w = (int)((int64_t)(c0 - p.sh.chunk0) * p.sh.shares / p.sh.chunks);  // (rounded down, so it may be one share early)
+  while (w + 1 < p.sh.shares && muon_share(p.sh, w + 1) <= c0) ++w;
+  if (muon_share(p.sh, w + 1) >= c1) return;  // one share did it all
+  const MuonResults<OP, PAIR, HB> res(p, t, at.tn / (BM / BN) != at.tm);
+  const int64_t row0 = (int64_t)at.tm * BM + wave / WN * TM * 32 + h * 32, col0 = (int64_t)at.tn * BN + wave % WN * TN * 32;
+  typename MuonResults<OP, PAIR, HB>::Old old;
+  res.ask(row0, col0, old);
+  v4f acc[2][HB];
+#pragma unroll
+  for (int i = 0; i < 2 * HB; ++i) acc[i / HB][i % HB] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int c = c0; c < c1; ++w) {
+    const int slot = c == muon_share(p.sh, w) ? 0 : 1;
+    const v4f* part = reinterpret_cast<const v4f*>(p.parts) + (int64_t)(2 * w + slot) * (BM * BN / 4) +
+                      wave * (HA * HB * 64) + h * 2 * HB * 64 + (threadIdx.x & 63);
+#pragma unroll
+    for (int i = 0; i < 2 * HB; ++i) acc[i / HB][i % HB] += part[i * 64];
+    c = muon_share(p.sh, w + 1);
+  }
+  res.put(lds, row0, col0, acc, old);
 }
 
 // ---------------------------------------------------------------- the host
@@ -390,56 +556,117 @@ bool muon_scales(const MuonOpts& o, float* sx, float* sa, float* sb) {
 // this many values ends (the workspace holds one group's X, A and B at a time).
 constexpr int64_t kGroupValues = int64_t(1) << 28;
 
+// The tiles that a launch may be made of, and what they cost as measured
+// (us): a chunk of a tile on a card full of such tiles, and what a tile takes
+// besides (first loads, results: of A and B, of X).
+struct MuonShape {
+  int bm, bn, slots;  // slots: workgroups that the card holds
+  double chunk, tile, update;
+};
+constexpr MuonShape kShapes[] = {
+    {256, 256, 256, 1.40, 10.0, 30.0}, {256, 128, 256, 0.85, 12.0, 22.0}, {128, 128, 512, 1.02, 8.0, 14.0}};
+constexpr double kJoin = 10.0, kJoinBytes = 4.0e6;  // a joining launch; bytes that parts move in a us
+
+struct MuonLaunch {
+  int shape;
+  MuonShares sh;
+};
 struct MuonGroup {
-  int first, n;
-  bool large;               // 256 x 256 tiles
-  int64_t sums, starts, sym, full;
-  int gram_splits, poly_splits, full_splits;
-  size_t sums_off, partial_off, mats_off, bytes;
+  int first, n, pieces;
+  std::vector<int> order;  // longest sums first
+  MuonLaunch gram, poly, full;
+  size_t sums_off, parts_off, mats_off, bytes;
 };
 
-static int64_t sym_tiles(int64_t k, int64_t b) { return cdiv(k, b) * (cdiv(k, b) + 1) / 2; }
+static int64_t norm_groups(const MuonTensor& t) { return std::min<int64_t>(kSumGroups, cdiv(t.r * t.c, kSumChunk)); }
+static int64_t start_groups(const MuonTensor& t) { return cdiv(t.r * (muon_ld(t.c) / 8), 256); }
+static int64_t op_tiles(const MuonTensor& t, int op, const MuonShape& s) {
+  if (op == kUpdate) return cdiv(t.r, s.bm) * cdiv(t.c, s.bn);
+  const int64_t k = std::min(t.r, t.c), m = cdiv(k, s.bm), n = cdiv(k, s.bn);
+  return m * n - s.bm / s.bn * (m * (m - 1) / 2);  // on and above the diagonal
+}
+static int64_t op_chunks(const MuonTensor& t, int op) {
+  return cdiv(op == kGram ? std::max(t.r, t.c) : std::min(t.r, t.c), t.pieces == 2 ? kMmaK<true> : kMmaK<false>);
+}
 
-// Pieces of the summed axis (of `chunks` chunks in the longest sum) for a
-// launch of so few tiles that most compute units would have none.
-static int splits_for(int64_t tiles, int64_t chunks, bool large) {
-  const int64_t slots = large ? 256 : 512;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({slots / tiles, chunks / 8, 16}));
+// The shape and the division that take least time by those figures.
+static MuonLaunch plan_launch(const std::vector<MuonTensor>& t, const MuonGroup& g, int op) {
+  MuonLaunch best{};
+  double least = 0.0;
+  const double per = g.pieces == 2 ? 1.5 : 1.0;  // (three products of 32 for two of 64)
+  for (int shape = 0; shape < 3; ++shape) {
+    const MuonShape& s = kShapes[shape];
+    const double tile = op == kUpdate ? s.update : s.tile;
+    int64_t tiles = 0, chunks = 0, longest = 0;
+    for (int i : g.order) {
+      const int64_t n = op_tiles(t[i], op, s), q = op_chunks(t[i], op);
+      tiles += n;
+      chunks += n * q;
+      longest = std::max(longest, q);
+    }
+    auto split = [&](int64_t whole) {  // the first `whole` tiles as they are, the rest shared
+      MuonShares h{};
+      h.tiles = (int32_t)tiles;
+      h.whole = (int32_t)whole;
+      int64_t at = 0, c = 0;
+      for (int i : g.order) {
+        const int64_t n = op_tiles(t[i], op, s), q = op_chunks(t[i], op), in = std::min(n, whole - at);
+        c += in * q;
+        at += in;
+      }
+      h.chunk0 = (int32_t)c;
+      h.chunks = (int32_t)(chunks - c);
+      h.shares = h.chunks ? (int32_t)std::max<int64_t>(1, std::min<int64_t>(s.slots, h.chunks / 6)) : 0;
+      return h;
+    };
+    auto consider = [&](int64_t whole) {
+      const MuonShares h = split(whole);
+      // (whole tiles: the average load, and at least the longest tile)
+      double us = 0.0;
+      if (whole) {
+        const double rounds = (double)cdiv(whole, s.slots);
+        us += std::max((double)h.chunk0 / (double)whole * rounds, (double)longest) * s.chunk * per + rounds * tile;
+      }
+      if (h.chunks) {
+        const double parts = h.shares > 1 ? std::min<double>(2.0 * h.shares, 2.0 * (double)(tiles - whole) + h.shares) : 0.0;
+        us += (double)h.chunks / h.shares * s.chunk * per + tile;
+        if (h.shares > 1) us += kJoin + parts * s.bm * s.bn * 8.0 / kJoinBytes;
+      }
+      if (least == 0.0 || us < least) least = us, best = {shape, h};
+    };
+    consider(tiles);
+    if (tiles % s.slots) consider(tiles / s.slots * s.slots);
+  }
+  return best;
 }
 
 static MuonGroup make_group(const std::vector<MuonTensor>& t, int first) {
   MuonGroup g{};
   g.first = first;
-  int64_t values = 0, sym256 = 0;
-  for (int i = first; i < (int)t.size() && g.n < kMuonGroup; ++i) {
-    const int64_t n = t[i].r * t[i].c;
-    if (g.n && values + n > kGroupValues) break;
-    values += n;
-    ++g.n;
-    sym256 += sym_tiles(std::min(t[i].r, t[i].c), 256);
-  }
-  g.large = sym256 >= 128;
-  const int64_t b = g.large ? 256 : 128;
-  int64_t gram = 0, poly = 0;
+  g.pieces = t[(size_t)first].pieces;
+  int64_t values = 0, sums = 0;
   size_t mats = 0;
-  for (int i = first; i < first + g.n; ++i) {
-    const int64_t r = t[i].r, c = t[i].c, k = std::min(r, c), terms = t[i].pieces == 2 ? 3 : 1;
-    g.sums += std::min<int64_t>(kSumGroups, cdiv(r * c, kSumChunk));
-    g.starts += cdiv(r * (muon_ld(c) / 8), 256);
-    g.sym += sym_tiles(k, b);
-    g.full += cdiv(r, b) * cdiv(c, b);
-    gram = std::max(gram, cdiv(std::max(r, c), kMmaK) * terms);
-    poly = std::max(poly, cdiv(k, kMmaK) * terms);
+  for (int i = first; i < (int)t.size() && g.n < kMuonGroup; ++i) {
+    const int64_t r = t[i].r, c = t[i].c, k = std::min(r, c);
+    if (g.n && (values + r * c > kGroupValues || t[i].pieces != g.pieces)) break;
+    values += r * c;
+    ++g.n;
+    g.order.push_back(i);
+    sums += norm_groups(t[i]);
     mats += 2 * up256((size_t)r * muon_ld(c) * 4) + 2 * up256((size_t)k * muon_ld(k) * 2 * t[i].pieces);
   }
-  g.gram_splits = splits_for(g.sym, gram, g.large);
-  g.poly_splits = splits_for(g.sym, poly, g.large);
-  g.full_splits = splits_for(g.full, poly, g.large);
-  const int64_t tiles = std::max({g.gram_splits > 1 ? g.gram_splits * g.sym : 0, g.poly_splits > 1 ? g.poly_splits * g.sym : 0,
-                                  g.full_splits > 1 ? g.full_splits * g.full : 0});
-  g.sums_off = 0;
-  g.partial_off = up256((size_t)g.sums * sizeof(double));
-  g.mats_off = g.partial_off + up256((size_t)tiles * b * b * sizeof(float));
+  std::stable_sort(g.order.begin(), g.order.end(), [&](int x, int y) {
+    return std::min(t[x].r, t[x].c) > std::min(t[y].r, t[y].c);
+  });
+  g.gram = plan_launch(t, g, kGram);
+  g.poly = plan_launch(t, g, kPoly);
+  g.full = plan_launch(t, g, kUpdate);
+  size_t parts = 0;
+  for (const MuonLaunch* l : {&g.gram, &g.poly, &g.full})
+    parts = std::max(parts, (size_t)2 * l->sh.shares * kShapes[l->shape].bm * kShapes[l->shape].bn * sizeof(float));
+  g.sums_off = up256(sizeof(MuonTable));
+  g.parts_off = g.sums_off + up256((size_t)sums * sizeof(double));
+  g.mats_off = g.parts_off + up256(parts);
   g.bytes = g.mats_off + mats;
   return g;
 }
@@ -454,68 +681,85 @@ size_t muon_workspace(const std::vector<MuonTensor>& t) {
   return bytes;
 }
 
-template <int OP, int WM, int WN, int TM, int TN>
-static void product(MuonArgs p, int64_t tiles, int splits, hipStream_t s) {
-  const dim3 b(64 * WM * WN);
-  p.splits = splits;
-  p.tiles = (int32_t)tiles;
-  if (splits == 1) {
-    hipLaunchKernelGGL((k_muon_product<OP, 0, WM, WN, TM, TN>), dim3((unsigned)tiles), b, 0, s, p);
-  } else {
-    hipLaunchKernelGGL((k_muon_product<OP, 1, WM, WN, TM, TN>), dim3((unsigned)tiles, (unsigned)splits), b, 0, s, p);
-    hipLaunchKernelGGL((k_muon_product<OP, 2, WM, WN, TM, TN>), dim3((unsigned)tiles), b, 0, s, p);
-  }
+template <int OP, bool PAIR, int WM, int WN, int TM, int TN>
+static void product(const MuonArgs& p, hipStream_t s) {
+  hipLaunchKernelGGL((k_muon_product<OP, PAIR, WM, WN, TM, TN>), dim3((unsigned)(p.sh.whole + p.sh.shares)),
+                     dim3(64 * WM * WN), 0, s, p);
+  if (p.sh.shares > 1)
+    hipLaunchKernelGGL((k_muon_join<OP, PAIR, WM, WN, TM, TN>), dim3((unsigned)((p.sh.tiles - p.sh.whole) * WM * WN * TM)),
+                       dim3(64), 0, s, p);
+}
+template <int OP, bool PAIR>
+static void product_in(const MuonArgs& p, int shape, hipStream_t s) {
+  if (shape == 0)
+    product<OP, PAIR, 2, 4, 4, 2>(p, s);
+  else if (shape == 1)
+    product<OP, PAIR, 4, 2, 2, 2>(p, s);
+  else
+    product<OP, PAIR, 2, 2, 2, 2>(p, s);
 }
 template <int OP>
-static void product_of(const MuonArgs& p, bool large, int64_t tiles, int splits, hipStream_t s) {
-  if (large)
-    product<OP, 2, 4, 4, 2>(p, tiles, splits, s);
+static void product_of(MuonArgs& p, const MuonGroup& g, const MuonLaunch& l, hipStream_t s) {
+  p.sh = l.sh;
+  if (g.pieces == 2)
+    product_in<OP, true>(p, l.shape, s);
   else
-    product<OP, 2, 2, 2, 2>(p, tiles, splits, s);
+    product_in<OP, false>(p, l.shape, s);
 }
 
 hipError_t launch_muon(const std::vector<MuonTensor>& t, const MuonOpts& o, void* workspace, hipStream_t s) {
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   for (int first = 0; first < (int)t.size();) {
     const MuonGroup g = make_group(t, first);
+    MuonTable* const table = reinterpret_cast<MuonTable*>(ws);
+    MuonTable m{};
+    for (int k = 0; k < kMuonKinds; ++k)
+      for (int i = 0; i < kMuonGroup; ++i) m.first[k][i] = m.chunk0[k][i] = INT32_MAX, m.chunks[k][i] = 1;
+    size_t at = g.mats_off / 256;
+    auto take = [&](size_t bytes) {
+      const size_t was = at;
+      at += up256(bytes) / 256;
+      return (uint32_t)was;
+    };
+    int64_t next[kMuonKinds] = {}, chunk[kMuonKinds] = {};
+    for (int i = 0; i < g.n; ++i) {
+      const MuonTensor& x = t[(size_t)g.order[(size_t)i]];
+      const int64_t k = std::min(x.r, x.c);
+      const size_t xb = (size_t)x.r * muon_ld(x.c) * 4, kb = (size_t)k * muon_ld(k) * 2 * x.pieces;
+      MuonMat& q = m.mat[i];
+      q.grad = x.grad, q.mom = x.mom, q.param = x.param, q.upd = x.upd;
+      q.x0 = take(xb), q.x1 = take(xb), q.a = take(kb), q.b = take(kb);
+      q.ldg = x.ldg, q.ldp = x.ldp, q.ldu = x.ldu, q.r = (int32_t)x.r, q.c = (int32_t)x.c, q.step = x.step;
+      q.gdt = (uint8_t)x.gdt, q.pdt = (uint8_t)x.pdt, q.udt = (uint8_t)x.udt, q.pieces = (uint8_t)x.pieces;
+      for (int kind = 0; kind < kMuonKinds; ++kind) {
+        const MuonLaunch* l = kind == kGram ? &g.gram : kind == kPoly ? &g.poly : &g.full;
+        const int64_t n = kind == kNorm ? norm_groups(x) : kind == kStart ? start_groups(x) : op_tiles(x, kind, kShapes[l->shape]);
+        const int64_t c = kind == kNorm ? n : kind == kStart ? 1 : op_chunks(x, kind);
+        m.first[kind][i] = (int32_t)next[kind];
+        m.chunk0[kind][i] = (int32_t)chunk[kind];
+        m.chunks[kind][i] = (int32_t)c;
+        next[kind] += n;
+        chunk[kind] += n * c;
+      }
+    }
+    hipLaunchKernelGGL(k_muon_table, dim3(1), dim3(256), 0, s, m, table);
     MuonArgs p{};
-    p.n = g.n;
+    p.table = table;
+    p.ws = ws;
     p.nesterov = o.nesterov, p.mu = o.mu, p.decay = o.decay, p.a = o.a, p.b = o.b, p.c = o.c, p.eps = o.eps;
     muon_scales(o, &p.sx, &p.sa, &p.sb);
     p.sums = reinterpret_cast<double*>(ws + g.sums_off);
-    p.partial = reinterpret_cast<float*>(ws + g.partial_off);
-    uint8_t* at = ws + g.mats_off;
-    auto take = [&](size_t bytes) {
-      uint16_t* const q = reinterpret_cast<uint16_t*>(at);
-      at += up256(bytes);
-      return q;
-    };
-    const int64_t b = g.large ? 256 : 128;
-    int32_t sum0 = 0, start0 = 0, sym0 = 0, full0 = 0;
-    for (int i = 0; i < g.n; ++i) {
-      const MuonTensor& x = t[(size_t)(first + i)];
-      const int64_t k = std::min(x.r, x.c);
-      const size_t xb = (size_t)x.r * muon_ld(x.c) * 4, kb = (size_t)k * muon_ld(k) * 2 * x.pieces;
-      MuonMat& m = p.mat[i];
-      m.grad = x.grad, m.mom = x.mom, m.param = x.param, m.upd = x.upd;
-      m.x0 = take(xb), m.x1 = take(xb), m.a = take(kb), m.b = take(kb);
-      m.ldg = x.ldg, m.ldp = x.ldp, m.ldu = x.ldu, m.r = (int32_t)x.r, m.c = (int32_t)x.c, m.step = x.step;
-      m.gdt = (uint8_t)x.gdt, m.pdt = (uint8_t)x.pdt, m.udt = (uint8_t)x.udt, m.pieces = (uint8_t)x.pieces;
-      m.sum0 = sum0, m.nsums = (int32_t)std::min<int64_t>(kSumGroups, cdiv(x.r * x.c, kSumChunk));
-      m.start0 = start0, m.sym0 = sym0, m.full0 = full0;
-      sum0 += m.nsums;
-      start0 += (int32_t)cdiv(x.r * (muon_ld(x.c) / 8), 256);
-      sym0 += (int32_t)sym_tiles(k, b);
-      full0 += (int32_t)(cdiv(x.r, b) * cdiv(x.c, b));
-    }
-    hipLaunchKernelGGL(k_muon_norm, dim3((unsigned)g.sums), dim3(256), 0, s, p);
-    hipLaunchKernelGGL(k_muon_start, dim3((unsigned)g.starts), dim3(256), 0, s, p);
+    p.parts = reinterpret_cast<float*>(ws + g.parts_off);
+    hipLaunchKernelGGL(k_muon_norm, dim3((unsigned)next[kNorm]), dim3(256), 0, s, p);
+    hipLaunchKernelGGL(k_muon_start, dim3((unsigned)next[kStart]), dim3(256), 0, s, p);
     for (int step = 0; step < o.steps; ++step) {
-      p.last = step + 1 == o.steps;
-      product_of<kGram>(p, g.large, g.sym, g.gram_splits, s);
-      product_of<kPoly>(p, g.large, g.sym, g.poly_splits, s);
-      product_of<kUpdate>(p, g.large, g.full, g.full_splits, s);
-      for (int i = 0; i < g.n; ++i) std::swap(p.mat[i].x0, p.mat[i].x1);
+      product_of<kGram>(p, g, g.gram, s);
+      product_of<kPoly>(p, g, g.poly, s);
+      if (step + 1 < o.steps)
+        product_of<kUpdate>(p, g, g.full, s);
+      else
+        product_of<kLast>(p, g, g.full, s);
+      p.odd = !p.odd;
     }
     first += g.n;
   }

@@ -17,7 +17,7 @@
 // that the products take; the target's entry, which would cancel, is formed
 // from the loss, exp(-loss) - 1, instead.  Sums, maxima and products are fp32.
 //
-// fp32 tensors are split into two fp16 planes (psgd_mma_device.h) under one
+// fp32 tensors are split into two fp16 pieces (psgd_mma_device.h) under one
 // power of two that brings the largest finite value to 2^13 .. 2^14.
 
 #include <hip/hip_runtime.h>
@@ -134,7 +134,8 @@ __global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool 
   sc[kAlphaB] = (float)ldexp(s, -eg);
 }
 
-// Rows to operands: `parts` planes of 16 bits, zeros behind the row's end.  One
+// Rows to operands: 16-bit values, or two pieces of fp32 ones side by side,
+// zeros behind the row's end.  One
 // thread = 8 values.  clean: rows of ignored tokens become zero in a second
 // copy, the one that dw's product takes: their G is zero, and zero times what
 // such a row may hold need not be.
@@ -168,10 +169,10 @@ __global__ __launch_bounds__(256) void k_xent_pack(const void* x, int64_t ld, in
   } else {
     __builtin_memcpy(hi, v, sizeof hi);
   }
-  const int64_t at = row * dp + c, plane = rows * dp;
+  const int64_t at = row * dp * (DT == kF32 ? 2 : 1) + c;
   if (out) {
     __builtin_memcpy(out + at, hi, sizeof hi);
-    if constexpr (DT == kF32) __builtin_memcpy(out + plane + at, lo, sizeof lo);
+    if constexpr (DT == kF32) __builtin_memcpy(out + dp + at, lo, sizeof lo);
   }
   if (clean) {
     if (ignored(targets[row], ignore)) {
@@ -179,7 +180,7 @@ __global__ __launch_bounds__(256) void k_xent_pack(const void* x, int64_t ld, in
       for (int e = 0; e < 8; ++e) hi[e] = lo[e] = 0;
     }
     __builtin_memcpy(clean + at, hi, sizeof hi);
-    if constexpr (DT == kF32) __builtin_memcpy(clean + plane + at, lo, sizeof lo);
+    if constexpr (DT == kF32) __builtin_memcpy(clean + dp + at, lo, sizeof lo);
   }
 }
 
@@ -187,7 +188,6 @@ __global__ __launch_bounds__(256) void k_xent_pack(const void* x, int64_t ld, in
 struct XentTile {
   MmaSide x, w;
   int64_t t, v, d;  // tokens of the block
-  int terms;
   const float* sc;
   const void* bias;
   int bias_dtype;
@@ -254,23 +254,22 @@ __device__ __forceinline__ void xent_bias(const XentTile& p, int64_t col0, int g
   }
 }
 
-template <int DT, int KEEP, int WM, int WN, int TM, int TN>
+template <int DT, bool PAIR, int KEEP, int WM, int WN, int TM, int TN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_logits(XentTile p, int ntm, int ntn) {
-  using Tile = MmaTile<DT, true, true, WM, WN, TM, TN>;
+  using Tile = MmaTile<DT, PAIR, true, true, WM, WN, TM, TN>;
   __shared__ __align__(16) uint8_t a0[Tile::BM * kMmaBytes], b0[Tile::BN * kMmaBytes], a1[Tile::BM * kMmaBytes],
       b1[Tile::BN * kMmaBytes];
   int tm, tn;
   mma_tile_of_block(blockIdx.x, ntm, ntn, &tm, &tn);
-  const uint32_t nch = (uint32_t)((p.d + kMmaK - 1) / kMmaK);
   typename Tile::Acc acc;
-  Tile::run(p.x, p.w, p.d, p.terms, 0, nch * p.terms, (int64_t)tm * Tile::BM, (int64_t)tn * Tile::BN, a0, b0, a1, b1, acc);
+  Tile::run(p.x, p.w, p.d, 0, (uint32_t)((p.d + Tile::K - 1) / Tile::K), (int64_t)tm * Tile::BM, (int64_t)tn * Tile::BN, a0, b0, a1, b1, acc);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int64_t row0 = (int64_t)tm * Tile::BM + wave / WN * TM * 32 + r;
   const int64_t col0 = (int64_t)tn * Tile::BN + wave % WN * TN * 32;
   if (col0 >= p.v) return;
   v4f bias[Tile::HB];
   xent_bias<Tile::HB>(p, col0, g, bias);
-  const float is = p.terms > 1 ? p.sc[kInvSx] : 1.f, iw = p.terms > 1 ? p.sc[kInvSw] : 1.f;
+  const float is = PAIR ? p.sc[kInvSx] : 1.f, iw = PAIR ? p.sc[kInvSw] : 1.f;
 #pragma unroll
   for (int i = 0; i < Tile::HA; ++i) {
     const int64_t row = row0 + i * 16;
@@ -290,11 +289,11 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int DT, int KEEP, int MT>
+template <int DT, bool PAIR, int KEEP, int MT>
 __global__ __launch_bounds__(512, 1) void k_xent_logits_few(XentTile p) {
   constexpr int WAVES = 8, HB = 2;
-  using LX = MmaLoad<true, MT * 16, 1>;
-  using LW = MmaLoad<true, 32, 1>;
+  using LX = MmaLoad<PAIR, true, MT * 16, 1>;
+  using LW = MmaLoad<PAIR, true, 32, 1>;
   constexpr int STAGE = LX::kBytes + LW::kBytes, LOADS = LX::kLoads + LW::kLoads, TILES = MT * HB;
   static_assert(TILES * 1024 <= 2 * STAGE, "no room for the partial tiles");
   __shared__ __align__(16) uint8_t st0[WAVES * STAGE], st1[WAVES * STAGE];
@@ -305,12 +304,12 @@ __global__ __launch_bounds__(512, 1) void k_xent_logits_few(XentTile p) {
   LW lw(p.w, col0, 0, lane);
   const MmaRead<true, MT * 16> rx(0, lane);
   const MmaRead<true, 32> rw(0, lane);
-  const uint32_t nch = (uint32_t)((p.d + kMmaK - 1) / kMmaK), total = nch * p.terms;
+  const uint32_t total = (uint32_t)((p.d + LX::K - 1) / LX::K);
   uint8_t *const m0 = st0 + wave * STAGE, *const m1 = st1 + wave * STAGE;
   auto fetch = [&](uint32_t c, uint8_t* m) {
-    const uint32_t term = c / nch + 3 - p.terms, kc = c % nch, left = c < total ? (uint32_t)p.d - kc * kMmaK : 0;
-    lx.seek(term == 1, kc, left);
-    lw.seek(term == 0, kc, left);
+    const uint32_t at = min(c, total - 1), left = c < total ? (uint32_t)p.d - at * LX::K : 0;
+    lx.seek(at, left);
+    lw.seek(at, left);
 #pragma unroll
     for (int j = 0; j < LW::kLoads; ++j) lw.load(j, m + LX::kBytes, 0);
 #pragma unroll
@@ -320,16 +319,22 @@ __global__ __launch_bounds__(512, 1) void k_xent_logits_few(XentTile p) {
 #pragma unroll
   for (int i = 0; i < TILES; ++i) acc[i / HB][i % HB] = v4f{0.f, 0.f, 0.f, 0.f};
   auto chunk = [&](const uint8_t* m) {
+    uint4 b[2][HB];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint4 b[HB];
+    for (int j = 0; j < 2 * HB; ++j) b[j / HB][j % HB] = rw(m + LX::kBytes, j / HB, j % HB);
 #pragma unroll
-      for (int j = 0; j < HB; ++j) b[j] = rw(m + LX::kBytes, s, j);
+    for (int i = 0; i < MT; ++i) {
+      const uint4 a0 = rx(m, 0, i), a1 = rx(m, 1, i);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const uint4 a = rx(m, s, i);
-#pragma unroll
-        for (int j = 0; j < HB; ++j) acc[i][j] = mma16<DT>(b[j], a, acc[i][j]);
+      for (int j = 0; j < HB; ++j) {
+        if constexpr (PAIR) {
+          acc[i][j] = mma16<DT>(b[1][j], a0, acc[i][j]);
+          acc[i][j] = mma16<DT>(b[0][j], a1, acc[i][j]);
+          acc[i][j] = mma16<DT>(b[0][j], a0, acc[i][j]);
+        } else {
+          acc[i][j] = mma16<DT>(b[0][j], a0, acc[i][j]);
+          acc[i][j] = mma16<DT>(b[1][j], a1, acc[i][j]);
+        }
       }
     }
   };
@@ -357,7 +362,7 @@ __global__ __launch_bounds__(512, 1) void k_xent_logits_few(XentTile p) {
 #pragma unroll
   for (int i = 0; i < TILES; ++i) *at(wave * TILES + i) = acc[i / HB][i % HB];
   __syncthreads();
-  const float is = p.terms > 1 ? p.sc[kInvSx] : 1.f, iw = p.terms > 1 ? p.sc[kInvSw] : 1.f;
+  const float is = PAIR ? p.sc[kInvSx] : 1.f, iw = PAIR ? p.sc[kInvSw] : 1.f;
   for (int i = wave; i < MT; i += WAVES) {
     if (i * 16 >= p.t) break;
     v4f v[HB], bias[HB];
@@ -406,14 +411,14 @@ struct XentGrad {
   const int64_t* targets;
   int64_t ignore;
   void* e;       // fp16 (G in its place) or fp32
-  uint16_t* g;   // G, or its two planes
+  uint16_t* g;   // G, or its two pieces side by side
   float* db;     // partial sums, or null
 };
 
 // E to G, eight columns a thread, kGradRows tokens a workgroup one after the
 // other: two readings of a line's worth are under way while one is worked on.
 // A workgroup's columns' sums go to its row of db.
-template <int DT>  // of G: kF16 and kBF16 in E's place, kF32 as two planes
+template <int DT>  // of G: kF16 and kBF16 in E's place, kF32 as two pieces
 __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
   const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, t0 = (int64_t)blockIdx.y * kGradRows;
   if (c >= p.vp) return;
@@ -457,12 +462,13 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
         const float r = v[e] - Elem<kF16>::up(h[e]);
         lo[e] = Elem<kF16>::down(r == r ? r : 0.f);
       }
-      __builtin_memcpy(p.g + p.t * p.vp + at, lo, sizeof lo);
+      __builtin_memcpy(p.g + row * 2 * p.vp + p.vp + c, lo, sizeof lo);
+      __builtin_memcpy(p.g + row * 2 * p.vp + c, h, sizeof h);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] = Elem<DT>::down(v[e]);
+      __builtin_memcpy(p.g + at, h, sizeof h);
     }
-    __builtin_memcpy(p.g + at, h, sizeof h);
   }
   if (p.db) {
     float* d = p.db + (int64_t)blockIdx.y * p.vp + c;
@@ -487,25 +493,24 @@ __global__ __launch_bounds__(256) void k_xent_db(const float* part, int64_t rows
 struct XentProduct {
   MmaSide a, b;
   int64_t k;
-  int terms;
   const float* alpha;  // or null: 1
   MmaOut out;
   int64_t split_stride;  // elements between the results of two pieces of the summed axis (gridDim.y of them)
 };
 
-template <int DT, int ODT, bool AKC, int WM, int WN, int TM, int TN>
+template <int DT, bool PAIR, int ODT, bool AKC, int WM, int WN, int TM, int TN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p, int ntm, int ntn) {
-  using Tile = MmaTile<DT, AKC, false, WM, WN, TM, TN>;
+  using Tile = MmaTile<DT, PAIR, AKC, false, WM, WN, TM, TN>;
   __shared__ __align__(16) uint8_t a0[Tile::BM * kMmaBytes], b0[Tile::BN * kMmaBytes], a1[Tile::BM * kMmaBytes],
       b1[Tile::BN * kMmaBytes];
   int tm, tn;
   mma_tile_of_block(blockIdx.x, ntm, ntn, &tm, &tn);
   const int64_t m0 = (int64_t)tm * Tile::BM, n0 = (int64_t)tn * Tile::BN;
-  const uint32_t total = (uint32_t)((p.k + kMmaK - 1) / kMmaK) * p.terms;
+  const uint32_t total = (uint32_t)((p.k + Tile::K - 1) / Tile::K);
   const uint32_t c0 = (uint32_t)((uint64_t)total * blockIdx.y / gridDim.y);
   const uint32_t c1 = (uint32_t)((uint64_t)total * (blockIdx.y + 1) / gridDim.y);
   typename Tile::Acc acc;
-  Tile::run(p.a, p.b, p.k, p.terms, c0, c1, m0, n0, a0, b0, a1, b1, acc);
+  Tile::run(p.a, p.b, p.k, c0, c1, m0, n0, a0, b0, a1, b1, acc);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* lds = mma_epilogue_lds<Tile>(wave, a0, b0, a1, b1);
   p.out.c = static_cast<typename Elem<ODT>::type*>(p.out.c) + blockIdx.y * p.split_stride;
@@ -554,7 +559,7 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   if (train) l.block = std::min(l.block, std::max<int64_t>(256, kBlockBytes / (l.vp * (f32 ? 8 : 2)) / 256 * 256));
   l.seg_shift = a.t <= kFewTokens ? 5 : 6;
   l.nseg = cdiv(a.v, int64_t(1) << l.seg_shift);
-  const int64_t tiles = cdiv(l.block, 128) * cdiv(a.d, 128), chunks = cdiv(a.v, kMmaK) * (f32 ? 3 : 1);
+  const int64_t tiles = cdiv(l.block, 128) * cdiv(a.d, 128), chunks = cdiv(a.v, f32 ? kMmaK<true> : kMmaK<false>);
   l.dx_splits = std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, tiles), chunks / 8, 128}));
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -597,66 +602,66 @@ static void pack_any(const void* x, int64_t ld, int64_t rows, int64_t dp, const 
     pack<kF16>(x, ld, rows, a.d, dp, scale, out, clean, a, s);
 }
 
-template <int DT, int KEEP>
+template <int DT, bool PAIR, int KEEP>
 static void logits(const XentTile& p, int64_t tokens, hipStream_t s) {
   if (tokens <= kFewTokens) {
     const dim3 g((unsigned)cdiv(p.v, 32)), b(512);
     if (p.t <= 16)
-      hipLaunchKernelGGL((k_xent_logits_few<DT, KEEP, 1>), g, b, 0, s, p);
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 1>), g, b, 0, s, p);
     else
-      hipLaunchKernelGGL((k_xent_logits_few<DT, KEEP, 2>), g, b, 0, s, p);
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 2>), g, b, 0, s, p);
     return;
   }
   if (cdiv(p.t, 256) * cdiv(p.v, 256) >= 256) {
     const int ntm = (int)cdiv(p.t, 256), ntn = (int)cdiv(p.v, 256);
-    hipLaunchKernelGGL((k_xent_logits<DT, KEEP, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
+    hipLaunchKernelGGL((k_xent_logits<DT, PAIR, KEEP, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
   } else {
     const int ntm = (int)cdiv(p.t, 128), ntn = (int)cdiv(p.v, 128);
-    hipLaunchKernelGGL((k_xent_logits<DT, KEEP, 2, 2, 2, 2>), dim3(ntm * ntn), dim3(256), 0, s, p, ntm, ntn);
+    hipLaunchKernelGGL((k_xent_logits<DT, PAIR, KEEP, 2, 2, 2, 2>), dim3(ntm * ntn), dim3(256), 0, s, p, ntm, ntn);
   }
 }
 
-template <int DT, int ODT, bool AKC>
+template <int DT, bool PAIR, int ODT, bool AKC>
 static void product_to(const XentProduct& p, int64_t pieces, hipStream_t s) {
   if (pieces == 1 && cdiv(p.out.m, 256) * cdiv(p.out.n, 256) >= 192) {
     const int ntm = (int)cdiv(p.out.m, 256), ntn = (int)cdiv(p.out.n, 256);
-    hipLaunchKernelGGL((k_xent_product<DT, ODT, AKC, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
+    hipLaunchKernelGGL((k_xent_product<DT, PAIR, ODT, AKC, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
   } else {
     const int ntm = (int)cdiv(p.out.m, 128), ntn = (int)cdiv(p.out.n, 128);
-    hipLaunchKernelGGL((k_xent_product<DT, ODT, AKC, 2, 2, 2, 2>), dim3(ntm * ntn, (unsigned)pieces), dim3(256), 0, s,
+    hipLaunchKernelGGL((k_xent_product<DT, PAIR, ODT, AKC, 2, 2, 2, 2>), dim3(ntm * ntn, (unsigned)pieces), dim3(256), 0, s,
                        p, ntm, ntn);
   }
 }
-template <int DT, bool AKC>
+template <int DT, bool PAIR, bool AKC>
 static void product(const XentProduct& p, int odt, int64_t pieces, hipStream_t s) {
   if (odt == kF32)
-    product_to<DT, kF32, AKC>(p, pieces, s);
+    product_to<DT, PAIR, kF32, AKC>(p, pieces, s);
   else if (odt == kBF16)
-    product_to<DT, kBF16, AKC>(p, pieces, s);
+    product_to<DT, PAIR, kBF16, AKC>(p, pieces, s);
   else
-    product_to<DT, kF16, AKC>(p, pieces, s);
+    product_to<DT, PAIR, kF16, AKC>(p, pieces, s);
 }
 
-// DT: what the products take; KEEP: how E is kept.
-template <int DT, int KEEP>
+// DT: what the products take; PAIR: two pieces of it for a value.
+template <int DT, bool PAIR>
 static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* ws, int64_t t0, hipStream_t s) {
-  const int64_t n = std::min(l.block, a.t - t0), plane_x = a.t * l.dp;
+  constexpr int KEEP = PAIR ? 2 : 1, PIECES = PAIR ? 2 : 1;
+  const int64_t n = std::min(l.block, a.t - t0), pitch = PIECES * l.dp;
   const float* sc = reinterpret_cast<const float*>(ws + l.scalars);
   uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
   float2* const stats = reinterpret_cast<float2*>(ws + l.stats);
   float* const target = reinterpret_cast<float*>(ws + l.target);
-  const int terms = l.parts == 2 ? 3 : 1;
   XentTile p{};
-  p.x = l.pack_x ? MmaSide{px + t0 * l.dp, plane_x, l.dp, n}
+  p.x = l.pack_x ? MmaSide{px + t0 * pitch, l.dp, pitch, n}
                  : MmaSide{static_cast<const uint16_t*>(a.x) + t0 * a.ldx, 0, a.ldx, n};
-  p.w = l.pack_w ? MmaSide{reinterpret_cast<uint16_t*>(ws + l.w), a.v * l.dp, l.dp, a.v}
+  p.w = l.pack_w ? MmaSide{reinterpret_cast<uint16_t*>(ws + l.w), l.dp, pitch, a.v}
                  : MmaSide{static_cast<const uint16_t*>(a.w), 0, a.ldw, a.v};
-  p.t = n, p.v = a.v, p.d = a.d, p.terms = terms, p.sc = sc, p.bias = a.bias, p.bias_dtype = a.dtype;
+  p.t = n, p.v = a.v, p.d = a.d, p.sc = sc, p.bias = a.bias, p.bias_dtype = a.dtype;
   p.targets = a.targets + t0, p.stats = stats, p.nseg = l.nseg, p.target = target, p.e = ws + l.e, p.vp = l.vp;
   if (train)
-    logits<DT, KEEP>(p, a.t, s);
+    logits<DT, PAIR, KEEP>(p, a.t, s);
   else
-    logits<DT, 0>(p, a.t, s);
+    logits<DT, PAIR, 0>(p, a.t, s);
   hipLaunchKernelGGL(k_xent_lse, dim3((unsigned)cdiv(n, 4)), dim3(256), 0, s, stats, n, l.nseg, a.v, a.targets + t0,
                      a.ignore, target, a.loss + t0, a.lse + t0);
   if (!train || !(a.dx || a.dw || a.dbias)) return;
@@ -665,37 +670,37 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   const int64_t parts = cdiv(n, kGradRows);
   const XentGrad q{n,     a.v, l.vp, l.nseg, l.seg_shift, stats, a.lse + t0, a.loss + t0, a.weights ? a.weights + t0 : nullptr,
                    sc, a.targets + t0, a.ignore, ws + l.e, g, a.dbias ? db : nullptr};
-  hipLaunchKernelGGL((k_xent_grad<KEEP == 2 ? kF32 : DT>), dim3((unsigned)cdiv(l.vp, 2048), (unsigned)parts), dim3(256),
+  hipLaunchKernelGGL((k_xent_grad<PAIR ? kF32 : DT>), dim3((unsigned)cdiv(l.vp, 2048), (unsigned)parts), dim3(256),
                      0, s, q);
   if (a.dbias)
     hipLaunchKernelGGL(k_xent_db, dim3(grid(a.v)), dim3(256), 0, s, db, parts, l.vp, a.v, sc, a.dbias, a.dtype,
                        a.accumulate || t0 > 0);
   if (a.dx) {
     XentProduct d{};
-    d.a = MmaSide{g, n * l.vp, l.vp, n};
+    d.a = MmaSide{g, l.vp, PIECES * l.vp, n};
     d.b = p.w;
     d.b.len = a.d;
-    d.k = a.v, d.terms = terms;
+    d.k = a.v;
     const int eb = dtype_bytes(a.dtype);
     uint8_t* const dx = static_cast<uint8_t*>(a.dx) + t0 * a.lddx * eb;
     if (l.dx_splits > 1) {
       float* const part = reinterpret_cast<float*>(ws + l.dxp);
       d.out = MmaOut{part, a.d, n, a.d, nullptr, false};
       d.split_stride = n * a.d;
-      product<DT, true>(d, kF32, l.dx_splits, s);
+      product<DT, PAIR, true>(d, kF32, l.dx_splits, s);
       hipLaunchKernelGGL(k_xent_dx, dim3(grid(n * a.d)), dim3(256), 0, s, part, l.dx_splits, n, a.d, sc + kAlphaX, dx,
                          a.dtype, a.lddx);
     } else {
       d.alpha = sc + kAlphaX;
       d.out = MmaOut{dx, a.lddx, n, a.d, nullptr, false};
-      product<DT, true>(d, a.dtype, 1, s);
+      product<DT, PAIR, true>(d, a.dtype, 1, s);
     }
   }
   if (a.dw) {
     XentProduct d{};
-    d.a = MmaSide{g, n * l.vp, l.vp, a.v};
-    d.b = MmaSide{px + (l.pack_x ? l.parts * plane_x : 0) + t0 * l.dp, plane_x, l.dp, a.d};
-    d.k = n, d.terms = terms, d.alpha = sc + kAlphaW;
+    d.a = MmaSide{g, l.vp, PIECES * l.vp, a.v};
+    d.b = MmaSide{px + (l.pack_x ? a.t * pitch : 0) + t0 * pitch, l.dp, pitch, a.d};
+    d.k = n, d.alpha = sc + kAlphaW;
     // Blocks before the last add up in fp32: in dw itself, or in memory of
     // their own where dw has fewer bits.
     const bool last = t0 + n == a.t, wide = a.dw_dtype == kF32;
@@ -706,7 +711,7 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
       d.out = MmaOut{sum, a.d, a.v, a.d, nullptr, t0 > 0};
     else
       d.out = MmaOut{a.dw, a.lddw, a.v, a.d, t0 > 0 ? sum : nullptr, a.accumulate};
-    product<DT, false>(d, wide || !last ? kF32 : a.dw_dtype, 1, s);
+    product<DT, PAIR, false>(d, wide || !last ? kF32 : a.dw_dtype, 1, s);
   }
 }
 
@@ -735,11 +740,11 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
   }
   for (int64_t t0 = 0; t0 < a.t; t0 += l.block) {
     if (a.dtype == kBF16)
-      block<kBF16, 1>(a, l, train, ws, t0, s);
+      block<kBF16, false>(a, l, train, ws, t0, s);
     else if (a.dtype == kF16)
-      block<kF16, 1>(a, l, train, ws, t0, s);
+      block<kF16, false>(a, l, train, ws, t0, s);
     else
-      block<kF16, 2>(a, l, train, ws, t0, s);
+      block<kF16, true>(a, l, train, ws, t0, s);
   }
   return hipGetLastError();
 }

@@ -2,20 +2,22 @@
 // the vocabulary cross entropy and the orthogonalised step share, each with
 // epilogues of its own.
 //
-// A workgroup computes a BM x BN tile of C = sum over terms of A_t B_t^T with
-// WM x WN wavefronts, each TM x TN tiles of 32 x 32 in accumulators, in chunks
-// of 64 along the summed axis.  A term is a pair of planes: a 16-bit matrix is
-// one plane and a product one term; an fp32 matrix is two fp16 planes, hi + lo
-// (22 bits of every value that is above 2^-39 of the scale they share), and a
-// product three terms, hi hi + hi lo + lo hi, summed in the same accumulators.
+// A workgroup computes a BM x BN tile of C = A B^T with WM x WN wavefronts, each
+// TM x TN tiles of 32 x 32 in accumulators, in chunks along the summed axis: 64
+// values of 16-bit matrices.  An fp32 matrix is held as two fp16 pieces, hi + lo
+// (22 bits of every value that is above 2^-39 of the scale they share), side by
+// side in its rows; of such matrices a chunk is 32 values, both pieces of both
+// operands, and a product hi lo + hi hi + lo hi.  (As three products one after
+// the other every piece is read one and a half times as often, and LDS reads
+// are what the smaller tiles wait for.)
 //
 // Each operand's tile goes from memory straight into LDS (16 bytes per lane, no
 // registers), two stages, so the next chunk arrives while the matrix cores work
 // on this one.  Operands come in two orders:
 //   K-contiguous  rows of the tile's axis, the summed axis along a row: 128
-//                 bytes of every row per chunk;
+//                 bytes of every row (and piece: 64) per chunk;
 //   K-strided     rows of the summed axis, the tile's axis along a row: 64 rows
-//                 of the tile's width per chunk, which the transposing LDS read
+//                 (or 32 of each piece) of the tile's width per chunk, which the transposing LDS read
 //                 hands to the matrix cores in their own order.  So no operand
 //                 is ever transposed in memory.
 // The hardware writes LDS in lane order; each lane therefore *fetches* the 16
@@ -33,18 +35,19 @@ namespace psgd {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-constexpr int kMmaK = 64;                 // values of the summed axis in a chunk
-constexpr int kMmaBytes = kMmaK * 2;      // their bytes
-constexpr uint32_t kMmaOff = 0x80000000u; // an offset that no descriptor reaches
+template <bool PAIR>
+constexpr int kMmaK = PAIR ? 32 : 64;      // values of the summed axis in a chunk
+constexpr int kMmaBytes = 128;             // bytes of a tile's row in a chunk
+constexpr uint32_t kMmaOff = 0x80000000u;  // an offset that no descriptor reaches
 
-// One operand: planes of `len` (K-contiguous) or k (K-strided) rows, 16-byte
-// aligned, the row stride a multiple of 8.  K-contiguous rows are zero from k on
-// to the next multiple of 8.
+// One operand: `len` (K-contiguous) or k (K-strided) rows, 16-byte aligned, the
+// row stride a multiple of 8.  K-contiguous rows are zero from k on to the next
+// multiple of 8.
 struct MmaSide {
   const uint16_t* p;
-  int64_t plane;  // elements from a plane to the next
-  int64_t ld;
-  int64_t len;    // size of the tile's axis
+  int64_t lo;   // from a value's upper piece to its lower one
+  int64_t ld;   // row stride
+  int64_t len;  // size of the tile's axis
 };
 
 template <int DT>
@@ -66,49 +69,54 @@ __device__ __forceinline__ int mma_key(int row) { return ((row >> 1) + 6) & 7; }
 // A transposing read takes rows 16 g + 8 s + 0..3 (or 4..7) of one unit for the
 // lanes' groups g: four neighbouring rows and two neighbouring g stay apart.
 template <int UNITS>
-__device__ __forceinline__ int mma_tkey(int k) {
-  return ((k & 3) | (k >> 2 & 4)) & (UNITS - 1);
+__device__ __forceinline__ int mma_tunit(int unit, int k) {
+  const int key = ((k & 3) | (k >> 2 & 4)) & (UNITS - 1);
+  return unit ^ (UNITS == 12 && unit >= 8 ? key & 3 : key);  // (of 12 units the last four among themselves)
 }
 
 // One operand's side of the tile loop: R rows of the tile's axis, W wavefronts
-// that load it.
-template <bool KC, int R, int W>
+// that load it.  The 16-byte blocks that a wavefront reads in its two steps
+// alternate (MmaRead), so pieces do: block 2 b of a K-contiguous row is block b
+// of the upper piece's values and block 2 b + 1 of the lower one's, and 8 rows of
+// a K-strided tile are of the upper piece, the next 8 of the lower one.
+template <bool PAIR, bool KC, int R, int W>
 struct MmaLoad {
-  static constexpr int kLoads = R / 8 / W, kBytes = R * kMmaBytes;
+  static constexpr int kLoads = R / 8 / W, kBytes = R * kMmaBytes, K = kMmaK<PAIR>;
   static_assert(R % (8 * W) == 0, "whole loads");
-  static constexpr int kSlots = R / 8, kRows = 64 / kSlots;  // K-strided: 16-byte slots of a row, rows of a load
+  static constexpr int kSlots = R / 8;  // K-strided: 16-byte slots of a row
   const uint16_t* p;  // the tile's first value
-  int64_t plane, ld;
-  uint32_t rows, left, off[kLoads], slot[2];
+  int64_t ld;
+  uint32_t lo, rows, left, off[kLoads], slot[2];
   __amdgpu_buffer_rsrc_t r;  // of the present chunk
   __device__ __forceinline__ MmaLoad(const MmaSide& s, int64_t r0, int wave, int lane) {
-    plane = s.plane;
     ld = s.ld;
+    lo = PAIR ? (uint32_t)s.lo * 2 : 0;
     rows = (uint32_t)min((int64_t)R, s.len - r0);
     p = s.p + r0 * (KC ? s.ld : 1);
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       if constexpr (KC) {
         const int row = (wave * kLoads + j) * 8 + (lane >> 3), b = (lane & 7) ^ mma_key(row);
-        off[j] = (uint32_t)(row * s.ld * 2) + b * 16;
+        off[j] = (uint32_t)(row * s.ld * 2) + (PAIR ? (b >> 1) * 16 + (b & 1) * lo : b * 16);
       } else {
-        const int row = (wave * kLoads + j) * kRows + lane / kSlots;
-        off[j] = (uint32_t)(row * s.ld * 2) + ((lane % kSlots) ^ mma_tkey<kSlots / 2>(row) * 2) * 16;
+        const int at = (wave * kLoads + j) * 64 + lane, row = at / kSlots, b = at % kSlots;
+        off[j] = (uint32_t)((PAIR ? (row >> 4) * 8 + (row & 7) : row) * s.ld * 2) + (PAIR ? (row >> 3 & 1) * lo : 0) +
+                 mma_tunit<kSlots / 2>(b >> 1, row) * 32 + (b & 1) * 16;
       }
     }
     if constexpr (KC) {  // first values of the blocks of even and odd groups of 8 rows
-      slot[0] = ((lane & 7) ^ mma_key(lane >> 3)) * 8;
-      slot[1] = ((lane & 7) ^ mma_key(8 + (lane >> 3))) * 8;
+      slot[0] = (((lane & 7) ^ mma_key(lane >> 3)) >> (PAIR ? 1 : 0)) * 8;
+      slot[1] = (((lane & 7) ^ mma_key(8 + (lane >> 3))) >> (PAIR ? 1 : 0)) * 8;
     }
   }
-  // To plane `second` of chunk `chunk`, of which `left` values are left (0: a
-  // chunk of zeros).  Without branches, which would cut the loop into pieces
-  // that the compiler schedules one by one.
-  __device__ __forceinline__ void seek(uint32_t second, uint32_t chunk, uint32_t left_) {
+  // To a chunk of which `left` values are left (0: a chunk of zeros).  Without
+  // branches, which would cut the loop into pieces that the compiler schedules
+  // one by one.
+  __device__ __forceinline__ void seek(uint32_t chunk, uint32_t left_) {
     left = left_;
-    const uint16_t* at = p + second * plane + (int64_t)chunk * kMmaK * (KC ? 1 : ld);
+    const uint16_t* at = p + (int64_t)chunk * K * (KC ? 1 : ld);
     const uint32_t some = min(left, 1u), pitch = (uint32_t)ld * 2;
-    const uint32_t n = KC ? (rows - 1) * pitch + left * 2 : (min(left, (uint32_t)kMmaK) - some) * pitch + rows * 2;
+    const uint32_t n = lo + (KC ? (rows - 1) * pitch + left * 2 : (min(left, (uint32_t)K) - some) * pitch + rows * 2);
     r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(at), 0, (int)(((n + 15) & ~15u) * some), 0x00020000);
   }
   // Load j of that chunk.
@@ -121,8 +129,8 @@ struct MmaLoad {
 };
 
 // What a wavefront reads of an operand's tile: its tile of 16 rows number i,
-// step s of a chunk; lane group g gets values (2 g + s) * 8 .. + 7 of the
-// summed axis.
+// step s of a chunk; lane group g gets blocks 2 g + s: values (2 g + s) * 8 .. + 7
+// of the summed axis, or values 8 g .. + 7 of the upper (s = 0) or lower piece.
 template <bool KC, int R>
 struct MmaRead {
   static constexpr int kReads = KC ? 1 : 2;  // LDS reads an operand takes
@@ -145,8 +153,7 @@ struct MmaRead {
     } else {
       // (rows 4 apart have the same key)
       typedef short v4s __attribute__((ext_vector_type(4)));
-      const int key = mma_tkey<R / 16>((threadIdx.x & 15) >> 2 | ((threadIdx.x >> 4 & 1) << 4));
-      const uint8_t* q = m + off[s] + (((base + i) ^ key) << 5);
+      const uint8_t* q = m + off[s] + (mma_tunit<R / 16>(base + i, (threadIdx.x & 15) >> 2 | (threadIdx.x & 16)) << 5);
       typedef __attribute__((address_space(3))) v4s* lds4;
       const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(__attribute__((address_space(3))) void*)(q));
       const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(__attribute__((address_space(3))) void*)(q + 4 * R * 2));
@@ -161,49 +168,43 @@ __device__ __forceinline__ void sched_lds_reads() {
   __builtin_amdgcn_sched_group_barrier(0x100, N, 0);
 }
 
-// The loop: accumulators of chunks c0 .. c1 - 1 of the terms' chunks (term t's
-// are t * nch .. + nch - 1).  Terms: one, planes (0, 0); or three, (0, 1),
-// (1, 0) and then (0, 0), so that the small ones are rounded at their own size.
+// The loop: accumulators of chunks c0 .. c1 - 1.
 //
 // Groups of products: one tile of 16 rows of A times all of the wavefront's B;
-// a chunk is two steps of HA groups.  A's operands are read DEPTH groups
-// ahead, B's one step ahead.  The barrier stands DEPTH groups before the
-// chunk's end: their operands are in registers, so their products cover it and
-// the first reads of the next chunk, and behind it every wavefront is done with
-// this chunk's stage.  From there on the loads of the chunk after the next go
-// into that stage, spread over the groups.
-template <int DT, bool AKC, bool BKC, int WM, int WN, int TM, int TN>
+// a chunk is two steps of HA groups, of pieces the upper one of A (times both of
+// B) and the lower one (times the upper one).  A's operands are read DEPTH
+// groups ahead, B's one step (of pieces: a chunk) ahead.  The barrier stands
+// DEPTH groups before the chunk's end: their operands are in registers, so their
+// products cover it and the first reads of the next chunk, and behind it every
+// wavefront is done with this chunk's stage.  From there on the loads of the
+// chunk after the next go into that stage, spread over the groups.
+template <int DT, bool PAIR, bool AKC, bool BKC, int WM, int WN, int TM, int TN>
 struct MmaTile {
   static constexpr int WAVES = WM * WN, BM = WM * 32 * TM, BN = WN * 32 * TN;
   static constexpr int HA = 2 * TM, HB = 2 * TN, GROUPS = 2 * HA, DEPTH = HA >= 8 ? 4 : 2;
-  using LA = MmaLoad<AKC, BM, WAVES>;
-  using LB = MmaLoad<BKC, BN, WAVES>;
-  static constexpr int PA = LA::kLoads, PB = LB::kLoads;
+  using LA = MmaLoad<PAIR, AKC, BM, WAVES>;
+  using LB = MmaLoad<PAIR, BKC, BN, WAVES>;
+  static constexpr int PA = LA::kLoads, PB = LB::kLoads, K = kMmaK<PAIR>;
   static constexpr int PER_GROUP = (PA + PB + GROUPS * 3 / 4 - 1) / (GROUPS * 3 / 4);
   static_assert(PA + PB <= PER_GROUP * GROUPS, "loads between two barriers");
   typedef v4f Acc[HA][HB];
 
-  static __device__ __forceinline__ void run(const MmaSide& sa, const MmaSide& sb, int64_t k, uint32_t terms,
-                                             uint32_t c0, uint32_t c1, int64_t m0, int64_t n0, uint8_t* a0, uint8_t* b0, uint8_t* a1,
+  static __device__ __forceinline__ void run(const MmaSide& sa, const MmaSide& sb, int64_t k, uint32_t c0, uint32_t c1,
+                                             int64_t m0, int64_t n0, uint8_t* a0, uint8_t* b0, uint8_t* a1,
                                              uint8_t* b1, Acc& acc) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     LA la(sa, m0, wave, lane);
     LB lb(sb, n0, wave, lane);
     const MmaRead<AKC, BM> ra(wave / WN * HA, lane);
     const MmaRead<BKC, BN> rb(wave % WN * HB, lane);
-    const uint32_t nch = (uint32_t)((k + kMmaK - 1) / kMmaK);
-    uint32_t term = c0 / nch + 3 - terms, kc = c0 % nch, chunks = c1 - c0;  // of the next chunk to load; chunks left
+    uint32_t at = c0;  // the next chunk to load
     auto seek = [&] {
-      const uint32_t left = ((uint32_t)k - kc * kMmaK) * min(chunks, 1u);
-      la.seek(term == 1, kc, left);
-      lb.seek(term == 0, kc, left);
+      const uint32_t c = min(at, c1 - 1), left = ((uint32_t)k - c * K) * min(c1 - min(at, c1), 1u);
+      la.seek(c, left);
+      lb.seek(c, left);
     };
     auto step = [&] {
-      chunks -= min(chunks, 1u);
-      ++kc;
-      const uint32_t over = kc == nch ? 1u : 0u;
-      kc -= over * nch;
-      term += over;
+      ++at;
       seek();
     };
     seek();
@@ -217,13 +218,17 @@ struct MmaTile {
     for (int i = 0; i < HA; ++i)
 #pragma unroll
       for (int j = 0; j < HB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    uint4 qa[DEPTH], qb[HB];  // entering a chunk: A's first DEPTH groups, B's step 0
+    // entering a chunk: A's first DEPTH groups, B's step 0 (of pieces: both)
+    constexpr int NB = PAIR ? 2 : 1;
+    uint4 qa[DEPTH], qb[NB][HB];
     auto chunk = [&](uint8_t* ca, uint8_t* cb, uint8_t* na, uint8_t* nb) {
-      uint4 a[GROUPS + DEPTH], b[3][HB];
+      uint4 a[GROUPS + DEPTH], b[2 + NB][HB];
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) a[d] = qa[d];
 #pragma unroll
-      for (int j = 0; j < HB; ++j) b[0][j] = qb[j];
+      for (int s = 0; s < NB; ++s)
+#pragma unroll
+        for (int j = 0; j < HB; ++j) b[s][j] = qb[s][j];
 #pragma unroll
       for (int q = 0; q < GROUPS; ++q) {
         const int s = q / HA, i = q % HA;
@@ -240,12 +245,24 @@ struct MmaTile {
           if (j < PA + PB) load(j, behind ? ca : na, behind ? cb : nb);
 #pragma unroll
         for (int j = 0; j < HB; ++j) {
-          if (q == j * (HA / 2) / HB) b[1][j] = rb(cb, 1, j), ++nb_reads;
-          if (q == GROUPS - DEPTH + j * (DEPTH / 2) / HB) b[2][j] = rb(nb, 0, j), ++nb_reads;
+          if (!PAIR && q == j * (HA / 2) / HB) b[1][j] = rb(cb, 1, j), ++nb_reads;
+          if (q == GROUPS - DEPTH + j * (PAIR ? DEPTH : DEPTH / 2) / HB) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n) b[2 + n][j] = rb(nb, n, j), ++nb_reads;
+          }
         }
         a[q + DEPTH] = q + DEPTH < GROUPS ? ra(ca, (q + DEPTH) / HA, (q + DEPTH) % HA) : ra(na, 0, q + DEPTH - GROUPS);
+        if constexpr (PAIR) {
+          if (s == 0) {
 #pragma unroll
-        for (int j = 0; j < HB; ++j) acc[i][j] = mma16<DT>(b[s][j], a[q], acc[i][j]);
+            for (int j = 0; j < HB; ++j) acc[i][j] = mma16<DT>(b[1][j], a[q], acc[i][j]);
+          }
+#pragma unroll
+          for (int j = 0; j < HB; ++j) acc[i][j] = mma16<DT>(b[0][j], a[q], acc[i][j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < HB; ++j) acc[i][j] = mma16<DT>(b[s][j], a[q], acc[i][j]);
+        }
         constexpr int RA = MmaRead<AKC, BM>::kReads, RB = MmaRead<BKC, BN>::kReads;
         if (nb_reads == 0)
           sched_lds_reads<RA>();
@@ -255,13 +272,18 @@ struct MmaTile {
           sched_lds_reads<RA + 2 * RB>();
         else
           sched_lds_reads<RA + 4 * RB>();
-        __builtin_amdgcn_sched_group_barrier(0x008, HB, 0);  // products
+        if (PAIR && s == 0)
+          __builtin_amdgcn_sched_group_barrier(0x008, 2 * HB, 0);  // products
+        else
+          __builtin_amdgcn_sched_group_barrier(0x008, HB, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) qa[d] = a[GROUPS + d];
 #pragma unroll
-      for (int j = 0; j < HB; ++j) qb[j] = b[2][j];
+      for (int s = 0; s < NB; ++s)
+#pragma unroll
+        for (int j = 0; j < HB; ++j) qb[s][j] = b[2 + s][j];
     };
 #pragma unroll
     for (int j = 0; j < PA + PB; ++j) load(j, a0, b0);
@@ -273,7 +295,9 @@ struct MmaTile {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) qa[d] = ra(a0, 0, d);
 #pragma unroll
-    for (int j = 0; j < HB; ++j) qb[j] = rb(b0, 0, j);
+    for (int s = 0; s < NB; ++s)
+#pragma unroll
+      for (int j = 0; j < HB; ++j) qb[s][j] = rb(b0, s, j);
     // (an odd last chunk is paired with one of zeros)
     for (uint32_t c = c0; c < c1; c += 2) {
       chunk(a0, b0, a1, b1);

@@ -10,35 +10,57 @@
 
 namespace psgd {
 
-// One matrix of a group, as the kernels' arguments carry it.
+// The kernels of a step, each with ranges of its own over a group's matrices.
+enum { kNorm, kStart, kGram, kPoly, kUpdate, kMuonKinds, kLast = kMuonKinds };
+
+constexpr int kMuonGroup = 27;  // matrices of a group (what the arguments of one launch hold)
+
+// One matrix of a group.
 struct MuonMat {
   const void* grad;
   float* mom;   // r x c, or null
   void* param;  // or null
   void* upd;    // or null
-  uint16_t *x0, *x1;  // X before and after a step: two fp16 planes of r x ldx
-  uint16_t *a, *b;    // A and B: `pieces` fp16 planes of k x ldk, k = min(r, c)
+  // Places in the workspace, in 256 bytes: X before and after every other step
+  // (r rows of two fp16 pieces), A and B (min(r, c) rows of `pieces` fp16 pieces).
+  uint32_t x0, x1, a, b;
   int64_t ldg, ldp, ldu;
   int32_t r, c;
-  float step;              // lr times the matrix's own scale
-  int32_t sum0, nsums;     // its workgroups of the norm
-  int32_t start0;          // its first workgroup of the first X
-  int32_t sym0, full0;     // its first tile of k x k (on and above the diagonal), of r x c
+  float step;  // lr times the matrix's own scale
   uint8_t gdt, pdt, udt, pieces;
 };
-static_assert(sizeof(MuonMat) == 128, "what the kernels' arguments hold");
-constexpr int kMuonGroup = 28;  // matrices of a launch (its arguments hold 4 KB)
+
+// A group's tables, in the workspace: the kernels of a step read them from
+// there.  (In every launch's own arguments, which lie in host memory, a search
+// over 20 matrices took longer than a small matrix's product.)
+struct MuonTable {
+  int32_t first[kMuonKinds][kMuonGroup];   // a matrix's first workgroup or tile; past the last matrix INT32_MAX
+  int32_t chunk0[kMuonKinds][kMuonGroup];  // its first chunk, alike
+  int32_t chunks[kMuonKinds][kMuonGroup];  // chunks of one of its tiles; workgroups of its norm
+  MuonMat mat[kMuonGroup];
+};
+static_assert(sizeof(MuonTable) <= 4080, "what a kernel's arguments hold beside the address");
+
+// How a launch of products is divided.  The first `whole` tiles are a workgroup
+// each.  The chunks of the others, from `chunk0` on, are divided evenly among
+// `shares` workgroups; a tile that several of them work on is put together by a
+// second launch, from the parts that each left in memory (its first and its last
+// tile can be such).
+struct MuonShares {
+  int32_t tiles, whole, shares;
+  int32_t chunk0, chunks;
+};
 
 struct MuonArgs {
-  MuonMat mat[kMuonGroup];
-  int32_t n;
-  bool nesterov, last;
-  float mu, decay;   // momentum; what a step leaves of a weight
+  const MuonTable* table;
+  uint8_t* ws;
+  bool nesterov, odd;  // odd: X is in x1
+  float mu, decay;     // momentum; what a step leaves of a weight
   float a, b, c, eps;
-  float sx, sa, sb;  // powers of two that X, A and B are held times
-  double* sums;      // the norm's partial sums of squares
-  float* partial;    // tiles' partial sums, where the summed axis is split
-  int32_t splits, tiles;  // pieces of the summed axis, tiles of a launch
+  float sx, sa, sb;    // powers of two that X, A and B are held times
+  double* sums;        // the norm's partial sums of squares
+  float* parts;        // tiles' sums of one share
+  MuonShares sh;
 };
 
 // What the caller gives for one matrix (sizes checked).

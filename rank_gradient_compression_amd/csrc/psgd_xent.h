@@ -36,7 +36,7 @@ struct XentArgs {
 // what it does not need), and how it splits its work.
 struct XentLayout {
   bool pack_x, pack_w;
-  int parts;                 // planes of an operand: 2 fp16 ones for fp32, else 1
+  int parts;                 // pieces of a value: 2 fp16 ones for fp32, else 1
   int64_t dp;                // row stride of packed operands
   int64_t vp;                // row stride of the probabilities
   int64_t block;             // tokens whose probabilities are held at a time
