@@ -250,36 +250,29 @@ __device__ __forceinline__ void muon_add(float (&v)[8], float f, uint4 q) {  // 
 
 // Eight neighbouring values of the caller's, n of them there.
 __device__ __forceinline__ void muon_save8(void* p, int dtype, int64_t i, const float (&v)[8], int n) {
-  uint8_t* at = static_cast<uint8_t*>(p) + i * dtype_bytes(dtype);
-  if (n >= 8 && ((uintptr_t)at & 15) == 0) {
-    if (dtype == kF32) {
-      __builtin_memcpy(__builtin_assume_aligned(at, 16), v, sizeof v);
-    } else {
-      uint16_t h[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = dtype == kBF16 ? Elem<kBF16>::down(v[e]) : Elem<kF16>::down(v[e]);
-      __builtin_memcpy(__builtin_assume_aligned(at, 16), h, sizeof h);
-    }
+  if (dtype == kF32) {
+    float* at = static_cast<float*>(p) + i;
+    const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+    store_run<kF32, 4>(at, a, n);
+    store_run<kF32, 4>(at + 4, b, n - 4);
+  } else if (dtype == kBF16) {
+    store_run<kBF16, 8>(static_cast<uint16_t*>(p) + i, v, n);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) muon_save(p, dtype, i + e, v[e]);
+    store_run<kF16, 8>(static_cast<uint16_t*>(p) + i, v, n);
   }
 }
 __device__ __forceinline__ void muon_load8(const void* p, int dtype, int64_t i, float (&v)[8], int n) {
-  const uint8_t* at = static_cast<const uint8_t*>(p) + i * dtype_bytes(dtype);
-  if (n >= 8 && ((uintptr_t)at & 15) == 0) {
-    if (dtype == kF32) {
-      __builtin_memcpy(v, __builtin_assume_aligned(at, 16), sizeof v);
-    } else {
-      uint16_t h[8];
-      __builtin_memcpy(h, __builtin_assume_aligned(at, 16), sizeof h);
+  if (dtype == kF32) {
+    const float* at = static_cast<const float*>(p) + i;
+    float a[4], b[4];
+    load_run<kF32, 4>(at, a, n);
+    load_run<kF32, 4>(at + 4, b, n - 4);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = dtype == kBF16 ? Elem<kBF16>::up(h[e]) : Elem<kF16>::up(h[e]);
-    }
+    for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+  } else if (dtype == kBF16) {
+    load_run<kBF16, 8>(static_cast<const uint16_t*>(p) + i, v, n);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? muon_load(p, dtype, i + e) : 0.f;
+    load_run<kF16, 8>(static_cast<const uint16_t*>(p) + i, v, n);
   }
 }
 
@@ -562,9 +555,11 @@ constexpr int64_t kGroupValues = int64_t(1) << 28;
 struct MuonShape {
   int bm, bn, slots;  // slots: workgroups that the card holds
   double chunk, tile, update;
+  double lone;  // a chunk where a compute unit has one such tile only
 };
-constexpr MuonShape kShapes[] = {
-    {256, 256, 256, 1.40, 10.0, 30.0}, {256, 128, 256, 0.85, 12.0, 22.0}, {128, 128, 512, 1.02, 8.0, 14.0}};
+constexpr MuonShape kShapes[] = {{256, 256, 256, 1.40, 10.0, 30.0, 1.40},
+                                 {256, 128, 256, 0.95, 12.0, 22.0, 0.95},
+                                 {128, 128, 512, 1.02, 8.0, 14.0, 0.80}};
 constexpr double kJoin = 10.0, kJoinBytes = 4.0e6;  // a joining launch; bytes that parts move in a us
 
 struct MuonLaunch {
@@ -625,7 +620,8 @@ static MuonLaunch plan_launch(const std::vector<MuonTensor>& t, const MuonGroup&
       double us = 0.0;
       if (whole) {
         const double rounds = (double)cdiv(whole, s.slots);
-        us += std::max((double)h.chunk0 / (double)whole * rounds, (double)longest) * s.chunk * per + rounds * tile;
+        us += std::max((double)h.chunk0 / (double)whole * rounds, (double)longest) * (whole <= 256 ? s.lone : s.chunk) * per +
+              rounds * tile;
       }
       if (h.chunks) {
         const double parts = h.shares > 1 ? std::min<double>(2.0 * h.shares, 2.0 * (double)(tiles - whole) + h.shares) : 0.0;

@@ -32,7 +32,7 @@ namespace psgd {
 // scalars that the device works out for itself
 enum { kSx, kSw, kInvSx, kInvSw, kGs, kAlphaX, kAlphaW, kAlphaB, kScalars };
 
-constexpr int kMaxGroups = 512;     // workgroups that look for a tensor's largest value
+constexpr int kMaxGroups = 1024;    // workgroups that look for a tensor's largest value
 constexpr int64_t kBlockBytes = int64_t(1) << 30;  // of E (and G) at a time
 constexpr int kGradRows = 16;       // tokens of a workgroup of the pass over E
 constexpr float kLog2e = 1.4426950408889634f;
@@ -65,18 +65,32 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // ------------------------------------------------------------ preparations
 // Largest finite magnitude of two fp32 matrices, one partial maximum per
-// workgroup: the first `kMaxGroups` take x, the others w.
+// workgroup: the first `kMaxGroups` take x, the others w.  Rows without gaps are
+// read as one.
 __global__ __launch_bounds__(256) void k_xent_max(XentArgs a, float* out) {
   const bool second = blockIdx.x >= kMaxGroups;
   const float* p = static_cast<const float*>(second ? a.w : a.x);
-  const int64_t rows = second ? a.v : a.t, ld = second ? a.ldw : a.ldx, d = a.d;
+  int64_t rows = second ? a.v : a.t, ld = second ? a.ldw : a.ldx, d = a.d;
   const int b = blockIdx.x % kMaxGroups;
   float m = 0.f;
-  for (int64_t row = b; row < rows; row += kMaxGroups) {
-    const float* q = p + row * ld;
-    for (int64_t i = threadIdx.x; i < d; i += 256) {
-      const float v = fabsf(q[i]);
-      m = v < __builtin_inff() ? fmaxf(m, v) : m;
+  auto take = [&](float v) {
+    v = fabsf(v);
+    m = v < __builtin_inff() ? fmaxf(m, v) : m;
+  };
+  if (ld == d && ((uintptr_t)p & 15) == 0) {
+    const int64_t n = rows * d, n4 = n / 4;
+    const float4* q = reinterpret_cast<const float4*>(p);
+#pragma unroll 8
+    for (int64_t i = (int64_t)b * 256 + threadIdx.x; i < n4; i += kMaxGroups * 256) {
+      const float4 v = q[i];
+      take(v.x), take(v.y), take(v.z), take(v.w);
+    }
+    if (b == 0 && threadIdx.x < n - n4 * 4) take(p[n4 * 4 + threadIdx.x]);
+  } else {
+    for (int64_t row = (int64_t)b * 4 + (threadIdx.x >> 6); row < rows; row += kMaxGroups * 4) {
+      const float* q = p + row * ld;
+#pragma unroll 8
+      for (int64_t i = threadIdx.x & 63; i < d; i += 64) take(q[i]);
     }
   }
   m = wave_max(m);
@@ -95,7 +109,7 @@ __device__ __forceinline__ int fit_exponent(float m) {
 }
 
 // The scalars, by one workgroup.
-__global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool split, const float* partmax, float* sc) {
+__device__ void xent_scalars(const XentArgs& a, bool train, bool split, const float* partmax, float* sc) {
   float u = 0.f, mx = 0.f, mw = 0.f;
   double n = 0.0;
   if (train)
@@ -132,6 +146,10 @@ __global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool 
   sc[kAlphaX] = (float)ldexp(s, -eg - ew);
   sc[kAlphaW] = (float)ldexp(s, -eg - ex);
   sc[kAlphaB] = (float)ldexp(s, -eg);
+}
+
+__global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, const float* partmax, float* sc) {
+  xent_scalars(a, train, true, partmax, sc);
 }
 
 // Rows to operands: 16-bit values, or two pieces of fp32 ones side by side,
@@ -200,29 +218,29 @@ struct XentTile {
 };
 
 // A row's logits of one segment: lane group g has columns col0 + 16 j + 4 g + e.
-// KEEP: 0 keeps no E, 1 fp16, 2 fp32.
-template <int HB, int KEEP>
+// They become E, and the segment's maximum and sum are written.
+template <bool PAIR, int HB>
 __device__ __forceinline__ void xent_row(const XentTile& p, int64_t row, int64_t col0, int g, const v4f (&acc)[HB],
-                                         const v4f (&bias)[HB], float is, float iw, int64_t y) {
+                                         const v4f (&bias)[HB], float is, float iw, int64_t y, float (&ex)[HB * 4]) {
   float l[HB * 4], m = -__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < HB * 4; ++i) {
-    const int64_t col = col0 + i / 4 * 16 + 4 * g + i % 4;
-    l[i] = acc[i / 4][i % 4] * is * iw + bias[i / 4][i % 4];
-    l[i] = col < p.v ? l[i] : -__builtin_inff();
-    m = fmaxf(m, l[i]);
+  for (int i = 0; i < HB * 4; ++i)
+    l[i] = (PAIR ? acc[i / 4][i % 4] * is * iw : acc[i / 4][i % 4]) + bias[i / 4][i % 4];
+  if (col0 + HB * 16 > p.v) {
+#pragma unroll
+    for (int i = 0; i < HB * 4; ++i) l[i] = col0 + i / 4 * 16 + 4 * g + i % 4 < p.v ? l[i] : -__builtin_inff();
   }
-  m = fmaxf(m, __shfl_xor(m, 16));
-  m = fmaxf(m, __shfl_xor(m, 32));
-  const float ref = m == -__builtin_inff() ? 0.f : m;  // (a segment of masked words: sums of zero)
-  float ex[HB * 4], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < HB * 4; ++i) m = fmaxf(m, l[i]);
+  m = groups_max(m);
+  const float ref = (m == -__builtin_inff() ? 0.f : m) * kLog2e;  // (a segment of masked words: sums of zero)
+  float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < HB * 4; ++i) {
-    ex[i] = __builtin_amdgcn_exp2f((l[i] - ref) * kLog2e);
+    ex[i] = __builtin_amdgcn_exp2f(fmaf(l[i], kLog2e, -ref));
     sum += ex[i];
   }
-  sum += __shfl_xor(sum, 16);
-  sum += __shfl_xor(sum, 32);
+  sum = groups_sum(sum);
   if (row >= p.t) return;
   if (g == 0) p.stats[row * p.nseg + col0 / (HB * 16)] = make_float2(m, sum);
   const int64_t at = y - col0 - 4 * g;  // the target among this lane's columns
@@ -231,18 +249,12 @@ __device__ __forceinline__ void xent_row(const XentTile& p, int64_t row, int64_t
     for (int i = 0; i < HB * 4; ++i)
       if (at == i / 4 * 16 + i % 4) p.target[row] = l[i];
   }
-  if constexpr (KEEP == 1) {
-    uint16_t* e = static_cast<uint16_t*>(p.e) + row * p.vp + col0 + 4 * g;
-#pragma unroll
-    for (int j = 0; j < HB; ++j)
-      *reinterpret_cast<uint2*>(e + j * 16) = make_uint2(Elem<kF16>::down2(ex[j * 4], ex[j * 4 + 1]),
-                                                         Elem<kF16>::down2(ex[j * 4 + 2], ex[j * 4 + 3]));
-  } else if constexpr (KEEP == 2) {
-    float* e = static_cast<float*>(p.e) + row * p.vp + col0 + 4 * g;
-#pragma unroll
-    for (int j = 0; j < HB; ++j)
-      *reinterpret_cast<float4*>(e + j * 16) = make_float4(ex[j * 4], ex[j * 4 + 1], ex[j * 4 + 2], ex[j * 4 + 3]);
-  }
+}
+
+__device__ __forceinline__ uint32_t two_halves(float v, float w) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{v, w}), v2h));
 }
 
 template <int HB>
@@ -270,16 +282,48 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_logits(XentTile p, int
   v4f bias[Tile::HB];
   xent_bias<Tile::HB>(p, col0, g, bias);
   const float is = PAIR ? p.sc[kInvSx] : 1.f, iw = PAIR ? p.sc[kInvSw] : 1.f;
+  // E goes out in whole rows of the wavefront's 64 columns, 32 rows at a time
+  // through LDS of its own (straight from the lanes' four columns it left in
+  // 32-byte pieces and took 20 us a round of tiles more).
+  constexpr int COLS = Tile::HB * 16, PITCH = COLS * (KEEP == 2 ? 4 : 2) + 16;
+  uint8_t* const lds = reinterpret_cast<uint8_t*>(mma_epilogue_lds<Tile>(__builtin_amdgcn_readfirstlane(wave), a0, b0, a1, b1));
+  int64_t ys[Tile::HA];
+#pragma unroll
+  for (int i = 0; i < Tile::HA; ++i) ys[i] = row0 + i * 16 < p.t ? p.targets[row0 + i * 16] : -1;
 #pragma unroll
   for (int i = 0; i < Tile::HA; ++i) {
-    const int64_t row = row0 + i * 16;
-    if (row - r >= p.t) break;
-    xent_row<Tile::HB, KEEP>(p, row, col0, g, acc[i], bias, is, iw, row < p.t ? p.targets[row] : -1);
+    float ex[Tile::HB * 4];
+    xent_row<PAIR, Tile::HB>(p, row0 + i * 16, col0, g, acc[i], bias, is, iw, ys[i], ex);
+    if constexpr (KEEP > 0) {
+      uint8_t* const wr = lds + (i % 2 * 16 + r) * PITCH + 4 * g * (KEEP == 2 ? 4 : 2);
+#pragma unroll
+      for (int j = 0; j < Tile::HB; ++j) {
+        if constexpr (KEEP == 2)
+          *reinterpret_cast<float4*>(wr + j * 64) = make_float4(ex[4 * j], ex[4 * j + 1], ex[4 * j + 2], ex[4 * j + 3]);
+        else
+          *reinterpret_cast<uint2*>(wr + j * 32) = make_uint2(two_halves(ex[4 * j], ex[4 * j + 1]),
+                                                              two_halves(ex[4 * j + 2], ex[4 * j + 3]));
+      }
+      if (i % 2 == 0) continue;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      constexpr int LPR = KEEP == 2 ? 16 : 8, RPI = 64 / LPR;
+      const int64_t first = row0 - r + (i - 1) * 16;
+      uint8_t* const out = static_cast<uint8_t*>(p.e) + (first * p.vp + col0) * (KEEP == 2 ? 4 : 2) + lane % LPR * 16;
+#pragma unroll
+      for (int q = 0; q < 32 / RPI; ++q) {
+        const int in = q * RPI + lane / LPR;
+        const uint4 x = *reinterpret_cast<const uint4*>(lds + in * PITCH + lane % LPR * 16);
+        if (first + in < p.t) *reinterpret_cast<uint4*>(out + in * p.vp * (KEEP == 2 ? 4 : 2)) = x;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
   }
 }
 
 // Few tokens: a stream of the weights, and what counts is how many of its bytes
-// are under way.  A workgroup takes all tokens (MT * 16) and 32 words; its eight
+// are under way.  A workgroup takes all tokens (MT * 16) and 32 words; its
 // wavefronts take the chunks in turn, each staging its own in LDS, two ahead,
 // in whole 128-byte rows, and their partial tiles are added in wavefront order.
 template <int N>
@@ -289,9 +333,9 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int DT, bool PAIR, int KEEP, int MT>
-__global__ __launch_bounds__(512, 1) void k_xent_logits_few(XentTile p) {
-  constexpr int WAVES = 8, HB = 2;
+template <int DT, bool PAIR, int KEEP, int MT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 1) void k_xent_logits_few(XentTile p) {
+  constexpr int HB = 2;
   using LX = MmaLoad<PAIR, true, MT * 16, 1>;
   using LW = MmaLoad<PAIR, true, 32, 1>;
   constexpr int STAGE = LX::kBytes + LW::kBytes, LOADS = LX::kLoads + LW::kLoads, TILES = MT * HB;
@@ -374,32 +418,59 @@ __global__ __launch_bounds__(512, 1) void k_xent_logits_few(XentTile p) {
     }
     xent_bias<HB>(p, col0, g, bias);
     const int64_t row = i * 16 + r;
-    xent_row<HB, KEEP>(p, row, col0, g, v, bias, is, iw, row < p.t ? p.targets[row] : -1);
+    float ex[HB * 4];
+    xent_row<PAIR, HB>(p, row, col0, g, v, bias, is, iw, row < p.t ? p.targets[row] : -1, ex);
+    if (row >= p.t) continue;
+    if constexpr (KEEP == 1) {
+      uint16_t* e = static_cast<uint16_t*>(p.e) + row * p.vp + col0 + 4 * g;
+#pragma unroll
+      for (int j = 0; j < HB; ++j)
+        *reinterpret_cast<uint2*>(e + j * 16) =
+            make_uint2(two_halves(ex[4 * j], ex[4 * j + 1]), two_halves(ex[4 * j + 2], ex[4 * j + 3]));
+    } else if constexpr (KEEP == 2) {
+      float* e = static_cast<float*>(p.e) + row * p.vp + col0 + 4 * g;
+#pragma unroll
+      for (int j = 0; j < HB; ++j)
+        *reinterpret_cast<float4*>(e + j * 16) = make_float4(ex[4 * j], ex[4 * j + 1], ex[4 * j + 2], ex[4 * j + 3]);
+    }
   }
 }
 
-// One wavefront per token: the sum over the segments, in a fixed order.
-__global__ __launch_bounds__(256) void k_xent_lse(const float2* stats, int64_t t, int64_t nseg, int64_t v,
-                                                  const int64_t* targets, int64_t ignore, const float* target,
-                                                  float* loss, float* lse) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= t) return;
-  const float2* s = stats + row * nseg;
+// One workgroup per token: the sum over the segments, in a fixed order.  One
+// more, where wanted, works out the scalars, which the gradients need.
+struct XentSums {
+  const float2* stats;
+  int64_t t, nseg;
+  const int64_t* targets;
+  const float* target;
+  float *loss, *lse, *sc;
+};
+__global__ __launch_bounds__(256) void k_xent_lse(XentArgs a, XentSums p) {
+  const int64_t row = blockIdx.x;
+  if (row == p.t) return xent_scalars(a, true, false, nullptr, p.sc);
+  const float2* s = p.stats + row * p.nseg;
   float m = -__builtin_inff(), sum = 0.f;
-  for (int64_t i = lane; i < nseg; i += 64) {
+  for (int64_t i = threadIdx.x; i < p.nseg; i += 256) {
     const float2 x = s[i];
     const float n = fmaxf(m, x.x), ref = n == -__builtin_inff() ? 0.f : n;
     sum = sum * __builtin_amdgcn_exp2f((m - ref) * kLog2e) + x.y * __builtin_amdgcn_exp2f((x.x - ref) * kLog2e);
     m = n;
   }
-  const float top = wave_max(m), ref = top == -__builtin_inff() ? 0.f : top;
+  __shared__ float tops[4], sums[4];
+  const int wave = threadIdx.x >> 6;
+  float top = wave_max(m);
+  if ((threadIdx.x & 63) == 0) tops[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  const float ref = top == -__builtin_inff() ? 0.f : top;
   sum = wave_sum(sum * __builtin_amdgcn_exp2f((m - ref) * kLog2e));
-  if (lane != 0) return;
-  const float l = ref + logf(sum);
-  lse[row] = l;
-  const int64_t y = targets[row];
-  loss[row] = ignored(y, ignore) ? 0.f : y < v ? l - target[row] : __builtin_nanf("");
+  if ((threadIdx.x & 63) == 0) sums[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  const float l = ref + logf(sums[0] + sums[1] + sums[2] + sums[3]);
+  p.lse[row] = l;
+  const int64_t y = p.targets[row];
+  p.loss[row] = ignored(y, a.ignore) ? 0.f : y < a.v ? l - p.target[row] : __builtin_nanf("");
 }
 
 // ------------------------------------------------------------- the gradient
@@ -605,11 +676,18 @@ static void pack_any(const void* x, int64_t ld, int64_t rows, int64_t dp, const 
 template <int DT, bool PAIR, int KEEP>
 static void logits(const XentTile& p, int64_t tokens, hipStream_t s) {
   if (tokens <= kFewTokens) {
-    const dim3 g((unsigned)cdiv(p.v, 32)), b(512);
-    if (p.t <= 16)
-      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 1>), g, b, 0, s, p);
+    // (four wavefronts, two workgroups to a compute unit, where eight would have
+    // hardly a chunk each)
+    const dim3 g((unsigned)cdiv(p.v, 32));
+    const bool brief = p.d <= 16 * kMmaK<PAIR>;
+    if (p.t <= 16 && brief)
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 1, 4>), g, dim3(256), 0, s, p);
+    else if (p.t <= 16)
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 1, 8>), g, dim3(512), 0, s, p);
+    else if (brief)
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 2, 4>), g, dim3(256), 0, s, p);
     else
-      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 2>), g, b, 0, s, p);
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 2, 8>), g, dim3(512), 0, s, p);
     return;
   }
   if (cdiv(p.t, 256) * cdiv(p.v, 256) >= 256) {
@@ -662,8 +740,10 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
     logits<DT, PAIR, KEEP>(p, a.t, s);
   else
     logits<DT, PAIR, 0>(p, a.t, s);
-  hipLaunchKernelGGL(k_xent_lse, dim3((unsigned)cdiv(n, 4)), dim3(256), 0, s, stats, n, l.nseg, a.v, a.targets + t0,
-                     a.ignore, target, a.loss + t0, a.lse + t0);
+  const bool scalars = train && !PAIR && t0 == 0;
+  hipLaunchKernelGGL(k_xent_lse, dim3((unsigned)n + (scalars ? 1 : 0)), dim3(256), 0, s, a,
+                     XentSums{stats, n, l.nseg, a.targets + t0, target, a.loss + t0, a.lse + t0,
+                              reinterpret_cast<float*>(ws + l.scalars)});
   if (!train || !(a.dx || a.dw || a.dbias)) return;
   uint16_t* const g = reinterpret_cast<uint16_t*>(ws + l.g);
   float* const db = reinterpret_cast<float*>(ws + l.db);
@@ -730,7 +810,7 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
     return hipGetLastError();
   }
   if (f32) hipLaunchKernelGGL(k_xent_max, dim3(2 * kMaxGroups), dim3(256), 0, s, a, partmax);
-  if (f32 || train) hipLaunchKernelGGL(k_xent_prep, dim3(1), dim3(256), 0, s, a, train, f32, partmax, sc);
+  if (f32) hipLaunchKernelGGL(k_xent_prep, dim3(1), dim3(256), 0, s, a, train, partmax, sc);
   if (l.pack_w)
     pack_any(a.w, a.ldw, a.v, l.dp, sc + kSw, reinterpret_cast<uint16_t*>(ws + l.w), nullptr, a, s);
   if (l.pack_x || train) {

@@ -328,6 +328,42 @@ __device__ __forceinline__ float* mma_epilogue_lds(int wave, uint8_t* a0, uint8_
   return reinterpret_cast<float*>(b1 + (wave - 2 * NA - NB) * NEED);
 }
 
+// N neighbouring values of the caller's memory, n of them there: as one vector,
+// as pairs where a row starts on a pair only, or one by one.
+template <int DT, int N>
+__device__ __forceinline__ void load_run(const typename Elem<DT>::type* at, float (&v)[N], int n) {
+  using T = typename Elem<DT>::type;
+  T o[N];
+  if (n >= N && ((uintptr_t)at & 15) == 0) {
+    __builtin_memcpy(o, __builtin_assume_aligned(at, 16), sizeof o);
+  } else if (n >= N && ((uintptr_t)at & (2 * sizeof(T) - 1)) == 0) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) __builtin_memcpy(o + e, __builtin_assume_aligned(at + e, 2 * sizeof(T)), 2 * sizeof(T));
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = e < n ? at[e] : (T)0;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = Elem<DT>::up(o[e]);
+}
+template <int DT, int N>
+__device__ __forceinline__ void store_run(typename Elem<DT>::type* at, const float (&v)[N], int n) {
+  using T = typename Elem<DT>::type;
+  T o[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) o[e] = Elem<DT>::down(v[e]);
+  if (n >= N && ((uintptr_t)at & 15) == 0) {
+    __builtin_memcpy(__builtin_assume_aligned(at, 16), o, sizeof o);
+  } else if (n >= N && ((uintptr_t)at & (2 * sizeof(T) - 1)) == 0) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) __builtin_memcpy(__builtin_assume_aligned(at + e, 2 * sizeof(T)), o + e, 2 * sizeof(T));
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < n) at[e] = o[e];
+  }
+}
+
 template <int DT, int HA, int HB>
 __device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* lds, int64_t row0, int64_t col0,
                                           const v4f (&acc)[HA][HB]) {
@@ -337,15 +373,14 @@ __device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* l
   constexpr int COLS = HB * 16, PITCH = COLS + 4, LPR = COLS / E, RPI = 64 / LPR;
   const int64_t rl = p.m - row0, cl = p.n - col0;  // rows and columns of C from here on
   if (rl <= 0 || cl <= 0) return;
-  const int cols = (int)min((int64_t)COLS, cl);
-  T* const base = static_cast<T*>(p.c) + row0 * p.ldc + col0;
-  const float* const add = p.add ? p.add + row0 * p.n + col0 : nullptr;
-  const bool wide = cols == COLS && ((uintptr_t)base & 15) == 0 && ((p.ldc * sizeof(T)) & 15) == 0 &&
-                    (!add || ((((uintptr_t)add) | (uintptr_t)(p.n * 4)) & 15) == 0);
-  float* wr = lds + (lane & 15) * PITCH + (lane >> 4) * 4;
+  T* const base = static_cast<T*>(p.c) + row0 * p.ldc + col0 + lane % LPR * E;
+  const float* const add = p.add ? p.add + row0 * p.n + col0 + lane % LPR * E : nullptr;
+  const int n = (int)min((int64_t)E, cl - lane % LPR * E);  // (what is past C's last column is not stored)
+  const bool whole = cl >= COLS && rl >= HA * 16 && ((uintptr_t)base & 15) == 0 && ((p.ldc * sizeof(T)) & 15) == 0 &&
+                     !add && !p.accumulate;
+  float* const wr = lds + (lane & 15) * PITCH + (lane >> 4) * 4;
 #pragma unroll
   for (int i = 0; i < HA / 2; ++i) {
-    if (i * 32 >= rl) break;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -357,46 +392,56 @@ __device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* l
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (wide) {
+    if (__all(whole)) {
 #pragma unroll
       for (int k = 0; k < 32 / RPI; ++k) {
         const int row = k * RPI + lane / LPR;
-        if (i * 32 + row >= rl) continue;
-        T* const at = base + (i * 32 + row) * p.ldc + (lane % LPR) * E;
         float v[E];
-        __builtin_memcpy(v, __builtin_assume_aligned(lds + row * PITCH + (lane % LPR) * E, 16), sizeof v);
+        __builtin_memcpy(v, __builtin_assume_aligned(lds + row * PITCH + lane % LPR * E, 16), sizeof v);
         T o[E];
-        if (add) {
-          float f[E];
-          __builtin_memcpy(f, __builtin_assume_aligned(add + (i * 32 + row) * p.n + (lane % LPR) * E, 16), sizeof f);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] += f[e];
-        }
-        if (p.accumulate) {
-          __builtin_memcpy(o, __builtin_assume_aligned(at, 16), sizeof o);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] += Elem<DT>::up(o[e]);
-        }
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = Elem<DT>::down(v[e]);
-        __builtin_memcpy(__builtin_assume_aligned(at, 16), o, sizeof o);
+        __builtin_memcpy(__builtin_assume_aligned(base + (i * 32 + row) * p.ldc, 16), o, sizeof o);
       }
     } else {
-#pragma unroll 1
-      for (int row = 0; row < 32 && i * 32 + row < rl; ++row) {
-#pragma unroll 1
-        for (int x = lane; x < cols; x += 64) {
-          float v = lds[row * PITCH + x];
-          if (add) v += add[(int64_t)(i * 32 + row) * p.n + x];
-          T* const at = base + (i * 32 + row) * p.ldc + x;
-          if (p.accumulate) v += Elem<DT>::up(*at);
-          *at = Elem<DT>::down(v);
+#pragma unroll 2
+      for (int k = 0; k < 32 / RPI; ++k) {
+        const int row = k * RPI + lane / LPR;
+        if (i * 32 + row >= rl || n <= 0) continue;
+        float v[E], w[E];
+        __builtin_memcpy(v, __builtin_assume_aligned(lds + row * PITCH + lane % LPR * E, 16), sizeof v);
+        if (add) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] += e < n ? add[(int64_t)(i * 32 + row) * p.n + e] : 0.f;
         }
+        T* const at = base + (i * 32 + row) * p.ldc;
+        if (p.accumulate) {
+          load_run<DT, E>(at, w, n);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] += w[e];
+        }
+        store_run<DT, E>(at, v, n);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+// Largest value and sum over the four groups of 16 lanes, in all of them.
+__device__ __forceinline__ float groups_max(float v) {
+  const uint32_t a = __float_as_uint(v);
+  const auto x = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])));
+  const auto y = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+__device__ __forceinline__ float groups_sum(float v) {
+  const uint32_t a = __float_as_uint(v);
+  const auto x = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(__uint_as_float(x[0]) + __uint_as_float(x[1]));
+  const auto y = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
 }
 
 // The walk over the tiles: groups of 8 tile rows, so that the 32 tiles that an
