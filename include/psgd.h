@@ -676,7 +676,9 @@ psgd_status_t psgd_xent_train(const psgd_xent_t* args, void* workspace, size_t w
  * Precision (opts.pieces): 1 takes the products on one fp16 value per entry of
  * X, A and B, with a X from two (about 2e-3 of the update, relative norm, what
  * bfloat16 has to give), 2 on two (about 1e-6; three products for one), 0
- * chooses per matrix: 1 where what is written is bfloat16, else 2.  Sums of
+ * chooses per matrix: 1 where what is written is bfloat16, else 2.  Entries of
+ * the first X below 2^-39 vanish: a gradient whose norm is far below eps has no
+ * update.  Sums of
  * squares are fp64, products are summed in fp32, in orders that depend on the
  * list's sizes alone: equal calls give equal bits.
  *

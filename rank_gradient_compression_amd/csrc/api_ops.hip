@@ -650,7 +650,8 @@ static psgd_status_t check_muon(const char* fn, int32_t n, const psgd_muon_tenso
     if (x.rows == 0 || x.cols == 0) continue;
     if (!x.param && !x.update) return invalid(fn, "a matrix has neither param nor update");
     // (the products' chunks are counted in 32 bits)
-    if ((x.rows / 128 + 1) * (x.cols / 128 + 1) * (std::max(x.rows, x.cols) / 64 + 1) * 3 > INT32_MAX)
+    const int64_t k = std::min(x.rows, x.cols), l = std::max(x.rows, x.cols), tiles = (k / 128 + 1) * (l / 128 + 1);
+    if (tiles * (k / 32 + 1) > INT32_MAX || (k / 128 + 1) * (k / 128 + 1) * (l / 32 + 1) > INT32_MAX)
       return invalid(fn, "a matrix is too large");
     const bool one = (!x.param || x.param_dtype == kBF16) && (!x.update || x.update_dtype == kBF16);
     const int pieces = o->pieces ? o->pieces : one ? 1 : 2;

@@ -17,6 +17,11 @@
 // that the products take; the target's entry, which would cancel, is formed
 // from the loss, exp(-loss) - 1, instead.  Sums, maxima and products are fp32.
 //
+// Tokens' weights.  A row of G is held times a power of two that brings its own
+// weight u_t to 2^13 .. 2^14, so that a token of small weight keeps its digits in
+// dx; the copy of x that dw's product takes carries the other powers of two,
+// relative to the largest weight's.
+//
 // fp32 tensors are split into two fp16 pieces (psgd_mma_device.h) under one
 // power of two that brings the largest finite value to 2^13 .. 2^14.
 
@@ -108,6 +113,13 @@ __device__ __forceinline__ int fit_exponent(float m) {
   return min(max(14 - e, -126), 126);
 }
 
+// Exponent of a token's weight; `most` (the largest weight's, the smallest
+// exponent) for one that has none.
+__device__ __forceinline__ int weight_exponent(float u, int most) {
+  u = fabsf(u);
+  return u > 0.f && u < __builtin_inff() ? max(fit_exponent(u), most) : most;
+}
+
 // The scalars, by one workgroup.
 __device__ void xent_scalars(const XentArgs& a, bool train, bool split, const float* partmax, float* sc) {
   float u = 0.f, mx = 0.f, mw = 0.f;
@@ -148,58 +160,79 @@ __device__ void xent_scalars(const XentArgs& a, bool train, bool split, const fl
   sc[kAlphaB] = (float)ldexp(s, -eg);
 }
 
-__global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, const float* partmax, float* sc) {
-  xent_scalars(a, train, true, partmax, sc);
+__global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool split, const float* partmax, float* sc) {
+  xent_scalars(a, train, split, partmax, sc);
 }
 
 // Rows to operands: 16-bit values, or two pieces of fp32 ones side by side,
-// zeros behind the row's end.  One
-// thread = 8 values.  clean: rows of ignored tokens become zero in a second
-// copy, the one that dw's product takes: their G is zero, and zero times what
-// such a row may hold need not be.
+// zeros behind the row's end.  One thread = 8 values.  clean: a second copy, the
+// one that dw's product takes, with rows of ignored tokens zero (their G is zero,
+// and zero times what such a row may hold need not be) and the others times their
+// weight's power of two, which goes to `factors` as well.
+struct XentPack {
+  const void* x;
+  int64_t ld, rows, d, dp;
+  const float* scale;
+  uint16_t *out, *clean;
+  const int64_t* targets;
+  int64_t ignore;
+  const float* weights;
+  const float* sc;
+  float* factors;
+};
 template <int DT>
-__global__ __launch_bounds__(256) void k_xent_pack(const void* x, int64_t ld, int64_t rows, int64_t d, int64_t dp,
-                                                   const float* scale, uint16_t* out, uint16_t* clean,
-                                                   const int64_t* targets, int64_t ignore) {
+__global__ __launch_bounds__(256) void k_xent_pack(XentPack p) {
   using T = typename Elem<DT>::type;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = dp / 8;
-  if (i >= rows * per) return;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = p.dp / 8;
+  if (i >= p.rows * per) return;
   const int64_t row = i / per, c = i % per * 8;
-  const T* p = static_cast<const T*>(x) + row * ld + c;
+  const T* q = static_cast<const T*>(p.x) + row * p.ld + c;
   T v[8];
-  if (c + 8 <= d) {
-    __builtin_memcpy(v, p, sizeof v);
+  if (c + 8 <= p.d) {
+    __builtin_memcpy(v, q, sizeof v);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < d ? p[e] : (T)0;
+    for (int e = 0; e < 8; ++e) v[e] = c + e < p.d ? q[e] : (T)0;
   }
-  uint16_t hi[8], lo[8];
-  if constexpr (DT == kF32) {
-    const float s = *scale;
+  const int64_t at = row * p.dp * (DT == kF32 ? 2 : 1) + c;
+  auto put = [&](uint16_t* to, float f) {
+    uint16_t hi[8], lo[8];
+    if constexpr (DT == kF32) {
+      const float s = *p.scale * f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float z = v[e] * s;
-      const _Float16 h = (_Float16)z;
-      hi[e] = __builtin_bit_cast(uint16_t, h);
-      const float r = z - (float)h;
-      lo[e] = Elem<kF16>::down(r == r ? r : 0.f);  // (infinite and NaN values stay so in hi)
+      for (int e = 0; e < 8; ++e) {
+        const float z = v[e] * s;
+        const _Float16 h = (_Float16)z;
+        hi[e] = __builtin_bit_cast(uint16_t, h);
+        const float r = z - (float)h;
+        lo[e] = Elem<kF16>::down(r == r ? r : 0.f);  // (infinite and NaN values stay so in hi)
+      }
+    } else {
+      __builtin_memcpy(hi, v, sizeof hi);
+      if (f != 1.f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hi[e] = Elem<DT>::down(Elem<DT>::up(hi[e]) * f);
+      }
     }
-  } else {
-    __builtin_memcpy(hi, v, sizeof hi);
-  }
-  const int64_t at = row * dp * (DT == kF32 ? 2 : 1) + c;
-  if (out) {
-    __builtin_memcpy(out + at, hi, sizeof hi);
-    if constexpr (DT == kF32) __builtin_memcpy(out + dp + at, lo, sizeof lo);
-  }
-  if (clean) {
-    if (ignored(targets[row], ignore)) {
+    if (f == 0.f) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) hi[e] = lo[e] = 0;
     }
-    __builtin_memcpy(clean + at, hi, sizeof hi);
-    if constexpr (DT == kF32) __builtin_memcpy(clean + dp + at, lo, sizeof lo);
+    __builtin_memcpy(to + at, hi, sizeof hi);
+    if constexpr (DT == kF32) __builtin_memcpy(to + p.dp + at, lo, sizeof lo);
+  };
+  if (p.out) put(p.out, 1.f);
+  if (!p.clean) return;
+  float f = 1.f;
+  if (p.weights) {
+    int top;
+    (void)frexpf(p.sc[kGs], &top);
+    const int most = top - 1;
+    f = ldexpf(1.f, most - weight_exponent(p.weights[row], most));
+    if (c == 0) p.factors[row] = f;
+    if (p.weights[row] == 0.f) f = 0.f;
   }
+  put(p.clean, ignored(p.targets[row], p.ignore) ? 0.f : f);
 }
 
 // ------------------------------------------------------------------ logits
@@ -478,7 +511,7 @@ struct XentGrad {
   int64_t t, v, vp, nseg;
   int seg_shift;
   const float2* stats;
-  const float *lse, *loss, *weights, *sc;
+  const float *lse, *loss, *weights, *factors, *sc;
   const int64_t* targets;
   int64_t ignore;
   void* e;       // fp16 (G in its place) or fp32
@@ -512,7 +545,8 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = Elem<kF16>::up(h[e]);
     }
-    const float u = (p.weights ? p.weights[row] : 1.f) * gs;
+    // (a row's own power of two: the largest weight's over the row's factor)
+    const float back = p.weights ? p.factors[row] : 1.f, u = p.weights ? p.weights[row] * (gs / back) : gs;
     const float f = u * __builtin_amdgcn_exp2f((p.stats[row * p.nseg + seg].x - p.lse[row]) * kLog2e);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = off || c + e >= p.v ? 0.f : v[e] * f;
@@ -523,7 +557,7 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
         if (y == c + e) v[e] = z;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[e] += v[e];
+    for (int e = 0; e < 8; ++e) sums[e] = fmaf(v[e], back, sums[e]);
     uint16_t h[8];
     if constexpr (DT == kF32) {
       uint16_t lo[8];
@@ -590,13 +624,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p,
 
 // dx = alpha * the pieces' sums in order.
 __global__ __launch_bounds__(256) void k_xent_dx(const float* part, int64_t pieces, int64_t t, int64_t d,
-                                                 const float* alpha, void* dx, int dtype, int64_t lddx) {
+                                                 const float* alpha, const float* factors, void* dx, int dtype,
+                                                 int64_t lddx) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= t * d) return;
   float s = 0.f;
 #pragma unroll 8
   for (int64_t k = 0; k < pieces; ++k) s += part[k * t * d + i];
-  store_any(dx, dtype, i / d * lddx + i % d, s * *alpha);
+  store_any(dx, dtype, i / d * lddx + i % d, s * *alpha * (factors ? factors[i / d] : 1.f));
 }
 
 // Gradients of a loss over no word or no token.
@@ -640,6 +675,7 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   };
   l.scalars = take(kScalars * sizeof(float));
   l.partmax = take(f32 ? 2 * kMaxGroups * sizeof(float) : 0);
+  l.rows = take(train && a.weights ? (size_t)a.t * sizeof(float) : 0);
   // x as the logits' operand, then (training) with ignored tokens' rows zero
   l.x = take((size_t)((l.pack_x ? 1 : 0) + (train ? 1 : 0)) * l.parts * a.t * l.dp * 2);
   l.w = take(l.pack_w ? (size_t)l.parts * a.v * l.dp * 2 : 0);
@@ -656,21 +692,15 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   return l;
 }
 
-template <int DT>
-static void pack(const void* x, int64_t ld, int64_t rows, int64_t d, int64_t dp, const float* scale, uint16_t* out,
-                 uint16_t* clean, const XentArgs& a, hipStream_t s) {
-  if (rows == 0 || d == 0) return;
-  hipLaunchKernelGGL((k_xent_pack<DT>), dim3(grid(rows * dp / 8)), dim3(256), 0, s, x, ld, rows, d, dp, scale, out,
-                     clean, a.targets, a.ignore);
-}
-static void pack_any(const void* x, int64_t ld, int64_t rows, int64_t dp, const float* scale, uint16_t* out,
-                     uint16_t* clean, const XentArgs& a, hipStream_t s) {
-  if (a.dtype == kF32)
-    pack<kF32>(x, ld, rows, a.d, dp, scale, out, clean, a, s);
-  else if (a.dtype == kBF16)
-    pack<kBF16>(x, ld, rows, a.d, dp, scale, out, clean, a, s);
+static void pack(const XentPack& p, int dtype, hipStream_t s) {
+  if (p.rows == 0) return;
+  const dim3 g(grid(p.rows * p.dp / 8)), b(256);
+  if (dtype == kF32)
+    hipLaunchKernelGGL((k_xent_pack<kF32>), g, b, 0, s, p);
+  else if (dtype == kBF16)
+    hipLaunchKernelGGL((k_xent_pack<kBF16>), g, b, 0, s, p);
   else
-    pack<kF16>(x, ld, rows, a.d, dp, scale, out, clean, a, s);
+    hipLaunchKernelGGL((k_xent_pack<kF16>), g, b, 0, s, p);
 }
 
 template <int DT, bool PAIR, int KEEP>
@@ -740,7 +770,7 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
     logits<DT, PAIR, KEEP>(p, a.t, s);
   else
     logits<DT, PAIR, 0>(p, a.t, s);
-  const bool scalars = train && !PAIR && t0 == 0;
+  const bool scalars = train && !PAIR && !a.weights && t0 == 0;
   hipLaunchKernelGGL(k_xent_lse, dim3((unsigned)n + (scalars ? 1 : 0)), dim3(256), 0, s, a,
                      XentSums{stats, n, l.nseg, a.targets + t0, target, a.loss + t0, a.lse + t0,
                               reinterpret_cast<float*>(ws + l.scalars)});
@@ -748,8 +778,10 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   uint16_t* const g = reinterpret_cast<uint16_t*>(ws + l.g);
   float* const db = reinterpret_cast<float*>(ws + l.db);
   const int64_t parts = cdiv(n, kGradRows);
-  const XentGrad q{n,     a.v, l.vp, l.nseg, l.seg_shift, stats, a.lse + t0, a.loss + t0, a.weights ? a.weights + t0 : nullptr,
-                   sc, a.targets + t0, a.ignore, ws + l.e, g, a.dbias ? db : nullptr};
+  const float* const factors = a.weights ? reinterpret_cast<float*>(ws + l.rows) + t0 : nullptr;
+  const XentGrad q{n,       a.v, l.vp,           l.nseg,   l.seg_shift, stats, a.lse + t0,                a.loss + t0,
+                   a.weights ? a.weights + t0 : nullptr, factors, sc, a.targets + t0, a.ignore, ws + l.e, g,
+                   a.dbias ? db : nullptr};
   hipLaunchKernelGGL((k_xent_grad<PAIR ? kF32 : DT>), dim3((unsigned)cdiv(l.vp, 2048), (unsigned)parts), dim3(256),
                      0, s, q);
   if (a.dbias)
@@ -765,14 +797,14 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
     uint8_t* const dx = static_cast<uint8_t*>(a.dx) + t0 * a.lddx * eb;
     if (l.dx_splits > 1) {
       float* const part = reinterpret_cast<float*>(ws + l.dxp);
-      d.out = MmaOut{part, a.d, n, a.d, nullptr, false};
+      d.out = MmaOut{part, a.d, n, a.d, nullptr, false, nullptr};
       d.split_stride = n * a.d;
       product<DT, PAIR, true>(d, kF32, l.dx_splits, s);
-      hipLaunchKernelGGL(k_xent_dx, dim3(grid(n * a.d)), dim3(256), 0, s, part, l.dx_splits, n, a.d, sc + kAlphaX, dx,
-                         a.dtype, a.lddx);
+      hipLaunchKernelGGL(k_xent_dx, dim3(grid(n * a.d)), dim3(256), 0, s, part, l.dx_splits, n, a.d, sc + kAlphaX,
+                         factors, dx, a.dtype, a.lddx);
     } else {
       d.alpha = sc + kAlphaX;
-      d.out = MmaOut{dx, a.lddx, n, a.d, nullptr, false};
+      d.out = MmaOut{dx, a.lddx, n, a.d, nullptr, false, factors};
       product<DT, PAIR, true>(d, a.dtype, 1, s);
     }
   }
@@ -786,11 +818,11 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
     const bool last = t0 + n == a.t, wide = a.dw_dtype == kF32;
     float* const sum = reinterpret_cast<float*>(ws + l.dwp);
     if (wide)
-      d.out = MmaOut{a.dw, a.lddw, a.v, a.d, nullptr, a.accumulate || t0 > 0};
+      d.out = MmaOut{a.dw, a.lddw, a.v, a.d, nullptr, a.accumulate || t0 > 0, nullptr};
     else if (!last)
-      d.out = MmaOut{sum, a.d, a.v, a.d, nullptr, t0 > 0};
+      d.out = MmaOut{sum, a.d, a.v, a.d, nullptr, t0 > 0, nullptr};
     else
-      d.out = MmaOut{a.dw, a.lddw, a.v, a.d, t0 > 0 ? sum : nullptr, a.accumulate};
+      d.out = MmaOut{a.dw, a.lddw, a.v, a.d, t0 > 0 ? sum : nullptr, a.accumulate, nullptr};
     product<DT, PAIR, false>(d, wide || !last ? kF32 : a.dw_dtype, 1, s);
   }
 }
@@ -810,13 +842,18 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
     return hipGetLastError();
   }
   if (f32) hipLaunchKernelGGL(k_xent_max, dim3(2 * kMaxGroups), dim3(256), 0, s, a, partmax);
-  if (f32) hipLaunchKernelGGL(k_xent_prep, dim3(1), dim3(256), 0, s, a, train, partmax, sc);
-  if (l.pack_w)
-    pack_any(a.w, a.ldw, a.v, l.dp, sc + kSw, reinterpret_cast<uint16_t*>(ws + l.w), nullptr, a, s);
+  if (f32 || (train && a.weights))
+    hipLaunchKernelGGL(k_xent_prep, dim3(1), dim3(256), 0, s, a, train, f32, partmax, sc);
+  if (l.pack_w) {
+    const XentPack p{a.w, a.ldw, a.v, a.d, l.dp, sc + kSw, reinterpret_cast<uint16_t*>(ws + l.w)};
+    pack(p, a.dtype, s);
+  }
   if (l.pack_x || train) {
     uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
-    pack_any(a.x, a.ldx, a.t, l.dp, sc + kSx, l.pack_x ? px : nullptr,
-             train ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr, a, s);
+    const XentPack p{a.x,      a.ldx,     a.t,     a.d, l.dp, sc + kSx, l.pack_x ? px : nullptr,
+                     train ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr,
+                     a.targets, a.ignore, a.weights, sc, reinterpret_cast<float*>(ws + l.rows)};
+    pack(p, a.dtype, s);
   }
   for (int64_t t0 = 0; t0 < a.t; t0 += l.block) {
     if (a.dtype == kBF16)

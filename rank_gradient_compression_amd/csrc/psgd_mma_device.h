@@ -307,7 +307,7 @@ struct MmaTile {
   }
 };
 
-// Accumulators to memory: C = alpha * sum (+ add) (+ C).  Each wavefront passes
+// Accumulators to memory: C = alpha * (row factor) * sum (+ add) (+ C).  Each wavefront passes
 // 32 rows at a time through LDS of its own and stores 16 bytes per lane, whole
 // rows of its TN * 32 columns; the row pitch of 4 floats beyond a multiple of 32
 // spreads the 16 rows that a write covers over all banks.
@@ -316,6 +316,7 @@ struct MmaOut {
   int64_t ldc, m, n;
   const float* add;  // m x n fp32, row stride n, or null
   bool accumulate;
+  const float* row;  // m factors, or null
 };
 
 template <class Tile>
@@ -398,6 +399,11 @@ __device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* l
         const int row = k * RPI + lane / LPR;
         float v[E];
         __builtin_memcpy(v, __builtin_assume_aligned(lds + row * PITCH + lane % LPR * E, 16), sizeof v);
+        if (p.row) {
+          const float f = p.row[row0 + i * 32 + row];
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] *= f;
+        }
         T o[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = Elem<DT>::down(v[e]);
@@ -410,6 +416,11 @@ __device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* l
         if (i * 32 + row >= rl || n <= 0) continue;
         float v[E], w[E];
         __builtin_memcpy(v, __builtin_assume_aligned(lds + row * PITCH + lane % LPR * E, 16), sizeof v);
+        if (p.row) {
+          const float f = p.row[row0 + i * 32 + row];
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] *= f;
+        }
         if (add) {
 #pragma unroll
           for (int e = 0; e < E; ++e) v[e] += e < n ? add[(int64_t)(i * 32 + row) * p.n + e] : 0.f;
