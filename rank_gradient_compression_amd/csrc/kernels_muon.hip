@@ -20,7 +20,12 @@
 // X itself in 16 bits, what rounding adds under large singular values grows by a
 // a step with the small ones (512 x 512, rank 16 over noise of 1/20: 6e-3 off
 // with fp16 X, 5e-2 with bfloat16, 1.5e-4 so; Gaussian: 1.5e-3).  Other results
-// take two pieces of everything, three products for one.
+// take two pieces of everything, three products for one.  In the last two steps,
+// where singular values are near 1 and B near b + c, the identity's part of a X
+// that cancels against B's goes into B instead, whose roundings are then of what
+// is left: X <- (a + b + c) X + (B - (b + c) I) X (Gaussian: 1.7e-3 -> 1.0e-3;
+// from the first step on it would cost the small singular values what the two
+// pieces gave them).
 
 #include <hip/hip_runtime.h>
 
@@ -217,6 +222,106 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   *reinterpret_cast<uint4*>(x + ld) = lo;
 }
 
+// ------------------------------------------------------- matrices in one piece
+// Where every matrix of a call is so small, a workgroup takes one whole: X (the
+// shorter side down), A and B in LDS in fp32, products on the fp32 matrix
+// instruction.  One launch for everything instead of eighteen.
+constexpr int kTinyShort = 64, kTinyLong = 256;
+constexpr int kTinyX = kTinyLong + 4, kTinyA = kTinyShort + 4;  // row pitches: 16 rows' values meet in no bank
+
+// Products of 16 x 16 tiles of lists a and b (their rows r0 + 0..15, summed along
+// the rows' 4 n values; b_down: b's tile is of columns, summed down them).
+template <bool B_DOWN>
+__device__ __forceinline__ v4f tiny_tile(const float* a, int pa, const float* b, int pb, int n, int lane) {
+  const int r = lane & 15, g = lane >> 4;
+  v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < n; ++s)
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r * pa + 4 * s + g], B_DOWN ? b[(4 * s + g) * pb + r] : b[r * pb + 4 * s + g],
+                                               acc, 0, 0, 0);
+  return acc;
+}
+
+__global__ __launch_bounds__(512) void k_muon_tiny(MuonTiny p) {
+  __shared__ float x[kTinyShort * kTinyX], a[kTinyShort * kTinyA], b[kTinyShort * kTinyA];
+  __shared__ double part[8];
+  const MuonMat t = p.mat[blockIdx.x];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const bool tall = t.r > t.c, has = t.mom != nullptr;
+  const int k = min(t.r, t.c), l = max(t.r, t.c), kt = (k + 15) / 16, lt = (l + 15) / 16, n = t.r * t.c;
+  for (int i = threadIdx.x; i < kt * 16 * kTinyX; i += 512) x[i] = 0.f;
+  __syncthreads();
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += 512) {
+    const int row = i / t.c, col = i % t.c;
+    const float v = muon_load(t.grad, t.gdt, row * t.ldg + col);
+    float m = 0.f;
+    if (has) t.mom[i] = m = muon_momentum(p.mu, t.mom[i], v);
+    const float u = !has ? v : p.nesterov ? fmaf(p.mu, m, v) : m;
+    x[tall ? col * kTinyX + row : row * kTinyX + col] = u;
+    s = fma((double)u, (double)u, s);
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);
+  if (lane == 0) part[wave] = s;
+  __syncthreads();
+  s = 0.0;
+  for (int i = 0; i < 8; ++i) s += part[i];
+  const double inv = 1.0 / (sqrt(s) + (double)p.eps);
+  for (int i = threadIdx.x; i < kt * 16 * lt * 16; i += 512) {
+    float& v = x[i / (lt * 16) * kTinyX + i % (lt * 16)];
+    v = (float)((double)v * inv);
+  }
+  __syncthreads();
+  for (int step = 0; step < p.steps; ++step) {
+    // (the product's lanes: column r, rows 4 g .. + 3; A and B are symmetric)
+    for (int i = wave; i < kt * kt; i += 8) {
+      const int m = i / kt * 16, c = i % kt * 16;
+      const v4f v = tiny_tile<false>(x + m * kTinyX, kTinyX, x + c * kTinyX, kTinyX, lt * 4, lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[(m + 4 * g + e) * kTinyA + c + r] = v[e];
+    }
+    __syncthreads();
+    for (int i = wave; i < kt * kt; i += 8) {
+      const int m = i / kt * 16, c = i % kt * 16;
+      const v4f v = tiny_tile<false>(a + m * kTinyA, kTinyA, a + c * kTinyA, kTinyA, kt * 4, lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = (m + 4 * g + e) * kTinyA + c + r;
+        b[at] = fmaf(p.c, v[e], p.b * a[at]);
+      }
+    }
+    __syncthreads();
+    constexpr int MOST = (kTinyShort / 16) * (kTinyLong / 16) / 8;
+    v4f next[MOST];
+#pragma unroll
+    for (int q = 0; q < MOST; ++q) {
+      const int i = wave + 8 * q, m = i / lt * 16, c = i % lt * 16;
+      if (i >= kt * lt) continue;
+      next[q] = tiny_tile<true>(b + m * kTinyA, kTinyA, x + c, kTinyX, kt * 4, lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) next[q][e] = fmaf(p.a, x[(m + 4 * g + e) * kTinyX + c + r], next[q][e]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < MOST; ++q) {
+      const int i = wave + 8 * q, m = i / lt * 16, c = i % lt * 16;
+      if (i >= kt * lt) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[(m + 4 * g + e) * kTinyX + c + r] = next[q][e];
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += 512) {
+    const int row = i / t.c, col = i % t.c;
+    const float v = x[tall ? col * kTinyX + row : row * kTinyX + col];
+    if (t.upd) muon_save(t.upd, t.udt, row * t.ldu + col, v);
+    if (t.param) {
+      const int64_t at = row * t.ldp + col;
+      muon_save(t.param, t.pdt, at, fmaf(p.decay, muon_load(t.param, t.pdt, at), -t.step * v));
+    }
+  }
+}
+
 // ---------------------------------------------------------------- products
 // Tile t of those on and above the diagonal of ntm x ntn, RB times as high as
 // wide: groups of 8 tile rows, column by column, so that neighbours share their
@@ -294,12 +399,14 @@ struct MuonResults {
   struct Old {
     uint4 hi[Q], lo[Q];
   };
+  bool vectors;
 
   __device__ __forceinline__ MuonResults(const MuonArgs& args, const MuonMat& mat, bool across)
       : p(args), t(mat), lane(threadIdx.x & 63), mirror(SYM && across), k(min(mat.r, mat.c)) {
     rows = SYM ? k : mat.r;
     ld = muon_ld(SYM ? k : mat.c);
     pitch = TWO ? 2 * ld : ld;
+    vectors = OP == kLast && t.param && !t.upd && t.c % 8 == 0 && ((uintptr_t)t.param & 15) == 0 && t.ldp % 8 == 0;
   }
   __device__ __forceinline__ void ask(int64_t row0, int64_t col0, Old& o) const {
     if constexpr (OP != kGram) {
@@ -310,6 +417,28 @@ struct MuonResults {
         o.hi[q] = *reinterpret_cast<const uint4*>(x);
         if (TWO) o.lo[q] = *reinterpret_cast<const uint4*>(x + ld);
       }
+    }
+  }
+  // Eight weights' new values, in place.
+  __device__ __forceinline__ void step8(uint4& w0, uint4& w1, const float (&v)[8]) const {
+    if (t.pdt == kF32) {
+      float a[4], b[4];
+      __builtin_memcpy(a, &w0, sizeof a);
+      __builtin_memcpy(b, &w1, sizeof b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] = fmaf(p.decay, a[e], -t.step * v[e]), b[e] = fmaf(p.decay, b[e], -t.step * v[4 + e]);
+      __builtin_memcpy(&w0, a, sizeof a);
+      __builtin_memcpy(&w1, b, sizeof b);
+    } else {
+      uint16_t h[8];
+      __builtin_memcpy(h, &w0, sizeof h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float w = t.pdt == kBF16 ? Elem<kBF16>::up(h[e]) : Elem<kF16>::up(h[e]);
+        const float n = fmaf(p.decay, w, -t.step * v[e]);
+        h[e] = t.pdt == kBF16 ? Elem<kBF16>::down(n) : Elem<kF16>::down(n);
+      }
+      __builtin_memcpy(&w0, h, sizeof h);
     }
   }
   __device__ __forceinline__ static void meet() {
@@ -328,7 +457,8 @@ struct MuonResults {
     meet();
     const float f = OP == kGram ? p.sa / (p.sx * p.sx) : OP == kPoly ? p.c * (p.sb / (p.sa * p.sa))
                                                        : OP == kUpdate ? 1.f / p.sb : 1.f / (p.sb * p.sx);
-    const float g = OP == kPoly ? p.b * (p.sb / p.sa) : OP == kUpdate ? p.a : p.a / p.sx;
+    const float g = OP == kPoly ? p.b * (p.sb / p.sa) : OP == kUpdate ? p.own : p.own / p.sx;
+    const bool diagonal = OP == kPoly && p.rest != 0.f && row0 < col0 + COLS && col0 < row0 + 32;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int in = q * RPI + lane / LPR;
@@ -341,6 +471,10 @@ struct MuonResults {
       if constexpr (OP != kGram) {
         muon_add(v, g, o.hi[q]);
         if (TWO) muon_add(v, g, o.lo[q]);
+      }
+      if (diagonal) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += row == col + e && row < k ? p.rest * p.sb : 0.f;
       }
       if (OP == kLast || mirror) __builtin_memcpy(__builtin_assume_aligned(at, 16), v, sizeof v);
       if constexpr (OP != kLast) {
@@ -355,20 +489,43 @@ struct MuonResults {
     }
     meet();
     if constexpr (OP == kLast) {
-      // (of any type and alignment: code too long to be there for each piece's rows)
       const int n = (int)min((int64_t)8, t.c - col);
-#pragma unroll 1
-      for (int q = 0; q < Q; ++q) {
-        const int64_t row = row0 + q * RPI + lane / LPR;
-        if (row >= rows || n <= 0) continue;
-        float v[8], w[8];
-        __builtin_memcpy(v, __builtin_assume_aligned(lds + (q * RPI + lane / LPR) * PITCH + lane % LPR * 8, 16), sizeof v);
-        if (t.upd) muon_save8(t.upd, t.udt, row * t.ldu + col, v, n);
-        if (t.param) {
-          muon_load8(t.param, t.pdt, row * t.ldp + col, w, n);
+      if (vectors) {
+        const int64_t eb = dtype_bytes(t.pdt);
+        uint8_t* const at = static_cast<uint8_t*>(t.param) + min(col, (int64_t)t.c - 8) * eb;
+        uint4 w[2 * Q];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = fmaf(p.decay, w[e], -t.step * v[e]);
-          muon_save8(t.param, t.pdt, row * t.ldp + col, w, n);
+        for (int q = 0; q < Q; ++q) {
+          const uint8_t* x = at + min(row0 + q * RPI + lane / LPR, rows - 1) * t.ldp * eb;
+          w[2 * q] = *reinterpret_cast<const uint4*>(x);
+          if (eb == 4) w[2 * q + 1] = *reinterpret_cast<const uint4*>(x + 16);
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int64_t row = row0 + q * RPI + lane / LPR;
+          float v[8];
+          __builtin_memcpy(v, __builtin_assume_aligned(lds + (q * RPI + lane / LPR) * PITCH + lane % LPR * 8, 16), sizeof v);
+          step8(w[2 * q], w[2 * q + 1], v);
+          if (row >= rows || n <= 0) continue;
+          uint8_t* out = at + row * t.ldp * eb;
+          *reinterpret_cast<uint4*>(out) = w[2 * q];
+          if (eb == 4) *reinterpret_cast<uint4*>(out + 16) = w[2 * q + 1];
+        }
+      } else {
+        // (of any type and alignment: code too long to be there for each piece's rows)
+#pragma unroll 1
+        for (int q = 0; q < Q; ++q) {
+          const int64_t row = row0 + q * RPI + lane / LPR;
+          if (row >= rows || n <= 0) continue;
+          float v[8], w[8];
+          __builtin_memcpy(v, __builtin_assume_aligned(lds + (q * RPI + lane / LPR) * PITCH + lane % LPR * 8, 16), sizeof v);
+          if (t.upd) muon_save8(t.upd, t.udt, row * t.ldu + col, v, n);
+          if (t.param) {
+            muon_load8(t.param, t.pdt, row * t.ldp + col, w, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = fmaf(p.decay, w[e], -t.step * v[e]);
+            muon_save8(t.param, t.pdt, row * t.ldp + col, w, n);
+          }
         }
       }
       meet();
@@ -528,15 +685,15 @@ bool muon_scales(const MuonOpts& o, float* sx, float* sa, float* sb) {
   double top = 1.0, xmax = 1.0, bmax = 0.0;
   for (int s = 0; s < o.steps; ++s) {
     double next = 0.0;
+    const double rest = muon_late(o, s) ? -(double)o.b - o.c : 0.0;
     for (int i = 0; i <= 512; ++i) {
       const double x = top * i / 512.0, y = x * x, q = (o.b + o.c * y) * y;
       next = std::max(next, std::abs(x * (o.a + q)));
-      bmax = std::max(bmax, std::abs(q));
+      bmax = std::max(bmax, std::abs(q + rest));
     }
     top = next * 1.02 + 1e-3;
     if (!(top < 16.0) || !(bmax < 4096.0)) return false;
     xmax = std::max(xmax, top);
-    if (s > 64) break;  // (bounded so far; what a step maps into itself stays there)
   }
   auto fit = [](double m) { return std::ldexp(1.0f, 14 - (int)std::ceil(std::log2(std::max(m, 1e-3)))); };
   *sx = fit(xmax);
@@ -667,8 +824,15 @@ static MuonGroup make_group(const std::vector<MuonTensor>& t, int first) {
   return g;
 }
 
+static bool all_tiny(const std::vector<MuonTensor>& t) {
+  return std::all_of(t.begin(), t.end(), [](const MuonTensor& x) {
+    return std::min(x.r, x.c) <= kTinyShort && std::max(x.r, x.c) <= kTinyLong;
+  });
+}
+
 size_t muon_workspace(const std::vector<MuonTensor>& t) {
   size_t bytes = 256;
+  if (all_tiny(t)) return bytes;
   for (int i = 0; i < (int)t.size();) {
     const MuonGroup g = make_group(t, i);
     bytes = std::max(bytes, g.bytes);
@@ -703,8 +867,26 @@ static void product_of(MuonArgs& p, const MuonGroup& g, const MuonLaunch& l, hip
     product_in<OP, false>(p, l.shape, s);
 }
 
+// What a matrix's entry says of the caller's tensors.
+static void describe(const MuonTensor& x, MuonMat* q) {
+  q->grad = x.grad, q->mom = x.mom, q->param = x.param, q->upd = x.upd;
+  q->ldg = x.ldg, q->ldp = x.ldp, q->ldu = x.ldu, q->r = (int32_t)x.r, q->c = (int32_t)x.c, q->step = x.step;
+  q->gdt = (uint8_t)x.gdt, q->pdt = (uint8_t)x.pdt, q->udt = (uint8_t)x.udt, q->pieces = (uint8_t)x.pieces;
+}
+
 hipError_t launch_muon(const std::vector<MuonTensor>& t, const MuonOpts& o, void* workspace, hipStream_t s) {
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  if (all_tiny(t)) {
+    for (size_t first = 0; first < t.size(); first += kMuonGroup) {
+      MuonTiny p{};
+      p.n = (int32_t)std::min<size_t>(kMuonGroup, t.size() - first);
+      for (int i = 0; i < p.n; ++i) describe(t[first + (size_t)i], &p.mat[i]);
+      p.mu = o.mu, p.decay = o.decay, p.a = o.a, p.b = o.b, p.c = o.c, p.eps = o.eps, p.steps = o.steps;
+      p.nesterov = o.nesterov;
+      hipLaunchKernelGGL(k_muon_tiny, dim3((unsigned)p.n), dim3(512), 0, s, p);
+    }
+    return hipGetLastError();
+  }
   for (int first = 0; first < (int)t.size();) {
     const MuonGroup g = make_group(t, first);
     MuonTable* const table = reinterpret_cast<MuonTable*>(ws);
@@ -723,10 +905,8 @@ hipError_t launch_muon(const std::vector<MuonTensor>& t, const MuonOpts& o, void
       const int64_t k = std::min(x.r, x.c);
       const size_t xb = (size_t)x.r * muon_ld(x.c) * 4, kb = (size_t)k * muon_ld(k) * 2 * x.pieces;
       MuonMat& q = m.mat[i];
-      q.grad = x.grad, q.mom = x.mom, q.param = x.param, q.upd = x.upd;
+      describe(x, &q);
       q.x0 = take(xb), q.x1 = take(xb), q.a = take(kb), q.b = take(kb);
-      q.ldg = x.ldg, q.ldp = x.ldp, q.ldu = x.ldu, q.r = (int32_t)x.r, q.c = (int32_t)x.c, q.step = x.step;
-      q.gdt = (uint8_t)x.gdt, q.pdt = (uint8_t)x.pdt, q.udt = (uint8_t)x.udt, q.pieces = (uint8_t)x.pieces;
       for (int kind = 0; kind < kMuonKinds; ++kind) {
         const MuonLaunch* l = kind == kGram ? &g.gram : kind == kPoly ? &g.poly : &g.full;
         const int64_t n = kind == kNorm ? norm_groups(x) : kind == kStart ? start_groups(x) : op_tiles(x, kind, kShapes[l->shape]);
@@ -749,6 +929,8 @@ hipError_t launch_muon(const std::vector<MuonTensor>& t, const MuonOpts& o, void
     hipLaunchKernelGGL(k_muon_norm, dim3((unsigned)next[kNorm]), dim3(256), 0, s, p);
     hipLaunchKernelGGL(k_muon_start, dim3((unsigned)next[kStart]), dim3(256), 0, s, p);
     for (int step = 0; step < o.steps; ++step) {
+      p.own = muon_late(o, step) ? o.a + o.b + o.c : o.a;
+      p.rest = o.a - p.own;
       product_of<kGram>(p, g, g.gram, s);
       product_of<kPoly>(p, g, g.poly, s);
       if (step + 1 < o.steps)

@@ -731,7 +731,8 @@ static void logits(const XentTile& p, int64_t tokens, hipStream_t s) {
 
 template <int DT, bool PAIR, int ODT, bool AKC>
 static void product_to(const XentProduct& p, int64_t pieces, hipStream_t s) {
-  if (pieces == 1 && cdiv(p.out.m, 256) * cdiv(p.out.n, 256) >= 192) {
+  // (sums of a chunk or two are a write of the result: small workgroups)
+  if (pieces == 1 && p.k > 2 * kMmaK<PAIR> && cdiv(p.out.m, 256) * cdiv(p.out.n, 256) >= 192) {
     const int ntm = (int)cdiv(p.out.m, 256), ntn = (int)cdiv(p.out.n, 256);
     hipLaunchKernelGGL((k_xent_product<DT, PAIR, ODT, AKC, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
   } else {

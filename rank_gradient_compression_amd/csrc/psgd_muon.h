@@ -57,6 +57,7 @@ struct MuonArgs {
   bool nesterov, odd;  // odd: X is in x1
   float mu, decay;     // momentum; what a step leaves of a weight
   float a, b, c, eps;
+  float own, rest;     // X <- own X + B X, B = b A + c A^2 + rest I: own + rest = a
   float sx, sa, sb;    // powers of two that X, A and B are held times
   double* sums;        // the norm's partial sums of squares
   float* parts;        // tiles' sums of one share
@@ -80,6 +81,15 @@ struct MuonOpts {
 // Powers of two that keep X, A and B within fp16 whatever the matrix; false
 // where the polynomial lets singular values grow beyond that.
 bool muon_scales(const MuonOpts& o, float* sx, float* sa, float* sb);
+// Steps from which on X's own part is as small as it gets (k_muon_product).
+inline bool muon_late(const MuonOpts& o, int step) { return step >= 3 && step + 2 >= o.steps; }
+struct MuonTiny {  // matrices that a workgroup each takes whole
+  MuonMat mat[kMuonGroup];
+  float mu, decay, a, b, c, eps;
+  int32_t n, steps;
+  bool nesterov;
+};
+static_assert(sizeof(MuonTiny) <= 4096, "what a kernel's arguments hold");
 size_t muon_workspace(const std::vector<MuonTensor>& t);
 hipError_t launch_muon(const std::vector<MuonTensor>& t, const MuonOpts& o, void* ws, hipStream_t s);
 

@@ -179,8 +179,11 @@ def test_muon_workspace():
     for ws, n in ((0, need), (WS + 64, need), (WS, need - 1)):
         refused(B.psgd_muon_step, table(matrix()), opts(), ws, n, status=B.PSGD_ERR_WORKSPACE, match="workspace")
     refused(B.psgd_muon_step, table(matrix()), opts(), 1 * MB, 1 << 40, match="overlap")
-    # two pieces need more; a long list is worked off in groups
-    assert B.psgd_muon_workspace(table(matrix()), opts(pieces=2)) > need
+    # two pieces need more; matrices that a workgroup each takes whole need nothing;
+    # a long list is worked off in groups
+    wide = matrix(rows=80, cols=300, ldg=300, ldp=300)
+    one = B.psgd_muon_workspace(table(wide), opts(pieces=1))
+    assert need == 256 < one < B.psgd_muon_workspace(table(wide), opts(pieces=2))
     big = matrix(rows=4096, cols=4096, ldg=4096, ldp=4096)
     ten, ninety = (B.psgd_muon_workspace(table(*[big] * n), opts()) for n in (16, 90))
     assert ninety == ten
