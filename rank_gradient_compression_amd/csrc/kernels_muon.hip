@@ -217,9 +217,11 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   for (int e = 0; e < 8; ++e) v[e] = col + e < t.c ? (float)((double)v[e] * inv) : 0.f;
   uint4 hi, lo;
   muon_pieces(v, &hi, &lo);
-  uint16_t* const x = muon_at(p, t.x0) + row * 2 * ld + col;
+  // (where products take both pieces, they alternate; else the lower ones follow
+  // behind a row's upper ones)
+  uint16_t* const x = muon_at(p, t.x0) + row * 2 * ld + (t.pieces == 2 ? mma_piece(col) : col);
   *reinterpret_cast<uint4*>(x) = hi;
-  *reinterpret_cast<uint4*>(x + ld) = lo;
+  *reinterpret_cast<uint4*>(x + (t.pieces == 2 ? kMmaLow : ld)) = lo;
 }
 
 // ------------------------------------------------------- matrices in one piece
@@ -394,8 +396,9 @@ struct MuonResults {
   const MuonMat& t;
   int lane;
   bool mirror;
-  int64_t k, rows, ld, pitch;  // (zeros behind a row's end as well; pieces side by side)
+  int64_t k, rows, ld, pitch, low;  // (zeros behind a row's end as well)
   static constexpr bool TWO = !SYM || PAIR;
+  __device__ __forceinline__ static int64_t place(int64_t c) { return PAIR ? mma_piece(c) : c; }
   struct Old {
     uint4 hi[Q], lo[Q];
   };
@@ -406,16 +409,18 @@ struct MuonResults {
     rows = SYM ? k : mat.r;
     ld = muon_ld(SYM ? k : mat.c);
     pitch = TWO ? 2 * ld : ld;
+    low = PAIR ? kMmaLow : ld;
     vectors = OP == kLast && t.param && !t.upd && t.c % 8 == 0 && ((uintptr_t)t.param & 15) == 0 && t.ldp % 8 == 0;
   }
   __device__ __forceinline__ void ask(int64_t row0, int64_t col0, Old& o) const {
     if constexpr (OP != kGram) {
-      const uint16_t* at = (OP == kPoly ? muon_at(p, t.a) : muon_x(p, t, false)) + min(col0 + lane % LPR * 8, ld - 8);
+      const uint16_t* at = (OP == kPoly ? muon_at(p, t.a) : muon_x(p, t, false)) +
+                           place(min(col0 + lane % LPR * 8, ld - 8));
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const uint16_t* x = at + min(row0 + q * RPI + lane / LPR, rows - 1) * pitch;
         o.hi[q] = *reinterpret_cast<const uint4*>(x);
-        if (TWO) o.lo[q] = *reinterpret_cast<const uint4*>(x + ld);
+        if (TWO) o.lo[q] = *reinterpret_cast<const uint4*>(x + low);
       }
     }
   }
@@ -479,11 +484,11 @@ struct MuonResults {
       if (OP == kLast || mirror) __builtin_memcpy(__builtin_assume_aligned(at, 16), v, sizeof v);
       if constexpr (OP != kLast) {
         if (row < rows && col < ld) {
-          uint16_t* out = (OP == kUpdate ? muon_x(p, t, true) : muon_at(p, OP == kGram ? t.a : t.b)) + row * pitch + col;
+          uint16_t* out = (OP == kUpdate ? muon_x(p, t, true) : muon_at(p, OP == kGram ? t.a : t.b)) + row * pitch + place(col);
           uint4 h, l;
           muon_pieces(v, &h, &l);
           *reinterpret_cast<uint4*>(out) = h;
-          if (TWO) *reinterpret_cast<uint4*>(out + ld) = l;
+          if (TWO) *reinterpret_cast<uint4*>(out + low) = l;
         }
       }
     }
@@ -533,7 +538,7 @@ struct MuonResults {
     if (mirror) {
       const int64_t mrow = col0 + lane;
       if (mrow < k) {
-        uint16_t* const out = muon_at(p, OP == kGram ? t.a : t.b) + mrow * pitch + row0;
+        uint16_t* const out = muon_at(p, OP == kGram ? t.a : t.b) + mrow * pitch;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float v[8];
@@ -541,8 +546,8 @@ struct MuonResults {
           for (int e = 0; e < 8; ++e) v[e] = row0 + q * 8 + e < k ? lds[(q * 8 + e) * PITCH + lane] : 0.f;
           uint4 h, l;
           muon_pieces(v, &h, &l);
-          *reinterpret_cast<uint4*>(out + q * 8) = h;
-          if (TWO) *reinterpret_cast<uint4*>(out + ld + q * 8) = l;
+          *reinterpret_cast<uint4*>(out + place(row0 + q * 8)) = h;
+          if (TWO) *reinterpret_cast<uint4*>(out + place(row0 + q * 8) + low) = l;
         }
       }
       meet();
@@ -604,8 +609,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_muon_product(MuonArgs p) {
     const int64_t m0 = (int64_t)at.tm * BM, n0 = (int64_t)at.tn * BN;
     const int64_t k = min(t.r, t.c), ldk = muon_ld(k), ld = muon_ld(t.c);
     const bool tall = t.r > t.c;
-    const MmaSide x{muon_x(p, t, false), ld, 2 * ld, OP == kGram ? k : tall ? t.r : t.c};
-    const MmaSide s{muon_at(p, OP == kPoly ? t.a : t.b), ldk, PAIR ? 2 * ldk : ldk, k};
+    const MmaSide x{muon_x(p, t, false), 2 * ld, OP == kGram ? k : tall ? t.r : t.c};
+    const MmaSide s{muon_at(p, OP == kPoly ? t.a : t.b), PAIR ? 2 * ldk : ldk, k};
     const int64_t sum = OP == kGram ? max(t.r, t.c) : k;
     typename Wide::Acc acc;
     if constexpr (OP == kPoly) {

@@ -39,7 +39,7 @@ enum { kSx, kSw, kInvSx, kInvSw, kGs, kAlphaX, kAlphaW, kAlphaB, kScalars };
 
 constexpr int kMaxGroups = 1024;    // workgroups that look for a tensor's largest value
 constexpr int64_t kBlockBytes = int64_t(1) << 30;  // of E (and G) at a time
-constexpr int kGradRows = 16;       // tokens of a workgroup of the pass over E
+constexpr int kGradRows = 16;       // tokens of a workgroup of the pass over E, at most
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float load_any(const void* p, int dtype, int64_t i) {
@@ -164,8 +164,8 @@ __global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool 
   xent_scalars(a, train, split, partmax, sc);
 }
 
-// Rows to operands: 16-bit values, or two pieces of fp32 ones side by side,
-// zeros behind the row's end.  One thread = 8 values.  clean: a second copy, the
+// Rows to operands: 16-bit values, or two pieces of fp32 ones, zeros behind the
+// row's end.  One thread = 8 values.  clean: a second copy, the
 // one that dw's product takes, with rows of ignored tokens zero (their G is zero,
 // and zero times what such a row may hold need not be) and the others times their
 // weight's power of two, which goes to `factors` as well.
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c + e < p.d ? q[e] : (T)0;
   }
-  const int64_t at = row * p.dp * (DT == kF32 ? 2 : 1) + c;
+  const int64_t at = DT == kF32 ? row * 2 * p.dp + mma_piece(c) : row * p.dp + c;
   auto put = [&](uint16_t* to, float f) {
     uint16_t hi[8], lo[8];
     if constexpr (DT == kF32) {
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack p) {
       for (int e = 0; e < 8; ++e) hi[e] = lo[e] = 0;
     }
     __builtin_memcpy(to + at, hi, sizeof hi);
-    if constexpr (DT == kF32) __builtin_memcpy(to + p.dp + at, lo, sizeof lo);
+    if constexpr (DT == kF32) __builtin_memcpy(to + kMmaLow + at, lo, sizeof lo);
   };
   if (p.out) put(p.out, 1.f);
   if (!p.clean) return;
@@ -509,26 +509,25 @@ __global__ __launch_bounds__(256) void k_xent_lse(XentArgs a, XentSums p) {
 // ------------------------------------------------------------- the gradient
 struct XentGrad {
   int64_t t, v, vp, nseg;
-  int seg_shift;
+  int seg_shift, rows;  // rows: tokens of a workgroup
   const float2* stats;
   const float *lse, *loss, *weights, *factors, *sc;
   const int64_t* targets;
   int64_t ignore;
   void* e;       // fp16 (G in its place) or fp32
-  uint16_t* g;   // G, or its two pieces side by side
+  uint16_t* g;   // G, or its two pieces
   float* db;     // partial sums, or null
 };
 
-// E to G, eight columns a thread, kGradRows tokens a workgroup one after the
-// other: two readings of a line's worth are under way while one is worked on.
+// E to G, eight columns a thread, `rows` tokens a workgroup one after the other: two readings of a line's worth are under way while one is worked on.
 // A workgroup's columns' sums go to its row of db.
 template <int DT>  // of G: kF16 and kBF16 in E's place, kF32 as two pieces
 __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
-  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, t0 = (int64_t)blockIdx.y * kGradRows;
+  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8, t0 = (int64_t)blockIdx.x * p.rows;
   if (c >= p.vp) return;
   const float gs = p.sc[kGs];
   const int64_t seg = min(c >> p.seg_shift, p.nseg - 1);
-  const int n = (int)min((int64_t)kGradRows, p.t - t0);
+  const int n = (int)min((int64_t)p.rows, p.t - t0);
   float sums[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sums[e] = 0.f;
@@ -567,8 +566,8 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
         const float r = v[e] - Elem<kF16>::up(h[e]);
         lo[e] = Elem<kF16>::down(r == r ? r : 0.f);
       }
-      __builtin_memcpy(p.g + row * 2 * p.vp + p.vp + c, lo, sizeof lo);
-      __builtin_memcpy(p.g + row * 2 * p.vp + c, h, sizeof h);
+      __builtin_memcpy(p.g + row * 2 * p.vp + mma_piece(c), h, sizeof h);
+      __builtin_memcpy(p.g + row * 2 * p.vp + mma_piece(c) + kMmaLow, lo, sizeof lo);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] = Elem<DT>::down(v[e]);
@@ -576,7 +575,7 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
     }
   }
   if (p.db) {
-    float* d = p.db + (int64_t)blockIdx.y * p.vp + c;
+    float* d = p.db + (int64_t)blockIdx.x * p.vp + c;
 #pragma unroll
     for (int e = 0; e < 8; ++e) d[e] = sums[e];
   }
@@ -622,6 +621,47 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p,
   mma_store<ODT>(p.out, p.alpha ? *p.alpha : 1.f, lds, m0 + wave / WN * TM * 32, n0 + wave % WN * TN * 32, acc);
 }
 
+// dw of at most 32 tokens: one step of the matrix cores and a write of the result.
+// A wavefront takes 64 x 64 of it and reads its operands' values one by one (the
+// summed axis is theirs' rows), from caches that hold them.
+template <int DT, bool PAIR, int ODT>
+__global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
+  __shared__ __align__(16) float lds[4][32 * 68];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int t = xcd_position(blockIdx.x, gridDim.x);
+  const int64_t m0 = (int64_t)(t / ntn) * 128 + wave / 2 * 64, n0 = (int64_t)(t % ntn) * 128 + wave % 2 * 64;
+  if (m0 >= p.out.m || n0 >= p.out.n) return;
+  auto read = [&](const MmaSide& s, int64_t first, int tile, int piece) {
+    const int64_t c = min(first + tile * 16 + r, s.len - 1);
+    const uint16_t* q = s.p + (PAIR ? mma_piece(c) + piece * kMmaLow : c);
+    uint16_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = 8 * g + e < p.k ? q[(8 * g + e) * s.ld] : (uint16_t)0;
+    uint4 v;
+    __builtin_memcpy(&v, h, sizeof v);
+    return v;
+  };
+  constexpr int N = PAIR ? 2 : 1;
+  uint4 a[N][4], b[N][4];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[n][i] = read(p.a, m0, i, n), b[n][i] = read(p.b, n0, i, n);
+  v4f acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      if constexpr (PAIR) {
+        acc[i][j] = mma16<DT>(b[N - 1][j], a[0][i], acc[i][j]);
+        acc[i][j] = mma16<DT>(b[0][j], a[N - 1][i], acc[i][j]);
+      }
+      acc[i][j] = mma16<DT>(b[0][j], a[0][i], acc[i][j]);
+    }
+  mma_store<ODT>(p.out, *p.alpha, lds[wave], m0, n0, acc);
+}
+
 // dx = alpha * the pieces' sums in order.
 __global__ __launch_bounds__(256) void k_xent_dx(const float* part, int64_t pieces, int64_t t, int64_t d,
                                                  const float* alpha, const float* factors, void* dx, int dtype,
@@ -651,6 +691,11 @@ static bool readable(const void* p, int64_t ld, int64_t d, int dtype) {
 }
 
 constexpr int64_t kFewTokens = 32;
+
+// Tokens of a workgroup of the pass over E: fewer where that leaves too few of them.
+static int64_t grad_rows(int64_t tokens, int64_t vp) {
+  return std::min<int64_t>(kGradRows, std::max<int64_t>(1, tokens * cdiv(vp, 2048) / 1024));
+}
 
 XentLayout xent_layout(const XentArgs& a, bool train) {
   XentLayout l{};
@@ -684,7 +729,7 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   if (train) {
     l.e = take((size_t)l.block * l.vp * (f32 ? 4 : 2));
     l.g = f32 ? take((size_t)l.block * l.vp * 4) : l.e;
-    l.db = take(a.dbias ? (size_t)cdiv(l.block, kGradRows) * l.vp * sizeof(float) : 0);
+    l.db = take(a.dbias ? (size_t)cdiv(l.block, grad_rows(l.block, l.vp)) * l.vp * sizeof(float) : 0);
     l.dxp = take(a.dx && l.dx_splits > 1 ? (size_t)l.dx_splits * l.block * a.d * sizeof(float) : 0);
     l.dwp = take(a.dw && a.dw_dtype != kF32 && l.block < a.t ? (size_t)a.v * a.d * sizeof(float) : 0);
   }
@@ -731,8 +776,12 @@ static void logits(const XentTile& p, int64_t tokens, hipStream_t s) {
 
 template <int DT, bool PAIR, int ODT, bool AKC>
 static void product_to(const XentProduct& p, int64_t pieces, hipStream_t s) {
-  // (sums of a chunk or two are a write of the result: small workgroups)
-  if (pieces == 1 && p.k > 2 * kMmaK<PAIR> && cdiv(p.out.m, 256) * cdiv(p.out.n, 256) >= 192) {
+  if (!AKC && p.k <= 32) {
+    const int64_t ntm = cdiv(p.out.m, 128), ntn = cdiv(p.out.n, 128);
+    hipLaunchKernelGGL((k_xent_outer<DT, PAIR, ODT>), dim3((unsigned)(ntm * ntn)), dim3(256), 0, s, p, (int)ntn);
+    return;
+  }
+  if (pieces == 1 && cdiv(p.out.m, 256) * cdiv(p.out.n, 256) >= 192) {
     const int ntm = (int)cdiv(p.out.m, 256), ntn = (int)cdiv(p.out.n, 256);
     hipLaunchKernelGGL((k_xent_product<DT, PAIR, ODT, AKC, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
   } else {
@@ -761,10 +810,10 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   float2* const stats = reinterpret_cast<float2*>(ws + l.stats);
   float* const target = reinterpret_cast<float*>(ws + l.target);
   XentTile p{};
-  p.x = l.pack_x ? MmaSide{px + t0 * pitch, l.dp, pitch, n}
-                 : MmaSide{static_cast<const uint16_t*>(a.x) + t0 * a.ldx, 0, a.ldx, n};
-  p.w = l.pack_w ? MmaSide{reinterpret_cast<uint16_t*>(ws + l.w), l.dp, pitch, a.v}
-                 : MmaSide{static_cast<const uint16_t*>(a.w), 0, a.ldw, a.v};
+  p.x = l.pack_x ? MmaSide{px + t0 * pitch, pitch, n}
+                 : MmaSide{static_cast<const uint16_t*>(a.x) + t0 * a.ldx, a.ldx, n};
+  p.w = l.pack_w ? MmaSide{reinterpret_cast<uint16_t*>(ws + l.w), pitch, a.v}
+                 : MmaSide{static_cast<const uint16_t*>(a.w), a.ldw, a.v};
   p.t = n, p.v = a.v, p.d = a.d, p.sc = sc, p.bias = a.bias, p.bias_dtype = a.dtype;
   p.targets = a.targets + t0, p.stats = stats, p.nseg = l.nseg, p.target = target, p.e = ws + l.e, p.vp = l.vp;
   if (train)
@@ -778,19 +827,20 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   if (!train || !(a.dx || a.dw || a.dbias)) return;
   uint16_t* const g = reinterpret_cast<uint16_t*>(ws + l.g);
   float* const db = reinterpret_cast<float*>(ws + l.db);
-  const int64_t parts = cdiv(n, kGradRows);
+  const int rows = (int)grad_rows(l.block, l.vp);
+  const int64_t parts = cdiv(n, rows);
   const float* const factors = a.weights ? reinterpret_cast<float*>(ws + l.rows) + t0 : nullptr;
-  const XentGrad q{n,       a.v, l.vp,           l.nseg,   l.seg_shift, stats, a.lse + t0,                a.loss + t0,
+  const XentGrad q{n,       a.v, l.vp,           l.nseg,   l.seg_shift, rows, stats, a.lse + t0,                a.loss + t0,
                    a.weights ? a.weights + t0 : nullptr, factors, sc, a.targets + t0, a.ignore, ws + l.e, g,
                    a.dbias ? db : nullptr};
-  hipLaunchKernelGGL((k_xent_grad<PAIR ? kF32 : DT>), dim3((unsigned)cdiv(l.vp, 2048), (unsigned)parts), dim3(256),
+  hipLaunchKernelGGL((k_xent_grad<PAIR ? kF32 : DT>), dim3((unsigned)parts, (unsigned)cdiv(l.vp, 2048)), dim3(256),
                      0, s, q);
   if (a.dbias)
     hipLaunchKernelGGL(k_xent_db, dim3(grid(a.v)), dim3(256), 0, s, db, parts, l.vp, a.v, sc, a.dbias, a.dtype,
                        a.accumulate || t0 > 0);
   if (a.dx) {
     XentProduct d{};
-    d.a = MmaSide{g, l.vp, PIECES * l.vp, n};
+    d.a = MmaSide{g, PIECES * l.vp, n};
     d.b = p.w;
     d.b.len = a.d;
     d.k = a.v;
@@ -811,8 +861,8 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   }
   if (a.dw) {
     XentProduct d{};
-    d.a = MmaSide{g, l.vp, PIECES * l.vp, a.v};
-    d.b = MmaSide{px + (l.pack_x ? a.t * pitch : 0) + t0 * pitch, l.dp, pitch, a.d};
+    d.a = MmaSide{g, PIECES * l.vp, a.v};
+    d.b = MmaSide{px + (l.pack_x ? a.t * pitch : 0) + t0 * pitch, pitch, a.d};
     d.k = n, d.alpha = sc + kAlphaW;
     // Blocks before the last add up in fp32: in dw itself, or in memory of
     // their own where dw has fewer bits.

@@ -5,9 +5,10 @@
 // A workgroup computes a BM x BN tile of C = A B^T with WM x WN wavefronts, each
 // TM x TN tiles of 32 x 32 in accumulators, in chunks along the summed axis: 64
 // values of 16-bit matrices.  An fp32 matrix is held as two fp16 pieces, hi + lo
-// (22 bits of every value that is above 2^-39 of the scale they share), side by
-// side in its rows; of such matrices a chunk is 32 values, both pieces of both
-// operands, and a product hi lo + hi hi + lo hi.  (As three products one after
+// (22 bits of every value that is above 2^-39 of the scale they share), 32 upper
+// pieces followed by the same values' lower ones (a line of 128 bytes); of such
+// matrices a chunk is 32 values, both pieces of both operands, and a product
+// hi lo + hi hi + lo hi.  (As three products one after
 // the other every piece is read one and a half times as often, and LDS reads
 // are what the smaller tiles wait for.)
 //
@@ -45,10 +46,13 @@ constexpr uint32_t kMmaOff = 0x80000000u;  // an offset that no descriptor reach
 // multiple of 8.
 struct MmaSide {
   const uint16_t* p;
-  int64_t lo;   // from a value's upper piece to its lower one
-  int64_t ld;   // row stride
+  int64_t ld;   // row stride (in pieces where there are two)
   int64_t len;  // size of the tile's axis
 };
+
+// Where value c of a row of pairs has its upper piece (its lower one: kMmaLow on).
+constexpr int kMmaLow = 32;
+__host__ __device__ constexpr int64_t mma_piece(int64_t c) { return c / 32 * 64 + c % 32; }
 
 template <int DT>
 __device__ __forceinline__ v4f mma16(uint4 a, uint4 b, v4f c) {
@@ -86,22 +90,23 @@ struct MmaLoad {
   static constexpr int kSlots = R / 8;  // K-strided: 16-byte slots of a row
   const uint16_t* p;  // the tile's first value
   int64_t ld;
-  uint32_t lo, rows, left, off[kLoads], slot[2];
+  uint32_t rows, left, off[kLoads], slot[2];
   __amdgpu_buffer_rsrc_t r;  // of the present chunk
   __device__ __forceinline__ MmaLoad(const MmaSide& s, int64_t r0, int wave, int lane) {
     ld = s.ld;
-    lo = PAIR ? (uint32_t)s.lo * 2 : 0;
     rows = (uint32_t)min((int64_t)R, s.len - r0);
-    p = s.p + r0 * (KC ? s.ld : 1);
+    p = s.p + (KC ? r0 * s.ld : PAIR ? mma_piece(r0) : r0);
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       if constexpr (KC) {
         const int row = (wave * kLoads + j) * 8 + (lane >> 3), b = (lane & 7) ^ mma_key(row);
-        off[j] = (uint32_t)(row * s.ld * 2) + (PAIR ? (b >> 1) * 16 + (b & 1) * lo : b * 16);
+        off[j] = (uint32_t)(row * s.ld * 2) + (PAIR ? (b >> 1) * 16 + (b & 1) * (kMmaLow * 2) : b * 16);
       } else {
         const int at = (wave * kLoads + j) * 64 + lane, row = at / kSlots, b = at % kSlots;
-        off[j] = (uint32_t)((PAIR ? (row >> 4) * 8 + (row & 7) : row) * s.ld * 2) + (PAIR ? (row >> 3 & 1) * lo : 0) +
-                 mma_tunit<kSlots / 2>(b >> 1, row) * 32 + (b & 1) * 16;
+        const int c = mma_tunit<kSlots / 2>(b >> 1, row) * 2 + (b & 1);  // the block of 8 columns
+        off[j] = PAIR ? (uint32_t)(((row >> 4) * 8 + (row & 7)) * s.ld * 2) + (c >> 2) * 128 + (c & 3) * 16 +
+                            (row >> 3 & 1) * (kMmaLow * 2)
+                      : (uint32_t)(row * s.ld * 2) + c * 16;
       }
     }
     if constexpr (KC) {  // first values of the blocks of even and odd groups of 8 rows
@@ -111,12 +116,16 @@ struct MmaLoad {
   }
   // To a chunk of which `left` values are left (0: a chunk of zeros).  Without
   // branches, which would cut the loop into pieces that the compiler schedules
-  // one by one.
+  // one by one.  (Rows of pairs are whole lines.)
   __device__ __forceinline__ void seek(uint32_t chunk, uint32_t left_) {
     left = left_;
-    const uint16_t* at = p + (int64_t)chunk * K * (KC ? 1 : ld);
+    const uint16_t* at = p + (int64_t)chunk * (KC ? 64 : K * ld);
     const uint32_t some = min(left, 1u), pitch = (uint32_t)ld * 2;
-    const uint32_t n = lo + (KC ? (rows - 1) * pitch + left * 2 : (min(left, (uint32_t)K) - some) * pitch + rows * 2);
+    uint32_t n;
+    if constexpr (KC)
+      n = (rows - 1) * pitch + (PAIR ? kMmaBytes : left * 2);
+    else
+      n = (min(left, (uint32_t)K) - some) * pitch + (PAIR ? (rows + 31) / 32 * 128 : rows * 2);
     r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(at), 0, (int)(((n + 15) & ~15u) * some), 0x00020000);
   }
   // Load j of that chunk.
