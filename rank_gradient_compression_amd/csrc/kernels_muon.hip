@@ -224,6 +224,61 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   *reinterpret_cast<uint4*>(x + (t.pieces == 2 ? kMmaLow : ld)) = lo;
 }
 
+// The last X to the caller's tensors where their rows are no whole vectors (else
+// the last product does it): two values a thread, pairs where they are aligned to
+// one.
+template <int DT>
+__device__ __forceinline__ void muon_pair(void* p, int64_t i, int n, bool read, float decay, float f, const float* v) {
+  using T = typename Elem<DT>::type;
+  T* const at = static_cast<T*>(p) + i;
+  T w[2] = {0, 0};
+  const bool pair = n == 2 && ((uintptr_t)at & (2 * sizeof(T) - 1)) == 0;
+  if (read) {
+    if (pair) {
+      __builtin_memcpy(w, __builtin_assume_aligned(at, 2 * sizeof(T)), sizeof w);
+    } else {
+      w[0] = at[0];
+      w[1] = at[n - 1];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) w[e] = Elem<DT>::down(read ? fmaf(decay, Elem<DT>::up(w[e]), f * v[e]) : f * v[e]);
+  if (pair) {
+    __builtin_memcpy(__builtin_assume_aligned(at, 2 * sizeof(T)), w, sizeof w);
+  } else {
+    at[0] = w[0];
+    if (n == 2) at[1] = w[1];
+  }
+}
+__device__ __forceinline__ void muon_pair_any(void* p, int dtype, int64_t i, int n, bool read, float decay, float f,
+                                              const float* v) {
+  if (dtype == kF32)
+    muon_pair<kF32>(p, i, n, read, decay, f, v);
+  else if (dtype == kBF16)
+    muon_pair<kBF16>(p, i, n, read, decay, f, v);
+  else
+    muon_pair<kF16>(p, i, n, read, decay, f, v);
+}
+__global__ __launch_bounds__(256) void k_muon_apply(MuonArgs p) {
+  const int i = muon_find(p.table->first[kStart], blockIdx.x);
+  const MuonMat t = p.table->mat[i];
+  const int64_t ld = muon_ld(t.c), per = ld / 2, base = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * 1024;
+  const uint16_t* const x = muon_x(p, t, false);
+  const int64_t low = t.pieces == 2 ? kMmaLow : ld;
+#pragma unroll 4
+  for (int q = 0; q < 4; ++q) {
+    const int64_t at = base + q * 256 + threadIdx.x, row = at / per, col = at % per * 2;
+    if (row >= t.r || col >= t.c) continue;
+    const uint16_t* y = x + row * 2 * ld + (t.pieces == 2 ? mma_piece(col) : col);
+    const uint32_t hi = *reinterpret_cast<const uint32_t*>(y), lo = *reinterpret_cast<const uint32_t*>(y + low);
+    const float v[2] = {(Elem<kF16>::up((uint16_t)hi) + Elem<kF16>::up((uint16_t)lo)) / p.sx,
+                        (Elem<kF16>::up((uint16_t)(hi >> 16)) + Elem<kF16>::up((uint16_t)(lo >> 16))) / p.sx};
+    const int n = (int)min((int64_t)2, t.c - col);
+    if (t.upd) muon_pair_any(t.upd, t.udt, row * t.ldu + col, n, false, 0.f, 1.f, v);
+    if (t.param) muon_pair_any(t.param, t.pdt, row * t.ldp + col, n, true, p.decay, -t.step, v);
+  }
+}
+
 // ------------------------------------------------------- matrices in one piece
 // Where every matrix of a call is so small, a workgroup takes one whole: X (the
 // shorter side down), A and B in LDS in fp32, products on the fp32 matrix
@@ -355,31 +410,25 @@ __device__ __forceinline__ void muon_add(float (&v)[8], float f, uint4 q) {  // 
   for (int e = 0; e < 8; ++e) v[e] = fmaf(f, Elem<kF16>::up(h[e]), v[e]);
 }
 
-// Eight neighbouring values of the caller's, n of them there.
-__device__ __forceinline__ void muon_save8(void* p, int dtype, int64_t i, const float (&v)[8], int n) {
+// w <- decay w + f v for eight values of a type (w0; of fp32, w0 and w1).
+__device__ __forceinline__ void muon_eight(int dtype, float decay, float f, const float (&v)[8], uint4& w0, uint4& w1) {
   if (dtype == kF32) {
-    float* at = static_cast<float*>(p) + i;
-    const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
-    store_run<kF32, 4>(at, a, n);
-    store_run<kF32, 4>(at + 4, b, n - 4);
-  } else if (dtype == kBF16) {
-    store_run<kBF16, 8>(static_cast<uint16_t*>(p) + i, v, n);
-  } else {
-    store_run<kF16, 8>(static_cast<uint16_t*>(p) + i, v, n);
-  }
-}
-__device__ __forceinline__ void muon_load8(const void* p, int dtype, int64_t i, float (&v)[8], int n) {
-  if (dtype == kF32) {
-    const float* at = static_cast<const float*>(p) + i;
     float a[4], b[4];
-    load_run<kF32, 4>(at, a, n);
-    load_run<kF32, 4>(at + 4, b, n - 4);
+    __builtin_memcpy(a, &w0, sizeof a);
+    __builtin_memcpy(b, &w1, sizeof b);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-  } else if (dtype == kBF16) {
-    load_run<kBF16, 8>(static_cast<const uint16_t*>(p) + i, v, n);
+    for (int e = 0; e < 4; ++e) a[e] = fmaf(decay, a[e], f * v[e]), b[e] = fmaf(decay, b[e], f * v[4 + e]);
+    __builtin_memcpy(&w0, a, sizeof a);
+    __builtin_memcpy(&w1, b, sizeof b);
   } else {
-    load_run<kF16, 8>(static_cast<const uint16_t*>(p) + i, v, n);
+    uint16_t h[8];
+    __builtin_memcpy(h, &w0, sizeof h);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float n = fmaf(decay, dtype == kBF16 ? Elem<kBF16>::up(h[e]) : Elem<kF16>::up(h[e]), f * v[e]);
+      h[e] = dtype == kBF16 ? Elem<kBF16>::down(n) : Elem<kF16>::down(n);
+    }
+    __builtin_memcpy(&w0, h, sizeof h);
   }
 }
 
@@ -402,7 +451,6 @@ struct MuonResults {
   struct Old {
     uint4 hi[Q], lo[Q];
   };
-  bool vectors;
 
   __device__ __forceinline__ MuonResults(const MuonArgs& args, const MuonMat& mat, bool across)
       : p(args), t(mat), lane(threadIdx.x & 63), mirror(SYM && across), k(min(mat.r, mat.c)) {
@@ -410,7 +458,6 @@ struct MuonResults {
     ld = muon_ld(SYM ? k : mat.c);
     pitch = TWO ? 2 * ld : ld;
     low = PAIR ? kMmaLow : ld;
-    vectors = OP == kLast && t.param && !t.upd && t.c % 8 == 0 && ((uintptr_t)t.param & 15) == 0 && t.ldp % 8 == 0;
   }
   __device__ __forceinline__ void ask(int64_t row0, int64_t col0, Old& o) const {
     if constexpr (OP != kGram) {
@@ -422,28 +469,6 @@ struct MuonResults {
         o.hi[q] = *reinterpret_cast<const uint4*>(x);
         if (TWO) o.lo[q] = *reinterpret_cast<const uint4*>(x + low);
       }
-    }
-  }
-  // Eight weights' new values, in place.
-  __device__ __forceinline__ void step8(uint4& w0, uint4& w1, const float (&v)[8]) const {
-    if (t.pdt == kF32) {
-      float a[4], b[4];
-      __builtin_memcpy(a, &w0, sizeof a);
-      __builtin_memcpy(b, &w1, sizeof b);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) a[e] = fmaf(p.decay, a[e], -t.step * v[e]), b[e] = fmaf(p.decay, b[e], -t.step * v[4 + e]);
-      __builtin_memcpy(&w0, a, sizeof a);
-      __builtin_memcpy(&w1, b, sizeof b);
-    } else {
-      uint16_t h[8];
-      __builtin_memcpy(h, &w0, sizeof h);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float w = t.pdt == kBF16 ? Elem<kBF16>::up(h[e]) : Elem<kF16>::up(h[e]);
-        const float n = fmaf(p.decay, w, -t.step * v[e]);
-        h[e] = t.pdt == kBF16 ? Elem<kBF16>::down(n) : Elem<kF16>::down(n);
-      }
-      __builtin_memcpy(&w0, h, sizeof h);
     }
   }
   __device__ __forceinline__ static void meet() {
@@ -493,9 +518,9 @@ struct MuonResults {
       }
     }
     meet();
-    if constexpr (OP == kLast) {
-      const int n = (int)min((int64_t)8, t.c - col);
-      if (vectors) {
+    if constexpr (OP == kLast) {  // (only where the caller's rows are whole vectors)
+      const bool there = col < t.c;
+      if (t.param) {
         const int64_t eb = dtype_bytes(t.pdt);
         uint8_t* const at = static_cast<uint8_t*>(t.param) + min(col, (int64_t)t.c - 8) * eb;
         uint4 w[2 * Q];
@@ -510,27 +535,26 @@ struct MuonResults {
           const int64_t row = row0 + q * RPI + lane / LPR;
           float v[8];
           __builtin_memcpy(v, __builtin_assume_aligned(lds + (q * RPI + lane / LPR) * PITCH + lane % LPR * 8, 16), sizeof v);
-          step8(w[2 * q], w[2 * q + 1], v);
-          if (row >= rows || n <= 0) continue;
+          muon_eight(t.pdt, p.decay, -t.step, v, w[2 * q], w[2 * q + 1]);
+          if (row >= rows || !there) continue;
           uint8_t* out = at + row * t.ldp * eb;
           *reinterpret_cast<uint4*>(out) = w[2 * q];
           if (eb == 4) *reinterpret_cast<uint4*>(out + 16) = w[2 * q + 1];
         }
-      } else {
-        // (of any type and alignment: code too long to be there for each piece's rows)
-#pragma unroll 1
+      }
+      if (t.upd) {
+        const int64_t eb = dtype_bytes(t.udt);
+#pragma unroll
         for (int q = 0; q < Q; ++q) {
           const int64_t row = row0 + q * RPI + lane / LPR;
-          if (row >= rows || n <= 0) continue;
-          float v[8], w[8];
+          float v[8];
+          uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
           __builtin_memcpy(v, __builtin_assume_aligned(lds + (q * RPI + lane / LPR) * PITCH + lane % LPR * 8, 16), sizeof v);
-          if (t.upd) muon_save8(t.upd, t.udt, row * t.ldu + col, v, n);
-          if (t.param) {
-            muon_load8(t.param, t.pdt, row * t.ldp + col, w, n);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = fmaf(p.decay, w[e], -t.step * v[e]);
-            muon_save8(t.param, t.pdt, row * t.ldp + col, w, n);
-          }
+          muon_eight(t.udt, 0.f, 1.f, v, w0, w1);
+          if (row >= rows || !there) continue;
+          uint8_t* out = static_cast<uint8_t*>(t.upd) + (row * t.ldu + col) * eb;
+          *reinterpret_cast<uint4*>(out) = w0;
+          if (eb == 4) *reinterpret_cast<uint4*>(out + 16) = w1;
         }
       }
       meet();
@@ -879,6 +903,15 @@ static void describe(const MuonTensor& x, MuonMat* q) {
   q->gdt = (uint8_t)x.gdt, q->pdt = (uint8_t)x.pdt, q->udt = (uint8_t)x.udt, q->pieces = (uint8_t)x.pieces;
 }
 
+// The caller's rows are whole vectors of eight values throughout a group.
+static bool whole_vectors(const std::vector<MuonTensor>& t, const MuonGroup& g) {
+  return std::all_of(g.order.begin(), g.order.end(), [&](int i) {
+    const MuonTensor& x = t[(size_t)i];
+    auto fits = [&](const void* p, int64_t ld) { return !p || (((uintptr_t)p & 15) == 0 && ld % 8 == 0); };
+    return x.c % 8 == 0 && fits(x.param, x.ldp) && fits(x.upd, x.ldu);
+  });
+}
+
 hipError_t launch_muon(const std::vector<MuonTensor>& t, const MuonOpts& o, void* workspace, hipStream_t s) {
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   if (all_tiny(t)) {
@@ -938,12 +971,13 @@ hipError_t launch_muon(const std::vector<MuonTensor>& t, const MuonOpts& o, void
       p.rest = o.a - p.own;
       product_of<kGram>(p, g, g.gram, s);
       product_of<kPoly>(p, g, g.poly, s);
-      if (step + 1 < o.steps)
+      if (step + 1 < o.steps || !whole_vectors(t, g))
         product_of<kUpdate>(p, g, g.full, s);
       else
         product_of<kLast>(p, g, g.full, s);
       p.odd = !p.odd;
     }
+    if (!whole_vectors(t, g)) hipLaunchKernelGGL(k_muon_apply, dim3((unsigned)next[kStart]), dim3(256), 0, s, p);
     first += g.n;
   }
   return hipGetLastError();

@@ -599,7 +599,8 @@ struct XentProduct {
   int64_t k;
   const float* alpha;  // or null: 1
   MmaOut out;
-  int64_t split_stride;  // elements between the results of two pieces of the summed axis (gridDim.y of them)
+  int64_t split_stride;  // elements between the results of two pieces of the summed axis
+  int pieces;            // of them
 };
 
 template <int DT, bool PAIR, int ODT, bool AKC, int WM, int WN, int TM, int TN>
@@ -607,17 +608,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p,
   using Tile = MmaTile<DT, PAIR, AKC, false, WM, WN, TM, TN>;
   __shared__ __align__(16) uint8_t a0[Tile::BM * kMmaBytes], b0[Tile::BN * kMmaBytes], a1[Tile::BM * kMmaBytes],
       b1[Tile::BN * kMmaBytes];
-  int tm, tn;
-  mma_tile_of_block(blockIdx.x, ntm, ntn, &tm, &tn);
+  // (the tiles of one piece of the summed axis share their operands: neighbours in
+  // the walk, which an XCD takes an eighth of)
+  int tm, tn, piece = 0;
+  if (p.pieces == 1) {
+    mma_tile_of_block(blockIdx.x, ntm, ntn, &tm, &tn);
+  } else {
+    const int t = xcd_position(blockIdx.x, gridDim.x), in = t % (ntm * ntn);
+    piece = t / (ntm * ntn);
+    tm = in % ntm;
+    tn = in / ntm;
+  }
   const int64_t m0 = (int64_t)tm * Tile::BM, n0 = (int64_t)tn * Tile::BN;
   const uint32_t total = (uint32_t)((p.k + Tile::K - 1) / Tile::K);
-  const uint32_t c0 = (uint32_t)((uint64_t)total * blockIdx.y / gridDim.y);
-  const uint32_t c1 = (uint32_t)((uint64_t)total * (blockIdx.y + 1) / gridDim.y);
+  const uint32_t c0 = (uint32_t)((uint64_t)total * piece / p.pieces);
+  const uint32_t c1 = (uint32_t)((uint64_t)total * (piece + 1) / p.pieces);
   typename Tile::Acc acc;
   Tile::run(p.a, p.b, p.k, c0, c1, m0, n0, a0, b0, a1, b1, acc);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* lds = mma_epilogue_lds<Tile>(wave, a0, b0, a1, b1);
-  p.out.c = static_cast<typename Elem<ODT>::type*>(p.out.c) + blockIdx.y * p.split_stride;
+  p.out.c = static_cast<typename Elem<ODT>::type*>(p.out.c) + piece * p.split_stride;
   mma_store<ODT>(p.out, p.alpha ? *p.alpha : 1.f, lds, m0 + wave / WN * TM * 32, n0 + wave % WN * TN * 32, acc);
 }
 
@@ -636,7 +646,9 @@ __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
     const uint16_t* q = s.p + (PAIR ? mma_piece(c) + piece * kMmaLow : c);
     uint16_t h[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = 8 * g + e < p.k ? q[(8 * g + e) * s.ld] : (uint16_t)0;
+    for (int e = 0; e < 8; ++e) h[e] = q[min((int64_t)8 * g + e, p.k - 1) * s.ld];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = 8 * g + e < p.k ? h[e] : (uint16_t)0;
     uint4 v;
     __builtin_memcpy(&v, h, sizeof v);
     return v;
@@ -775,7 +787,8 @@ static void logits(const XentTile& p, int64_t tokens, hipStream_t s) {
 }
 
 template <int DT, bool PAIR, int ODT, bool AKC>
-static void product_to(const XentProduct& p, int64_t pieces, hipStream_t s) {
+static void product_to(XentProduct p, int64_t pieces, hipStream_t s) {
+  p.pieces = (int)pieces;
   if (!AKC && p.k <= 32) {
     const int64_t ntm = cdiv(p.out.m, 128), ntn = cdiv(p.out.n, 128);
     hipLaunchKernelGGL((k_xent_outer<DT, PAIR, ODT>), dim3((unsigned)(ntm * ntn)), dim3(256), 0, s, p, (int)ntn);
@@ -786,7 +799,7 @@ static void product_to(const XentProduct& p, int64_t pieces, hipStream_t s) {
     hipLaunchKernelGGL((k_xent_product<DT, PAIR, ODT, AKC, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
   } else {
     const int ntm = (int)cdiv(p.out.m, 128), ntn = (int)cdiv(p.out.n, 128);
-    hipLaunchKernelGGL((k_xent_product<DT, PAIR, ODT, AKC, 2, 2, 2, 2>), dim3(ntm * ntn, (unsigned)pieces), dim3(256), 0, s,
+    hipLaunchKernelGGL((k_xent_product<DT, PAIR, ODT, AKC, 2, 2, 2, 2>), dim3((unsigned)(ntm * ntn * pieces)), dim3(256), 0, s,
                        p, ntm, ntn);
   }
 }

@@ -344,11 +344,11 @@ template <int DT, int N>
 __device__ __forceinline__ void load_run(const typename Elem<DT>::type* at, float (&v)[N], int n) {
   using T = typename Elem<DT>::type;
   T o[N];
-  if (n >= N && ((uintptr_t)at & 15) == 0) {
+  if (N > 2 && n >= N && ((uintptr_t)at & 15) == 0) {
     __builtin_memcpy(o, __builtin_assume_aligned(at, 16), sizeof o);
-  } else if (n >= N && ((uintptr_t)at & (2 * sizeof(T) - 1)) == 0) {
+  } else if (N > 1 && n >= N && ((uintptr_t)at & (2 * sizeof(T) - 1)) == 0) {
 #pragma unroll
-    for (int e = 0; e < N; e += 2) __builtin_memcpy(o + e, __builtin_assume_aligned(at + e, 2 * sizeof(T)), 2 * sizeof(T));
+    for (int e = 0; e + 1 < N; e += 2) __builtin_memcpy(o + e, __builtin_assume_aligned(at + e, 2 * sizeof(T)), 2 * sizeof(T));
   } else {
 #pragma unroll
     for (int e = 0; e < N; ++e) o[e] = e < n ? at[e] : (T)0;
@@ -362,15 +362,47 @@ __device__ __forceinline__ void store_run(typename Elem<DT>::type* at, const flo
   T o[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) o[e] = Elem<DT>::down(v[e]);
-  if (n >= N && ((uintptr_t)at & 15) == 0) {
+  if (N > 2 && n >= N && ((uintptr_t)at & 15) == 0) {
     __builtin_memcpy(__builtin_assume_aligned(at, 16), o, sizeof o);
-  } else if (n >= N && ((uintptr_t)at & (2 * sizeof(T) - 1)) == 0) {
+  } else if (N > 1 && n >= N && ((uintptr_t)at & (2 * sizeof(T) - 1)) == 0) {
 #pragma unroll
-    for (int e = 0; e < N; e += 2) __builtin_memcpy(__builtin_assume_aligned(at + e, 2 * sizeof(T)), o + e, 2 * sizeof(T));
+    for (int e = 0; e + 1 < N; e += 2) __builtin_memcpy(__builtin_assume_aligned(at + e, 2 * sizeof(T)), o + e, 2 * sizeof(T));
   } else {
 #pragma unroll
     for (int e = 0; e < N; ++e)
       if (e < n) at[e] = o[e];
+  }
+}
+
+// 32 rows of C from LDS, E neighbouring values a lane: as many as the address and
+// the row stride allow to be one access, so that lanes write without gaps.
+template <int DT, int E, int COLS>
+__device__ __forceinline__ void mma_store_rows(const MmaOut& p, const float* lds, int64_t row0, int64_t col0) {
+  using T = typename Elem<DT>::type;
+  constexpr int PITCH = COLS + 4, LPR = COLS / E, RPI = 64 / LPR;
+  const int lane = threadIdx.x & 63, c = lane % LPR * E;
+  const int n = (int)min((int64_t)E, p.n - col0 - c);
+#pragma unroll 4
+  for (int k = 0; k < 32 / RPI; ++k) {
+    const int in = k * RPI + lane / LPR;
+    const int64_t row = row0 + in;
+    if (row >= p.m || n <= 0) continue;
+    float v[E], w[E];
+    __builtin_memcpy(v, __builtin_assume_aligned(lds + in * PITCH + c, E >= 4 ? 16 : 4 * E), sizeof v);
+    const float f = p.row ? p.row[row] : 1.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= f;
+    if (p.add) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += e < n ? p.add[row * p.n + col0 + c + e] : 0.f;
+    }
+    T* const at = static_cast<T*>(p.c) + row * p.ldc + col0 + c;
+    if (p.accumulate) {
+      load_run<DT, E>(at, w, n);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += w[e];
+    }
+    store_run<DT, E>(at, v, n);
   }
 }
 
@@ -381,13 +413,10 @@ __device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* l
   const int lane = threadIdx.x & 63;
   constexpr int E = 16 / (int)sizeof(T);
   constexpr int COLS = HB * 16, PITCH = COLS + 4, LPR = COLS / E, RPI = 64 / LPR;
-  const int64_t rl = p.m - row0, cl = p.n - col0;  // rows and columns of C from here on
-  if (rl <= 0 || cl <= 0) return;
-  T* const base = static_cast<T*>(p.c) + row0 * p.ldc + col0 + lane % LPR * E;
-  const float* const add = p.add ? p.add + row0 * p.n + col0 + lane % LPR * E : nullptr;
-  const int n = (int)min((int64_t)E, cl - lane % LPR * E);  // (what is past C's last column is not stored)
-  const bool whole = cl >= COLS && rl >= HA * 16 && ((uintptr_t)base & 15) == 0 && ((p.ldc * sizeof(T)) & 15) == 0 &&
-                     !add && !p.accumulate;
+  if (row0 >= p.m || col0 >= p.n) return;
+  T* const base = static_cast<T*>(p.c) + row0 * p.ldc + col0;
+  const uintptr_t step = (uintptr_t)base | (uintptr_t)(p.ldc * (int64_t)sizeof(T));
+  const bool whole = (step & 15) == 0 && p.n - col0 >= COLS && p.m - row0 >= HA * 16 && !p.add && !p.accumulate && !p.row;
   float* const wr = lds + (lane & 15) * PITCH + (lane >> 4) * 4;
 #pragma unroll
   for (int i = 0; i < HA / 2; ++i) {
@@ -402,46 +431,23 @@ __device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* l
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if (__all(whole)) {
+    if (whole) {
 #pragma unroll
       for (int k = 0; k < 32 / RPI; ++k) {
         const int row = k * RPI + lane / LPR;
         float v[E];
         __builtin_memcpy(v, __builtin_assume_aligned(lds + row * PITCH + lane % LPR * E, 16), sizeof v);
-        if (p.row) {
-          const float f = p.row[row0 + i * 32 + row];
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] *= f;
-        }
         T o[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = Elem<DT>::down(v[e]);
-        __builtin_memcpy(__builtin_assume_aligned(base + (i * 32 + row) * p.ldc, 16), o, sizeof o);
+        __builtin_memcpy(__builtin_assume_aligned(base + (i * 32 + row) * p.ldc + lane % LPR * E, 16), o, sizeof o);
       }
+    } else if ((step & 15) == 0) {
+      mma_store_rows<DT, E, COLS>(p, lds, row0 + i * 32, col0);
+    } else if ((step & (2 * sizeof(T) - 1)) == 0) {
+      mma_store_rows<DT, 2, COLS>(p, lds, row0 + i * 32, col0);
     } else {
-#pragma unroll 2
-      for (int k = 0; k < 32 / RPI; ++k) {
-        const int row = k * RPI + lane / LPR;
-        if (i * 32 + row >= rl || n <= 0) continue;
-        float v[E], w[E];
-        __builtin_memcpy(v, __builtin_assume_aligned(lds + row * PITCH + lane % LPR * E, 16), sizeof v);
-        if (p.row) {
-          const float f = p.row[row0 + i * 32 + row];
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] *= f;
-        }
-        if (add) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] += e < n ? add[(int64_t)(i * 32 + row) * p.n + e] : 0.f;
-        }
-        T* const at = base + (i * 32 + row) * p.ldc;
-        if (p.accumulate) {
-          load_run<DT, E>(at, w, n);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[e] += w[e];
-        }
-        store_run<DT, E>(at, v, n);
-      }
+      mma_store_rows<DT, 1, COLS>(p, lds, row0 + i * 32, col0);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
