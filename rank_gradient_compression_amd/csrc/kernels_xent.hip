@@ -632,8 +632,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p,
 }
 
 // dw of at most 32 tokens: one step of the matrix cores and a write of the result.
-// A wavefront takes 64 x 64 of it and reads its operands' values one by one (the
-// summed axis is theirs' rows), from caches that hold them.
+// A wavefront takes 64 x 64 of it.  The summed axis is the operands' rows, so a
+// lane reads four neighbouring values of each of its eight rows, one for each of
+// its four tiles: tile i has rows 4 r + i of the 64, and lane (r, g) ends up with
+// columns 16 g .. + 15 of rows 4 r .. + 3.
 template <int DT, bool PAIR, int ODT>
 __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
   __shared__ __align__(16) float lds[4][32 * 68];
@@ -641,24 +643,29 @@ __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
   const int t = xcd_position(blockIdx.x, gridDim.x);
   const int64_t m0 = (int64_t)(t / ntn) * 128 + wave / 2 * 64, n0 = (int64_t)(t % ntn) * 128 + wave % 2 * 64;
   if (m0 >= p.out.m || n0 >= p.out.n) return;
-  auto read = [&](const MmaSide& s, int64_t first, int tile, int piece) {
-    const int64_t c = min(first + tile * 16 + r, s.len - 1);
+  auto read = [&](const MmaSide& s, int64_t first, int piece, uint4 (&v)[4]) {
+    const int64_t c = first + 4 * r;  // (rows are padded to 64 values)
     const uint16_t* q = s.p + (PAIR ? mma_piece(c) + piece * kMmaLow : c);
-    uint16_t h[8];
+    uint2 x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = q[min((int64_t)8 * g + e, p.k - 1) * s.ld];
+    for (int e = 0; e < 8; ++e) x[e] = *reinterpret_cast<const uint2*>(q + min((int64_t)8 * g + e, p.k - 1) * s.ld);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = 8 * g + e < p.k ? h[e] : (uint16_t)0;
-    uint4 v;
-    __builtin_memcpy(&v, h, sizeof v);
-    return v;
+    for (int e = 0; e < 8; ++e) x[e] = 8 * g + e < p.k ? x[e] : make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = __builtin_amdgcn_perm(i < 2 ? x[2 * e + 1].x : x[2 * e + 1].y, i < 2 ? x[2 * e].x : x[2 * e].y,
+                                     i % 2 ? 0x07060302u : 0x05040100u);
+      v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   };
   constexpr int N = PAIR ? 2 : 1;
   uint4 a[N][4], b[N][4];
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[n][i] = read(p.a, m0, i, n), b[n][i] = read(p.b, n0, i, n);
+  for (int n = 0; n < N; ++n) read(p.a, m0, n, a[n]), read(p.b, n0, n, b[n]);
+  const float alpha = *p.alpha;
   v4f acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -671,7 +678,23 @@ __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
       }
       acc[i][j] = mma16<DT>(b[0][j], a[0][i], acc[i][j]);
     }
-  mma_store<ODT>(p.out, *p.alpha, lds[wave], m0, n0, acc);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // 32 rows, half of the lanes', at a time
+    if (r / 8 == h) {
+      float* const wr = lds[wave] + 4 * (r % 8) * 68 + 16 * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<v4f*>(wr + i * 68 + 4 * e) =
+              v4f{acc[i][0][e] * alpha, acc[i][1][e] * alpha, acc[i][2][e] * alpha, acc[i][3][e] * alpha};
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    mma_store_any<ODT, 64>(p.out, lds[wave], m0 + h * 32, n0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
 }
 
 // dx = alpha * the pieces' sums in order.

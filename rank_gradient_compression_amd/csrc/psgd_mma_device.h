@@ -402,8 +402,27 @@ __device__ __forceinline__ void mma_store_rows(const MmaOut& p, const float* lds
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] += w[e];
     }
-    store_run<DT, E>(at, v, n);
+    if (n < E) {
+      store_run<DT, E>(at, v, n);
+    } else {
+      T o[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = Elem<DT>::down(v[e]);
+      __builtin_memcpy(__builtin_assume_aligned(at, E * sizeof(T)), o, sizeof o);
+    }
   }
+}
+
+template <int DT, int COLS>
+__device__ __forceinline__ void mma_store_any(const MmaOut& p, const float* lds, int64_t row0, int64_t col0) {
+  using T = typename Elem<DT>::type;
+  const uintptr_t step = (uintptr_t)(static_cast<T*>(p.c) + row0 * p.ldc + col0) | (uintptr_t)(p.ldc * (int64_t)sizeof(T));
+  if ((step & 15) == 0)
+    mma_store_rows<DT, 16 / (int)sizeof(T), COLS>(p, lds, row0, col0);
+  else if ((step & (2 * sizeof(T) - 1)) == 0)
+    mma_store_rows<DT, 2, COLS>(p, lds, row0, col0);
+  else
+    mma_store_rows<DT, 1, COLS>(p, lds, row0, col0);
 }
 
 template <int DT, int HA, int HB>
@@ -442,12 +461,8 @@ __device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* l
         for (int e = 0; e < E; ++e) o[e] = Elem<DT>::down(v[e]);
         __builtin_memcpy(__builtin_assume_aligned(base + (i * 32 + row) * p.ldc + lane % LPR * E, 16), o, sizeof o);
       }
-    } else if ((step & 15) == 0) {
-      mma_store_rows<DT, E, COLS>(p, lds, row0 + i * 32, col0);
-    } else if ((step & (2 * sizeof(T) - 1)) == 0) {
-      mma_store_rows<DT, 2, COLS>(p, lds, row0 + i * 32, col0);
     } else {
-      mma_store_rows<DT, 1, COLS>(p, lds, row0 + i * 32, col0);
+      mma_store_any<DT, COLS>(p, lds, row0 + i * 32, col0);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
