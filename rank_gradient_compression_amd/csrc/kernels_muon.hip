@@ -38,7 +38,7 @@
 namespace psgd {
 
 constexpr int kSumGroups = 1024;  // workgroups of one matrix's norm, at most
-constexpr int kSumChunk = 8192;   // values of a workgroup at a time
+constexpr int kSumChunk = 4096;   // values of a workgroup at a time
 
 __host__ __device__ inline int64_t muon_ld(int64_t c) { return (c + 63) / 64 * 64; }
 
@@ -113,15 +113,15 @@ __global__ __launch_bounds__(256) void k_muon_norm(MuonArgs p) {
   double s = 0.0;
   for (int64_t e0 = (int64_t)(blockIdx.x - sum0) * kSumChunk; e0 < n; e0 += (int64_t)nsums * kSumChunk) {
     if (wide && e0 + kSumChunk <= n) {
-      float4 g[8], m[8];
+      float4 g[4], m[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] = muon_load4(t.grad, t.gdt, e0 + (k * 256 + threadIdx.x) * 4);
+      for (int k = 0; k < 4; ++k) g[k] = muon_load4(t.grad, t.gdt, e0 + (k * 256 + threadIdx.x) * 4);
       if (has) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m[k] = *reinterpret_cast<const float4*>(t.mom + e0 + (k * 256 + threadIdx.x) * 4);
+        for (int k = 0; k < 4; ++k) m[k] = *reinterpret_cast<const float4*>(t.mom + e0 + (k * 256 + threadIdx.x) * 4);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4; ++k) {
         float gv[4] = {g[k].x, g[k].y, g[k].z, g[k].w}, mv[4] = {m[k].x, m[k].y, m[k].z, m[k].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -163,7 +163,8 @@ __device__ __forceinline__ void muon_pieces(const float (&v)[8], uint4* hi, uint
   __builtin_memcpy(lo, l, sizeof l);
 }
 
-// The first X, zeros behind a row's end: eight values a thread.
+// The first X, zeros behind a row's end: eight values a thread at a time.
+constexpr int kStartRounds = 4;  // (every workgroup adds up the norm's sums: 8192 values share that)
 __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   const int i = muon_find(p.table->first[kStart], blockIdx.x);
   const int sum0 = p.table->first[kNorm][i], nsums = p.table->chunks[kNorm][i];
@@ -180,48 +181,50 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   const double norm = sqrt(part[0] + part[1] + part[2] + part[3]);
   // (a double: 1 over the norm of tiny gradients is no fp32 number)
   const double inv = (double)p.sx / (norm + (double)p.eps);
-  const int64_t ld = muon_ld(t.c), per = ld / 8, at = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * 256 + threadIdx.x;
-  if (at >= t.r * per) return;
-  const int64_t row = at / per, col = at % per * 8;
+  const int64_t ld = muon_ld(t.c), per = ld / 8;
+  const int64_t first = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * (256 * kStartRounds) + threadIdx.x;
   const bool has = t.mom != nullptr;
-  float v[8];
-  const int64_t ge = row * t.ldg + col, me = row * t.c + col;
-  const bool wide = col + 8 <= t.c && t.c % 4 == 0 && t.ldg % 4 == 0 && aligned4(t.grad, t.gdt) &&
-                    (!has || aligned4(t.mom, kF32));
-  const bool pairs = col + 8 <= t.c && t.c % 2 == 0 && t.ldg % 2 == 0 && aligned2(t.grad, t.gdt) &&
-                     (!has || aligned2(t.mom, kF32));
-  if (wide) {
+  const bool whole4 = t.c % 4 == 0 && t.ldg % 4 == 0 && aligned4(t.grad, t.gdt) && (!has || aligned4(t.mom, kF32));
+  const bool whole2 = t.c % 2 == 0 && t.ldg % 2 == 0 && aligned2(t.grad, t.gdt) && (!has || aligned2(t.mom, kF32));
+#pragma unroll 1
+  for (int round = 0; round < kStartRounds; ++round) {
+    const int64_t at = first + round * 256;
+    if (at >= t.r * per) return;
+    const int64_t row = at / per, col = at % per * 8, ge = row * t.ldg + col, me = row * t.c + col;
+    float v[8];
+    if (whole4 && col + 8 <= t.c) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 g = muon_load4(t.grad, t.gdt, ge + 4 * h);
-      const float4 m = has ? *reinterpret_cast<const float4*>(t.mom + me + 4 * h) : make_float4(0.f, 0.f, 0.f, 0.f);
-      v[4 * h] = muon_update(p, has, g.x, m.x), v[4 * h + 1] = muon_update(p, has, g.y, m.y);
-      v[4 * h + 2] = muon_update(p, has, g.z, m.z), v[4 * h + 3] = muon_update(p, has, g.w, m.w);
+      for (int h = 0; h < 2; ++h) {
+        const float4 g = muon_load4(t.grad, t.gdt, ge + 4 * h);
+        const float4 m = has ? *reinterpret_cast<const float4*>(t.mom + me + 4 * h) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[4 * h] = muon_update(p, has, g.x, m.x), v[4 * h + 1] = muon_update(p, has, g.y, m.y);
+        v[4 * h + 2] = muon_update(p, has, g.z, m.z), v[4 * h + 3] = muon_update(p, has, g.w, m.w);
+      }
+    } else if (whole2 && col + 8 <= t.c) {
+      float2 g[4], m[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        g[h] = muon_load2(t.grad, t.gdt, ge + 2 * h);
+        m[h] = has ? *reinterpret_cast<const float2*>(t.mom + me + 2 * h) : make_float2(0.f, 0.f);
+      }
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        v[2 * h] = muon_update(p, has, g[h].x, m[h].x), v[2 * h + 1] = muon_update(p, has, g[h].y, m[h].y);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = col + e < t.c ? muon_update(p, has, muon_load(t.grad, t.gdt, ge + e), has ? t.mom[me + e] : 0.f) : 0.f;
     }
-  } else if (pairs) {
-    float2 g[4], m[4];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      g[h] = muon_load2(t.grad, t.gdt, ge + 2 * h);
-      m[h] = has ? *reinterpret_cast<const float2*>(t.mom + me + 2 * h) : make_float2(0.f, 0.f);
-    }
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-      v[2 * h] = muon_update(p, has, g[h].x, m[h].x), v[2 * h + 1] = muon_update(p, has, g[h].y, m[h].y);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = col + e < t.c ? muon_update(p, has, muon_load(t.grad, t.gdt, ge + e), has ? t.mom[me + e] : 0.f) : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = col + e < t.c ? (float)((double)v[e] * inv) : 0.f;
+    uint4 hi, lo;
+    muon_pieces(v, &hi, &lo);
+    // (where products take both pieces, they alternate; else the lower ones follow
+    // behind a row's upper ones)
+    uint16_t* const x = muon_at(p, t.x0) + row * 2 * ld + (t.pieces == 2 ? mma_piece(col) : col);
+    *reinterpret_cast<uint4*>(x) = hi;
+    *reinterpret_cast<uint4*>(x + (t.pieces == 2 ? kMmaLow : ld)) = lo;
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = col + e < t.c ? (float)((double)v[e] * inv) : 0.f;
-  uint4 hi, lo;
-  muon_pieces(v, &hi, &lo);
-  // (where products take both pieces, they alternate; else the lower ones follow
-  // behind a row's upper ones)
-  uint16_t* const x = muon_at(p, t.x0) + row * 2 * ld + (t.pieces == 2 ? mma_piece(col) : col);
-  *reinterpret_cast<uint4*>(x) = hi;
-  *reinterpret_cast<uint4*>(x + (t.pieces == 2 ? kMmaLow : ld)) = lo;
 }
 
 // The last X to the caller's tensors where their rows are no whole vectors (else
@@ -262,11 +265,12 @@ __device__ __forceinline__ void muon_pair_any(void* p, int dtype, int64_t i, int
 __global__ __launch_bounds__(256) void k_muon_apply(MuonArgs p) {
   const int i = muon_find(p.table->first[kStart], blockIdx.x);
   const MuonMat t = p.table->mat[i];
-  const int64_t ld = muon_ld(t.c), per = ld / 2, base = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * 1024;
+  const int64_t ld = muon_ld(t.c), per = ld / 2;
+  const int64_t base = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * (1024 * kStartRounds);
   const uint16_t* const x = muon_x(p, t, false);
   const int64_t low = t.pieces == 2 ? kMmaLow : ld;
 #pragma unroll 4
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 4 * kStartRounds; ++q) {
     const int64_t at = base + q * 256 + threadIdx.x, row = at / per, col = at % per * 2;
     if (row >= t.r || col >= t.c) continue;
     const uint16_t* y = x + row * 2 * ld + (t.pieces == 2 ? mma_piece(col) : col);
@@ -760,7 +764,7 @@ struct MuonGroup {
 };
 
 static int64_t norm_groups(const MuonTensor& t) { return std::min<int64_t>(kSumGroups, cdiv(t.r * t.c, kSumChunk)); }
-static int64_t start_groups(const MuonTensor& t) { return cdiv(t.r * (muon_ld(t.c) / 8), 256); }
+static int64_t start_groups(const MuonTensor& t) { return cdiv(t.r * (muon_ld(t.c) / 8), 256 * kStartRounds); }
 static int64_t op_tiles(const MuonTensor& t, int op, const MuonShape& s) {
   if (op == kUpdate) return cdiv(t.r, s.bm) * cdiv(t.c, s.bn);
   const int64_t k = std::min(t.r, t.c), m = cdiv(k, s.bm), n = cdiv(k, s.bn);
