@@ -164,7 +164,11 @@ __device__ __forceinline__ void muon_pieces(const float (&v)[8], uint4* hi, uint
 }
 
 // The first X, zeros behind a row's end: eight values a thread at a time.
-constexpr int kStartRounds = 4;  // (every workgroup adds up the norm's sums: 8192 values share that)
+// Rounds of 2048 values of a workgroup of the first X and of new weights.  Each adds
+// up the matrix's sums of squares: where they are many, four rounds share that (a
+// 4096 x 4096 matrix 21 us, with one round 28), else more workgroups are worth more
+// (six of 2600 x 650 30 us, with four rounds 34).
+__host__ __device__ constexpr int muon_rounds(int64_t sums) { return sums >= 1024 ? 4 : 1; }
 __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   const int i = muon_find(p.table->first[kStart], blockIdx.x);
   const int sum0 = p.table->first[kNorm][i], nsums = p.table->chunks[kNorm][i];
@@ -182,12 +186,13 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   // (a double: 1 over the norm of tiny gradients is no fp32 number)
   const double inv = (double)p.sx / (norm + (double)p.eps);
   const int64_t ld = muon_ld(t.c), per = ld / 8;
-  const int64_t first = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * (256 * kStartRounds) + threadIdx.x;
+  const int rounds = muon_rounds(nsums);
+  const int64_t first = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * (256 * rounds) + threadIdx.x;
   const bool has = t.mom != nullptr;
   const bool whole4 = t.c % 4 == 0 && t.ldg % 4 == 0 && aligned4(t.grad, t.gdt) && (!has || aligned4(t.mom, kF32));
   const bool whole2 = t.c % 2 == 0 && t.ldg % 2 == 0 && aligned2(t.grad, t.gdt) && (!has || aligned2(t.mom, kF32));
 #pragma unroll 1
-  for (int round = 0; round < kStartRounds; ++round) {
+  for (int round = 0; round < rounds; ++round) {
     const int64_t at = first + round * 256;
     if (at >= t.r * per) return;
     const int64_t row = at / per, col = at % per * 8, ge = row * t.ldg + col, me = row * t.c + col;
@@ -266,11 +271,12 @@ __global__ __launch_bounds__(256) void k_muon_apply(MuonArgs p) {
   const int i = muon_find(p.table->first[kStart], blockIdx.x);
   const MuonMat t = p.table->mat[i];
   const int64_t ld = muon_ld(t.c), per = ld / 2;
-  const int64_t base = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * (1024 * kStartRounds);
+  const int rounds = muon_rounds(p.table->chunks[kNorm][i]);
+  const int64_t base = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * (1024 * rounds);
   const uint16_t* const x = muon_x(p, t, false);
   const int64_t low = t.pieces == 2 ? kMmaLow : ld;
 #pragma unroll 4
-  for (int q = 0; q < 4 * kStartRounds; ++q) {
+  for (int q = 0; q < 4 * rounds; ++q) {
     const int64_t at = base + q * 256 + threadIdx.x, row = at / per, col = at % per * 2;
     if (row >= t.r || col >= t.c) continue;
     const uint16_t* y = x + row * 2 * ld + (t.pieces == 2 ? mma_piece(col) : col);
@@ -764,7 +770,7 @@ struct MuonGroup {
 };
 
 static int64_t norm_groups(const MuonTensor& t) { return std::min<int64_t>(kSumGroups, cdiv(t.r * t.c, kSumChunk)); }
-static int64_t start_groups(const MuonTensor& t) { return cdiv(t.r * (muon_ld(t.c) / 8), 256 * kStartRounds); }
+static int64_t start_groups(const MuonTensor& t) { return cdiv(t.r * (muon_ld(t.c) / 8), 256 * muon_rounds(norm_groups(t))); }
 static int64_t op_tiles(const MuonTensor& t, int op, const MuonShape& s) {
   if (op == kUpdate) return cdiv(t.r, s.bm) * cdiv(t.c, s.bn);
   const int64_t k = std::min(t.r, t.c), m = cdiv(k, s.bm), n = cdiv(k, s.bn);
