@@ -103,11 +103,22 @@ def cross_entropy_train(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     return loss, lse, dx, dw, dbias
 
 
+def _total(v: torch.Tensor) -> torch.Tensor:
+    """The sum, by blocks of 1024: one sum over more is split over workgroups that
+    meet in memory cleared by a copy engine's fill, which a captured graph must not
+    hold.  (Counts of fewer than 2^24 tokens are exact.)"""
+    while v.numel() > 1024:
+        v = torch.nn.functional.pad(v, (0, -v.numel() % 1024)).view(-1, 1024).sum(1)
+    return v.sum()
+
+
 class _CrossEntropyFunction(torch.autograd.Function):
     """mean and sum: the gradients are formed with the loss, from the same
     logits, and the backward pass multiplies them by the one incoming value.
     none: the incoming gradient has a value per token, so the backward pass forms
-    the logits again."""
+    the logits again.  float16 too, whatever the reduction: its gradients may be
+    too small or too large for the type until the incoming value (a loss scale of
+    65536, say) is part of them."""
 
     @staticmethod
     def forward(ctx, x, w, bias, targets, reduction, ignore_index):
@@ -115,33 +126,35 @@ class _CrossEntropyFunction(torch.autograd.Function):
         b = None if bias is None else bias.contiguous()
         ctx.x_shape, ctx.reduction, ctx.ignore_index = x.shape, reduction, ignore_index
         need = ctx.needs_input_grad[:3]
-        if reduction == "none":
+        ctx.late = reduction == "none" or x.dtype == torch.float16
+        if ctx.late or not any(need):
             loss, _ = cross_entropy(xm, wm, y, b, ignore_index)
             if any(need):
                 ctx.save_for_backward(xm, wm, b, y)
-            return loss.view(targets.shape)
-        if any(need):
+            if reduction == "none":
+                return loss.view(targets.shape)
+        else:
             loss, _, dx, dw, db = cross_entropy_train(xm, wm, y, b, reduction=reduction, ignore_index=ignore_index,
                                                       need_dx=need[0], need_dw=need[1], need_dbias=need[2])
             ctx.save_for_backward(dx, dw, db)
-        else:
-            loss, _ = cross_entropy(xm, wm, y, b, ignore_index)
-        total = loss.sum()
+        total = _total(loss)
         if reduction == "mean":
-            total = total / ((y >= 0) & (y != ignore_index)).sum().clamp(min=1)
+            total = total / _total(((y >= 0) & (y != ignore_index)).float()).clamp(min=1)
         return total
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         need = ctx.needs_input_grad[:3]
-        if ctx.reduction == "none":
+        if ctx.late:
             x, w, b, y = ctx.saved_tensors
-            _, _, dx, dw, db = cross_entropy_train(x, w, y, b, weights=grad.reshape(-1).float(), reduction="sum",
-                                                   ignore_index=ctx.ignore_index, need_dx=need[0], need_dw=need[1],
-                                                   need_dbias=need[2])
+            reduction = "mean" if ctx.reduction == "mean" else "sum"
+            _, _, dx, dw, db = cross_entropy_train(x, w, y, b, weights=grad.float().reshape(-1).expand(y.numel()),
+                                                   reduction=reduction, ignore_index=ctx.ignore_index, need_dx=need[0],
+                                                   need_dw=need[1], need_dbias=need[2])
         else:
-            dx, dw, db = (None if g is None else g * grad.to(g.dtype) for g in ctx.saved_tensors)
+            # (the incoming value stays fp32: one rounding to the type, of the product)
+            dx, dw, db = (None if g is None else (g * grad.float().expand(1)).to(g.dtype) for g in ctx.saved_tensors)
         return None if dx is None else dx.view(ctx.x_shape), dw, db, None, None, None
 
 

@@ -389,6 +389,50 @@ def test_autograd(reduction, dtype):
         close("total", out, ref.loss.sum() / n, (keep.sum() + 60 * U * ref.loss.abs().sum()) / n + U)
 
 
+@pytest.mark.parametrize("dtype,up", [(F16, 65536.0), (F16, 2.0 ** -10), (BF16, 0.3), (F32, 1e30)])
+def test_autograd_incoming_scale(dtype, up):
+    """An incoming scale beyond the type's own range or digits: the bounds are those
+    of gradients of a loss times that scale, and one more rounding of the product."""
+    x, w, y, b = inputs(70, 500, 40, dtype, True, seed=23)
+    leaves = [v.clone().requires_grad_(True) for v in (x, w, b)]
+    T.linear_cross_entropy(leaves[0], leaves[1], y, leaves[2]).backward(torch.tensor(up, device=DEV))
+    # (float16 takes the scale as a weight of every token, with the bound of weights)
+    weights = torch.full((70,), up, device=DEV) if dtype == F16 else None
+    ref = Reference(x, w, y, b, weights, 1.0 if dtype == F16 else up, True)
+    for name, leaf, want, tol in (("dx", leaves[0], ref.dx, ref.tol_dx), ("dw", leaves[1], ref.dw, ref.tol_dw),
+                                  ("db", leaves[2], ref.db, ref.tol_db)):
+        assert torch.isfinite(leaf.grad).all(), name
+        close(name, leaf.grad, want, tol + OUT[dtype] * want.abs(), dtype)
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum"])
+def test_autograd_captured(reduction):
+    """Loss and gradients of 20,000 tokens in a graph, replayed between eager work."""
+    x, w, y, b = inputs(20000, 60, 24, BF16, True, seed=24)
+
+    def step(*leaves):
+        out = T.linear_cross_entropy(leaves[0], leaves[1], y, leaves[2], reduction=reduction)
+        return (out.detach(),) + torch.autograd.grad(out, leaves)
+
+    fixed = [v.clone().requires_grad_(True) for v in (x, w, b)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*fixed)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*fixed)
+    for k in range(4):
+        with torch.no_grad():
+            fixed[0].copy_(x.roll(k, 0) * (1 + k))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(*[v.detach().clone().requires_grad_(True) for v in fixed])
+        for name, a, e in zip(("total", "dx", "dw", "db"), got, want):
+            assert torch.equal(a, e), (name, k)
+
+
 def test_autograd_parts_and_strides():
     x, w, y, b = inputs(30, 50, 24, F32, True, seed=18)
     wt = w.t().contiguous().requires_grad_(True)  # (a transposed weight is copied)
