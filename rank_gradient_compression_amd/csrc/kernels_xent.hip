@@ -181,9 +181,11 @@ struct XentPack {
   float* factors;
 };
 template <int DT>
-__global__ __launch_bounds__(256) void k_xent_pack(XentPack p) {
+__global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsigned first) {
   using T = typename Elem<DT>::type;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = p.dp / 8;
+  const bool second = blockIdx.x >= first;
+  const XentPack p = second ? x : w;
+  const int64_t i = (int64_t)(blockIdx.x - (second ? first : 0)) * 256 + threadIdx.x, per = p.dp / 8;
   if (i >= p.rows * per) return;
   const int64_t row = i / per, c = i % per * 8;
   const T* q = static_cast<const T*>(p.x) + row * p.ld + c;
@@ -631,6 +633,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p,
   mma_store<ODT>(p.out, p.alpha ? *p.alpha : 1.f, lds, m0 + wave / WN * TM * 32, n0 + wave % WN * TN * 32, acc);
 }
 
+// Four neighbouring values of each of a lane's eight rows of an operand of at most
+// 32, by tile.
+template <bool PAIR>
+__device__ __forceinline__ void outer_read(const MmaSide& s, int64_t k, int64_t first, int piece, uint4 (&v)[4]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int64_t c = first + 4 * r;  // (rows are padded to 64 values)
+  const uint16_t* q = s.p + (PAIR ? mma_piece(c) + piece * kMmaLow : c);
+  uint2 x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = *reinterpret_cast<const uint2*>(q + min((int64_t)8 * g + e, k - 1) * s.ld);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 8 * g + e < k ? x[e] : make_uint2(0, 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = __builtin_amdgcn_perm(i < 2 ? x[2 * e + 1].x : x[2 * e + 1].y, i < 2 ? x[2 * e].x : x[2 * e].y,
+                                   i % 2 ? 0x07060302u : 0x05040100u);
+    v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // dw of at most 32 tokens: one step of the matrix cores and a write of the result.
 // A wavefront takes 64 x 64 of it.  The summed axis is the operands' rows, so a
 // lane reads four neighbouring values of each of its eight rows, one for each of
@@ -643,28 +668,10 @@ __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
   const int t = xcd_position(blockIdx.x, gridDim.x);
   const int64_t m0 = (int64_t)(t / ntn) * 128 + wave / 2 * 64, n0 = (int64_t)(t % ntn) * 128 + wave % 2 * 64;
   if (m0 >= p.out.m || n0 >= p.out.n) return;
-  auto read = [&](const MmaSide& s, int64_t first, int piece, uint4 (&v)[4]) {
-    const int64_t c = first + 4 * r;  // (rows are padded to 64 values)
-    const uint16_t* q = s.p + (PAIR ? mma_piece(c) + piece * kMmaLow : c);
-    uint2 x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = *reinterpret_cast<const uint2*>(q + min((int64_t)8 * g + e, p.k - 1) * s.ld);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 8 * g + e < p.k ? x[e] : make_uint2(0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = __builtin_amdgcn_perm(i < 2 ? x[2 * e + 1].x : x[2 * e + 1].y, i < 2 ? x[2 * e].x : x[2 * e].y,
-                                     i % 2 ? 0x07060302u : 0x05040100u);
-      v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  };
   constexpr int N = PAIR ? 2 : 1;
   uint4 a[N][4], b[N][4];
 #pragma unroll
-  for (int n = 0; n < N; ++n) read(p.a, m0, n, a[n]), read(p.b, n0, n, b[n]);
+  for (int n = 0; n < N; ++n) outer_read<PAIR>(p.a, p.k, m0, n, a[n]), outer_read<PAIR>(p.b, p.k, n0, n, b[n]);
   const float alpha = *p.alpha;
   v4f acc[4][4];
 #pragma unroll
@@ -695,6 +702,80 @@ __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+// The same for rows that are no whole vectors but follow each other without a gap:
+// a workgroup takes 32 whole rows, which lie in one piece that starts on a vector,
+// puts them together in LDS as they lie in memory and writes that.  A lane reads two
+// neighbouring values of G's rows here: tile i has rows 2 r + i of the 32.
+template <int DT, bool PAIR, int ODT>
+__global__ __launch_bounds__(256) void k_xent_outer_rows(XentProduct p) {
+  using T = typename Elem<ODT>::type;
+  extern __shared__ __align__(16) uint8_t rows_lds[];
+  T* const lds = reinterpret_cast<T*>(rows_lds);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int64_t m0 = (int64_t)xcd_position(blockIdx.x, gridDim.x) * 32;
+  const int n = (int)p.out.n;
+  constexpr int N = PAIR ? 2 : 1;
+  const float alpha = *p.alpha;
+  uint4 a[N][2];
+#pragma unroll
+  for (int h = 0; h < N; ++h) {
+    const int64_t c = m0 + 2 * r;  // (rows are padded to 64 values)
+    const uint16_t* q = p.a.p + (PAIR ? mma_piece(c) + h * kMmaLow : c);
+    uint32_t x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = *reinterpret_cast<const uint32_t*>(q + min((int64_t)8 * g + e, p.k - 1) * p.a.ld);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 8 * g + e < p.k ? x[e] : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_perm(x[2 * e + 1], x[2 * e], i ? 0x07060302u : 0x05040100u);
+      a[h][i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  for (int n0 = wave * 64; n0 < n; n0 += 256) {
+    uint4 b[N][4];
+#pragma unroll
+    for (int h = 0; h < N; ++h) outer_read<PAIR>(p.b, p.k, n0, h, b[h]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v4f acc[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        if constexpr (PAIR) {
+          acc[j] = mma16<DT>(b[N - 1][j], a[0][i], acc[j]);
+          acc[j] = mma16<DT>(b[0][j], a[N - 1][i], acc[j]);
+        }
+        acc[j] = mma16<DT>(b[0][j], a[0][i], acc[j]);
+      }
+      const int row = 2 * r + i;
+      T* const to = lds + row * n;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // columns 16 g + 2 e and the next
+        const int col = n0 + 16 * g + 2 * e;
+        const float u = acc[e % 2 * 2][e / 2] * alpha, v = acc[e % 2 * 2 + 1][e / 2] * alpha;
+        if constexpr (sizeof(T) == 2) {
+          if (n % 2 == 0) {
+            const uint32_t both = (uint32_t)Elem<ODT>::down(u) | (uint32_t)Elem<ODT>::down(v) << 16;
+            if (col < n) *reinterpret_cast<uint32_t*>(to + col) = both;
+            continue;
+          }
+        }
+        if (col < n) to[col] = Elem<ODT>::down(u);
+        if (col + 1 < n) to[col + 1] = Elem<ODT>::down(v);
+      }
+    }
+  }
+  __syncthreads();
+  const int values = (int)min((int64_t)32, p.out.m - m0) * n, whole = values / (16 / (int)sizeof(T));
+  T* const out = static_cast<T*>(p.out.c) + m0 * n;
+  for (int i = threadIdx.x; i < whole; i += 256)
+    reinterpret_cast<uint4*>(out)[i] = reinterpret_cast<const uint4*>(lds)[i];
+  for (int i = whole * (16 / (int)sizeof(T)) + threadIdx.x; i < values; i += 256) out[i] = lds[i];
 }
 
 // dx = alpha * the pieces' sums in order.
@@ -772,15 +853,16 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   return l;
 }
 
-static void pack(const XentPack& p, int dtype, hipStream_t s) {
-  if (p.rows == 0) return;
-  const dim3 g(grid(p.rows * p.dp / 8)), b(256);
+// The weights' operand and the hidden states' in one launch; rows 0: none of it.
+static void pack(const XentPack& w, const XentPack& x, int dtype, hipStream_t s) {
+  const unsigned first = grid(w.rows * w.dp / 8), all = first + grid(x.rows * x.dp / 8);
+  if (all == 0) return;
   if (dtype == kF32)
-    hipLaunchKernelGGL((k_xent_pack<kF32>), g, b, 0, s, p);
+    hipLaunchKernelGGL((k_xent_pack<kF32>), dim3(all), dim3(256), 0, s, w, x, first);
   else if (dtype == kBF16)
-    hipLaunchKernelGGL((k_xent_pack<kBF16>), g, b, 0, s, p);
+    hipLaunchKernelGGL((k_xent_pack<kBF16>), dim3(all), dim3(256), 0, s, w, x, first);
   else
-    hipLaunchKernelGGL((k_xent_pack<kF16>), g, b, 0, s, p);
+    hipLaunchKernelGGL((k_xent_pack<kF16>), dim3(all), dim3(256), 0, s, w, x, first);
 }
 
 template <int DT, bool PAIR, int KEEP>
@@ -813,6 +895,12 @@ template <int DT, bool PAIR, int ODT, bool AKC>
 static void product_to(XentProduct p, int64_t pieces, hipStream_t s) {
   p.pieces = (int)pieces;
   if (!AKC && p.k <= 32) {
+    const int64_t es = sizeof(typename Elem<ODT>::type), rows = 32 * p.out.n * es;
+    if (!p.out.add && !p.out.accumulate && !p.out.row && p.out.ldc == p.out.n && ((uintptr_t)p.out.c & 15) == 0 &&
+        p.out.n * es % 16 != 0 && rows <= 64 * 1024) {
+      hipLaunchKernelGGL((k_xent_outer_rows<DT, PAIR, ODT>), dim3((unsigned)cdiv(p.out.m, 32)), dim3(256), (size_t)rows, s, p);
+      return;
+    }
     const int64_t ntm = cdiv(p.out.m, 128), ntn = cdiv(p.out.n, 128);
     hipLaunchKernelGGL((k_xent_outer<DT, PAIR, ODT>), dim3((unsigned)(ntm * ntn)), dim3(256), 0, s, p, (int)ntn);
     return;
@@ -931,17 +1019,15 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
   if (f32) hipLaunchKernelGGL(k_xent_max, dim3(2 * kMaxGroups), dim3(256), 0, s, a, partmax);
   if (f32 || (train && a.weights))
     hipLaunchKernelGGL(k_xent_prep, dim3(1), dim3(256), 0, s, a, train, f32, partmax, sc);
-  if (l.pack_w) {
-    const XentPack p{a.w, a.ldw, a.v, a.d, l.dp, sc + kSw, reinterpret_cast<uint16_t*>(ws + l.w)};
-    pack(p, a.dtype, s);
-  }
+  XentPack w{}, x{};
+  if (l.pack_w) w = XentPack{a.w, a.ldw, a.v, a.d, l.dp, sc + kSw, reinterpret_cast<uint16_t*>(ws + l.w)};
   if (l.pack_x || train) {
     uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
-    const XentPack p{a.x,      a.ldx,     a.t,     a.d, l.dp, sc + kSx, l.pack_x ? px : nullptr,
-                     train ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr,
-                     a.targets, a.ignore, a.weights, sc, reinterpret_cast<float*>(ws + l.rows)};
-    pack(p, a.dtype, s);
+    x = XentPack{a.x,       a.ldx,    a.t,       a.d, l.dp, sc + kSx, l.pack_x ? px : nullptr,
+                 train ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr,
+                 a.targets, a.ignore, a.weights, sc,  reinterpret_cast<float*>(ws + l.rows)};
   }
+  pack(w, x, a.dtype, s);
   for (int64_t t0 = 0; t0 < a.t; t0 += l.block) {
     if (a.dtype == kBF16)
       block<kBF16, false>(a, l, train, ws, t0, s);

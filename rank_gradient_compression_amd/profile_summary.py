@@ -63,6 +63,10 @@ def source_file(kernel: str) -> str:
         return "kernels_mxquant.hip"
     if k.startswith("k_mx"):
         return "kernels_mxprod.hip"
+    if k.startswith("k_xent"):
+        return "kernels_xent.hip"
+    if k.startswith("k_muon"):
+        return "kernels_muon.hip"
     return "kernels_valu.hip"
 
 
