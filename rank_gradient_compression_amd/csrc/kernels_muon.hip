@@ -184,7 +184,7 @@ __global__ __launch_bounds__(256) void k_muon_start(MuonArgs p) {
   __syncthreads();
   const double norm = sqrt(part[0] + part[1] + part[2] + part[3]);
   // (a double: 1 over the norm of tiny gradients is no fp32 number)
-  const double inv = (double)p.sx / (norm + (double)p.eps);
+  const double under = norm + (double)p.eps, inv = under == 0.0 ? 0.0 : (double)p.sx / under;  // (0 stays 0 without eps)
   const int64_t ld = muon_ld(t.c), per = ld / 8;
   const int rounds = muon_rounds(nsums);
   const int64_t first = (int64_t)(blockIdx.x - p.table->first[kStart][i]) * (256 * rounds) + threadIdx.x;
@@ -333,7 +333,7 @@ __global__ __launch_bounds__(512) void k_muon_tiny(MuonTiny p) {
   __syncthreads();
   s = 0.0;
   for (int i = 0; i < 8; ++i) s += part[i];
-  const double inv = 1.0 / (sqrt(s) + (double)p.eps);
+  const double under = sqrt(s) + (double)p.eps, inv = under == 0.0 ? 0.0 : 1.0 / under;
   for (int i = threadIdx.x; i < kt * 16 * lt * 16; i += 512) {
     float& v = x[i / (lt * 16) * kTinyX + i % (lt * 16)];
     v = (float)((double)v * inv);

@@ -130,6 +130,11 @@ def test_any_size_of_gradient(scale):
     assert norm(unit - E.newton_schulz(cpu(tiny), eps=0.0)) <= 1e-5 * norm(unit)
 
 
+@pytest.mark.parametrize("r,c", [(50, 30), (300, 280)])
+def test_zero_without_eps(r, c):
+    assert not T.orthogonalize(torch.zeros(r, c, device=DEV), eps=0.0).any()
+
+
 def test_zero_rank_one_and_orthogonal():
     assert not T.orthogonalize(torch.zeros(50, 30, device=DEV)).any()
     u, v = np.random.default_rng(6).standard_normal((2, 60))
