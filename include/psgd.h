@@ -604,8 +604,11 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
  *
  * Precision: products are summed in fp32.  16-bit tensors: probabilities and G
  * have one rounding each to 16 bits (fp16, then `dtype`) before the gradients'
- * products.  fp32 tensors are taken as sums of two fp16 values (22 bits;
- * values below 2^-39 of a tensor's largest vanish).  Sums run in an order that
+ * products (a row of G times a power of two that brings its token's weight to
+ * the type's upper range, so that small weights keep their digits in dx; in dw
+ * G's values below about 2^-24 of the largest weight vanish with fp16).  fp32
+ * tensors are taken as sums of two fp16 values (22 bits; values below 2^-39 of a
+ * tensor's largest vanish).  Sums run in an order that
  * depends on the sizes alone: equal calls give equal bits.
  *
  * workspace: psgd_xent_workspace bytes for the same arguments (`train`: for
