@@ -624,9 +624,10 @@ __device__ __forceinline__ int muon_share(const MuonShares& s, int w) {
 // tiles: their old pieces are read and the new ones written (4 + 4 bytes a value, 25 -
 // 30 us for a round of 256 tiles) after the sums, on a compute unit that holds one
 // workgroup, so nothing runs under them.  4096 x 4096: 100 + 101 + 126 us, 136
-// tiles, then 256, one round each.  Small matrices wait for loads instead: a chunk
-// of a lone 128 x 128 tile takes 0.8 us, 0.35 of them products (six of 2600 x 650
-// fp32: 39 + 27 + 59 us).
+// tiles, then 256, one round each.  Small matrices are start, end and latency: six of
+// 2600 x 650 fp32 39 + 27 + 59 us, and A^2's 21 chunks a tile are 7 us of products.
+// (With the loads of two chunks under way, three stages and one workgroup a compute
+// unit: 41 + 24 us.)
 template <int OP, bool PAIR, int WM, int WN, int TM, int TN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_muon_product(MuonArgs p) {
   using Wide = MmaTile<kF16, PAIR, true, OP == kGram || OP == kPoly, WM, WN, TM, TN>;
