@@ -366,10 +366,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_logits(XentTile p, int
 
 // Few tokens: a stream of the weights, and what counts is how many of its bytes
 // are under way.  A workgroup takes all tokens (MT * 16) and 32 words; its
-// wavefronts take the chunks in turn, each staging its own in LDS, two ahead,
-// in whole 128-byte rows, and their partial tiles are added in wavefront order.
-// 32000 x 4096 bf16 weights (262 MB): 1 token 50 - 52 us, 5.1 TB/s, 24 tokens 54 - 57;
-// 33278 x 650 from the last level of cache, where the copy has just gone: 18 us.
+// wavefronts take the chunks in turn, each staging its own weights in LDS, two
+// chunks ahead, in whole 128-byte rows, and its blocks of x, which every workgroup
+// reads from L2, in registers (staged in LDS as well they left room for one
+// workgroup to a compute unit: 50 us for the 47 below).  The wavefronts' partial
+// tiles are added in their order.  32000 x 4096 bf16 weights (262 MB): 1 token 47 us,
+// 5.5 TB/s, 24 tokens 54 - 57; 33278 x 650 from the last level of cache, where the
+// copy has just gone: 16 us.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_sched_barrier(0);
@@ -380,39 +383,48 @@ __device__ __forceinline__ void wait_loads() {
 template <int DT, bool PAIR, int KEEP, int MT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, 1) void k_xent_logits_few(XentTile p) {
   constexpr int HB = 2;
-  using LX = MmaLoad<PAIR, true, MT * 16, 1>;
   using LW = MmaLoad<PAIR, true, 32, 1>;
-  constexpr int STAGE = LX::kBytes + LW::kBytes, LOADS = LX::kLoads + LW::kLoads, TILES = MT * HB;
+  constexpr int STAGE = LW::kBytes, LOADS = LW::kLoads + 2 * MT, TILES = MT * HB;
   static_assert(TILES * 1024 <= 2 * STAGE, "no room for the partial tiles");
   __shared__ __align__(16) uint8_t st0[WAVES * STAGE], st1[WAVES * STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int64_t col0 = (int64_t)xcd_position(blockIdx.x, gridDim.x) * 32;
-  LX lx(p.x, 0, 0, lane);
   LW lw(p.w, col0, 0, lane);
-  const MmaRead<true, MT * 16> rx(0, lane);
   const MmaRead<true, 32> rw(0, lane);
-  const uint32_t total = (uint32_t)((p.d + LX::K - 1) / LX::K);
+  const uint32_t total = (uint32_t)((p.d + LW::K - 1) / LW::K);
+  // A lane's blocks of x, as the products take them, two of a chunk for each 16 rows,
+  // go to registers; rows past the last and blocks past a row's end read as zero.
+  typedef v4u Rows[MT][2];
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(p.x.p), 0, (int)(((p.t - 1) * p.x.ld + (PAIR ? 2 * LW::K * total : (p.d + 7) / 8 * 8)) * 2), 0x00020000);
+  uint32_t xo[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xo[i] = i * 16 + r < p.t ? (uint32_t)((i * 16 + r) * p.x.ld * 2) + g * (PAIR ? 16 : 32) : kMmaOff;
   uint8_t *const m0 = st0 + wave * STAGE, *const m1 = st1 + wave * STAGE;
-  auto fetch = [&](uint32_t c, uint8_t* m) {
-    const uint32_t at = min(c, total - 1), left = c < total ? (uint32_t)p.d - at * LX::K : 0;
-    lx.seek(at, left);
+  auto fetch = [&](uint32_t c, uint8_t* m, Rows& x) {
+    const uint32_t at = min(c, total - 1), left = c < total ? (uint32_t)p.d - at * LW::K : 0;
     lw.seek(at, left);
 #pragma unroll
-    for (int j = 0; j < LW::kLoads; ++j) lw.load(j, m + LX::kBytes, 0);
+    for (int j = 0; j < LW::kLoads; ++j) lw.load(j, m, 0);
 #pragma unroll
-    for (int j = 0; j < LX::kLoads; ++j) lx.load(j, m, 0);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        x[i][h] = __builtin_amdgcn_raw_buffer_load_b128(
+            rx, (PAIR ? g * 8u : (2 * g + h) * 8u) < left ? (int)(xo[i] + at * kMmaBytes) : (int)kMmaOff,
+            h * (PAIR ? kMmaLow * 2 : 16), 0);
   };
   v4f acc[MT][HB];
 #pragma unroll
   for (int i = 0; i < TILES; ++i) acc[i / HB][i % HB] = v4f{0.f, 0.f, 0.f, 0.f};
-  auto chunk = [&](const uint8_t* m) {
+  auto chunk = [&](const uint8_t* m, const Rows& x) {
     uint4 b[2][HB];
 #pragma unroll
-    for (int j = 0; j < 2 * HB; ++j) b[j / HB][j % HB] = rw(m + LX::kBytes, j / HB, j % HB);
+    for (int j = 0; j < 2 * HB; ++j) b[j / HB][j % HB] = rw(m, j / HB, j % HB);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const uint4 a0 = rx(m, 0, i), a1 = rx(m, 1, i);
+      const uint4 a0 = __builtin_bit_cast(uint4, x[i][0]), a1 = __builtin_bit_cast(uint4, x[i][1]);
 #pragma unroll
       for (int j = 0; j < HB; ++j) {
         if constexpr (PAIR) {
@@ -427,19 +439,20 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_xent_logits_few(XentTile p) {
     }
   };
   uint32_t c = wave;
-  fetch(c, m0);
+  Rows x0, x1;
+  fetch(c, m0, x0);
   __builtin_amdgcn_sched_barrier(0);
-  fetch(c + WAVES, m1);
+  fetch(c + WAVES, m1, x1);
   // (a wavefront without a chunk adds one of zeros)
   do {
     wait_loads<LOADS>();
-    chunk(m0);
+    chunk(m0, x0);
     __builtin_amdgcn_sched_barrier(0);
-    fetch(c + 2 * WAVES, m0);
+    fetch(c + 2 * WAVES, m0, x0);
     wait_loads<LOADS>();
-    chunk(m1);
+    chunk(m1, x1);
     __builtin_amdgcn_sched_barrier(0);
-    fetch(c + 3 * WAVES, m1);
+    fetch(c + 3 * WAVES, m1, x1);
     c += 2 * WAVES;
   } while (c < total);
   __syncthreads();  // (waits for the last fetches, of nothing, as well)
@@ -887,7 +900,7 @@ static void pack(const XentPack& w, const XentPack& x, int dtype, hipStream_t s)
 template <int DT, bool PAIR, int KEEP>
 static void logits(const XentTile& p, int64_t tokens, hipStream_t s) {
   if (tokens <= kFewTokens) {
-    // (four wavefronts, two workgroups to a compute unit, where eight would have
+    // (four wavefronts, five workgroups to a compute unit, where eight would have
     // hardly a chunk each)
     const dim3 g((unsigned)cdiv(p.v, 32));
     const bool brief = p.d <= 16 * kMmaK<PAIR>;
