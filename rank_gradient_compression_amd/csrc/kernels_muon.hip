@@ -397,26 +397,24 @@ __global__ __launch_bounds__(512) void k_muon_tiny(MuonTiny p) {
 }
 
 // ---------------------------------------------------------------- products
-// Tile t of those on and above the diagonal of ntm x ntn, RB times as high as
-// wide: groups of 8 tile rows, column by column, so that neighbours share their
-// operands in L2.
-template <int RB>
-__device__ __forceinline__ void muon_sym_tile(int t, int ntm, int ntn, int* tm, int* tn) {
+// Tile t of those on and above the diagonal of n x n: groups of 8 tile rows,
+// column by column, so that neighbours share their operands in L2.
+__device__ __forceinline__ void muon_sym_tile(int t, int n, int* tm, int* tn) {
   for (int g = 0;; g += 8) {
-    const int h = min(8, ntm - g), cols = ntn - RB * g, edge = min(RB * h, cols);  // columns that the diagonal crosses
+    const int h = min(8, n - g), cols = n - g;  // the diagonal crosses the first h columns
     int c = 0;
-    for (; c < edge && t >= c / RB + 1; ++c) t -= c / RB + 1;
-    if (c < edge) {
+    for (; c < h && t >= c + 1; ++c) t -= c + 1;
+    if (c < h) {
       *tm = g + t;
-      *tn = RB * g + c;
+      *tn = g + c;
       return;
     }
-    if (t < h * (cols - edge)) {
+    if (t < h * (cols - h)) {
       *tm = g + t % h;
-      *tn = RB * g + edge + t / h;
+      *tn = g + h + t / h;
       return;
     }
-    t -= h * (cols - edge);
+    t -= h * (cols - h);
   }
 }
 
@@ -608,7 +606,7 @@ __device__ __forceinline__ MuonTile muon_tile(const MuonMat& t, int at) {  // ti
     r.tm = first + in % rows;
     r.tn = in / rows;
   } else {
-    muon_sym_tile<BM / BN>(at, (min(t.r, t.c) + BM - 1) / BM, (min(t.r, t.c) + BN - 1) / BN, &r.tm, &r.tn);
+    muon_sym_tile(at, (min(t.r, t.c) + BM - 1) / BM, &r.tm, &r.tn);
   }
   return r;
 }
@@ -625,15 +623,18 @@ __device__ __forceinline__ int muon_share(const MuonShares& s, int w) {
 // 30 us for a round of 256 tiles) after the sums, on a compute unit that holds one
 // workgroup, so nothing runs under them.  4096 x 4096: 100 + 101 + 126 us, 136
 // tiles, then 256, one round each.  Small matrices are start, end and latency: six of
-// 2600 x 650 fp32 39 + 27 + 59 us, and A^2's 21 chunks a tile are 7 us of products.
-// (With the loads of two chunks under way, three stages and one workgroup a compute
-// unit: 41 + 24 us.)
+// 2600 x 650 fp32 40 + 23 + 59 us, and A^2's 21 chunks a tile are 7 us of products; tiles of
+// 64 x 64, where all fit one round, shorten that (27 us in tiles of 128 x 128; over
+// ResNet18's convolutions 15 for 21).  (With the loads of two chunks under way, three
+// stages and one workgroup a compute unit, tiles of 128 x 128 took 41 + 24 us.)
 template <int OP, bool PAIR, int WM, int WN, int TM, int TN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_muon_product(MuonArgs p) {
   using Wide = MmaTile<kF16, PAIR, true, OP == kGram || OP == kPoly, WM, WN, TM, TN>;
   using Tall = MmaTile<kF16, PAIR, OP != kGram, OP != kGram, WM, WN, TM, TN>;
   constexpr int HA = Wide::HA, HB = Wide::HB, BM = Wide::BM, BN = Wide::BN;
   __shared__ __align__(16) uint8_t a0[BM * kMmaBytes], b0[BN * kMmaBytes], a1[BM * kMmaBytes], b1[BN * kMmaBytes];
+  constexpr bool kOwn = TM * TN == 2;  // (a stage is too small for results)
+  __shared__ __align__(16) float own[kOwn ? WM * WN * 32 * 68 : 4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   constexpr int KIND = OP == kLast ? kUpdate : OP;
   const MuonTable& tab = *p.table;
@@ -673,8 +674,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_muon_product(MuonArgs p) {
         Wide::run(OP == kGram ? x : s, x, sum, c0, c1, m0, n0, a0, b0, a1, b1, acc);
     }
     if (c1 - c0 == chunks) {
-      float* const lds = mma_epilogue_lds<Wide>(wave, a0, b0, a1, b1);
-      const MuonResults<OP, PAIR, HB> res(p, t, at.tn / (BM / BN) != at.tm);
+      float* lds;
+      if constexpr (kOwn)
+        lds = own + wave * (32 * 68);
+      else
+        lds = mma_epilogue_lds<Wide>(wave, a0, b0, a1, b1);
+      const MuonResults<OP, PAIR, HB> res(p, t, at.tn != at.tm);
       const int64_t row0 = m0 + wave / WN * TM * 32, col0 = n0 + wave % WN * TN * 32;
       typename MuonResults<OP, PAIR, HB>::Old old[2];
       res.ask(row0, col0, old[0]);
@@ -715,7 +720,7 @@ __global__ __launch_bounds__(64) void k_muon_join(MuonArgs p) {
   int w = (int)((int64_t)(c0 - p.sh.chunk0) * p.sh.shares / p.sh.chunks);  // (rounded down, so it may be one share early)
   while (w + 1 < p.sh.shares && muon_share(p.sh, w + 1) <= c0) ++w;
   if (muon_share(p.sh, w + 1) >= c1) return;  // one share did it all
-  const MuonResults<OP, PAIR, HB> res(p, t, at.tn / (BM / BN) != at.tm);
+  const MuonResults<OP, PAIR, HB> res(p, t, at.tn != at.tm);
   const int64_t row0 = (int64_t)at.tm * BM + wave / WN * TM * 32 + h * 32, col0 = (int64_t)at.tn * BN + wave % WN * TN * 32;
   typename MuonResults<OP, PAIR, HB>::Old old;
   res.ask(row0, col0, old);
@@ -766,16 +771,20 @@ constexpr int64_t kGroupValues = int64_t(1) << 28;
 
 // The tiles that a launch may be made of, and what they cost as measured
 // (us): a chunk of a tile on a card full of such tiles, and what a tile takes
-// besides (first loads, results: of A and B, of X).
+// besides (first loads, results: of A and B, of X).  The small ones are for one round
+// of a few.
 struct MuonShape {
   int bm, bn, slots;  // slots: workgroups that the card holds
   double chunk, tile, update;
   double lone;  // a chunk where a compute unit has one such tile only
 };
 constexpr MuonShape kShapes[] = {{256, 256, 256, 1.40, 10.0, 30.0, 1.40},
-                                 {256, 128, 256, 0.95, 12.0, 22.0, 0.95},
-                                 {128, 128, 512, 1.02, 8.0, 14.0, 0.80}};
-constexpr double kJoin = 10.0, kJoinBytes = 4.0e6;  // a joining launch; bytes that parts move in a us
+                                 {128, 128, 512, 1.02, 8.0, 14.0, 0.80},
+                                 {64, 64, 768, 0.42, 6.0, 9.0, 0.38}};
+constexpr double kJoin = 10.0;  // a joining launch
+// Bytes that parts move in a us: as many as the last level of cache keeps beside the
+// operands, or more.
+constexpr double kPartsKept = 64.0e6, kKeptRate = 12.0e6, kPartsRate = 4.0e6;
 
 struct MuonLaunch {
   int shape;
@@ -792,8 +801,8 @@ static int64_t norm_groups(const MuonTensor& t) { return std::min<int64_t>(kSumG
 static int64_t start_groups(const MuonTensor& t) { return cdiv(t.r * (muon_ld(t.c) / 8), 256 * muon_rounds(norm_groups(t))); }
 static int64_t op_tiles(const MuonTensor& t, int op, const MuonShape& s) {
   if (op == kUpdate) return cdiv(t.r, s.bm) * cdiv(t.c, s.bn);
-  const int64_t k = std::min(t.r, t.c), m = cdiv(k, s.bm), n = cdiv(k, s.bn);
-  return m * n - s.bm / s.bn * (m * (m - 1) / 2);  // on and above the diagonal
+  const int64_t m = cdiv(std::min(t.r, t.c), s.bm);
+  return m * (m + 1) / 2;  // on and above the diagonal
 }
 static int64_t op_chunks(const MuonTensor& t, int op) {
   return cdiv(op == kGram ? std::max(t.r, t.c) : std::min(t.r, t.c), t.pieces == 2 ? kMmaK<true> : kMmaK<false>);
@@ -814,6 +823,7 @@ static MuonLaunch plan_launch(const std::vector<MuonTensor>& t, const MuonGroup&
       chunks += n * q;
       longest = std::max(longest, q);
     }
+    if (s.bm == 64 && tiles > s.slots) continue;  // (in shares they lost: ResNet18's convolutions' A 48 us for 41)
     auto split = [&](int64_t whole) {  // the first `whole` tiles as they are, the rest shared
       MuonShares h{};
       h.tiles = (int32_t)tiles;
@@ -841,12 +851,13 @@ static MuonLaunch plan_launch(const std::vector<MuonTensor>& t, const MuonGroup&
       if (h.chunks) {
         const double parts = h.shares > 1 ? std::min<double>(2.0 * h.shares, 2.0 * (double)(tiles - whole) + h.shares) : 0.0;
         us += (double)h.chunks / h.shares * s.chunk * per + tile;
-        if (h.shares > 1) us += kJoin + parts * s.bm * s.bn * 8.0 / kJoinBytes;
+        const double bytes = parts * s.bm * s.bn * sizeof(float);
+        if (h.shares > 1) us += kJoin + 2.0 * bytes / (bytes <= kPartsKept ? kKeptRate : kPartsRate);
       }
       if (least == 0.0 || us < least) least = us, best = {shape, h};
     };
     consider(tiles);
-    if (tiles % s.slots) consider(tiles / s.slots * s.slots);
+    if (s.bm > 64 && tiles % s.slots) consider(tiles / s.slots * s.slots);
   }
   return best;
 }
@@ -903,18 +914,20 @@ template <int OP, bool PAIR, int WM, int WN, int TM, int TN>
 static void product(const MuonArgs& p, hipStream_t s) {
   hipLaunchKernelGGL((k_muon_product<OP, PAIR, WM, WN, TM, TN>), dim3((unsigned)(p.sh.whole + p.sh.shares)),
                      dim3(64 * WM * WN), 0, s, p);
-  if (p.sh.shares > 1)
-    hipLaunchKernelGGL((k_muon_join<OP, PAIR, WM, WN, TM, TN>), dim3((unsigned)((p.sh.tiles - p.sh.whole) * WM * WN * TM)),
-                       dim3(64), 0, s, p);
+  if constexpr (TM * TN > 2) {
+    if (p.sh.shares > 1)
+      hipLaunchKernelGGL((k_muon_join<OP, PAIR, WM, WN, TM, TN>), dim3((unsigned)((p.sh.tiles - p.sh.whole) * WM * WN * TM)),
+                         dim3(64), 0, s, p);
+  }
 }
 template <int OP, bool PAIR>
 static void product_in(const MuonArgs& p, int shape, hipStream_t s) {
   if (shape == 0)
     product<OP, PAIR, 2, 4, 4, 2>(p, s);
   else if (shape == 1)
-    product<OP, PAIR, 4, 2, 2, 2>(p, s);
-  else
     product<OP, PAIR, 2, 2, 2, 2>(p, s);
+  else
+    product<OP, PAIR, 2, 1, 1, 2>(p, s);
 }
 template <int OP>
 static void product_of(MuonArgs& p, const MuonGroup& g, const MuonLaunch& l, hipStream_t s) {
