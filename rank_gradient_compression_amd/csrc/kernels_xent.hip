@@ -270,11 +270,13 @@ __device__ __forceinline__ void xent_row(const XentTile& p, int64_t row, int64_t
 #pragma unroll
   for (int i = 0; i < HB * 4; ++i) m = fmaxf(m, l[i]);
   m = groups_max(m);
-  const float ref = (m == -__builtin_inff() ? 0.f : m) * kLog2e;  // (a segment of masked words: sums of zero)
+  const float ref = m == -__builtin_inff() ? 0.f : m;  // (a segment of masked words: sums of zero)
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < HB * 4; ++i) {
-    ex[i] = __builtin_amdgcn_exp2f(fmaf(l[i], kLog2e, -ref));
+    // (the difference first: times log2 e each, m's rounding would be left of a
+    // segment of large logits, and a finite mask's is anything, infinity included)
+    ex[i] = __builtin_amdgcn_exp2f((l[i] - ref) * kLog2e);
     sum += ex[i];
   }
   sum = groups_sum(sum);
