@@ -16,7 +16,10 @@
 // 4096 x 32000 x 4096 bf16, the products 0.93, 0.83 and 0.89 ms).
 // E in fp16 carries a relative error of 2^-12, G is rounded once to the type
 // that the products take; the target's entry, which would cancel, is formed
-// from the loss, exp(-loss) - 1, instead.  Sums, maxima and products are fp32.
+// from the loss, exp(-loss) - 1, instead.  Sums, maxima and products are fp32.  A
+// row's largest logit M and its S = sum exp(l - M) are kept apart for loss =
+// log S - (l_y - M) and p = exp(l - M) / S: lse, rounded at its full size, would
+// leave that in both (an entry of -0.0106 was 0.4% off with logits around 1000).
 //
 // Tokens' weights.  A row of G is held times a power of two that brings its own
 // weight u_t to 2^13 .. 2^14, so that a token of small weight keeps its digits in
@@ -504,6 +507,7 @@ struct XentSums {
   const int64_t* targets;
   const float* target;
   float *loss, *lse, *sc;
+  float2* sums;  // largest logit and 1 over the sum of exponentials below it, for the gradient
 };
 __global__ __launch_bounds__(256) void k_xent_lse(XentArgs a, XentSums p) {
   const int64_t row = blockIdx.x;
@@ -527,18 +531,21 @@ __global__ __launch_bounds__(256) void k_xent_lse(XentArgs a, XentSums p) {
   if ((threadIdx.x & 63) == 0) sums[wave] = sum;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  const float l = ref + logf(sums[0] + sums[1] + sums[2] + sums[3]);
-  p.lse[row] = l;
+  // (the loss from differences to the largest logit: lse is rounded at its full
+  // size, which would stay in the loss and in the target's entry of G)
+  const float s1 = sums[0] + sums[1] + sums[2] + sums[3], l = logf(s1);
+  p.lse[row] = ref + l;
+  if (p.sums) p.sums[row] = make_float2(ref, 1.f / s1);
   const int64_t y = p.targets[row];
-  p.loss[row] = ignored(y, a.ignore) ? 0.f : y < a.v ? l - p.target[row] : __builtin_nanf("");
+  p.loss[row] = ignored(y, a.ignore) ? 0.f : y < a.v ? l - (p.target[row] - ref) : __builtin_nanf("");
 }
 
 // ------------------------------------------------------------- the gradient
 struct XentGrad {
   int64_t t, v, vp, nseg;
   int seg_shift, rows;  // rows: tokens of a workgroup
-  const float2* stats;
-  const float *lse, *loss, *weights, *factors, *sc;
+  const float2 *stats, *sums;
+  const float *loss, *weights, *factors, *sc;
   const int64_t* targets;
   int64_t ignore;
   void* e;       // fp16 (G in its place) or fp32
@@ -575,7 +582,8 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
     }
     // (a row's own power of two: the largest weight's over the row's factor)
     const float back = p.weights ? p.factors[row] : 1.f, u = p.weights ? p.weights[row] * (gs / back) : gs;
-    const float f = u * __builtin_amdgcn_exp2f((p.stats[row * p.nseg + seg].x - p.lse[row]) * kLog2e);
+    const float2 sum = p.sums[row];
+    const float f = u * (__builtin_amdgcn_exp2f((p.stats[row * p.nseg + seg].x - sum.x) * kLog2e) * sum.y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = off || c + e >= p.v ? 0.f : v[e] * f;
     if (!off && y >= c && y < c + 8) {
@@ -877,6 +885,7 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   l.stats = take((size_t)l.block * l.nseg * sizeof(float2));
   l.target = take((size_t)l.block * sizeof(float));
   if (train) {
+    l.sums = take((size_t)l.block * sizeof(float2));
     l.e = take((size_t)l.block * l.vp * (f32 ? 4 : 2));
     l.g = f32 ? take((size_t)l.block * l.vp * 4) : l.e;
     l.db = take(a.dbias ? (size_t)cdiv(l.block, grad_rows(l.block, l.vp)) * l.vp * sizeof(float) : 0);
@@ -979,16 +988,17 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   else
     logits<DT, PAIR, 0>(p, a.t, s);
   const bool scalars = train && !PAIR && !a.weights && t0 == 0;
+  float2* const sums = train ? reinterpret_cast<float2*>(ws + l.sums) : nullptr;
   hipLaunchKernelGGL(k_xent_lse, dim3((unsigned)n + (scalars ? 1 : 0)), dim3(256), 0, s, a,
                      XentSums{stats, n, l.nseg, a.targets + t0, target, a.loss + t0, a.lse + t0,
-                              reinterpret_cast<float*>(ws + l.scalars)});
+                              reinterpret_cast<float*>(ws + l.scalars), sums});
   if (!train || !(a.dx || a.dw || a.dbias)) return;
   uint16_t* const g = reinterpret_cast<uint16_t*>(ws + l.g);
   float* const db = reinterpret_cast<float*>(ws + l.db);
   const int rows = (int)grad_rows(l.block, l.vp);
   const int64_t parts = cdiv(n, rows);
   const float* const factors = a.weights ? reinterpret_cast<float*>(ws + l.rows) + t0 : nullptr;
-  const XentGrad q{n,       a.v, l.vp,           l.nseg,   l.seg_shift, rows, stats, a.lse + t0,                a.loss + t0,
+  const XentGrad q{n,       a.v, l.vp,           l.nseg,   l.seg_shift, rows, stats, sums, a.loss + t0,
                    a.weights ? a.weights + t0 : nullptr, factors, sc, a.targets + t0, a.ignore, ws + l.e, g,
                    a.dbias ? db : nullptr};
   hipLaunchKernelGGL((k_xent_grad<PAIR ? kF32 : DT>), dim3((unsigned)parts, (unsigned)cdiv(l.vp, 2048)), dim3(256),

@@ -40,3 +40,60 @@ def test_finite_masks_of_whole_segments(t, dtype, mask):
     assert not dw[gone].any() and not db[gone].any()
     again = T.cross_entropy(x, w, y, b)
     assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("t", [20, 130])
+@pytest.mark.parametrize("top", [100.0, 1000.0])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_an_offset_of_all_logits_cancels(t, top, dtype):
+    """Logits of 100 or 1000 and some that every type holds exactly, as does fp32 the
+    sums: what is lost is relative to the distances from a token's largest logit
+    (at most 20 here), not to the logits.
+      loss  the sum of 90 exponentials 2^-19, logf 2^-22, a difference and a rounding of at most 25: 2^-17 in all
+      G     E (fp16: 2^-11 p and 2^-25 of the largest p; fp32 tensors: exact), exponentials and sums 2^-18 p (the
+            target's entry: p times the loss's error, and expm1f's 2^-22), and half a step of the type"""
+    v, d = 90, 8
+    g = torch.Generator(device=DEV)
+    g.manual_seed(41)
+    near = torch.randint(0, 81, (v,), generator=g, device=DEV) * 0.25 - 20.0
+    w = torch.zeros(v, d, dtype=dtype, device=DEV)
+    w[:, 0], w[:, 1], w[:, 2] = 1.0, near.to(dtype), 1.0
+    x = torch.zeros(t, d, dtype=dtype, device=DEV)
+    x[:, 0], x[:, 1] = top, torch.exp2(-(torch.arange(t, device=DEV) % 4).double()).to(dtype)
+    x[torch.arange(t, device=DEV), 2 + torch.arange(t, device=DEV) % 6] = 0.5
+    y = torch.randint(0, v, (t,), generator=g, device=DEV)
+    y[0] = int(near.argmax())
+    l = x.double() @ w.double().t()
+    assert torch.equal(l.float().double(), l)
+    l = l - top
+    want = torch.logsumexp(l, 1) - l.gather(1, y[:, None])[:, 0]
+    say(f"[xent] offset {top} {t} {dtype}")
+    out = torch.zeros(v, d, device=DEV)
+    loss, lse, dx, dw, _ = T.cross_entropy_train(x, w, y, reduction="sum", dw=out)
+    close("loss", loss, want, torch.full_like(want, 2.0 ** -17))
+    p = torch.softmax(l, 1)
+    hot = torch.nn.functional.one_hot(y, v).bool()
+    G = torch.where(hot, torch.expm1(-want)[:, None].expand_as(p), p)
+    half = {F32: 2.0 ** -22, BF16: 2.0 ** -8, F16: 2.0 ** -11}[dtype]
+    e = 0.0 if dtype == F32 else 2.0 ** -11
+    dg = torch.where(hot, p * 2.0 ** -17 + 2.0 ** -22 * G.abs(), p * (e + 2.0 ** -18) + 2.0 ** -25 * p.max(1, keepdim=True).values)
+    dg = dg + half * G.abs()
+    xd, wd = x.double(), w.double()
+    close("dx", dx, G @ wd, dg @ wd.abs() + 200 * U * (G.abs() @ wd.abs()), dtype)
+    # (by column: the one that all share is 100 or 1000, the others 1)
+    close("dw", dw, G.t() @ xd, dg.t() @ xd.abs() + (200 * U) * (G.abs().t() @ xd.abs()), F32)
+
+
+@pytest.mark.parametrize("t", [3, 100])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_every_word_at_the_lowest_value(t, dtype):
+    """Logits that fp32 cannot tell apart: the words are equally likely."""
+    v, d = 200, 16
+    x, w, y, b = inputs(t, v, d, dtype, True, seed=42, ignored=0.0)
+    b[:] = torch.finfo(dtype).min
+    loss, lse, dx, dw, db = T.cross_entropy_train(x, w, y, b, reduction="sum", dw=torch.zeros(v, d, device=DEV))
+    want = torch.full_like(loss, float(np.log(v))).double()
+    close("loss", loss, want, torch.full_like(want, 2.0 ** -20))
+    n = torch.bincount(y, minlength=v).double()
+    e = {F32: 2.0 ** -18, BF16: 2.0 ** -10}[dtype]
+    close("dbias", db, t / v - n, t / v * e + n * 2.0 ** -18, dtype)
