@@ -591,7 +591,8 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
  * its G are zero and its row of x is not looked at for dw (its lse is still
  * written).  A target of `vocab` or more is an error in the data: its loss is
  * NaN and its G zero.  weights: u_t, one float per token (not looked at for
- * ignored tokens), or NULL for ones.  s is `scale`, divided by the number of
+ * ignored tokens; a weight of 0 makes G zero whatever the token's row holds), or
+ * NULL for ones.  s is `scale`, divided by the number of
  * tokens that are not ignored (by 1 if there is none) where `mean` is set.
  * A bias of -infinity takes a word out of the vocabulary.
  *
@@ -607,9 +608,13 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
  * products (a row of G times a power of two that brings its token's weight to
  * the type's upper range, so that small weights keep their digits in dx; in dw
  * G's values below about 2^-24 of the largest weight vanish with fp16).  fp32
- * tensors are taken as sums of two fp16 values (22 bits; values below 2^-39 of a
- * tensor's largest vanish).  Sums run in an order that
- * depends on the sizes alone: equal calls give equal bits.
+ * tensors are taken as sums of two fp16 values under a power of two: 22 bits of
+ * a value down to 2^-16 of the largest under the same power, and an error of
+ * 2^-39 of that largest below.  In the logits every row of x has a power of its
+ * own, so that loss, lse and dx of a token do not depend on other tokens' values;
+ * w has one, and in dw all rows of x that count (not those of ignored tokens and of
+ * weight 0).  Sums run in an order that depends on the sizes alone: equal calls give
+ * equal bits.
  *
  * workspace: psgd_xent_workspace bytes for the same arguments (`train`: for
  * psgd_xent_train), 256-byte aligned, scratch.  It holds at most 1 GiB of

@@ -26,8 +26,11 @@
 // dx; the copy of x that dw's product takes carries the other powers of two,
 // relative to the largest weight's.
 //
-// fp32 tensors are split into two fp16 pieces (psgd_mma_device.h) under one
-// power of two that brings the largest finite value to 2^13 .. 2^14.
+// fp32 tensors are split into two fp16 pieces (psgd_mma_device.h) under a power of
+// two that brings the largest finite value to 2^13 .. 2^14: of its row for x in the
+// logits, which take it back row by row, so that no token's digits depend on what
+// another one, or a row of padding, holds; of the whole matrix for w, and of all
+// rows that count for x in dw, whose sum runs over them.
 
 #include <hip/hip_runtime.h>
 
@@ -39,7 +42,7 @@
 namespace psgd {
 
 // scalars that the device works out for itself
-enum { kSx, kSw, kInvSx, kInvSw, kGs, kAlphaX, kAlphaW, kAlphaB, kScalars };
+enum { kSx, kSw, kEw, kGs, kAlphaX, kAlphaW, kAlphaB, kScalars };  // (kEw: kSw's exponent)
 
 constexpr int kMaxGroups = 1024;    // workgroups that look for a tensor's largest value
 constexpr int64_t kBlockBytes = int64_t(1) << 30;  // of E (and G) at a time
@@ -73,48 +76,78 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // ------------------------------------------------------------ preparations
-// Largest finite magnitude of two fp32 matrices, one partial maximum per
-// workgroup: the first `kMaxGroups` take x, the others w.  Rows without gaps are
-// read as one.  Bound by HBM's latency and reads (33278 x 650: 24 us, 3.7 TB/s).
-__global__ __launch_bounds__(256) void k_xent_max(XentArgs a, float* out) {
-  const bool second = blockIdx.x >= kMaxGroups;
-  const float* p = static_cast<const float*>(second ? a.w : a.x);
-  int64_t rows = second ? a.v : a.t, ld = second ? a.ldw : a.ldx, d = a.d;
-  const int b = blockIdx.x % kMaxGroups;
-  float m = 0.f;
-  auto take = [&](float v) {
-    v = fabsf(v);
-    m = v < __builtin_inff() ? fmaxf(m, v) : m;
-  };
-  if (ld == d && ((uintptr_t)p & 15) == 0) {
-    const int64_t n = rows * d, n4 = n / 4;
-    const float4* q = reinterpret_cast<const float4*>(p);
-#pragma unroll 8
-    for (int64_t i = (int64_t)b * 256 + threadIdx.x; i < n4; i += kMaxGroups * 256) {
-      const float4 v = q[i];
-      take(v.x), take(v.y), take(v.z), take(v.w);
-    }
-    if (b == 0 && threadIdx.x < n - n4 * 4) take(p[n4 * 4 + threadIdx.x]);
-  } else {
-    for (int64_t row = (int64_t)b * 4 + (threadIdx.x >> 6); row < rows; row += kMaxGroups * 4) {
-      const float* q = p + row * ld;
-#pragma unroll 8
-      for (int64_t i = threadIdx.x & 63; i < d; i += 64) take(q[i]);
-    }
-  }
-  m = wave_max(m);
-  __shared__ float part[4];
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x == 0) out[blockIdx.x] = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-}
-
 // 2^e that brings m to 2^13 .. 2^14, e within what fp32 can hold and invert.
 __device__ __forceinline__ int fit_exponent(float m) {
   if (!(m > 0.f)) return 0;
   int e;
   (void)frexpf(m, &e);  // m = f 2^e, f in [1/2, 1)
   return min(max(14 - e, -126), 126);
+}
+
+// A token that the gradients see.
+__device__ __forceinline__ bool counted(const XentArgs& a, int64_t t) {
+  const int64_t y = a.targets[t];
+  return !ignored(y, a.ignore) && y < a.v && !(a.weights && a.weights[t] == 0.f);
+}
+
+// Largest finite magnitude of w and of the rows of x that count, one partial maximum
+// per workgroup: the first `kMaxGroups` take x, the others w; and the exponent of
+// every row of x.  A row of x is a workgroup's where each can have one, else a
+// wavefront's; rows of w without gaps are read as one.  Bound by HBM's latency and
+// reads (33278 x 650: 24 us, 3.7 TB/s).
+__global__ __launch_bounds__(256) void k_xent_max(XentArgs a, bool train, float* out, int* rows_x) {
+  const int b = blockIdx.x % kMaxGroups, wave = threadIdx.x >> 6;
+  __shared__ float part[4];
+  float m = 0.f;
+  auto larger = [](float& to, float v) {
+    v = fabsf(v);
+    to = v < __builtin_inff() ? fmaxf(to, v) : to;
+  };
+  auto larger4 = [&](float& to, const float4& v) { larger(to, v.x), larger(to, v.y), larger(to, v.z), larger(to, v.w); };
+  if (blockIdx.x < kMaxGroups) {
+    const float* p = static_cast<const float*>(a.x);
+    const bool whole = a.t <= kMaxGroups, vec = a.d % 4 == 0 && a.ldx % 4 == 0 && ((uintptr_t)p & 15) == 0;
+    const int64_t lane = whole ? threadIdx.x : threadIdx.x & 63, lanes = whole ? 256 : 64;
+    for (int64_t row = whole ? b : (int64_t)b * 4 + wave; row < a.t; row += whole ? kMaxGroups : kMaxGroups * 4) {
+      const float* q = p + row * a.ldx;
+      float r = 0.f;
+      if (vec) {
+#pragma unroll 8
+        for (int64_t i = lane; i < a.d / 4; i += lanes) larger4(r, reinterpret_cast<const float4*>(q)[i]);
+      } else {
+#pragma unroll 8
+        for (int64_t i = lane; i < a.d; i += lanes) larger(r, q[i]);
+      }
+      r = wave_max(r);
+      if (whole) {  // (one row at most: the barrier is every thread's)
+        if ((threadIdx.x & 63) == 0) part[wave] = r;
+        __syncthreads();
+        r = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+        __syncthreads();
+      }
+      if (lane == 0) rows_x[row] = fit_exponent(r);
+      if (train && counted(a, row)) m = fmaxf(m, r);
+    }
+  } else {
+    const float* p = static_cast<const float*>(a.w);
+    if (a.ldw == a.d && ((uintptr_t)p & 15) == 0) {
+      const int64_t n = a.v * a.d, n4 = n / 4;
+      const float4* q = reinterpret_cast<const float4*>(p);
+#pragma unroll 8
+      for (int64_t i = (int64_t)b * 256 + threadIdx.x; i < n4; i += kMaxGroups * 256) larger4(m, q[i]);
+      if (b == 0 && threadIdx.x < n - n4 * 4) larger(m, p[n4 * 4 + threadIdx.x]);
+    } else {
+      for (int64_t row = (int64_t)b * 4 + wave; row < a.v; row += kMaxGroups * 4) {
+        const float* q = p + row * a.ldw;
+#pragma unroll 8
+        for (int64_t i = threadIdx.x & 63; i < a.d; i += 64) larger(m, q[i]);
+      }
+    }
+  }
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) part[wave] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) out[blockIdx.x] = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
 }
 
 // Exponent of a token's weight; `most` (the largest weight's, the smallest
@@ -156,8 +189,7 @@ __device__ void xent_scalars(const XentArgs& a, bool train, bool split, const fl
   const double s = a.mean ? (double)a.scale / fmax(n, 1.0) : (double)a.scale;
   sc[kSx] = ldexpf(1.f, ex);
   sc[kSw] = ldexpf(1.f, ew);
-  sc[kInvSx] = ldexpf(1.f, -ex);
-  sc[kInvSw] = ldexpf(1.f, -ew);
+  sc[kEw] = (float)ew;
   sc[kGs] = ldexpf(1.f, eg);
   sc[kAlphaX] = (float)ldexp(s, -eg - ew);
   sc[kAlphaW] = (float)ldexp(s, -eg - ex);
@@ -169,18 +201,21 @@ __global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool 
 }
 
 // Rows to operands: 16-bit values, or two pieces of fp32 ones, zeros behind the
-// row's end.  One thread = 8 values.  clean: a second copy, the
-// one that dw's product takes, with rows of ignored tokens zero (their G is zero,
-// and zero times what such a row may hold need not be) and the others times their
+// row's end.  One thread = 8 values.  fp32 rows of x have a power of two each.
+// clean: a second copy, the
+// one that dw's product takes, under one power of two, with rows of tokens that do
+// not count zero (their G is zero, and zero times what such a row may hold need not
+// be) and the others times their
 // weight's power of two, which goes to `factors` as well.  Bound by HBM: 33278 x
 // 650 fp16 18 us, 92 MB read and written, 5.1 TB/s; fp32 31 us, 176 MB, 5.7 TB/s.
 struct XentPack {
   const void* x;
   int64_t ld, rows, d, dp;
-  const float* scale;
+  const float* scale;   // of the whole matrix
+  const int* exponents;  // of every row in `out`, or null: the matrix's
   uint16_t *out, *clean;
   const int64_t* targets;
-  int64_t ignore;
+  int64_t ignore, v;
   const float* weights;
   const float* sc;
   float* factors;
@@ -202,10 +237,10 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsig
     for (int e = 0; e < 8; ++e) v[e] = c + e < p.d ? q[e] : (T)0;
   }
   const int64_t at = DT == kF32 ? row * 2 * p.dp + mma_piece(c) : row * p.dp + c;
-  auto put = [&](uint16_t* to, float f) {
+  auto put = [&](uint16_t* to, float f, float scale) {
     uint16_t hi[8], lo[8];
     if constexpr (DT == kF32) {
-      const float s = *p.scale * f;
+      const float s = scale * f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float z = v[e] * s;
@@ -228,7 +263,7 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsig
     __builtin_memcpy(to + at, hi, sizeof hi);
     if constexpr (DT == kF32) __builtin_memcpy(to + kMmaLow + at, lo, sizeof lo);
   };
-  if (p.out) put(p.out, 1.f);
+  if (p.out) put(p.out, 1.f, DT != kF32 ? 1.f : p.exponents ? ldexpf(1.f, p.exponents[row]) : *p.scale);
   if (!p.clean) return;
   float f = 1.f;
   if (p.weights) {
@@ -239,7 +274,8 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsig
     if (c == 0) p.factors[row] = f;
     if (p.weights[row] == 0.f) f = 0.f;
   }
-  put(p.clean, ignored(p.targets[row], p.ignore) ? 0.f : f);
+  const int64_t y = p.targets[row];
+  put(p.clean, ignored(y, p.ignore) || y >= p.v ? 0.f : f, DT != kF32 ? 1.f : *p.scale);
 }
 
 // ------------------------------------------------------------------ logits
@@ -247,6 +283,7 @@ struct XentTile {
   MmaSide x, w;
   int64_t t, v, d;  // tokens of the block
   const float* sc;
+  const int* exponents;  // of the rows of x as pairs
   const void* bias;
   int bias_dtype;
   const int64_t* targets;
@@ -257,15 +294,21 @@ struct XentTile {
   int64_t vp;
 };
 
+// Exponent that the sums of a row of pairs are to be taken times.
+template <bool PAIR>
+__device__ __forceinline__ int xent_shift(const XentTile& p, int64_t row) {
+  return PAIR && row < p.t ? -(p.exponents[row] + (int)p.sc[kEw]) : 0;
+}
+
 // A row's logits of one segment: lane group g has columns col0 + 16 j + 4 g + e.
 // They become E, and the segment's maximum and sum are written.
 template <bool PAIR, int HB>
 __device__ __forceinline__ void xent_row(const XentTile& p, int64_t row, int64_t col0, int g, const v4f (&acc)[HB],
-                                         const v4f (&bias)[HB], float is, float iw, int64_t y, float (&ex)[HB * 4]) {
+                                         const v4f (&bias)[HB], int shift, int64_t y, float (&ex)[HB * 4]) {
   float l[HB * 4], m = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < HB * 4; ++i)
-    l[i] = (PAIR ? acc[i / 4][i % 4] * is * iw : acc[i / 4][i % 4]) + bias[i / 4][i % 4];
+    l[i] = (PAIR ? __builtin_amdgcn_ldexpf(acc[i / 4][i % 4], shift) : acc[i / 4][i % 4]) + bias[i / 4][i % 4];
   if (col0 + HB * 16 > p.v) {
 #pragma unroll
     for (int i = 0; i < HB * 4; ++i) l[i] = col0 + i / 4 * 16 + 4 * g + i % 4 < p.v ? l[i] : -__builtin_inff();
@@ -328,7 +371,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_logits(XentTile p, int
   if (col0 >= p.v) return;
   v4f bias[Tile::HB];
   xent_bias<Tile::HB>(p, col0, g, bias);
-  const float is = PAIR ? p.sc[kInvSx] : 1.f, iw = PAIR ? p.sc[kInvSw] : 1.f;
   // E goes out in whole rows of the wavefront's 64 columns, 32 rows at a time
   // through LDS of its own (straight from the lanes' four columns it left in
   // 32-byte pieces and took 20 us a round of tiles more).
@@ -340,7 +382,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_logits(XentTile p, int
 #pragma unroll
   for (int i = 0; i < Tile::HA; ++i) {
     float ex[Tile::HB * 4];
-    xent_row<PAIR, Tile::HB>(p, row0 + i * 16, col0, g, acc[i], bias, is, iw, ys[i], ex);
+    xent_row<PAIR, Tile::HB>(p, row0 + i * 16, col0, g, acc[i], bias, xent_shift<PAIR>(p, row0 + i * 16), ys[i], ex);
     if constexpr (KEEP > 0) {
       uint8_t* const wr = lds + (i % 2 * 16 + r) * PITCH + 4 * g * (KEEP == 2 ? 4 : 2);
 #pragma unroll
@@ -468,7 +510,6 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_xent_logits_few(XentTile p) {
 #pragma unroll
   for (int i = 0; i < TILES; ++i) *at(wave * TILES + i) = acc[i / HB][i % HB];
   __syncthreads();
-  const float is = PAIR ? p.sc[kInvSx] : 1.f, iw = PAIR ? p.sc[kInvSw] : 1.f;
   for (int i = wave; i < MT; i += WAVES) {
     if (i * 16 >= p.t) break;
     v4f v[HB], bias[HB];
@@ -481,7 +522,7 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_xent_logits_few(XentTile p) {
     xent_bias<HB>(p, col0, g, bias);
     const int64_t row = i * 16 + r;
     float ex[HB * 4];
-    xent_row<PAIR, HB>(p, row, col0, g, v, bias, is, iw, row < p.t ? p.targets[row] : -1, ex);
+    xent_row<PAIR, HB>(p, row, col0, g, v, bias, xent_shift<PAIR>(p, row), row < p.t ? p.targets[row] : -1, ex);
     if (row >= p.t) continue;
     if constexpr (KEEP == 1) {
       uint16_t* e = static_cast<uint16_t*>(p.e) + row * p.vp + col0 + 4 * g;
@@ -570,7 +611,7 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
     const int64_t row = t0 + i, at = row * p.vp + c, y = p.targets[row];
-    const bool off = ignored(y, p.ignore) || y >= p.v;
+    const bool off = ignored(y, p.ignore) || y >= p.v || (p.weights && p.weights[row] == 0.f);
     float v[8];
     if constexpr (DT == kF32) {
       __builtin_memcpy(v, static_cast<const float*>(p.e) + at, sizeof v);
@@ -878,6 +919,7 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   };
   l.scalars = take(kScalars * sizeof(float));
   l.partmax = take(f32 ? 2 * kMaxGroups * sizeof(float) : 0);
+  l.xrow = take(f32 ? (size_t)a.t * sizeof(int) : 0);
   l.rows = take(train && a.weights ? (size_t)a.t * sizeof(float) : 0);
   // x as the logits' operand, then (training) with ignored tokens' rows zero
   l.x = take((size_t)((l.pack_x ? 1 : 0) + (train ? 1 : 0)) * l.parts * a.t * l.dp * 2);
@@ -981,7 +1023,7 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
                  : MmaSide{static_cast<const uint16_t*>(a.x) + t0 * a.ldx, a.ldx, n};
   p.w = l.pack_w ? MmaSide{reinterpret_cast<uint16_t*>(ws + l.w), pitch, a.v}
                  : MmaSide{static_cast<const uint16_t*>(a.w), a.ldw, a.v};
-  p.t = n, p.v = a.v, p.d = a.d, p.sc = sc, p.bias = a.bias, p.bias_dtype = a.dtype;
+  p.t = n, p.v = a.v, p.d = a.d, p.sc = sc, p.exponents = reinterpret_cast<const int*>(ws + l.xrow) + t0, p.bias = a.bias, p.bias_dtype = a.dtype;
   p.targets = a.targets + t0, p.stats = stats, p.nseg = l.nseg, p.target = target, p.e = ws + l.e, p.vp = l.vp;
   if (train)
     logits<DT, PAIR, KEEP>(p, a.t, s);
@@ -1050,6 +1092,7 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   float* const sc = reinterpret_cast<float*>(ws + l.scalars);
   float* const partmax = reinterpret_cast<float*>(ws + l.partmax);
+  int* const xrow = reinterpret_cast<int*>(ws + l.xrow);
   const bool f32 = a.dtype == kF32;
   if (a.t == 0) {
     if (train && !a.accumulate) {
@@ -1060,16 +1103,16 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
     }
     return hipGetLastError();
   }
-  if (f32) hipLaunchKernelGGL(k_xent_max, dim3(2 * kMaxGroups), dim3(256), 0, s, a, partmax);
+  if (f32) hipLaunchKernelGGL(k_xent_max, dim3(2 * kMaxGroups), dim3(256), 0, s, a, train, partmax, xrow);
   if (f32 || (train && a.weights))
     hipLaunchKernelGGL(k_xent_prep, dim3(1), dim3(256), 0, s, a, train, f32, partmax, sc);
   XentPack w{}, x{};
-  if (l.pack_w) w = XentPack{a.w, a.ldw, a.v, a.d, l.dp, sc + kSw, reinterpret_cast<uint16_t*>(ws + l.w)};
+  if (l.pack_w) w = XentPack{a.w, a.ldw, a.v, a.d, l.dp, sc + kSw, nullptr, reinterpret_cast<uint16_t*>(ws + l.w)};
   if (l.pack_x || train) {
     uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
-    x = XentPack{a.x,       a.ldx,    a.t,       a.d, l.dp, sc + kSx, l.pack_x ? px : nullptr,
+    x = XentPack{a.x,       a.ldx,    a.t,       a.d, l.dp, sc + kSx, xrow, l.pack_x ? px : nullptr,
                  train ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr,
-                 a.targets, a.ignore, a.weights, sc,  reinterpret_cast<float*>(ws + l.rows)};
+                 a.targets, a.ignore, a.v, a.weights, sc, reinterpret_cast<float*>(ws + l.rows)};
   }
   pack(w, x, a.dtype, s);
   for (int64_t t0 = 0; t0 < a.t; t0 += l.block) {

@@ -97,3 +97,44 @@ def test_every_word_at_the_lowest_value(t, dtype):
     n = torch.bincount(y, minlength=v).double()
     e = {F32: 2.0 ** -18, BF16: 2.0 ** -10}[dtype]
     close("dbias", db, t / v - n, t / v * e + n * 2.0 ** -18, dtype)
+
+
+@pytest.mark.parametrize("size", [1e9, 1e12, 3e38])
+@pytest.mark.parametrize("t", [12, 140])
+def test_large_values_in_ignored_rows(t, size):
+    """fp32 padding of any finite size: bounds of the other rows alone."""
+    v, d = 200, 40
+    x, w, y, b = inputs(t, v, d, F32, True, seed=43, ignored=0.0)
+    gone = torch.arange(t, device=DEV) % 3 == 0
+    x[gone] = size
+    x[gone, ::2] *= -1
+    y[gone] = -100
+    pad = gone.clone()
+    y[1] = v + 5  # (past the vocabulary: no part of the gradients either)
+    x[1] = size
+    gone[1] = True
+    say(f"[xent] padding of {size} beside {t} tokens")
+    loss, lse, dx, dw, db = T.cross_entropy_train(x, w, y, b, reduction="sum", scale=0.25)
+    ref = Reference(x[~gone], w, y[~gone], b, scale=0.25)
+    check(ref, loss[~gone], lse[~gone], dx[~gone], dw, db)
+    assert not loss[pad].any() and torch.isnan(loss[1]) and not dx[gone].any()
+    again = T.cross_entropy(x, w, y, b)
+    assert torch.equal(again[0][~gone], loss[~gone]) and torch.equal(again[1][~gone], lse[~gone])
+    # a weight of zero takes a row out just so
+    y[gone] = 3
+    u = torch.where(gone, 0.0, 1.0)
+    dx, dw = T.cross_entropy_train(x, w, y, b, reduction="sum", scale=0.25, weights=u)[2:4]
+    close("dw", dw, ref.dw, ref.tol_dw, F32)
+    close("dx", dx[~gone], ref.dx, ref.tol_dx, F32)
+
+
+@pytest.mark.parametrize("t", [12, 140])
+def test_one_token_far_larger_than_the_others(t):
+    """Loss, lse and dx of a token go by its own row."""
+    v, d = 200, 40
+    x, w, y, b = inputs(t, v, d, F32, True, seed=44, ignored=0.0)
+    x[5] *= 1e12
+    rest = torch.arange(t, device=DEV) != 5
+    loss, lse, dx, _, _ = T.cross_entropy_train(x, w, y, b, reduction="sum")
+    check(Reference(x[rest], w, y[rest], b), loss[rest], lse[rest], dx[rest])
+    check(Reference(x[5:6], w, y[5:6], b), loss[5:6], lse[5:6])
