@@ -659,14 +659,20 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
   }
 }
 
-// db = (add +) alpha * the partial sums in order.
+// db = (add +) alpha * the partial sums in order.  Blocks of tokens before the last
+// add up in `sum`, fp32: one rounding to db's type, and no partial sum in it.
 __global__ __launch_bounds__(256) void k_xent_db(const float* part, int64_t rows, int64_t vp, int64_t v, const float* sc,
-                                                 void* db, int dtype, bool add) {
+                                                 float* sum, bool first, bool last, void* db, int dtype, bool add) {
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= v) return;
   float s = 0.f;
 #pragma unroll 8
   for (int64_t i = 0; i < rows; ++i) s += part[i * vp + c];
+  if (!first) s += sum[c];
+  if (!last) {
+    sum[c] = s;
+    return;
+  }
   s *= sc[kAlphaB];
   if (add) s += load_any(db, dtype, c);
   store_any(db, dtype, c, s);
@@ -931,6 +937,7 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
     l.e = take((size_t)l.block * l.vp * (f32 ? 4 : 2));
     l.g = f32 ? take((size_t)l.block * l.vp * 4) : l.e;
     l.db = take(a.dbias ? (size_t)cdiv(l.block, grad_rows(l.block, l.vp)) * l.vp * sizeof(float) : 0);
+    l.dbs = take(a.dbias && l.block < a.t ? (size_t)a.v * sizeof(float) : 0);
     l.dxp = take(a.dx && l.dx_splits > 1 ? (size_t)l.dx_splits * l.block * a.d * sizeof(float) : 0);
     l.dwp = take(a.dw && a.dw_dtype != kF32 && l.block < a.t ? (size_t)a.v * a.d * sizeof(float) : 0);
   }
@@ -1046,8 +1053,8 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   hipLaunchKernelGGL((k_xent_grad<PAIR ? kF32 : DT>), dim3((unsigned)parts, (unsigned)cdiv(l.vp, 2048)), dim3(256),
                      0, s, q);
   if (a.dbias)
-    hipLaunchKernelGGL(k_xent_db, dim3(grid(a.v)), dim3(256), 0, s, db, parts, l.vp, a.v, sc, a.dbias, a.dtype,
-                       a.accumulate || t0 > 0);
+    hipLaunchKernelGGL(k_xent_db, dim3(grid(a.v)), dim3(256), 0, s, db, parts, l.vp, a.v, sc,
+                       reinterpret_cast<float*>(ws + l.dbs), t0 == 0, t0 + n == a.t, a.dbias, a.dtype, a.accumulate);
   if (a.dx) {
     XentProduct d{};
     d.a = MmaSide{g, PIECES * l.vp, n};

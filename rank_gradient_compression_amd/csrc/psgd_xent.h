@@ -43,7 +43,7 @@ struct XentLayout {
   int seg_shift;             // columns that share a maximum: 32 (few tokens) or 64
   int64_t nseg;
   int64_t dx_splits;         // pieces of the vocabulary that dx is summed in
-  size_t scalars, partmax, xrow, rows, x, w, stats, target, sums, e, g, db, dxp, dwp, bytes;
+  size_t scalars, partmax, xrow, rows, x, w, stats, target, sums, e, g, db, dbs, dxp, dwp, bytes;
 };
 XentLayout xent_layout(const XentArgs& a, bool train);
 hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void* ws, hipStream_t s);

@@ -138,3 +138,54 @@ def test_one_token_far_larger_than_the_others(t):
     loss, lse, dx, _, _ = T.cross_entropy_train(x, w, y, b, reduction="sum")
     check(Reference(x[rest], w, y[rest], b), loss[rest], lse[rest], dx[rest])
     check(Reference(x[5:6], w, y[5:6], b), loss[5:6], lse[5:6])
+
+
+def half_step(want, dtype):
+    """Half of the distance between the type's numbers around a value."""
+    bits = {BF16: 8, F16: 11, F32: 24}[dtype]
+    return torch.exp2(torch.floor(torch.log2(want.abs().clamp(min=1e-30))) - bits)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_bias_gradient_of_many_blocks(dtype):
+    """Eight blocks of 4096 tokens: dbias is rounded once, at the end (what comes
+    before: E's 2^-11 of every probability, sums of 32768 in fp32)."""
+    t, v, d = 8 * 4096, 1 << 17, 8
+    g = torch.Generator(device=DEV)
+    g.manual_seed(45)
+    x = torch.randn(t, d, generator=g, device=DEV).to(dtype)
+    w = torch.randn(v, d, generator=g, device=DEV).to(dtype) * 0.5
+    b = torch.randn(v, generator=g, device=DEV).to(dtype)
+    y = torch.randint(0, 64, (t,), generator=g, device=DEV)
+    scale = 1024.0 if dtype == BF16 else 64.0  # (512 hits of a target, times 1024, are no fp16 number)
+    old = (torch.randn(v, generator=g, device=DEV) * 300).to(dtype)
+    say(f"[xent] eight blocks {dtype}")
+    _, lse, _, _, db = T.cross_entropy_train(x, w, y, b, reduction="sum", scale=scale, need_dx=False, need_dw=False)
+    more = old.clone()
+    T.cross_entropy_train(x, w, y, b, reduction="sum", scale=scale, need_dx=False, need_dw=False, dbias=more, accumulate=True)
+    total = torch.zeros(v, dtype=torch.float64, device=DEV)
+    for a in range(0, t, 1024):
+        l = x[a:a + 1024].double() @ w.double().t() + b.double()
+        total += torch.softmax(l, 1).sum(0)
+    hits = torch.bincount(y, minlength=v).double()
+    want = scale * (total - hits)
+    # (logits of at most 30, in error by 20 u of the sizes that add up to them)
+    tol = scale * (total * (2.0 ** -11 + 2.0 ** -16) + hits * 2.0 ** -16 + 2.0 ** -24)
+    got = db.double()
+    assert ((got - want).abs() <= tol + half_step(want, dtype) * 1.0001).all()
+    want = want + old.double()
+    assert ((more.double() - want).abs() <= tol + half_step(want, dtype) * 1.0001).all()
+
+
+def test_bias_gradient_whose_blocks_cancel():
+    """fp16: a partial sum beyond the type's range whose total is within it."""
+    t, v, d = 4096, 1 << 17, 8
+    x = torch.zeros(2 * t, d, dtype=F16, device=DEV)
+    w = torch.zeros(v, d, dtype=F16, device=DEV)
+    b = torch.zeros(v, dtype=F16, device=DEV)
+    b[7] = 12.0
+    y = torch.full((2 * t,), 9, device=DEV)
+    u = torch.ones(2 * t, device=DEV) * 64.0
+    u[t:] *= -1
+    db = T.cross_entropy_train(x, w, y, b, weights=u, reduction="sum", need_dx=False, need_dw=False)[4]
+    assert not db.any()
