@@ -42,7 +42,10 @@
 namespace psgd {
 
 // scalars that the device works out for itself
-enum { kSx, kSw, kEw, kGs, kAlphaX, kAlphaW, kAlphaB, kScalars };  // (kEw: kSw's exponent)
+// (kE*: exponents.  A product's factor, scale over the operands' powers of two, may be
+// no fp32 number where the result is one: it is kept as kS times 2 to kEdx, kEdw or
+// kEdb.)
+enum { kSx, kSw, kEw, kEg, kS, kEdx, kEdw, kEdb, kScalars };
 
 constexpr int kMaxGroups = 1024;    // workgroups that look for a tensor's largest value
 constexpr int64_t kBlockBytes = int64_t(1) << 30;  // of E (and G) at a time
@@ -151,7 +154,8 @@ __global__ __launch_bounds__(256) void k_xent_max(XentArgs a, bool train, float*
 }
 
 // Exponent of a token's weight; `most` (the largest weight's, the smallest
-// exponent) for one that has none.
+// exponent) for one that has none.  The two may be 240 apart, so a power of two
+// between them is no fp32 number: what goes by both takes the difference.
 __device__ __forceinline__ int weight_exponent(float u, int most) {
   u = fabsf(u);
   return u > 0.f && u < __builtin_inff() ? max(fit_exponent(u), most) : most;
@@ -190,10 +194,12 @@ __device__ void xent_scalars(const XentArgs& a, bool train, bool split, const fl
   sc[kSx] = ldexpf(1.f, ex);
   sc[kSw] = ldexpf(1.f, ew);
   sc[kEw] = (float)ew;
-  sc[kGs] = ldexpf(1.f, eg);
-  sc[kAlphaX] = (float)ldexp(s, -eg - ew);
-  sc[kAlphaW] = (float)ldexp(s, -eg - ex);
-  sc[kAlphaB] = (float)ldexp(s, -eg);
+  int es;
+  sc[kS] = (float)frexp(s, &es);
+  sc[kEg] = (float)eg;
+  sc[kEdx] = (float)(es - eg - ew);
+  sc[kEdw] = (float)(es - eg - ex);
+  sc[kEdb] = (float)(es - eg);
 }
 
 __global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool split, const float* partmax, float* sc) {
@@ -206,7 +212,7 @@ __global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool 
 // one that dw's product takes, under one power of two, with rows of tokens that do
 // not count zero (their G is zero, and zero times what such a row may hold need not
 // be) and the others times their
-// weight's power of two, which goes to `factors` as well.  Bound by HBM: 33278 x
+// weight's power of two, whose exponent goes to `factors` as well.  Bound by HBM: 33278 x
 // 650 fp16 18 us, 92 MB read and written, 5.1 TB/s; fp32 31 us, 176 MB, 5.7 TB/s.
 struct XentPack {
   const void* x;
@@ -218,7 +224,7 @@ struct XentPack {
   int64_t ignore, v;
   const float* weights;
   const float* sc;
-  float* factors;
+  int* factors;
 };
 template <int DT>
 __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsigned first) {
@@ -267,11 +273,9 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsig
   if (!p.clean) return;
   float f = 1.f;
   if (p.weights) {
-    int top;
-    (void)frexpf(p.sc[kGs], &top);
-    const int most = top - 1;
-    f = ldexpf(1.f, most - weight_exponent(p.weights[row], most));
-    if (c == 0) p.factors[row] = f;
+    const int most = (int)p.sc[kEg], less = most - weight_exponent(p.weights[row], most);
+    f = ldexpf(1.f, less);  // (0 where that is no fp32 number: the row vanishes beside the largest weight's)
+    if (c == 0) p.factors[row] = less;
     if (p.weights[row] == 0.f) f = 0.f;
   }
   const int64_t y = p.targets[row];
@@ -586,7 +590,8 @@ struct XentGrad {
   int64_t t, v, vp, nseg;
   int seg_shift, rows;  // rows: tokens of a workgroup
   const float2 *stats, *sums;
-  const float *loss, *weights, *factors, *sc;
+  const float *loss, *weights, *sc;
+  const int* factors;  // exponents
   const int64_t* targets;
   int64_t ignore;
   void* e;       // fp16 (G in its place) or fp32
@@ -602,7 +607,8 @@ template <int DT>  // of G: kF16 and kBF16 in E's place, kF32 as two pieces
 __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
   const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8, t0 = (int64_t)blockIdx.x * p.rows;
   if (c >= p.vp) return;
-  const float gs = p.sc[kGs];
+  const int most = (int)p.sc[kEg];
+  const float gs = ldexpf(1.f, most);
   const int64_t seg = min(c >> p.seg_shift, p.nseg - 1);
   const int n = (int)min((int64_t)p.rows, p.t - t0);
   float sums[8];
@@ -621,8 +627,9 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = Elem<kF16>::up(h[e]);
     }
-    // (a row's own power of two: the largest weight's over the row's factor)
-    const float back = p.weights ? p.factors[row] : 1.f, u = p.weights ? p.weights[row] * (gs / back) : gs;
+    // (a row's own power of two: the largest weight's less the row's exponent)
+    const int less = p.weights ? p.factors[row] : 0;
+    const float back = ldexpf(1.f, less), u = p.weights ? ldexpf(p.weights[row], most - less) : gs;
     const float2 sum = p.sums[row];
     const float f = u * (__builtin_amdgcn_exp2f((p.stats[row * p.nseg + seg].x - sum.x) * kLog2e) * sum.y);
 #pragma unroll
@@ -659,7 +666,7 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
   }
 }
 
-// db = (add +) alpha * the partial sums in order.  Blocks of tokens before the last
+// db = (add +) the scale times the partial sums in order.  Blocks of tokens before the last
 // add up in `sum`, fp32: one rounding to db's type, and no partial sum in it.
 __global__ __launch_bounds__(256) void k_xent_db(const float* part, int64_t rows, int64_t vp, int64_t v, const float* sc,
                                                  float* sum, bool first, bool last, void* db, int dtype, bool add) {
@@ -673,7 +680,7 @@ __global__ __launch_bounds__(256) void k_xent_db(const float* part, int64_t rows
     sum[c] = s;
     return;
   }
-  s *= sc[kAlphaB];
+  s = ldexpf(s * sc[kS], (int)sc[kEdb]);
   if (add) s += load_any(db, dtype, c);
   store_any(db, dtype, c, s);
 }
@@ -681,7 +688,8 @@ __global__ __launch_bounds__(256) void k_xent_db(const float* part, int64_t rows
 struct XentProduct {
   MmaSide a, b;
   int64_t k;
-  const float* alpha;  // or null: 1
+  const float* sc;  // the scalars, or null: the sums as they are
+  int exponent;     // which of them the result is 2 to the power of
   MmaOut out;
   int64_t split_stride;  // elements between the results of two pieces of the summed axis
   int pieces;            // of them
@@ -717,7 +725,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p,
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* lds = mma_epilogue_lds<Tile>(wave, a0, b0, a1, b1);
   p.out.c = static_cast<typename Elem<ODT>::type*>(p.out.c) + piece * p.split_stride;
-  mma_store<ODT>(p.out, p.alpha ? *p.alpha : 1.f, lds, m0 + wave / WN * TM * 32, n0 + wave % WN * TN * 32, acc);
+  mma_store<ODT>(p.out, p.sc ? p.sc[kS] : 1.f, p.sc ? (int)p.sc[p.exponent] : 0, lds, m0 + wave / WN * TM * 32, n0 + wave % WN * TN * 32, acc);
 }
 
 // Four neighbouring values of each of a lane's eight rows of an operand of at most
@@ -759,7 +767,8 @@ __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
   uint4 a[N][4], b[N][4];
 #pragma unroll
   for (int n = 0; n < N; ++n) outer_read<PAIR>(p.a, p.k, m0, n, a[n]), outer_read<PAIR>(p.b, p.k, n0, n, b[n]);
-  const float alpha = *p.alpha;
+  const float alpha = p.sc[kS];
+  const int exponent = (int)p.sc[p.exponent];
   v4f acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -781,11 +790,12 @@ __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           *reinterpret_cast<v4f*>(wr + i * 68 + 4 * e) =
-              v4f{acc[i][0][e] * alpha, acc[i][1][e] * alpha, acc[i][2][e] * alpha, acc[i][3][e] * alpha};
+              v4f{mma_scaled(acc[i][0][e], alpha, exponent), mma_scaled(acc[i][1][e], alpha, exponent),
+                  mma_scaled(acc[i][2][e], alpha, exponent), mma_scaled(acc[i][3][e], alpha, exponent)};
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    mma_store_any<ODT, 64>(p.out, lds[wave], m0 + h * 32, n0);
+    mma_store_any<ODT, 64>(p.out, 0, lds[wave], m0 + h * 32, n0);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
@@ -806,7 +816,8 @@ __global__ __launch_bounds__(kOuterThreads) void k_xent_outer_rows(XentProduct p
   const int64_t m0 = (int64_t)xcd_position(blockIdx.x, gridDim.x) * 32;
   const int n = (int)p.out.n;
   constexpr int N = PAIR ? 2 : 1;
-  const float alpha = *p.alpha;
+  const float alpha = p.sc[kS];
+  const int exponent = (int)p.sc[p.exponent];
   uint4 a[N][2];
 #pragma unroll
   for (int h = 0; h < N; ++h) {
@@ -846,7 +857,8 @@ __global__ __launch_bounds__(kOuterThreads) void k_xent_outer_rows(XentProduct p
 #pragma unroll
       for (int e = 0; e < 8; ++e) {  // columns 16 g + 2 e and the next
         const int col = n0 + 16 * g + 2 * e;
-        const float u = acc[e % 2 * 2][e / 2] * alpha, v = acc[e % 2 * 2 + 1][e / 2] * alpha;
+        const float u = mma_scaled(acc[e % 2 * 2][e / 2], alpha, exponent);
+        const float v = mma_scaled(acc[e % 2 * 2 + 1][e / 2], alpha, exponent);
         if constexpr (sizeof(T) == 2) {
           if (n % 2 == 0) {
             const uint32_t both = (uint32_t)Elem<ODT>::down(u) | (uint32_t)Elem<ODT>::down(v) << 16;
@@ -867,16 +879,16 @@ __global__ __launch_bounds__(kOuterThreads) void k_xent_outer_rows(XentProduct p
   for (int i = whole * (16 / (int)sizeof(T)) + threadIdx.x; i < values; i += kOuterThreads) out[i] = lds[i];
 }
 
-// dx = alpha * the pieces' sums in order.
+// dx = the scale times the pieces' sums in order.
 __global__ __launch_bounds__(256) void k_xent_dx(const float* part, int64_t pieces, int64_t t, int64_t d,
-                                                 const float* alpha, const float* factors, void* dx, int dtype,
+                                                 const float* sc, const int* factors, void* dx, int dtype,
                                                  int64_t lddx) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= t * d) return;
   float s = 0.f;
 #pragma unroll 8
   for (int64_t k = 0; k < pieces; ++k) s += part[k * t * d + i];
-  store_any(dx, dtype, i / d * lddx + i % d, s * *alpha * (factors ? factors[i / d] : 1.f));
+  store_any(dx, dtype, i / d * lddx + i % d, mma_scaled(s, sc[kS], (int)sc[kEdx] + (factors ? factors[i / d] : 0)));
 }
 
 // Gradients of a loss over no word or no token.
@@ -926,7 +938,7 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   l.scalars = take(kScalars * sizeof(float));
   l.partmax = take(f32 ? 2 * kMaxGroups * sizeof(float) : 0);
   l.xrow = take(f32 ? (size_t)a.t * sizeof(int) : 0);
-  l.rows = take(train && a.weights ? (size_t)a.t * sizeof(float) : 0);
+  l.rows = take(train && a.weights ? (size_t)a.t * sizeof(int) : 0);
   // x as the logits' operand, then (training) with ignored tokens' rows zero
   l.x = take((size_t)((l.pack_x ? 1 : 0) + (train ? 1 : 0)) * l.parts * a.t * l.dp * 2);
   l.w = take(l.pack_w ? (size_t)l.parts * a.v * l.dp * 2 : 0);
@@ -1046,9 +1058,9 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   float* const db = reinterpret_cast<float*>(ws + l.db);
   const int rows = (int)grad_rows(l.block, l.vp);
   const int64_t parts = cdiv(n, rows);
-  const float* const factors = a.weights ? reinterpret_cast<float*>(ws + l.rows) + t0 : nullptr;
+  const int* const factors = a.weights ? reinterpret_cast<int*>(ws + l.rows) + t0 : nullptr;
   const XentGrad q{n,       a.v, l.vp,           l.nseg,   l.seg_shift, rows, stats, sums, a.loss + t0,
-                   a.weights ? a.weights + t0 : nullptr, factors, sc, a.targets + t0, a.ignore, ws + l.e, g,
+                   a.weights ? a.weights + t0 : nullptr, sc, factors, a.targets + t0, a.ignore, ws + l.e, g,
                    a.dbias ? db : nullptr};
   hipLaunchKernelGGL((k_xent_grad<PAIR ? kF32 : DT>), dim3((unsigned)parts, (unsigned)cdiv(l.vp, 2048)), dim3(256),
                      0, s, q);
@@ -1068,10 +1080,10 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
       d.out = MmaOut{part, a.d, n, a.d, nullptr, false, nullptr};
       d.split_stride = n * a.d;
       product<DT, PAIR, true>(d, kF32, l.dx_splits, s);
-      hipLaunchKernelGGL(k_xent_dx, dim3(grid(n * a.d)), dim3(256), 0, s, part, l.dx_splits, n, a.d, sc + kAlphaX,
+      hipLaunchKernelGGL(k_xent_dx, dim3(grid(n * a.d)), dim3(256), 0, s, part, l.dx_splits, n, a.d, sc,
                          factors, dx, a.dtype, a.lddx);
     } else {
-      d.alpha = sc + kAlphaX;
+      d.sc = sc, d.exponent = kEdx;
       d.out = MmaOut{dx, a.lddx, n, a.d, nullptr, false, factors};
       product<DT, PAIR, true>(d, a.dtype, 1, s);
     }
@@ -1080,7 +1092,7 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
     XentProduct d{};
     d.a = MmaSide{g, PIECES * l.vp, a.v};
     d.b = MmaSide{px + (l.pack_x ? a.t * pitch : 0) + t0 * pitch, pitch, a.d};
-    d.k = n, d.alpha = sc + kAlphaW;
+    d.k = n, d.sc = sc, d.exponent = kEdw;
     // Blocks before the last add up in fp32: in dw itself, or in memory of
     // their own where dw has fewer bits.
     const bool last = t0 + n == a.t, wide = a.dw_dtype == kF32;
@@ -1119,7 +1131,7 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
     uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
     x = XentPack{a.x,       a.ldx,    a.t,       a.d, l.dp, sc + kSx, xrow, l.pack_x ? px : nullptr,
                  train ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr,
-                 a.targets, a.ignore, a.v, a.weights, sc, reinterpret_cast<float*>(ws + l.rows)};
+                 a.targets, a.ignore, a.v, a.weights, sc, reinterpret_cast<int*>(ws + l.rows)};
   }
   pack(w, x, a.dtype, s);
   for (int64_t t0 = 0; t0 < a.t; t0 += l.block) {

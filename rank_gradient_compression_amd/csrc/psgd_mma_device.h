@@ -317,8 +317,8 @@ struct MmaTile {
   }
 };
 
-// Accumulators to memory: C = alpha * (row factor) * sum (+ add) (+ C).  Each wavefront passes
-// 32 rows at a time through LDS of its own and stores 16 bytes per lane, whole
+// Accumulators to memory: C = alpha * 2^(exponent + the row's) * sum (+ add) (+ C).
+// Each wavefront passes 32 rows at a time through LDS of its own and stores 16 bytes per lane, whole
 // rows of its TN * 32 columns; the row pitch of 4 floats beyond a multiple of 32
 // spreads the 16 rows that a write covers over all banks.
 struct MmaOut {
@@ -326,8 +326,13 @@ struct MmaOut {
   int64_t ldc, m, n;
   const float* add;  // m x n fp32, row stride n, or null
   bool accumulate;
-  const float* row;  // m factors, or null
+  const int* row;  // m exponents, or null
 };
+
+// v times a power of two that need be no fp32 number, behind one rounding.
+__device__ __forceinline__ float mma_scaled(float v, float alpha, int exponent) {
+  return __builtin_amdgcn_ldexpf(v * alpha, exponent);
+}
 
 template <class Tile>
 __device__ __forceinline__ float* mma_epilogue_lds(int wave, uint8_t* a0, uint8_t* b0, uint8_t* a1, uint8_t* b1) {
@@ -378,7 +383,7 @@ __device__ __forceinline__ void store_run(typename Elem<DT>::type* at, const flo
 // 32 rows of C from LDS, E neighbouring values a lane: as many as the address and
 // the row stride allow to be one access, so that lanes write without gaps.
 template <int DT, int E, int COLS>
-__device__ __forceinline__ void mma_store_rows(const MmaOut& p, const float* lds, int64_t row0, int64_t col0) {
+__device__ __forceinline__ void mma_store_rows(const MmaOut& p, int exponent, const float* lds, int64_t row0, int64_t col0) {
   using T = typename Elem<DT>::type;
   constexpr int PITCH = COLS + 4, LPR = COLS / E, RPI = 64 / LPR;
   const int lane = threadIdx.x & 63, c = lane % LPR * E;
@@ -390,9 +395,9 @@ __device__ __forceinline__ void mma_store_rows(const MmaOut& p, const float* lds
     if (row >= p.m || n <= 0) continue;
     float v[E], w[E];
     __builtin_memcpy(v, __builtin_assume_aligned(lds + in * PITCH + c, E >= 4 ? 16 : 4 * E), sizeof v);
-    const float f = p.row ? p.row[row] : 1.f;
+    const int x = exponent + (p.row ? p.row[row] : 0);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= f;
+    for (int e = 0; e < E; ++e) v[e] = __builtin_amdgcn_ldexpf(v[e], x);
     if (p.add) {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] += e < n ? p.add[row * p.n + col0 + c + e] : 0.f;
@@ -414,20 +419,21 @@ __device__ __forceinline__ void mma_store_rows(const MmaOut& p, const float* lds
   }
 }
 
+// (exponent: of what is in LDS, which may be taken times it here or before)
 template <int DT, int COLS>
-__device__ __forceinline__ void mma_store_any(const MmaOut& p, const float* lds, int64_t row0, int64_t col0) {
+__device__ __forceinline__ void mma_store_any(const MmaOut& p, int exponent, const float* lds, int64_t row0, int64_t col0) {
   using T = typename Elem<DT>::type;
   const uintptr_t step = (uintptr_t)(static_cast<T*>(p.c) + row0 * p.ldc + col0) | (uintptr_t)(p.ldc * (int64_t)sizeof(T));
   if ((step & 15) == 0)
-    mma_store_rows<DT, 16 / (int)sizeof(T), COLS>(p, lds, row0, col0);
+    mma_store_rows<DT, 16 / (int)sizeof(T), COLS>(p, exponent, lds, row0, col0);
   else if ((step & (2 * sizeof(T) - 1)) == 0)
-    mma_store_rows<DT, 2, COLS>(p, lds, row0, col0);
+    mma_store_rows<DT, 2, COLS>(p, exponent, lds, row0, col0);
   else
-    mma_store_rows<DT, 1, COLS>(p, lds, row0, col0);
+    mma_store_rows<DT, 1, COLS>(p, exponent, lds, row0, col0);
 }
 
 template <int DT, int HA, int HB>
-__device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* lds, int64_t row0, int64_t col0,
+__device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, int exponent, float* lds, int64_t row0, int64_t col0,
                                           const v4f (&acc)[HA][HB]) {
   using T = typename Elem<DT>::type;
   const int lane = threadIdx.x & 63;
@@ -459,11 +465,11 @@ __device__ __forceinline__ void mma_store(const MmaOut& p, float alpha, float* l
         __builtin_memcpy(v, __builtin_assume_aligned(lds + row * PITCH + lane % LPR * E, 16), sizeof v);
         T o[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = Elem<DT>::down(v[e]);
+        for (int e = 0; e < E; ++e) o[e] = Elem<DT>::down(__builtin_amdgcn_ldexpf(v[e], exponent));
         __builtin_memcpy(__builtin_assume_aligned(base + (i * 32 + row) * p.ldc + lane % LPR * E, 16), o, sizeof o);
       }
     } else {
-      mma_store_any<DT, COLS>(p, lds, row0 + i * 32, col0);
+      mma_store_any<DT, COLS>(p, exponent, lds, row0 + i * 32, col0);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();

@@ -189,3 +189,38 @@ def test_bias_gradient_whose_blocks_cancel():
     u[t:] *= -1
     db = T.cross_entropy_train(x, w, y, b, weights=u, reduction="sum", need_dx=False, need_dw=False)[4]
     assert not db.any()
+
+
+@pytest.mark.parametrize("dtype,scale", [(BF16, 1.0), (F32, 1.0), (F16, 1e-28)])
+@pytest.mark.parametrize("t", [12, 70])
+def test_weights_very_far_apart(t, dtype, scale):
+    """The smallest weight 2^-200 of the largest."""
+    v, d = 150, 24
+    x, w, y, b = inputs(t, v, d, dtype, True, seed=46, ignored=0.2)
+    u = torch.ones(t, device=DEV)
+    u[0::4], u[1::4], u[2::4] = 1e30, -1e-30, 1e-5
+    say(f"[xent] weights far apart {t} {dtype}")
+    loss, lse, dx, dw, db = T.cross_entropy_train(x, w, y, b, weights=u, reduction="sum", scale=scale,
+                                                  dw=torch.zeros(v, d, device=DEV))
+    check(Reference(x, w, y, b, u, scale), loss, lse, dx, dw, db)
+
+
+def test_factors_beyond_fp32():
+    """The powers of two of G and w together are no fp32 number, dx is one.  (G: 2^-25 of
+    a third; w: 2^-39 of 2^-16 of its largest; p 4.5e-5 to 2^-18: 2^-16 in all.)"""
+    t, v, d = 40, 64, 16
+    x = torch.zeros(t, d, device=DEV)
+    x[:, 0] = 2.0 ** -60
+    w = torch.zeros(v, d, device=DEV)
+    w[:, 0], w[5, 1] = 2.0 ** 60, 2.0 ** 44
+    b = torch.full((v,), -10.0, device=DEV)
+    b[3] = 0.0
+    y = torch.full((t,), 3, device=DEV)
+    u = torch.full((t,), 2.0 ** 97, device=DEV)
+    dx, dw = T.cross_entropy_train(x, w, y, b, weights=u, reduction="sum")[2:4]
+    p = float(np.exp(-10.0) / (1 + 63 * np.exp(-10.0)))
+    want = torch.full((t,), 2.0 ** (97 + 44) * p, dtype=torch.float64, device=DEV)
+    close("dx", dx[:, 1], want, want * 2.0 ** -16)
+    assert not dx[:, 2:].any()
+    want = torch.full((60,), t * 2.0 ** (97 - 60) * p, dtype=torch.float64, device=DEV)
+    close("dw", dw[4:, 0], want, want * 2.0 ** -16)
