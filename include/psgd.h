@@ -605,16 +605,18 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
  *
  * Precision: products are summed in fp32.  16-bit tensors: probabilities and G
  * have one rounding each to 16 bits (fp16, then `dtype`) before the gradients'
- * products (a row of G times a power of two that brings its token's weight to
- * the type's upper range, so that small weights keep their digits in dx; in dw
- * G's values below about 2^-24 of the largest weight vanish with fp16).  fp32
- * tensors are taken as sums of two fp16 values under a power of two: 22 bits of
- * a value down to 2^-16 of the largest under the same power, and an error of
- * 2^-39 of that largest below.  In the logits every row of x has a power of its
- * own, so that loss, lse and dx of a token do not depend on other tokens' values;
- * w has one, and in dw all rows of x that count (not those of ignored tokens and of
- * weight 0).  Sums run in an order that depends on the sizes alone: equal calls give
- * equal bits.
+ * products; a probability below 2^-40 of the largest of its 64 (of at most 32
+ * tokens: 32) neighbours in the vocabulary is taken for 0 there.  A row of G is held
+ * times a power of two that brings its token's weight to the type's upper range, so
+ * that small weights keep their digits in dx; in dw the token's row of x takes the
+ * power back relative to the largest weight's, and what falls below fp16's 2^-24 so
+ * vanishes with fp16.  fp32 tensors are taken as sums of two fp16 values under a
+ * power of two: 22 bits of a value down to 2^-16 of the largest under the same
+ * power, and an error of 2^-38 of that largest below.  In the logits every row of x
+ * has a power of its own, so that loss, lse and dx of a token do not depend on other
+ * tokens' values; w has one, and in dw all rows of x that count (not those of
+ * ignored tokens and of weight 0).  Sums run in an order that depends on the sizes
+ * alone: equal calls give equal bits.
  *
  * workspace: psgd_xent_workspace bytes for the same arguments (`train`: for
  * psgd_xent_train), 256-byte aligned, scratch.  It holds at most 1 GiB of

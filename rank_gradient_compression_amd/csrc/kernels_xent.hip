@@ -14,7 +14,9 @@
 // instead of keeping E would be a fourth (a third more of the time), the pass
 // over E and G is 4 bytes a value (4% of it at D = 4096: 0.11 of 2.6 ms at
 // 4096 x 32000 x 4096 bf16, the products 0.93, 0.83 and 0.89 ms).
-// E in fp16 carries a relative error of 2^-12, G is rounded once to the type
+// E is held times 2^15 in fp16: a relative error of 2^-11 down to 2^-29 of its
+// segment's largest (20 nats below), 2^-40 of that largest under it, and nothing of
+// what is below 2^-40 (28 nats; held as it is, 17).  G is rounded once to the type
 // that the products take; the target's entry, which would cancel, is formed
 // from the loss, exp(-loss) - 1, instead.  Sums, maxima and products are fp32.  A
 // row's largest logit M and its S = sum exp(l - M) are kept apart for loss =
@@ -51,6 +53,7 @@ constexpr int kMaxGroups = 1024;    // workgroups that look for a tensor's large
 constexpr int64_t kBlockBytes = int64_t(1) << 30;  // of E (and G) at a time
 constexpr int kGradRows = 16;       // tokens of a workgroup of the pass over E, at most
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kHeld = 32768.f;  // what E is held times in fp16
 
 __device__ __forceinline__ float load_any(const void* p, int dtype, int64_t i) {
   if (dtype == kF32) return static_cast<const float*>(p)[i];
@@ -346,6 +349,8 @@ __device__ __forceinline__ uint32_t two_halves(float v, float w) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{v, w}), v2h));
 }
 
+__device__ __forceinline__ uint32_t held_halves(float v, float w) { return two_halves(v * kHeld, w * kHeld); }
+
 template <int HB>
 __device__ __forceinline__ void xent_bias(const XentTile& p, int64_t col0, int g, v4f (&bias)[HB]) {
 #pragma unroll
@@ -394,8 +399,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_logits(XentTile p, int
         if constexpr (KEEP == 2)
           *reinterpret_cast<float4*>(wr + j * 64) = make_float4(ex[4 * j], ex[4 * j + 1], ex[4 * j + 2], ex[4 * j + 3]);
         else
-          *reinterpret_cast<uint2*>(wr + j * 32) = make_uint2(two_halves(ex[4 * j], ex[4 * j + 1]),
-                                                              two_halves(ex[4 * j + 2], ex[4 * j + 3]));
+          *reinterpret_cast<uint2*>(wr + j * 32) = make_uint2(held_halves(ex[4 * j], ex[4 * j + 1]),
+                                                              held_halves(ex[4 * j + 2], ex[4 * j + 3]));
       }
       if (i % 2 == 0) continue;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -533,7 +538,7 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_xent_logits_few(XentTile p) {
 #pragma unroll
       for (int j = 0; j < HB; ++j)
         *reinterpret_cast<uint2*>(e + j * 16) =
-            make_uint2(two_halves(ex[4 * j], ex[4 * j + 1]), two_halves(ex[4 * j + 2], ex[4 * j + 3]));
+            make_uint2(held_halves(ex[4 * j], ex[4 * j + 1]), held_halves(ex[4 * j + 2], ex[4 * j + 3]));
     } else if constexpr (KEEP == 2) {
       float* e = static_cast<float*>(p.e) + row * p.vp + col0 + 4 * g;
 #pragma unroll
@@ -631,7 +636,8 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
     const int less = p.weights ? p.factors[row] : 0;
     const float back = ldexpf(1.f, less), u = p.weights ? ldexpf(p.weights[row], most - less) : gs;
     const float2 sum = p.sums[row];
-    const float f = u * (__builtin_amdgcn_exp2f((p.stats[row * p.nseg + seg].x - sum.x) * kLog2e) * sum.y);
+    const float f = u * (__builtin_amdgcn_exp2f((p.stats[row * p.nseg + seg].x - sum.x) * kLog2e) * sum.y) *
+                    (DT == kF32 ? 1.f : 1.f / kHeld);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = off || c + e >= p.v ? 0.f : v[e] * f;
     if (!off && y >= c && y < c + 8) {

@@ -5,9 +5,8 @@
 // A workgroup computes a BM x BN tile of C = A B^T with WM x WN wavefronts, each
 // TM x TN tiles of 32 x 32 in accumulators, in chunks along the summed axis: 64
 // values of 16-bit matrices.  An fp32 matrix is held as two fp16 pieces, hi + lo
-// (22 bits of a value down to 2^-16 of the largest of the scale they share; fp16's
-// smallest step, 2^-39 of that largest, below), 32 upper
-// pieces followed by the same values' lower ones (a line of 128 bytes); of such
+// (22 bits of a value down to 2^-16 of the largest of the scale they share; 2^-38 of
+// that largest, half of fp16's smallest step, below), 32 upper pieces followed by the same values' lower ones (a line of 128 bytes); of such
 // matrices a chunk is 32 values, both pieces of both operands, and a product
 // hi lo + hi hi + lo hi.  (As three products one after
 // the other every piece is read one and a half times as often, and LDS reads

@@ -224,3 +224,22 @@ def test_factors_beyond_fp32():
     assert not dx[:, 2:].any()
     want = torch.full((60,), t * 2.0 ** (97 - 60) * p, dtype=torch.float64, device=DEV)
     close("dw", dw[4:, 0], want, want * 2.0 ** -16)
+
+
+@pytest.mark.parametrize("t", [4, 100])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_small_probabilities_of_16_bit_tensors(t, dtype):
+    """20 nats under a segment's largest, 2e-9: E holds it with its 11 bits, and the
+    gradient's own type is what it is rounded to (fp16: half a step of 2^-24 under a
+    row's weight at 2^13)."""
+    v, d = 64, 8
+    w = torch.zeros(v, d, dtype=dtype, device=DEV)
+    w[1:, 0] = -20.0
+    x = torch.zeros(t, d, dtype=dtype, device=DEV)
+    x[:, 0] = 1.0
+    y = torch.zeros(t, dtype=torch.int64, device=DEV)
+    dw = T.cross_entropy_train(x, w, y, reduction="sum", dw=torch.zeros(v, d, device=DEV))[3]
+    p = np.exp(-20.0) / (1 + 63 * np.exp(-20.0))
+    want = torch.full((v - 1,), t * p, dtype=torch.float64, device=DEV)
+    tol = want * (2.0 ** -11 + (2.0 ** -8 if dtype == BF16 else 0.0) + 2.0 ** -18) + (t * 2.0 ** -25 * 2.0 ** -13 if dtype == F16 else 0.0)
+    close("dw", dw[1:, 0], want, tol)
