@@ -594,7 +594,8 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
  * ignored tokens; a weight of 0 makes G zero whatever the token's row holds), or
  * NULL for ones.  s is `scale`, divided by the number of
  * tokens that are not ignored (by 1 if there is none) where `mean` is set.
- * A bias of -infinity takes a word out of the vocabulary.
+ * A bias of -infinity takes a word out of the vocabulary, whatever finite values its
+ * row of w holds as long as its products with x are finite.
  *
  * psgd_xent_forward   loss and lse, tokens floats each: scoring, evaluation.
  * psgd_xent_train     the same, and the gradients that are wanted (not NULL):

@@ -96,11 +96,17 @@ __device__ __forceinline__ bool counted(const XentArgs& a, int64_t t) {
   return !ignored(y, a.ignore) && y < a.v && !(a.weights && a.weights[t] == 0.f);
 }
 
-// Largest finite magnitude of w and of the rows of x that count, one partial maximum
-// per workgroup: the first `kMaxGroups` take x, the others w; and the exponent of
-// every row of x.  A row of x is a workgroup's where each can have one, else a
-// wavefront's; rows of w without gaps are read as one.  Bound by HBM's latency and
-// reads (33278 x 650: 24 us, 3.7 TB/s).
+// A word that a bias of minus infinity takes out (fp32).
+__device__ __forceinline__ bool word_out(const void* bias, int64_t v) {
+  return bias && static_cast<const float*>(bias)[v] == -__builtin_inff();
+}
+
+// Largest finite magnitude of the rows of w that a bias leaves in and of the rows of
+// x that count, one partial maximum per workgroup: the first `kMaxGroups` take x, the
+// others w; and the exponent of every row of x.  A row of x is a workgroup's where
+// each can have one, else a wavefront's; rows of w without gaps are read as one, with
+// the biases of the two rows that four values may lie in.  Bound by HBM's latency and
+// reads (33278 x 650: 24 us, 3.7 TB/s; 28 with a bias).
 __global__ __launch_bounds__(256) void k_xent_max(XentArgs a, bool train, float* out, int* rows_x) {
   const int b = blockIdx.x % kMaxGroups, wave = threadIdx.x >> 6;
   __shared__ float part[4];
@@ -136,14 +142,30 @@ __global__ __launch_bounds__(256) void k_xent_max(XentArgs a, bool train, float*
     }
   } else {
     const float* p = static_cast<const float*>(a.w);
-    if (a.ldw == a.d && ((uintptr_t)p & 15) == 0) {
-      const int64_t n = a.v * a.d, n4 = n / 4;
+    if (a.ldw == a.d && a.d >= 4 && ((uintptr_t)p & 15) == 0) {
+      const int64_t n = a.v * a.d, n4 = n / 4, i0 = (int64_t)b * 256 + threadIdx.x;
       const float4* q = reinterpret_cast<const float4*>(p);
+      if (a.bias) {
+        constexpr int64_t step = kMaxGroups * 256 * 4;
+        const int64_t rows = step / a.d, cols = step % a.d;
+        int64_t row = i0 * 4 / a.d, col = i0 * 4 % a.d;
 #pragma unroll 8
-      for (int64_t i = (int64_t)b * 256 + threadIdx.x; i < n4; i += kMaxGroups * 256) larger4(m, q[i]);
-      if (b == 0 && threadIdx.x < n - n4 * 4) larger(m, p[n4 * 4 + threadIdx.x]);
+        for (int64_t i = i0; i < n4; i += kMaxGroups * 256) {
+          const float4 v = q[i];
+          const bool out = word_out(a.bias, row), next = word_out(a.bias, min(row + 1, a.v - 1));
+          larger(m, out ? 0.f : v.x), larger(m, (col + 1 < a.d ? out : next) ? 0.f : v.y);
+          larger(m, (col + 2 < a.d ? out : next) ? 0.f : v.z), larger(m, (col + 3 < a.d ? out : next) ? 0.f : v.w);
+          row += rows, col += cols;
+          if (col >= a.d) col -= a.d, ++row;
+        }
+      } else {
+#pragma unroll 8
+        for (int64_t i = i0; i < n4; i += kMaxGroups * 256) larger4(m, q[i]);
+      }
+      if (b == 0 && threadIdx.x < n - n4 * 4 && !word_out(a.bias, a.v - 1)) larger(m, p[n4 * 4 + threadIdx.x]);
     } else {
       for (int64_t row = (int64_t)b * 4 + wave; row < a.v; row += kMaxGroups * 4) {
+        if (word_out(a.bias, row)) continue;
         const float* q = p + row * a.ldw;
 #pragma unroll 8
         for (int64_t i = threadIdx.x & 63; i < a.d; i += 64) larger(m, q[i]);
@@ -210,7 +232,8 @@ __global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool 
 }
 
 // Rows to operands: 16-bit values, or two pieces of fp32 ones, zeros behind the
-// row's end.  One thread = 8 values.  fp32 rows of x have a power of two each.
+// row's end.  One thread = 8 values.  fp32 rows of x have a power of two each; those
+// of w that a bias takes out are zeros, so that they may hold any finite values.
 // clean: a second copy, the
 // one that dw's product takes, under one power of two, with rows of tokens that do
 // not count zero (their G is zero, and zero times what such a row may hold need not
@@ -220,7 +243,8 @@ __global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool 
 struct XentPack {
   const void* x;
   int64_t ld, rows, d, dp;
-  const float* scale;   // of the whole matrix
+  const void* bias;      // of w's rows where they are fp32, or null
+  const float* scale;    // of the whole matrix
   const int* exponents;  // of every row in `out`, or null: the matrix's
   uint16_t *out, *clean;
   const int64_t* targets;
@@ -272,7 +296,7 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsig
     __builtin_memcpy(to + at, hi, sizeof hi);
     if constexpr (DT == kF32) __builtin_memcpy(to + kMmaLow + at, lo, sizeof lo);
   };
-  if (p.out) put(p.out, 1.f, DT != kF32 ? 1.f : p.exponents ? ldexpf(1.f, p.exponents[row]) : *p.scale);
+  if (p.out) put(p.out, DT == kF32 && word_out(p.bias, row) ? 0.f : 1.f, DT != kF32 ? 1.f : p.exponents ? ldexpf(1.f, p.exponents[row]) : *p.scale);
   if (!p.clean) return;
   float f = 1.f;
   if (p.weights) {
@@ -1132,10 +1156,10 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
   if (f32 || (train && a.weights))
     hipLaunchKernelGGL(k_xent_prep, dim3(1), dim3(256), 0, s, a, train, f32, partmax, sc);
   XentPack w{}, x{};
-  if (l.pack_w) w = XentPack{a.w, a.ldw, a.v, a.d, l.dp, sc + kSw, nullptr, reinterpret_cast<uint16_t*>(ws + l.w)};
+  if (l.pack_w) w = XentPack{a.w, a.ldw, a.v, a.d, l.dp, f32 ? a.bias : nullptr, sc + kSw, nullptr, reinterpret_cast<uint16_t*>(ws + l.w)};
   if (l.pack_x || train) {
     uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
-    x = XentPack{a.x,       a.ldx,    a.t,       a.d, l.dp, sc + kSx, xrow, l.pack_x ? px : nullptr,
+    x = XentPack{a.x,       a.ldx,    a.t,       a.d, l.dp, nullptr, sc + kSx, xrow, l.pack_x ? px : nullptr,
                  train ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr,
                  a.targets, a.ignore, a.v, a.weights, sc, reinterpret_cast<int*>(ws + l.rows)};
   }

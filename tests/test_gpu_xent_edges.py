@@ -243,3 +243,21 @@ def test_small_probabilities_of_16_bit_tensors(t, dtype):
     want = torch.full((v - 1,), t * p, dtype=torch.float64, device=DEV)
     tol = want * (2.0 ** -11 + (2.0 ** -8 if dtype == BF16 else 0.0) + 2.0 ** -18) + (t * 2.0 ** -25 * 2.0 ** -13 if dtype == F16 else 0.0)
     close("dw", dw[1:, 0], want, tol)
+
+
+@pytest.mark.parametrize("t", [9, 90])
+def test_words_without_a_place_may_hold_anything(t):
+    """fp32: a bias of -infinity takes a word out, whatever finite values its row of
+    weights holds (a vocabulary's unused end)."""
+    v, d = 300, 24
+    x, w, y, b = inputs(t, v, d, F32, True, seed=47, ignored=0.1)
+    y.clamp_(max=279)
+    live = torch.arange(v, device=DEV) < 280
+    b[~live] = -float("inf")
+    for size in (1e12, 1e30):
+        big = w.clone()
+        big[~live] = size
+        big[~live, ::2] *= -1
+        loss, lse, dx, dw, db = T.cross_entropy_train(x, big, y, b)
+        check(Reference(x, w[live], y, b[live], mean=True), loss, lse, dx, dw[live], db[live])
+        assert not dw[~live].any() and not db[~live].any()
