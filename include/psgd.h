@@ -621,8 +621,8 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
  *
  * workspace: psgd_xent_workspace bytes for the same arguments (`train`: for
  * psgd_xent_train), 256-byte aligned, scratch.  It holds at most 1 GiB of
- * probabilities (or those of 256 tokens) whatever the number of tokens, and
- * copies of operands that the kernels cannot read in place: fp32 ones, and
+ * probabilities, or without gradients of sums over 64 words each (or those of 256
+ * tokens) whatever the number of tokens, and copies of operands that the kernels cannot read in place: fp32 ones, and
  * 16-bit ones whose address is no multiple of 16 bytes or whose dim or row
  * stride is no multiple of 8.
  *

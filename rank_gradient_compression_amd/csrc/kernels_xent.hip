@@ -50,7 +50,8 @@ namespace psgd {
 enum { kSx, kSw, kEw, kEg, kS, kEdx, kEdw, kEdb, kScalars };
 
 constexpr int kMaxGroups = 1024;    // workgroups that look for a tensor's largest value
-constexpr int64_t kBlockBytes = int64_t(1) << 30;  // of E (and G) at a time
+constexpr int64_t kBlockBytes = int64_t(1) << 30;  // of E (and G) at a time, or of segments' sums without gradients
+constexpr int64_t kBlockTokens = int64_t(1) << 23;  // (a launch holds 2^32 threads)
 constexpr int kGradRows = 16;       // tokens of a workgroup of the pass over E, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHeld = 32768.f;  // what E is held times in fp16
@@ -252,6 +253,21 @@ struct XentPack {
   const float* weights;
   const float* sc;
   int* factors;
+
+  XentPack rows_from(int64_t at, int64_t n, int dtype) const {  // `n` of the rows, from `at` on
+    XentPack p = *this;
+    const int64_t pitch = dp * (dtype == kF32 ? 2 : 1);
+    p.x = static_cast<const uint8_t*>(x) + at * ld * dtype_bytes(dtype);
+    p.rows = n;
+    if (bias) p.bias = static_cast<const float*>(bias) + at;
+    if (exponents) p.exponents = exponents + at;
+    if (out) p.out = out + at * pitch;
+    if (clean) p.clean = clean + at * pitch;
+    if (targets) p.targets = targets + at;
+    if (weights) p.weights = weights + at;
+    if (factors) p.factors = factors + at;
+    return p;
+  }
 };
 template <int DT>
 __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsigned first) {
@@ -923,8 +939,8 @@ __global__ __launch_bounds__(256) void k_xent_dx(const float* part, int64_t piec
 
 // Gradients of a loss over no word or no token.
 __global__ __launch_bounds__(256) void k_xent_zero(void* p, int dtype, int64_t rows, int64_t cols, int64_t ld) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < rows * cols) store_any(p, dtype, i / cols * ld + i % cols, 0.f);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * cols; i += (int64_t)gridDim.x * 256)
+    store_any(p, dtype, i / cols * ld + i % cols, 0.f);
 }
 
 // ---------------------------------------------------------------- the host
@@ -952,11 +968,12 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   l.pack_w = !readable(a.w, a.ldw, a.d, a.dtype);
   l.dp = up(a.d, 64);
   l.vp = up(a.v, 64);
-  // (a block's rows are a multiple of the tiles', and few tokens are one block)
-  l.block = std::max<int64_t>(1, a.t);
-  if (train) l.block = std::min(l.block, std::max<int64_t>(256, kBlockBytes / (l.vp * (f32 ? 8 : 2)) / 256 * 256));
   l.seg_shift = a.t <= kFewTokens ? 5 : 6;
   l.nseg = cdiv(a.v, int64_t(1) << l.seg_shift);
+  // (a block's rows are a multiple of the tiles', and few tokens are one block; its
+  // size bounds the workspace and every launch of a workgroup a token)
+  const int64_t held = train ? l.vp * (f32 ? 8 : 2) : l.nseg * (int64_t)sizeof(float2);
+  l.block = std::min({std::max<int64_t>(1, a.t), kBlockTokens, std::max<int64_t>(256, kBlockBytes / held / 256 * 256)});
   const int64_t tiles = cdiv(l.block, 128) * cdiv(a.d, 128), chunks = cdiv(a.v, f32 ? kMmaK<true> : kMmaK<false>);
   l.dx_splits = std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, tiles), chunks / 8, 128}));
   size_t at = 0;
@@ -989,6 +1006,22 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
 
 // The weights' operand and the hidden states' in one launch; rows 0: none of it.
 static void pack(const XentPack& w, const XentPack& x, int dtype, hipStream_t s) {
+  // (a launch holds 2^32 threads: larger operands in pieces, one after the other)
+  constexpr int64_t most = int64_t(1) << 31;
+  if (w.rows * (w.dp / 8) + x.rows * (x.dp / 8) > most) {
+    if (w.rows && x.rows) {
+      pack(w, XentPack{}, dtype, s);
+      pack(XentPack{}, x, dtype, s);
+    } else {
+      const XentPack& p = w.rows ? w : x;
+      const int64_t half = p.rows / 2;
+      for (int64_t at : {int64_t(0), half}) {
+        const XentPack q = p.rows_from(at, at ? p.rows - half : half, dtype);
+        pack(w.rows ? q : XentPack{}, w.rows ? XentPack{} : q, dtype, s);
+      }
+    }
+    return;
+  }
   const unsigned first = grid(w.rows * w.dp / 8), all = first + grid(x.rows * x.dp / 8);
   if (all == 0) return;
   if (dtype == kF32)
@@ -1146,7 +1179,7 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
   if (a.t == 0) {
     if (train && !a.accumulate) {
       if (a.dw && a.v && a.d)
-        hipLaunchKernelGGL(k_xent_zero, dim3(grid(a.v * a.d)), dim3(256), 0, s, a.dw, a.dw_dtype, a.v, a.d, a.lddw);
+        hipLaunchKernelGGL(k_xent_zero, dim3(std::min(grid(a.v * a.d), 1u << 16)), dim3(256), 0, s, a.dw, a.dw_dtype, a.v, a.d, a.lddw);
       if (a.dbias)
         hipLaunchKernelGGL(k_xent_zero, dim3(grid(a.v)), dim3(256), 0, s, a.dbias, a.dtype, int64_t(1), a.v, a.v);
     }

@@ -1,0 +1,15 @@
+"""Workspaces and refusals at the far ends of the cross entropy's and the
+orthogonalised step's arguments.  Host side only: these run without a GPU."""
+import pytest
+
+pytest.importorskip("rank_gradient_compression_amd")
+from rank_gradient_compression_amd import binding as B  # noqa: E402
+from test_ends_abi import MB, xent  # noqa: E402
+
+
+@pytest.mark.parametrize("vocab", [1, 5, 32000, 2000000])
+def test_scoring_many_tokens_needs_no_more_than_a_block(vocab):
+    """Sums of 64 words each for a block of tokens, not for all of them."""
+    some = B.psgd_xent_workspace(xent(tokens=1 << 23, vocab=vocab), False)
+    many = B.psgd_xent_workspace(xent(tokens=(1 << 31) - 1, vocab=vocab), False)
+    assert some == many < (1 << 30) + (1 << 26)

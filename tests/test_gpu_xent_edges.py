@@ -261,3 +261,38 @@ def test_words_without_a_place_may_hold_anything(t):
         loss, lse, dx, dw, db = T.cross_entropy_train(x, big, y, b)
         check(Reference(x, w[live], y, b[live], mean=True), loss, lse, dx, dw[live], db[live])
         assert not dw[~live].any() and not db[~live].any()
+
+
+def test_tokens_beyond_2_24():
+    """More tokens than one launch has workgroups for."""
+    t, v, d = (1 << 24) + 777, 5, 8
+    g = torch.Generator(device=DEV)
+    g.manual_seed(48)
+    x = torch.randn(t, d, generator=g, device=DEV).to(BF16)
+    w = torch.randn(v, d, generator=g, device=DEV).to(BF16)
+    y = torch.full((t,), -100, device=DEV)
+    at = torch.cat([torch.arange(0, t, 4099, device=DEV), torch.arange(t - 500, t, device=DEV)]).unique()
+    y[at] = torch.randint(0, v, (len(at),), generator=g, device=DEV)
+    say("[xent] 2^24 tokens and some")
+    loss, lse = T.cross_entropy(x, w, y)
+    ref = Reference(x[at], w, y[at], mean=True)
+    check(ref, loss[at], lse[at])
+    assert int((loss != 0).sum()) == len(at) and torch.isfinite(lse).all()
+    loss2, lse2, dx, dw, _ = T.cross_entropy_train(x, w, y, dw=torch.zeros(v, d, device=DEV))
+    check(ref, loss2[at], lse2[at], dx[at], dw)
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+
+
+def test_operands_beyond_2_31_threads():
+    """Rows whose copy, eight values a thread, is more than one launch holds."""
+    t, v = (1 << 28) + 1001, 3
+    x = (torch.arange(t, device=DEV, dtype=torch.int32) % 251).to(BF16).view(t, 1) / 64
+    w = torch.tensor([[0.5], [-1.0], [2.0]], dtype=BF16, device=DEV)
+    y = torch.full((t,), -100, device=DEV)
+    at = torch.cat([torch.arange(0, t, 65537, device=DEV), torch.arange(t - 500, t, device=DEV),
+                    torch.arange(t // 2 - 300, t // 2 + 300, device=DEV)]).unique()
+    y[at] = at % v
+    say("[xent] 2^28 tokens of one value")
+    loss, lse = T.cross_entropy(x, w, y)
+    check(Reference(x[at], w, y[at]), loss[at], lse[at])
+    assert torch.equal(lse[:251].repeat(4), lse[251 * 1000000:251 * 1000004])
