@@ -584,7 +584,9 @@ extern "C" psgd_status_t psgd_xent_workspace(const psgd_xent_t* args, int32_t tr
   XentArgs a;
   if (psgd_status_t s = check_xent(fn, args, train != 0, &a)) return s;
   if (!bytes) return invalid(fn, "bytes is NULL");
-  *bytes = xent_layout(a, train != 0).bytes;
+  const XentLayout l = xent_layout(a, train != 0);
+  if (psgd_status_t s = check_xent_layout(fn, a, l)) return s;
+  *bytes = l.bytes;
   return PSGD_OK;
 }
 

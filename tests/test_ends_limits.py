@@ -13,3 +13,11 @@ def test_scoring_many_tokens_needs_no_more_than_a_block(vocab):
     some = B.psgd_xent_workspace(xent(tokens=1 << 23, vocab=vocab), False)
     many = B.psgd_xent_workspace(xent(tokens=(1 << 31) - 1, vocab=vocab), False)
     assert some == many < (1 << 30) + (1 << 26)
+
+
+def test_the_workspace_query_refuses_what_the_call_refuses():
+    far = xent(ldw=2000008, vocab=2, w=1 << 40)  # (read in place: its row stride is too large)
+    for train in (False, True):
+        with pytest.raises(B.PsgdError, match="in place") as e:
+            B.psgd_xent_workspace(far, train)
+        assert e.value.status == B.PSGD_ERR_INVALID_ARG
