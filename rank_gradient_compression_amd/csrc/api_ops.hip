@@ -635,6 +635,7 @@ static psgd_status_t check_muon(const char* fn, int32_t n, const psgd_muon_tenso
   if (o->eps < 0.f) return invalid(fn, "eps is negative");
   if (o->steps < 1 || o->steps > 100) return invalid(fn, "steps is outside 1 .. 100");
   if (o->pieces < 0 || o->pieces > 2) return invalid(fn, "pieces must be 0, 1 or 2");
+  if (!finite(1.f - o->lr * o->weight_decay)) return invalid(fn, "lr times weight_decay is not finite");
   *opts = MuonOpts{o->momentum, 1.f - o->lr * o->weight_decay, o->a, o->b, o->c, o->eps, o->steps, o->nesterov != 0};
   float sx, sa, sb;
   if (!muon_scales(*opts, &sx, &sa, &sb)) return invalid(fn, "the coefficients let singular values grow beyond 16");

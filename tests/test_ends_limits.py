@@ -4,7 +4,7 @@ import pytest
 
 pytest.importorskip("rank_gradient_compression_amd")
 from rank_gradient_compression_amd import binding as B  # noqa: E402
-from test_ends_abi import MB, xent  # noqa: E402
+from test_ends_abi import MB, matrix, opts, table, xent  # noqa: E402
 
 
 @pytest.mark.parametrize("vocab", [1, 5, 32000, 2000000])
@@ -20,4 +20,12 @@ def test_the_workspace_query_refuses_what_the_call_refuses():
     for train in (False, True):
         with pytest.raises(B.PsgdError, match="in place") as e:
             B.psgd_xent_workspace(far, train)
+        assert e.value.status == B.PSGD_ERR_INVALID_ARG
+
+
+def test_a_decay_that_is_no_number_is_refused():
+    both = opts(lr=1e30, weight_decay=1e30)
+    for fn, args in ((B.psgd_muon_workspace, ()), (B.psgd_muon_step, (64 * MB, 1 << 30))):
+        with pytest.raises(B.PsgdError, match="weight_decay") as e:
+            fn(table(matrix()), both, *args)
         assert e.value.status == B.PSGD_ERR_INVALID_ARG
