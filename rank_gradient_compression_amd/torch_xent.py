@@ -121,11 +121,12 @@ class _CrossEntropyFunction(torch.autograd.Function):
     65536, say) is part of them."""
 
     @staticmethod
-    def forward(ctx, x, w, bias, targets, reduction, ignore_index):
+    def forward(ctx, x, w, bias, targets, reduction, ignore_index, grad):
         xm, wm, y = _as_matrix(x), _as_matrix(w), targets.reshape(-1)
         b = None if bias is None else bias.contiguous()
         ctx.x_shape, ctx.reduction, ctx.ignore_index = x.shape, reduction, ignore_index
-        need = ctx.needs_input_grad[:3]
+        # (needs_input_grad goes by the inputs alone, under no_grad too)
+        need = tuple(grad and n for n in ctx.needs_input_grad[:3])
         ctx.late = reduction == "none" or x.dtype == torch.float16
         if ctx.late or not any(need):
             loss, _ = cross_entropy(xm, wm, y, b, ignore_index)
@@ -155,7 +156,7 @@ class _CrossEntropyFunction(torch.autograd.Function):
         else:
             # (the incoming value stays fp32: one rounding to the type, of the product)
             dx, dw, db = (None if g is None else (g * grad.float().expand(1)).to(g.dtype) for g in ctx.saved_tensors)
-        return None if dx is None else dx.view(ctx.x_shape), dw, db, None, None, None
+        return None if dx is None else dx.view(ctx.x_shape), dw, db, None, None, None, None
 
 
 def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -168,4 +169,4 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
         raise ValueError('reduction must be "mean", "sum" or "none"')
     if targets.shape != x.shape[:-1]:
         raise ValueError(f"targets of shape {tuple(targets.shape)} for x of shape {tuple(x.shape)}")
-    return _CrossEntropyFunction.apply(x, w, bias, targets, reduction, ignore_index)
+    return _CrossEntropyFunction.apply(x, w, bias, targets, reduction, ignore_index, torch.is_grad_enabled())
