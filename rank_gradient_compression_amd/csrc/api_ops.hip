@@ -578,13 +578,16 @@ static psgd_status_t check_xent_layout(const char* fn, const XentArgs& a, const 
   return PSGD_OK;
 }
 
+// (set by check_xent for a training call only; one that wants none is a forward)
+static bool wants_gradients(const XentArgs& a) { return a.dx || a.dw || a.dbias; }
+
 extern "C" psgd_status_t psgd_xent_workspace(const psgd_xent_t* args, int32_t train, size_t* bytes) {
   clear_error();
   const char* fn = "psgd_xent_workspace";
   XentArgs a;
   if (psgd_status_t s = check_xent(fn, args, train != 0, &a)) return s;
   if (!bytes) return invalid(fn, "bytes is NULL");
-  const XentLayout l = xent_layout(a, train != 0);
+  const XentLayout l = xent_layout(a, wants_gradients(a));
   if (psgd_status_t s = check_xent_layout(fn, a, l)) return s;
   *bytes = l.bytes;
   return PSGD_OK;
@@ -595,7 +598,8 @@ static psgd_status_t run_xent(const char* fn, const psgd_xent_t* args, bool trai
   clear_error();
   XentArgs a;
   if (psgd_status_t s = check_xent(fn, args, train, &a)) return s;
-  const XentLayout l = xent_layout(a, train);
+  const bool gradients = wants_gradients(a);
+  const XentLayout l = xent_layout(a, gradients);
   if (psgd_status_t s = check_xent_layout(fn, a, l)) return s;
   if (psgd_status_t s = check_workspace(fn, l.bytes, ws, bytes)) return s;
   const size_t e = (size_t)dtype_bytes(a.dtype), tf = (size_t)a.t * sizeof(float);
@@ -611,7 +615,7 @@ static psgd_status_t run_xent(const char* fn, const psgd_xent_t* args, bool trai
                      {a.targets, (size_t)a.t * sizeof(int64_t)},
                      {a.weights, tf}};
   if (outputs_overlap(r, 6)) return invalid(fn, "an output or the workspace overlaps another buffer");
-  return launch_status(launch_xent(a, l, train, ws, stream), fn);
+  return launch_status(launch_xent(a, l, gradients, ws, stream), fn);
 }
 
 extern "C" psgd_status_t psgd_xent_forward(const psgd_xent_t* args, void* ws, size_t bytes, hipStream_t stream) {

@@ -313,7 +313,7 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsig
     if constexpr (DT == kF32) __builtin_memcpy(to + kMmaLow + at, lo, sizeof lo);
   };
   if (p.out) put(p.out, DT == kF32 && word_out(p.bias, row) ? 0.f : 1.f, DT != kF32 ? 1.f : p.exponents ? ldexpf(1.f, p.exponents[row]) : *p.scale);
-  if (!p.clean) return;
+  if (!p.factors) return;
   float f = 1.f;
   if (p.weights) {
     const int most = (int)p.sc[kEg], less = most - weight_exponent(p.weights[row], most);
@@ -321,6 +321,7 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsig
     if (c == 0) p.factors[row] = less;
     if (p.weights[row] == 0.f) f = 0.f;
   }
+  if (!p.clean) return;
   const int64_t y = p.targets[row];
   put(p.clean, ignored(y, p.ignore) || y >= p.v ? 0.f : f, DT != kF32 ? 1.f : *p.scale);
 }
@@ -960,6 +961,7 @@ static int64_t grad_rows(int64_t tokens, int64_t vp) {
   return std::min<int64_t>(kGradRows, std::max<int64_t>(1, tokens * cdiv(vp, 2048) / 1024));
 }
 
+// (train: with gradients, one at least)
 XentLayout xent_layout(const XentArgs& a, bool train) {
   XentLayout l{};
   const bool f32 = a.dtype == kF32;
@@ -986,8 +988,8 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   l.partmax = take(f32 ? 2 * kMaxGroups * sizeof(float) : 0);
   l.xrow = take(f32 ? (size_t)a.t * sizeof(int) : 0);
   l.rows = take(train && a.weights ? (size_t)a.t * sizeof(int) : 0);
-  // x as the logits' operand, then (training) with ignored tokens' rows zero
-  l.x = take((size_t)((l.pack_x ? 1 : 0) + (train ? 1 : 0)) * l.parts * a.t * l.dp * 2);
+  // x as the logits' operand, then (for dw) with rows of tokens that do not count zero
+  l.x = take((size_t)((l.pack_x ? 1 : 0) + (train && a.dw ? 1 : 0)) * l.parts * a.t * l.dp * 2);
   l.w = take(l.pack_w ? (size_t)l.parts * a.v * l.dp * 2 : 0);
   l.stats = take((size_t)l.block * l.nseg * sizeof(float2));
   l.target = take((size_t)l.block * sizeof(float));
@@ -1116,7 +1118,7 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   hipLaunchKernelGGL(k_xent_lse, dim3((unsigned)n + (scalars ? 1 : 0)), dim3(256), 0, s, a,
                      XentSums{stats, n, l.nseg, a.targets + t0, target, a.loss + t0, a.lse + t0,
                               reinterpret_cast<float*>(ws + l.scalars), sums});
-  if (!train || !(a.dx || a.dw || a.dbias)) return;
+  if (!train) return;
   uint16_t* const g = reinterpret_cast<uint16_t*>(ws + l.g);
   float* const db = reinterpret_cast<float*>(ws + l.db);
   const int rows = (int)grad_rows(l.block, l.vp);
@@ -1190,11 +1192,11 @@ hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void*
     hipLaunchKernelGGL(k_xent_prep, dim3(1), dim3(256), 0, s, a, train, f32, partmax, sc);
   XentPack w{}, x{};
   if (l.pack_w) w = XentPack{a.w, a.ldw, a.v, a.d, l.dp, f32 ? a.bias : nullptr, sc + kSw, nullptr, reinterpret_cast<uint16_t*>(ws + l.w)};
-  if (l.pack_x || train) {
+  if (l.pack_x || (train && (a.dw || a.weights))) {
     uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
     x = XentPack{a.x,       a.ldx,    a.t,       a.d, l.dp, nullptr, sc + kSx, xrow, l.pack_x ? px : nullptr,
-                 train ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr,
-                 a.targets, a.ignore, a.v, a.weights, sc, reinterpret_cast<int*>(ws + l.rows)};
+                 train && a.dw ? px + (l.pack_x ? l.parts * a.t * l.dp : 0) : nullptr,
+                 a.targets, a.ignore, a.v, a.weights, sc, train ? reinterpret_cast<int*>(ws + l.rows) : nullptr};
   }
   pack(w, x, a.dtype, s);
   for (int64_t t0 = 0; t0 < a.t; t0 += l.block) {

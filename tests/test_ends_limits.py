@@ -29,3 +29,11 @@ def test_a_decay_that_is_no_number_is_refused():
         with pytest.raises(B.PsgdError, match="weight_decay") as e:
             fn(table(matrix()), both, *args)
         assert e.value.status == B.PSGD_ERR_INVALID_ARG
+
+
+def test_gradients_that_are_not_wanted_take_no_memory():
+    many = dict(tokens=100000, vocab=64, dim=32, ldx=32)
+    ask = lambda train=True, **kw: B.psgd_xent_workspace(xent(**many, **kw), train)  # noqa: E731
+    copy = 100000 * 64 * 2  # (x's rows, padded, of 16 bits: what dw's product takes)
+    assert copy <= ask() - ask(dw=0) <= copy + 256
+    assert ask(dx=0, dw=0) == ask(False)

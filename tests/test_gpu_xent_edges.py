@@ -296,3 +296,15 @@ def test_operands_beyond_2_31_threads():
     loss, lse = T.cross_entropy(x, w, y)
     check(Reference(x[at], w, y[at]), loss[at], lse[at])
     assert torch.equal(lse[:251].repeat(4), lse[251 * 1000000:251 * 1000004])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_only_what_is_wanted_under_weights(dtype):
+    t, v, d = 75, 130, 40
+    x, w, y, b = inputs(t, v, d, dtype, True, seed=49)
+    u = torch.logspace(-5, 5, t, device=DEV)
+    full = T.cross_entropy_train(x, w, y, b, weights=u)
+    for need in ((True, False, False), (False, True, False), (False, False, True), (True, False, True)):
+        got = T.cross_entropy_train(x, w, y, b, weights=u, need_dx=need[0], need_dw=need[1], need_dbias=need[2])
+        for n, a, c in zip((True, True) + need, got, full):
+            assert (a is not None) == n and (not n or torch.equal(a, c))
