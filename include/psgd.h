@@ -663,6 +663,17 @@ psgd_status_t psgd_xent_forward(const psgd_xent_t* args, void* workspace, size_t
 psgd_status_t psgd_xent_train(const psgd_xent_t* args, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Gradients times a factor that only the device knows (the value that comes into a
+ * backward pass): out = in * *factor for n contiguous values of type `dtype`, the
+ * product in fp32 and rounded once.  out may be in itself.  Errors:
+ * PSGD_ERR_INVALID_ARG (an unknown type, sizes, NULL or misaligned buffers, an out
+ * that overlaps factor, or in without being it); PSGD_ERR_HIP.  Only enqueues a
+ * kernel.
+ */
+psgd_status_t psgd_xent_scale(const void* in, int32_t dtype, int64_t n, const float* factor, void* out,
+                              hipStream_t stream);
+
+/*
  * Orthogonalised updates of a list of matrices, and the optimiser step around
  * them (Muon): what may follow the decompression instead of momentum SGD.
  *

@@ -626,6 +626,21 @@ extern "C" psgd_status_t psgd_xent_train(const psgd_xent_t* args, void* ws, size
   return run_xent("psgd_xent_train", args, true, ws, bytes, stream);
 }
 
+extern "C" psgd_status_t psgd_xent_scale(const void* in, int32_t dtype, int64_t n, const float* factor, void* out,
+                                         hipStream_t stream) {
+  clear_error();
+  const char* fn = "psgd_xent_scale";
+  if (!known_dtype(dtype)) return invalid(fn, "unknown element type");
+  if (n < 0 || n > (int64_t(1) << 42)) return invalid(fn, "the number of values is negative or above 2^42");
+  if (n && (!in || !out || !factor)) return invalid(fn, "a required buffer is NULL");
+  if (misaligned(in, dtype_bytes(dtype)) || misaligned(out, dtype_bytes(dtype)) || misaligned(factor, 4))
+    return invalid(fn, "a buffer is not aligned to its element type");
+  const size_t bytes = (size_t)n * dtype_bytes(dtype);
+  if ((in != out && overlap(in, bytes, out, bytes)) || overlap(factor, 4, out, bytes))
+    return invalid(fn, "out overlaps the factor, or the values without being them");
+  return launch_status(launch_xent_scale(in, dtype, n, factor, out, stream), fn);
+}
+
 // ------------------------------------------------------ orthogonalised step
 static bool finite(float v) { return v - v == 0.f; }
 

@@ -47,5 +47,6 @@ struct XentLayout {
 };
 XentLayout xent_layout(const XentArgs& a, bool train);
 hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void* ws, hipStream_t s);
+hipError_t launch_xent_scale(const void* in, int dtype, int64_t n, const float* factor, void* out, hipStream_t s);
 
 }  // namespace psgd

@@ -112,6 +112,13 @@ def _total(v: torch.Tensor) -> torch.Tensor:
     return v.sum()
 
 
+def _times(g: torch.Tensor, factor: torch.Tensor) -> torch.Tensor:
+    """A gradient times one float32 value on its device (psgd_xent_scale)."""
+    out = torch.empty_like(g)
+    _call(g.device, B.psgd_xent_scale, g.data_ptr(), _dtype(g), g.numel(), factor.data_ptr(), out.data_ptr())
+    return out
+
+
 class _CrossEntropyFunction(torch.autograd.Function):
     """mean and sum: the gradients are formed with the loss, from the same
     logits, and the backward pass multiplies them by the one incoming value.
@@ -154,8 +161,7 @@ class _CrossEntropyFunction(torch.autograd.Function):
                                                    reduction=reduction, ignore_index=ctx.ignore_index, need_dx=need[0],
                                                    need_dw=need[1], need_dbias=need[2])
         else:
-            # (the incoming value stays fp32: one rounding to the type, of the product)
-            dx, dw, db = (None if g is None else (g * grad.float().expand(1)).to(g.dtype) for g in ctx.saved_tensors)
+            dx, dw, db = (None if g is None else _times(g, grad.float()) for g in ctx.saved_tensors)
         return None if dx is None else dx.view(ctx.x_shape), dw, db, None, None, None, None
 
 

@@ -37,3 +37,16 @@ def test_gradients_that_are_not_wanted_take_no_memory():
     copy = 100000 * 64 * 2  # (x's rows, padded, of 16 bits: what dw's product takes)
     assert copy <= ask() - ask(dw=0) <= copy + 256
     assert ask(dx=0, dw=0) == ask(False)
+
+
+@pytest.mark.parametrize("args,match", [
+    ((MB, 3, 8, 2 * MB, 3 * MB), "type"), ((MB, 0, -1, 2 * MB, 3 * MB), "number"), ((MB, 0, 1 << 43, 2 * MB, 3 * MB), "number"),
+    ((0, 0, 8, 2 * MB, 3 * MB), "NULL"), ((MB, 0, 8, 0, 3 * MB), "NULL"), ((MB, 0, 8, 2 * MB, 0), "NULL"),
+    ((MB + 1, 1, 8, 2 * MB, 3 * MB), "aligned"), ((MB, 0, 8, 2 * MB + 2, 3 * MB), "aligned"),
+    ((MB, 0, 8, 2 * MB, 3 * MB + 2), "aligned"), ((MB, 0, 8, 2 * MB, MB + 16), "overlaps"),
+    ((MB, 0, 8, MB + 4, MB), "overlaps"),
+])
+def test_scale_refused(args, match):
+    with pytest.raises(B.PsgdError, match=match) as e:
+        B.psgd_xent_scale(*args)
+    assert e.value.status == B.PSGD_ERR_INVALID_ARG

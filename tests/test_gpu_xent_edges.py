@@ -12,7 +12,9 @@ if not torch.cuda.is_available():
 
 from gpu_util import say  # noqa: E402
 from test_gpu_xent import BF16, DEV, F16, F32, OUT, Reference, U, check, close, inputs  # noqa: E402
+from rank_gradient_compression_amd import binding as B  # noqa: E402
 from rank_gradient_compression_amd import torch_api as T  # noqa: E402
+from rank_gradient_compression_amd import torch_xent as X  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -308,3 +310,45 @@ def test_only_what_is_wanted_under_weights(dtype):
         got = T.cross_entropy_train(x, w, y, b, weights=u, need_dx=need[0], need_dw=need[1], need_dbias=need[2])
         for n, a, c in zip((True, True) + need, got, full):
             assert (a is not None) == n and (not n or torch.equal(a, c))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_backward_multiplies_in_place_of_fp32_copies(dtype):
+    """One product in fp32 and one rounding; beside the gradients themselves the
+    backward pass takes no memory of their size."""
+    x, w, y, b = inputs(64, 8192, 1024, dtype, True, seed=50)
+    want = T.cross_entropy_train(x, w, y, b)[2:]
+    for up in (1.0, 0.3, -1e-30, float("inf")):
+        leaves = [v.clone().requires_grad_(True) for v in (x, w, b)]
+        out = T.linear_cross_entropy(leaves[0], leaves[1], y, leaves[2])
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        out.backward(torch.tensor(up, device=DEV), retain_graph=True)
+        extra = torch.cuda.max_memory_allocated() - before
+        assert extra <= sum(v.numel() * v.element_size() for v in leaves) + (1 << 20)
+        for leaf, g in zip(leaves, want):
+            assert torch.equal(leaf.grad.nan_to_num(7.0), (g.float() * up).to(dtype).nan_to_num(7.0))
+        out.backward(torch.tensor(up, device=DEV))  # (again, from the same saved gradients)
+        for leaf, g in zip(leaves, want):
+            one = (g.float() * up).to(dtype)
+            assert torch.equal(leaf.grad.nan_to_num(7.0), (one + one).nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_scale_of_any_length_and_address(dtype):
+    """Half a step of the type, and what the product's rounding to fp32 may add where it
+    brings it to a tie (the compiler rounds some products to fp16 at once, some so)."""
+    flat = torch.randn(5000, device=DEV).to(dtype)
+    f = torch.tensor([3.0, -0.7], device=DEV)[1:]
+    half = torch.finfo(dtype).eps / 2 + 2.0 ** -23
+    for at, n, to in ((0, 0, 0), (0, 1, 0), (1, 7, 0), (8, 4096, 16), (3, 4097, 3), (0, 5000, 0)):
+        out = torch.full((5100,), 9.0, dtype=dtype, device=DEV)
+        v, o = flat[at:at + n], out[to:to + n]
+        X._call(DEV, B.psgd_xent_scale, v.data_ptr(), X._dtype(v), n, f.data_ptr(), o.data_ptr())
+        want = v.double() * f.double()
+        assert ((o.double() - want).abs() <= half * want.abs() + (2.0 ** -25 if dtype == F16 else 0.0)).all()
+        assert (out[:to] == 9.0).all() and (out[to + n:] == 9.0).all()
+        v = v.clone()
+        X._call(DEV, B.psgd_xent_scale, v.data_ptr(), X._dtype(v), n, f.data_ptr(), v.data_ptr())
+        assert ((v.double() - want).abs() <= half * want.abs() + (2.0 ** -25 if dtype == F16 else 0.0)).all()
