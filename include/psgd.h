@@ -663,6 +663,19 @@ psgd_status_t psgd_xent_forward(const psgd_xent_t* args, void* workspace, size_t
 psgd_status_t psgd_xent_train(const psgd_xent_t* args, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * The sum of `tokens` losses, with `mean` divided by the number of targets that are
+ * neither negative nor ignore_index (by 1 if there is none; targets is not looked at
+ * otherwise), to total[0]: summed in fp64, in an order that depends on the number
+ * alone.  0 for no token.  workspace: PSGD_XENT_TOTAL_BYTES, 256-byte aligned,
+ * scratch.  Errors: PSGD_ERR_INVALID_ARG (sizes, NULL or misaligned buffers, a total or
+ * workspace that overlaps another buffer); PSGD_ERR_WORKSPACE; PSGD_ERR_HIP.  Only
+ * enqueues kernels.
+ */
+#define PSGD_XENT_TOTAL_BYTES 4096
+psgd_status_t psgd_xent_total(const float* loss, const int64_t* targets, int64_t tokens, int64_t ignore_index,
+                              int32_t mean, float* total, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Gradients times a factor that only the device knows (the value that comes into a
  * backward pass): out = in * *factor for n contiguous values of type `dtype`, the
  * product in fp32 and rounded once.  out may be in itself.  Errors:

@@ -15,7 +15,7 @@ from .binding import (PSGD_FLAG_GRADS_BF16, PSGD_FLAG_MOMENTUM, PSGD_KIND_COMPRE
                       psgd_clip_workspace, psgd_clip_workspace_init, psgd_mx_dequantize, psgd_mx_linear,
                       psgd_mx_linear_workspace, psgd_mx_product, psgd_mx_quantize, psgd_mx_sizes,
                       psgd_mx_train_backward, psgd_mx_train_forward, psgd_mx_train_workspace, PSGD_DTYPE_BF16, PSGD_DTYPE_F16, PSGD_DTYPE_F32,
-                      psgd_muon_opts_t, psgd_muon_step, psgd_muon_tensor_t, psgd_muon_workspace, psgd_xent_forward, psgd_xent_scale, psgd_xent_t, psgd_xent_train, psgd_xent_workspace,
+                      psgd_muon_opts_t, psgd_muon_step, psgd_muon_tensor_t, psgd_muon_workspace, psgd_xent_forward, psgd_xent_scale, psgd_xent_t, psgd_xent_total, psgd_xent_train, psgd_xent_workspace,
                       psgd_step_stats, psgd_stream_probe, psgd_subspace_overlap,
                       psgd_timing_enable, psgd_timing_read, psgd_timing_stages, psgd_version, psgd_workspace_init,
                       step_opts)

@@ -60,8 +60,8 @@ EXPORTED = [
     "psgd_clip_norm", "psgd_clip_apply",
     "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize", "psgd_mx_product", "psgd_mx_linear_workspace",
     "psgd_mx_linear", "psgd_mx_train_workspace", "psgd_mx_train_forward", "psgd_mx_train_backward",
-    "psgd_xent_workspace", "psgd_xent_forward", "psgd_xent_train", "psgd_xent_scale", "psgd_muon_workspace",
-    "psgd_muon_step",
+    "psgd_xent_workspace", "psgd_xent_forward", "psgd_xent_train", "psgd_xent_total", "psgd_xent_scale",
+    "psgd_muon_workspace", "psgd_muon_step",
     "psgd_timing_enable", "psgd_timing_stages", "psgd_timing_read", "psgd_stream_probe", "psgd_stream_copy", "psgd_last_error",
     "psgd_version",
 ]
@@ -206,6 +206,7 @@ lib.psgd_mx_train_backward.argtypes = [_i64, _i64, _i64, _vp, _i32, _i64, _vp, _
 lib.psgd_xent_workspace.argtypes = [ctypes.POINTER(psgd_xent_t), _i32, _szp]
 lib.psgd_xent_forward.argtypes = [ctypes.POINTER(psgd_xent_t), _vp, _sz, _vp]
 lib.psgd_xent_train.argtypes = lib.psgd_xent_forward.argtypes
+lib.psgd_xent_total.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _sz, _vp]
 lib.psgd_xent_scale.argtypes = [_vp, _i32, _i64, _vp, _vp, _vp]
 lib.psgd_muon_workspace.argtypes = [_i32, ctypes.POINTER(psgd_muon_tensor_t), ctypes.POINTER(psgd_muon_opts_t), _szp]
 lib.psgd_muon_step.argtypes = [_i32, ctypes.POINTER(psgd_muon_tensor_t), ctypes.POINTER(psgd_muon_opts_t), _vp, _sz, _vp]
@@ -220,7 +221,7 @@ for _f in ["psgd_plan_create", "psgd_plan_get_info", "psgd_plan_tensor", "psgd_w
            "psgd_clip_apply", "psgd_mx_sizes", "psgd_mx_quantize", "psgd_mx_dequantize",
            "psgd_mx_product", "psgd_mx_linear_workspace", "psgd_mx_linear", "psgd_mx_train_workspace",
            "psgd_mx_train_forward", "psgd_mx_train_backward", "psgd_xent_workspace", "psgd_xent_forward",
-           "psgd_xent_train", "psgd_xent_scale", "psgd_muon_workspace", "psgd_muon_step"]:
+           "psgd_xent_train", "psgd_xent_total", "psgd_xent_scale", "psgd_muon_workspace", "psgd_muon_step"]:
     getattr(lib, _f).restype = ctypes.c_int
 
 
@@ -454,6 +455,15 @@ def psgd_xent_forward(args: psgd_xent_t, workspace: int, workspace_bytes: int, s
 
 def psgd_xent_train(args: psgd_xent_t, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
     _check("psgd_xent_train", lib.psgd_xent_train(ctypes.byref(args), workspace, workspace_bytes, stream))
+
+
+PSGD_XENT_TOTAL_BYTES = 4096
+
+
+def psgd_xent_total(loss: int, targets: int, tokens: int, ignore_index: int, mean: bool, total: int, workspace: int,
+                    workspace_bytes: int, stream: int = 0) -> None:
+    _check("psgd_xent_total", lib.psgd_xent_total(loss, targets, tokens, ignore_index, 1 if mean else 0, total, workspace,
+                                                  workspace_bytes, stream))
 
 
 def psgd_xent_scale(values: int, dtype: int, n: int, factor: int, out: int, stream: int = 0) -> None:

@@ -626,6 +626,22 @@ extern "C" psgd_status_t psgd_xent_train(const psgd_xent_t* args, void* ws, size
   return run_xent("psgd_xent_train", args, true, ws, bytes, stream);
 }
 
+static_assert(kXentTotalBytes == PSGD_XENT_TOTAL_BYTES, "the header's number");
+
+extern "C" psgd_status_t psgd_xent_total(const float* loss, const int64_t* targets, int64_t tokens, int64_t ignore_index,
+                                         int32_t mean, float* total, void* ws, size_t bytes, hipStream_t stream) {
+  clear_error();
+  const char* fn = "psgd_xent_total";
+  if (bad_dim(tokens)) return invalid(fn, "the number of tokens is negative or above INT32_MAX");
+  if (!total || (tokens && (!loss || (mean && !targets)))) return invalid(fn, "a required buffer is NULL");
+  if (misaligned(loss, 4) || misaligned(targets, 8) || misaligned(total, 4))
+    return invalid(fn, "a buffer is not aligned to its element type");
+  if (psgd_status_t s = check_workspace(fn, kXentTotalBytes, ws, bytes)) return s;
+  const Range r[] = {{total, 4}, {ws, kXentTotalBytes}, {loss, (size_t)tokens * 4}, {targets, mean ? (size_t)tokens * 8 : 0}};
+  if (outputs_overlap(r, 2)) return invalid(fn, "total or the workspace overlaps another buffer");
+  return launch_status(launch_xent_total(loss, targets, tokens, ignore_index, mean != 0, total, ws, stream), fn);
+}
+
 extern "C" psgd_status_t psgd_xent_scale(const void* in, int32_t dtype, int64_t n, const float* factor, void* out,
                                          hipStream_t stream) {
   clear_error();

@@ -47,6 +47,9 @@ struct XentLayout {
 };
 XentLayout xent_layout(const XentArgs& a, bool train);
 hipError_t launch_xent(const XentArgs& a, const XentLayout& l, bool train, void* ws, hipStream_t s);
+constexpr size_t kXentTotalBytes = 4096;  // of its workspace
+hipError_t launch_xent_total(const float* loss, const int64_t* targets, int64_t t, int64_t ignore, bool mean,
+                             float* total, void* ws, hipStream_t s);
 hipError_t launch_xent_scale(const void* in, int dtype, int64_t n, const float* factor, void* out, hipStream_t s);
 
 }  // namespace psgd

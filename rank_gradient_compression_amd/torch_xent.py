@@ -103,13 +103,14 @@ def cross_entropy_train(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     return loss, lse, dx, dw, dbias
 
 
-def _total(v: torch.Tensor) -> torch.Tensor:
-    """The sum, by blocks of 1024: one sum over more is split over workgroups that
-    meet in memory cleared by a copy engine's fill, which a captured graph must not
-    hold.  (Counts of fewer than 2^24 tokens are exact.)"""
-    while v.numel() > 1024:
-        v = torch.nn.functional.pad(v, (0, -v.numel() % 1024)).view(-1, 1024).sum(1)
-    return v.sum()
+def _total(loss: torch.Tensor, targets: torch.Tensor, mean: bool, ignore_index: int) -> torch.Tensor:
+    """The losses' sum or mean (psgd_xent_total)."""
+    out = torch.empty((), dtype=torch.float32, device=loss.device)
+    targets = targets.contiguous()
+    ws, ptr = _scratch(B.PSGD_XENT_TOTAL_BYTES, loss.device)
+    _call(loss.device, B.psgd_xent_total, loss.data_ptr(), targets.data_ptr(), loss.numel(), ignore_index, mean,
+          out.data_ptr(), ptr, B.PSGD_XENT_TOTAL_BYTES)
+    return out
 
 
 def _times(g: torch.Tensor, factor: torch.Tensor) -> torch.Tensor:
@@ -145,10 +146,7 @@ class _CrossEntropyFunction(torch.autograd.Function):
             loss, _, dx, dw, db = cross_entropy_train(xm, wm, y, b, reduction=reduction, ignore_index=ignore_index,
                                                       need_dx=need[0], need_dw=need[1], need_dbias=need[2])
             ctx.save_for_backward(dx, dw, db)
-        total = _total(loss)
-        if reduction == "mean":
-            total = total / _total(((y >= 0) & (y != ignore_index)).float()).clamp(min=1)
-        return total
+        return _total(loss, y, reduction == "mean", ignore_index)
 
     @staticmethod
     @torch.autograd.function.once_differentiable

@@ -50,3 +50,25 @@ def test_scale_refused(args, match):
     with pytest.raises(B.PsgdError, match=match) as e:
         B.psgd_xent_scale(*args)
     assert e.value.status == B.PSGD_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("args,match", [
+    ((MB, 2 * MB, -1, 0, True, 3 * MB), "tokens"), ((MB, 2 * MB, 1 << 31, 0, True, 3 * MB), "tokens"),
+    ((0, 2 * MB, 5, 0, True, 3 * MB), "NULL"), ((MB, 0, 5, 0, True, 3 * MB), "NULL"), ((MB, 0, 0, 0, True, 0), "NULL"),
+    ((MB + 2, 0, 5, 0, False, 3 * MB), "aligned"), ((MB, 2 * MB + 4, 5, 0, True, 3 * MB), "aligned"),
+    ((MB, 0, 5, 0, False, 3 * MB + 1), "aligned"), ((MB, 0, 5, 0, False, MB + 16), "overlaps"),
+    ((MB, 2 * MB, 5, 0, True, 2 * MB + 36), "overlaps"),
+])
+def test_total_refused(args, match):
+    with pytest.raises(B.PsgdError, match=match) as e:
+        B.psgd_xent_total(*args, 64 * MB, 4096)
+    assert e.value.status == B.PSGD_ERR_INVALID_ARG
+
+
+def test_total_workspace_refused():
+    for ws, n in ((0, 4096), (64 * MB + 128, 4096), (64 * MB, 4095)):
+        with pytest.raises(B.PsgdError, match="workspace") as e:
+            B.psgd_xent_total(MB, 2 * MB, 5, 0, True, 3 * MB, ws, n)
+        assert e.value.status == B.PSGD_ERR_WORKSPACE
+    with pytest.raises(B.PsgdError, match="overlaps"):
+        B.psgd_xent_total(MB, 2 * MB, 5, 0, True, 3 * MB, MB, 4096)

@@ -352,3 +352,21 @@ def test_scale_of_any_length_and_address(dtype):
         v = v.clone()
         X._call(DEV, B.psgd_xent_scale, v.data_ptr(), X._dtype(v), n, f.data_ptr(), v.data_ptr())
         assert ((v.double() - want).abs() <= half * want.abs() + (2.0 ** -25 if dtype == F16 else 0.0)).all()
+
+
+@pytest.mark.parametrize("t", [0, 1, 63, 1025, 65536, 65537, 300003])
+def test_total(t):
+    """fp64 sums of the losses as they are, rounded once."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(51)
+    loss = torch.rand(t, generator=g, device=DEV) * 20
+    y = torch.randint(-2, 6, (t,), generator=g, device=DEV)
+    n = int(((y >= 0) & (y != 4)).sum())
+    want = float(loss.double().sum())
+    for mean, value in ((True, want / max(1, n)), (False, want)):
+        got = X._total(loss, y, mean, 4)
+        assert got.shape == () and abs(float(got) - value) <= (2.0 ** -24 + t * 2.0 ** -53) * abs(value)
+    if t > 1:
+        assert torch.equal(X._total(loss, y.repeat_interleave(2)[::2], True, 4), X._total(loss, y, True, 4))
+        loss[t // 2] = float("nan")
+        assert torch.isnan(X._total(loss, y, False, 4))
