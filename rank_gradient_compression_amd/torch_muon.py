@@ -128,8 +128,13 @@ class Muon:
 
     def step(self, lr: Optional[float] = None) -> None:
         """One step (psgd_muon_step) with the gradients' present values; lr: from
-        this step on."""
+        this step on (where it raises, the handle keeps the one that it had)."""
+        kept = self.opts.lr
         if lr is not None:
             self.opts.lr = lr
         self._order()
-        _call(self.device, B.psgd_muon_step, self.table, self.opts, self._ws, self.ws_bytes)
+        try:
+            _call(self.device, B.psgd_muon_step, self.table, self.opts, self._ws, self.ws_bytes)
+        except B.PsgdError:
+            self.opts.lr = kept
+            raise
