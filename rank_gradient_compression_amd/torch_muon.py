@@ -12,7 +12,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from . import binding as B
-from .torch_ops import _call, _dtype, _matrix, _raw_stream, _result, _scratch
+from .torch_ops import _call, _dtype, _matrix, _raw_stream, _result, _scratch, _written
 
 _COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
@@ -40,6 +40,7 @@ def orthogonalize(x: torch.Tensor, out: Optional[torch.Tensor] = None, steps: in
     need = B.psgd_muon_workspace(t, opts)
     ws, ptr = _scratch(need, x.device)
     _call(x.device, B.psgd_muon_step, t, opts, ptr, need)
+    _written([out])
     return out
 
 
@@ -138,3 +139,4 @@ class Muon:
         except B.PsgdError:
             self.opts.lr = kept
             raise
+        _written(self.params)

@@ -55,6 +55,12 @@ def _train_workspace(m: int, n: int, k: int) -> int:
     return B.psgd_mx_train_workspace(m, n, k)
 
 
+def _written(tensors) -> None:
+    """Tensors of the caller's that a call of the library has written: a backward
+    pass that saved one of them raises, as behind an operation of PyTorch's."""
+    torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
+
+
 def _scratch(nbytes: int, device: torch.device):
     """(tensor, address) of nbytes of scratch; (None, 0) for none."""
     if nbytes == 0:

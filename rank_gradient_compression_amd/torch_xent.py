@@ -10,7 +10,7 @@ from typing import Optional
 import torch
 
 from . import binding as B
-from .torch_ops import _as_matrix, _call, _dtype, _matrix, _result, _scratch
+from .torch_ops import _as_matrix, _call, _dtype, _matrix, _result, _scratch, _written
 
 
 def _arguments(x, w, targets, bias, ignore_index: int):
@@ -100,6 +100,7 @@ def cross_entropy_train(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
     else:
         dbias = None
     _run(B.psgd_xent_train, a, True, device)
+    _written([g for g in (dw, dbias) if g is not None])
     return loss, lse, dx, dw, dbias
 
 
@@ -139,7 +140,7 @@ class _CrossEntropyFunction(torch.autograd.Function):
         if ctx.late or not any(need):
             loss, _ = cross_entropy(xm, wm, y, b, ignore_index)
             if any(need):
-                ctx.save_for_backward(xm, wm, b, y)
+                ctx.save_for_backward(x, w, bias, y)  # (the inputs themselves: what is written to them is noticed)
             if reduction == "none":
                 return loss.view(targets.shape)
         else:
@@ -153,11 +154,13 @@ class _CrossEntropyFunction(torch.autograd.Function):
     def backward(ctx, grad):
         need = ctx.needs_input_grad[:3]
         if ctx.late:
-            x, w, b, y = ctx.saved_tensors
+            x, w, bias, y = ctx.saved_tensors
+            b = None if bias is None else bias.contiguous()
             reduction = "mean" if ctx.reduction == "mean" else "sum"
-            _, _, dx, dw, db = cross_entropy_train(x, w, y, b, weights=grad.float().reshape(-1).expand(y.numel()),
-                                                   reduction=reduction, ignore_index=ctx.ignore_index, need_dx=need[0],
-                                                   need_dw=need[1], need_dbias=need[2])
+            weights = grad.float().reshape(-1).expand(y.numel())
+            _, _, dx, dw, db = cross_entropy_train(_as_matrix(x), _as_matrix(w), y, b, weights=weights, reduction=reduction,
+                                                   ignore_index=ctx.ignore_index, need_dx=need[0], need_dw=need[1],
+                                                   need_dbias=need[2])
         else:
             dx, dw, db = (None if g is None else _times(g, grad.float()) for g in ctx.saved_tensors)
         return None if dx is None else dx.view(ctx.x_shape), dw, db, None, None, None, None

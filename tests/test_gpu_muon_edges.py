@@ -26,3 +26,24 @@ def test_a_refused_learning_rate_is_not_kept(lr):
     opt.step()
     other.step()
     assert all(torch.equal(a, b) for a, b in zip(params + momentum, clean + m2))
+
+
+@pytest.mark.parametrize("shape", [(30, 16), (300, 64)])
+def test_a_step_between_forward_and_backward_is_noticed(shape):
+    """The loss "none" keeps the weights for its backward pass: with other weights than
+    it saw it would be of no loss at all."""
+    w = torch.randn(shape, device=DEV, requires_grad=True)
+    x, y = torch.randn(8, shape[1], device=DEV), torch.randint(0, shape[0], (8,), device=DEV)
+    opt = T.Muon([w.detach()], [torch.randn(shape, device=DEV)])
+    out = T.linear_cross_entropy(x, w, y, reduction="none")
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    out = T.linear_cross_entropy(x, w, y, reduction="none")
+    T.orthogonalize(w.detach(), out=w.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    T.linear_cross_entropy(x, w, y, reduction="none").sum().backward()
+    with torch.inference_mode():
+        p, g = torch.randn(shape, device=DEV), torch.randn(shape, device=DEV)
+        T.Muon([p], [g]).step()
