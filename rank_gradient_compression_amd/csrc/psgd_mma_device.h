@@ -4,13 +4,13 @@
 //
 // A workgroup computes a BM x BN tile of C = A B^T with WM x WN wavefronts, each
 // TM x TN tiles of 32 x 32 in accumulators, in chunks along the summed axis: 64
-// values of 16-bit matrices.  An fp32 matrix is held as two fp16 pieces, hi + lo
-// (22 bits of a value down to 2^-16 of the largest of the scale they share; 2^-38 of
-// that largest, half of fp16's smallest step, below), 32 upper pieces followed by the same values' lower ones (a line of 128 bytes); of such
-// matrices a chunk is 32 values, both pieces of both operands, and a product
-// hi lo + hi hi + lo hi.  (As three products one after
-// the other every piece is read one and a half times as often, and LDS reads
-// are what the smaller tiles wait for.)
+// values of 16-bit matrices.  An fp32 matrix is held as two fp16 pieces, hi + lo (22
+// bits of a value down to 2^-16 of the largest of the scale they share; an error of
+// 2^-38 of that largest, half of fp16's smallest step, below): 32 upper pieces
+// followed by the same values' lower ones (a line of 128 bytes); of such matrices a
+// chunk is 32 values, both pieces of both operands, and a product
+// hi lo + hi hi + lo hi.  (As three products one after the other every piece is read
+// one and a half times as often, and LDS reads are what the smaller tiles wait for.)
 //
 // Each operand's tile goes from memory straight into LDS (16 bytes per lane, no
 // registers), two stages, so the next chunk arrives while the matrix cores work
@@ -18,9 +18,9 @@
 //   K-contiguous  rows of the tile's axis, the summed axis along a row: 128
 //                 bytes of every row (and piece: 64) per chunk;
 //   K-strided     rows of the summed axis, the tile's axis along a row: 64 rows
-//                 (or 32 of each piece) of the tile's width per chunk, which the transposing LDS read
-//                 hands to the matrix cores in their own order.  So no operand
-//                 is ever transposed in memory.
+//                 (or 32 of each piece) of the tile's width per chunk, which the
+//                 transposing LDS read hands to the matrix cores in their own
+//                 order.  So no operand is ever transposed in memory.
 // The hardware writes LDS in lane order; each lane therefore *fetches* the 16
 // bytes that belong at its place.  Buffer descriptors end with the operand:
 // rows past it read as zero, without a fault.
@@ -74,8 +74,8 @@ __device__ __forceinline__ int mma_key(int row) { return ((row >> 1) + 6) & 7; }
 // lanes' groups g: four neighbouring rows and two neighbouring g stay apart.
 template <int UNITS>
 __device__ __forceinline__ int mma_tunit(int unit, int k) {
-  const int key = ((k & 3) | (k >> 2 & 4)) & (UNITS - 1);
-  return unit ^ (UNITS == 12 && unit >= 8 ? key & 3 : key);  // (of 12 units the last four among themselves)
+  static_assert((UNITS & (UNITS - 1)) == 0, "keys of whole powers of two");
+  return unit ^ (((k & 3) | (k >> 2 & 4)) & (UNITS - 1));
 }
 
 // One operand's side of the tile loop: R rows of the tile's axis, W wavefronts
