@@ -170,10 +170,14 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
                          reduction: str = "mean", ignore_index: int = -100) -> torch.Tensor:
     """The loss of x w^T + bias under autograd: x of any leading shape, targets of
     that shape, w vocab x dim, any strides (copied where their rows are not
-    contiguous).  reduction: "mean" over the tokens that are not ignored (0 where
-    all are), "sum", or "none" (a value per token)."""
+    contiguous), one type; under autocast all are taken in autocast's.  reduction:
+    "mean" over the tokens that are not ignored (0 where all are), "sum", or "none" (a
+    value per token)."""
     if reduction not in ("mean", "sum", "none"):
         raise ValueError('reduction must be "mean", "sum" or "none"')
     if targets.shape != x.shape[:-1]:
         raise ValueError(f"targets of shape {tuple(targets.shape)} for x of shape {tuple(x.shape)}")
+    if torch.is_autocast_enabled(x.device.type):
+        dtype = torch.get_autocast_dtype(x.device.type)
+        x, w, bias = x.to(dtype), w.to(dtype), None if bias is None else bias.to(dtype)
     return _CrossEntropyFunction.apply(x, w, bias, targets, reduction, ignore_index, torch.is_grad_enabled())

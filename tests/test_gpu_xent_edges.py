@@ -370,3 +370,22 @@ def test_total(t):
         assert torch.equal(X._total(loss, y.repeat_interleave(2)[::2], True, 4), X._total(loss, y, True, 4))
         loss[t // 2] = float("nan")
         assert torch.isnan(X._total(loss, y, False, 4))
+
+
+@pytest.mark.parametrize("low", [BF16, F16])
+def test_autocast(low):
+    """Under autocast the inputs are taken in its type, as by a linear layer: 16-bit
+    hidden states with a float32 head, gradients in each input's own type."""
+    x, w, y, b = inputs(60, 140, 40, F32, True, seed=52)
+    leaves = [x.to(low).requires_grad_(True), w.clone().requires_grad_(True), b.clone().requires_grad_(True)]
+    with torch.autocast("cuda", dtype=low):
+        out = T.linear_cross_entropy(leaves[0], leaves[1], y, leaves[2])
+    out.backward()
+    same = [v.detach().to(low).requires_grad_(True) for v in leaves]
+    want = T.linear_cross_entropy(same[0], same[1], y, same[2])
+    want.backward()
+    assert torch.equal(out, want)
+    for a, c in zip(leaves, same):
+        assert a.grad.dtype == a.dtype and torch.equal(a.grad, c.grad.to(a.dtype))
+    with torch.autocast("cuda", enabled=False), pytest.raises(ValueError):
+        T.linear_cross_entropy(leaves[0], leaves[1], y)
