@@ -47,3 +47,17 @@ def test_a_step_between_forward_and_backward_is_noticed(shape):
     with torch.inference_mode():
         p, g = torch.randn(shape, device=DEV), torch.randn(shape, device=DEV)
         T.Muon([p], [g]).step()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_not_finite_stays_in_its_large_matrix(dtype):
+    """One value that is not finite, in matrices of several tiles: all of its matrix's
+    update is NaN and nothing of the others'."""
+    shapes = [(200, 330), (330, 200), (70, 300), (300, 70)]
+    params, grads, momentum = step_case(shapes, dtype, seed=110)
+    clean, m2 = [p.clone() for p in params], [m.clone() for m in momentum]
+    T.Muon(clean, grads, momentum_buffers=m2).step()
+    grads[1][329, 0], grads[2][3, 4] = float("nan"), float("-inf")
+    T.Muon(params, grads, momentum_buffers=momentum).step()
+    assert torch.equal(params[0], clean[0]) and torch.equal(params[3], clean[3])
+    assert torch.isnan(params[1]).all() and torch.isnan(params[2]).all()
