@@ -604,10 +604,12 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
  *                     dbias, vocab values of type `dtype`.  With `accumulate`
  *                     dw and dbias are added to what is there.
  *
- * Precision: products are summed in fp32.  16-bit tensors: probabilities and G
- * have one rounding each to 16 bits (fp16, then `dtype`) before the gradients'
- * products; a probability below 2^-40 of the largest of its 64 (of at most 32
- * tokens: 32) neighbours in the vocabulary is taken for 0 there.  A row of G is held
+ * Precision: products are summed in fp32.  16-bit tensors, more than 32 tokens:
+ * probabilities and G have one rounding each to 16 bits (fp16, then `dtype`) before
+ * the gradients' products, which leaves gradients 1.05 to 1.25 times as inexact as
+ * their own rounding does; a probability below 2^-40 of the largest of its 64
+ * neighbours in the vocabulary is taken for 0 there.  Up to 32 tokens probabilities
+ * are fp32 and G is a sum of two values of `dtype`.  A row of G is held
  * times a power of two that brings its token's weight to the type's upper range, so
  * that small weights keep their digits in dx; in dw the token's row of x takes the
  * power back relative to the largest weight's, and what falls below fp16's 2^-24 so

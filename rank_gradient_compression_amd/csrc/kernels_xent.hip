@@ -7,17 +7,16 @@
 //
 // The vocabulary is taken in pieces: a tile of the product x w^T ends with its
 // rows' maximum m and sum of exp(l - m) over each segment of columns, and the
-// logits are gone.  Training keeps E = exp(l - m), at most 1, in 16 bits (fp32
-// tensors: 32) for a block of tokens whatever the batch, from which one
+// logits are gone.  Training keeps E = exp(l - m), at most 1, in 16 or 32 bits for a block of tokens whatever the batch, from which one
 // pass over the block makes G once the rows' sums are known.  That is three
 // products of T x V x D in all; forming the logits again for the gradients
 // instead of keeping E would be a fourth (a third more of the time), the pass
 // over E and G is 4 bytes a value (4% of it at D = 4096: 0.11 of 2.6 ms at
 // 4096 x 32000 x 4096 bf16, the products 0.93, 0.83 and 0.89 ms).
-// E is held times 2^15 in fp16: a relative error of 2^-11 down to 2^-29 of its
+// E is fp32 for fp32 tensors and few tokens, else held times 2^15 in fp16: a relative error of 2^-11 down to 2^-29 of its
 // segment's largest (20 nats below), 2^-40 of that largest under it, and nothing of
 // what is below 2^-40 (28 nats; held as it is, 17).  G is rounded once to the type
-// that the products take; the target's entry, which would cancel, is formed
+// that the products take (of few tokens it has two pieces of it); the target's entry, which would cancel, is formed
 // from the loss, exp(-loss) - 1, instead.  Sums, maxima and products are fp32.  A
 // row's largest logit M and its S = sum exp(l - M) are kept apart for loss =
 // log S - (l_y - M) and p = exp(l - M) / S: lse, rounded at its full size, would
@@ -49,6 +48,7 @@ namespace psgd {
 // kEdb.)
 enum { kSx, kSw, kEw, kEg, kS, kEdx, kEdw, kEdb, kScalars };
 
+constexpr int64_t kFewTokens = 32;  // of few tokens: a stream of the weights, one block
 constexpr int kMaxGroups = 1024;    // workgroups that look for a tensor's largest value
 constexpr int64_t kBlockBytes = int64_t(1) << 30;  // of E (and G) at a time, or of segments' sums without gradients
 constexpr int64_t kBlockTokens = int64_t(1) << 23;  // (a launch holds 2^32 threads)
@@ -477,7 +477,7 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int DT, bool PAIR, int KEEP, int MT, int WAVES>
+template <int DT, bool PAIR, bool KEEP, int MT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, 1) void k_xent_logits_few(XentTile p) {
   constexpr int HB = 2;
   using LW = MmaLoad<PAIR, true, 32, 1>;
@@ -574,13 +574,7 @@ __global__ __launch_bounds__(WAVES * 64, 1) void k_xent_logits_few(XentTile p) {
     float ex[HB * 4];
     xent_row<PAIR, HB>(p, row, col0, g, v, bias, xent_shift<PAIR>(p, row), row < p.t ? p.targets[row] : -1, ex);
     if (row >= p.t) continue;
-    if constexpr (KEEP == 1) {
-      uint16_t* e = static_cast<uint16_t*>(p.e) + row * p.vp + col0 + 4 * g;
-#pragma unroll
-      for (int j = 0; j < HB; ++j)
-        *reinterpret_cast<uint2*>(e + j * 16) =
-            make_uint2(held_halves(ex[4 * j], ex[4 * j + 1]), held_halves(ex[4 * j + 2], ex[4 * j + 3]));
-    } else if constexpr (KEEP == 2) {
+    if constexpr (KEEP) {
       float* e = static_cast<float*>(p.e) + row * p.vp + col0 + 4 * g;
 #pragma unroll
       for (int j = 0; j < HB; ++j)
@@ -641,7 +635,7 @@ struct XentGrad {
   const int64_t* targets;
   int64_t ignore;
   void* e;       // fp16 (G in its place) or fp32
-  uint16_t* g;   // G, or its two pieces
+  uint16_t* g;   // G, or its two pieces; of few tokens' the lower ones kFewTokens rows on
   float* db;     // partial sums, or null
 };
 
@@ -649,7 +643,7 @@ struct XentGrad {
 // next readings under way while one is worked on.  A workgroup's columns' sums go to
 // its row of db.  Bound by HBM: 4096 x 32000 in 16 bits 111 us, 4.9 TB/s; 700 x 33278
 // from fp32 to two pieces 47 us, 4.0 TB/s.
-template <int DT>  // of G: kF16 and kBF16 in E's place, kF32 as two pieces
+template <int DT, bool FEW>  // of G: kF16 and kBF16 in E's place, kF32 as two pieces; FEW: two pieces of a 16-bit type
 __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
   const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8, t0 = (int64_t)blockIdx.x * p.rows;
   if (c >= p.vp) return;
@@ -665,7 +659,7 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
     const int64_t row = t0 + i, at = row * p.vp + c, y = p.targets[row];
     const bool off = ignored(y, p.ignore) || y >= p.v || (p.weights && p.weights[row] == 0.f);
     float v[8];
-    if constexpr (DT == kF32) {
+    if constexpr (DT == kF32 || FEW) {
       __builtin_memcpy(v, static_cast<const float*>(p.e) + at, sizeof v);
     } else {
       uint16_t h[8];
@@ -678,7 +672,7 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
     const float back = ldexpf(1.f, less), u = p.weights ? ldexpf(p.weights[row], most - less) : gs;
     const float2 sum = p.sums[row];
     const float f = u * (__builtin_amdgcn_exp2f((p.stats[row * p.nseg + seg].x - sum.x) * kLog2e) * sum.y) *
-                    (DT == kF32 ? 1.f : 1.f / kHeld);
+                    (DT == kF32 || FEW ? 1.f : 1.f / kHeld);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = off || c + e >= p.v ? 0.f : v[e] * f;
     if (!off && y >= c && y < c + 8) {
@@ -690,16 +684,18 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[e] = fmaf(v[e], back, sums[e]);
     uint16_t h[8];
-    if constexpr (DT == kF32) {
+    if constexpr (DT == kF32 || FEW) {
+      constexpr int T = DT == kF32 ? kF16 : DT;
       uint16_t lo[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        h[e] = Elem<kF16>::down(v[e]);
-        const float r = v[e] - Elem<kF16>::up(h[e]);
-        lo[e] = Elem<kF16>::down(r == r ? r : 0.f);
+        h[e] = Elem<T>::down(v[e]);
+        const float r = v[e] - Elem<T>::up(h[e]);
+        lo[e] = Elem<T>::down(r == r ? r : 0.f);
       }
-      __builtin_memcpy(p.g + row * 2 * p.vp + mma_piece(c), h, sizeof h);
-      __builtin_memcpy(p.g + row * 2 * p.vp + mma_piece(c) + kMmaLow, lo, sizeof lo);
+      uint16_t* const g = FEW ? p.g + at : p.g + row * 2 * p.vp + mma_piece(c);
+      __builtin_memcpy(g, h, sizeof h);
+      __builtin_memcpy(g + (FEW ? kFewTokens * p.vp : kMmaLow), lo, sizeof lo);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] = Elem<DT>::down(v[e]);
@@ -740,6 +736,7 @@ struct XentProduct {
   MmaOut out;
   int64_t split_stride;  // elements between the results of two pieces of the summed axis
   int pieces;            // of them
+  int64_t low;           // elements from a's rows to their lower pieces, kFewTokens rows on, 0: none
 };
 
 // dx (G's rows K-contiguous) and dw (K-strided).  4096 x 32000 x 4096 bf16: dx 0.78 -
@@ -769,6 +766,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_xent_product(XentProduct p,
   const uint32_t c1 = (uint32_t)((uint64_t)total * (piece + 1) / p.pieces);
   typename Tile::Acc acc;
   Tile::run(p.a, p.b, p.k, c0, c1, m0, n0, a0, b0, a1, b1, acc);
+  if (AKC && !PAIR && p.low) {  // (few tokens: rows 32 on are the lower pieces of the first ones)
+    static_assert(Tile::HA >= 4 && kFewTokens == 32, "both pieces' rows in one wavefront");
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < Tile::HB; ++j) acc[i][j] += acc[i + 2][j];
+  }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float* lds = mma_epilogue_lds<Tile>(wave, a0, b0, a1, b1);
   p.out.c = static_cast<typename Elem<ODT>::type*>(p.out.c) + piece * p.split_stride;
@@ -811,9 +815,11 @@ __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
   const int64_t m0 = (int64_t)(t / ntn) * 128 + wave / 2 * 64, n0 = (int64_t)(t % ntn) * 128 + wave % 2 * 64;
   if (m0 >= p.out.m || n0 >= p.out.n) return;
   constexpr int N = PAIR ? 2 : 1;
-  uint4 a[N][4], b[N][4];
+  uint4 a[2][4], b[N][4];
 #pragma unroll
   for (int n = 0; n < N; ++n) outer_read<PAIR>(p.a, p.k, m0, n, a[n]), outer_read<PAIR>(p.b, p.k, n0, n, b[n]);
+  const bool low = !PAIR && p.low != 0;
+  if (low) outer_read<false>(MmaSide{p.a.p + p.low, p.a.ld, p.a.len}, p.k, m0, 0, a[1]);
   const float alpha = p.sc[kS];
   const int exponent = (int)p.sc[p.exponent];
   v4f acc[4][4];
@@ -824,8 +830,9 @@ __global__ __launch_bounds__(256) void k_xent_outer(XentProduct p, int ntn) {
       acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
       if constexpr (PAIR) {
         acc[i][j] = mma16<DT>(b[N - 1][j], a[0][i], acc[i][j]);
-        acc[i][j] = mma16<DT>(b[0][j], a[N - 1][i], acc[i][j]);
+        acc[i][j] = mma16<DT>(b[0][j], a[1][i], acc[i][j]);
       }
+      if (low) acc[i][j] = mma16<DT>(b[0][j], a[1][i], acc[i][j]);
       acc[i][j] = mma16<DT>(b[0][j], a[0][i], acc[i][j]);
     }
 #pragma unroll
@@ -865,11 +872,13 @@ __global__ __launch_bounds__(kOuterThreads) void k_xent_outer_rows(XentProduct p
   constexpr int N = PAIR ? 2 : 1;
   const float alpha = p.sc[kS];
   const int exponent = (int)p.sc[p.exponent];
-  uint4 a[N][2];
+  const bool low = !PAIR && p.low != 0;
+  uint4 a[2][2];
 #pragma unroll
-  for (int h = 0; h < N; ++h) {
+  for (int h = 0; h < 2; ++h) {
+    if (!PAIR && h == 1 && !low) break;
     const int64_t c = m0 + 2 * r;  // (rows are padded to 64 values)
-    const uint16_t* q = p.a.p + (PAIR ? mma_piece(c) + h * kMmaLow : c);
+    const uint16_t* q = p.a.p + (PAIR ? mma_piece(c) + h * kMmaLow : c + h * p.low);
     uint32_t x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = *reinterpret_cast<const uint32_t*>(q + min((int64_t)8 * g + e, p.k - 1) * p.a.ld);
@@ -895,8 +904,9 @@ __global__ __launch_bounds__(kOuterThreads) void k_xent_outer_rows(XentProduct p
         acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
         if constexpr (PAIR) {
           acc[j] = mma16<DT>(b[N - 1][j], a[0][i], acc[j]);
-          acc[j] = mma16<DT>(b[0][j], a[N - 1][i], acc[j]);
+          acc[j] = mma16<DT>(b[0][j], a[1][i], acc[j]);
         }
+        if (low) acc[j] = mma16<DT>(b[0][j], a[1][i], acc[j]);
         acc[j] = mma16<DT>(b[0][j], a[0][i], acc[j]);
       }
       const int row = 2 * r + i;
@@ -1012,7 +1022,13 @@ static bool readable(const void* p, int64_t ld, int64_t d, int dtype) {
   return dtype != kF32 && ((uintptr_t)p & 15) == 0 && ld % 8 == 0 && d % 8 == 0;
 }
 
-constexpr int64_t kFewTokens = 32;
+// Of few tokens of a 16-bit type G has two pieces, from an E in fp32: single
+// entries of G (the target's) dominate a sum over few, whose rounding to the type
+// made the gradients of one or two tokens up to 1.7 times as inexact as their own
+// rounding does (over many tokens 1.05 to 1.25 times, which two pieces would cost a
+// second product each for).  Here they cost no more than the second piece's rows, in
+// tiles that are mostly empty: 20 x 33278 x 650 fp16 81 us a call, 80 with one.
+static bool few_pieces(const XentArgs& a) { return a.dtype != kF32 && a.t <= kFewTokens; }
 
 // Tokens of a workgroup of the pass over E: fewer where that leaves too few of them.
 static int64_t grad_rows(int64_t tokens, int64_t vp) {
@@ -1051,10 +1067,11 @@ XentLayout xent_layout(const XentArgs& a, bool train) {
   l.w = take(l.pack_w ? (size_t)l.parts * a.v * l.dp * 2 : 0);
   l.stats = take((size_t)l.block * l.nseg * sizeof(float2));
   l.target = take((size_t)l.block * sizeof(float));
+  const bool few = few_pieces(a);
   if (train) {
     l.sums = take((size_t)l.block * sizeof(float2));
-    l.e = take((size_t)l.block * l.vp * (f32 ? 4 : 2));
-    l.g = f32 ? take((size_t)l.block * l.vp * 4) : l.e;
+    l.e = take((size_t)l.block * l.vp * (f32 || few ? 4 : 2));
+    l.g = f32 ? take((size_t)l.block * l.vp * 4) : few ? take((size_t)2 * kFewTokens * l.vp * 2) : l.e;
     l.db = take(a.dbias ? (size_t)cdiv(l.block, grad_rows(l.block, l.vp)) * l.vp * sizeof(float) : 0);
     l.dbs = take(a.dbias && l.block < a.t ? (size_t)a.v * sizeof(float) : 0);
     l.dxp = take(a.dx && l.dx_splits > 1 ? (size_t)l.dx_splits * l.block * a.d * sizeof(float) : 0);
@@ -1092,7 +1109,7 @@ static void pack(const XentPack& w, const XentPack& x, int dtype, hipStream_t s)
     hipLaunchKernelGGL((k_xent_pack<kF16>), dim3(all), dim3(256), 0, s, w, x, first);
 }
 
-template <int DT, bool PAIR, int KEEP>
+template <int DT, bool PAIR, bool TRAIN>
 static void logits(const XentTile& p, int64_t tokens, hipStream_t s) {
   if (tokens <= kFewTokens) {
     // (four wavefronts, five workgroups to a compute unit, where eight would have
@@ -1100,15 +1117,16 @@ static void logits(const XentTile& p, int64_t tokens, hipStream_t s) {
     const dim3 g((unsigned)cdiv(p.v, 32));
     const bool brief = p.d <= 16 * kMmaK<PAIR>;
     if (p.t <= 16 && brief)
-      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 1, 4>), g, dim3(256), 0, s, p);
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, TRAIN, 1, 4>), g, dim3(256), 0, s, p);
     else if (p.t <= 16)
-      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 1, 8>), g, dim3(512), 0, s, p);
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, TRAIN, 1, 8>), g, dim3(512), 0, s, p);
     else if (brief)
-      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 2, 4>), g, dim3(256), 0, s, p);
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, TRAIN, 2, 4>), g, dim3(256), 0, s, p);
     else
-      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, KEEP, 2, 8>), g, dim3(512), 0, s, p);
+      hipLaunchKernelGGL((k_xent_logits_few<DT, PAIR, TRAIN, 2, 8>), g, dim3(512), 0, s, p);
     return;
   }
+  constexpr int KEEP = !TRAIN ? 0 : PAIR ? 2 : 1;
   if (cdiv(p.t, 256) * cdiv(p.v, 256) >= 256) {
     const int ntm = (int)cdiv(p.t, 256), ntn = (int)cdiv(p.v, 256);
     hipLaunchKernelGGL((k_xent_logits<DT, PAIR, KEEP, 2, 4, 4, 2>), dim3(ntm * ntn), dim3(512), 0, s, p, ntm, ntn);
@@ -1154,7 +1172,7 @@ static void product(const XentProduct& p, int odt, int64_t pieces, hipStream_t s
 // DT: what the products take; PAIR: two pieces of it for a value.
 template <int DT, bool PAIR>
 static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* ws, int64_t t0, hipStream_t s) {
-  constexpr int KEEP = PAIR ? 2 : 1, PIECES = PAIR ? 2 : 1;
+  constexpr int PIECES = PAIR ? 2 : 1;
   const int64_t n = std::min(l.block, a.t - t0), pitch = PIECES * l.dp;
   const float* sc = reinterpret_cast<const float*>(ws + l.scalars);
   uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
@@ -1168,9 +1186,9 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   p.t = n, p.v = a.v, p.d = a.d, p.sc = sc, p.exponents = reinterpret_cast<const int*>(ws + l.xrow) + t0, p.bias = a.bias, p.bias_dtype = a.dtype;
   p.targets = a.targets + t0, p.stats = stats, p.nseg = l.nseg, p.target = target, p.e = ws + l.e, p.vp = l.vp;
   if (train)
-    logits<DT, PAIR, KEEP>(p, a.t, s);
+    logits<DT, PAIR, true>(p, a.t, s);
   else
-    logits<DT, PAIR, 0>(p, a.t, s);
+    logits<DT, PAIR, false>(p, a.t, s);
   const bool scalars = train && !PAIR && !a.weights && t0 == 0;
   float2* const sums = train ? reinterpret_cast<float2*>(ws + l.sums) : nullptr;
   hipLaunchKernelGGL(k_xent_lse, dim3((unsigned)n + (scalars ? 1 : 0)), dim3(256), 0, s, a,
@@ -1185,14 +1203,20 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
   const XentGrad q{n,       a.v, l.vp,           l.nseg,   l.seg_shift, rows, stats, sums, a.loss + t0,
                    a.weights ? a.weights + t0 : nullptr, sc, factors, a.targets + t0, a.ignore, ws + l.e, g,
                    a.dbias ? db : nullptr};
-  hipLaunchKernelGGL((k_xent_grad<PAIR ? kF32 : DT>), dim3((unsigned)parts, (unsigned)cdiv(l.vp, 2048)), dim3(256),
-                     0, s, q);
+  const bool few = few_pieces(a);
+  const int64_t low = few ? kFewTokens * l.vp : 0;
+  const dim3 gg((unsigned)parts, (unsigned)cdiv(l.vp, 2048));
+  if (few)
+    hipLaunchKernelGGL((k_xent_grad<DT, !PAIR>), gg, dim3(256), 0, s, q);
+  else
+    hipLaunchKernelGGL((k_xent_grad<PAIR ? kF32 : DT, false>), gg, dim3(256), 0, s, q);
   if (a.dbias)
     hipLaunchKernelGGL(k_xent_db, dim3(grid(a.v)), dim3(256), 0, s, db, parts, l.vp, a.v, sc,
                        reinterpret_cast<float*>(ws + l.dbs), t0 == 0, t0 + n == a.t, a.dbias, a.dtype, a.accumulate);
   if (a.dx) {
     XentProduct d{};
-    d.a = MmaSide{g, PIECES * l.vp, n};
+    d.a = MmaSide{g, PIECES * l.vp, few ? 2 * kFewTokens : n};  // (rows in between are anything, and so are their sums)
+    d.low = low;
     d.b = p.w;
     d.b.len = a.d;
     d.k = a.v;
@@ -1215,7 +1239,7 @@ static void block(const XentArgs& a, const XentLayout& l, bool train, uint8_t* w
     XentProduct d{};
     d.a = MmaSide{g, PIECES * l.vp, a.v};
     d.b = MmaSide{px + (l.pack_x ? a.t * pitch : 0) + t0 * pitch, pitch, a.d};
-    d.k = n, d.sc = sc, d.exponent = kEdw;
+    d.k = n, d.sc = sc, d.exponent = kEdw, d.low = low;
     // Blocks before the last add up in fp32: in dw itself, or in memory of
     // their own where dw has fewer bits.
     const bool last = t0 + n == a.t, wide = a.dw_dtype == kF32;

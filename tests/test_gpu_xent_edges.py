@@ -389,3 +389,37 @@ def test_autocast(low):
         assert a.grad.dtype == a.dtype and torch.equal(a.grad, c.grad.to(a.dtype))
     with torch.autocast("cuda", enabled=False), pytest.raises(ValueError):
         T.linear_cross_entropy(leaves[0], leaves[1], y)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("t", [1, 2, 15, 16, 17, 32])
+@pytest.mark.parametrize("v,d", [(300, 40), (1000, 650), (90, 64)])
+def test_gradients_of_few_tokens_are_rounded_once(t, v, d, dtype):
+    """Up to 32 tokens of a 16-bit type: half a step of dx, dw and dbias, and before it
+    fp32's roundings and G's as two values of the type (bf16 2^-16; fp16 2^-21, and
+    2^-38 of the token's weight)."""
+    x, w, y, b = inputs(t, v, d, dtype, True, seed=53, ignored=0.0)
+    u = torch.linspace(0.3, 3.0, t, device=DEV)
+    xd, wd = x.double(), w.double()
+    l = xd @ wd.t() + b.double()
+    size = xd.abs() @ wd.abs().t() + b.double().abs()
+    p = torch.softmax(l, 1)
+    g = u.double()[:, None] * (p - torch.nn.functional.one_hot(y, v))
+    dl = ((d / 16 + 16) * U) * size
+    e = u.double()[:, None] * p * (dl + dl.max(1, keepdim=True).values + 2.0 ** -18)
+    e = e + g.abs() * (2.0 ** -16 if dtype == BF16 else 2.0 ** -21) + (u.double()[:, None] * 2.0 ** -38 if dtype == F16 else 0.0)
+    # (dw: a token's row of x under its weight's power of two, up to 2^-4 here, in fp16)
+    small = 2.0 ** -25 * 16 * float(u.max()) * t if dtype == F16 else 0.0
+    say(f"[xent] {t} tokens once rounded, {v} x {d} {dtype}")
+    for weights in (u, None):
+        if weights is None:
+            g, e, small = g / u.double()[:, None], e / u.double()[:, None], 0.0
+        dx, dw, db = T.cross_entropy_train(x, w, y, b, weights=weights, reduction="sum")[2:]
+        many = (v / 16 + 160) * U
+        for name, got, want, tol in (("dx", dx, g @ wd, e @ wd.abs() + many * (g.abs() @ wd.abs())),
+                                     ("dw", dw, g.t() @ xd, e.t() @ xd.abs() + many * (g.abs().t() @ xd.abs()) + small),
+                                     ("db", db, g.sum(0), e.sum(0) + many * g.abs().sum(0))):
+            close(name, got, want, tol + half_step(want.abs() + tol, dtype) + (2.0 ** -25 if dtype == F16 else 0.0))
+        half = T.cross_entropy_train(x, w, y, b, weights=weights, reduction="sum", dw=torch.ones(v, d, device=DEV), accumulate=True,
+                                     dbias=torch.zeros_like(b))[3]
+        close("dw on top", half, 1 + g.t() @ xd, e.t() @ xd.abs() + many * (g.abs().t() @ xd.abs()) + small + 2.0 ** -23)
