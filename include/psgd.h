@@ -711,9 +711,12 @@ psgd_status_t psgd_xent_scale(const void* in, int32_t dtype, int64_t n, const fl
  *                  and param NaN.
  *
  * Precision (opts.pieces): 1 takes the products on one fp16 value per entry of
- * X, A and B, with a X from two (about 2e-3 of the update, relative norm, what
- * bfloat16 has to give), 2 on two (about 1e-6; three products for one), 0
- * chooses per matrix: 1 where what is written is bfloat16, else 2.  Entries of
+ * X, A and B, with a X from two (about 7e-4 of the update, relative norm, beside the
+ * 1.7e-3 of bfloat16's own rounding; more where few singular values share it: 2.5e-3
+ * where a side is 17), 2 on two (about 1e-6; three products for one), 0 chooses per
+ * matrix: 1 where what is written is bfloat16 and both sides are above 48 (and the
+ * list's others do not make two pieces cheaper), else 2.
+ * Entries of
  * the first X below 2^-39 vanish: a gradient whose norm is far below eps has no
  * update.  Sums of
  * squares are fp64, products are summed in fp32, in orders that depend on the

@@ -691,14 +691,21 @@ static psgd_status_t check_muon(const char* fn, int32_t n, const psgd_muon_tenso
     const int64_t k = std::min(x.rows, x.cols), l = std::max(x.rows, x.cols), tiles = (k / 128 + 1) * (l / 128 + 1);
     if (tiles * (k / 32 + 1) > INT32_MAX || (k / 128 + 1) * (k / 128 + 1) * (l / 32 + 1) > INT32_MAX)
       return invalid(fn, "a matrix is too large");
-    const bool one = (!x.param || x.param_dtype == kBF16) && (!x.update || x.update_dtype == kBF16);
+    const bool one = (!x.param || x.param_dtype == kBF16) && (!x.update || x.update_dtype == kBF16) && k > kMuonThin;
     const int pieces = o->pieces ? o->pieces : one ? 1 : 2;
     out->push_back(MuonTensor{x.grad, x.momentum, x.param, x.update, x.rows > 1 ? x.ldg : x.cols,
                               x.rows > 1 ? x.ldp : x.cols, x.rows > 1 ? x.ldu : x.cols, x.rows, x.cols,
                               o->lr * x.lr_scale, x.grad_dtype, x.param ? x.param_dtype : kF32,
                               x.update ? x.update_dtype : kF32, pieces});
   }
-  // (a group of matrices has as many pieces throughout)
+  // (a group of matrices has as many pieces throughout: a little work on one piece
+  // joins the rest, which costs less than launches of its own)
+  double work = 0.0;
+  for (const MuonTensor& x : *out)
+    if (x.pieces == 1) work += 4.0 * o->steps * (double)std::min(x.r, x.c) * (double)(x.r * x.c);
+  const bool two = std::any_of(out->begin(), out->end(), [](const MuonTensor& x) { return x.pieces == 2; });
+  if (two && work <= kMuonJoined)
+    for (MuonTensor& x : *out) x.pieces = 2;
   std::stable_sort(out->begin(), out->end(), [](const MuonTensor& x, const MuonTensor& y) { return x.pieces < y.pieces; });
   return PSGD_OK;
 }

@@ -19,8 +19,8 @@
 // the small singular values from step to step, is formed from both pieces: with
 // X itself in 16 bits, what rounding adds under large singular values grows by a
 // a step with the small ones (512 x 512, rank 16 over noise of 1/20: 6e-3 off
-// with fp16 X, 5e-2 with bfloat16, 1.5e-4 so; Gaussian: 1.5e-3).  Other results
-// take two pieces of everything, three products for one.  In the last two steps,
+// with fp16 X, 5e-2 with bfloat16, 1.5e-4 so; Gaussian: 1.5e-3).  Other results, and
+// thin matrices' (kMuonThin), take two pieces of everything, three products for one.  In the last two steps,
 // where singular values are near 1 and B near b + c, the identity's part of a X
 // that cancels against B's goes into B instead, whose roundings are then of what
 // is left: X <- (a + b + c) X + (B - (b + c) I) X (Gaussian: 1.7e-3 -> 1.0e-3;
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(256) void k_muon_apply(MuonArgs p) {
 }
 
 // ------------------------------------------------------- matrices in one piece
-// Where every matrix of a call is so small, a workgroup takes one whole: X (the
+// Where every matrix of a call, or of a group, is so small, a workgroup takes one whole: X (the
 // shorter side down), A and B in LDS in fp32, products on the fp32 matrix
 // instruction.  One launch for everything instead of eighteen: a 64 x 27 matrix 15
 // us, 100 by those.  Bound by the chain of the steps' products and barriers.
@@ -893,10 +893,12 @@ static MuonGroup make_group(const std::vector<MuonTensor>& t, int first) {
   return g;
 }
 
-static bool all_tiny(const std::vector<MuonTensor>& t) {
-  return std::all_of(t.begin(), t.end(), [](const MuonTensor& x) {
-    return std::min(x.r, x.c) <= kTinyShort && std::max(x.r, x.c) <= kTinyLong;
-  });
+static bool tiny(const MuonTensor& x) {
+  return std::min(x.r, x.c) <= kTinyShort && std::max(x.r, x.c) <= kTinyLong;
+}
+static bool all_tiny(const std::vector<MuonTensor>& t) { return std::all_of(t.begin(), t.end(), tiny); }
+static bool all_tiny(const std::vector<MuonTensor>& t, const MuonGroup& g) {
+  return std::all_of(g.order.begin(), g.order.end(), [&](int i) { return tiny(t[(size_t)i]); });
 }
 
 size_t muon_workspace(const std::vector<MuonTensor>& t) {
@@ -904,7 +906,7 @@ size_t muon_workspace(const std::vector<MuonTensor>& t) {
   if (all_tiny(t)) return bytes;
   for (int i = 0; i < (int)t.size();) {
     const MuonGroup g = make_group(t, i);
-    bytes = std::max(bytes, g.bytes);
+    if (!all_tiny(t, g)) bytes = std::max(bytes, g.bytes);
     i += g.n;
   }
   return bytes;
@@ -954,21 +956,30 @@ static bool whole_vectors(const std::vector<MuonTensor>& t, const MuonGroup& g) 
   });
 }
 
+// `n` matrices from `first` on, a workgroup each.
+static void launch_tiny(const std::vector<MuonTensor>& t, size_t first, size_t n, const MuonOpts& o, hipStream_t s) {
+  MuonTiny p{};
+  p.n = (int32_t)n;
+  for (int i = 0; i < p.n; ++i) describe(t[first + (size_t)i], &p.mat[i]);
+  p.mu = o.mu, p.decay = o.decay, p.a = o.a, p.b = o.b, p.c = o.c, p.eps = o.eps, p.steps = o.steps;
+  p.nesterov = o.nesterov;
+  hipLaunchKernelGGL(k_muon_tiny, dim3((unsigned)p.n), dim3(512), 0, s, p);
+}
+
 hipError_t launch_muon(const std::vector<MuonTensor>& t, const MuonOpts& o, void* workspace, hipStream_t s) {
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   if (all_tiny(t)) {
-    for (size_t first = 0; first < t.size(); first += kMuonGroup) {
-      MuonTiny p{};
-      p.n = (int32_t)std::min<size_t>(kMuonGroup, t.size() - first);
-      for (int i = 0; i < p.n; ++i) describe(t[first + (size_t)i], &p.mat[i]);
-      p.mu = o.mu, p.decay = o.decay, p.a = o.a, p.b = o.b, p.c = o.c, p.eps = o.eps, p.steps = o.steps;
-      p.nesterov = o.nesterov;
-      hipLaunchKernelGGL(k_muon_tiny, dim3((unsigned)p.n), dim3(512), 0, s, p);
-    }
+    for (size_t first = 0; first < t.size(); first += kMuonGroup)
+      launch_tiny(t, first, std::min<size_t>(kMuonGroup, t.size() - first), o, s);
     return hipGetLastError();
   }
   for (int first = 0; first < (int)t.size();) {
     const MuonGroup g = make_group(t, first);
+    if (all_tiny(t, g)) {
+      launch_tiny(t, (size_t)first, (size_t)g.n, o, s);
+      first += g.n;
+      continue;
+    }
     MuonTable* const table = reinterpret_cast<MuonTable*>(ws);
     MuonTable m{};
     for (int k = 0; k < kMuonKinds; ++k)

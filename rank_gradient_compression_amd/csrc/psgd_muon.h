@@ -13,6 +13,16 @@ namespace psgd {
 // The kernels of a step, each with ranges of its own over a group's matrices.
 enum { kNorm, kStart, kGram, kPoly, kUpdate, kMuonKinds, kLast = kMuonKinds };
 
+// Matrices whose shorter side is at most this take two pieces for bfloat16 results
+// too: the roundings of one, which many singular values share out, fall on few (one
+// piece left 17 x 650 1.8 times as far off as bfloat16's own rounding does, 33 x 650
+// 1.4, 48 x 650 1.3, 97 x 650 1.25 times).  64 of 16 x 4096 take 745 us so, with one
+// piece 629; 48 x 2600 149, with one 166.
+constexpr int kMuonThin = 48;
+// Operations of a list's matrices of one piece, up to which they take two beside
+// others of two: with two of 27 x 512, three of 1152 x 256 (4.5e9) 225 us so, in
+// groups of their own 281; two of 1024 x 1024 (43e9) 388 and 389, four 469 and 435.
+constexpr double kMuonJoined = 40e9;
 constexpr int kMuonGroup = 27;  // matrices of a group (what the arguments of one launch hold)
 
 // One matrix of a group.

@@ -6,7 +6,9 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a GPU", allow_module_level=True)
 
-from test_gpu_muon import BF16, DEV, F32, gradient, step_case  # noqa: E402
+from gpu_util import cpu, say  # noqa: E402
+from oracle import ends as E  # noqa: E402
+from test_gpu_muon import BF16, DEV, F32, check_step, gradient, step_case  # noqa: E402
 from rank_gradient_compression_amd import binding as B  # noqa: E402
 from rank_gradient_compression_amd import torch_api as T  # noqa: E402
 
@@ -61,3 +63,30 @@ def test_not_finite_stays_in_its_large_matrix(dtype):
     T.Muon(params, grads, momentum_buffers=momentum).step()
     assert torch.equal(params[0], clean[0]) and torch.equal(params[3], clean[3])
     assert torch.isnan(params[1]).all() and torch.isnan(params[2]).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(13, 650), (2600, 17), (27, 4096), (31, 900), (48, 700)])
+def test_thin_matrices_keep_bfloat16s_digits(rows, cols):
+    """Few singular values share a piece's roundings: two pieces, so that what is left
+    is bfloat16's own rounding (half a step of each entry) and 1e-5 of the update."""
+    x = gradient(rows, cols, BF16, seed=120)
+    out = T.orthogonalize(x)
+    exact = torch.from_numpy(E.newton_schulz(cpu(x))).to(DEV)
+    rounded = exact.to(BF16).double()
+    own = float((rounded - exact).norm() / exact.norm())
+    off = float((out.double() - exact).norm() / exact.norm())
+    say(f"[muon] thin {rows} x {cols}: off {off:.2e}, rounding alone {own:.2e}")
+    # (an entry next to a tie may go to the other side of it: the distances add)
+    assert off <= 1.02 * own + 1e-5
+
+
+@pytest.mark.parametrize("shapes", [[(27, 64), (300, 500), (40, 30)], [(27, 64)] * 3 + [(700, 900)] * 3 + [(20, 800)],
+                                    [(64, 27)] * 30 + [(1100, 1300)] * 3 + [(1300, 1100)]])
+def test_lists_of_thin_and_large_matrices(shapes):
+    """bfloat16 weights of both kinds in one list, joined or in groups of their own, one of
+    small matrices only among them."""
+    params, grads, momentum = step_case(shapes, BF16, seed=130)
+    before, m0 = [p.clone() for p in params], [m.clone() for m in momentum]
+    T.Muon(params, grads, lr=0.05, momentum=0.9, weight_decay=0.1, momentum_buffers=momentum).step()
+    factors = [max(1.0, r / c) ** 0.5 for r, c in shapes]
+    check_step(before, params, grads, m0, momentum, 0.05, 0.9, True, 0.1, factors, BF16, 1)
