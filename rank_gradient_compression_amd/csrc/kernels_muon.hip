@@ -19,13 +19,14 @@
 // the small singular values from step to step, is formed from both pieces: with
 // X itself in 16 bits, what rounding adds under large singular values grows by a
 // a step with the small ones (512 x 512, rank 16 over noise of 1/20: 6e-3 off
-// with fp16 X, 5e-2 with bfloat16, 1.5e-4 so; Gaussian: 1.5e-3).  Other results, and
-// thin matrices' (kMuonThin), take two pieces of everything, three products for one.  In the last two steps,
-// where singular values are near 1 and B near b + c, the identity's part of a X
-// that cancels against B's goes into B instead, whose roundings are then of what
-// is left: X <- (a + b + c) X + (B - (b + c) I) X (Gaussian: 1.7e-3 -> 1.0e-3;
-// from the first step on it would cost the small singular values what the two
-// pieces gave them).
+// with fp16 X, 5e-2 with bfloat16, 1.5e-4 so; Gaussian: 1.5e-3).  Over gradients'
+// spectra that is 1.77e-3 where bfloat16's own rounding is 1.66e-3.  Other results,
+// and thin matrices' (kMuonThin), take two pieces of everything, three products for
+// one.  In the last two steps, where singular values are near 1 and B near b + c, the
+// identity's part of a X that cancels against B's goes into B instead, whose
+// roundings are then of what is left: X <- (a + b + c) X + (B - (b + c) I) X
+// (Gaussian: 1.7e-3 -> 1.0e-3; from the first step on it would cost the small singular
+// values what the two pieces gave them).
 
 #include <hip/hip_runtime.h>
 

@@ -7,20 +7,24 @@
 //
 // The vocabulary is taken in pieces: a tile of the product x w^T ends with its
 // rows' maximum m and sum of exp(l - m) over each segment of columns, and the
-// logits are gone.  Training keeps E = exp(l - m), at most 1, in 16 or 32 bits for a block of tokens whatever the batch, from which one
-// pass over the block makes G once the rows' sums are known.  That is three
-// products of T x V x D in all; forming the logits again for the gradients
-// instead of keeping E would be a fourth (a third more of the time), the pass
-// over E and G is 4 bytes a value (4% of it at D = 4096: 0.11 of 2.6 ms at
-// 4096 x 32000 x 4096 bf16, the products 0.93, 0.83 and 0.89 ms).
-// E is fp32 for fp32 tensors and few tokens, else held times 2^15 in fp16: a relative error of 2^-11 down to 2^-29 of its
+// logits are gone.  Training keeps E = exp(l - m), at most 1, for a block of tokens
+// whatever the batch, from which one pass over the block makes G once the rows' sums
+// are known.  That is three products of T x V x D in all; forming the logits again
+// for the gradients instead of keeping E would be a fourth (a third more of the
+// time), the pass over E and G is 4 bytes a value (4% of it at D = 4096: 0.11 of 2.6
+// ms at 4096 x 32000 x 4096 bf16, the products 0.93, 0.83 and 0.89 ms).
+//
+// Digits.  Sums, maxima and products are fp32.  E is fp32 for fp32 tensors and few
+// tokens, else held times 2^15 in fp16: a relative error of 2^-11 down to 2^-29 of its
 // segment's largest (20 nats below), 2^-40 of that largest under it, and nothing of
 // what is below 2^-40 (28 nats; held as it is, 17).  G is rounded once to the type
-// that the products take (of few tokens it has two pieces of it); the target's entry, which would cancel, is formed
-// from the loss, exp(-loss) - 1, instead.  Sums, maxima and products are fp32.  A
-// row's largest logit M and its S = sum exp(l - M) are kept apart for loss =
-// log S - (l_y - M) and p = exp(l - M) / S: lse, rounded at its full size, would
-// leave that in both (an entry of -0.0106 was 0.4% off with logits around 1000).
+// that the products take (of few tokens it has two pieces of it): with more it would
+// be a second product for dx and for dw each, and what one leaves is 1.05 to 1.25
+// times the gradients' own rounding.  The target's entry, which would cancel, is
+// formed from the loss, exp(-loss) - 1.  A row's largest logit M and its S = sum
+// exp(l - M) are kept apart for loss = log S - (l_y - M) and p = exp(l - M) / S: lse,
+// rounded at its full size, would leave that in both (an entry of -0.0106 was 0.4%
+// off with logits around 1000).
 //
 // Tokens' weights.  A row of G is held times a power of two that brings its own
 // weight u_t to 2^13 .. 2^14, so that a token of small weight keeps its digits in

@@ -29,7 +29,8 @@ def orthogonalize(x: torch.Tensor, out: Optional[torch.Tensor] = None, steps: in
     (psgd_muon_step on one matrix): X = x / (||x|| + eps), then X <- a X +
     (b A + c A^2) X with A = X X^T.  out: of x's shape and any of the three types
     (None: a new one of x's type; x itself: in place).  pieces: 1 for bfloat16's
-    precision, 2 for float32's, 0 goes by out's type."""
+    precision, 2 for float32's, 0 goes by out's type (a bfloat16 matrix with a side of
+    at most 48 takes 2)."""
     rows, cols, ld = _matrix(x, "x")
     out, ldo = _result(out, rows, cols, x.dtype, x.device)
     t = (B.psgd_muon_tensor_t * 1)()
