@@ -11,7 +11,7 @@
 // whatever the batch, from which one pass over the block makes G once the rows' sums
 // are known.  That is three products of T x V x D in all; forming the logits again
 // for the gradients instead of keeping E would be a fourth (a third more of the
-// time), the pass over E and G is 4 bytes a value (4% of it at D = 4096: 0.11 of 2.6
+// time), the pass over E and G is 4 bytes a value (4% of it at D = 4096: 0.12 of 2.6
 // ms at 4096 x 32000 x 4096 bf16, the products 0.93, 0.83 and 0.89 ms).
 //
 // Digits.  Sums, maxima and products are fp32.  E is fp32 for fp32 tensors and few
@@ -644,9 +644,10 @@ struct XentGrad {
 };
 
 // E to G, eight columns a thread, `rows` tokens a workgroup one after the other, the
-// next readings under way while one is worked on.  A workgroup's columns' sums go to
-// its row of db.  Bound by HBM: 4096 x 32000 in 16 bits 111 us, 4.9 TB/s; 700 x 33278
-// from fp32 to two pieces 47 us, 4.0 TB/s.
+// next reading under way while one is worked on (two at a time: with four the
+// registers cost 4096 x 32000 8 us).  A workgroup's columns' sums go to its row of
+// db.  Bound by HBM: 4096 x 32000 in 16 bits 115 us, 4.6 TB/s; 700 x 33278 from fp32 to
+// two pieces 46 us, 4.1 TB/s.
 template <int DT, bool FEW>  // of G: kF16 and kBF16 in E's place, kF32 as two pieces; FEW: two pieces of a 16-bit type
 __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
   const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8, t0 = (int64_t)blockIdx.x * p.rows;
@@ -658,7 +659,7 @@ __global__ __launch_bounds__(256) void k_xent_grad(XentGrad p) {
   float sums[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sums[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
   for (int i = 0; i < n; ++i) {
     const int64_t row = t0 + i, at = row * p.vp + c, y = p.targets[row];
     const bool off = ignored(y, p.ignore) || y >= p.v || (p.weights && p.weights[row] == 0.f);
