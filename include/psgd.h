@@ -594,6 +594,8 @@ psgd_status_t psgd_mx_train_backward(int64_t m, int64_t n, int64_t k, const void
  * ignored tokens; a weight of 0 makes G zero whatever the token's row holds), or
  * NULL for ones.  s is `scale`, divided by the number of
  * tokens that are not ignored (by 1 if there is none) where `mean` is set.
+ * A logit of +infinity or NaN makes its token's loss, lse and G NaN (and with fp32
+ * tensors every logit that an infinite value of x or w is part of is NaN).
  * A bias of -infinity takes a word out of the vocabulary, whatever finite values its
  * row of w holds as long as its products with x are finite.
  *

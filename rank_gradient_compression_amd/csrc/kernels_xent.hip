@@ -239,12 +239,11 @@ __global__ __launch_bounds__(256) void k_xent_prep(XentArgs a, bool train, bool 
 // Rows to operands: 16-bit values, or two pieces of fp32 ones, zeros behind the
 // row's end.  One thread = 8 values.  fp32 rows of x have a power of two each; those
 // of w that a bias takes out are zeros, so that they may hold any finite values.
-// clean: a second copy, the
-// one that dw's product takes, under one power of two, with rows of tokens that do
-// not count zero (their G is zero, and zero times what such a row may hold need not
-// be) and the others times their
-// weight's power of two, whose exponent goes to `factors` as well.  Bound by HBM: 33278 x
-// 650 fp16 18 us, 92 MB read and written, 5.1 TB/s; fp32 31 us, 176 MB, 5.7 TB/s.
+// clean: a second copy, the one that dw's product takes, under one power of two, with
+// rows of tokens that do not count zero (their G is zero, and zero times what such a
+// row may hold need not be) and the others times their weight's power of two, whose
+// exponent goes to `factors` as well.  Bound by HBM: 33278 x 650 fp16 18 us, 92 MB read
+// and written, 5.1 TB/s; fp32 31 us, 176 MB, 5.7 TB/s.
 struct XentPack {
   const void* x;
   int64_t ld, rows, d, dp;
@@ -316,7 +315,10 @@ __global__ __launch_bounds__(256) void k_xent_pack(XentPack w, XentPack x, unsig
     __builtin_memcpy(to + at, hi, sizeof hi);
     if constexpr (DT == kF32) __builtin_memcpy(to + kMmaLow + at, lo, sizeof lo);
   };
-  if (p.out) put(p.out, DT == kF32 && word_out(p.bias, row) ? 0.f : 1.f, DT != kF32 ? 1.f : p.exponents ? ldexpf(1.f, p.exponents[row]) : *p.scale);
+  if (p.out) {
+    const float scale = DT != kF32 ? 1.f : p.exponents ? ldexpf(1.f, p.exponents[row]) : *p.scale;
+    put(p.out, DT == kF32 && word_out(p.bias, row) ? 0.f : 1.f, scale);
+  }
   if (!p.factors) return;
   float f = 1.f;
   if (p.weights) {

@@ -423,3 +423,20 @@ def test_gradients_of_few_tokens_are_rounded_once(t, v, d, dtype):
         half = T.cross_entropy_train(x, w, y, b, weights=weights, reduction="sum", dw=torch.ones(v, d, device=DEV), accumulate=True,
                                      dbias=torch.zeros_like(b))[3]
         close("dw on top", half, 1 + g.t() @ xd, e.t() @ xd.abs() + many * (g.abs().t() @ xd.abs()) + small + 2.0 ** -23)
+
+
+@pytest.mark.parametrize("t", [6, 60])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_an_infinite_logit_is_not_a_number(t, dtype):
+    """exp(inf - inf): the token's loss, lse and gradients, and no other token's loss."""
+    x, w, y, b = inputs(t, 100, 24, dtype, True, seed=54, ignored=0.0)
+    x[3, 5] = float("inf")
+    w[:, 5] = w[:, 5].abs() + 0.25
+    loss, lse, dx, _, _ = T.cross_entropy_train(x, w, y, b)
+    others = torch.arange(t, device=DEV) != 3
+    assert torch.isnan(loss[3]) and torch.isnan(lse[3]) and torch.isnan(dx[3]).all()
+    check(Reference(x[others], w, y[others], b), loss[others], lse[others])
+    assert torch.isfinite(dx[others]).all()
+    b[9] = float("inf")
+    loss, lse = T.cross_entropy(x, w, y, b)
+    assert torch.isnan(loss).all() and torch.isnan(lse).all()
