@@ -393,7 +393,7 @@ def test_autocast(low):
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("t", [1, 2, 15, 16, 17, 32])
-@pytest.mark.parametrize("v,d", [(300, 40), (1000, 650), (90, 64)])
+@pytest.mark.parametrize("v,d", [(300, 40), (1000, 650), (90, 64), (70, 50001), (66, 49160)])
 def test_gradients_of_few_tokens_are_rounded_once(t, v, d, dtype):
     """Up to 32 tokens of a 16-bit type: half a step of dx, dw and dbias, and before it
     fp32's roundings and G's as two values of the type (bf16 2^-16; fp16 2^-21, and
@@ -440,3 +440,33 @@ def test_an_infinite_logit_is_not_a_number(t, dtype):
     b[9] = float("inf")
     loss, lse = T.cross_entropy(x, w, y, b)
     assert torch.isnan(loss).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("dtype,t", [(F16, 20), (F16, 90), (BF16, 5), (F32, 40)])
+@pytest.mark.parametrize("reduction", ["none", "mean"])
+def test_autograd_of_every_kind_captured(dtype, t, reduction):
+    """Loss and gradients in a graph, replayed between eager work on other inputs."""
+    x, w, y, b = inputs(t, 210, 40, dtype, True, seed=55)
+    up = torch.linspace(0.1, 2.0, t, device=DEV) if reduction == "none" else torch.tensor(0.7, device=DEV)
+
+    def step(*leaves):
+        out = T.linear_cross_entropy(leaves[0], leaves[1], y, leaves[2], reduction=reduction)
+        return (out.detach(),) + torch.autograd.grad(out, leaves, up)
+
+    fixed = [v.clone().requires_grad_(True) for v in (x, w, b)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*fixed)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*fixed)
+    for k in range(4):
+        with torch.no_grad():
+            fixed[0].copy_(x.roll(k, 0) * (1 + k))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(*[v.detach().clone().requires_grad_(True) for v in fixed])
+        for name, a, e in zip(("loss", "dx", "dw", "db"), got, want):
+            assert torch.equal(a, e), (name, k)
